@@ -59,6 +59,57 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, what):
+    """(pointer, token stride, head stride) of a bf16 CUDA tensor [N, heads, hd] whose features are contiguous."""
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError("%s: expected a CUDA bfloat16 tensor, got %s on %s" % (what, t.dtype, t.device))
+    s0, s1, s2 = t.stride()
+    n, h, d = t.shape
+    if s2 != 1 and d > 1:
+        raise ValueError("%s: the features of a head must be contiguous (strides %s)" % (what, t.stride()))
+    if h == 1:
+        s1 = d
+    if n <= 1:
+        s0 = s1 * h
+    return t.data_ptr(), s0, s1
+
+
+def _vec(t, n, dtype, what):
+    """Pointer of a contiguous CUDA tensor of n values; None -> NULL."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous CUDA tensor of %d %s, got %s %s on %s" % (what, n, dtype, tuple(t.shape), t.dtype, t.device))
+    return t.data_ptr()
+
+
+class PagedCache:
+    """A csa_paged: pages of key rows k [n_pages, page, kv_heads, hd] and value rows v alike (None: the key rows are
+    the values), bf16 CUDA tensors or views of either order of rows and heads (the features contiguous)."""
+
+    def __init__(self, k, v=None):
+        for t, what in ((k, "k"), (v, "v")):
+            if t is None and what == "v":
+                continue
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape != k.shape or t.stride(3) != 1:
+                raise ValueError("%s: expected a CUDA bfloat16 tensor [n_pages, page, kv_heads, hd] with contiguous "
+                                 "features, got %s %s, strides %s on %s" % (what, tuple(t.shape), t.dtype, t.stride(), t.device))
+        self.k, self.v = k, v
+        self.n_pages, self.page, self.kv_heads, self.head_dim = k.shape
+        st = lambda t: [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]  # noqa: E731
+        self.c = _abi.Paged(k.data_ptr(), None if v is None else v.data_ptr(), *st(k), *(st(v) if v is not None else (0, 0, 0)),
+                            *k.shape)
+        self.ref = ctypes.byref(self.c)
+
+
 CFG_FIELDS = [f for f, _ in _abi.Cfg._fields_]
 
 
@@ -281,6 +332,74 @@ class Context:
                                      _stream(stream)), "csa_sparse_attn")
 
 
+    # -- a continuous batch over a paged cache ---------------------------------------------------
+    def qk_norm_rope(self, q, k, v, cache, pos, slot=None, tab=None, rd=0, rope_at=None, half=False, q_norm=None,
+                     k_norm=None, eps=None, q_out=None, stream=None):
+        """csa_qk_norm_rope: RMSNorm (q_norm, k_norm f32 [hd] or None) of each head of q [N, H, hd] and
+        k [N, kv_heads, hd], rotation of the rd features from rope_at (default: the last rd) by the angles
+        tab[pos] (adjacent pairs, or with half pairs rd / 2 apart), key and value rows written to rows slot of
+        the PagedCache.  q, k, v may be strided views (of a fused projection, say); q may be None, v too where
+        the cache has no values.  pos, slot int32 [N]; pos < 0: a padding row, left as it is; slot -1: no
+        cache row.  Returns q_out (allocated unless given; q itself for in place)."""
+        N, Hk, hd = k.shape
+        if Hk != cache.kv_heads or hd != cache.head_dim:
+            raise ValueError("k: expected [N, %d, %d], got %s" % (cache.kv_heads, cache.head_dim, tuple(k.shape)))
+        if cache.v is not None and (v is None or v.shape != k.shape):
+            raise ValueError("v: expected %s, got %s" % (tuple(k.shape), None if v is None else tuple(v.shape)))
+        H = 0
+        qp = op = None
+        q_t = q_h = o_t = o_h = 0
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != N or q.shape[2] != hd:
+                raise ValueError("q: expected [%d, H, %d], got %s" % (N, hd, tuple(q.shape)))
+            H = q.shape[1]
+            if q_out is None:
+                q_out = _empty((N, H, hd), torch.bfloat16, q.device, stream)
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out: expected %s, got %s" % (tuple(q.shape), tuple(q_out.shape)))
+            qp, q_t, q_h = _rows(q, "q")
+            op, o_t, o_h = _rows(q_out, "q_out")
+        kp, k_t, k_h = _rows(k, "k")
+        vp, v_t, v_h = _rows(v, "v") if cache.v is not None else (None, 0, 0)
+        if tab is not None and rd and (tab.dim() != 3 or tab.shape[1] * 2 != rd or tab.shape[2] != 2):
+            raise ValueError("tab: expected [positions, %d, 2], got %s" % (rd // 2, tuple(tab.shape)))
+        _check(lib().csa_qk_norm_rope(
+            self.h, qp, q_t, q_h, kp, k_t, k_h, vp, v_t, v_h, N, H, cache.ref, _vec(pos, N, torch.int32, "pos"),
+            _vec(slot, N, torch.int32, "slot"), _vec(q_norm, hd, torch.float32, "q_norm"),
+            _vec(k_norm, hd, torch.float32, "k_norm"), self.cfg.eps if eps is None else eps,
+            _dev(tab, torch.float32, "tab"), 0 if tab is None else tab.shape[0], rd,
+            hd - rd if rope_at is None else rope_at, 1 if half else 0, op, o_t, o_h, _stream(stream)), "csa_qk_norm_rope")
+        return q_out
+
+    def paged_attn(self, q, cache, table, pos, scale, req=None, sink=None, window=0, out=None, lse=None,
+                   with_lse=False, stream=None):
+        """csa_paged_attn: row n of q [N, H, hd] (a token stride is allowed) attends rows max(0, pos[n]+1-window)
+        .. pos[n] of request req[n] (None: request n) of the PagedCache through table int32 [R, width].
+        pos -1: no rows (zeros); pos < -1 or req < 0: padding, its row of out is left as it is.  sink f32 [H].
+        Returns out, or (out, lse) with lse f32 [N, H] the log of the sum of exponentials (without the sink)
+        when lse is given or with_lse is set."""
+        N, H, hd = q.shape
+        if hd != cache.head_dim:
+            raise ValueError("q: expected [N, H, %d], got %s" % (cache.head_dim, tuple(q.shape)))
+        if table.dim() != 2:
+            raise ValueError("table: expected [requests, width], got %s" % (tuple(table.shape),))
+        if out is None:
+            out = _empty((N, H, hd), torch.bfloat16, q.device, stream)
+        elif out.shape != q.shape:
+            raise ValueError("out: expected %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+        if lse is None and with_lse:
+            lse = _empty((N, H), torch.float32, q.device, stream)
+        qp, q_t, q_h = _rows(q, "q")
+        op, o_t, o_h = _rows(out, "out")
+        if H > 1 and (q_h != hd or o_h != hd):
+            raise ValueError("q, out: the heads of a token must follow one another")
+        _check(lib().csa_paged_attn(
+            self.h, qp, q_t, N, H, cache.ref, _dev(table, torch.int32, "table"), table.shape[0], table.shape[1],
+            _vec(req, N, torch.int32, "req"), _vec(pos, N, torch.int32, "pos"), _vec(sink, H, torch.float32, "sink"),
+            scale, window, op, o_t, _vec(lse, N * H, torch.float32, "lse"), _stream(stream)), "csa_paged_attn")
+        return out if lse is None else (out, lse)
+
+
 def rmsnorm(x, w, eps, out=None, stream=None):
     N = x.shape[-1]
     out = torch.empty_like(x) if out is None else out
@@ -335,3 +454,25 @@ def index_topk(S, B, T, start_pos, compress_len, ratio, K, out, offset=0, cand=N
                                 _dev(cand, torch.uint8, "cand"), 0 if cand is None else cand.shape[-1], cand_block, K, offset,
                                 _dev(out, torch.int32, "out"), _stream(stream)), "csa_index_topk")
     return out
+
+
+def page_step(new_len, length, table, free, state, page, tok_req, tok_pos, tok_slot, cu=None, length_out=None,
+              state_out=None, info=None, stream=None):
+    """csa_page_step: the token maps and tables of one step of a continuous batch.  new_len, length int32 [R]; table
+    int32 [R, width]; free int32 [n_pages], state int32 [2] the ring of free pages; tok_req, tok_pos, tok_slot int32
+    [N], cu int32 [R+1].  length_out, state_out: where the state after the step goes (default: length and state
+    themselves).  Returns info int32 [4]: tokens, pages taken, pages released, error bits."""
+    R, N = new_len.numel(), tok_req.numel()
+    if table.dim() != 2 or table.shape[0] != R:
+        raise ValueError("table: expected [%d, width], got %s" % (R, tuple(table.shape)))
+    if info is None:
+        info = _empty((4,), torch.int32, new_len.device, stream)
+    i32 = torch.int32
+    _check(lib().csa_page_step(
+        _vec(new_len, R, i32, "new_len"), R, page, _vec(length, R, i32, "length"), _dev(table, i32, "table"),
+        table.shape[1], _vec(free, free.numel(), i32, "free"), free.numel(), _vec(state, 2, i32, "state"),
+        _vec(tok_req, N, i32, "tok_req"), _vec(tok_pos, N, i32, "tok_pos"), _vec(tok_slot, N, i32, "tok_slot"), N,
+        _vec(cu, R + 1, i32, "cu"), _vec(length if length_out is None else length_out, R, i32, "length_out"),
+        _vec(state if state_out is None else state_out, 2, i32, "state_out"), _vec(info, 4, i32, "info"),
+        _stream(stream)), "csa_page_step")
+    return info

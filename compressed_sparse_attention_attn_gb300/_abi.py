@@ -57,6 +57,12 @@ class Debug(ctypes.Structure):
     _fields_ = [(n, P) for n in ("q", "kv", "kv_codes", "kv_scale", "idx", "scores", "o", "og", "qr", "qI", "wI")]
 
 
+class Paged(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P)] + \
+               [(n, I64) for n in ("k_page", "k_row", "k_head", "v_page", "v_row", "v_head")] + \
+               [(n, I) for n in ("n_pages", "page", "kv_heads", "head_dim")]
+
+
 # name -> (restype, argtypes); mirrors include/csa.h
 SIGNATURES = {
     "csa_create": (I, [ctypes.POINTER(Cfg), ctypes.POINTER(P)]),
@@ -88,6 +94,10 @@ SIGNATURES = {
     "csa_index_topk": (I, [P, I, I, I, I, I, I, P, I, I, I, I, P, P]),
     "csa_candidate_blocks": (I, [P, I, I, I, I, I, I, I, I, P, I, P]),
     "csa_sparse_attn": (I, [P, P, I, I, I, I, P, I64, I, P, I64, I, P, I, P, I, P, F, P, P, I, I, P, I, P]),
+    "csa_page_step": (I, [P, I, I, P, P, I, P, I, P, P, P, P, I, P, P, P, P, P]),
+    "csa_qk_norm_rope": (I, [P, P, I64, I64, P, I64, I64, P, I64, I64, I, I, P, P, P, P, P, F, P, I, I, I, I, P, I64,
+                             I64, P]),
+    "csa_paged_attn": (I, [P, P, I64, I, I, P, P, I, I, P, P, P, F, I, P, I64, P, P]),
 }
 
 

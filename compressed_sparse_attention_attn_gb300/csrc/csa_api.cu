@@ -549,6 +549,97 @@ int csa_sparse_attn(csa_ctx *ctx, const csa_bf16 *q, int B, int T, int H, int hd
 }
 
 // ---------------------------------------------------------------------------------------------
+// a continuous batch over a paged cache
+// ---------------------------------------------------------------------------------------------
+
+int csa_page_step(const int32_t *new_len, int R, int page, const int32_t *length, int32_t *table, int width,
+                  int32_t *free_ring, int n_pages, const int32_t *state, int32_t *tok_req, int32_t *tok_pos,
+                  int32_t *tok_slot, int N, int32_t *cu, int32_t *length_out, int32_t *state_out, int32_t *info,
+                  csa_stream stream) {
+  constexpr int kMax = 1 << 30;
+  if (!new_len || !length || !table || !free_ring || !state || !length_out || !state_out || !info ||
+      (N > 0 && (!tok_req || !tok_pos || !tok_slot)))
+    return fail(CSA_ERR_ARG, "csa_page_step: NULL argument");
+  if (R <= 0 || R > csa::kPageStepMaxR) return fail(CSA_ERR_SHAPE, "csa_page_step: %d requests outside [1, %d]", R, csa::kPageStepMaxR);
+  if (page <= 0 || n_pages <= 0 || (int64_t)n_pages * page >= kMax || width <= 0 || (int64_t)width * page >= kMax || N < 0 || N >= kMax)
+    return fail(CSA_ERR_ARG, "csa_page_step: page %d, n_pages %d, width %d, N %d", page, n_pages, width, N);
+  csa::PageStepArgs a{new_len, length, R, page, table, width, free_ring, n_pages, state, tok_req, tok_pos, tok_slot, N,
+                      cu, length_out, state_out, info};
+  CSA_CUDA(csa::launch_page_step(a, (cudaStream_t)stream), "csa_page_step");
+  return CSA_OK;
+}
+
+// A cache description the kernels can address; CSA_OK or an error code.
+static int check_paged(const csa_paged *c, const char *who) {
+  if (!c || !c->k) return fail(CSA_ERR_ARG, "%s: no cache", who);
+  if (c->n_pages <= 0 || c->page <= 0 || (int64_t)c->n_pages * c->page >= ((int64_t)1 << 31) || c->kv_heads <= 0 ||
+      c->head_dim <= 0 || c->head_dim % 8)
+    return fail(CSA_ERR_ARG, "%s: cache of %d pages of %d rows, %d heads of %d features", who, c->n_pages, c->page,
+                c->kv_heads, c->head_dim);
+  const int64_t st[6] = {c->k_page, c->k_row, c->k_head, c->v ? c->v_page : 0, c->v ? c->v_row : 0, c->v ? c->v_head : 0};
+  for (int64_t v : st)
+    if (v < 0 || v % 8) return fail(CSA_ERR_ARG, "%s: cache strides must be non-negative multiples of 8 elements", who);
+  if (((uintptr_t)c->k | (uintptr_t)c->v) & 15) return fail(CSA_ERR_ARG, "%s: the cache must be 16-byte aligned", who);
+  return CSA_OK;
+}
+
+int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, const csa_bf16 *k, int64_t k_t,
+                     int64_t k_h, const csa_bf16 *v, int64_t v_t, int64_t v_h, int N, int H, const csa_paged *cache,
+                     const int32_t *pos, const int32_t *slot, const float *q_norm, const float *k_norm, float eps,
+                     const float *tab, int tab_rows, int rd, int at, int half, csa_bf16 *q_out, int64_t o_t,
+                     int64_t o_h, csa_stream stream) {
+  const char *who = "csa_qk_norm_rope";
+  if (!ctx || !k || !pos || (q && !q_out)) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
+  if (int rc = check_paged(cache, who)) return rc;
+  if (cache->v && !v) return fail(CSA_ERR_ARG, "%s: the cache holds values, v is NULL", who);
+  const int hd = cache->head_dim;
+  if (N < 0 || (q && H <= 0) || hd > 1024) return fail(CSA_ERR_ARG, "%s: N %d, H %d, head_dim %d (<= 1024)", who, N, H, hd);
+  if (rd < 0 || rd % 2 || at < 0 || at % 2 || at + rd > hd || (rd > 0 && (!tab || tab_rows <= 0)))
+    return fail(CSA_ERR_ARG, "%s: rotation of %d features from %d of %d, %d table rows", who, rd, at, hd, tab_rows);
+  if ((uintptr_t)tab & 7) return fail(CSA_ERR_ARG, "%s: the table must be 8-byte aligned", who);
+  const void *al[] = {q, k, v, q_out};
+  for (const void *p : al)
+    if ((uintptr_t)p & 15) return fail(CSA_ERR_ARG, "%s: rows must be 16-byte aligned", who);
+  const int64_t st[] = {q ? q_t : 0, q ? q_h : 0, k_t, k_h, cache->v ? v_t : 0, cache->v ? v_h : 0, q ? o_t : 0, q ? o_h : 0};
+  for (int64_t x : st)
+    if (x < 0 || x % 8) return fail(CSA_ERR_ARG, "%s: strides must be non-negative multiples of 8 elements", who);
+  if (!slot && N > (int64_t)cache->n_pages * cache->page)
+    return fail(CSA_ERR_SHAPE, "%s: %d tokens and no slots, %d rows", who, N, cache->n_pages * cache->page);
+  if (int rc = check_device(ctx, who)) return rc;
+  if (N == 0) return CSA_OK;
+  csa::NormRopeArgs a{(const bf16 *)q, (const bf16 *)k, (const bf16 *)(cache->v ? v : nullptr), q_t, q_h, k_t, k_h, v_t, v_h, N,
+                      q ? H : 0, *cache, pos, slot, q_norm, k_norm, eps, tab, tab_rows, rd, at, half ? 1 : 0,
+                      (bf16 *)q_out, o_t, o_h, ctx->status};
+  CSA_CUDA(csa::launch_norm_rope(a, (cudaStream_t)stream), who);
+  return CSA_OK;
+}
+
+int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
+                   const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos, const float *sink,
+                   float scale, int window, csa_bf16 *o, int64_t o_t, float *lse, csa_stream stream) {
+  const char *who = "csa_paged_attn";
+  if (!ctx || !q || !table || !pos || !o) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
+  if (int rc = check_paged(cache, who)) return rc;
+  const int hd = cache->head_dim;
+  if (N < 0 || H <= 0 || H % cache->kv_heads || H > 65535 || R <= 0 || width <= 0 || window < 0 ||
+      (int64_t)width * cache->page >= ((int64_t)1 << 31))
+    return fail(CSA_ERR_ARG, "%s: N %d, H %d over %d kv heads, R %d, width %d, window %d", who, N, H, cache->kv_heads, R,
+                width, window);
+  if (!req && N > R) return fail(CSA_ERR_SHAPE, "%s: %d rows over %d requests and no req", who, N, R);
+  if (hd > 512 || (hd > 256 && cache->v))
+    return fail(CSA_ERR_UNSUPPORTED, "%s: head_dim %d: up to 256, or up to 512 where the key rows are the values", who, hd);
+  if (((uintptr_t)q | (uintptr_t)o) & 15) return fail(CSA_ERR_ARG, "%s: q and o must be 16-byte aligned", who);
+  if (q_t < (int64_t)H * hd || q_t % 8 || o_t < (int64_t)H * hd || o_t % 8)
+    return fail(CSA_ERR_ARG, "%s: token strides must hold the heads and be multiples of 8", who);
+  if (int rc = check_device(ctx, who)) return rc;
+  if (N == 0) return CSA_OK;
+  csa::PagedAttnArgs a{(const bf16 *)q, q_t, N, H, *cache, table, R, width, req, pos, sink, scale, window, (bf16 *)o, o_t, lse,
+                       ctx->status};
+  CSA_CUDA(csa::launch_paged_attn(a, (cudaStream_t)stream), who);
+  return CSA_OK;
+}
+
+// ---------------------------------------------------------------------------------------------
 // the layer
 // ---------------------------------------------------------------------------------------------
 

@@ -223,6 +223,59 @@ bool compress_supported(const CompressArgs &a);
 cudaError_t launch_compress(const CompressArgs &a, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s);
 cudaError_t launch_fill_f32(float *p, int64_t n, float v, cudaStream_t s);
 
+// ---- a continuous batch over a paged cache -------------------------------------------------------
+// The step's token maps and tables from the requests' lengths (k_page_step.cu; csa_page_step's arguments).
+struct PageStepArgs {
+  const int32_t *new_len, *length;
+  int R, page;
+  int32_t *table;
+  int width;
+  int32_t *free_ring;
+  int n_pages;
+  const int32_t *state;
+  int32_t *tok_req, *tok_pos, *tok_slot;
+  int N;
+  int32_t *cu, *length_out, *state_out, *info;
+};
+constexpr int kPageStepMaxR = 16384;
+cudaError_t launch_page_step(const PageStepArgs &a, cudaStream_t s);
+
+// Head norms, rotation and the cache write of N tokens (k_norm_rope.cu; csa_qk_norm_rope's arguments).
+struct NormRopeArgs {
+  const bf16 *q, *k, *v;
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h;
+  int N, H;
+  csa_paged c;
+  const int32_t *pos, *slot;
+  const float *q_norm, *k_norm;
+  float eps;
+  const float *tab;
+  int tab_rows, rd, at, half;
+  bf16 *q_out;
+  int64_t o_t, o_h;
+  int *status;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s);
+
+// Attention of single tokens over the paged cache (csa_paged_attn's arguments).
+struct PagedAttnArgs {
+  const bf16 *q;
+  int64_t q_t;
+  int N, H;
+  csa_paged c;
+  const int32_t *table;
+  int R, width;
+  const int32_t *req, *pos;
+  const float *sink;
+  float scale;
+  int window;
+  bf16 *o;
+  int64_t o_t;
+  float *lse;
+  int *status;
+};
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t s);
+
 // Record the calling thread's last error (attn_v41_last_error) and return `code`.
 int set_error(int code, const char *fmt, ...);
 

@@ -349,6 +349,90 @@ CSA_API int csa_sparse_attn(csa_ctx *ctx, const csa_bf16 *q, int B, int T, int H
                     csa_bf16 *o, csa_bf16 *o_rot, int rd, int start_pos, const float *tab, int tab_rows,
                     csa_stream stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A continuous batch over a paged cache
+ *
+ * A server's requests have lengths of their own and share one pool of pages.  The pages print no paged
+ * cache; these three calls are additions beside csa_kv_finish (rotation and cache write),
+ * csa_rmsnorm / csa_rope and csa_sparse_attn.  One step of such a batch is
+ *   csa_page_step      the step's tokens from the requests' lengths: request, position and slot of each
+ *   csa_qk_norm_rope   their query and key heads normed and turned, key and value rows into their slots
+ *   csa_paged_attn     each token's attention over its request's rows 0 .. position
+ * and nothing of it is decided on the host: the three can be captured into one CUDA graph whose
+ * replays serve successive steps (csa_page_step in place on length and state).
+ * -------------------------------------------------------------------------------------------*/
+
+/* A pool of n_pages pages of `page` rows, kv_heads heads of head_dim features each.  Element strides:
+ * feature d of head h of row r of page p is k[p*k_page + r*k_row + h*k_head + d], likewise v; so either
+ * order of rows and heads inside a page is taken.  v NULL: the key rows are the values too (latent rows).
+ * k, v 16-byte aligned, strides non-negative multiples of 8, head_dim a multiple of 8; n_pages * page < 2^31.
+ * Row `slot` is row slot % page of page slot / page. */
+typedef struct csa_paged {
+  csa_bf16 *k, *v;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  int n_pages, page, kv_heads, head_dim;
+} csa_paged;
+
+/* The token maps and block tables of one step, built on the device from the requests' lengths.
+ * new_len[r] > 0: request r adds that many tokens behind its length[r] rows; 0: it waits; < 0: it has
+ * ended, its pages go back to the pool and its length becomes 0.  (all int32, device)
+ *   length [R], table [R][width]   rows and pages of each request; entries past ceil(length/page) are
+ *                                  never read.  New pages are written to the table in place
+ *   free [n_pages], state [2]      the free pages, a ring: `count` = state[1] pages from free[state[0]] on.
+ *                                  Pages are taken from its front in the order of the requests; released
+ *                                  ones go behind its end, in the same order, and serve the next step
+ *   tok_req, tok_pos, tok_slot [N] request, position and cache slot of the step's tokens, request after
+ *                                  request; -1 in all three behind the last token (padding)
+ *   cu [R+1]                       first token of each request (may be NULL)
+ *   length_out [R], state_out [2]  the state after the step; they may be length and state themselves
+ *   info [4]                       tokens, pages taken, pages released, error bits
+ * Nothing but info, tok_* (-1) and cu (0) changes when an error bit is set (length_out and state_out receive
+ * the old values): 1 more than N tokens, 2 a length negative or past width pages, 4 more pages needed than
+ * are free, 8 a state outside the ring.  A table or ring entry outside [0, n_pages) gives its tokens slot -1.
+ * R <= 16384, width, N and n_pages * page below 2^30.  Not tied to a context; calls that share buffers are
+ * ordered by the caller. */
+CSA_API int csa_page_step(const int32_t *new_len, int R, int page, const int32_t *length, int32_t *table, int width,
+                          int32_t *free_ring, int n_pages, const int32_t *state, int32_t *tok_req, int32_t *tok_pos,
+                          int32_t *tok_slot, int N, int32_t *cu, int32_t *length_out, int32_t *state_out,
+                          int32_t *info, csa_stream stream);
+
+/* RMSNorm and rotation of the query and key heads of N tokens in one pass, the key and value rows written to
+ * their slots of the cache.  Per token n and head: y = x / sqrt(mean(x^2) + eps) * w (w NULL: y = x), then
+ * the features at .. at+rd-1 turned by the token's angles (rd 0: none) in f32, rounded once to bf16: pair i
+ * is (at+2i, at+2i+1), or with half != 0 (at+i, at+i+rd/2), and becomes (a c - b s, a s + b c) with
+ * (c, s) = tab[pos[n]][i], tab f32 [tab_rows][rd/2][2] (csa_rope_table_get's layout; tables scaled for long
+ * contexts come in through it).  Value rows are copied.
+ * q [N][H][head_dim], k and v [N][cache->kv_heads][head_dim] with element strides per token and head (x_t, x_h,
+ * multiples of 8, 16-byte aligned bases); q_out likewise, it may be q itself.  pos, slot int32 [N].
+ * A token with pos < 0 is padding: nothing of it is read or written.  slot -1: only its query is produced.
+ * cache->v NULL: v is not read (may be NULL).  q NULL: keys and values only.  slot NULL: token n goes to row
+ * n.  No two tokens may have the same slot, and k, v may not overlap the cache.
+ * A pos >= tab_rows or a slot outside [-1, n_pages * page) is a caller error: the token is skipped and
+ * recorded in the context's status word (csa_status).  head_dim <= 1024, at even. */
+CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, const csa_bf16 *k, int64_t k_t,
+                             int64_t k_h, const csa_bf16 *v, int64_t v_t, int64_t v_h, int N, int H,
+                             const csa_paged *cache, const int32_t *pos, const int32_t *slot, const float *q_norm,
+                             const float *k_norm, float eps, const float *tab, int tab_rows, int rd, int at, int half,
+                             csa_bf16 *q_out, int64_t o_t, int64_t o_h, csa_stream stream);
+
+/* Attention of one new token a row over a paged cache: row n attends rows j = max(0, pos[n]+1-window) ..
+ * pos[n] (window 0: from 0) of request req[n] (req NULL: request n), its own just-written row among them.
+ * Query head h uses kv head h / (H / kv_heads).  S_j = scale q_h . K_j, O = sum_j e^{S_j} V_j / (e^{sink_h} +
+ * sum_j e^{S_j}) (sink NULL: without that term), lse = ln sum_j e^{S_j} (without the sink); scores, maxima and
+ * sums in f32, O rounded once to bf16.  pos -1: no rows, O = 0 and lse = -inf.  A row with pos < -1 or
+ * req < 0 is padding: nothing of it is written.
+ * q, o bf16 [N][H][head_dim] with a stride per token (elements, multiples of 8; heads follow one another);
+ * table int32 [R][width] of page ids; lse f32 [N][H] or NULL; sink f32 [H] or NULL.
+ * head_dim <= 256 with separate or shared values, or up to 512 with cache->v NULL.  A req >= R (its row is
+ * left as it was), a pos past width pages (the rows past them are left out) and a page id outside
+ * [0, n_pages) (its rows are left out) are caller errors, recorded in the context's status word.
+ * Rows of different length are dealt evenly over the device and joined within the one launch, in a fixed
+ * order (the same inputs give the same bits); the shares lie in the context's workspace. */
+CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
+                           const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos,
+                           const float *sink, float scale, int window, csa_bf16 *o, int64_t o_t, float *lse,
+                           csa_stream stream);
+
 /* Allocation-free projection.  The pages have no counterpart: this is an addition for callers that
  * cannot allocate device memory -- a host runtime that owns a fixed device-memory budget and forbids
  * allocations outside it, or code that has no csa_ctx (csa_create allocates the context's
