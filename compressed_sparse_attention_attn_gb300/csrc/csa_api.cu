@@ -59,6 +59,7 @@ struct csa_ctx {
   int xpart_rows = 0;
   int32_t *idx_win = nullptr;
   int *status = nullptr;
+  int *paged_counters = nullptr;  // the paged attention's arrivals (zero between launches)
   float *ws = nullptr;  // Stream-K counters and partials, the attention's split shares, the compressor's partials
   size_t ws_bytes = 0;
   size_t gemm_ws_bytes() const { return ws_bytes; }
@@ -218,6 +219,7 @@ int csa_create(const csa_cfg *cfg, csa_ctx **out) {
   ALLOC(x_stage, nt * g.dim);
   ALLOC(out_stage, nt * g.dim);
   ALLOC(status, 4);
+  ALLOC(paged_counters, csa::kPagedCounters);
   {
     float *w = nullptr;
     if (e == cudaSuccess) e = c->alloc(&w, c->ws_bytes / sizeof(float));
@@ -226,6 +228,7 @@ int csa_create(const csa_cfg *cfg, csa_ctx **out) {
 #undef ALLOC
   if (e == cudaSuccess) e = cudaMemset(c->status, 0, 4 * sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(c->ws, 0, csa::kGemmCounterBytes);  // Stream-K arrival counters
+  if (e == cudaSuccess) e = cudaMemset(c->paged_counters, 0, csa::kPagedCounters * sizeof(int));
   if (e != cudaSuccess) {
     c->release();
     delete c;
@@ -635,7 +638,8 @@ int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, c
   if (N == 0) return CSA_OK;
   csa::PagedAttnArgs a{(const bf16 *)q, q_t, N, H, *cache, table, R, width, req, pos, sink, scale, window, (bf16 *)o, o_t, lse,
                        ctx->status};
-  CSA_CUDA(csa::launch_paged_attn(a, (cudaStream_t)stream), who);
+  CSA_CUDA(csa::launch_paged_attn(a, ctx->comp_ws(), ctx->comp_ws_bytes(), ctx->paged_counters, ctx->num_sms,
+                                  (cudaStream_t)stream), who);
   return CSA_OK;
 }
 

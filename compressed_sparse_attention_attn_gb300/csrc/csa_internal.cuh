@@ -274,7 +274,10 @@ struct PagedAttnArgs {
   float *lse;
   int *status;
 };
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t s);
+// ws: the shares of rows that several CTAs work on; counters: kPagedCounters ints, zero between launches.
+constexpr int kPagedCounters = 3 * 640;
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms,
+                              cudaStream_t s);
 
 // Record the calling thread's last error (attn_v41_last_error) and return `code`.
 int set_error(int code, const char *fmt, ...);
