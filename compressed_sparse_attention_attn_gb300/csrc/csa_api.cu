@@ -310,7 +310,11 @@ int csa_status(csa_ctx *ctx, int clear) {
   if (clear) {
     CSA_CUDA(cudaMemset(ctx->status, 0, sizeof(int)), "csa_status: clear");
     // a projection that gave up may have left Stream-K arrival counters raised: start them at zero
-    if (st & csa::kStatusTimeout) CSA_CUDA(cudaMemset(ctx->ws, 0, csa::kGemmCounterBytes), "csa_status: counters");
+    // (and the paged attention's arrivals)
+    if (st & csa::kStatusTimeout) {
+      CSA_CUDA(cudaMemset(ctx->ws, 0, csa::kGemmCounterBytes), "csa_status: counters");
+      CSA_CUDA(cudaMemset(ctx->paged_counters, 0, csa::kPagedCounters * sizeof(int)), "csa_status: counters");
+    }
     CSA_CUDA(cudaDeviceSynchronize(), "csa_status: clear");
   }
   if (st & csa::kStatusTimeout) return fail(CSA_ERR_DEVICE_TIMEOUT, "a bounded device-side wait ran out");

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
         }
       }
       __syncthreads();  // the stage may be refilled
-      if (!whole) publish<kHeads, HD, kThreads>(P, sb, se, rg, cc.n, h0, nh, s_join, &s_flag);
+      if (!whole) publish<kHeads, HD, kThreads, 0>(P, tid, sb, se, rg, cc.n, h0, nh, s_join, &s_flag);
       if (u + 1 < rg.end) {
         advance(cc);
         seg = u + 1;
@@ -367,8 +367,8 @@ cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream
   return cudaGetLastError();
 }
 
-// (head_dim above 256)
-cudaError_t launch_rows(const PagedAttnArgs &a, cudaStream_t s);
+// (head_dim above 256: k_paged_attn_tc.cu)
+cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s);
 
 }  // namespace paged
 
@@ -384,7 +384,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes
   if (hd <= 64) return paged::launch<64>(p, ws, ws_bytes, num_sms, s);
   if (hd <= 128) return paged::launch<128>(p, ws, ws_bytes, num_sms, s);
   if (hd <= 256) return paged::launch<256>(p, ws, ws_bytes, num_sms, s);
-  return paged::launch_rows(a, s);
+  return paged::launch_latent(p, ws, ws_bytes, num_sms, s);
 }
 
 }  // namespace csa

@@ -1,0 +1,523 @@
+// k_paged_attn_tc.cu -- attention of single tokens over a paged cache of latent rows (head_dim above 256, the key
+// rows are the values) on the 5th-generation tensor cores.
+//
+// Up to 64 query heads share a row of 512 features that is key and value: 4 x 64 x 512 flops for 1 KB, 860
+// TFLOP/s at the card's copy rate, which warp-level products do not reach.  A CTA an SM works through its
+// range of 64-position tiles (paged_common.cuh), the accumulators in tensor memory:
+//   S[h][r] = sum_d q[h][d] K[r][d]       M = 128 lanes (64 heads; the other lanes read what lies behind q and are
+//                                         never looked at), N = 64 positions, K = 512
+//   p = exp2(S scale - m), bf16           a thread a head: the running maximum m and the sum never leave it; m is
+//                                         raised only by more than 2^8 (the sums so far are then rescaled)
+//   O^T[d][h] += sum_r K[r][d] p[h][r]    M = 4 x 128 features, N = 64 heads, K = 64 positions (the same tile read
+//                                         as an MN-major operand)
+// p rounded to bf16 is off by at most 2^-8 of itself, which moves O by at most 2^-8 sum_r w_r |K_rd|; scores,
+// maxima, sums and O are f32.
+//
+// Shared memory holds q (64 KB) and two tiles (64 KB each), so that one is in flight while the other is used:
+// 64 KB an SM in flight covers the copy rate's latency twice.  A pair of warps serves each tile buffer (cp.async
+// from the page of each position, 16 bytes a lane, rows past the end as zeros), and signals it a quarter of the
+// features at a time; one thread issues whichever product is ready first, the next tile's scores or
+// this tile's values, so a buffer is handed back as soon as its weights are there.  Two warps do the softmax, and
+// load the next segment's q behind the last scores that read it; four warps rescale O and write it out.  All
+// waits are time-bounded.
+#include <algorithm>
+#include <cstring>
+
+#include "attn_common.cuh"
+#include "paged_common.cuh"
+
+namespace csa {
+namespace paged {
+namespace latent {
+
+constexpr int kHD = 512;
+constexpr int kHeads = 64;              // query heads of a head group
+constexpr int kUnit = 64;               // positions of a tile
+constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile (and of q)
+constexpr int kBlocks = kHD / 64;
+constexpr int kThreads = 352;           // warps 0, 1 softmax; 2, 3 and 8, 9 copies; 4-7 O; 10 products
+constexpr int kJoinBar = 1;             // named barrier of warps 4-7
+
+struct L {
+  static constexpr size_t q = 0;                                             // [8][64][128 B]
+  static constexpr size_t t = q + (size_t)kBlocks * kBlock;                  // [2][8][64][128 B]
+  static constexpr size_t p = t + (size_t)2 * kBlocks * kBlock;              // [2][64][128 B]
+  static constexpr size_t join = p + (size_t)2 * kHeads * 128;               // float
+  static constexpr size_t alpha = join + sizeof(float) * kJoinFloats<kHeads>;  // float [2][64]
+  static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
+  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [15]
+  static constexpr size_t bars = scan + 16 * 8;                              // u64 [20]
+  static constexpr size_t misc = bars + 20 * 8;                              // masks [2][2], flags, slot, abort
+  static constexpr size_t total = misc + 64;
+};
+static_assert(L::total + 1024 <= 232448, "one CTA's shared memory");
+
+// Every lane waits (each acquires what the barrier publishes); the warp goes on only if all succeeded.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  const bool ok = tc::mbar_wait(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+// Whether all `count` threads of named barrier `id` say yes.
+__device__ __forceinline__ bool all_agree(int id, int count, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(yes ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+struct Cursor {
+  int n, hg, t;
+  Row row;
+};
+__device__ __forceinline__ void advance(const Params &P, Cursor &c) {
+  if (++c.t < c.row.units) return;
+  c.t = 0;
+  if (++c.hg < P.Hg) return;
+  c.hg = 0;
+  do {
+    if (++c.n >= P.a.N) {
+      c.row.units = 1;
+      c.row.rows = 0;
+      return;
+    }
+    c.row = row_of<kUnit>(P.a, c.n, false);
+  } while (c.row.units == 0);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  uint8_t *smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  const uint32_t s_q = tc::smem_u32(smem + L::q), s_t = tc::smem_u32(smem + L::t), s_p = tc::smem_u32(smem + L::p);
+  float *alpha_sm = reinterpret_cast<float *>(smem + L::alpha), *f_sm = reinterpret_cast<float *>(smem + L::f);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
+  // full [2][4]: a quarter of the features of a tile has landed; empty [2]: its values have been used
+  uint64_t *full = bars, *empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12, *stat = bars + 14, *fin = bars + 16,
+           *q_full = bars + 18, *drain = bars + 19;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::misc);  // [2][2]: positions of a tile that are there
+  int *flags = reinterpret_cast<int *>(masks + 4);                 // [2][2]: a maximum was raised (by warp)
+  int *join_flag = flags + 4;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(join_flag + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const PagedAttnArgs &a = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
+  const int nkb = (hd + 63) / 64;
+
+  const Range rg = find_range<kUnit, kThreads>(P, reinterpret_cast<int64_t *>(smem + L::scan));
+  if (rg.begin >= rg.end) return;
+  const int64_t nt = rg.end - rg.begin;  // this CTA's tiles
+  Cursor c;
+  c.n = rg.row;
+  c.row = row_of<kUnit>(a, c.n, false);
+  {
+    const int64_t in = rg.begin - rg.before;
+    c.hg = (int)(in / c.row.units);
+    c.t = (int)(in - (int64_t)c.hg * c.row.units);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&full[i], 64);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&empty[b], 1);
+      tc::mbar_init(&s_full[b], 1);
+      tc::mbar_init(&p_full[b], 64 + 128);
+      tc::mbar_init(&stat[b], 64);
+    }
+    tc::mbar_init(&fin[0], 64);
+    tc::mbar_init(&fin[1], 64);
+    tc::mbar_init(q_full, 64);
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 10) tc::tmem_alloc(tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kUnit;  // S: 2 x 64 columns, O^T: 4 x 64
+  auto par = [](int64_t i) { return (uint32_t)((i >> 1) & 1); };  // phase of tile i's barriers
+  auto last_of = [&](int64_t i) { return c.t == c.row.units - 1 || i + 1 == nt; };  // of a segment, in this CTA
+
+  if (warp < 2) {
+    // ------------------------------------------------------------------------------ softmax
+    const int h = tid;  // head of the group
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    auto load_q = [&](const Cursor &k) {
+      const int kvh = k.hg / P.sub, sg = k.hg - kvh * P.sub;
+      const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
+      const bf16 *q = a.q + (int64_t)k.n * a.q_t + (int64_t)h0 * hd;
+      const int cc = lane & 7;
+#pragma unroll 1
+      for (int kb = 0; kb < nkb; ++kb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = warp * 32 + 4 * i + (lane >> 3), d = kb * 64 + cc * 8;
+          const bool in = r < nh && d < hd;
+          attn::cp_async16(s_q + kb * kBlock + r * 128 + ((cc ^ (r & 7)) << 4), in ? q + (int64_t)r * hd + d : a.q, in);
+        }
+    };
+    load_q(c);
+    attn::cp_async_wait_all();
+    attn::fence_proxy_async();
+    tc::mbar_arrive(q_full);
+    float m = -INFINITY, l = 0.f;
+    int nseg = 0;
+    bool first = true;
+    int64_t seg = 0;  // the segment's first tile here
+    for (int64_t i = 0; i < nt; ++i) {
+      const int b = (int)(i & 1);
+      if (!warp_wait(&full[4 * b + 3], par(i), abort_flag)) break;  // (its mask)
+      const uint32_t ok0 = masks[2 * b], ok1 = masks[2 * b + 1];
+      if (!warp_wait(&s_full[b], par(i), abort_flag)) break;
+      tc::tc_fence_after();
+      const bool last = last_of(i);
+      Cursor nx = c;
+      if (last && i + 1 < nt) {  // q's last reader is done: the next segment's q on its way
+        nx.t = nx.row.units - 1;
+        advance(P, nx);
+        load_q(nx);
+      }
+      float s[64];
+      {
+        float v[32];
+        attn::tmem_ld_32cols(tmem + (uint32_t)(b * kUnit) + lane_off, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = v[k];
+        attn::tmem_ld_32cols(tmem + (uint32_t)(b * kUnit + 32) + lane_off, v);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[32 + k] = v[k];
+      }
+      float mx = -INFINITY;
+      if ((ok0 & ok1) == 0xffffffffu) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          s[k] *= P.scale_log2;
+          mx = fmaxf(mx, s[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          s[k] = ((k < 32 ? ok0 : ok1) >> (k & 31)) & 1u ? s[k] * P.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[k]);
+        }
+      }
+      float al = 1.f;
+      bool raised = false;
+      if (first) {
+        m = mx;
+      } else if (mx > m + 8.f || (m == -INFINITY && mx > m)) {
+        al = m == -INFINITY ? 0.f : exp2f(m - mx);
+        m = mx;
+        raised = true;
+      }
+      alpha_sm[b * kHeads + h] = al;
+      const bool any = __any_sync(0xffffffffu, raised);
+      if (lane == 0) flags[2 * b + warp] = any ? 1 : 0;
+      tc::mbar_arrive(&stat[b]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+      const uint32_t prow = s_p + b * kHeads * 128 + h * 128;
+#pragma unroll
+      for (int k = 0; k < 64; k += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = exp2f(s[k + 2 * e] - ref), y = exp2f(s[k + 2 * e + 1] - ref);
+          sum += x + y;
+          const __nv_bfloat162 pk = __floats2bfloat162_rn(x, y);
+          w[e] = *reinterpret_cast<const uint32_t *>(&pk);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (((k >> 3) ^ (h & 7)) << 4)), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3])
+                     : "memory");
+      }
+      l = l * al + sum;
+      attn::fence_proxy_async();
+      tc::tc_fence_before();
+      tc::mbar_arrive(&p_full[b]);
+      first = false;
+      if (last) {
+        const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
+        const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
+        const int64_t sb = i - c.t, se = sb + c.row.units;  // the whole segment, from this CTA's first tile
+        const bool whole = sb >= 0 && se <= nt;
+        float fo = 1.f;
+        if (h < nh) {
+          if (whole) {
+            fo = out_factor(m, l, a.sink, h0 + h);
+            if (a.lse) a.lse[(int64_t)c.n * a.H + h0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          } else {
+            const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
+            *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + h) * 2) = make_float2(m, l);
+          }
+        }
+        f_sm[(nseg & 1) * kHeads + h] = fo;
+        tc::mbar_arrive(&fin[nseg & 1]);
+        ++nseg;
+        seg = i + 1;
+        first = true;
+        m = -INFINITY;
+        l = 0.f;
+        if (i + 1 < nt) {
+          attn::cp_async_wait_all();
+          attn::fence_proxy_async();
+          tc::mbar_arrive(q_full);
+        }
+        c = nx;
+      } else {
+        ++c.t;
+      }
+    }
+    attn::cp_async_wait_all();
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------------------------ O: rescaling, results, joins
+    const int quad = warp - 4, jt = tid - 128;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    bool first = true, ok = true;  // once a wait has run out the warp goes through the rest idle: the four meet at joins
+    int nseg = 0;
+    int64_t seg = 0;
+    for (int64_t i = 0; i < nt; ++i) {
+      const int b = (int)(i & 1);
+      ok = ok && warp_wait(&stat[b], par(i), abort_flag);
+      const bool rescale = ok && !first && (flags[2 * b] | flags[2 * b + 1]);
+      if (rescale) ok = warp_wait(&empty[b ^ 1], par(i - 1), abort_flag);
+      if (rescale && ok) {
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int cq = 0; cq < 4 * 4; ++cq) {
+          if ((cq >> 2) * 128 >= hd) break;
+          uint32_t v[16];
+          const uint32_t ta = tO + (uint32_t)(cq * 16) + lane_off;
+          float av[16];
+          attn::lds16(av, alpha_sm + b * kHeads + (cq & 3) * 16);
+          tc::tmem_ld16_wait(ta, v);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * av[k]);
+          attn::tmem_st16(ta, v);
+        }
+        attn::tmem_st_wait();
+        tc::tc_fence_before();
+      }
+      const bool last = last_of(i);
+      if (ok) tc::mbar_arrive(&p_full[b]);
+      first = false;
+      if (!last) {
+        ++c.t;
+        continue;
+      }
+      ok = ok && warp_wait(&fin[nseg & 1], (uint32_t)((nseg >> 1) & 1), abort_flag);
+      ok = ok && warp_wait(&empty[b], par(i), abort_flag);
+      tc::tc_fence_after();
+      const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
+      const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
+      const int64_t sb = i - c.t, se = sb + c.row.units;
+      const bool whole = sb >= 0 && se <= nt;
+      const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
+#pragma unroll 1
+      for (int cq = 0; cq < 4 * 2; ++cq) {
+        const int hh = (cq & 1) * 32, d = (cq >> 1) * 128 + quad * 32 + lane;
+        if (!ok || (cq >> 1) * 128 >= hd) break;
+        if (hh >= nh) continue;
+        float v[32];
+        attn::tmem_ld_32cols(tO + (uint32_t)((cq >> 1) * kHeads + hh) + lane_off, v);
+        if (whole) {
+          const float *f = f_sm + (nseg & 1) * kHeads + hh;
+          bf16 *o = a.o + (int64_t)c.n * a.o_t + (int64_t)(h0 + hh) * hd + (d & ~1);
+          const bool odd = lane & 1;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {  // two heads at a time: even lanes write the first, two features each
+            const float x = v[k] * f[k], y = v[k + 1] * f[k + 1];
+            const float z = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+            if (hh + k + (odd ? 1 : 0) < nh && d < hd)
+              *reinterpret_cast<__nv_bfloat162 *>(o + (int64_t)(k + (odd ? 1 : 0)) * hd) =
+                  odd ? __floats2bfloat162_rn(z, y) : __floats2bfloat162_rn(x, z);
+          }
+        } else if (d < hd) {
+          float *o = P.share_o + ((int64_t)slot * kHeads + hh) * kHD + d;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (hh + k < nh) o[k * kHD] = v[k];
+        }
+      }
+      tc::tc_fence_before();
+      if (!whole && all_agree(kJoinBar, 128, ok))
+        publish<kHeads, kHD, 128, kJoinBar>(P, jt, sb + rg.begin, se + rg.begin, rg, c.n, h0, nh,
+                                            reinterpret_cast<float *>(smem + L::join), join_flag);
+      first = true;
+      ++nseg;
+      seg = i + 1;
+      c.t = c.row.units - 1;
+      if (i + 1 < nt) advance(P, c);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t id1 = tc::idesc_bf16_f32(128, kUnit);
+      const uint32_t id2 = tc::idesc_bf16_f32(128, kHeads, /*a_mn_major=*/true, /*b_mn_major=*/false);
+      auto scores = [&](int b, int w) {  // quarter w of the features
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int kb = 2 * w; kb < min(2 * w + 2, nkb); ++kb) {
+          const uint64_t ad = tc::sdesc_sw128(s_q + kb * kBlock, 16, 1024);
+          const uint64_t bd = tc::sdesc_sw128(s_t + (b * kBlocks + kb) * kBlock, 16, 1024);
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+            tc::mma_bf16(tmem + (uint32_t)(b * kUnit), ad + 2ull * k4, bd + 2ull * k4, id1, (kb | k4) ? 1u : 0u);
+        }
+        if (w == 3) tc::mma_commit(&s_full[b]);
+      };
+      auto values = [&](int b, bool first) {
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch * 128 < hd; ++ch)
+#pragma unroll
+          for (int ii = 0; ii < kUnit / 16; ++ii) {
+            const uint64_t ad = tc::sdesc_sw128(s_t + (b * kBlocks + 2 * ch) * kBlock + ii * 2048, kBlock, 1024);
+            const uint64_t bd = tc::sdesc_sw128(s_p + b * kHeads * 128 + ii * 32, 16, 1024);
+            tc::mma_bf16(tO + (uint32_t)(ch * kHeads), ad, bd, id2, (first && ii == 0) ? 0u : 1u);
+          }
+        tc::mma_commit(&empty[b]);
+      };
+      bool ok = tc::mbar_wait(q_full, 0, abort_flag), first = true;
+      int nq = 1;  // segments whose q has been waited for
+      for (int w = 0; w < 4 && ok; ++w) {
+        ok = tc::mbar_wait(&full[w], 0, abort_flag);
+        if (ok) scores(0, w);
+      }
+      for (int64_t i = 0; i < nt && ok; ++i) {
+        const int b = (int)(i & 1), nb = b ^ 1;
+        const bool last = last_of(i);
+        // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
+        // only behind the values)
+        bool pv = false;
+        int w = i + 1 < nt ? 0 : 4;
+        const uint64_t t0 = tc::global_ns();
+        uint32_t spins = 0;
+        while (!pv || w < 4) {
+          if (!pv && tc::mbar_try_wait(&p_full[b], par(i))) {
+            values(b, first);
+            pv = true;
+            if (last && w < 4) {
+              if (!(ok = tc::mbar_wait(q_full, (uint32_t)(nq & 1), abort_flag))) break;
+              ++nq;
+            }
+            spins = 0;
+          } else if (w < 4 && (pv || !last) && tc::mbar_try_wait(&full[4 * nb + w], par(i + 1))) {
+            scores(nb, w);
+            ++w;
+            spins = 0;
+          } else if ((++spins & 63) == 0 && (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+        }
+        if (!ok) break;
+        first = last;
+        if (last) {
+          c.t = c.row.units - 1;
+          if (i + 1 < nt) advance(P, c);
+        } else {
+          ++c.t;
+        }
+      }
+      // nothing may still read shared memory, write TMEM or arrive when the CTA ends
+      tc::mma_commit(drain);
+      const uint64_t t0 = tc::global_ns();
+      while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t0 < tc::kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------------------ copies: warps 2, 3 even tiles, 8, 9 odd
+    const int b = warp >= 8 ? 1 : 0, half = warp & 1;
+    const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
+    const int cc = lane & 7;
+    if (b == 1 && nt > 1) advance(P, c);
+    for (int64_t i = b; i < nt; i += 2) {
+      const int j = c.t * kUnit + half * 32 + lane;
+      const bool there = j < c.row.rows;
+      const uint32_t pos = (uint32_t)(c.row.first + j), pg = P.page.div(pos);
+      const int id = there ? a.table[(int64_t)c.row.req * a.width + pg] : 0;
+      const bool good = there && id >= 0 && id < a.c.n_pages;
+      if (there && !good) atomicOr(a.status, kStatusBadIndex);
+      const int64_t off = good ? (int64_t)id * a.c.k_page + (int64_t)(pos - pg * P.page.d) * a.c.k_row +
+                                     (int64_t)(c.hg / P.sub) * a.c.k_head
+                               : -1;
+      const uint32_t mask = __ballot_sync(0xffffffffu, good);
+      int64_t ro[8];  // rows 4 u + lane / 8 of this warp's half
+#pragma unroll
+      for (int u = 0; u < 8; ++u) ro[u] = __shfl_sync(0xffffffffu, off, 4 * u + (lane >> 3));
+      if (i >= 2) {
+        if (!warp_wait(&empty[b], par(i) ^ 1u, abort_flag)) break;
+      }
+      if (lane == 0) masks[2 * b + half] = mask;
+      const uint32_t dst = s_t + b * kBlocks * kBlock + (half * 32 + (lane >> 3)) * 128;
+#pragma unroll
+      for (int kb = 0; kb < kBlocks; ++kb) {
+        const bool f_in = kb * 64 + cc * 8 < hd;
+        if (kb < nkb) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const bool in = ro[u] >= 0 && f_in;
+            const int r7 = (4 * u + (lane >> 3)) & 7;
+            attn::cp_async16(dst + kb * kBlock + u * 512 + ((cc ^ r7) << 4), in ? kbase + ro[u] + kb * 64 + cc * 8 : kbase, in);
+          }
+        }
+        if (kb & 1) asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      asm volatile("cp.async.wait_group 3;" ::: "memory");
+      attn::fence_proxy_async();
+      tc::mbar_arrive(&full[4 * b]);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      attn::fence_proxy_async();
+      tc::mbar_arrive(&full[4 * b + 1]);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      attn::fence_proxy_async();
+      tc::mbar_arrive(&full[4 * b + 2]);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      attn::fence_proxy_async();
+      tc::mbar_arrive(&full[4 * b + 3]);
+      if (i + 1 < nt) advance(P, c);
+      if (i + 2 < nt) advance(P, c);
+    }
+    attn::cp_async_wait_all();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_flag) atomicOr(a.status, kStatusTimeout);
+}
+
+}  // namespace latent
+
+cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+  using namespace latent;
+  static SmemAttr attr;
+  const size_t smem = L::total + 1024;
+  cudaError_t e = attr.ensure((const void *)k_paged_attn_latent, (int)smem);
+  if (e != cudaSuccess) return e;
+  const PagedAttnArgs &a = p.a;
+  p.g = a.H / a.c.kv_heads;
+  p.sub = (p.g + kHeads - 1) / kHeads;
+  p.Hg = p.sub * a.c.kv_heads;
+  const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
+  const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + kUnit - 1) / kUnit);
+  const int64_t grid = std::min<int64_t>(std::min<int64_t>(units, num_sms), kMaxCtas);
+  p.share_o = ws;
+  p.share_ml = ws + 2 * grid * kHeads * kHD;
+  if (sizeof(float) * 2 * grid * kHeads * (kHD + 2) > ws_bytes) return cudaErrorInvalidValue;
+  k_paged_attn_latent<<<(unsigned)grid, kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace csa

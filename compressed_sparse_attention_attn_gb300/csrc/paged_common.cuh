@@ -16,6 +16,7 @@
 #pragma once
 
 #include "csa_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace csa {
 namespace paged {
@@ -168,21 +169,30 @@ __device__ __forceinline__ float out_factor(float M, float L, const float *sink,
   return below == 0.f ? 0.f : em / below;
 }
 
-// Join `parts` shares, shares i of slots slot(i), of NH heads x HD features by the NT threads of the CTA.  fin: write
+// Barrier of the NT threads that join: the whole CTA (BAR 0) or named barrier BAR.
+template <int NT, int BAR>
+__device__ __forceinline__ void join_sync() {
+  if constexpr (BAR == 0)
+    __syncthreads();
+  else
+    tc::named_bar(BAR, NT);
+}
+
+// Join `parts` shares, shares i of slots slot(i), of NH heads x HD features by NT threads (tid of them).  fin: write
 // O and lse of heads h0 .. h0+nh-1 of row n; else the joined share to slot `to`.
 // sf: kJoinFloats<NH> floats of shared memory.
 template <int NH>
 constexpr int kJoinFloats = (kMaxJoin + 2) * NH;
-template <int NH, int HD, int NT, class Slot>
-__device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool fin, int to, int n, int h0, int nh, float *sf) {
+template <int NH, int HD, int NT, int BAR, class Slot>
+__device__ __forceinline__ void join(const Params &P, int tid, int parts, Slot slot, bool fin, int to, int n, int h0, int nh,
+                                     float *sf) {
   const PagedAttnArgs &a = P.a;
   float *sM = sf + kMaxJoin * NH, *sL = sM + NH;
-  const int tid = threadIdx.x;
   for (int i = tid; i < parts * nh; i += NT) {
     const int p = i / nh, h = i % nh;
     sf[p * NH + h] = __ldcg(P.share_ml + ((int64_t)slot(p) * NH + h) * 2);
   }
-  __syncthreads();
+  join_sync<NT, BAR>();
   if (tid < nh) {
     float M = -INFINITY;
     for (int p = 0; p < parts; ++p) M = fmaxf(M, sf[p * NH + tid]);
@@ -202,7 +212,7 @@ __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool
       sM[tid] = M;
     }
   }
-  __syncthreads();
+  join_sync<NT, BAR>();
   const int hd = a.c.head_dim;
   for (int i = tid; i < nh * (HD / 4); i += NT) {
     const int h = i / (HD / 4), d = (i % (HD / 4)) * 4;
@@ -236,32 +246,32 @@ __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool
     float2 ml = make_float2(sM[tid], sL[tid]);
     *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)to * NH + tid) * 2) = ml;
   }
-  __syncthreads();
+  join_sync<NT, BAR>();
 }
 
-// Publish this CTA's share of the segment of units [sb, se) (already written to its slot by all threads) and join
-// what it completes.  flag: an int in shared memory.
-template <int NH, int HD, int NT>
-__device__ __forceinline__ void publish(const Params &P, int64_t sb, int64_t se, const Range &r, int n, int h0, int nh,
+// Publish this CTA's share of the segment of units [sb, se) (already written to its slot by the NT threads, or
+// by threads they have synchronised with) and join what it completes.  flag: an int in shared memory.
+template <int NH, int HD, int NT, int BAR>
+__device__ __forceinline__ void publish(const Params &P, int tid, int64_t sb, int64_t se, const Range &r, int n, int h0, int nh,
                                         float *sf, int *flag) {
   const int c0 = cta_of(sb, r), c1 = cta_of(se - 1, r);
   const int parts = c1 - c0 + 1, mine = (int)blockIdx.x - c0, grp = mine / kJoin, ngrp = (parts + kJoin - 1) / kJoin;
   const int in_grp = min(kJoin, parts - grp * kJoin);
   auto slot_of = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
-  __syncthreads();
-  if (threadIdx.x == 0) {
+  join_sync<NT, BAR>();
+  if (tid == 0) {
     int *ctr = grp == 0 ? P.counters + kMaxCtas + c0 : P.counters + c0 + grp * kJoin;
     *flag = arrive_last(ctr, in_grp) ? 1 : 0;
   }
-  __syncthreads();
+  join_sync<NT, BAR>();
   if (!*flag) return;
   const int first = grp * kJoin;
-  join<NH, HD, NT>(P, in_grp, [&](int p) { return slot_of(first + p); }, ngrp == 1, slot_of(first), n, h0, nh, sf);
+  join<NH, HD, NT, BAR>(P, tid, in_grp, [&](int p) { return slot_of(first + p); }, ngrp == 1, slot_of(first), n, h0, nh, sf);
   if (ngrp == 1) return;
-  if (threadIdx.x == 0) *flag = arrive_last(P.counters + 2 * kMaxCtas + c0, ngrp) ? 1 : 0;
-  __syncthreads();
+  if (tid == 0) *flag = arrive_last(P.counters + 2 * kMaxCtas + c0, ngrp) ? 1 : 0;
+  join_sync<NT, BAR>();
   if (!*flag) return;
-  join<NH, HD, NT>(P, ngrp, [&](int p) { return slot_of(p * kJoin); }, true, 0, n, h0, nh, sf);
+  join<NH, HD, NT, BAR>(P, tid, ngrp, [&](int p) { return slot_of(p * kJoin); }, true, 0, n, h0, nh, sf);
 }
 
 }  // namespace paged
