@@ -617,7 +617,7 @@ int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, 
   csa::NormRopeArgs a{(const bf16 *)q, (const bf16 *)k, (const bf16 *)(cache->v ? v : nullptr), q_t, q_h, k_t, k_h, v_t, v_h, N,
                       q ? H : 0, *cache, pos, slot, q_norm, k_norm, eps, tab, tab_rows, rd, at, half ? 1 : 0,
                       (bf16 *)q_out, o_t, o_h, ctx->status};
-  CSA_CUDA(csa::launch_norm_rope(a, (cudaStream_t)stream), who);
+  CSA_CUDA(csa::launch_norm_rope(a, ctx->num_sms, (cudaStream_t)stream), who);
   return CSA_OK;
 }
 

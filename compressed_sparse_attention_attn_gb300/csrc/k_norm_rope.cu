@@ -36,170 +36,255 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
 }
 
 // 8 floats of w at feature f (ones where w is NULL)
-__device__ __forceinline__ void load_w(const float *w, int f, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = w ? __ldg(w + f + e) : 1.f;
-}
-
-// Turn the 8 normed features y at f .. f+7 of a row.  xr: the row's bf16 values in memory, scale r and weights w for
-// the partners.  FAST: the turned part starts and ends on vector borders, as do its halves.
 template <bool FAST>
-__device__ __forceinline__ void turn(const NormRopeArgs &a, const bf16 *xr, const uint4 &partner, const float2 *tp, float r,
-                                     const float *w, int f, float (&y)[8]) {
-  const int h2 = a.rd >> 1;
-  if (FAST) {
-    if (f < a.at || f >= a.at + a.rd) return;
-    if (a.half) {
-      const bool low = f < a.at + h2;
-      const int i0 = low ? f - a.at : f - a.at - h2;
-      float z[8], wz[8];
-      unpack(partner, z);
-      load_w(w, low ? f + h2 : f - h2, wz);
+__device__ __forceinline__ void load_w(const float *w, int f, float (&v)[8]) {
+  if (!w) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float4 cs = __ldg(reinterpret_cast<const float4 *>(tp + i0 + e));
-        const float z0 = z[e] * r * wz[e], z1 = z[e + 1] * r * wz[e + 1];
-        y[e] = low ? y[e] * cs.x - z0 * cs.y : z0 * cs.y + y[e] * cs.x;
-        y[e + 1] = low ? y[e + 1] * cs.z - z1 * cs.w : z1 * cs.w + y[e + 1] * cs.z;
-      }
-    } else {
-      const int i0 = (f - a.at) >> 1;
+    for (int e = 0; e < 8; ++e) v[e] = 1.f;
+  } else if (FAST) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 cs = __ldg(reinterpret_cast<const float4 *>(tp + i0 + e / 2));
-        const float a0 = y[e], b0 = y[e + 1], a1 = y[e + 2], b1 = y[e + 3];
-        y[e] = a0 * cs.x - b0 * cs.y;
-        y[e + 1] = a0 * cs.y + b0 * cs.x;
-        y[e + 2] = a1 * cs.z - b1 * cs.w;
-        y[e + 3] = a1 * cs.w + b1 * cs.z;
-      }
+    for (int e = 0; e < 8; e += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(w + f + e));
+      v[e] = x.x;
+      v[e + 1] = x.y;
+      v[e + 2] = x.z;
+      v[e + 3] = x.w;
     }
   } else {
-    float out[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = f + e - a.at;  // feature of the turned part
-      out[e] = y[e];
-      if (d < 0 || d >= a.rd) continue;
-      const bool first = a.half ? d < h2 : !(d & 1);
-      const int i = a.half ? (first ? d : d - h2) : d >> 1;
-      const int fp = a.half ? (first ? f + e + h2 : f + e - h2) : (first ? f + e + 1 : f + e - 1);
-      const float z = __bfloat162float(xr[fp]) * r * (w ? __ldg(w + fp) : 1.f);
-      const float2 cs = __ldg(tp + i);
-      out[e] = first ? y[e] * cs.x - z * cs.y : z * cs.y + y[e] * cs.x;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = out[e];
+    for (int e = 0; e < 8; ++e) v[e] = __ldg(w + f + e);
   }
 }
 
-// G lanes a row, V vectors a lane (head_dim <= 8 G V).  Items are (token, head) with a token's query, key and value
-// heads in a row.
-template <int G, int V, bool FAST>
-__global__ void __launch_bounds__(kThreads) k_norm_rope(NormRopeArgs a, int per_token, int64_t items) {
+// The (cos, sin) that the 8 features from f on are turned by, and the sign with which the partner enters: (y, z) ->
+// y c + z s' with s' = -s for the first of a pair.  FAST: the turned part and its halves start and end on
+// vector borders.  Outside the turned part: c = 1, s' = 0.
+template <bool FAST>
+__device__ __forceinline__ void load_angles(const NormRopeArgs &a, const float2 *tp, int f, float (&c)[8], float (&s)[8]) {
+  const int h2 = a.rd >> 1;
+  if (FAST && (f < a.at || f >= a.at + a.rd)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+  } else if (FAST && a.half) {
+    const bool low = f < a.at + h2;
+    const int i0 = low ? f - a.at : f - a.at - h2;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(tp + i0 + e));
+      c[e] = x.x;
+      c[e + 1] = x.z;
+      s[e] = low ? -x.y : x.y;
+      s[e + 1] = low ? -x.w : x.w;
+    }
+  } else if (FAST) {
+    const int i0 = (f - a.at) >> 1;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(tp + i0 + e / 2));
+      c[e] = c[e + 1] = x.x;
+      s[e] = -x.y;
+      s[e + 1] = x.y;
+      c[e + 2] = c[e + 3] = x.z;
+      s[e + 2] = -x.w;
+      s[e + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = f + e - a.at;  // feature of the turned part
+      c[e] = 1.f;
+      s[e] = 0.f;
+      if (d < 0 || d >= a.rd) continue;
+      const bool first = a.half ? d < h2 : !(d & 1);
+      const float2 x = __ldg(tp + (a.half ? (first ? d : d - h2) : d >> 1));
+      c[e] = x.x;
+      s[e] = first ? -x.y : x.y;
+    }
+  }
+}
+
+// The partners' normed values (before the scale r): features half the turned part away, from the row in memory.
+template <bool FAST>
+__device__ __forceinline__ void load_partners(const NormRopeArgs &a, const bf16 *x, int f, uint4 &z) {
+  const int h2 = a.rd >> 1;
+  z = make_uint4(0, 0, 0, 0);
+  if (FAST) {
+    if (f >= a.at && f < a.at + a.rd) z = *reinterpret_cast<const uint4 *>(x + (f < a.at + h2 ? f + h2 : f - h2));
+  } else {
+    bf16 *zb = reinterpret_cast<bf16 *>(&z);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = f + e - a.at;
+      if (d >= 0 && d < a.rd) zb[e] = x[d < h2 ? f + e + h2 : f + e - h2];
+    }
+  }
+}
+template <bool FAST>
+__device__ __forceinline__ void load_partner_w(const NormRopeArgs &a, const float *w, int f, float (&v)[8]) {
+  const int h2 = a.rd >> 1;
+  if (FAST) {
+    load_w<true>(w, f >= a.at && f < a.at + a.rd ? (f < a.at + h2 ? f + h2 : f - h2) : f, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int d = f + e - a.at;
+      v[e] = w && d >= 0 && d < a.rd ? __ldg(w + (d < h2 ? f + e + h2 : f + e - h2)) : 1.f;
+    }
+  }
+}
+
+// G lanes a row, V vectors a lane (head_dim <= 8 G V), U heads of one token a group: the norm's weights and the token's
+// angles are read once for them, and U V vectors are in flight a lane.  Items are (token, block of U heads), a
+// token's query, key and value heads in a row.
+template <int G, int V, int U, bool HALF, bool FAST>
+__global__ void __launch_bounds__(kThreads, HALF || V == 4 ? 2 : 3) k_norm_rope(const __grid_constant__ NormRopeArgs a, int q_blocks, int k_blocks,
+                                                        int per_token, int64_t items) {
   const int lane = threadIdx.x & (G - 1);
-  const int hd = a.c.head_dim, Hk = a.c.kv_heads;
+  const int hd = a.c.head_dim;
   const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G;
   const bool in = item < items;
   const int n = in ? (int)(item / per_token) : 0;
-  const int h = in ? (int)(item - (int64_t)n * per_token) : 0;
-  const int kind = h < a.H ? 0 : (h < a.H + Hk ? 1 : 2);  // query, key, value
-  const int hh = kind == 0 ? h : (kind == 1 ? h - a.H : h - a.H - Hk);
+  const int jb = in ? (int)(item - (int64_t)n * per_token) : 0;
+  const int kind = jb < q_blocks ? 0 : (jb < q_blocks + k_blocks ? 1 : 2);  // query, key, value
+  const int h0 = (kind == 0 ? jb : (kind == 1 ? jb - q_blocks : jb - q_blocks - k_blocks)) * U;
+  const int nh = min(U, (kind == 0 ? a.H : a.c.kv_heads) - h0);
   const int p = in ? a.pos[n] : -1;
   const int64_t rows = (int64_t)a.c.n_pages * a.c.page;
   const int64_t slot = !in ? -1 : (a.slot ? a.slot[n] : n);
   bool live = in && p >= 0;
-  const bool bad = live && ((a.rd > 0 && p >= a.tab_rows) || slot < -1 || slot >= rows);
-  if (bad) {
-    if (h == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
+  if (live && ((a.rd > 0 && p >= a.tab_rows) || slot < -1 || slot >= rows)) {
+    if (jb == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
     live = false;
   }
   if (kind != 0 && slot < 0) live = false;
-  const bf16 *x = kind == 0 ? a.q + n * a.q_t + hh * a.q_h
-                            : (kind == 1 ? a.k + n * a.k_t + hh * a.k_h : a.v + n * a.v_t + hh * a.v_h);
+  const int64_t x_h = kind == 0 ? a.q_h : (kind == 1 ? a.k_h : a.v_h);
+  const bf16 *x = (kind == 0 ? a.q + n * a.q_t : (kind == 1 ? a.k + n * a.k_t : a.v + n * a.v_t)) + h0 * x_h;
+  int64_t y_h;
   bf16 *y;
   if (kind == 0) {
-    y = a.q_out + n * a.o_t + hh * a.o_h;
+    y_h = a.o_h;
+    y = a.q_out + n * a.o_t + h0 * y_h;
   } else {
-    const int64_t pg = live ? slot / a.c.page : 0, row = live ? slot % a.c.page : 0;
-    y = kind == 1 ? reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row + hh * a.c.k_head
-                  : reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row + hh * a.c.v_head;
+    const int64_t pg = live ? slot / a.c.page : 0, row = live ? slot - pg * a.c.page : 0;
+    y_h = kind == 1 ? a.c.k_head : a.c.v_head;
+    y = (kind == 1 ? reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row
+                   : reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row) + h0 * y_h;
   }
-  const int h2 = a.rd >> 1;
   const bool turns = kind != 2 && a.rd > 0;
-  uint4 xv[V], xp[V];
-  float ss = 0.f;
+  uint4 xv[U][V], xp[U][V];  // (xp: the partners, where they are not the vector's own)
 #pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int f = 8 * (lane + G * u);
-    xv[u] = xp[u] = make_uint4(0, 0, 0, 0);
-    if (live && f < hd) {
-      xv[u] = *reinterpret_cast<const uint4 *>(x + f);
-      if (FAST && turns && a.half && f >= a.at && f < a.at + a.rd)
-        xp[u] = *reinterpret_cast<const uint4 *>(x + (f < a.at + h2 ? f + h2 : f - h2));
+  for (int t = 0; t < U; ++t)
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int f = 8 * (lane + G * u);
+      xv[t][u] = xp[t][u] = make_uint4(0, 0, 0, 0);
+      if (live && t < nh && f < hd) {
+        xv[t][u] = *reinterpret_cast<const uint4 *>(x + t * x_h + f);
+        if (HALF && turns) load_partners<FAST>(a, x + t * x_h, f, xp[t][u]);
+      }
     }
-  }
-  float r = 1.f;
   const float *w = kind == 0 ? a.q_norm : a.k_norm;
+  float r[U];
 #pragma unroll
-  for (int u = 0; u < V; ++u) {
-    float v[8];
-    unpack(xv[u], v);
+  for (int t = 0; t < U; ++t) {
+    float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-  }
+    for (int u = 0; u < V; ++u) {
+      float v[8];
+      unpack(xv[t][u], v);
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (kind != 2 && w) r = 1.0f / sqrtf(ss / (float)hd + a.eps);
-  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)(live && a.rd > 0 ? p : 0) * h2;
-  uint4 out[V];
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int f = 8 * (lane + G * u);
-    out[u] = xv[u];
-    if (live && f < hd && kind != 2) {
-      float v[8], wv[8];
-      unpack(xv[u], v);
-      load_w(w, f, wv);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= r * wv[e];
-      if (turns) turn<FAST>(a, x, xp[u], tp, r, w, f, v);
-      out[u] = pack(v);
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
     }
+    r[t] = ss;
   }
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int t = 0; t < U; ++t) r[t] += __shfl_xor_sync(0xffffffffu, r[t], o);
+#pragma unroll
+  for (int t = 0; t < U; ++t) r[t] = w ? 1.0f / sqrtf(r[t] / (float)hd + a.eps) : 1.f;
   __syncwarp();  // (q_out may be q: every lane has read its partners)
+  if (!live) return;
+  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)(a.rd > 0 ? p : 0) * (a.rd >> 1);
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int f = 8 * (lane + G * u);
-    if (live && f < hd) *reinterpret_cast<uint4 *>(y + f) = out[u];
+    if (f >= hd) continue;
+    if (kind == 2) {
+#pragma unroll
+      for (int t = 0; t < U; ++t)
+        if (t < nh) *reinterpret_cast<uint4 *>(y + t * y_h + f) = xv[t][u];
+      continue;
+    }
+    float wv[8], c[8], s[8], wp[8];
+    load_w<FAST>(w, f, wv);
+    if (turns) {
+      load_angles<FAST>(a, tp, f, c, s);
+      if (HALF) load_partner_w<FAST>(a, w, f, wp);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // the weights into the angles: the value's own, its partner's
+        s[e] *= HALF ? wp[e] : wv[e ^ 1];
+        c[e] *= wv[e];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      if (t >= nh) continue;
+      float v[8], o[8];
+      unpack(xv[t][u], v);
+      if (turns) {
+        float z[8];
+        if (HALF) {
+          unpack(xp[t][u], z);
+        } else {  // (outside the turned part there is no partner, which may be infinite)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[e] = f + e >= a.at && f + e < a.at + a.rd ? v[e ^ 1] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = r[t] * fmaf(v[e], c[e], z[e] * s[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = r[t] * (v[e] * wv[e]);
+      }
+      *reinterpret_cast<uint4 *>(y + t * y_h + f) = pack(o);
+    }
   }
 }
 
-template <int G, int V>
+template <int G, int V, int U>
 cudaError_t launch(const NormRopeArgs &a, cudaStream_t s) {
-  const int per_token = a.H + a.c.kv_heads * (a.v ? 2 : 1);
+  const int q_blocks = (a.H + U - 1) / U, k_blocks = (a.c.kv_heads + U - 1) / U;
+  const int per_token = q_blocks + k_blocks * (a.v ? 2 : 1);
   const int64_t items = (int64_t)a.N * per_token;
   const int64_t blocks = (items * G + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  // vectors of angles and partners: the turned part (and its halves) on vector borders, 16-byte angles
-  const bool fast = a.at % 8 == 0 && a.rd % (a.half ? 16 : 8) == 0 && ((uintptr_t)a.tab & 15) == 0;
-  if (fast)
-    k_norm_rope<G, V, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, per_token, items);
-  else
-    k_norm_rope<G, V, false><<<(unsigned)blocks, kThreads, 0, s>>>(a, per_token, items);
+  // vectors of weights, angles and partners: 16-byte aligned, the turned part (and its halves) on vector borders
+  const bool fast = a.at % 8 == 0 && a.rd % (a.half ? 16 : 8) == 0 &&
+                    (((uintptr_t)a.tab | (uintptr_t)a.q_norm | (uintptr_t)a.k_norm) & 15) == 0;
+  auto *k = a.half ? (fast ? k_norm_rope<G, V, U, true, true> : k_norm_rope<G, V, U, true, false>)
+                   : (fast ? k_norm_rope<G, V, U, false, true> : k_norm_rope<G, V, U, false, false>);
+  k<<<(unsigned)blocks, kThreads, 0, s>>>(a, q_blocks, k_blocks, per_token, items);
   return cudaGetLastError();
+}
+
+// Several heads a group once that leaves every SM with a full complement of warps; fewer rows take one head a group,
+// which spreads them over more SMs.
+template <int G, int V, int U>
+cudaError_t launch_sized(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
+  const int64_t threads = (int64_t)a.N * (a.H + a.c.kv_heads * (a.v ? 2 : 1)) * G;
+  return threads >= (int64_t)num_sms * 2048 * U ? launch<G, V, U>(a, s) : launch<G, V, 1>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s) {
+cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
   const int hd = a.c.head_dim;
-  if (hd <= 32) return launch<4, 1>(a, s);
-  if (hd <= 64) return launch<8, 1>(a, s);
-  if (hd <= 128) return launch<16, 1>(a, s);
-  if (hd <= 256) return launch<32, 1>(a, s);
-  if (hd <= 512) return launch<32, 2>(a, s);
-  return launch<32, 4>(a, s);
+  if (hd <= 32) return launch_sized<4, 1, 4>(a, num_sms, s);
+  if (hd <= 64) return launch_sized<8, 1, 4>(a, num_sms, s);
+  if (hd <= 128) return launch_sized<16, 1, 4>(a, num_sms, s);
+  if (hd <= 256) return launch_sized<32, 1, 4>(a, num_sms, s);
+  if (hd <= 512) return launch_sized<32, 2, 2>(a, num_sms, s);
+  return launch<32, 4, 1>(a, s);
 }
 
 }  // namespace csa

@@ -14,7 +14,7 @@
 // maxima, sums and O are f32.
 //
 // Shared memory holds q (64 KB) and two tiles (64 KB each), so that one is in flight while the other is used:
-// 64 KB an SM in flight covers the copy rate's latency twice.  A pair of warps serves each tile buffer (cp.async
+// 64 KB an SM in flight covers the copy rate's latency twice.  Four warps serve each tile buffer (cp.async
 // from the page of each position, 16 bytes a lane, rows past the end as zeros), and signals it a quarter of the
 // features at a time; one thread issues whichever product is ready first, the next tile's scores or
 // this tile's values, so a buffer is handed back as soon as its weights are there.  Two warps do the softmax, and
@@ -35,19 +35,17 @@ constexpr int kHeads = 64;              // query heads of a head group
 constexpr int kUnit = 64;               // positions of a tile
 constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile (and of q)
 constexpr int kBlocks = kHD / 64;
-constexpr int kThreads = 352;           // warps 0, 1 softmax; 2, 3 and 8, 9 copies; 4-7 O; 10 products
-constexpr int kJoinBar = 1;             // named barrier of warps 4-7
+constexpr int kThreads = 512;           // warps 0, 1 softmax; 2 products; 4-7 O; 8-11 and 12-15 copies (a buffer each)
 
 struct L {
   static constexpr size_t q = 0;                                             // [8][64][128 B]
   static constexpr size_t t = q + (size_t)kBlocks * kBlock;                  // [2][8][64][128 B]
   static constexpr size_t p = t + (size_t)2 * kBlocks * kBlock;              // [2][64][128 B]
-  static constexpr size_t join = p + (size_t)2 * kHeads * 128;               // float
-  static constexpr size_t alpha = join + sizeof(float) * kJoinFloats<kHeads>;  // float [2][64]
+  static constexpr size_t alpha = p + (size_t)2 * kHeads * 128;              // float [2][64]
   static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
-  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [15]
-  static constexpr size_t bars = scan + 16 * 8;                              // u64 [20]
-  static constexpr size_t misc = bars + 20 * 8;                              // masks [2][2], flags, slot, abort
+  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [20]
+  static constexpr size_t bars = scan + 20 * 8;                              // u64 [26]
+  static constexpr size_t misc = bars + 26 * 8;                              // masks [2][4], flags, slot, abort
   static constexpr size_t total = misc + 64;
 };
 static_assert(L::total + 1024 <= 232448, "one CTA's shared memory");
@@ -57,18 +55,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   const bool ok = tc::mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
-// Whether all `count` threads of named barrier `id` say yes.
-__device__ __forceinline__ bool all_agree(int id, int count, bool yes) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"(yes ? 1u : 0u)
-      : "memory");
-  return r != 0;
+// 2^x for x <= 8; results below the smallest normal number are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 struct Cursor {
@@ -97,20 +88,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
   const uint32_t s_q = tc::smem_u32(smem + L::q), s_t = tc::smem_u32(smem + L::t), s_p = tc::smem_u32(smem + L::p);
   float *alpha_sm = reinterpret_cast<float *>(smem + L::alpha), *f_sm = reinterpret_cast<float *>(smem + L::f);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
-  // full [2][4]: a quarter of the features of a tile has landed; empty [2]: its values have been used
-  uint64_t *full = bars, *empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12, *stat = bars + 14, *fin = bars + 16,
-           *q_full = bars + 18, *drain = bars + 19;
-  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::misc);  // [2][2]: positions of a tile that are there
-  int *flags = reinterpret_cast<int *>(masks + 4);                 // [2][2]: a maximum was raised (by warp)
-  int *join_flag = flags + 4;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(join_flag + 1);
+  // full, empty [2][4]: a quarter of the features of a tile has landed, has been used
+  uint64_t *full = bars, *empty = bars + 8, *s_full = bars + 16, *p_full = bars + 18, *stat = bars + 20, *fin = bars + 22,
+           *q_full = bars + 24, *drain = bars + 25;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::misc);  // [2][4]: positions of a tile that are there (16 each)
+  int *flags = reinterpret_cast<int *>(masks + 8);                 // [2][2]: a maximum was raised (by warp)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(flags + 4);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   const int nkb = (hd + 63) / 64;
 
   const Range rg = find_range<kUnit, kThreads>(P, reinterpret_cast<int64_t *>(smem + L::scan));
-  if (rg.begin >= rg.end) return;
+  if (rg.begin >= rg.end) {
+    if (tid == 0 && !P.by_segment) P.split[blockIdx.x] = make_int2(0, 0);
+    return;
+  }
   const int64_t nt = rg.end - rg.begin;  // this CTA's tiles
   Cursor c;
   c.n = rg.row;
@@ -121,9 +114,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     c.t = (int)(in - (int64_t)c.hg * c.row.units);
   }
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) tc::mbar_init(&full[i], 64);
+    for (int i = 0; i < 8; ++i) {
+      tc::mbar_init(&full[i], 128);  // the lanes of the buffer's four warps
+      tc::mbar_init(&empty[i], 1);
+    }
     for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&empty[b], 1);
       tc::mbar_init(&s_full[b], 1);
       tc::mbar_init(&p_full[b], 64 + 128);
       tc::mbar_init(&stat[b], 64);
@@ -135,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 10) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == 2) tc::tmem_alloc(tmem_slot, 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -172,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     for (int64_t i = 0; i < nt; ++i) {
       const int b = (int)(i & 1);
       if (!warp_wait(&full[4 * b + 3], par(i), abort_flag)) break;  // (its mask)
-      const uint32_t ok0 = masks[2 * b], ok1 = masks[2 * b + 1];
+      const uint32_t ok0 = masks[4 * b] | masks[4 * b + 1] << 16, ok1 = masks[4 * b + 2] | masks[4 * b + 3] << 16;
       if (!warp_wait(&s_full[b], par(i), abort_flag)) break;
       tc::tc_fence_after();
       const bool last = last_of(i);
@@ -192,20 +187,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
 #pragma unroll
         for (int k = 0; k < 32; ++k) s[32 + k] = v[k];
       }
-      float mx = -INFINITY;
-      if ((ok0 & ok1) == 0xffffffffu) {
+      float sc = P.scale_log2;
+      if ((ok0 & ok1) != 0xffffffffu) {  // positions that are not there: -inf (scaled here, so that a scale of 0 is right)
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          s[k] *= P.scale_log2;
-          mx = fmaxf(mx, s[k]);
-        }
+        for (int k = 0; k < 64; ++k) s[k] = ((k < 32 ? ok0 : ok1) >> (k & 31)) & 1u ? s[k] * sc : -INFINITY;
+        sc = 1.f;
+      }
+      float mx = s[0];  // the largest scaled score, of a scale of either sign
+      if (sc < 0.f) {
+#pragma unroll
+        for (int k = 1; k < 64; ++k) mx = fminf(mx, s[k]);
       } else {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          s[k] = ((k < 32 ? ok0 : ok1) >> (k & 31)) & 1u ? s[k] * P.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s[k]);
-        }
+        for (int k = 1; k < 64; ++k) mx = fmaxf(mx, s[k]);
       }
+      mx *= sc;
       float al = 1.f;
       bool raised = false;
       if (first) {
@@ -227,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = exp2f(s[k + 2 * e] - ref), y = exp2f(s[k + 2 * e + 1] - ref);
+          const float x = ex2(fmaf(s[k + 2 * e], sc, -ref)), y = ex2(fmaf(s[k + 2 * e + 1], sc, -ref));
           sum += x + y;
           const __nv_bfloat162 pk = __floats2bfloat162_rn(x, y);
           w[e] = *reinterpret_cast<const uint32_t *>(&pk);
@@ -278,15 +274,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     // ------------------------------------------------------------------------------ O: rescaling, results, joins
     const int quad = warp - 4, jt = tid - 128;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    bool first = true, ok = true;  // once a wait has run out the warp goes through the rest idle: the four meet at joins
+    bool first = true, told = false;
     int nseg = 0;
     int64_t seg = 0;
     for (int64_t i = 0; i < nt; ++i) {
       const int b = (int)(i & 1);
-      ok = ok && warp_wait(&stat[b], par(i), abort_flag);
-      const bool rescale = ok && !first && (flags[2 * b] | flags[2 * b + 1]);
-      if (rescale) ok = warp_wait(&empty[b ^ 1], par(i - 1), abort_flag);
-      if (rescale && ok) {
+      if (!warp_wait(&stat[b], par(i), abort_flag)) break;
+      if (!first && (flags[2 * b] | flags[2 * b + 1])) {
+        if (!warp_wait(&empty[4 * (b ^ 1) + 3], par(i - 1), abort_flag)) break;
         tc::tc_fence_after();
 #pragma unroll 1
         for (int cq = 0; cq < 4 * 4; ++cq) {
@@ -304,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
         tc::tc_fence_before();
       }
       const bool last = last_of(i);
-      if (ok) tc::mbar_arrive(&p_full[b]);
+      tc::mbar_arrive(&p_full[b]);
       first = false;
       if (!last) {
         ++c.t;
         continue;
       }
-      ok = ok && warp_wait(&fin[nseg & 1], (uint32_t)((nseg >> 1) & 1), abort_flag);
-      ok = ok && warp_wait(&empty[b], par(i), abort_flag);
+      if (!warp_wait(&fin[nseg & 1], (uint32_t)((nseg >> 1) & 1), abort_flag)) break;
+      if (!warp_wait(&empty[4 * b + 3], par(i), abort_flag)) break;
       tc::tc_fence_after();
       const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
       const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
@@ -321,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
 #pragma unroll 1
       for (int cq = 0; cq < 4 * 2; ++cq) {
         const int hh = (cq & 1) * 32, d = (cq >> 1) * 128 + quad * 32 + lane;
-        if (!ok || (cq >> 1) * 128 >= hd) break;
+        if ((cq >> 1) * 128 >= hd) break;
         if (hh >= nh) continue;
         float v[32];
         attn::tmem_ld_32cols(tO + (uint32_t)((cq >> 1) * kHeads + hh) + lane_off, v);
@@ -345,102 +340,140 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
         }
       }
       tc::tc_fence_before();
-      if (!whole && all_agree(kJoinBar, 128, ok))
-        publish<kHeads, kHD, 128, kJoinBar>(P, jt, sb + rg.begin, se + rg.begin, rg, c.n, h0, nh,
-                                            reinterpret_cast<float *>(smem + L::join), join_flag);
+      if (seg == sb && jt == 0) {  // (the segment begins here)
+        const int parts = whole ? 0 : cta_of(se + rg.begin - 1, rg) - (int)blockIdx.x + 1;
+        if (P.by_segment) {
+          P.split[(int64_t)c.n * P.Hg + c.hg] = make_int2(blockIdx.x, parts);
+        } else if (!whole) {
+          P.split[blockIdx.x] = make_int2(c.n * P.Hg + c.hg, parts);
+          told = true;
+        }
+      }
       first = true;
       ++nseg;
       seg = i + 1;
       c.t = c.row.units - 1;
       if (i + 1 < nt) advance(P, c);
     }
-  } else if (warp == 10) {
+    if (!P.by_segment && jt == 0 && !told) P.split[blockIdx.x] = make_int2(0, 0);
+  } else if (warp == 2) {
     // ------------------------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t id1 = tc::idesc_bf16_f32(128, kUnit);
-      const uint32_t id2 = tc::idesc_bf16_f32(128, kHeads, /*a_mn_major=*/true, /*b_mn_major=*/false);
-      auto scores = [&](int b, int w) {  // quarter w of the features
-        tc::tc_fence_after();
-#pragma unroll 1
-        for (int kb = 2 * w; kb < min(2 * w + 2, nkb); ++kb) {
-          const uint64_t ad = tc::sdesc_sw128(s_q + kb * kBlock, 16, 1024);
-          const uint64_t bd = tc::sdesc_sw128(s_t + (b * kBlocks + kb) * kBlock, 16, 1024);
+    // The whole warp goes through the loop, one elected lane issues: the operands' descriptors then stay in uniform
+    // registers (issued from a one-lane branch each product cost about 115 cycles, of which it computes 48).
+    const uint32_t id1 = tc::idesc_bf16_f32(128, kUnit);
+    const uint32_t id2 = tc::idesc_bf16_f32(128, kHeads, /*a_mn_major=*/true, /*b_mn_major=*/false);
+    const uint64_t dq = tc::sdesc_sw128(s_q, 16, 1024), dk = tc::sdesc_sw128(s_t, 16, 1024),
+                   dv = tc::sdesc_sw128(s_t, kBlock, 1024), dp = tc::sdesc_sw128(s_p, 16, 1024);
+    constexpr uint64_t kStep = kBlock >> 4;  // a block, in descriptor units
+    auto block = [&](int b, int kb) {        // (by the elected lane) the scores' products over 64 features
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4)
-            tc::mma_bf16(tmem + (uint32_t)(b * kUnit), ad + 2ull * k4, bd + 2ull * k4, id1, (kb | k4) ? 1u : 0u);
-        }
+      for (int k4 = 0; k4 < 4; ++k4)
+        tc::mma_bf16(tmem + (uint32_t)(b * kUnit), dq + kb * kStep + 2 * k4, dk + (b * kBlocks + kb) * kStep + 2 * k4, id1,
+                     (kb | k4) ? 1u : 0u);
+    };
+    auto scores = [&](int b, int w) {  // quarter w of the features
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+        if (2 * w < nkb) block(b, 2 * w);
+        if (2 * w + 1 < nkb) block(b, 2 * w + 1);
         if (w == 3) tc::mma_commit(&s_full[b]);
-      };
-      auto values = [&](int b, bool first) {
-        tc::tc_fence_after();
-#pragma unroll 1
-        for (int ch = 0; ch * 128 < hd; ++ch)
-#pragma unroll
-          for (int ii = 0; ii < kUnit / 16; ++ii) {
-            const uint64_t ad = tc::sdesc_sw128(s_t + (b * kBlocks + 2 * ch) * kBlock + ii * 2048, kBlock, 1024);
-            const uint64_t bd = tc::sdesc_sw128(s_p + b * kHeads * 128 + ii * 32, 16, 1024);
-            tc::mma_bf16(tO + (uint32_t)(ch * kHeads), ad, bd, id2, (first && ii == 0) ? 0u : 1u);
-          }
-        tc::mma_commit(&empty[b]);
-      };
-      bool ok = tc::mbar_wait(q_full, 0, abort_flag), first = true;
-      int nq = 1;  // segments whose q has been waited for
-      for (int w = 0; w < 4 && ok; ++w) {
-        ok = tc::mbar_wait(&full[w], 0, abort_flag);
-        if (ok) scores(0, w);
       }
-      for (int64_t i = 0; i < nt && ok; ++i) {
-        const int b = (int)(i & 1), nb = b ^ 1;
-        const bool last = last_of(i);
-        // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
-        // only behind the values)
-        bool pv = false;
-        int w = i + 1 < nt ? 0 : 4;
-        const uint64_t t0 = tc::global_ns();
-        uint32_t spins = 0;
-        while (!pv || w < 4) {
-          if (!pv && tc::mbar_try_wait(&p_full[b], par(i))) {
-            values(b, first);
-            pv = true;
-            if (last && w < 4) {
-              if (!(ok = tc::mbar_wait(q_full, (uint32_t)(nq & 1), abort_flag))) break;
-              ++nq;
-            }
-            spins = 0;
-          } else if (w < 4 && (pv || !last) && tc::mbar_try_wait(&full[4 * nb + w], par(i + 1))) {
-            scores(nb, w);
-            ++w;
-            spins = 0;
-          } else if ((++spins & 63) == 0 && (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs)) {
+      __syncwarp();
+    };
+    auto scores_all = [&](int b) {
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int kb = 0; kb < kBlocks; ++kb)
+          if (kb < nkb) block(b, kb);
+        tc::mma_commit(&s_full[b]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int b, bool first) {
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int ch = 0; ch < kHD / 128; ++ch) {
+          if (ch * 128 < hd) {
+#pragma unroll
+            for (int ii = 0; ii < kUnit / 16; ++ii)
+              tc::mma_bf16(tO + (uint32_t)(ch * kHeads), dv + (b * kBlocks + 2 * ch) * kStep + ii * 128,
+                           dp + b * (kHeads * 128 >> 4) + ii * 2, id2, (first && ii == 0) ? 0u : 1u);
+          }
+          tc::mma_commit(&empty[4 * b + ch]);
+        }
+      }
+      __syncwarp();
+    };
+    auto ready = [](uint64_t *bar, uint32_t parity) {
+      const bool r = tc::mbar_test_wait(bar, parity);
+      return __all_sync(0xffffffffu, r);
+    };
+    bool ok = warp_wait(q_full, 0, abort_flag), first = true;
+    int nq = 1;  // segments whose q has been waited for
+    for (int w = 0; w < 4 && ok; ++w) {
+      ok = warp_wait(&full[w], 0, abort_flag);
+      if (ok) scores(0, w);
+    }
+    for (int64_t i = 0; i < nt && ok; ++i) {
+      const int b = (int)(i & 1), nb = b ^ 1;
+      const bool last = last_of(i);
+      // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
+      // only behind the values)
+      bool pv = false;
+      int w = i + 1 < nt ? 0 : 4;
+      const uint64_t t0 = tc::global_ns();
+      uint32_t spins = 0;
+      while (!pv || w < 4) {
+        if (!pv && ready(&p_full[b], par(i))) {
+          values(b, first);
+          pv = true;
+          if (last && w < 4) {
+            if (!(ok = warp_wait(q_full, (uint32_t)(nq & 1), abort_flag))) break;
+            ++nq;
+          }
+          spins = 0;
+        } else if (w == 0 && (pv || !last) && ready(&full[4 * nb + 3], par(i + 1))) {
+          scores_all(nb);
+          w = 4;
+        } else if (w < 4 && (pv || !last) && ready(&full[4 * nb + w], par(i + 1))) {
+          scores(nb, w);
+          ++w;
+          spins = 0;
+        } else if ((++spins & 63) == 0) {
+          const bool gone = *abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs;
+          if (__any_sync(0xffffffffu, gone)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
         }
-        if (!ok) break;
-        first = last;
-        if (last) {
-          c.t = c.row.units - 1;
-          if (i + 1 < nt) advance(P, c);
-        } else {
-          ++c.t;
-        }
       }
-      // nothing may still read shared memory, write TMEM or arrive when the CTA ends
-      tc::mma_commit(drain);
-      const uint64_t t0 = tc::global_ns();
-      while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t0 < tc::kWaitLimitNs) {
+      if (!ok) break;
+      first = last;
+      if (last) {
+        c.t = c.row.units - 1;
+        if (i + 1 < nt) advance(P, c);
+      } else {
+        ++c.t;
       }
     }
+    // nothing may still read shared memory, write TMEM or arrive when the CTA ends
+    if (tc::elect_one()) tc::mma_commit(drain);
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------------------------ copies: warps 2, 3 even tiles, 8, 9 odd
-    const int b = warp >= 8 ? 1 : 0, half = warp & 1;
+    const uint64_t t1 = tc::global_ns();
+    while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------------------ copies: 16 positions a warp
+    const int b = (warp - 8) >> 2, part = warp & 3;
     const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
     const int cc = lane & 7;
     if (b == 1 && nt > 1) advance(P, c);
     for (int64_t i = b; i < nt; i += 2) {
-      const int j = c.t * kUnit + half * 32 + lane;
+      const int j = c.t * kUnit + part * 16 + (lane & 15);
       const bool there = j < c.row.rows;
       const uint32_t pos = (uint32_t)(c.row.first + j), pg = P.page.div(pos);
       const int id = there ? a.table[(int64_t)c.row.req * a.width + pg] : 0;
@@ -449,28 +482,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       const int64_t off = good ? (int64_t)id * a.c.k_page + (int64_t)(pos - pg * P.page.d) * a.c.k_row +
                                      (int64_t)(c.hg / P.sub) * a.c.k_head
                                : -1;
-      const uint32_t mask = __ballot_sync(0xffffffffu, good);
-      int64_t ro[8];  // rows 4 u + lane / 8 of this warp's half
+      const uint32_t mask = __ballot_sync(0xffffffffu, good) & 0xffffu;
+      int64_t ro[4];  // positions 4 u + lane / 8 of this warp's sixteen
 #pragma unroll
-      for (int u = 0; u < 8; ++u) ro[u] = __shfl_sync(0xffffffffu, off, 4 * u + (lane >> 3));
-      if (i >= 2) {
-        if (!warp_wait(&empty[b], par(i) ^ 1u, abort_flag)) break;
-      }
-      if (lane == 0) masks[2 * b + half] = mask;
-      const uint32_t dst = s_t + b * kBlocks * kBlock + (half * 32 + (lane >> 3)) * 128;
+      for (int u = 0; u < 4; ++u) ro[u] = __shfl_sync(0xffffffffu, off, 4 * u + (lane >> 3));
+      const uint32_t dst = s_t + b * kBlocks * kBlock + (part * 16 + (lane >> 3)) * 128;
+      bool ok = true;
 #pragma unroll
-      for (int kb = 0; kb < kBlocks; ++kb) {
-        const bool f_in = kb * 64 + cc * 8 < hd;
-        if (kb < nkb) {
+      for (int w = 0; w < 4; ++w) {  // a quarter of the features as soon as the values before have read it
+        if (ok && i >= 2) ok = warp_wait(&empty[4 * b + w], par(i) ^ 1u, abort_flag);
+        if (ok && w == 3 && lane == 0) masks[4 * b + part] = mask;  // (the tile before is done with)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const bool in = ro[u] >= 0 && f_in;
-            const int r7 = (4 * u + (lane >> 3)) & 7;
-            attn::cp_async16(dst + kb * kBlock + u * 512 + ((cc ^ r7) << 4), in ? kbase + ro[u] + kb * 64 + cc * 8 : kbase, in);
+        for (int kb = 2 * w; kb < 2 * w + 2; ++kb) {
+          const bool f_in = kb * 64 + cc * 8 < hd;
+          if (ok && kb < nkb) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const bool in = ro[u] >= 0 && f_in;
+              const int r7 = (4 * u + (lane >> 3)) & 7;
+              attn::cp_async16(dst + kb * kBlock + u * 512 + ((cc ^ r7) << 4), in ? kbase + ro[u] + kb * 64 + cc * 8 : kbase, in);
+            }
           }
         }
-        if (kb & 1) asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
       }
+      if (!ok) break;
       asm volatile("cp.async.wait_group 3;" ::: "memory");
       attn::fence_proxy_async();
       tc::mbar_arrive(&full[4 * b]);
@@ -490,11 +526,82 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == 2) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
   if (tid == 0 && *abort_flag) atomicOr(a.status, kStatusTimeout);
+}
+
+// Join the shares of the segments that several CTAs worked on: block x a segment (or the CTA that a split segment
+// began in), its heads and 64-feature chunks dealt over the warps of the blocks y.  A share is 128 KB, which the
+// last CTA to finish alone would take tens of microseconds to read; here the whole device reads them.  Shares are
+// added in their order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinChunk = 64;
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid_constant__ Params P) {
+  __shared__ float s_f[kJoinThreads / 32][kMaxCtas];
+  const PagedAttnArgs &a = P.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (a programmatic dependent of the kernel above)
+  const int2 sp = P.split[blockIdx.x];
+  const int n_hg = P.by_segment ? (int)blockIdx.x : sp.x, n = n_hg / P.Hg, hg = n_hg - n * P.Hg, parts = sp.y;
+  if (P.by_segment && row_of<kUnit>(a, n, false).units == 0) return;  // (a row that was left alone: nothing told)
+  const int c0 = P.by_segment ? sp.x : (int)blockIdx.x;
+  // (after a wait that ran out the notes may be those of another call: nothing outside the workspace is read)
+  if (parts <= 1 || c0 < 0 || parts > P.ctas - c0 || n < 0 || n >= a.N) return;
+  auto slot = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
+  const int kvh = hg / P.sub, sg = hg - kvh * P.sub, h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
+  const int hd = a.c.head_dim, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (hd + kJoinChunk - 1) / kJoinChunk;
+  float *f = s_f[warp];
+  for (int it = blockIdx.y * (kJoinThreads / 32) + warp; it < nh * chunks; it += gridDim.y * (kJoinThreads / 32)) {
+    const int h = it / chunks, d = (it - h * chunks) * kJoinChunk + (lane & 15) * 4;
+    float M = -INFINITY, Lp = 0.f;
+    for (int p = lane; p < parts; p += 32) {
+      const float m = __ldcg(P.share_ml + ((int64_t)slot(p) * kHeads + h) * 2);
+      f[p] = m;
+      M = fmaxf(M, m);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int p = lane; p < parts; p += 32) {
+      const float e = f[p] == -INFINITY ? 0.f : exp2f(f[p] - M);
+      f[p] = e;
+      Lp = fmaf(__ldcg(P.share_ml + ((int64_t)slot(p) * kHeads + h) * 2 + 1), e, Lp);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) Lp += __shfl_xor_sync(0xffffffffu, Lp, o);
+    __syncwarp();
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = lane >> 4; p0 < parts; p0 += 8) {  // the half-warps take every other share, four in flight
+      float4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p0 + 2 * u < parts && d < hd)
+          x[u] = __ldcg(reinterpret_cast<const float4 *>(P.share_o + ((int64_t)slot(p0 + 2 * u) * kHeads + h) * kHD + d));
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p0 + 2 * u < parts && d < hd) {
+          const float e = f[p0 + 2 * u];
+          v.x = fmaf(x[u].x, e, v.x);
+          v.y = fmaf(x[u].y, e, v.y);
+          v.z = fmaf(x[u].z, e, v.z);
+          v.w = fmaf(x[u].w, e, v.w);
+        }
+    }
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, 16);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+    if (lane < 16 && d < hd) {
+      const float fo = out_factor(M, Lp, a.sink, h0 + h);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * fo, v.y * fo), hi = __floats2bfloat162_rn(v.z * fo, v.w * fo);
+      *reinterpret_cast<uint2 *>(a.o + (int64_t)n * a.o_t + (int64_t)(h0 + h) * hd + d) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+      if (a.lse && d == 0) a.lse[(int64_t)n * a.H + h0 + h] = Lp == 0.f ? -INFINITY : (M + log2f(Lp)) * 0.6931471805599453f;
+    }
+    __syncwarp();
+  }
 }
 
 }  // namespace latent
@@ -512,11 +619,29 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
   const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
   const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + kUnit - 1) / kUnit);
   const int64_t grid = std::min<int64_t>(std::min<int64_t>(units, num_sms), kMaxCtas);
+  const int64_t segments = (int64_t)a.N * p.Hg;
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * kHeads * kHD;
-  if (sizeof(float) * 2 * grid * kHeads * (kHD + 2) > ws_bytes) return cudaErrorInvalidValue;
+  p.split = reinterpret_cast<int2 *>(p.share_ml + 2 * grid * kHeads * 2);
+  p.by_segment = segments <= grid;
+  p.ctas = (int)grid;
+  if (sizeof(float) * 2 * grid * kHeads * (kHD + 2) + sizeof(int2) * grid > ws_bytes) return cudaErrorInvalidValue;
   k_paged_attn_latent<<<(unsigned)grid, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || segments == units) return e;  // (one tile a segment: nothing is shared)
+  // about 600 blocks of the join, and no more than there is work
+  const int64_t x = std::min(segments, grid), y = std::min<int64_t>(std::max<int64_t>(1, 4 * num_sms / x), kHeads);
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)x, (unsigned)y);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k_paged_join_latent, p);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace paged

@@ -48,6 +48,9 @@ struct Params {
   float *share_o;       // [2 G][heads of a group][padded head_dim]
   float *share_ml;      // [2 G][heads of a group][2]
   int *counters;        // [3][kMaxCtas]: groups past a segment's first, first groups, segments
+  int2 *split;          // latent rows: of the segments that several CTAs shared, the first CTA and how many
+  int ctas;             // CTAs launched
+  int by_segment;       // `split` is by segment (no more of them than CTAs), else by first CTA
 };
 
 // The positions first .. first + rows - 1 of row n; units of U rows (0: a row that is left alone).
