@@ -67,10 +67,17 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, what):
-    """(pointer, token stride, head stride) of a bf16 CUDA tensor [N, heads, hd] whose features are contiguous."""
-    if not t.is_cuda or t.dtype != torch.bfloat16:
-        raise ValueError("%s: expected a CUDA bfloat16 tensor, got %s on %s" % (what, t.dtype, t.device))
+def _now(stream):
+    """(current device, raw stream) of a call; looked up once a call, without building a Stream object."""
+    dev = torch._C._cuda_getDevice()
+    return dev, (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+
+
+def _rows(t, dev, what):
+    """(pointer, token stride, head stride) of a bf16 tensor [N, heads, hd] on CUDA device dev whose features are
+    contiguous."""
+    if t.get_device() != dev or t.dtype is not torch.bfloat16:
+        raise ValueError("%s: expected a bfloat16 tensor on the current CUDA device, got %s on %s" % (what, t.dtype, t.device))
     s0, s1, s2 = t.stride()
     n, h, d = t.shape
     if s2 != 1 and d > 1:
@@ -82,12 +89,13 @@ def _rows(t, what):
     return t.data_ptr(), s0, s1
 
 
-def _vec(t, n, dtype, what):
-    """Pointer of a contiguous CUDA tensor of n values; None -> NULL."""
+def _vec(t, n, dtype, dev, what):
+    """Pointer of a contiguous tensor of n values on CUDA device dev; None -> NULL."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s: expected a contiguous CUDA tensor of %d %s, got %s %s on %s" % (what, n, dtype, tuple(t.shape), t.dtype, t.device))
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous tensor of %d %s on the current CUDA device, got %s %s on %s" % (
+            what, n, dtype, tuple(t.shape), t.dtype, t.device))
     return t.data_ptr()
 
 
@@ -108,6 +116,7 @@ class PagedCache:
         self.c = _abi.Paged(k.data_ptr(), None if v is None else v.data_ptr(), *st(k), *(st(v) if v is not None else (0, 0, 0)),
                             *k.shape)
         self.ref = ctypes.byref(self.c)
+        self.device = k.get_device()
 
 
 CFG_FIELDS = [f for f, _ in _abi.Cfg._fields_]
@@ -342,13 +351,14 @@ class Context:
         the cache has no values.  pos, slot int32 [N]; pos < 0: a padding row, left as it is; slot -1: no
         cache row.  Returns q_out (allocated unless given; q itself for in place)."""
         N, Hk, hd = k.shape
+        dev, st = _now(stream)
         if Hk != cache.kv_heads or hd != cache.head_dim:
             raise ValueError("k: expected [N, %d, %d], got %s" % (cache.kv_heads, cache.head_dim, tuple(k.shape)))
-        if cache.v is not None and (v is None or v.shape != k.shape):
-            raise ValueError("v: expected %s, got %s" % (tuple(k.shape), None if v is None else tuple(v.shape)))
+        if cache.device != dev:
+            raise ValueError("cache: on CUDA device %d, the current one is %d" % (cache.device, dev))
         H = 0
-        qp = op = None
-        q_t = q_h = o_t = o_h = 0
+        qp = op = vp = tp = None
+        q_t = q_h = o_t = o_h = v_t = v_h = rows = 0
         if q is not None:
             if q.dim() != 3 or q.shape[0] != N or q.shape[2] != hd:
                 raise ValueError("q: expected [%d, H, %d], got %s" % (N, hd, tuple(q.shape)))
@@ -357,18 +367,23 @@ class Context:
                 q_out = _empty((N, H, hd), torch.bfloat16, q.device, stream)
             elif q_out.shape != q.shape:
                 raise ValueError("q_out: expected %s, got %s" % (tuple(q.shape), tuple(q_out.shape)))
-            qp, q_t, q_h = _rows(q, "q")
-            op, o_t, o_h = _rows(q_out, "q_out")
-        kp, k_t, k_h = _rows(k, "k")
-        vp, v_t, v_h = _rows(v, "v") if cache.v is not None else (None, 0, 0)
-        if tab is not None and rd and (tab.dim() != 3 or tab.shape[1] * 2 != rd or tab.shape[2] != 2):
-            raise ValueError("tab: expected [positions, %d, 2], got %s" % (rd // 2, tuple(tab.shape)))
+            qp, q_t, q_h = _rows(q, dev, "q")
+            op, o_t, o_h = _rows(q_out, dev, "q_out")
+        kp, k_t, k_h = _rows(k, dev, "k")
+        if cache.v is not None:
+            if v is None or v.shape != k.shape:
+                raise ValueError("v: expected %s, got %s" % (tuple(k.shape), None if v is None else tuple(v.shape)))
+            vp, v_t, v_h = _rows(v, dev, "v")
+        if tab is not None and rd:
+            if tab.dim() != 3 or tab.shape[1] * 2 != rd or tab.shape[2] != 2:
+                raise ValueError("tab: expected [positions, %d, 2], got %s" % (rd // 2, tuple(tab.shape)))
+            rows = tab.shape[0]
+            tp = _vec(tab, rows * rd, torch.float32, dev, "tab")
         _check(lib().csa_qk_norm_rope(
-            self.h, qp, q_t, q_h, kp, k_t, k_h, vp, v_t, v_h, N, H, cache.ref, _vec(pos, N, torch.int32, "pos"),
-            _vec(slot, N, torch.int32, "slot"), _vec(q_norm, hd, torch.float32, "q_norm"),
-            _vec(k_norm, hd, torch.float32, "k_norm"), self.cfg.eps if eps is None else eps,
-            _dev(tab, torch.float32, "tab"), 0 if tab is None else tab.shape[0], rd,
-            hd - rd if rope_at is None else rope_at, 1 if half else 0, op, o_t, o_h, _stream(stream)), "csa_qk_norm_rope")
+            self.h, qp, q_t, q_h, kp, k_t, k_h, vp, v_t, v_h, N, H, cache.ref, _vec(pos, N, torch.int32, dev, "pos"),
+            _vec(slot, N, torch.int32, dev, "slot"), _vec(q_norm, hd, torch.float32, dev, "q_norm"),
+            _vec(k_norm, hd, torch.float32, dev, "k_norm"), self.cfg.eps if eps is None else eps, tp, rows, rd,
+            hd - rd if rope_at is None else rope_at, 1 if half else 0, op, o_t, o_h, st), "csa_qk_norm_rope")
         return q_out
 
     def paged_attn(self, q, cache, table, pos, scale, req=None, sink=None, window=0, out=None, lse=None,
@@ -379,24 +394,29 @@ class Context:
         Returns out, or (out, lse) with lse f32 [N, H] the log of the sum of exponentials (without the sink)
         when lse is given or with_lse is set."""
         N, H, hd = q.shape
+        dev, st = _now(stream)
         if hd != cache.head_dim:
             raise ValueError("q: expected [N, H, %d], got %s" % (cache.head_dim, tuple(q.shape)))
+        if cache.device != dev:
+            raise ValueError("cache: on CUDA device %d, the current one is %d" % (cache.device, dev))
         if table.dim() != 2:
             raise ValueError("table: expected [requests, width], got %s" % (tuple(table.shape),))
+        R, width = table.shape
         if out is None:
             out = _empty((N, H, hd), torch.bfloat16, q.device, stream)
         elif out.shape != q.shape:
             raise ValueError("out: expected %s, got %s" % (tuple(q.shape), tuple(out.shape)))
         if lse is None and with_lse:
             lse = _empty((N, H), torch.float32, q.device, stream)
-        qp, q_t, q_h = _rows(q, "q")
-        op, o_t, o_h = _rows(out, "out")
+        qp, q_t, q_h = _rows(q, dev, "q")
+        op, o_t, o_h = _rows(out, dev, "out")
         if H > 1 and (q_h != hd or o_h != hd):
             raise ValueError("q, out: the heads of a token must follow one another")
         _check(lib().csa_paged_attn(
-            self.h, qp, q_t, N, H, cache.ref, _dev(table, torch.int32, "table"), table.shape[0], table.shape[1],
-            _vec(req, N, torch.int32, "req"), _vec(pos, N, torch.int32, "pos"), _vec(sink, H, torch.float32, "sink"),
-            scale, window, op, o_t, _vec(lse, N * H, torch.float32, "lse"), _stream(stream)), "csa_paged_attn")
+            self.h, qp, q_t, N, H, cache.ref, _vec(table, R * width, torch.int32, dev, "table"), R, width,
+            _vec(req, N, torch.int32, dev, "req"), _vec(pos, N, torch.int32, dev, "pos"),
+            _vec(sink, H, torch.float32, dev, "sink"), scale, window, op, o_t,
+            _vec(lse, N * H, torch.float32, dev, "lse"), st), "csa_paged_attn")
         return out if lse is None else (out, lse)
 
 
@@ -463,16 +483,18 @@ def page_step(new_len, length, table, free, state, page, tok_req, tok_pos, tok_s
     [N], cu int32 [R+1].  length_out, state_out: where the state after the step goes (default: length and state
     themselves).  Returns info int32 [4]: tokens, pages taken, pages released, error bits."""
     R, N = new_len.numel(), tok_req.numel()
+    dev, st = _now(stream)
     if table.dim() != 2 or table.shape[0] != R:
         raise ValueError("table: expected [%d, width], got %s" % (R, tuple(table.shape)))
     if info is None:
         info = _empty((4,), torch.int32, new_len.device, stream)
-    i32 = torch.int32
+    i32, width, n_pages = torch.int32, table.shape[1], free.numel()
+    lp, sp = _vec(length, R, i32, dev, "length"), _vec(state, 2, i32, dev, "state")
     _check(lib().csa_page_step(
-        _vec(new_len, R, i32, "new_len"), R, page, _vec(length, R, i32, "length"), _dev(table, i32, "table"),
-        table.shape[1], _vec(free, free.numel(), i32, "free"), free.numel(), _vec(state, 2, i32, "state"),
-        _vec(tok_req, N, i32, "tok_req"), _vec(tok_pos, N, i32, "tok_pos"), _vec(tok_slot, N, i32, "tok_slot"), N,
-        _vec(cu, R + 1, i32, "cu"), _vec(length if length_out is None else length_out, R, i32, "length_out"),
-        _vec(state if state_out is None else state_out, 2, i32, "state_out"), _vec(info, 4, i32, "info"),
-        _stream(stream)), "csa_page_step")
+        _vec(new_len, R, i32, dev, "new_len"), R, page, lp, _vec(table, R * width, i32, dev, "table"), width,
+        _vec(free, n_pages, i32, dev, "free"), n_pages, sp, _vec(tok_req, N, i32, dev, "tok_req"),
+        _vec(tok_pos, N, i32, dev, "tok_pos"), _vec(tok_slot, N, i32, dev, "tok_slot"), N, _vec(cu, R + 1, i32, dev, "cu"),
+        lp if length_out is None else _vec(length_out, R, i32, dev, "length_out"),
+        sp if state_out is None else _vec(state_out, 2, i32, dev, "state_out"), _vec(info, 4, i32, dev, "info"), st),
+        "csa_page_step")
     return info

@@ -237,7 +237,7 @@ struct PageStepArgs {
   int N;
   int32_t *cu, *length_out, *state_out, *info;
 };
-constexpr int kPageStepMaxR = 16384;
+constexpr int kPageStepMaxR = 14000;
 cudaError_t launch_page_step(const PageStepArgs &a, cudaStream_t s);
 
 // Head norms, rotation and the cache write of N tokens (k_norm_rope.cu; csa_qk_norm_rope's arguments).

@@ -11,6 +11,8 @@
 //
 // Bound by HBM: a row is read and written once; the angles of a token are shared by its heads through L1.
 // Value rows are copies of the same shape.
+#include <algorithm>
+
 #include "csa_internal.cuh"
 #include "rowops.cuh"
 
@@ -133,12 +135,13 @@ __device__ __forceinline__ void load_partner_w(const NormRopeArgs &a, const floa
   }
 }
 
-// G lanes a row, V vectors a lane (head_dim <= 8 G V), U heads of one token a group: the norm's weights and the token's
-// angles are read once for them, and U V vectors are in flight a lane.  Items are (token, block of U heads), a
-// token's query, key and value heads in a row.
+// G lanes a row, V vectors a lane (head_dim <= 8 G V).  A group of lanes takes `per` heads of one kind (query, key,
+// value) of one token, U at a time with the next U's vectors in flight; the norm's weights and the token's angles,
+// multiplied together, stay in registers for all of them.  Items are (token, block of `per` heads), a token's
+// query, key and value blocks in a row.
 template <int G, int V, int U, bool HALF, bool FAST>
-__global__ void __launch_bounds__(kThreads, HALF || V == 4 ? 2 : 3) k_norm_rope(const __grid_constant__ NormRopeArgs a, int q_blocks, int k_blocks,
-                                                        int per_token, int64_t items) {
+__global__ void __launch_bounds__(kThreads, V == 4 ? 1 : (V == 2 && HALF ? 2 : 3)) k_norm_rope(const __grid_constant__ NormRopeArgs a, int per, int q_blocks,
+                                                           int k_blocks, int per_token, int64_t items) {
   const int lane = threadIdx.x & (G - 1);
   const int hd = a.c.head_dim;
   const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G;
@@ -146,115 +149,143 @@ __global__ void __launch_bounds__(kThreads, HALF || V == 4 ? 2 : 3) k_norm_rope(
   const int n = in ? (int)(item / per_token) : 0;
   const int jb = in ? (int)(item - (int64_t)n * per_token) : 0;
   const int kind = jb < q_blocks ? 0 : (jb < q_blocks + k_blocks ? 1 : 2);  // query, key, value
-  const int h0 = (kind == 0 ? jb : (kind == 1 ? jb - q_blocks : jb - q_blocks - k_blocks)) * U;
-  const int nh = min(U, (kind == 0 ? a.H : a.c.kv_heads) - h0);
+  const int h0 = (kind == 0 ? jb : (kind == 1 ? jb - q_blocks : jb - q_blocks - k_blocks)) * per;
+  const int nh = min(per, (kind == 0 ? a.H : a.c.kv_heads) - h0);
+  const int64_t x_h = kind == 0 ? a.q_h : (kind == 1 ? a.k_h : a.v_h);
+  const bf16 *x = (kind == 0 ? a.q + n * a.q_t : (kind == 1 ? a.k + n * a.k_t : a.v + n * a.v_t)) + h0 * x_h;
+  uint4 cur[U][V], nxt[U][V];
+  auto load = [&](uint4 (&d)[U][V], int t0) {
+#pragma unroll
+    for (int t = 0; t < U; ++t)
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        const int f = 8 * (lane + G * u);
+        d[t][u] = make_uint4(0, 0, 0, 0);
+        if (in && t0 + t < nh && f < hd) d[t][u] = *reinterpret_cast<const uint4 *>(x + (int64_t)(t0 + t) * x_h + f);
+      }
+  };
+  load(cur, 0);  // (the rows of padding tokens exist too)
   const int p = in ? a.pos[n] : -1;
-  const int64_t rows = (int64_t)a.c.n_pages * a.c.page;
-  const int64_t slot = !in ? -1 : (a.slot ? a.slot[n] : n);
+  const int rows = a.c.n_pages * a.c.page;
+  const int slot = !in ? -1 : (a.slot ? a.slot[n] : n);
   bool live = in && p >= 0;
   if (live && ((a.rd > 0 && p >= a.tab_rows) || slot < -1 || slot >= rows)) {
     if (jb == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
     live = false;
   }
   if (kind != 0 && slot < 0) live = false;
-  const int64_t x_h = kind == 0 ? a.q_h : (kind == 1 ? a.k_h : a.v_h);
-  const bf16 *x = (kind == 0 ? a.q + n * a.q_t : (kind == 1 ? a.k + n * a.k_t : a.v + n * a.v_t)) + h0 * x_h;
   int64_t y_h;
   bf16 *y;
   if (kind == 0) {
     y_h = a.o_h;
     y = a.q_out + n * a.o_t + h0 * y_h;
   } else {
-    const int64_t pg = live ? slot / a.c.page : 0, row = live ? slot - pg * a.c.page : 0;
+    const int pg = live ? (int)((uint32_t)slot / (uint32_t)a.c.page) : 0, row = live ? slot - pg * a.c.page : 0;
     y_h = kind == 1 ? a.c.k_head : a.c.v_head;
     y = (kind == 1 ? reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row
                    : reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row) + h0 * y_h;
   }
-  const bool turns = kind != 2 && a.rd > 0;
-  uint4 xv[U][V], xp[U][V];  // (xp: the partners, where they are not the vector's own)
-#pragma unroll
-  for (int t = 0; t < U; ++t)
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const int f = 8 * (lane + G * u);
-      xv[t][u] = xp[t][u] = make_uint4(0, 0, 0, 0);
-      if (live && t < nh && f < hd) {
-        xv[t][u] = *reinterpret_cast<const uint4 *>(x + t * x_h + f);
-        if (HALF && turns) load_partners<FAST>(a, x + t * x_h, f, xp[t][u]);
-      }
-    }
   const float *w = kind == 0 ? a.q_norm : a.k_norm;
-  float r[U];
-#pragma unroll
-  for (int t = 0; t < U; ++t) {
-    float ss = 0.f;
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      float v[8];
-      unpack(xv[t][u], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-    }
-    r[t] = ss;
-  }
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int t = 0; t < U; ++t) r[t] += __shfl_xor_sync(0xffffffffu, r[t], o);
-#pragma unroll
-  for (int t = 0; t < U; ++t) r[t] = w ? 1.0f / sqrtf(r[t] / (float)hd + a.eps) : 1.f;
-  __syncwarp();  // (q_out may be q: every lane has read its partners)
-  if (!live) return;
-  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)(a.rd > 0 ? p : 0) * (a.rd >> 1);
+  const bool plain = kind == 2, turns = !plain && a.rd > 0;
+  // y = r (x c + z s) with z the partner's value: c = weight x cos, s = partner's weight x (+-sin)
+  float c[V][8], s[V][8];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int f = 8 * (lane + G * u);
-    if (f >= hd) continue;
-    if (kind == 2) {
 #pragma unroll
-      for (int t = 0; t < U; ++t)
-        if (t < nh) *reinterpret_cast<uint4 *>(y + t * y_h + f) = xv[t][u];
-      continue;
-    }
-    float wv[8], c[8], s[8], wp[8];
+    for (int e = 0; e < 8; ++e) c[u][e] = 1.f, s[u][e] = 0.f;
+    if (!live || plain || f >= hd) continue;
+    float wv[8];
     load_w<FAST>(w, f, wv);
     if (turns) {
-      load_angles<FAST>(a, tp, f, c, s);
+      const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)p * (a.rd >> 1);
+      load_angles<FAST>(a, tp, f, c[u], s[u]);
+      float wp[8];
       if (HALF) load_partner_w<FAST>(a, w, f, wp);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {  // the weights into the angles: the value's own, its partner's
-        s[e] *= HALF ? wp[e] : wv[e ^ 1];
-        c[e] *= wv[e];
-      }
+      for (int e = 0; e < 8; ++e) s[u][e] *= HALF ? wp[e] : wv[e ^ 1];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[u][e] *= wv[e];
+  }
+  // (every group of the warp goes through as many rounds: the shuffles below are the warp's)
+  int rounds = (max(nh, 0) + U - 1) / U;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, o));
+  for (int rnd = 0; rnd < rounds; ++rnd) {
+    const int t0 = rnd * U;
+    load(nxt, t0 + U);
+    uint4 xp[U][V];  // the partners' vectors, from the lines just read
+    if (HALF) {
+#pragma unroll
+      for (int t = 0; t < U; ++t)
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+          const int f = 8 * (lane + G * u);
+          xp[t][u] = make_uint4(0, 0, 0, 0);
+          if (live && turns && t0 + t < nh && f < hd) load_partners<FAST>(a, x + (int64_t)(t0 + t) * x_h, f, xp[t][u]);
+        }
+    }
+    float r[U];
 #pragma unroll
     for (int t = 0; t < U; ++t) {
-      if (t >= nh) continue;
-      float v[8], o[8];
-      unpack(xv[t][u], v);
-      if (turns) {
-        float z[8];
-        if (HALF) {
-          unpack(xp[t][u], z);
-        } else {  // (outside the turned part there is no partner, which may be infinite)
+      r[t] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = f + e >= a.at && f + e < a.at + a.rd ? v[e ^ 1] : 0.f;
-        }
+      for (int u = 0; u < V; ++u) {
+        float v[8];
+        unpack(cur[t][u], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = r[t] * fmaf(v[e], c[e], z[e] * s[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = r[t] * (v[e] * wv[e]);
+        for (int e = 0; e < 8; ++e) r[t] = fmaf(v[e], v[e], r[t]);
       }
-      *reinterpret_cast<uint4 *>(y + t * y_h + f) = pack(o);
     }
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int t = 0; t < U; ++t) r[t] += __shfl_xor_sync(0xffffffffu, r[t], o);
+#pragma unroll
+    for (int t = 0; t < U; ++t) r[t] = !plain && w ? 1.0f / sqrtf(r[t] / (float)hd + a.eps) : 1.f;
+    __syncwarp();  // (q_out may be q: every lane has read its partners)
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      if (!live || t0 + t >= nh) continue;
+      bf16 *yt = y + (int64_t)(t0 + t) * y_h;
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        const int f = 8 * (lane + G * u);
+        if (f >= hd) continue;
+        if (plain) {
+          *reinterpret_cast<uint4 *>(yt + f) = cur[t][u];
+          continue;
+        }
+        float v[8], z[8], o[8];
+        unpack(cur[t][u], v);
+        if (HALF) unpack(xp[t][u], z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // (outside the turned part there is no partner, which may be infinite)
+          if (!HALF) z[e] = turns && f + e >= a.at && f + e < a.at + a.rd ? v[e ^ 1] : 0.f;
+          o[e] = r[t] * fmaf(v[e], c[u][e], z[e] * s[u][e]);
+        }
+        *reinterpret_cast<uint4 *>(yt + f) = pack(o);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < U; ++t)
+#pragma unroll
+      for (int u = 0; u < V; ++u) cur[t][u] = nxt[t][u];
   }
 }
 
 template <int G, int V, int U>
-cudaError_t launch(const NormRopeArgs &a, cudaStream_t s) {
-  const int q_blocks = (a.H + U - 1) / U, k_blocks = (a.c.kv_heads + U - 1) / U;
-  const int per_token = q_blocks + k_blocks * (a.v ? 2 : 1);
+cudaError_t launch(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
+  // Heads a group: as many (up to 16) as still leave a full complement of warps (24 an SM), at least U where there
+  // are rows enough, else one, which spreads few rows over more SMs.
+  const int most = std::max(a.H, a.c.kv_heads);
+  auto blocks_of = [](int h, int per) { return (h + per - 1) / per; };
+  auto per_token_of = [&](int per) { return blocks_of(a.H, per) + blocks_of(a.c.kv_heads, per) * (a.v ? 2 : 1); };
+  int per = 1;
+  while (per < 16 && per < most && (int64_t)a.N * per_token_of(2 * per) * G >= (int64_t)num_sms * 24 * 32) per *= 2;
+  const int q_blocks = blocks_of(a.H, per), k_blocks = blocks_of(a.c.kv_heads, per), per_token = per_token_of(per);
   const int64_t items = (int64_t)a.N * per_token;
   const int64_t blocks = (items * G + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
@@ -263,28 +294,20 @@ cudaError_t launch(const NormRopeArgs &a, cudaStream_t s) {
                     (((uintptr_t)a.tab | (uintptr_t)a.q_norm | (uintptr_t)a.k_norm) & 15) == 0;
   auto *k = a.half ? (fast ? k_norm_rope<G, V, U, true, true> : k_norm_rope<G, V, U, true, false>)
                    : (fast ? k_norm_rope<G, V, U, false, true> : k_norm_rope<G, V, U, false, false>);
-  k<<<(unsigned)blocks, kThreads, 0, s>>>(a, q_blocks, k_blocks, per_token, items);
+  k<<<(unsigned)blocks, kThreads, 0, s>>>(a, per, q_blocks, k_blocks, per_token, items);
   return cudaGetLastError();
-}
-
-// Several heads a group once that leaves every SM with a full complement of warps; fewer rows take one head a group,
-// which spreads them over more SMs.
-template <int G, int V, int U>
-cudaError_t launch_sized(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
-  const int64_t threads = (int64_t)a.N * (a.H + a.c.kv_heads * (a.v ? 2 : 1)) * G;
-  return threads >= (int64_t)num_sms * 2048 * U ? launch<G, V, U>(a, s) : launch<G, V, 1>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
   const int hd = a.c.head_dim;
-  if (hd <= 32) return launch_sized<4, 1, 4>(a, num_sms, s);
-  if (hd <= 64) return launch_sized<8, 1, 4>(a, num_sms, s);
-  if (hd <= 128) return launch_sized<16, 1, 4>(a, num_sms, s);
-  if (hd <= 256) return launch_sized<32, 1, 4>(a, num_sms, s);
-  if (hd <= 512) return launch_sized<32, 2, 2>(a, num_sms, s);
-  return launch<32, 4, 1>(a, s);
+  if (hd <= 32) return launch<4, 1, 2>(a, num_sms, s);
+  if (hd <= 64) return launch<8, 1, 2>(a, num_sms, s);
+  if (hd <= 128) return launch<16, 1, 2>(a, num_sms, s);
+  if (hd <= 256) return launch<32, 1, 2>(a, num_sms, s);
+  if (hd <= 512) return launch<32, 2, 1>(a, num_sms, s);
+  return launch<32, 4, 1>(a, num_sms, s);
 }
 
 }  // namespace csa

@@ -9,14 +9,14 @@
 // step does not write) or one it takes now (a ring entry), so no thread reads what another one writes.
 //
 // Bound by latency: a 64-token step moves 2 KB.  One CTA does small steps; larger ones take one cluster of
-// eight CTAs, each of which forms the sums for itself (R <= 16384 lengths from L2, kept in its shared memory)
+// eight CTAs, each of which forms the sums for itself (R <= 14000 lengths from L2, kept in its shared memory)
 // and takes an eighth of the tokens and pages.  The hardware's cluster barrier, after everything has been
 // read, lets length_out and state_out be length and state: one launch, and no counter that two calls could
 // share.
 #include <cstring>
 
 #include "csa_internal.cuh"
-#include "tc_ptx.cuh"
+#include "paged_common.cuh"
 
 namespace csa {
 namespace {
@@ -48,9 +48,10 @@ __device__ __forceinline__ int first_above(const uint32_t *incl, int n, uint32_t
   return lo;
 }
 
-__global__ void __launch_bounds__(1024) k_page_step(PageStepArgs a) {
-  extern __shared__ uint32_t sm[];  // running sums of add, need, back: [R] each
+__global__ void __launch_bounds__(1024) k_page_step(const __grid_constant__ PageStepArgs a, const __grid_constant__ paged::FastDiv a_page) {
+  extern __shared__ uint32_t sm[];  // running sums of add, need, back and the lengths: [R] each
   uint32_t *s_add = sm, *s_need = sm + a.R, *s_back = sm + 2 * a.R;
+  int *s_len = reinterpret_cast<int *>(sm + 3 * a.R);
   __shared__ Sums s_warp[32];
   __shared__ int s_err;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5, nw = nt >> 5;
@@ -64,14 +65,15 @@ __global__ void __launch_bounds__(1024) k_page_step(PageStepArgs a) {
   int err = 0;
   for (int r = r0; r < r1; ++r) {
     const int len = a.length[r], nw_r = a.new_len[r];
-    const int have = (int)(((int64_t)len + a.page - 1) / a.page);
+    s_len[r] = len;
+    const int have = len < 0 ? 0 : (int)a_page.div((uint32_t)min((int64_t)len + a.page - 1, (int64_t)0x7fffffff));
     Sums one{0, 0, 0};
     if (len < 0 || have > a.width) {
       err |= 2;
     } else if (nw_r > a.N) {
       err |= 1;
     } else if (nw_r > 0) {
-      const int64_t after = ((int64_t)len + nw_r + a.page - 1) / a.page;
+      const int64_t after = a_page.div((uint32_t)min((int64_t)len + nw_r + a.page - 1, (int64_t)0x7fffffff));
       if (after > a.width)
         err |= 2;
       else
@@ -119,35 +121,54 @@ __global__ void __launch_bounds__(1024) k_page_step(PageStepArgs a) {
   else if (total.need > (uint32_t)count)
     err |= 4;
   __syncthreads();
-  // ---- tokens
+  // ---- tokens, four a thread at a time (their searches and loads side by side)
   const int n_tok = err ? 0 : (int)total.add;
-  for (int t = gt; t < a.N; t += gn) {
-    int req = -1, pos = -1, slot = -1;
-    if (t < n_tok) {
-      req = first_above(s_add, a.R, (uint32_t)t);
-      const int len = a.length[req];
-      pos = len + t - (int)(req ? s_add[req - 1] : 0u);
-      const int p = pos / a.page, have = (len + a.page - 1) / a.page;
-      int id;
-      if (p < have) {
-        id = a.table[(int64_t)req * a.width + p];
-      } else {
-        const uint32_t i = (uint32_t)head + (req ? s_need[req - 1] : 0u) + (uint32_t)(p - have);
-        id = a.free_ring[i % (uint32_t)a.n_pages];
+  constexpr int kAtOnce = 4;
+  for (int t0 = gt; t0 < a.N; t0 += kAtOnce * gn) {
+    int req[kAtOnce], pos[kAtOnce], id[kAtOnce], at[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int t = t0 + k * gn;
+      req[k] = pos[k] = -1;
+      if (t < n_tok) {
+        req[k] = first_above(s_add, a.R, (uint32_t)t);
+        pos[k] = t - (int)(req[k] ? s_add[req[k] - 1] : 0u);
       }
-      if (id >= 0 && id < a.n_pages) slot = id * a.page + (pos - p * a.page);
     }
-    a.tok_req[t] = req;
-    a.tok_pos[t] = pos;
-    a.tok_slot[t] = slot;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (req[k] >= 0) pos[k] += s_len[req[k]];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      id[k] = -1;
+      at[k] = 0;
+      if (req[k] < 0) continue;
+      const uint32_t p = a_page.div((uint32_t)pos[k]), have = a_page.div((uint32_t)(s_len[req[k]] + a.page - 1));
+      at[k] = pos[k] - (int)p * a.page;
+      if (p < have) {
+        id[k] = a.table[(int64_t)req[k] * a.width + p];
+      } else {
+        const uint32_t i = (uint32_t)head + (req[k] ? s_need[req[k] - 1] : 0u) + (p - have);  // (below 2 n_pages)
+        id[k] = a.free_ring[i >= (uint32_t)a.n_pages ? i - (uint32_t)a.n_pages : i];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int t = t0 + k * gn;
+      if (t >= a.N) continue;
+      a.tok_req[t] = req[k];
+      a.tok_pos[t] = pos[k];
+      a.tok_slot[t] = id[k] >= 0 && id[k] < a.n_pages ? id[k] * a.page + at[k] : -1;
+    }
   }
+  auto wrap = [&](uint32_t i) { return i >= (uint32_t)a.n_pages ? i - (uint32_t)a.n_pages : i; };
   // ---- pages taken into the tables, pages released behind the ring's end
   if (!err) {
     for (int i = gt; i < (int)total.need; i += gn) {
       const int r = first_above(s_need, a.R, (uint32_t)i);
-      const int have = (a.length[r] + a.page - 1) / a.page;
+      const int have = (int)a_page.div((uint32_t)(s_len[r] + a.page - 1));
       a.table[(int64_t)r * a.width + have + (i - (int)(r ? s_need[r - 1] : 0u))] =
-          a.free_ring[((uint32_t)head + (uint32_t)i) % (uint32_t)a.n_pages];
+          a.free_ring[wrap((uint32_t)head + (uint32_t)i)];
     }
     for (int i = gt; i < (int)total.back; i += gn) {
       const int r = first_above(s_back, a.R, (uint32_t)i);
@@ -161,7 +182,7 @@ __global__ void __launch_bounds__(1024) k_page_step(PageStepArgs a) {
   else
     __syncthreads();
   for (int r = gt; r < a.R; r += gn) {
-    const int len = a.length[r], nw_r = a.new_len[r];
+    const int len = s_len[r], nw_r = a.new_len[r];
     a.length_out[r] = err ? len : (nw_r < 0 ? 0 : len + nw_r);
     if (a.cu) a.cu[r + 1] = err ? 0 : (int)s_add[r];
   }
@@ -180,7 +201,7 @@ __global__ void __launch_bounds__(1024) k_page_step(PageStepArgs a) {
 
 cudaError_t launch_page_step(const PageStepArgs &a, cudaStream_t s) {
   static SmemAttr attr;
-  const size_t smem = 3 * sizeof(uint32_t) * (size_t)a.R;
+  const size_t smem = 4 * sizeof(uint32_t) * (size_t)a.R;
   cudaError_t e = attr.ensure((const void *)k_page_step, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
@@ -196,7 +217,7 @@ cudaError_t launch_page_step(const PageStepArgs &a, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_page_step, a);
+  e = cudaLaunchKernelEx(&cfg, k_page_step, a, paged::FastDiv((uint32_t)a.page));
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

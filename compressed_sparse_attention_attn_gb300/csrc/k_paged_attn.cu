@@ -1,21 +1,20 @@
 // k_paged_attn.cu -- attention of single tokens over a paged key-value cache (head_dim up to 256).
 //
 // Row n, query head h over kv head h / g: S_j = scale q_h . K_j over the positions j of its request, O = sum_j
-// e^{S_j} V_j / (e^{sink} + sum_j e^{S_j}).  Up to 16 query heads of one kv head are the rows of an m16n8k16
+// e^{S_j} V_j / (e^{sink} + sum_j e^{S_j}).  Up to 16 query heads of one kv head are the rows (up to 8: the columns) of an m16n8k16
 // product, so a cache row is read once for all of them (a kv head with more query heads takes several head
 // groups).  A decode step does 4 g flops a byte of cache: at g = 8 that is 54 TFLOP/s at the card's copy
 // rate, far below what warp-level products give, and their accumulators stay in registers -- no trip
 // through tensor memory between the scores and the values.
 //
-// A unit is 64 positions: 16 for each of a CTA's four warps.  Every warp streams its own tiles (16 key rows,
+// A unit is 16 positions for each of a CTA's warps (four; six at 256 features).  Every warp streams its own tiles (16 key rows,
 // 16 value rows) through a ring of its own in shared memory, with no barrier between the warps before the
 // end of a segment; the ring runs on across segments.  Rows come by 16-byte cp.async from the page of each
-// position (looked up one tile ahead), rows past the end and features past head_dim as zeros; chunks are
+// position (looked up two tiles ahead), rows past the end and features past head_dim as zeros; chunks are
 // XOR-swizzled by the row so that ldmatrix reads without conflicts.  Softmax statistics are f32 (base 2); the
 // weights enter the second product as two bf16 terms (their sum carries 16 bits), so the only rounding that
 // counts is the result's.  At the end of a segment each warp leaves its accumulators in the stage it has
-// just read (exactly as large: 16 rows of keys and values in bf16 are 16 heads of f32), and the CTA joins the
-// four.  How CTAs share the rows: paged_common.cuh.
+// just read (exactly as large: 16 rows of keys and values in bf16 are 16 heads of f32), and the CTA joins them.  How CTAs share the rows: paged_common.cuh.
 #include <algorithm>
 #include <cstring>
 
@@ -25,17 +24,19 @@
 namespace csa {
 namespace paged {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;               // positions of a warp's tile
-constexpr int kUnit = kWarps * kTile;   // positions of a unit
-constexpr int kHeads = 16;              // query heads of a head group
+constexpr int kTile = 16;  // positions of a warp's tile
 
-template <int HD>
+// Warps and ring stages are set so that the rings fill an SM's shared memory and 64 to 128 KB are in flight: 4 x 3 x 4 KB
+// x 4 (or 3) CTAs at 64 features, 4 x 2 x 8 KB x 3 (x 3 x 8 KB x 2 where 16 heads' accumulators need the
+// registers) at 128, 6 x 2 x 16 KB x 1 at 256 (4 warps of 3 stages took 94 against 81 us over 48 rows of 16 x 256).
+template <int HD, int NH>
 struct Shape {
-  static constexpr int kStages = 3;
-  static constexpr int kStageBytes = 2 * kTile * HD * 2;          // key rows, value rows
-  static constexpr int kCtas = HD == 64 ? 4 : (HD == 128 ? 2 : 1);  // resident an SM
+  static constexpr int kWarps = HD == 256 ? 6 : 4;
+  static constexpr int kStages = HD == 256 || (HD == 128 && NH == 8) ? 2 : 3;
+  static constexpr int kCtas = HD == 64 ? (NH == 8 ? 4 : 3) : (HD == 128 ? (NH == 8 ? 3 : 2) : 1);  // resident an SM
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kUnit = kWarps * kTile;            // positions of a unit
+  static constexpr int kStageBytes = 2 * kTile * HD * 2;  // key rows, value rows
   static constexpr int kSmem = kWarps * kStages * kStageBytes;
 };
 
@@ -51,6 +52,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// The transpose of an 8 x 8 matrix of 16-bit values, a row in the four lanes of a quad.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -65,107 +72,123 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
   lo = bits(__floats2bfloat162_rn(x - __low2float(h), y - __high2float(h)));
 }
 
-// Where a CTA is in its range: segment (row n, head group hg), unit t of it.
-struct Cursor {
-  int n, hg, t;
-  Row row;
-};
+// Where a thread's values of a 16-bit or f32 fragment lie in a row of a segment's accumulators in shared memory.
+template <int NH>
+__device__ __forceinline__ int swizzle(int h) {
+  return (NH == 8 ? (h >> 1) & 3 : h & 3) << 3;
+}
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const __grid_constant__ Params P) {
-  using S = Shape<HD>;
+template <int HD, int NH>
+__global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCtas)) k_paged_attn(const __grid_constant__ Params P) {
+  using S = Shape<HD, NH>;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kUnit = S::kUnit, kHeads = NH;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[kWarps + 4];
+  __shared__ int64_t s_scan[kWarps + 1];
   __shared__ float s_ml[2][kWarps][kHeads];
   __shared__ float s_f[kWarps][kHeads];
-  __shared__ float s_join[kJoinFloats<kHeads>];
-  __shared__ float s_out[2][kHeads];
+  __shared__ float s_out[kHeads];
   __shared__ int s_flag;
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
-  const Range rg = find_range<kUnit, kThreads>(P, s_scan);
-  if (rg.begin >= rg.end) return;
-  const int64_t nunits = rg.end - rg.begin;
+  __shared__ Rows rows;
+  __shared__ Range rg;
+  const int nunits = find_range<kUnit, kThreads>(P, s_scan, rows, rg);
+  if (nunits == 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
-
-  Cursor cl;  // of the copies
-  cl.n = rg.row;
-  cl.row = row_of<kUnit>(a, cl.n, false);
-  {
-    const int64_t in = rg.begin - rg.before;
-    cl.hg = (int)(in / cl.row.units);
-    cl.t = (int)(in - (int64_t)cl.hg * cl.row.units);
-  }
-  Cursor cc = cl;  // of the products
-  auto advance = [&](Cursor &c) {
-    if (++c.t < c.row.units) return;
-    c.t = 0;
-    if (++c.hg < P.Hg) return;
-    c.hg = 0;
-    do {
-      ++c.n;
-      if (c.n >= a.N) {
-        c.row.units = 1;
-        c.row.rows = 0;
-        return;
-      }
-      c.row = row_of<kUnit>(a, c.n, false);
-    } while (c.row.units == 0);
-  };
+  Cursor cl = first_unit(rg, rows), cc = cl;  // of the lookups, of the products
   const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
   const bf16 *vbase = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) : kbase;
   const int64_t v_page = a.c.v ? a.c.v_page : a.c.k_page, v_row = a.c.v ? a.c.v_row : a.c.k_row,
                 v_head = a.c.v ? a.c.v_head : a.c.k_head;
-  // lanes 0-15: the page of this lane's position of a tile (-1: no such position)
-  auto lookup = [&](const Cursor &c, bool in) -> int {
-    const int j = c.t * kUnit + warp * kTile + (lane & 15);
-    if (!in || j >= c.row.rows) return -1;
-    return a.table[(int64_t)c.row.req * a.width + P.page.div((uint32_t)(c.row.first + j))];
+  // Two tiles ahead of the copies: the page of this lane's position (the tables' latency passes while the tiles before are
+  // copied).  pos -1: no such position.
+  struct Found {
+    int page, pos, kvh;
   };
-  int64_t todo = nunits;  // units not yet copied
-  int pid = lookup(cl, true);
-  // Copy the cursor's tile into a stage; returns the mask of its positions that are there.
-  auto issue = [&](int stage) -> uint32_t {
-    uint32_t ok = 0;
+  int todo = nunits;  // units not yet looked up
+  auto lookup = [&]() -> Found {
+    Found f{0, -1, -1};
     if (todo > 0) {
-      const int j = cl.t * kUnit + warp * kTile + (lane & 15);
-      const bool there = j < cl.row.rows, good = there && pid >= 0 && pid < a.c.n_pages;
-      if (there && !good && lane < 16) atomicOr(a.status, kStatusBadIndex);
-      ok = __ballot_sync(0xffffffffu, good) & 0xffffu;
-      const uint32_t p = (uint32_t)(cl.row.first + j), r = p - P.page.div(p) * P.page.d;
-      const int kvh = cl.hg / P.sub;
-      const int64_t ko = good ? (int64_t)pid * a.c.k_page + (int64_t)r * a.c.k_row : -1;
-      const int64_t vo = good ? (int64_t)pid * v_page + (int64_t)r * v_row : -1;
-      const bf16 *kh = kbase + (int64_t)kvh * a.c.k_head, *vh = vbase + (int64_t)kvh * v_head;
-      constexpr int CH = HD / 8;  // 16-byte chunks of a row
-      const uint32_t st = ring + stage * S::kStageBytes;
-      // rows of the tile that hold something (the others' weights are 0, but 0 x NaN is not: they are zeroed)
-#pragma unroll
-      for (int i = 0; i < kTile * CH / 32; ++i) {
-        const int e = lane + 32 * i, row = e / CH, ch = e % CH;
-        const int64_t k_off = __shfl_sync(0xffffffffu, ko, row), v_off = __shfl_sync(0xffffffffu, vo, row);
-        const bool in = k_off >= 0 && ch * 8 < hd;
-        const uint32_t dst = st + row * (HD * 2) + ((ch ^ (row & 7)) << 4);
-        attn::cp_async16(dst, in ? kh + k_off + ch * 8 : kbase, in);
-        attn::cp_async16(dst + kTile * HD * 2, in ? vh + v_off + ch * 8 : vbase, in);
+      const int j = cl.t * kUnit + warp * kTile + (lane & (kTile - 1));
+      f.kvh = cl.hg / P.sub;
+      const Row row = rows.get<kUnit>(a, cl.n);
+      if (j < row.rows) {
+        f.pos = row.first + j;
+        f.page = a.table[(int64_t)row.req * a.width + P.page.div((uint32_t)f.pos)];
       }
       --todo;
-      advance(cl);
-      pid = lookup(cl, todo > 0);
+      const int hg0 = cl.hg, n0 = cl.n;
+      advance<kUnit>(a, P.Hg, rows, cl);
+      if (warp == 0 && todo > 0 && (cl.hg != hg0 || cl.n != n0)) {  // the next segment's q on its way to L1
+        const int kv2 = cl.hg / P.sub, sg = cl.hg - kv2 * P.sub, nq = min(NH, P.g - sg * NH);
+        const bf16 *q = a.q + (int64_t)cl.n * a.q_t + (int64_t)(kv2 * P.g + sg * NH) * hd;
+        for (int i = lane * 64; i < nq * hd; i += 32 * 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+      }
+    }
+    return f;
+  };
+  constexpr uint32_t kAll = (1u << kTile) - 1;
+  Found f0 = lookup(), f1 = lookup();
+  // Copy the tile looked up first into a stage; returns the mask of its positions that are there.
+  auto issue = [&](int stage) -> uint32_t {
+    uint32_t ok = 0;
+    const Found f = f0;
+    f0 = f1;
+    f1 = lookup();
+    if (f.kvh >= 0) {
+      const bool there = f.pos >= 0, good = there && f.page >= 0 && f.page < a.c.n_pages;
+      if (there && !good && lane < kTile) atomicOr(a.status, kStatusBadIndex);
+      ok = __ballot_sync(0xffffffffu, good) & kAll;
+      const uint32_t p = (uint32_t)f.pos, r = p - P.page.div(p) * P.page.d;
+      const int64_t ko = good ? (int64_t)f.page * a.c.k_page + (int64_t)r * a.c.k_row : -1;
+      const int64_t vo = good ? (int64_t)f.page * v_page + (int64_t)r * v_row : -1;
+      const bf16 *kh = kbase + (int64_t)f.kvh * a.c.k_head, *vh = vbase + (int64_t)f.kvh * v_head;
+      constexpr int CH = HD / 8;             // 16-byte chunks of a row
+      constexpr int RI = 32 / CH > 0 ? 32 / CH : 1;  // rows a warp copies at a time
+      const uint32_t st = ring + stage * S::kStageBytes;
+      const int ch = lane % CH, r0 = lane / CH;
+      const bool f_in = ch * 8 < hd;
+      if (ok == kAll && __all_sync(0xffffffffu, __shfl_sync(0xffffffffu, r, 0) + (lane & (kTile - 1)) == r)) {
+        // the tile lies in one page: rows one k_row apart
+        const bf16 *ks = kh + __shfl_sync(0xffffffffu, ko, 0) + r0 * a.c.k_row + ch * 8;
+        const bf16 *vs = vh + __shfl_sync(0xffffffffu, vo, 0) + r0 * v_row + ch * 8;
+        if (!f_in) ks = kbase, vs = vbase;
+        const int64_t k_step = f_in ? RI * a.c.k_row : 0, v_step = f_in ? RI * v_row : 0;
+#pragma unroll
+        for (int i = 0; i < kTile / RI; ++i) {
+          const int row = r0 + RI * i;
+          const uint32_t dst = st + row * (HD * 2) + ((ch ^ (row & 7)) << 4);
+          attn::cp_async16(dst, ks, f_in);
+          attn::cp_async16(dst + kTile * HD * 2, vs, f_in);
+          ks += k_step;
+          vs += v_step;
+        }
+      } else {
+        // (rows that are not there as zeros: their weights are 0, but 0 x NaN is not)
+#pragma unroll 4
+        for (int i = 0; i < kTile / RI; ++i) {
+          const int row = r0 + RI * i;
+          const int64_t k_off = __shfl_sync(0xffffffffu, ko, row), v_off = __shfl_sync(0xffffffffu, vo, row);
+          const bool in = k_off >= 0 && f_in;
+          const uint32_t dst = st + row * (HD * 2) + ((ch ^ (row & 7)) << 4);
+          attn::cp_async16(dst, in ? kh + k_off + ch * 8 : kbase, in);
+          attn::cp_async16(dst + kTile * HD * 2, in ? vh + v_off + ch * 8 : vbase, in);
+        }
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     return ok;
   };
 
-  uint32_t masks[S::kStages];  // of the tiles in flight, the oldest first
-#pragma unroll
-  for (int i = 0; i < S::kStages - 1; ++i) masks[i] = issue(i);
-
-  uint32_t qf[HD / 16][4];
-  float acc[HD / 8][4], m[2], l[2];
+  // NH 16: heads are the rows of both products (q and the weights their first operands).  NH 8: positions are the
+  // rows of the first product, features of the second, and the heads the columns of both: half the products,
+  // exponentials and registers where a kv head has no more than eight query heads.
+  constexpr int QR = NH == 16 ? 4 : 2, AT = NH == 16 ? HD / 8 : HD / 16;
+  uint32_t qf[HD / 16][QR];
+  float acc[AT][4], m[2], l[2];  // m, l: of heads qr, qr + 8 (NH 16) or qc, qc + 1 (NH 8); l of this thread's positions
   int h0 = 0, nh = 0;
-  int64_t seg = rg.begin;  // the CTA's first unit of the current segment
+  int seg = 0;  // the CTA's first unit of the current segment
   const int qr = lane >> 2, qc = 2 * (lane & 3);
   auto begin_segment = [&]() {
     const int kvh = cc.hg / P.sub, sg = cc.hg - kvh * P.sub;
@@ -175,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int h = qr + 8 * (e & 1), d = 16 * kk + qc + 8 * (e >> 1);
+      for (int e = 0; e < QR; ++e) {
+        const int h = NH == 16 ? qr + 8 * (e & 1) : qr, d = 16 * kk + qc + 8 * (NH == 16 ? e >> 1 : e);
         qf[kk][e] = h < nh && d < hd ? *reinterpret_cast<const uint32_t *>(q + h * hd + d) : 0u;
       }
 #pragma unroll
-    for (int t = 0; t < HD / 8; ++t)
+    for (int t = 0; t < AT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
     m[0] = m[1] = -INFINITY;
@@ -188,106 +211,142 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
   };
   begin_segment();
 
-  int stage = 0;
-  for (int64_t u = rg.begin; u < rg.end; ++u) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-    __syncwarp();
-    masks[S::kStages - 1] = issue((stage + S::kStages - 1) % S::kStages);
+  uint32_t masks[S::kStages] = {};  // of the tiles in flight, the oldest first
+  int stage = 1;  // of unit u, which goes around the ring with u
+  for (int u = 1 - S::kStages; u < nunits; ++u) {  // (the first rounds only fill the ring)
+    if (u >= 0) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+      __syncwarp();
+    }
+    masks[S::kStages - 1] = issue(stage == 0 ? S::kStages - 1 : stage - 1);
     const uint32_t ok = masks[0];
     const uint32_t sk = ring + stage * S::kStageBytes, sv = sk + kTile * HD * 2;
-    if (ok) {
-      // ---- scores of 16 heads x 16 positions
-      float c[2][4];
+    if (u >= 0 && ok) {
+      // ---- scores: c[t][e], of the head with statistics si(e)
+      constexpr int NT = NH == 16 ? 2 : 1;
+      float c[NT][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[t][e] = 0.f;
-      const int krow = (lane >> 4) * 8 + (lane & 7), kch = (lane >> 3) & 1;
+      const int krow = NH == 16 ? (lane >> 4) * 8 + (lane & 7) : lane & 15, kch = NH == 16 ? (lane >> 3) & 1 : lane >> 4;
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk) {
         uint32_t b[4];
         ldsm4(b, sk + krow * (HD * 2) + (((2 * kk + kch) ^ (krow & 7)) << 4));
-        mma16816(c[0], qf[kk], b[0], b[1]);
-        mma16816(c[1], qf[kk], b[2], b[3]);
-      }
-      // ---- running maximum and sum (a head's 16 scores lie in the four lanes of a quad)
-      float mx[2] = {m[0], m[1]};
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * t + qc + (e & 1);
-          c[t][e] = (ok >> j) & 1u ? c[t][e] * P.scale_log2 : -INFINITY;
-          mx[e >> 1] = fmaxf(mx[e >> 1], c[t][e]);
+        if constexpr (NH == 16) {
+          mma16816(c[0], qf[kk], b[0], b[1]);
+          mma16816(c[1], qf[kk], b[2], b[3]);
+        } else {
+          mma16816(c[0], b, qf[kk][0], qf[kk][1]);
         }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
       }
+      auto si = [](int e) { return NH == 16 ? e >> 1 : e & 1; };
+      // ---- running maxima and sums (NH 16: a head's scores lie in the four lanes of a quad; NH 8: in every fourth lane)
+      float mx[2] = {m[0], m[1]};
+      if (ok == kAll) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            c[t][e] *= P.scale_log2;
+            mx[si(e)] = fmaxf(mx[si(e)], c[t][e]);
+          }
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = NH == 16 ? 8 * t + qc + (e & 1) : qr + 8 * (e >> 1);
+            c[t][e] = (ok >> j) & 1u ? c[t][e] * P.scale_log2 : -INFINITY;
+            mx[si(e)] = fmaxf(mx[si(e)], c[t][e]);
+          }
+      }
+#pragma unroll
+      for (int o = NH == 16 ? 1 : 4; o < (NH == 16 ? 4 : 32); o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
       if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
         float f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          f[i] = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mx[i]);
+          f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mx[i]);
           l[i] *= f[i];
           m[i] = mx[i];
         }
 #pragma unroll
-        for (int t = 0; t < HD / 8; ++t)
+        for (int t = 0; t < AT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][e] *= f[e >> 1];
+          for (int e = 0; e < 4; ++e) acc[t][e] *= f[si(e)];
       }
-      uint32_t ph[4], pl[4];
-      {
-        const float r0 = m[0] == -INFINITY ? 0.f : m[0], r1 = m[1] == -INFINITY ? 0.f : m[1];
+      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      uint32_t ph[2 * NT], pl[2 * NT];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            c[t][e] = exp2f(c[t][e] - (e < 2 ? r0 : r1));
-            l[e >> 1] += c[t][e];
-          }
-          split2(c[t][0], c[t][1], ph[2 * t], pl[2 * t]);
-          split2(c[t][2], c[t][3], ph[2 * t + 1], pl[2 * t + 1]);
+        for (int e = 0; e < 4; ++e) {
+          c[t][e] = ex2(c[t][e] - ref[si(e)]);
+          l[si(e)] += c[t][e];
         }
+        split2(c[t][0], c[t][1], ph[2 * t], pl[2 * t]);
+        split2(c[t][2], c[t][3], ph[2 * t + 1], pl[2 * t + 1]);
       }
       // ---- weighted values
-      const int vrow = lane & 15, vch = lane >> 4;
+      const int vrow = NH == 16 ? lane & 15 : (lane >> 4) * 8 + (lane & 7), vch = NH == 16 ? lane >> 4 : (lane >> 3) & 1;
+      if constexpr (NH == 8) {
+#pragma unroll
+        for (int t = 0; t < 2 * NT; ++t) {
+          ph[t] = transpose8(ph[t]);
+          pl[t] = transpose8(pl[t]);
+        }
+      }
 #pragma unroll
       for (int t = 0; t < HD / 16; ++t) {
         uint32_t b[4];
         ldsm4_t(b, sv + vrow * (HD * 2) + (((2 * t + vch) ^ (vrow & 7)) << 4));
-        mma16816(acc[2 * t], ph, b[0], b[1]);
-        mma16816(acc[2 * t + 1], ph, b[2], b[3]);
-        mma16816(acc[2 * t], pl, b[0], b[1]);
-        mma16816(acc[2 * t + 1], pl, b[2], b[3]);
+        if constexpr (NH == 16) {
+          mma16816(acc[2 * t], ph, b[0], b[1]);
+          mma16816(acc[2 * t + 1], ph, b[2], b[3]);
+          mma16816(acc[2 * t], pl, b[0], b[1]);
+          mma16816(acc[2 * t + 1], pl, b[2], b[3]);
+        } else {
+          mma16816(acc[t], b, ph[0], ph[1]);
+          mma16816(acc[t], b, pl[0], pl[1]);
+        }
       }
     }
-    const bool last = cc.t == cc.row.units - 1;
-    if (last || u + 1 == rg.end) {
+    if (u >= 0 && (cc.t == cc.units - 1 || u + 1 == nunits)) {
       // ---- the segment's end in this CTA: the four warps' accumulators joined
       float *mine = reinterpret_cast<float *>(ring_p + stage * S::kStageBytes);
       __syncwarp();
 #pragma unroll
-      for (int t = 0; t < HD / 8; ++t)
+      for (int t = 0; t < AT; ++t) {
+        if constexpr (NH == 16) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int h = qr + 8 * i;
-          *reinterpret_cast<float2 *>(mine + h * HD + ((8 * t + qc) ^ ((h & 3) << 3))) = make_float2(acc[t][2 * i], acc[t][2 * i + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const int h = qr + 8 * i;
+            *reinterpret_cast<float2 *>(mine + h * HD + ((8 * t + qc) ^ swizzle<NH>(h))) = make_float2(acc[t][2 * i], acc[t][2 * i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int h = qc + (e & 1), d = 16 * t + qr + 8 * (e >> 1);
+            mine[h * HD + (d ^ swizzle<NH>(h))] = acc[t][e];
+          }
         }
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if ((lane & 3) == 0) {
-          s_ml[0][warp][qr + 8 * i] = m[i];
-          s_ml[1][warp][qr + 8 * i] = l[i];
+#pragma unroll
+        for (int o = NH == 16 ? 1 : 4; o < (NH == 16 ? 4 : 32); o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+        if (NH == 16 ? (lane & 3) == 0 : lane < 4) {
+          s_ml[0][warp][NH == 16 ? qr + 8 * i : qc + i] = m[i];
+          s_ml[1][warp][NH == 16 ? qr + 8 * i : qc + i] = l[i];
         }
       }
       __syncthreads();
-      const int64_t sb = u - cc.t, se = sb + cc.row.units;  // the whole segment
-      const bool whole = sb >= rg.begin && se <= rg.end;
+      const int sb = u - cc.t, se = sb + cc.units;  // the whole segment, from this CTA's first unit
+      const bool whole = sb >= 0 && se <= nunits;
       const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
       if (tid < nh) {
         float M = -INFINITY, L = 0.f;
@@ -300,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
           L = fmaf(s_ml[1][w][tid], f, L);
         }
         if (whole) {
-          s_out[0][tid] = out_factor(M, L, a.sink, h0 + tid);
+          s_out[tid] = out_factor(M, L, a.sink, h0 + tid);
           if (a.lse) a.lse[(int64_t)cc.n * a.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         } else {
           *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + tid) * 2) = make_float2(M, L);
@@ -314,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float *src = reinterpret_cast<const float *>(smem + w * (S::kStages * S::kStageBytes) + stage * S::kStageBytes);
-          const float4 x = *reinterpret_cast<const float4 *>(src + h * HD + (d ^ ((h & 3) << 3)));
+          const float4 x = *reinterpret_cast<const float4 *>(src + h * HD + (d ^ swizzle<NH>(h)));
           const float f = s_f[w][h];
           v.x = fmaf(x.x, f, v.x);
           v.y = fmaf(x.y, f, v.y);
@@ -322,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
           v.w = fmaf(x.w, f, v.w);
         }
         if (whole) {
-          const float f = s_out[0][h];
+          const float f = s_out[h];
           *reinterpret_cast<uint2 *>(a.o + (int64_t)cc.n * a.o_t + (int64_t)(h0 + h) * hd + d) =
               make_uint2(bits(__floats2bfloat162_rn(v.x * f, v.y * f)), bits(__floats2bfloat162_rn(v.z * f, v.w * f)));
         } else {
@@ -330,13 +389,13 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
         }
       }
       __syncthreads();  // the stage may be refilled
-      if (!whole) publish<kHeads, HD, kThreads, 0>(P, tid, sb, se, rg, cc.n, h0, nh, s_join, &s_flag);
-      if (u + 1 < rg.end) {
-        advance(cc);
+      if (!whole) publish<kHeads, HD, kThreads>(P, rg.begin + sb, rg.begin + se, rg, cc.n, h0, nh, &s_flag);
+      if (u + 1 < nunits) {
+        advance<kUnit>(a, P.Hg, rows, cc);
         seg = u + 1;
         begin_segment();
       }
-    } else {
+    } else if (u >= 0) {
       ++cc.t;
     }
 #pragma unroll
@@ -346,25 +405,29 @@ __global__ void __launch_bounds__(kThreads, Shape<HD>::kCtas) k_paged_attn(const
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int HD>
-cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
-  using S = Shape<HD>;
+template <int HD, int NH>
+cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+  using S = Shape<HD, NH>;
   static SmemAttr attr;
-  cudaError_t e = attr.ensure((const void *)k_paged_attn<HD>, S::kSmem);
+  cudaError_t e = attr.ensure((const void *)k_paged_attn<HD, NH>, S::kSmem);
   if (e != cudaSuccess) return e;
   const PagedAttnArgs &a = p.a;
-  p.g = a.H / a.c.kv_heads;
-  p.sub = (p.g + kHeads - 1) / kHeads;
+  p.sub = (p.g + NH - 1) / NH;
   p.Hg = p.sub * a.c.kv_heads;
   // no more CTAs than there can be units
   const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
-  const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + kUnit - 1) / kUnit);
+  const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + S::kUnit - 1) / S::kUnit);
   const int64_t grid = std::min<int64_t>(std::min(units, (int64_t)num_sms * S::kCtas), kMaxCtas);
   p.share_o = ws;
-  p.share_ml = ws + 2 * grid * kHeads * HD;
-  if (sizeof(float) * 2 * grid * kHeads * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;
-  k_paged_attn<HD><<<(unsigned)grid, kThreads, S::kSmem, s>>>(p);
+  p.share_ml = ws + 2 * grid * NH * HD;
+  if (sizeof(float) * 2 * grid * NH * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;
+  k_paged_attn<HD, NH><<<(unsigned)grid, S::kThreads, S::kSmem, s>>>(p);
   return cudaGetLastError();
+}
+template <int HD>
+cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+  p.g = p.a.H / p.a.c.kv_heads;
+  return p.g <= 8 ? launch_heads<HD, 8>(p, ws, ws_bytes, num_sms, s) : launch_heads<HD, 16>(p, ws, ws_bytes, num_sms, s);
 }
 
 // (head_dim above 256: k_paged_attn_tc.cu)

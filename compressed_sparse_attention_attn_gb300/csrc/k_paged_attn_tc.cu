@@ -43,44 +43,18 @@ struct L {
   static constexpr size_t p = t + (size_t)2 * kBlocks * kBlock;              // [2][64][128 B]
   static constexpr size_t alpha = p + (size_t)2 * kHeads * 128;              // float [2][64]
   static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
-  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [20]
+  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [17]
   static constexpr size_t bars = scan + 20 * 8;                              // u64 [26]
   static constexpr size_t misc = bars + 26 * 8;                              // masks [2][4], flags, slot, abort
   static constexpr size_t total = misc + 64;
 };
-static_assert(L::total + 1024 <= 232448, "one CTA's shared memory");
+static_assert(L::total + 1024 + sizeof(Rows) + sizeof(Range) + 64 <= 232448, "one CTA's shared memory");
 
 // Every lane waits (each acquires what the barrier publishes); the warp goes on only if all succeeded.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   const bool ok = tc::mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
-// 2^x for x <= 8; results below the smallest normal number are 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-struct Cursor {
-  int n, hg, t;
-  Row row;
-};
-__device__ __forceinline__ void advance(const Params &P, Cursor &c) {
-  if (++c.t < c.row.units) return;
-  c.t = 0;
-  if (++c.hg < P.Hg) return;
-  c.hg = 0;
-  do {
-    if (++c.n >= P.a.N) {
-      c.row.units = 1;
-      c.row.rows = 0;
-      return;
-    }
-    c.row = row_of<kUnit>(P.a, c.n, false);
-  } while (c.row.units == 0);
-}
-
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -99,20 +73,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   const int nkb = (hd + 63) / 64;
 
-  const Range rg = find_range<kUnit, kThreads>(P, reinterpret_cast<int64_t *>(smem + L::scan));
-  if (rg.begin >= rg.end) {
+  __shared__ Rows rows;
+  __shared__ Range rg;
+  const int nt = find_range<kUnit, kThreads>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
+  if (nt == 0) {
     if (tid == 0 && !P.by_segment) P.split[blockIdx.x] = make_int2(0, 0);
     return;
   }
-  const int64_t nt = rg.end - rg.begin;  // this CTA's tiles
-  Cursor c;
-  c.n = rg.row;
-  c.row = row_of<kUnit>(a, c.n, false);
-  {
-    const int64_t in = rg.begin - rg.before;
-    c.hg = (int)(in / c.row.units);
-    c.t = (int)(in - (int64_t)c.hg * c.row.units);
-  }
+  Cursor c = first_unit(rg, rows);
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
       tc::mbar_init(&full[i], 128);  // the lanes of the buffer's four warps
@@ -135,8 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kUnit;  // S: 2 x 64 columns, O^T: 4 x 64
-  auto par = [](int64_t i) { return (uint32_t)((i >> 1) & 1); };  // phase of tile i's barriers
-  auto last_of = [&](int64_t i) { return c.t == c.row.units - 1 || i + 1 == nt; };  // of a segment, in this CTA
+  auto par = [](int i) { return (uint32_t)((i >> 1) & 1); };  // phase of tile i's barriers
+  auto last_of = [&](int i) { return c.t == c.units - 1 || i + 1 == nt; };  // of a segment, in this CTA
 
   if (warp < 2) {
     // ------------------------------------------------------------------------------ softmax
@@ -163,8 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     float m = -INFINITY, l = 0.f;
     int nseg = 0;
     bool first = true;
-    int64_t seg = 0;  // the segment's first tile here
-    for (int64_t i = 0; i < nt; ++i) {
+    int seg = 0;  // the segment's first tile here
+    for (int i = 0; i < nt; ++i) {
       const int b = (int)(i & 1);
       if (!warp_wait(&full[4 * b + 3], par(i), abort_flag)) break;  // (its mask)
       const uint32_t ok0 = masks[4 * b] | masks[4 * b + 1] << 16, ok1 = masks[4 * b + 2] | masks[4 * b + 3] << 16;
@@ -173,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       const bool last = last_of(i);
       Cursor nx = c;
       if (last && i + 1 < nt) {  // q's last reader is done: the next segment's q on its way
-        nx.t = nx.row.units - 1;
-        advance(P, nx);
+        nx.t = nx.units - 1;
+        advance<kUnit>(a, P.Hg, rows, nx);
         load_q(nx);
       }
       float s[64];
@@ -240,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       if (last) {
         const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
         const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
-        const int64_t sb = i - c.t, se = sb + c.row.units;  // the whole segment, from this CTA's first tile
+        const int sb = i - c.t, se = sb + c.units;  // the whole segment, from this CTA's first tile
         const bool whole = sb >= 0 && se <= nt;
         float fo = 1.f;
         if (h < nh) {
@@ -276,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     bool first = true, told = false;
     int nseg = 0;
-    int64_t seg = 0;
-    for (int64_t i = 0; i < nt; ++i) {
+    int seg = 0;
+    for (int i = 0; i < nt; ++i) {
       const int b = (int)(i & 1);
       if (!warp_wait(&stat[b], par(i), abort_flag)) break;
       if (!first && (flags[2 * b] | flags[2 * b + 1])) {
@@ -310,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       tc::tc_fence_after();
       const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
       const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
-      const int64_t sb = i - c.t, se = sb + c.row.units;
+      const int sb = i - c.t, se = sb + c.units;
       const bool whole = sb >= 0 && se <= nt;
       const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
 #pragma unroll 1
@@ -352,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       first = true;
       ++nseg;
       seg = i + 1;
-      c.t = c.row.units - 1;
-      if (i + 1 < nt) advance(P, c);
+      c.t = c.units - 1;
+      if (i + 1 < nt) advance<kUnit>(a, P.Hg, rows, c);
     }
     if (!P.by_segment && jt == 0 && !told) P.split[blockIdx.x] = make_int2(0, 0);
   } else if (warp == 2) {
@@ -416,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       ok = warp_wait(&full[w], 0, abort_flag);
       if (ok) scores(0, w);
     }
-    for (int64_t i = 0; i < nt && ok; ++i) {
+    for (int i = 0; i < nt && ok; ++i) {
       const int b = (int)(i & 1), nb = b ^ 1;
       const bool last = last_of(i);
       // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
@@ -453,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       if (!ok) break;
       first = last;
       if (last) {
-        c.t = c.row.units - 1;
-        if (i + 1 < nt) advance(P, c);
+        c.t = c.units - 1;
+        if (i + 1 < nt) advance<kUnit>(a, P.Hg, rows, c);
       } else {
         ++c.t;
       }
@@ -471,12 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     const int b = (warp - 8) >> 2, part = warp & 3;
     const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
     const int cc = lane & 7;
-    if (b == 1 && nt > 1) advance(P, c);
-    for (int64_t i = b; i < nt; i += 2) {
+    if (b == 1 && nt > 1) advance<kUnit>(a, P.Hg, rows, c);
+    for (int i = b; i < nt; i += 2) {
+      const Row row = rows.get<kUnit>(a, c.n);
       const int j = c.t * kUnit + part * 16 + (lane & 15);
-      const bool there = j < c.row.rows;
-      const uint32_t pos = (uint32_t)(c.row.first + j), pg = P.page.div(pos);
-      const int id = there ? a.table[(int64_t)c.row.req * a.width + pg] : 0;
+      const bool there = j < row.rows;
+      const uint32_t pos = (uint32_t)(row.first + j), pg = P.page.div(pos);
+      const int id = there ? a.table[(int64_t)row.req * a.width + pg] : 0;
       const bool good = there && id >= 0 && id < a.c.n_pages;
       if (there && !good) atomicOr(a.status, kStatusBadIndex);
       const int64_t off = good ? (int64_t)id * a.c.k_page + (int64_t)(pos - pg * P.page.d) * a.c.k_row +
@@ -519,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       attn::fence_proxy_async();
       tc::mbar_arrive(&full[4 * b + 3]);
-      if (i + 1 < nt) advance(P, c);
-      if (i + 2 < nt) advance(P, c);
+      if (i + 1 < nt) advance<kUnit>(a, P.Hg, rows, c);
+      if (i + 2 < nt) advance<kUnit>(a, P.Hg, rows, c);
     }
     attn::cp_async_wait_all();
   }

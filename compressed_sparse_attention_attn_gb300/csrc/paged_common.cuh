@@ -3,16 +3,16 @@
 //
 // A segment is the work of one (row, head group): its positions in units of U rows, at least one (an empty row
 // writes zeros).  The segments' units stand one behind the other (row, head group, unit); of their total T
-// CTA c of G takes [T c / G, T (c + 1) / G), so every CTA has the same number of rows to read whatever the
-// lengths are, and at most the first and the last segment of its range are shared with others.  The host knows
+// each of G CTAs takes T / G in a row (the first T mod G one more), so every CTA has the same number of rows to read whatever the
+// lengths are (the first T mod G CTAs one unit more), and at most the first and the last segment of its range are shared with others.  The host knows
 // no lengths: every CTA sums the units itself.
 //
 // A CTA's share of a segment is (M, L, O): its running maximum (base 2), sum of weights and weighted sum of
 // values relative to M, in f32, in one of its two slots (0: a segment that began in an earlier CTA, 1: one
-// that begins here).  Twenty consecutive shares of a segment are a group.  The CTA that completes a group
+// that begins here).  Twelve consecutive shares of a segment are a group.  The CTA that completes a group
 // joins it (in the order of the shares, whoever is last); with more than one group the joined shares go to
 // the group's first slot, and the CTA that completes the last group joins those.  So a long row over 300
-// CTAs is joined in two steps of at most 20, and nothing waits.  The counters return to zero.
+// CTAs is joined in two steps, of 12 and of 26 shares, and nothing waits.  The counters return to zero.
 #pragma once
 
 #include "csa_internal.cuh"
@@ -21,9 +21,8 @@
 namespace csa {
 namespace paged {
 
-constexpr int kJoin = 20;          // shares of a group
-constexpr int kMaxJoin = 32;       // groups of a segment
-constexpr int kMaxCtas = kJoin * kMaxJoin;
+constexpr int kJoin = 12;          // shares of a group
+constexpr int kMaxCtas = 640;
 
 // x / d for 0 <= x < 2^31 by a multiplication: m = ceil(2^(31+s) / d), s = ceil(log2 d); m d - 2^(31+s) < d <=
 // 2^s, so the error x (m d - 2^(31+s)) / (d 2^(31+s)) stays below 1 / d (Granlund and Montgomery, 1994).
@@ -82,20 +81,49 @@ __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report
   return r;
 }
 
-// A CTA's range of units and the row its first unit lies in.
+// A CTA's range of units and the row its first unit lies in.  Units are counted in 32 bits: a call whose rows come
+// to 2^31 units or more (2^37 positions and heads) does nothing but report it.
 struct Range {
-  int64_t total, begin, end;  // units
-  int ctas;                   // CTAs that share them: no more than there are units, so that none between two has nothing
+  uint32_t total, begin, end;  // units
+  uint32_t each, more;         // units a CTA; the first `more` CTAs have one more
+  uint32_t before;             // units (of all its segments) before the row
   int row;
-  int64_t before;             // units (of all its segments) before that row
 };
-// Called by all NT threads of the CTA.  scratch: int64 [NT / 32 + 4] in shared memory.
+// The first rows of a CTA's range, kept in shared memory: the cursors read a new row there and not through two
+// dependent loads from global memory.
+constexpr int kRowsKept = 32;
+struct Rows {
+  int n0;
+  Row row[kRowsKept];
+  template <int U>
+  __device__ __forceinline__ Row get(const PagedAttnArgs &a, int n) const {
+    return (unsigned)(n - n0) < (unsigned)kRowsKept ? row[n - n0] : row_of<U>(a, n, false);
+  }
+};
+
+// Where a thread is in its CTA's range: segment (row n, head group hg) of `units` units, unit t of it.
+struct Cursor {
+  int n, hg, t, units;
+};
+template <int U>
+__device__ __forceinline__ void advance(const PagedAttnArgs &a, int Hg, const Rows &rows, Cursor &c) {
+  if (++c.t < c.units) return;
+  c.t = 0;
+  if (++c.hg < Hg) return;
+  c.hg = 0;
+  do {
+    if (++c.n >= a.N) return;  // (past the last unit: not used any more)
+    c.units = rows.get<U>(a, c.n).units;
+  } while (c.units == 0);
+}
+
+// Called by all NT threads of the CTA.  scratch: int64 [NT / 32 + 1], rows, out: all in shared memory.  Returns how many
+// units the CTA has.
 template <int U, int NT>
-__device__ __forceinline__ Range find_range(const Params &P, int64_t *scratch) {
+__device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Rows &rows, Range &out) {
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   constexpr int NW = NT / 32;
-  int64_t *found = scratch + NW;  // row, before, total
   const bool report = blockIdx.x == 0;
   auto scan = [&](int64_t v, int64_t &sum) -> int64_t {  // inclusive over the CTA; sum: of all
     int64_t x = v;
@@ -116,19 +144,26 @@ __device__ __forceinline__ Range find_range(const Params &P, int64_t *scratch) {
     }
     return x + b;
   };
-  Range r;
   int64_t mine = 0;
   for (int n = tid; n < a.N; n += NT) mine += row_of<U>(a, n, report).units;
   int64_t sum;
   int64_t incl = scan(mine, sum);
-  r.total = sum * P.Hg;
-  r.ctas = (int)min((int64_t)gridDim.x, r.total);
-  const bool works = (int)blockIdx.x < r.ctas;
-  r.begin = works ? r.total * blockIdx.x / r.ctas : 0;
-  r.end = works ? r.total * (blockIdx.x + 1) / r.ctas : 0;
-  r.row = 0;
-  r.before = 0;
-  if (r.begin >= r.end) return r;
+  if (sum * P.Hg > 0x7fffffff) {
+    if (report && tid == 0) atomicOr(a.status, kStatusBadIndex);
+    return 0;
+  }
+  // no more CTAs than there are units, so that none between two has nothing
+  const uint32_t total = (uint32_t)sum * P.Hg, ctas = min(gridDim.x, total);
+  if (blockIdx.x >= ctas) return 0;
+  const uint32_t each = total / ctas, more = total - each * ctas;
+  const uint32_t begin = each * blockIdx.x + min(blockIdx.x, more), end = begin + each + (blockIdx.x < more ? 1 : 0);
+  if (tid == 0) {
+    out.total = total;
+    out.begin = begin;
+    out.end = end;
+    out.each = each;
+    out.more = more;
+  }
   int64_t base = 0;
   for (int n0 = 0; n0 < a.N; n0 += NT) {  // one round for up to NT rows
     if (a.N > NT) {
@@ -136,21 +171,46 @@ __device__ __forceinline__ Range find_range(const Params &P, int64_t *scratch) {
       incl = scan(mine, sum);
     }
     const int64_t lo = (base + incl - mine) * P.Hg, hi = (base + incl) * P.Hg;
-    if (r.begin >= lo && r.begin < hi) {
-      found[0] = n0 + tid;
-      found[1] = lo;
+    if (begin >= lo && begin < hi) {
+      out.row = n0 + tid;
+      out.before = (uint32_t)lo;
     }
     base += sum;
-    if (r.begin < base * P.Hg) break;
+    if (begin < base * P.Hg) break;
   }
   __syncthreads();
-  r.row = (int)found[0];
-  r.before = found[1];
-  return r;
+  if (tid < kRowsKept) {
+    const int n = out.row + tid;
+    const Row none{0, 0, 0, 0};
+    if (tid == 0) rows.n0 = n;
+    rows.row[tid] = n < a.N ? row_of<U>(a, n, false) : none;
+  }
+  __syncthreads();
+  return (int)(end - begin);
+}
+// The cursor at the beginning of the range.
+__device__ __forceinline__ Cursor first_unit(const Range &r, const Rows &rows) {
+  Cursor c;
+  c.n = r.row;
+  c.units = rows.row[0].units;
+  const uint32_t in = r.begin - r.before;
+  c.hg = (int)(in / (uint32_t)c.units);
+  c.t = (int)(in - (uint32_t)c.hg * c.units);
+  return c;
 }
 
-// The CTA that unit u belongs to: the largest c with T c / G <= u.
-__device__ __forceinline__ int cta_of(int64_t u, const Range &r) { return (int)(((u + 1) * r.ctas - 1) / r.total); }
+// 2^x; results below the smallest normal number are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The CTA that unit u belongs to.
+__device__ __forceinline__ int cta_of(uint32_t u, const Range &r) {
+  const uint32_t first = r.more * (r.each + 1);  // units of the CTAs with one more
+  return (int)(u < first ? u / (r.each + 1) : r.more + (u - first) / r.each);
+}
 
 // One more arrival at a counter of `of` (by one thread, after a CTA barrier behind the writes it publishes);
 // true for the last, which finds the others' writes.
@@ -172,109 +232,103 @@ __device__ __forceinline__ float out_factor(float M, float L, const float *sink,
   return below == 0.f ? 0.f : em / below;
 }
 
-// Barrier of the NT threads that join: the whole CTA (BAR 0) or named barrier BAR.
-template <int NT, int BAR>
-__device__ __forceinline__ void join_sync() {
-  if constexpr (BAR == 0)
-    __syncthreads();
-  else
-    tc::named_bar(BAR, NT);
-}
-
-// Join `parts` shares, shares i of slots slot(i), of NH heads x HD features by NT threads (tid of them).  fin: write
-// O and lse of heads h0 .. h0+nh-1 of row n; else the joined share to slot `to`.
-// sf: kJoinFloats<NH> floats of shared memory.
-template <int NH>
-constexpr int kJoinFloats = (kMaxJoin + 2) * NH;
-template <int NH, int HD, int NT, int BAR, class Slot>
-__device__ __forceinline__ void join(const Params &P, int tid, int parts, Slot slot, bool fin, int to, int n, int h0, int nh,
-                                     float *sf) {
+// Join `parts` shares, shares i of slots slot(i), of NH heads x HD features by the NT threads of the CTA.  fin: write O
+// and lse of heads h0 .. h0+nh-1 of row n; else the joined share to slot `to` (one of the slots: a thread writes
+// only what it alone has read, the maxima and sums behind a barrier).  A thread reads the maxima and sums of its
+// head itself, with the values: one round trip a dozen shares, and no barrier.
+template <int NH, int HD, int NT, class Slot>
+__device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool fin, int to, int n, int h0, int nh) {
   const PagedAttnArgs &a = P.a;
-  float *sM = sf + kMaxJoin * NH, *sL = sM + NH;
-  for (int i = tid; i < parts * nh; i += NT) {
-    const int p = i / nh, h = i % nh;
-    sf[p * NH + h] = __ldcg(P.share_ml + ((int64_t)slot(p) * NH + h) * 2);
-  }
-  join_sync<NT, BAR>();
-  if (tid < nh) {
-    float M = -INFINITY;
-    for (int p = 0; p < parts; ++p) M = fmaxf(M, sf[p * NH + tid]);
-    float L = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float m = sf[p * NH + tid];
-      const float f = m == -INFINITY ? 0.f : exp2f(m - M);
-      sf[p * NH + tid] = f;
-      L = fmaf(__ldcg(P.share_ml + ((int64_t)slot(p) * NH + tid) * 2 + 1), f, L);
-    }
-    sL[tid] = L;
-    if (fin) {
-      sM[tid] = out_factor(M, L, a.sink, h0 + tid);
-      if (a.lse) a.lse[(int64_t)n * a.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-    } else {
-      sM[tid] = M;
-    }
-  }
-  join_sync<NT, BAR>();
   const int hd = a.c.head_dim;
-  for (int i = tid; i < nh * (HD / 4); i += NT) {
-    const int h = i / (HD / 4), d = (i % (HD / 4)) * 4;
-    if (d >= hd) continue;
+  float M = -INFINITY, L = 0.f;
+  constexpr int kRounds = (NH * (HD / 4) + NT - 1) / NT;
+  float keep_m[kRounds], keep_l[kRounds];
+#pragma unroll
+  for (int rd = 0; rd < kRounds; ++rd) {
+    const int i = threadIdx.x + rd * NT, h = i / (HD / 4), d = (i % (HD / 4)) * 4;
+    keep_m[rd] = keep_l[rd] = 0.f;
+    if (h >= nh || d >= hd) continue;
+    M = -INFINITY;
+    L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < parts; p0 += 8) {
-      float4 x[8];
+    for (int p0 = 0; p0 < parts; p0 += kJoin) {
+      float2 ml[kJoin];
+      float4 x[kJoin];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (p0 + u < parts) x[u] = __ldcg(reinterpret_cast<const float4 *>(P.share_o + ((int64_t)slot(p0 + u) * NH + h) * HD + d));
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < kJoin; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p0 + u < parts) {
-          const float f = sf[(p0 + u) * NH + h];
-          v.x = fmaf(x[u].x, f, v.x);
-          v.y = fmaf(x[u].y, f, v.y);
-          v.z = fmaf(x[u].z, f, v.z);
-          v.w = fmaf(x[u].w, f, v.w);
+          const int64_t at = (int64_t)slot(p0 + u) * NH + h;
+          ml[u] = __ldcg(reinterpret_cast<const float2 *>(P.share_ml) + at);
+          x[u] = __ldcg(reinterpret_cast<const float4 *>(P.share_o + at * HD + d));
         }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) top = fmaxf(top, ml[u].x);
+      const float ref = top == -INFINITY ? 0.f : top, f0 = ex2(M - ref);  // (2^-inf = 0)
+      M = top;
+      L *= f0;
+      v.x *= f0;
+      v.y *= f0;
+      v.z *= f0;
+      v.w *= f0;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const float f = ex2(ml[u].x - ref);
+        L = fmaf(ml[u].y, f, L);
+        v.x = fmaf(x[u].x, f, v.x);
+        v.y = fmaf(x[u].y, f, v.y);
+        v.z = fmaf(x[u].z, f, v.z);
+        v.w = fmaf(x[u].w, f, v.w);
+      }
     }
+    keep_m[rd] = M;
+    keep_l[rd] = L;
     if (fin) {
-      const float f = sM[h];
-      __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
-      uint2 w = make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-      *reinterpret_cast<uint2 *>(a.o + (int64_t)n * a.o_t + (int64_t)(h0 + h) * hd + d) = w;
+      const float f = out_factor(M, L, a.sink, h0 + h);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+      *reinterpret_cast<uint2 *>(a.o + (int64_t)n * a.o_t + (int64_t)(h0 + h) * hd + d) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+      if (a.lse && d == 0) a.lse[(int64_t)n * a.H + h0 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     } else {
       *reinterpret_cast<float4 *>(P.share_o + ((int64_t)to * NH + h) * HD + d) = v;
     }
   }
-  if (!fin && tid < nh) {
-    float2 ml = make_float2(sM[tid], sL[tid]);
-    *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)to * NH + tid) * 2) = ml;
+  if (fin) return;
+  __syncthreads();  // every thread has read the slots' maxima and sums
+#pragma unroll
+  for (int rd = 0; rd < kRounds; ++rd) {
+    const int i = threadIdx.x + rd * NT, h = i / (HD / 4), d = (i % (HD / 4)) * 4;
+    if (h < nh && d == 0)
+      *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)to * NH + h) * 2) = make_float2(keep_m[rd], keep_l[rd]);
   }
-  join_sync<NT, BAR>();
 }
 
-// Publish this CTA's share of the segment of units [sb, se) (already written to its slot by the NT threads, or
-// by threads they have synchronised with) and join what it completes.  flag: an int in shared memory.
-template <int NH, int HD, int NT, int BAR>
-__device__ __forceinline__ void publish(const Params &P, int tid, int64_t sb, int64_t se, const Range &r, int n, int h0, int nh,
-                                        float *sf, int *flag) {
+// Publish this CTA's share of the segment of units [sb, se) (already written to its slot by the CTA's threads) and join
+// what it completes.  flag: an int in shared memory.
+template <int NH, int HD, int NT>
+__device__ __forceinline__ void publish(const Params &P, uint32_t sb, uint32_t se, const Range &r, int n, int h0, int nh,
+                                        int *flag) {
   const int c0 = cta_of(sb, r), c1 = cta_of(se - 1, r);
   const int parts = c1 - c0 + 1, mine = (int)blockIdx.x - c0, grp = mine / kJoin, ngrp = (parts + kJoin - 1) / kJoin;
-  const int in_grp = min(kJoin, parts - grp * kJoin);
+  const int first = grp * kJoin, in_grp = min(kJoin, parts - first);
   auto slot_of = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
-  join_sync<NT, BAR>();
-  if (tid == 0) {
-    int *ctr = grp == 0 ? P.counters + kMaxCtas + c0 : P.counters + c0 + grp * kJoin;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int *ctr = grp == 0 ? P.counters + kMaxCtas + c0 : P.counters + c0 + first;
     *flag = arrive_last(ctr, in_grp) ? 1 : 0;
   }
-  join_sync<NT, BAR>();
+  __syncthreads();
   if (!*flag) return;
-  const int first = grp * kJoin;
-  join<NH, HD, NT, BAR>(P, tid, in_grp, [&](int p) { return slot_of(first + p); }, ngrp == 1, slot_of(first), n, h0, nh, sf);
+  join<NH, HD, NT>(P, in_grp, [&](int p) { return slot_of(first + p); }, ngrp == 1, slot_of(first), n, h0, nh);
   if (ngrp == 1) return;
-  if (tid == 0) *flag = arrive_last(P.counters + 2 * kMaxCtas + c0, ngrp) ? 1 : 0;
-  join_sync<NT, BAR>();
+  __syncthreads();
+  if (threadIdx.x == 0) *flag = arrive_last(P.counters + 2 * kMaxCtas + c0, ngrp) ? 1 : 0;
+  __syncthreads();
   if (!*flag) return;
-  join<NH, HD, NT, BAR>(P, tid, ngrp, [&](int p) { return slot_of(p * kJoin); }, true, 0, n, h0, nh, sf);
+  join<NH, HD, NT>(P, ngrp, [&](int p) { return slot_of(p * kJoin); }, true, 0, n, h0, nh);
 }
 
 }  // namespace paged

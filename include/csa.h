@@ -389,7 +389,7 @@ typedef struct csa_paged {
  * Nothing but info, tok_* (-1) and cu (0) changes when an error bit is set (length_out and state_out receive
  * the old values): 1 more than N tokens, 2 a length negative or past width pages, 4 more pages needed than
  * are free, 8 a state outside the ring.  A table or ring entry outside [0, n_pages) gives its tokens slot -1.
- * R <= 16384, width, N and n_pages * page below 2^30.  Not tied to a context; calls that share buffers are
+ * R <= 14000, width, N and n_pages * page below 2^30.  Not tied to a context; calls that share buffers are
  * ordered by the caller. */
 CSA_API int csa_page_step(const int32_t *new_len, int R, int page, const int32_t *length, int32_t *table, int width,
                           int32_t *free_ring, int n_pages, const int32_t *state, int32_t *tok_req, int32_t *tok_pos,
@@ -404,7 +404,7 @@ CSA_API int csa_page_step(const int32_t *new_len, int R, int page, const int32_t
  * contexts come in through it).  Value rows are copied.
  * q [N][H][head_dim], k and v [N][cache->kv_heads][head_dim] with element strides per token and head (x_t, x_h,
  * multiples of 8, 16-byte aligned bases); q_out likewise, it may be q itself.  pos, slot int32 [N].
- * A token with pos < 0 is padding: nothing of it is read or written.  slot -1: only its query is produced.
+ * A token with pos < 0 is padding: nothing of it is written.  slot -1: only its query is produced.
  * cache->v NULL: v is not read (may be NULL).  q NULL: keys and values only.  slot NULL: token n goes to row
  * n.  No two tokens may have the same slot, and k, v may not overlap the cache.
  * A pos >= tab_rows or a slot outside [-1, n_pages * page) is a caller error: the token is skipped and

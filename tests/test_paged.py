@@ -139,7 +139,7 @@ def test_page_step_small(csa, page, in_place):
     check_step(csa, lens, steps, page, need, 3 * page + 12, 6 * page + 12, need - 2, in_place=in_place)
 
 
-@pytest.mark.parametrize("R,N,page", [(1, 1, 16), (1, 5000, 16), (300, 300, 16), (1025, 4500, 32), (5000, 9000, 7), (16384, 20000, 64)])
+@pytest.mark.parametrize("R,N,page", [(1, 1, 16), (1, 5000, 16), (300, 300, 16), (1025, 4500, 32), (5000, 9000, 7), (14000, 20000, 64)])
 def test_page_step_sizes(csa, R, N, page):
     rng = np.random.default_rng(R)
     lens = rng.integers(0, 6 * page, R).tolist()
