@@ -601,6 +601,8 @@ int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, 
   if (cache->v && !v) return fail(CSA_ERR_ARG, "%s: the cache holds values, v is NULL", who);
   const int hd = cache->head_dim;
   if (N < 0 || (q && H <= 0) || hd > 1024) return fail(CSA_ERR_ARG, "%s: N %d, H %d, head_dim %d (<= 1024)", who, N, H, hd);
+  if ((int64_t)N * ((q ? H : 0) + (int64_t)cache->kv_heads * (cache->v ? 2 : 1)) > 0x7fffffff)
+    return fail(CSA_ERR_SHAPE, "%s: %d tokens of %d query heads: more than 2^31 rows", who, N, H);
   if (rd < 0 || rd % 2 || at < 0 || at % 2 || at + rd > hd || (rd > 0 && (!tab || tab_rows <= 0)))
     return fail(CSA_ERR_ARG, "%s: rotation of %d features from %d of %d, %d table rows", who, rd, at, hd, tab_rows);
   if ((uintptr_t)tab & 7) return fail(CSA_ERR_ARG, "%s: the table must be 8-byte aligned", who);
@@ -617,7 +619,7 @@ int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, 
   csa::NormRopeArgs a{(const bf16 *)q, (const bf16 *)k, (const bf16 *)(cache->v ? v : nullptr), q_t, q_h, k_t, k_h, v_t, v_h, N,
                       q ? H : 0, *cache, pos, slot, q_norm, k_norm, eps, tab, tab_rows, rd, at, half ? 1 : 0,
                       (bf16 *)q_out, o_t, o_h, ctx->status};
-  CSA_CUDA(csa::launch_norm_rope(a, ctx->num_sms, (cudaStream_t)stream), who);
+  CSA_CUDA(csa::launch_norm_rope(a, (cudaStream_t)stream), who);
   return CSA_OK;
 }
 

@@ -255,7 +255,7 @@ struct NormRopeArgs {
   int64_t o_t, o_h;
   int *status;
 };
-cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s);
 
 // Attention of single tokens over the paged cache (csa_paged_attn's arguments).
 struct PagedAttnArgs {

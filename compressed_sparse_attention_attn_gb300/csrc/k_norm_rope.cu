@@ -1,313 +1,296 @@
 // k_norm_rope.cu -- RMSNorm of each query and key head, the position rotation and the write into a paged
 // cache, in one pass over the rows.
 //
-// A head's row (head_dim features) is held by a group of 4 to 32 lanes, V vectors of 8 features a lane
-// (vector lane + G*u of the row), so the sum of squares is a few shuffles and a row is read once:
 //   y = x r w,  r = 1 / sqrt(mean(x^2) + eps);  (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c) over the pairs
-// of the turned part, everything in f32, one rounding to bf16 at the store (a normed value rounded before
-// its turn would add a second error of the same size).  Adjacent pairs lie in one lane's vector.  Pairs half
-// the turned part apart do not: a lane reads its partners' vectors too (the L1 lines its neighbours have
-// just fetched), which needs no rule on where a partner's lane is.
+// of the turned part, everything in f32, one rounding to bf16 at the store (a normed value rounded before its
+// turn would add a second error of the same size).  A group of 2 to 32
+// lanes holds a row, its angles and weights come from L1 (all rows of a token, and all tokens, share them).
 //
-// Bound by HBM: a row is read and written once; the angles of a token are shared by its heads through L1.
-// Value rows are copies of the same shape.
+// Bound by HBM: a row is read and written once (4096 tokens of 64 x 512 and one 512-wide key row, 546 MB: 96 us, 5.7
+// TB/s; 8000 tokens of 32 + 8 + 8 heads of 128, 201 MB: 42 us, 4.8 TB/s).  The instructions come close to it at 64 to
+// 128 features, so the arithmetic is on pairs of f32 and a lane holds both vectors of a pair of halves: nothing is
+// read twice, and only the sum of squares crosses lanes.
 #include <algorithm>
 
 #include "csa_internal.cuh"
-#include "rowops.cuh"
+#include "paged_common.cuh"
 
 namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void unpack(const uint4 &w, float (&v)[8]) {
-  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[2 * e] = __low2float(h[e]);
-    v[2 * e + 1] = __high2float(h[e]);
-  }
+// ---- two f32 at a time ----
+struct f2 {
+  float x, y;
+};
+__device__ __forceinline__ unsigned long long pk(f2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
-  uint4 w;
-  __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&w);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-  return w;
+__device__ __forceinline__ f2 up(unsigned long long r) {
+  f2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
 }
-
-// 8 floats of w at feature f (ones where w is NULL)
-template <bool FAST>
-__device__ __forceinline__ void load_w(const float *w, int f, float (&v)[8]) {
-  if (!w) {
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)), "l"(pk(c)));
+  return up(r);
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+  return up(r);
+}
+// four pairs of a 16-byte vector of bf16
+__device__ __forceinline__ void unpack(const uint4 &w, f2 (&v)[4]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 1.f;
-  } else if (FAST) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(w + f + e));
-      v[e] = x.x;
-      v[e + 1] = x.y;
-      v[e + 2] = x.z;
-      v[e + 3] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __ldg(w + f + e);
-  }
+  for (int e = 0; e < 4; ++e) v[e] = {__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)};
+}
+__device__ __forceinline__ uint32_t pack2(f2 a) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The (cos, sin) that the 8 features from f on are turned by, and the sign with which the partner enters: (y, z) ->
-// y c + z s' with s' = -s for the first of a pair.  FAST: the turned part and its halves start and end on
-// vector borders.  Outside the turned part: c = 1, s' = 0.
-template <bool FAST>
-__device__ __forceinline__ void load_angles(const NormRopeArgs &a, const float2 *tp, int f, float (&c)[8], float (&s)[8]) {
-  const int h2 = a.rd >> 1;
-  if (FAST && (f < a.at || f >= a.at + a.rd)) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
-  } else if (FAST && a.half) {
-    const bool low = f < a.at + h2;
-    const int i0 = low ? f - a.at : f - a.at - h2;
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(tp + i0 + e));
-      c[e] = x.x;
-      c[e + 1] = x.z;
-      s[e] = low ? -x.y : x.y;
-      s[e + 1] = low ? -x.w : x.w;
-    }
-  } else if (FAST) {
-    const int i0 = (f - a.at) >> 1;
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(tp + i0 + e / 2));
-      c[e] = c[e + 1] = x.x;
-      s[e] = -x.y;
-      s[e + 1] = x.y;
-      c[e + 2] = c[e + 3] = x.z;
-      s[e + 2] = -x.w;
-      s[e + 3] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = f + e - a.at;  // feature of the turned part
-      c[e] = 1.f;
-      s[e] = 0.f;
-      if (d < 0 || d >= a.rd) continue;
-      const bool first = a.half ? d < h2 : !(d & 1);
-      const float2 x = __ldg(tp + (a.half ? (first ? d : d - h2) : d >> 1));
-      c[e] = x.x;
-      s[e] = first ? -x.y : x.y;
-    }
-  }
-}
-
-// The partners' normed values (before the scale r): features half the turned part away, from the row in memory.
-template <bool FAST>
-__device__ __forceinline__ void load_partners(const NormRopeArgs &a, const bf16 *x, int f, uint4 &z) {
-  const int h2 = a.rd >> 1;
-  z = make_uint4(0, 0, 0, 0);
-  if (FAST) {
-    if (f >= a.at && f < a.at + a.rd) z = *reinterpret_cast<const uint4 *>(x + (f < a.at + h2 ? f + h2 : f - h2));
-  } else {
-    bf16 *zb = reinterpret_cast<bf16 *>(&z);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = f + e - a.at;
-      if (d >= 0 && d < a.rd) zb[e] = x[d < h2 ? f + e + h2 : f + e - h2];
-    }
-  }
-}
-template <bool FAST>
-__device__ __forceinline__ void load_partner_w(const NormRopeArgs &a, const float *w, int f, float (&v)[8]) {
-  const int h2 = a.rd >> 1;
-  if (FAST) {
-    load_w<true>(w, f >= a.at && f < a.at + a.rd ? (f < a.at + h2 ? f + h2 : f - h2) : f, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = f + e - a.at;
-      v[e] = w && d >= 0 && d < a.rd ? __ldg(w + (d < h2 ? f + e + h2 : f + e - h2)) : 1.f;
-    }
-  }
-}
-
-// G lanes a row, V vectors a lane (head_dim <= 8 G V).  A group of lanes takes `per` heads of one kind (query, key,
-// value) of one token, U at a time with the next U's vectors in flight; the norm's weights and the token's angles,
-// multiplied together, stay in registers for all of them.  Items are (token, block of `per` heads), a token's
-// query, key and value blocks in a row.
-template <int G, int V, int U, bool HALF, bool FAST>
-__global__ void __launch_bounds__(kThreads, V == 4 ? 1 : (V == 2 && HALF ? 2 : 3)) k_norm_rope(const __grid_constant__ NormRopeArgs a, int per, int q_blocks,
-                                                           int k_blocks, int per_token, int64_t items) {
-  const int lane = threadIdx.x & (G - 1);
-  const int hd = a.c.head_dim;
-  const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G;
-  const bool in = item < items;
-  const int n = in ? (int)(item / per_token) : 0;
-  const int jb = in ? (int)(item - (int64_t)n * per_token) : 0;
-  const int kind = jb < q_blocks ? 0 : (jb < q_blocks + k_blocks ? 1 : 2);  // query, key, value
-  const int h0 = (kind == 0 ? jb : (kind == 1 ? jb - q_blocks : jb - q_blocks - k_blocks)) * per;
-  const int nh = min(per, (kind == 0 ? a.H : a.c.kv_heads) - h0);
-  const int64_t x_h = kind == 0 ? a.q_h : (kind == 1 ? a.k_h : a.v_h);
-  const bf16 *x = (kind == 0 ? a.q + n * a.q_t : (kind == 1 ? a.k + n * a.k_t : a.v + n * a.v_t)) + h0 * x_h;
-  uint4 cur[U][V], nxt[U][V];
-  auto load = [&](uint4 (&d)[U][V], int t0) {
-#pragma unroll
-    for (int t = 0; t < U; ++t)
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const int f = 8 * (lane + G * u);
-        d[t][u] = make_uint4(0, 0, 0, 0);
-        if (in && t0 + t < nh && f < hd) d[t][u] = *reinterpret_cast<const uint4 *>(x + (int64_t)(t0 + t) * x_h + f);
-      }
-  };
-  load(cur, 0);  // (the rows of padding tokens exist too)
-  const int p = in ? a.pos[n] : -1;
-  const int rows = a.c.n_pages * a.c.page;
-  const int slot = !in ? -1 : (a.slot ? a.slot[n] : n);
-  bool live = in && p >= 0;
-  if (live && ((a.rd > 0 && p >= a.tab_rows) || slot < -1 || slot >= rows)) {
-    if (jb == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
-    live = false;
-  }
-  if (kind != 0 && slot < 0) live = false;
-  int64_t y_h;
+// What the two kernels share: the row a group of lanes works on, and whether it is written.
+struct Item {
+  bool in, live, plain;  // plain: a value row, copied
+  int n, pos;
+  const bf16 *x;
   bf16 *y;
-  if (kind == 0) {
-    y_h = a.o_h;
-    y = a.q_out + n * a.o_t + h0 * y_h;
-  } else {
-    const int pg = live ? (int)((uint32_t)slot / (uint32_t)a.c.page) : 0, row = live ? slot - pg * a.c.page : 0;
-    y_h = kind == 1 ? a.c.k_head : a.c.v_head;
-    y = (kind == 1 ? reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row
-                   : reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row) + h0 * y_h;
+  const float *w;
+};
+struct Grid {  // items are (token, head), a token's query, key and value heads in a row
+  int items;
+  paged::FastDiv per_token, page;
+};
+__device__ __forceinline__ int find_item(const NormRopeArgs &a, const Grid &g, int64_t i, Item &t) {
+  t.in = i < g.items;
+  const int item = t.in ? (int)i : 0;
+  t.n = (int)g.per_token.div((uint32_t)item);
+  const int h = item - t.n * (int)g.per_token.d;
+  const int kind = h < a.H ? 0 : (h < a.H + a.c.kv_heads ? 1 : 2);
+  const int hh = kind == 0 ? h : (kind == 1 ? h - a.H : h - a.H - a.c.kv_heads);
+  t.plain = kind == 2;
+  t.x = kind == 0 ? a.q + t.n * a.q_t + hh * a.q_h
+                  : (kind == 1 ? a.k + t.n * a.k_t + hh * a.k_h : a.v + t.n * a.v_t + hh * a.v_h);
+  t.w = kind == 0 ? a.q_norm : (kind == 1 ? a.k_norm : nullptr);
+  return h;
+}
+__device__ __forceinline__ void find_place(const NormRopeArgs &a, const Grid &g, int h, int lane, Item &t) {
+  t.pos = a.pos[t.n];
+  const int slot = a.slot ? a.slot[t.n] : t.n;
+  t.live = t.in && t.pos >= 0;
+  if (t.live && ((a.rd > 0 && t.pos >= a.tab_rows) || slot < -1 || slot >= a.c.n_pages * a.c.page)) {
+    if (h == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
+    t.live = false;
   }
-  const float *w = kind == 0 ? a.q_norm : a.k_norm;
-  const bool plain = kind == 2, turns = !plain && a.rd > 0;
-  // y = r (x c + z s) with z the partner's value: c = weight x cos, s = partner's weight x (+-sin)
-  float c[V][8], s[V][8];
+  if (h < a.H) {
+    t.y = a.q_out + t.n * a.o_t + h * a.o_h;
+  } else {
+    if (slot < 0) t.live = false;
+    const int pg = t.live ? (int)g.page.div((uint32_t)slot) : 0, row = t.live ? slot - pg * a.c.page : 0;
+    const int hk = h - a.H;
+    t.y = t.plain ? reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row + (hk - a.c.kv_heads) * a.c.v_head
+                  : reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row + hk * a.c.k_head;
+  }
+}
+
+__device__ __forceinline__ void load8(const float *w, f2 (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(w + 2 * e));
+    v[e] = {x.x, x.y};
+    v[e + 1] = {x.z, x.w};
+  }
+}
+
+// G lanes a row, V (even) vectors of 8 features a lane, head_dim <= 8 G V a multiple of 16; the turned part and its halves
+// start and end on vector borders.  Adjacent pairs lie inside a vector; with HALF vectors u and u + 1 (u even) of a lane are
+// partners, rd / 2 features apart, or lie both outside the turned part.  A row a group and no loop: what hides the
+// latency is many resident warps (five or six CTAs an SM), each with its row in flight; keeping a token's
+// weights and angles in registers over several rows needed 80 to 128 of them and took 113 against 96 us.
+template <int G, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads, V == 2 ? (HALF ? 5 : 6) : 1) k_norm_rope(const __grid_constant__ NormRopeArgs a,
+                                                                                    const __grid_constant__ Grid g) {
+  const int lane = threadIdx.x & (G - 1);
+  const int hd = a.c.head_dim, h2 = a.rd >> 1;
+  Item t;
+  const int h = find_item(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
+  int f[V];  // first feature of this lane's vectors (hd: none)
+  uint4 x[V];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int f = 8 * (lane + G * u);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[u][e] = 1.f, s[u][e] = 0.f;
-    if (!live || plain || f >= hd) continue;
-    float wv[8];
-    load_w<FAST>(w, f, wv);
-    if (turns) {
-      const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)p * (a.rd >> 1);
-      load_angles<FAST>(a, tp, f, c[u], s[u]);
-      float wp[8];
-      if (HALF) load_partner_w<FAST>(a, w, f, wp);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[u][e] *= HALF ? wp[e] : wv[e ^ 1];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[u][e] *= wv[e];
-  }
-  // (every group of the warp goes through as many rounds: the shuffles below are the warp's)
-  int rounds = (max(nh, 0) + U - 1) / U;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, o));
-  for (int rnd = 0; rnd < rounds; ++rnd) {
-    const int t0 = rnd * U;
-    load(nxt, t0 + U);
-    uint4 xp[U][V];  // the partners' vectors, from the lines just read
     if (HALF) {
-#pragma unroll
-      for (int t = 0; t < U; ++t)
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
-          const int f = 8 * (lane + G * u);
-          xp[t][u] = make_uint4(0, 0, 0, 0);
-          if (live && turns && t0 + t < nh && f < hd) load_partners<FAST>(a, x + (int64_t)(t0 + t) * x_h, f, xp[t][u]);
-        }
+      const int j = lane + G * (u >> 1), turned = h2 >> 3;  // pair of vectors j
+      if (j < turned) {
+        f[u] = a.at + 8 * j + (u & 1) * h2;
+      } else {
+        const int v = 8 * (2 * (j - turned) + (u & 1));
+        f[u] = v < a.at ? v : v + a.rd;
+      }
+    } else {
+      f[u] = 8 * (lane + G * u);
     }
-    float r[U];
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (f[u] < hd) x[u] = *reinterpret_cast<const uint4 *>(t.x + f[u]);
+  }
+  find_place(a, g, h, lane, t);
+  f2 v[V][4], q[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-    for (int t = 0; t < U; ++t) {
-      r[t] = 0.f;
+  for (int u = 0; u < V; ++u) {
+    unpack(x[u], v[u]);
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        float v[8];
-        unpack(cur[t][u], v);
+    for (int e = 0; e < 4; ++e) q[e & 1] = fma2(v[u][e], v[u][e], q[e & 1]);
+  }
+  float r = (q[0].x + q[0].y) + (q[1].x + q[1].y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[t] = fmaf(v[e], v[e], r[t]);
+  for (int o = G / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  if (!t.live) return;
+  if (t.plain) {
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (f[u] < hd) *reinterpret_cast<uint4 *>(t.y + f[u]) = x[u];
+    return;
+  }
+  if (t.w) {
+    r = rsqrtf(r / (float)hd + a.eps);  // (within 2 units of the last place: 2^-22, far below the result's 2^-8)
+    const f2 rr = {r, r};
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      if (f[u] >= hd) continue;
+      f2 w[4];
+      load8(t.w + f[u], w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[u][e] = mul2(mul2(v[u][e], rr), w[e]);
+    }
+  }
+  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)t.pos * h2;
+#pragma unroll
+  for (int u = 0; u < V; u += HALF ? 2 : 1) {
+    if (f[u] < a.at || f[u] >= a.at + a.rd) continue;
+    if (HALF) {
+      const float4 *ap = reinterpret_cast<const float4 *>(tp + (f[u] - a.at));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 cs = __ldg(ap + e);
+        const f2 c = {cs.x, cs.z}, s = {cs.y, cs.w}, m = {-cs.y, -cs.w}, lo = v[u][e], hi = v[u + 1][e];
+        v[u][e] = fma2(hi, m, mul2(lo, c));
+        v[u + 1][e] = fma2(lo, s, mul2(hi, c));
+      }
+    } else {
+      const float4 *ap = reinterpret_cast<const float4 *>(tp + ((f[u] - a.at) >> 1));
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float4 cs = __ldg(ap + e / 2);
+        v[u][e] = fma2(f2{v[u][e].y, v[u][e].x}, f2{-cs.y, cs.y}, mul2(v[u][e], f2{cs.x, cs.x}));
+        v[u][e + 1] = fma2(f2{v[u][e + 1].y, v[u][e + 1].x}, f2{-cs.w, cs.w}, mul2(v[u][e + 1], f2{cs.z, cs.z}));
       }
     }
+  }
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1)
+  for (int u = 0; u < V; ++u)
+    if (f[u] < hd)
+      *reinterpret_cast<uint4 *>(t.y + f[u]) = make_uint4(pack2(v[u][0]), pack2(v[u][1]), pack2(v[u][2]), pack2(v[u][3]));
+}
+
+// Any even turned part and alignment of weights and angles: a feature at a time, partners read from the row again.
+template <int G, int V>
+__global__ void __launch_bounds__(kThreads) k_norm_rope_any(const __grid_constant__ NormRopeArgs a,
+                                                            const __grid_constant__ Grid g) {
+  const int lane = threadIdx.x & (G - 1);
+  const int hd = a.c.head_dim, h2 = a.rd >> 1;
+  Item t;
+  const int h = find_item(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
+  uint4 x[V];
+  float r = 0.f, z[V][8];  // z: partners, normed but for r
 #pragma unroll
-      for (int t = 0; t < U; ++t) r[t] += __shfl_xor_sync(0xffffffffu, r[t], o);
+  for (int u = 0; u < V; ++u) {
+    const int f0 = 8 * (lane + G * u);
+    x[u] = f0 < hd ? *reinterpret_cast<const uint4 *>(t.x + f0) : make_uint4(0, 0, 0, 0);
+    f2 v[4];
+    unpack(x[u], v);
 #pragma unroll
-    for (int t = 0; t < U; ++t) r[t] = !plain && w ? 1.0f / sqrtf(r[t] / (float)hd + a.eps) : 1.f;
-    __syncwarp();  // (q_out may be q: every lane has read its partners)
+    for (int e = 0; e < 4; ++e) r = fmaf(v[e].x, v[e].x, fmaf(v[e].y, v[e].y, r));
 #pragma unroll
-    for (int t = 0; t < U; ++t) {
-      if (!live || t0 + t >= nh) continue;
-      bf16 *yt = y + (int64_t)(t0 + t) * y_h;
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const int f = 8 * (lane + G * u);
-        if (f >= hd) continue;
-        if (plain) {
-          *reinterpret_cast<uint4 *>(yt + f) = cur[t][u];
-          continue;
-        }
-        float v[8], z[8], o[8];
-        unpack(cur[t][u], v);
-        if (HALF) unpack(xp[t][u], z);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // (outside the turned part there is no partner, which may be infinite)
-          if (!HALF) z[e] = turns && f + e >= a.at && f + e < a.at + a.rd ? v[e ^ 1] : 0.f;
-          o[e] = r[t] * fmaf(v[e], c[u][e], z[e] * s[u][e]);
-        }
-        *reinterpret_cast<uint4 *>(yt + f) = pack(o);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const int f = f0 + e, d = f - a.at;
+      z[u][e] = 0.f;
+      if (t.plain || f >= hd || d < 0 || d >= a.rd) continue;
+      const int fp = a.half ? (d < h2 ? f + h2 : f - h2) : (d & 1 ? f - 1 : f + 1);
+      z[u][e] = __bfloat162float(t.x[fp]) * (t.w ? __ldg(t.w + fp) : 1.f);
     }
+  }
+  find_place(a, g, h, lane, t);
 #pragma unroll
-    for (int t = 0; t < U; ++t)
+  for (int o = G / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  __syncwarp();  // (q_out may be q: every lane has read its partners)
+  if (!t.live) return;
+  r = t.w ? rsqrtf(r / (float)hd + a.eps) : 1.f;
+  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)t.pos * h2;
 #pragma unroll
-      for (int u = 0; u < V; ++u) cur[t][u] = nxt[t][u];
+  for (int u = 0; u < V; ++u) {
+    const int f0 = 8 * (lane + G * u);
+    if (f0 >= hd) continue;
+    uint4 out = x[u];
+    if (!t.plain) {
+      f2 v[4];
+      unpack(x[u], v);
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int f = f0 + e, d = f - a.at;
+        o[e] = (e & 1 ? v[e >> 1].y : v[e >> 1].x) * (t.w ? __ldg(t.w + f) : 1.f);
+        if (d >= 0 && d < a.rd) {
+          const bool first = a.half ? d < h2 : !(d & 1);
+          const float2 cs = __ldg(tp + (a.half ? (first ? d : d - h2) : d >> 1));
+          o[e] = first ? o[e] * cs.x - z[u][e] * cs.y : z[u][e] * cs.y + o[e] * cs.x;
+        }
+        o[e] *= r;
+      }
+      out = make_uint4(pack2({o[0], o[1]}), pack2({o[2], o[3]}), pack2({o[4], o[5]}), pack2({o[6], o[7]}));
+    }
+    *reinterpret_cast<uint4 *>(t.y + f0) = out;
   }
 }
 
-template <int G, int V, int U>
-cudaError_t launch(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
-  // Heads a group: as many (up to 16) as still leave a full complement of warps (24 an SM), at least U where there
-  // are rows enough, else one, which spreads few rows over more SMs.
-  const int most = std::max(a.H, a.c.kv_heads);
-  auto blocks_of = [](int h, int per) { return (h + per - 1) / per; };
-  auto per_token_of = [&](int per) { return blocks_of(a.H, per) + blocks_of(a.c.kv_heads, per) * (a.v ? 2 : 1); };
-  int per = 1;
-  while (per < 16 && per < most && (int64_t)a.N * per_token_of(2 * per) * G >= (int64_t)num_sms * 24 * 32) per *= 2;
-  const int q_blocks = blocks_of(a.H, per), k_blocks = blocks_of(a.c.kv_heads, per), per_token = per_token_of(per);
+using Kernel = void (*)(NormRopeArgs, Grid);
+
+cudaError_t launch(Kernel k, int G, const NormRopeArgs &a, cudaStream_t s) {
+  const int per_token = a.H + a.c.kv_heads * (a.v ? 2 : 1);
   const int64_t items = (int64_t)a.N * per_token;
-  const int64_t blocks = (items * G + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  // vectors of weights, angles and partners: 16-byte aligned, the turned part (and its halves) on vector borders
-  const bool fast = a.at % 8 == 0 && a.rd % (a.half ? 16 : 8) == 0 &&
-                    (((uintptr_t)a.tab | (uintptr_t)a.q_norm | (uintptr_t)a.k_norm) & 15) == 0;
-  auto *k = a.half ? (fast ? k_norm_rope<G, V, U, true, true> : k_norm_rope<G, V, U, true, false>)
-                   : (fast ? k_norm_rope<G, V, U, false, true> : k_norm_rope<G, V, U, false, false>);
-  k<<<(unsigned)blocks, kThreads, 0, s>>>(a, per, q_blocks, k_blocks, per_token, items);
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;  // (refused by the entry)
+  const Grid g{(int)items, paged::FastDiv((uint32_t)per_token), paged::FastDiv((uint32_t)a.c.page)};
+  k<<<(unsigned)((items * G + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, g);
   return cudaGetLastError();
+}
+template <int G, int V>
+cudaError_t launch_vectors(const NormRopeArgs &a, cudaStream_t s) {
+  return launch(a.half ? (Kernel)k_norm_rope<G, V, true> : (Kernel)k_norm_rope<G, V, false>, G, a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t s) {
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s) {
   const int hd = a.c.head_dim;
-  if (hd <= 32) return launch<4, 1, 2>(a, num_sms, s);
-  if (hd <= 64) return launch<8, 1, 2>(a, num_sms, s);
-  if (hd <= 128) return launch<16, 1, 2>(a, num_sms, s);
-  if (hd <= 256) return launch<32, 1, 2>(a, num_sms, s);
-  if (hd <= 512) return launch<32, 2, 1>(a, num_sms, s);
-  return launch<32, 4, 1>(a, num_sms, s);
+  // whole vectors: weights and angles 16-byte aligned, the turned part (and its halves) on vector borders
+  const bool vectors = hd % 16 == 0 && a.at % 8 == 0 && a.rd % (a.half ? 16 : 8) == 0 &&
+                       (((uintptr_t)a.tab | (uintptr_t)a.q_norm | (uintptr_t)a.k_norm) & 15) == 0;
+  if (!vectors) {
+    if (hd <= 64) return launch(k_norm_rope_any<8, 1>, 8, a, s);
+    if (hd <= 128) return launch(k_norm_rope_any<16, 1>, 16, a, s);
+    if (hd <= 256) return launch(k_norm_rope_any<32, 1>, 32, a, s);
+    return launch(hd <= 512 ? (Kernel)k_norm_rope_any<32, 2> : (Kernel)k_norm_rope_any<32, 4>, 32, a, s);
+  }
+  if (hd <= 32) return launch_vectors<2, 2>(a, s);
+  if (hd <= 64) return launch_vectors<4, 2>(a, s);
+  if (hd <= 128) return launch_vectors<8, 2>(a, s);
+  if (hd <= 256) return launch_vectors<16, 2>(a, s);
+  if (hd <= 512) return launch_vectors<32, 2>(a, s);
+  return launch_vectors<32, 4>(a, s);
 }
 
 }  // namespace csa
