@@ -1395,6 +1395,19 @@ bool tma_map_2d_bf16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t 
   return gemm::map_2d(m, base, inner, outer, ld, box_inner, box_outer);
 }
 
+bool tma_map_pages_bf16(CUtensorMap *m, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t box_inner,
+                        uint32_t box_rows) {
+  gemm::EncodeTiledFn enc = gemm::encoder();
+  if (!enc) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t box[4] = {box_inner, 1, box_rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), d, st, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // L2 policies: a weight read by one token tile only (few tokens) streams past evict-first; one
 // re-read by several token tiles stays normal.  Activations that all weight tiles re-read stay
 // evict-last while they are small next to L2, normal otherwise.

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   __shared__ Rows rows;
   __shared__ Range rg;
-  const int nunits = find_range<kUnit, kThreads>(P, s_scan, rows, rg);
+  const int nunits = find_range<kUnit, kThreads, false>(P, s_scan, rows, rg);
   if (nunits == 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
@@ -112,14 +112,14 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
     if (todo > 0) {
       const int j = cl.t * kUnit + warp * kTile + (lane & (kTile - 1));
       f.kvh = cl.hg / P.sub;
-      const Row row = rows.get<kUnit>(a, cl.n);
+      const Row row = rows.get<kUnit, false>(a, cl.n);
       if (j < row.rows) {
         f.pos = row.first + j;
         f.page = a.table[(int64_t)row.req * a.width + P.page.div((uint32_t)f.pos)];
       }
       --todo;
       const int hg0 = cl.hg, n0 = cl.n;
-      advance<kUnit>(a, P.Hg, rows, cl);
+      advance<kUnit, false>(a, P.Hg, rows, cl);
       if (warp == 0 && todo > 0 && (cl.hg != hg0 || cl.n != n0)) {  // the next segment's q on its way to L1
         const int kv2 = cl.hg / P.sub, sg = cl.hg - kv2 * P.sub, nq = min(NH, P.g - sg * NH);
         const bf16 *q = a.q + (int64_t)cl.n * a.q_t + (int64_t)(kv2 * P.g + sg * NH) * hd;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       __syncthreads();  // the stage may be refilled
       if (!whole) publish<kHeads, HD, kThreads>(P, rg.begin + sb, rg.begin + se, rg, cc.n, h0, nh, &s_flag);
       if (u + 1 < nunits) {
-        advance<kUnit>(a, P.Hg, rows, cc);
+        advance<kUnit, false>(a, P.Hg, rows, cc);
         seg = u + 1;
         begin_segment();
       }

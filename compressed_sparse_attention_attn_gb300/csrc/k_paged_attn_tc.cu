@@ -27,6 +27,11 @@
 #include "paged_common.cuh"
 
 namespace csa {
+
+// 4-D bf16 tensor map with 128-byte swizzle, boxes {box_inner, 1, box_rows, 1} (defined with the GEMM's TMA helpers).
+bool tma_map_pages_bf16(CUtensorMap *m, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t box_inner,
+                        uint32_t box_rows);
+
 namespace paged {
 namespace latent {
 
@@ -35,7 +40,11 @@ constexpr int kHeads = 64;              // query heads of a head group
 constexpr int kUnit = 64;               // positions of a tile
 constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile (and of q)
 constexpr int kBlocks = kHD / 64;
-constexpr int kThreads = 512;           // warps 0, 1 softmax; 2 products; 4-7 O; 8-11 and 12-15 copies (a buffer each)
+// warps 0-3 softmax; 4-7 O; 8 products; from 9 on copies: by TMA (four, a quarter of the features each) or by cp.async (four
+// for each tile buffer)
+constexpr int kFirstCopy = 9;
+template <bool TMA>
+constexpr int kThreads = (kFirstCopy + (TMA ? 4 : 8)) * 32;
 
 struct L {
   static constexpr size_t q = 0;                                             // [8][64][128 B]
@@ -43,10 +52,10 @@ struct L {
   static constexpr size_t p = t + (size_t)2 * kBlocks * kBlock;              // [2][64][128 B]
   static constexpr size_t alpha = p + (size_t)2 * kHeads * 128;              // float [2][64]
   static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
-  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [17]
+  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [18]
   static constexpr size_t bars = scan + 20 * 8;                              // u64 [26]
-  static constexpr size_t misc = bars + 26 * 8;                              // masks [2][4], flags, slot, abort
-  static constexpr size_t total = misc + 64;
+  static constexpr size_t misc = bars + 26 * 8;                              // masks [2][4], flags [2][4], slot, abort
+  static constexpr size_t total = misc + 96;
 };
 static_assert(L::total + 1024 + sizeof(Rows) + sizeof(Range) + 64 <= 232448, "one CTA's shared memory");
 
@@ -55,7 +64,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   const bool ok = tc::mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
-__global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_constant__ Params P) {
+// What a CTA's copies need beyond the parameters (TMA): the map of the pages [page][row][kv head][feature], boxes of
+// box_rows rows x 64 features inside a page, a power of two that divides `page`.
+struct Pages {
+  CUtensorMap map;
+  int box_rows;
+};
+
+template <bool TMA>
+__global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __grid_constant__ Params P,
+                                                                        const __grid_constant__ Pages PG) {
+  constexpr bool ALIGN = TMA;  // (tiles then hold whole boxes)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
   uint8_t *smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
@@ -66,8 +85,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
   uint64_t *full = bars, *empty = bars + 8, *s_full = bars + 16, *p_full = bars + 18, *stat = bars + 20, *fin = bars + 22,
            *q_full = bars + 24, *drain = bars + 25;
   uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::misc);  // [2][4]: positions of a tile that are there (16 each)
-  int *flags = reinterpret_cast<int *>(masks + 8);                 // [2][2]: a maximum was raised (by warp)
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(flags + 4);
+  int *flags = reinterpret_cast<int *>(masks + 8);                 // [2][4]: a maximum was raised (by warp)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(flags + 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
@@ -75,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
 
   __shared__ Rows rows;
   __shared__ Range rg;
-  const int nt = find_range<kUnit, kThreads>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
+  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
   if (nt == 0) {
     if (tid == 0 && !P.by_segment) P.split[blockIdx.x] = make_int2(0, 0);
     return;
@@ -83,32 +102,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
   Cursor c = first_unit(rg, rows);
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&full[i], 128);  // the lanes of the buffer's four warps
+      tc::mbar_init(&full[i], TMA ? 1 : 128);  // (the lanes of the buffer's four warps)
       tc::mbar_init(&empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&s_full[b], 1);
-      tc::mbar_init(&p_full[b], 64 + 128);
-      tc::mbar_init(&stat[b], 64);
+      tc::mbar_init(&p_full[b], 128 + 128);
+      tc::mbar_init(&stat[b], 128);
     }
-    tc::mbar_init(&fin[0], 64);
-    tc::mbar_init(&fin[1], 64);
-    tc::mbar_init(q_full, 64);
+    tc::mbar_init(&fin[0], 128);
+    tc::mbar_init(&fin[1], 128);
+    tc::mbar_init(q_full, 128);
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 2) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kUnit;  // S: 2 x 64 columns, O^T: 4 x 64
   auto par = [](int i) { return (uint32_t)((i >> 1) & 1); };  // phase of tile i's barriers
+  // The positions of tile buffer b that are there, as two words (behind the barrier that publishes them).
+  auto mask_of = [&](int b, uint32_t &lo, uint32_t &hi) {
+    if (TMA) {
+      lo = masks[4 * b];
+      hi = masks[4 * b + 1];
+    } else {
+      lo = masks[4 * b] | masks[4 * b + 1] << 16;
+      hi = masks[4 * b + 2] | masks[4 * b + 3] << 16;
+    }
+  };
   auto last_of = [&](int i) { return c.t == c.units - 1 || i + 1 == nt; };  // of a segment, in this CTA
 
-  if (warp < 2) {
+  if (warp < 4) {
     // ------------------------------------------------------------------------------ softmax
-    const int h = tid;  // head of the group
+    // The scores' 64 rows lie in the first 16 lanes of each quarter of tensor memory; a thread holds 16 positions of two
+    // heads, hA and hB = hA + 8, a head's 64 positions the four lanes of a quad.
+    const int hA = 16 * warp + (lane >> 2), qc = 2 * (lane & 3);
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     auto load_q = [&](const Cursor &k) {
       const int kvh = k.hg / P.sub, sg = k.hg - kvh * P.sub;
@@ -118,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
 #pragma unroll 1
       for (int kb = 0; kb < nkb; ++kb)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = warp * 32 + 4 * i + (lane >> 3), d = kb * 64 + cc * 8;
+        for (int i = 0; i < 4; ++i) {
+          const int r = warp * 16 + 4 * i + (lane >> 3), d = kb * 64 + cc * 8;
           const bool in = r < nh && d < hd;
           attn::cp_async16(s_q + kb * kBlock + r * 128 + ((cc ^ (r & 7)) << 4), in ? q + (int64_t)r * hd + d : a.q, in);
         }
@@ -128,79 +159,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     attn::cp_async_wait_all();
     attn::fence_proxy_async();
     tc::mbar_arrive(q_full);
-    float m = -INFINITY, l = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: of this thread's positions
     int nseg = 0;
     bool first = true;
     int seg = 0;  // the segment's first tile here
     for (int i = 0; i < nt; ++i) {
       const int b = (int)(i & 1);
-      if (!warp_wait(&full[4 * b + 3], par(i), abort_flag)) break;  // (its mask)
-      const uint32_t ok0 = masks[4 * b] | masks[4 * b + 1] << 16, ok1 = masks[4 * b + 2] | masks[4 * b + 3] << 16;
+      if (!warp_wait(&full[4 * b + (TMA ? 0 : 3)], par(i), abort_flag)) break;  // (its mask)
+      uint32_t ok0, ok1;
+      mask_of(b, ok0, ok1);
       if (!warp_wait(&s_full[b], par(i), abort_flag)) break;
       tc::tc_fence_after();
       const bool last = last_of(i);
       Cursor nx = c;
       if (last && i + 1 < nt) {  // q's last reader is done: the next segment's q on its way
         nx.t = nx.units - 1;
-        advance<kUnit>(a, P.Hg, rows, nx);
+        advance<kUnit, ALIGN>(a, P.Hg, rows, nx);
         load_q(nx);
       }
-      float s[64];
+      float s[32];  // s[4 j + 2 x + e]: position 8 j + qc + e of head x
       {
-        float v[32];
-        attn::tmem_ld_32cols(tmem + (uint32_t)(b * kUnit) + lane_off, v);
+        uint32_t r[32];
+        tc::tmem_ld_16x64_wait(tmem + (uint32_t)(b * kUnit) + lane_off, r);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = v[k];
-        attn::tmem_ld_32cols(tmem + (uint32_t)(b * kUnit + 32) + lane_off, v);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) s[32 + k] = v[k];
+        for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(r[k]);
       }
       float sc = P.scale_log2;
       if ((ok0 & ok1) != 0xffffffffu) {  // positions that are not there: -inf (scaled here, so that a scale of 0 is right)
+        ok0 >>= qc;
+        ok1 >>= qc;
 #pragma unroll
-        for (int k = 0; k < 64; ++k) s[k] = ((k < 32 ? ok0 : ok1) >> (k & 31)) & 1u ? s[k] * sc : -INFINITY;
+        for (int k = 0; k < 32; ++k)
+          s[k] = ((k < 16 ? ok0 : ok1) >> (8 * ((k >> 2) & 3) + (k & 1))) & 1u ? s[k] * sc : -INFINITY;
         sc = 1.f;
       }
-      float mx = s[0];  // the largest scaled score, of a scale of either sign
-      if (sc < 0.f) {
-#pragma unroll
-        for (int k = 1; k < 64; ++k) mx = fminf(mx, s[k]);
-      } else {
-#pragma unroll
-        for (int k = 1; k < 64; ++k) mx = fmaxf(mx, s[k]);
-      }
-      mx *= sc;
-      float al = 1.f;
+      float al[2];
       bool raised = false;
-      if (first) {
-        m = mx;
-      } else if (mx > m + 8.f || (m == -INFINITY && mx > m)) {
-        al = m == -INFINITY ? 0.f : exp2f(m - mx);
-        m = mx;
-        raised = true;
-      }
-      alpha_sm[b * kHeads + h] = al;
-      const bool any = __any_sync(0xffffffffu, raised);
-      if (lane == 0) flags[2 * b + warp] = any ? 1 : 0;
-      tc::mbar_arrive(&stat[b]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
-      const uint32_t prow = s_p + b * kHeads * 128 + h * 128;
 #pragma unroll
-      for (int k = 0; k < 64; k += 8) {
-        uint32_t w[4];
+      for (int x = 0; x < 2; ++x) {
+        float mx = s[2 * x];  // the largest scaled score, of a scale of either sign
+        if (sc < 0.f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = ex2(fmaf(s[k + 2 * e], sc, -ref)), y = ex2(fmaf(s[k + 2 * e + 1], sc, -ref));
-          sum += x + y;
-          const __nv_bfloat162 pk = __floats2bfloat162_rn(x, y);
-          w[e] = *reinterpret_cast<const uint32_t *>(&pk);
+          for (int k = 0; k < 16; ++k) mx = fminf(mx, s[4 * (k >> 1) + 2 * x + (k & 1)]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) mx = fmaxf(mx, s[4 * (k >> 1) + 2 * x + (k & 1)]);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(prow + (((k >> 3) ^ (h & 7)) << 4)), "r"(w[0]), "r"(w[1]),
-                     "r"(w[2]), "r"(w[3])
-                     : "memory");
+        mx *= sc;
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        al[x] = 1.f;
+        if (first) {
+          m[x] = mx;
+        } else if (mx > m[x] + 8.f || (m[x] == -INFINITY && mx > m[x])) {
+          al[x] = m[x] == -INFINITY ? 0.f : exp2f(m[x] - mx);
+          m[x] = mx;
+          raised = true;
+        }
+        if (qc == 0) alpha_sm[b * kHeads + hA + 8 * x] = al[x];
       }
-      l = l * al + sum;
+      const bool any = __any_sync(0xffffffffu, raised);
+      if (lane == 0) flags[4 * b + warp] = any ? 1 : 0;
+      __syncwarp();
+      tc::mbar_arrive(&stat[b]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float ref = m[x] == -INFINITY ? 0.f : m[x];
+        const int h = hA + 8 * x;
+        const uint32_t prow = s_p + b * kHeads * 128 + h * 128 + 2 * qc;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float p0 = ex2(fmaf(s[4 * j + 2 * x], sc, -ref)), p1 = ex2(fmaf(s[4 * j + 2 * x + 1], sc, -ref));
+          sum += p0 + p1;
+          const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + ((j ^ (h & 7)) << 4)), "r"(*reinterpret_cast<const uint32_t *>(&pk))
+                       : "memory");
+        }
+        l[x] = l[x] * al[x] + sum;
+      }
       attn::fence_proxy_async();
       tc::tc_fence_before();
       tc::mbar_arrive(&p_full[b]);
@@ -210,23 +247,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
         const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
         const int sb = i - c.t, se = sb + c.units;  // the whole segment, from this CTA's first tile
         const bool whole = sb >= 0 && se <= nt;
-        float fo = 1.f;
-        if (h < nh) {
-          if (whole) {
-            fo = out_factor(m, l, a.sink, h0 + h);
-            if (a.lse) a.lse[(int64_t)c.n * a.H + h0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-          } else {
-            const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
-            *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + h) * 2) = make_float2(m, l);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+          const int h = hA + 8 * x;
+          float fo = 1.f;
+          if (qc == 0 && h < nh) {
+            if (whole) {
+              fo = out_factor(m[x], l[x], a.sink, h0 + h);
+              if (a.lse)
+                a.lse[(int64_t)c.n * a.H + h0 + h] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * 0.6931471805599453f;
+            } else {
+              const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
+              *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + h) * 2) = make_float2(m[x], l[x]);
+            }
           }
+          if (qc == 0) f_sm[(nseg & 1) * kHeads + h] = fo;
+          m[x] = -INFINITY;
+          l[x] = 0.f;
         }
-        f_sm[(nseg & 1) * kHeads + h] = fo;
+        __syncwarp();
         tc::mbar_arrive(&fin[nseg & 1]);
         ++nseg;
         seg = i + 1;
         first = true;
-        m = -INFINITY;
-        l = 0.f;
         if (i + 1 < nt) {
           attn::cp_async_wait_all();
           attn::fence_proxy_async();
@@ -248,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     for (int i = 0; i < nt; ++i) {
       const int b = (int)(i & 1);
       if (!warp_wait(&stat[b], par(i), abort_flag)) break;
-      if (!first && (flags[2 * b] | flags[2 * b + 1])) {
+      if (!first && (flags[4 * b] | flags[4 * b + 1] | flags[4 * b + 2] | flags[4 * b + 3])) {
         if (!warp_wait(&empty[4 * (b ^ 1) + 3], par(i - 1), abort_flag)) break;
         tc::tc_fence_after();
 #pragma unroll 1
@@ -265,6 +310,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
         }
         attn::tmem_st_wait();
         tc::tc_fence_before();
+      }
+      if (TMA) {
+        // positions that are not there hold what the page holds (or an older tile): their weights are 0, but 0 x NaN is not,
+        // so their rows are zeroed before the values' products read them
+        uint32_t ok0, ok1;
+        bool landed = warp_wait(&full[4 * b], par(i), abort_flag);
+        mask_of(b, ok0, ok1);
+        if (landed && (ok0 & ok1) != 0xffffffffu) {
+          for (int w = 1; w < 4 && landed; ++w) landed = warp_wait(&full[4 * b + w], par(i), abort_flag);
+          if (landed) {
+            for (int r = jt >> 6; r < kUnit; r += 2)
+              if (!(((r < 32 ? ok0 : ok1) >> (r & 31)) & 1u))
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 s_t + (b * kBlocks + ((jt >> 3) & 7)) * kBlock + r * 128 + (jt & 7) * 16),
+                             "r"(0)
+                             : "memory");
+            attn::fence_proxy_async();
+          }
+        }
+        if (!landed) break;
       }
       const bool last = last_of(i);
       tc::mbar_arrive(&p_full[b]);
@@ -321,14 +386,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       ++nseg;
       seg = i + 1;
       c.t = c.units - 1;
-      if (i + 1 < nt) advance<kUnit>(a, P.Hg, rows, c);
+      if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
     }
     if (!P.by_segment && jt == 0 && !told) P.split[blockIdx.x] = make_int2(0, 0);
-  } else if (warp == 2) {
+  } else if (warp == 8) {
     // ------------------------------------------------------------------------------ products
     // The whole warp goes through the loop, one elected lane issues: the operands' descriptors then stay in uniform
     // registers (issued from a one-lane branch each product cost about 115 cycles, of which it computes 48).
-    const uint32_t id1 = tc::idesc_bf16_f32(128, kUnit);
+    const uint32_t id1 = tc::idesc_bf16_f32(kHeads, kUnit);
     const uint32_t id2 = tc::idesc_bf16_f32(128, kHeads, /*a_mn_major=*/true, /*b_mn_major=*/false);
     const uint64_t dq = tc::sdesc_sw128(s_q, 16, 1024), dk = tc::sdesc_sw128(s_t, 16, 1024),
                    dv = tc::sdesc_sw128(s_t, kBlock, 1024), dp = tc::sdesc_sw128(s_p, 16, 1024);
@@ -348,12 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       }
       __syncwarp();
     };
-    auto scores_all = [&](int b) {
+    auto scores_from = [&](int b, int w) {  // quarters w, w + 1, ...: without a pause between them
       tc::tc_fence_after();
       if (tc::elect_one()) {
 #pragma unroll
         for (int kb = 0; kb < kBlocks; ++kb)
-          if (kb < nkb) block(b, kb);
+          if (kb >= 2 * w && kb < nkb) block(b, kb);
         tc::mma_commit(&s_full[b]);
       }
       __syncwarp();
@@ -377,6 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     auto ready = [](uint64_t *bar, uint32_t parity) {
       const bool r = tc::mbar_test_wait(bar, parity);
       return __all_sync(0xffffffffu, r);
+    };
+    auto landed = [&](int b, int w, int i) {  // all of quarters w .. 3
+      bool r = true;
+      for (int k = 3; k >= w && r; --k) r = ready(&full[4 * b + k], par(i));
+      return r;
     };
     bool ok = warp_wait(q_full, 0, abort_flag), first = true;
     int nq = 1;  // segments whose q has been waited for
@@ -402,9 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
             ++nq;
           }
           spins = 0;
-        } else if (w == 0 && (pv || !last) && ready(&full[4 * nb + 3], par(i + 1))) {
-          scores_all(nb);
+        } else if (w < 3 && (pv || !last) && landed(nb, w, i + 1)) {
+          scores_from(nb, w);
           w = 4;
+          spins = 0;
         } else if (w < 4 && (pv || !last) && ready(&full[4 * nb + w], par(i + 1))) {
           scores(nb, w);
           ++w;
@@ -422,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       first = last;
       if (last) {
         c.t = c.units - 1;
-        if (i + 1 < nt) advance<kUnit>(a, P.Hg, rows, c);
+        if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
       } else {
         ++c.t;
       }
@@ -434,14 +505,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
     while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
     }
     __syncwarp();
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------------------------ copies: 16 positions a warp
-    const int b = (warp - 8) >> 2, part = warp & 3;
+  } else if (TMA) {
+    // ------------------------------------------------------------------------------ copies by TMA: a quarter of the features a warp
+    const int w = warp - kFirstCopy, R = PG.box_rows, nbox = kUnit / R;
+    const int nb_kb = max(0, min(2, nkb - 2 * w));  // its 64-feature blocks
+    if (lane == 0) tc::prefetch_tmap(&PG.map);
+    int issued = 0;
+    for (int i = 0; i < nt; ++i) {
+      const int b = i & 1;
+      const Row row = rows.get<kUnit, ALIGN>(a, c.n);
+      const int lo = max(row.lead - c.t * kUnit, 0), hi = min(row.rows - c.t * kUnit, kUnit);  // its positions lo .. hi - 1
+      const int kvh = c.hg / P.sub;
+      // lane k: box k of the tile (rows k R .. k R + R - 1 lie in one page)
+      const bool wanted = lane < nbox && lane * R < hi && (lane + 1) * R > lo;
+      const uint32_t pos = (uint32_t)(row.first + c.t * kUnit + lane * R), pg = P.page.div(pos);
+      const int id = wanted ? a.table[(int64_t)row.req * a.width + pg] : 0;
+      const bool good = wanted && id >= 0 && id < a.c.n_pages;
+      if (wanted && !good) atomicOr(a.status, kStatusBadIndex);
+      const uint32_t boxes = __ballot_sync(0xffffffffu, good);
+      if (i >= 2 && !warp_wait(&empty[4 * b + w], par(i) ^ 1u, abort_flag)) break;
+      if (w == 0) {
+        const uint32_t m0 = __ballot_sync(0xffffffffu, lane >= lo && lane < hi && ((boxes >> (lane / R)) & 1u));
+        const uint32_t m1 = __ballot_sync(0xffffffffu, lane + 32 >= lo && lane + 32 < hi && ((boxes >> ((lane + 32) / R)) & 1u));
+        if (lane == 0) {  // (the mask of the tile before has been read: its values' products are under way)
+          masks[4 * b] = m0;
+          masks[4 * b + 1] = m1;
+        }
+      }
+      if (lane == 0) tc::mbar_expect_tx(&full[4 * b + w], (uint32_t)(__popc(boxes) * nb_kb * R * 128));
+      __syncwarp();
+      if (good)
+        for (int kb = 0; kb < nb_kb; ++kb)
+          tc::tma_load_4d(s_t + (b * kBlocks + 2 * w + kb) * kBlock + lane * R * 128, &PG.map, &full[4 * b + w], (2 * w + kb) * 64,
+                          kvh, (int)(pos - pg * P.page.d), id);
+      issued = i + 1;
+      if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+    }
+    // nothing is in flight when the CTA ends, even after a wait that ran out
+    for (int i = max(issued - 2, 0); i < issued; ++i) {
+      const uint64_t t0 = tc::global_ns();
+      while (!tc::mbar_try_wait(&full[4 * (i & 1) + w], par(i)) && tc::global_ns() - t0 < tc::kWaitLimitNs) {
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------------------ copies by cp.async: 16 positions a warp
+    const int b = (warp - kFirstCopy) >> 2, part = (warp - kFirstCopy) & 3;
     const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
     const int cc = lane & 7;
-    if (b == 1 && nt > 1) advance<kUnit>(a, P.Hg, rows, c);
+    if (b == 1 && nt > 1) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
     for (int i = b; i < nt; i += 2) {
-      const Row row = rows.get<kUnit>(a, c.n);
+      const Row row = rows.get<kUnit, ALIGN>(a, c.n);
       const int j = c.t * kUnit + part * 16 + (lane & 15);
       const bool there = j < row.rows;
       const uint32_t pos = (uint32_t)(row.first + j), pg = P.page.div(pos);
@@ -488,14 +601,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attn_latent(const __grid_
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       attn::fence_proxy_async();
       tc::mbar_arrive(&full[4 * b + 3]);
-      if (i + 1 < nt) advance<kUnit>(a, P.Hg, rows, c);
-      if (i + 2 < nt) advance<kUnit>(a, P.Hg, rows, c);
+      if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+      if (i + 2 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
     }
     attn::cp_async_wait_all();
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 2) {
+  if (warp == 8) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -514,7 +627,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (a programmatic dependent of the kernel above)
   const int2 sp = P.split[blockIdx.x];
   const int n_hg = P.by_segment ? (int)blockIdx.x : sp.x, n = n_hg / P.Hg, hg = n_hg - n * P.Hg, parts = sp.y;
-  if (P.by_segment && row_of<kUnit>(a, n, false).units == 0) return;  // (a row that was left alone: nothing told)
+  if (P.by_segment && row_of<kUnit, false>(a, n, false).units == 0) return;  // (a row that was left alone: nothing told)
   const int c0 = P.by_segment ? sp.x : (int)blockIdx.x;
   // (after a wait that ran out the notes may be those of another call: nothing outside the workspace is read)
   if (parts <= 1 || c0 < 0 || parts > P.ctas - c0 || n < 0 || n >= a.N) return;
@@ -577,16 +690,31 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid
 
 cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   using namespace latent;
-  static SmemAttr attr;
-  const size_t smem = L::total + 1024;
-  cudaError_t e = attr.ensure((const void *)k_paged_attn_latent, (int)smem);
-  if (e != cudaSuccess) return e;
   const PagedAttnArgs &a = p.a;
+  // TMA where pages hold whole boxes of at least 8 rows (the swizzle's period), up to a tile; cp.async for other pages
+  Pages pg;
+  memset(&pg, 0, sizeof(pg));
+  pg.box_rows = a.c.page & -a.c.page;
+  if (pg.box_rows > kUnit) pg.box_rows = kUnit;
+  bool tma = pg.box_rows >= 8;
+  if (tma) {
+    const uint64_t dims[4] = {(uint64_t)a.c.head_dim, (uint64_t)a.c.kv_heads, (uint64_t)a.c.page, (uint64_t)a.c.n_pages};
+    // (strides of dimensions of size 1 may be anything: a row's)
+    const uint64_t row = 2 * (uint64_t)a.c.head_dim;
+    const uint64_t strides[3] = {a.c.kv_heads > 1 ? 2 * (uint64_t)a.c.k_head : row, 2 * (uint64_t)a.c.k_row,
+                                 a.c.n_pages > 1 ? 2 * (uint64_t)a.c.k_page : row};
+    tma = tma_map_pages_bf16(&pg.map, a.c.k, dims, strides, 64, (uint32_t)pg.box_rows);
+  }
+  static SmemAttr attr_tma, attr_copy;
+  const size_t smem = L::total + 1024;
+  cudaError_t e = tma ? attr_tma.ensure((const void *)k_paged_attn_latent<true>, (int)smem)
+                      : attr_copy.ensure((const void *)k_paged_attn_latent<false>, (int)smem);
+  if (e != cudaSuccess) return e;
   p.g = a.H / a.c.kv_heads;
   p.sub = (p.g + kHeads - 1) / kHeads;
   p.Hg = p.sub * a.c.kv_heads;
   const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
-  const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + kUnit - 1) / kUnit);
+  const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + kUnit - 1) / kUnit + (a.window > 0 ? 1 : 0));
   const int64_t grid = std::min<int64_t>(std::min<int64_t>(units, num_sms), kMaxCtas);
   const int64_t segments = (int64_t)a.N * p.Hg;
   p.share_o = ws;
@@ -595,7 +723,10 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
   p.by_segment = segments <= grid;
   p.ctas = (int)grid;
   if (sizeof(float) * 2 * grid * kHeads * (kHD + 2) + sizeof(int2) * grid > ws_bytes) return cudaErrorInvalidValue;
-  k_paged_attn_latent<<<(unsigned)grid, kThreads, smem, s>>>(p);
+  if (tma)
+    k_paged_attn_latent<true><<<(unsigned)grid, kThreads<true>, smem, s>>>(p, pg);
+  else
+    k_paged_attn_latent<false><<<(unsigned)grid, kThreads<false>, smem, s>>>(p, pg);
   if ((e = cudaGetLastError()) != cudaSuccess || segments == units) return e;  // (one tile a segment: nothing is shared)
   // about 600 blocks of the join, and no more than there is work
   const int64_t x = std::min(segments, grid), y = std::min<int64_t>(std::max<int64_t>(1, 4 * num_sms / x), kHeads);

@@ -52,16 +52,17 @@ struct Params {
   int by_segment;       // `split` is by segment (no more of them than CTAs), else by first CTA
 };
 
-// The positions first .. first + rows - 1 of row n; units of U rows (0: a row that is left alone).
+// The positions first + lead .. first + rows - 1 of row n; units of U rows from `first` on (0: a row that is left alone).
+// ALIGN: `first` is a multiple of U (with a window it may lie before the first position that counts), else lead is 0.
 struct Row {
-  int req, first, rows, units;
+  int req, first, lead, rows, units;
 };
-template <int U>
+template <int U, bool ALIGN>
 __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report) {
   Row r;
   r.req = a.req ? a.req[n] : n;
   const int pos = a.pos[n];
-  r.first = r.rows = r.units = 0;
+  r.first = r.lead = r.rows = r.units = 0;
   if (r.req < 0 || pos < -1) return r;
   if (r.req >= a.R) {
     if (report) atomicOr(a.status, kStatusBadIndex);
@@ -77,6 +78,11 @@ __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report
   }
   if (a.window > 0) r.first = max(0, pos - a.window + 1);
   r.rows = max(0, end - r.first);
+  if (ALIGN && r.rows > 0) {
+    r.lead = r.first % U;
+    r.first -= r.lead;
+    r.rows += r.lead;
+  }
   r.units = max(1, (r.rows + U - 1) / U);
   return r;
 }
@@ -95,9 +101,9 @@ constexpr int kRowsKept = 32;
 struct Rows {
   int n0;
   Row row[kRowsKept];
-  template <int U>
+  template <int U, bool ALIGN>
   __device__ __forceinline__ Row get(const PagedAttnArgs &a, int n) const {
-    return (unsigned)(n - n0) < (unsigned)kRowsKept ? row[n - n0] : row_of<U>(a, n, false);
+    return (unsigned)(n - n0) < (unsigned)kRowsKept ? row[n - n0] : row_of<U, ALIGN>(a, n, false);
   }
 };
 
@@ -105,7 +111,7 @@ struct Rows {
 struct Cursor {
   int n, hg, t, units;
 };
-template <int U>
+template <int U, bool ALIGN>
 __device__ __forceinline__ void advance(const PagedAttnArgs &a, int Hg, const Rows &rows, Cursor &c) {
   if (++c.t < c.units) return;
   c.t = 0;
@@ -113,13 +119,13 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, int Hg, const Ro
   c.hg = 0;
   do {
     if (++c.n >= a.N) return;  // (past the last unit: not used any more)
-    c.units = rows.get<U>(a, c.n).units;
+    c.units = rows.get<U, ALIGN>(a, c.n).units;
   } while (c.units == 0);
 }
 
 // Called by all NT threads of the CTA.  scratch: int64 [NT / 32 + 1], rows, out: all in shared memory.  Returns how many
 // units the CTA has.
-template <int U, int NT>
+template <int U, int NT, bool ALIGN>
 __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Rows &rows, Range &out) {
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -145,7 +151,7 @@ __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Row
     return x + b;
   };
   int64_t mine = 0;
-  for (int n = tid; n < a.N; n += NT) mine += row_of<U>(a, n, report).units;
+  for (int n = tid; n < a.N; n += NT) mine += row_of<U, ALIGN>(a, n, report).units;
   int64_t sum;
   int64_t incl = scan(mine, sum);
   if (sum * P.Hg > 0x7fffffff) {
@@ -167,7 +173,7 @@ __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Row
   int64_t base = 0;
   for (int n0 = 0; n0 < a.N; n0 += NT) {  // one round for up to NT rows
     if (a.N > NT) {
-      mine = n0 + tid < a.N ? row_of<U>(a, n0 + tid, false).units : 0;
+      mine = n0 + tid < a.N ? row_of<U, ALIGN>(a, n0 + tid, false).units : 0;
       incl = scan(mine, sum);
     }
     const int64_t lo = (base + incl - mine) * P.Hg, hi = (base + incl) * P.Hg;
@@ -181,9 +187,9 @@ __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Row
   __syncthreads();
   if (tid < kRowsKept) {
     const int n = out.row + tid;
-    const Row none{0, 0, 0, 0};
+    const Row none{0, 0, 0, 0, 0};
     if (tid == 0) rows.n0 = n;
-    rows.row[tid] = n < a.N ? row_of<U>(a, n, false) : none;
+    rows.row[tid] = n < a.N ? row_of<U, ALIGN>(a, n, false) : none;
   }
   __syncthreads();
   return (int)(end - begin);
