@@ -37,27 +37,34 @@ namespace latent {
 
 constexpr int kHD = 512;
 constexpr int kHeads = 64;              // query heads of a head group
-constexpr int kUnit = 64;               // positions of a tile
-constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile (and of q)
+constexpr int kUnit = 48;               // positions of a tile
+constexpr int kJ = kUnit / 8;
+constexpr int kBufs = 3;                // tile buffers
+constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile
+constexpr int kQBlock = kHeads * 128;   // and of q
+constexpr int kS = 64;                  // columns of a score accumulator (kUnit used)
+constexpr uint32_t kHalf = 0xffffffu;   // the positions of half a tile
 constexpr int kBlocks = kHD / 64;
-// warps 0-3 softmax; 4-7 O; 8 products; from 9 on copies: by TMA (four, a quarter of the features each) or by cp.async (four
+// warps 0-3 softmax; 4-7 O; 8 products; from 9 on copies: by TMA (four, a quarter of the features each) or by cp.async (two
 // for each tile buffer)
 constexpr int kFirstCopy = 9;
 template <bool TMA>
-constexpr int kThreads = (kFirstCopy + (TMA ? 4 : 8)) * 32;
+constexpr int kThreads = (kFirstCopy + (TMA ? 4 : 2 * kBufs)) * 32;
 
 struct L {
   static constexpr size_t q = 0;                                             // [8][64][128 B]
-  static constexpr size_t t = q + (size_t)kBlocks * kBlock;                  // [2][8][64][128 B]
-  static constexpr size_t p = t + (size_t)2 * kBlocks * kBlock;              // [2][64][128 B]
+  static constexpr size_t t = q + (size_t)kBlocks * kQBlock;                 // [3][8][48][128 B]
+  static constexpr size_t p = t + (size_t)kBufs * kBlocks * kBlock;          // [2][64][128 B]
   static constexpr size_t alpha = p + (size_t)2 * kHeads * 128;              // float [2][64]
   static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
   static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [18]
-  static constexpr size_t bars = scan + 20 * 8;                              // u64 [26]
-  static constexpr size_t misc = bars + 26 * 8;                              // masks [2][4], flags [2][4], slot, abort
+  static constexpr size_t range = scan + 18 * 8;                             // Range
+  static constexpr size_t rows = range + ((sizeof(Range) + 7) & ~7);         // Rows
+  static constexpr size_t bars = rows + ((sizeof(Rows) + 7) & ~7);                            // u64 [16]
+  static constexpr size_t misc = bars + 16 * 8;                              // masks [3][2], flags [2][4], slot, abort
   static constexpr size_t total = misc + 96;
 };
-static_assert(L::total + 1024 + sizeof(Rows) + sizeof(Range) + 64 <= 232448, "one CTA's shared memory");
+static_assert(L::total <= 232448, "one CTA's shared memory");
 
 // Every lane waits (each acquires what the barrier publishes); the warp goes on only if all succeeded.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
@@ -75,25 +82,23 @@ template <bool TMA>
 __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __grid_constant__ Params P,
                                                                         const __grid_constant__ Pages PG) {
   constexpr bool ALIGN = TMA;  // (tiles then hold whole boxes)
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = tc::smem_u32(smem_raw);
-  uint8_t *smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t smem[];  // (all of the kernel's shared memory: the swizzled tiles come first)
   const uint32_t s_q = tc::smem_u32(smem + L::q), s_t = tc::smem_u32(smem + L::t), s_p = tc::smem_u32(smem + L::p);
   float *alpha_sm = reinterpret_cast<float *>(smem + L::alpha), *f_sm = reinterpret_cast<float *>(smem + L::f);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bars);
-  // full, empty [2][4]: a quarter of the features of a tile has landed, has been used
-  uint64_t *full = bars, *empty = bars + 8, *s_full = bars + 16, *p_full = bars + 18, *stat = bars + 20, *fin = bars + 22,
-           *q_full = bars + 24, *drain = bars + 25;
-  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::misc);  // [2][4]: positions of a tile that are there (16 each)
-  int *flags = reinterpret_cast<int *>(masks + 8);                 // [2][4]: a maximum was raised (by warp)
+  // full, empty [3]: a tile has landed, has been used
+  uint64_t *full = bars, *empty = bars + kBufs, *s_full = bars + 2 * kBufs, *p_full = s_full + 2, *stat = s_full + 4,
+           *fin = s_full + 6, *q_full = s_full + 8, *drain = s_full + 9;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::misc);  // [3][2]: positions of a tile that are there (24 each)
+  int *flags = reinterpret_cast<int *>(masks + 2 * kBufs);         // [2][4]: a maximum was raised (by warp)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(flags + 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   const int nkb = (hd + 63) / 64;
 
-  __shared__ Rows rows;
-  __shared__ Range rg;
+  Rows &rows = *reinterpret_cast<Rows *>(smem + L::rows);
+  Range &rg = *reinterpret_cast<Range *>(smem + L::range);
   const int nt = find_range<kUnit, kThreads<TMA>, ALIGN>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
   if (nt == 0) {
     if (tid == 0 && !P.by_segment) P.split[blockIdx.x] = make_int2(0, 0);
@@ -101,8 +106,8 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
   }
   Cursor c = first_unit(rg, rows);
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&full[i], TMA ? 1 : 128);  // (the lanes of the buffer's four warps)
+    for (int i = 0; i < kBufs; ++i) {
+      tc::mbar_init(&full[i], TMA ? 4 : 64);  // the four warps, or the lanes of the buffer's two
       tc::mbar_init(&empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -121,16 +126,14 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kUnit;  // S: 2 x 64 columns, O^T: 4 x 64
-  auto par = [](int i) { return (uint32_t)((i >> 1) & 1); };  // phase of tile i's barriers
-  // The positions of tile buffer b that are there, as two words (behind the barrier that publishes them).
-  auto mask_of = [&](int b, uint32_t &lo, uint32_t &hi) {
-    if (TMA) {
-      lo = masks[4 * b];
-      hi = masks[4 * b + 1];
-    } else {
-      lo = masks[4 * b] | masks[4 * b + 1] << 16;
-      hi = masks[4 * b + 2] | masks[4 * b + 3] << 16;
+  const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kS;  // S: 2 x 64 columns, O^T: 4 x 64
+  // Scores, weights and what goes with them alternate by tile (phases: par), tile buffers go round.
+  auto par = [](int i) { return (uint32_t)((i >> 1) & 1); };
+  struct Ring {  // buffer and phase of a tile
+    int b = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+      if (++b == kBufs) b = 0, ph ^= 1u;
     }
   };
   auto last_of = [&](int i) { return c.t == c.units - 1 || i + 1 == nt; };  // of a segment, in this CTA
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         for (int i = 0; i < 4; ++i) {
           const int r = warp * 16 + 4 * i + (lane >> 3), d = kb * 64 + cc * 8;
           const bool in = r < nh && d < hd;
-          attn::cp_async16(s_q + kb * kBlock + r * 128 + ((cc ^ (r & 7)) << 4), in ? q + (int64_t)r * hd + d : a.q, in);
+          attn::cp_async16(s_q + kb * kQBlock + r * 128 + ((cc ^ (r & 7)) << 4), in ? q + (int64_t)r * hd + d : a.q, in);
         }
     };
     load_q(c);
@@ -163,11 +166,11 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     int nseg = 0;
     bool first = true;
     int seg = 0;  // the segment's first tile here
-    for (int i = 0; i < nt; ++i) {
-      const int b = (int)(i & 1);
-      if (!warp_wait(&full[4 * b + (TMA ? 0 : 3)], par(i), abort_flag)) break;  // (its mask)
-      uint32_t ok0, ok1;
-      mask_of(b, ok0, ok1);
+    Ring tile;
+    for (int i = 0; i < nt; ++i, tile.next()) {
+      const int b = i & 1;
+      if (!warp_wait(&full[tile.b], tile.ph, abort_flag)) break;  // (its mask)
+      uint32_t ok0 = masks[2 * tile.b], ok1 = masks[2 * tile.b + 1];
       if (!warp_wait(&s_full[b], par(i), abort_flag)) break;
       tc::tc_fence_after();
       const bool last = last_of(i);
@@ -177,20 +180,20 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         advance<kUnit, ALIGN>(a, P.Hg, rows, nx);
         load_q(nx);
       }
-      float s[32];  // s[4 j + 2 x + e]: position 8 j + qc + e of head x
+      float s[4 * kJ];  // s[4 j + 2 x + e]: position 8 j + qc + e of head x
       {
-        uint32_t r[32];
-        tc::tmem_ld_16x64_wait(tmem + (uint32_t)(b * kUnit) + lane_off, r);
+        uint32_t r[4 * kJ];
+        tc::tmem_ld_16x48_wait(tmem + (uint32_t)(b * kS) + lane_off, r);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(r[k]);
+        for (int k = 0; k < 4 * kJ; ++k) s[k] = __uint_as_float(r[k]);
       }
       float sc = P.scale_log2;
-      if ((ok0 & ok1) != 0xffffffffu) {  // positions that are not there: -inf (scaled here, so that a scale of 0 is right)
+      if ((ok0 & ok1) != kHalf) {  // positions that are not there: -inf (scaled here, so that a scale of 0 is right)
         ok0 >>= qc;
         ok1 >>= qc;
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          s[k] = ((k < 16 ? ok0 : ok1) >> (8 * ((k >> 2) & 3) + (k & 1))) & 1u ? s[k] * sc : -INFINITY;
+        for (int k = 0; k < 4 * kJ; ++k)
+          s[k] = ((k < 2 * kJ ? ok0 : ok1) >> (8 * ((k >> 2) % (kJ / 2)) + (k & 1))) & 1u ? s[k] * sc : -INFINITY;
         sc = 1.f;
       }
       float al[2];
@@ -200,10 +203,10 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         float mx = s[2 * x];  // the largest scaled score, of a scale of either sign
         if (sc < 0.f) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mx = fminf(mx, s[4 * (k >> 1) + 2 * x + (k & 1)]);
+          for (int k = 0; k < 2 * kJ; ++k) mx = fminf(mx, s[4 * (k >> 1) + 2 * x + (k & 1)]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mx = fmaxf(mx, s[4 * (k >> 1) + 2 * x + (k & 1)]);
+          for (int k = 0; k < 2 * kJ; ++k) mx = fmaxf(mx, s[4 * (k >> 1) + 2 * x + (k & 1)]);
         }
         mx *= sc;
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         const uint32_t prow = s_p + b * kHeads * 128 + h * 128 + 2 * qc;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kJ; ++j) {
           const float p0 = ex2(fmaf(s[4 * j + 2 * x], sc, -ref)), p1 = ex2(fmaf(s[4 * j + 2 * x + 1], sc, -ref));
           sum += p0 + p1;
           const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
@@ -290,11 +293,27 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     bool first = true, told = false;
     int nseg = 0;
     int seg = 0;
-    for (int i = 0; i < nt; ++i) {
-      const int b = (int)(i & 1);
+    Ring tile, before;  // this tile's buffer, the one's before
+    for (int i = 0; i < nt; ++i, before = tile, tile.next()) {
+      const int b = i & 1;
+      if (TMA) {
+        // positions that are not there hold what the page holds (or an older tile): their weights are 0, but 0 x NaN is not,
+        // so their rows are zeroed before the values' products read them
+        if (!warp_wait(&full[tile.b], tile.ph, abort_flag)) break;
+        const uint32_t ok0 = masks[2 * tile.b], ok1 = masks[2 * tile.b + 1];
+        if ((ok0 & ok1) != kHalf) {
+          for (int r = jt >> 6; r < kUnit; r += 2)
+            if (!(((r < kUnit / 2 ? ok0 : ok1) >> (r % (kUnit / 2))) & 1u))
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               s_t + (tile.b * kBlocks + ((jt >> 3) & 7)) * kBlock + r * 128 + (jt & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          attn::fence_proxy_async();
+        }
+      }
       if (!warp_wait(&stat[b], par(i), abort_flag)) break;
       if (!first && (flags[4 * b] | flags[4 * b + 1] | flags[4 * b + 2] | flags[4 * b + 3])) {
-        if (!warp_wait(&empty[4 * (b ^ 1) + 3], par(i - 1), abort_flag)) break;
+        if (!warp_wait(&empty[before.b], before.ph, abort_flag)) break;
         tc::tc_fence_after();
 #pragma unroll 1
         for (int cq = 0; cq < 4 * 4; ++cq) {
@@ -311,26 +330,6 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         attn::tmem_st_wait();
         tc::tc_fence_before();
       }
-      if (TMA) {
-        // positions that are not there hold what the page holds (or an older tile): their weights are 0, but 0 x NaN is not,
-        // so their rows are zeroed before the values' products read them
-        uint32_t ok0, ok1;
-        bool landed = warp_wait(&full[4 * b], par(i), abort_flag);
-        mask_of(b, ok0, ok1);
-        if (landed && (ok0 & ok1) != 0xffffffffu) {
-          for (int w = 1; w < 4 && landed; ++w) landed = warp_wait(&full[4 * b + w], par(i), abort_flag);
-          if (landed) {
-            for (int r = jt >> 6; r < kUnit; r += 2)
-              if (!(((r < 32 ? ok0 : ok1) >> (r & 31)) & 1u))
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                 s_t + (b * kBlocks + ((jt >> 3) & 7)) * kBlock + r * 128 + (jt & 7) * 16),
-                             "r"(0)
-                             : "memory");
-            attn::fence_proxy_async();
-          }
-        }
-        if (!landed) break;
-      }
       const bool last = last_of(i);
       tc::mbar_arrive(&p_full[b]);
       first = false;
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         continue;
       }
       if (!warp_wait(&fin[nseg & 1], (uint32_t)((nseg >> 1) & 1), abort_flag)) break;
-      if (!warp_wait(&empty[4 * b + 3], par(i), abort_flag)) break;
+      if (!warp_wait(&empty[tile.b], tile.ph, abort_flag)) break;
       tc::tc_fence_after();
       const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
       const int h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
@@ -391,172 +390,165 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     if (!P.by_segment && jt == 0 && !told) P.split[blockIdx.x] = make_int2(0, 0);
   } else if (warp == 8) {
     // ------------------------------------------------------------------------------ products
-    // The whole warp goes through the loop, one elected lane issues: the operands' descriptors then stay in uniform
-    // registers (issued from a one-lane branch each product cost about 115 cycles, of which it computes 48).
-    const uint32_t id1 = tc::idesc_bf16_f32(kHeads, kUnit);
-    const uint32_t id2 = tc::idesc_bf16_f32(128, kHeads, /*a_mn_major=*/true, /*b_mn_major=*/false);
-    const uint64_t dq = tc::sdesc_sw128(s_q, 16, 1024), dk = tc::sdesc_sw128(s_t, 16, 1024),
-                   dv = tc::sdesc_sw128(s_t, kBlock, 1024), dp = tc::sdesc_sw128(s_p, 16, 1024);
-    constexpr uint64_t kStep = kBlock >> 4;  // a block, in descriptor units
-    auto block = [&](int b, int kb) {        // (by the elected lane) the scores' products over 64 features
+    // One elected lane (by elect.sync, which lets the operands' descriptors stay in uniform registers: issued by `lane == 0`
+    // each product cost about 115 cycles, of which it computes 40 or 57).
+    if (tc::elect_one()) {
+      const uint32_t id1 = tc::idesc_bf16_f32(kHeads, kUnit);
+      const uint32_t id2 = tc::idesc_bf16_f32(128, kHeads, /*a_mn_major=*/true, /*b_mn_major=*/false);
+      // the operands' descriptors differ in their lower words (address, leading offset) only
+      const uint32_t dq = (uint32_t)tc::sdesc_sw128(s_q, 16, 1024), dk = (uint32_t)tc::sdesc_sw128(s_t, 16, 1024),
+                     dv = (uint32_t)tc::sdesc_sw128(s_t, kBlock, 1024), dp = (uint32_t)tc::sdesc_sw128(s_p, 16, 1024);
+      const uint32_t hi = (uint32_t)(tc::sdesc_sw128(0, 16, 1024) >> 32);
+      constexpr uint32_t kStep = kBlock >> 4, kQStep = kQBlock >> 4;  // a block, in descriptor units
+      auto mma = [hi](uint32_t d, uint32_t al, uint32_t bl, uint32_t id, uint32_t acc) {
+        tc::mma_bf16(d, (uint64_t)hi << 32 | al, (uint64_t)hi << 32 | bl, id, acc);
+      };
+      // (Rolled loops: unrolled, the products' code is fetched anew for every tile while eleven other warps run theirs.)
+      auto scores = [&](int b, int sb) {
+        const uint32_t d = tmem + (uint32_t)(sb * kS);
+        uint32_t al = dq, bl = dk + b * kBlocks * kStep;
+#pragma unroll 1
+        for (int kb = 0; kb < nkb; ++kb, al += kQStep, bl += kStep) {
+          mma(d, al, bl, id1, kb ? 1u : 0u);
 #pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4)
-        tc::mma_bf16(tmem + (uint32_t)(b * kUnit), dq + kb * kStep + 2 * k4, dk + (b * kBlocks + kb) * kStep + 2 * k4, id1,
-                     (kb | k4) ? 1u : 0u);
-    };
-    auto scores = [&](int b, int w) {  // quarter w of the features
-      tc::tc_fence_after();
-      if (tc::elect_one()) {
-        if (2 * w < nkb) block(b, 2 * w);
-        if (2 * w + 1 < nkb) block(b, 2 * w + 1);
-        if (w == 3) tc::mma_commit(&s_full[b]);
-      }
-      __syncwarp();
-    };
-    auto scores_from = [&](int b, int w) {  // quarters w, w + 1, ...: without a pause between them
-      tc::tc_fence_after();
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int kb = 0; kb < kBlocks; ++kb)
-          if (kb >= 2 * w && kb < nkb) block(b, kb);
-        tc::mma_commit(&s_full[b]);
-      }
-      __syncwarp();
-    };
-    auto values = [&](int b, bool first) {
-      tc::tc_fence_after();
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int ch = 0; ch < kHD / 128; ++ch) {
-          if (ch * 128 < hd) {
-#pragma unroll
-            for (int ii = 0; ii < kUnit / 16; ++ii)
-              tc::mma_bf16(tO + (uint32_t)(ch * kHeads), dv + (b * kBlocks + 2 * ch) * kStep + ii * 128,
-                           dp + b * (kHeads * 128 >> 4) + ii * 2, id2, (first && ii == 0) ? 0u : 1u);
-          }
-          tc::mma_commit(&empty[4 * b + ch]);
+          for (int k4 = 1; k4 < 4; ++k4) mma(d, al + 2 * k4, bl + 2 * k4, id1, 1u);
         }
-      }
-      __syncwarp();
-    };
-    auto ready = [](uint64_t *bar, uint32_t parity) {
-      const bool r = tc::mbar_test_wait(bar, parity);
-      return __all_sync(0xffffffffu, r);
-    };
-    auto landed = [&](int b, int w, int i) {  // all of quarters w .. 3
-      bool r = true;
-      for (int k = 3; k >= w && r; --k) r = ready(&full[4 * b + k], par(i));
-      return r;
-    };
-    bool ok = warp_wait(q_full, 0, abort_flag), first = true;
-    int nq = 1;  // segments whose q has been waited for
-    for (int w = 0; w < 4 && ok; ++w) {
-      ok = warp_wait(&full[w], 0, abort_flag);
-      if (ok) scores(0, w);
-    }
-    for (int i = 0; i < nt && ok; ++i) {
-      const int b = (int)(i & 1), nb = b ^ 1;
-      const bool last = last_of(i);
-      // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
-      // only behind the values)
-      bool pv = false;
-      int w = i + 1 < nt ? 0 : 4;
-      const uint64_t t0 = tc::global_ns();
-      uint32_t spins = 0;
-      while (!pv || w < 4) {
-        if (!pv && ready(&p_full[b], par(i))) {
-          values(b, first);
-          pv = true;
-          if (last && w < 4) {
-            if (!(ok = warp_wait(q_full, (uint32_t)(nq & 1), abort_flag))) break;
-            ++nq;
+        tc::mma_commit(&s_full[sb]);
+      };
+      auto values = [&](int b, int sb, bool first) {
+        tc::tc_fence_after();
+        const uint32_t p0 = dp + sb * (kHeads * 128 >> 4);
+#pragma unroll 1
+        for (int ch = 0; ch * 128 < hd; ++ch) {
+          const uint32_t v0 = dv + (b * kBlocks + 2 * ch) * kStep;
+#pragma unroll
+          for (int ii = 0; ii < kUnit / 16; ++ii)
+            mma(tO + (uint32_t)(ch * kHeads), v0 + ii * 128, p0 + ii * 2, id2, (first && ii == 0) ? 0u : 1u);
+        }
+        tc::mma_commit(&empty[b]);
+      };
+      bool ok = tc::mbar_wait(q_full, 0, abort_flag), first = true;
+      int nq = 1;  // segments whose q has been waited for
+      if (ok && (ok = tc::mbar_wait(&full[0], 0, abort_flag))) scores(0, 0);
+      Ring tile, nx;
+      nx.next();
+      for (int i = 0; i < nt && ok; ++i, tile = nx, nx.next()) {
+        const int sb = i & 1;
+        const bool last = last_of(i);
+        // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
+        // only behind the values)
+        bool pv = false, qk = i + 1 == nt;
+        const uint64_t t0 = tc::global_ns();
+        uint32_t spins = 0;
+        while (!pv || !qk) {
+          // (both barriers asked at once: a read of shared memory takes 250 cycles beside the products' operands)
+          const bool p_ready = tc::mbar_test_wait(&p_full[sb], par(i)), t_ready = tc::mbar_test_wait(&full[nx.b], nx.ph);
+          if (!pv && p_ready) {
+            values(tile.b, sb, first);
+            pv = true;
+            if (last && !qk) {
+              if (!(ok = tc::mbar_wait(q_full, (uint32_t)(nq & 1), abort_flag))) break;
+              ++nq;
+            }
           }
-          spins = 0;
-        } else if (w < 3 && (pv || !last) && landed(nb, w, i + 1)) {
-          scores_from(nb, w);
-          w = 4;
-          spins = 0;
-        } else if (w < 4 && (pv || !last) && ready(&full[4 * nb + w], par(i + 1))) {
-          scores(nb, w);
-          ++w;
-          spins = 0;
-        } else if ((++spins & 63) == 0) {
-          const bool gone = *abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs;
-          if (__any_sync(0xffffffffu, gone)) {
+          if (!qk && (pv || !last) && t_ready) {
+            scores(nx.b, sb ^ 1);
+            qk = true;
+          }
+          if ((++spins & 63) == 0 && (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
         }
+        if (!ok) break;
+        first = last;
+        if (last) {
+          c.t = c.units - 1;
+          if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+        } else {
+          ++c.t;
+        }
       }
-      if (!ok) break;
-      first = last;
-      if (last) {
-        c.t = c.units - 1;
-        if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
-      } else {
-        ++c.t;
+      // nothing may still read shared memory, write TMEM or arrive when the CTA ends
+      tc::mma_commit(drain);
+      const uint64_t t1 = tc::global_ns();
+      while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
       }
-    }
-    // nothing may still read shared memory, write TMEM or arrive when the CTA ends
-    if (tc::elect_one()) tc::mma_commit(drain);
-    __syncwarp();
-    const uint64_t t1 = tc::global_ns();
-    while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
     }
     __syncwarp();
   } else if (TMA) {
     // ------------------------------------------------------------------------------ copies by TMA: a quarter of the features a warp
-    const int w = warp - kFirstCopy, R = PG.box_rows, nbox = kUnit / R;
+    const int w = warp - kFirstCopy, R = PG.box_rows, nbox = kUnit / R, r_log = __ffs(R) - 1;
     const int nb_kb = max(0, min(2, nkb - 2 * w));  // its 64-feature blocks
     if (lane == 0) tc::prefetch_tmap(&PG.map);
-    int issued = 0;
-    for (int i = 0; i < nt; ++i) {
-      const int b = i & 1;
-      const Row row = rows.get<kUnit, ALIGN>(a, c.n);
-      const int lo = max(row.lead - c.t * kUnit, 0), hi = min(row.rows - c.t * kUnit, kUnit);  // its positions lo .. hi - 1
-      const int kvh = c.hg / P.sub;
-      // lane k: box k of the tile (rows k R .. k R + R - 1 lie in one page)
-      const bool wanted = lane < nbox && lane * R < hi && (lane + 1) * R > lo;
-      const uint32_t pos = (uint32_t)(row.first + c.t * kUnit + lane * R), pg = P.page.div(pos);
-      const int id = wanted ? a.table[(int64_t)row.req * a.width + pg] : 0;
-      const bool good = wanted && id >= 0 && id < a.c.n_pages;
-      if (wanted && !good) atomicOr(a.status, kStatusBadIndex);
-      const uint32_t boxes = __ballot_sync(0xffffffffu, good);
-      if (i >= 2 && !warp_wait(&empty[4 * b + w], par(i) ^ 1u, abort_flag)) break;
-      if (w == 0) {
-        const uint32_t m0 = __ballot_sync(0xffffffffu, lane >= lo && lane < hi && ((boxes >> (lane / R)) & 1u));
-        const uint32_t m1 = __ballot_sync(0xffffffffu, lane + 32 >= lo && lane + 32 < hi && ((boxes >> ((lane + 32) / R)) & 1u));
-        if (lane == 0) {  // (the mask of the tile before has been read: its values' products are under way)
-          masks[4 * b] = m0;
-          masks[4 * b + 1] = m1;
-        }
+    // Box k of a tile (its positions k R .. k R + R - 1, which lie in one page) is lane k's; m0, m1: the tile's positions
+    // that are there.  A tile is looked up two tiles ahead, so that nothing but the copies is left to do when its buffer
+    // is handed back.
+    struct Tile {
+      uint32_t boxes, m0, m1;
+      int kvh, page, row;
+    };
+    int looked = 0, issued = 0;
+    auto look = [&]() {
+      Tile x{0, 0, 0, 0, 0, 0};
+      if (looked < nt) {
+        const Row row = rows.get<kUnit, ALIGN>(a, c.n);
+        const int lo = max(row.lead - c.t * kUnit, 0), hi = min(row.rows - c.t * kUnit, kUnit);  // positions lo .. hi - 1
+        x.kvh = c.hg / P.sub;
+        const bool wanted = lane < nbox && lane * R < hi && (lane + 1) * R > lo;
+        const uint32_t pos = (uint32_t)(row.first + c.t * kUnit + lane * R), pg = P.page.div(pos);
+        x.row = (int)(pos - pg * P.page.d);
+        x.page = wanted ? a.table[(int64_t)row.req * a.width + pg] : 0;
+        const bool good = wanted && x.page >= 0 && x.page < a.c.n_pages;
+        if (wanted && !good) atomicOr(a.status, kStatusBadIndex);
+        x.boxes = __ballot_sync(0xffffffffu, good);
+        constexpr int kH = kUnit / 2;
+        x.m0 = __ballot_sync(0xffffffffu, lane < kH && lane >= lo && lane < hi && ((x.boxes >> (lane >> r_log)) & 1u));
+        x.m1 = __ballot_sync(0xffffffffu, lane < kH && lane + kH >= lo && lane + kH < hi && ((x.boxes >> ((lane + kH) >> r_log)) & 1u));
+        if (++looked < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
       }
-      if (lane == 0) tc::mbar_expect_tx(&full[4 * b + w], (uint32_t)(__popc(boxes) * nb_kb * R * 128));
+      return x;
+    };
+    Tile t0 = look(), t1 = look();
+    Ring tile;
+    for (int i = 0; i < nt; ++i, tile.next()) {
+      if (i >= kBufs && !warp_wait(&empty[tile.b], tile.ph ^ 1u, abort_flag)) break;
+      uint64_t *bar = &full[tile.b];
+      if (lane == 0) {
+        if (w == 0) {  // (the mask of the tile before has been read: its values are done)
+          masks[2 * tile.b] = t0.m0;
+          masks[2 * tile.b + 1] = t0.m1;
+        }
+        tc::mbar_expect_tx(bar, (uint32_t)(__popc(t0.boxes) * nb_kb * R * 128));
+      }
       __syncwarp();
-      if (good)
+      if ((t0.boxes >> lane) & 1u)
         for (int kb = 0; kb < nb_kb; ++kb)
-          tc::tma_load_4d(s_t + (b * kBlocks + 2 * w + kb) * kBlock + lane * R * 128, &PG.map, &full[4 * b + w], (2 * w + kb) * 64,
-                          kvh, (int)(pos - pg * P.page.d), id);
+          tc::tma_load_4d(s_t + (tile.b * kBlocks + 2 * w + kb) * kBlock + lane * R * 128, &PG.map, bar, (2 * w + kb) * 64, t0.kvh,
+                          t0.row, t0.page);
+      t0 = t1;
+      t1 = look();
       issued = i + 1;
-      if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
     }
     // nothing is in flight when the CTA ends, even after a wait that ran out
-    for (int i = max(issued - 2, 0); i < issued; ++i) {
-      const uint64_t t0 = tc::global_ns();
-      while (!tc::mbar_try_wait(&full[4 * (i & 1) + w], par(i)) && tc::global_ns() - t0 < tc::kWaitLimitNs) {
+    for (int i = max(issued - kBufs, 0); i < issued; ++i) {
+      const uint64_t t2 = tc::global_ns();
+      while (!tc::mbar_try_wait(&full[i % kBufs], (uint32_t)((i / kBufs) & 1)) && tc::global_ns() - t2 < tc::kWaitLimitNs) {
       }
     }
   } else {
-    // ------------------------------------------------------------------------------ copies by cp.async: 16 positions a warp
-    const int b = (warp - kFirstCopy) >> 2, part = (warp - kFirstCopy) & 3;
+    // ------------------------------------------------------------------------------ copies by cp.async: 24 positions a warp
+    const int b = (warp - kFirstCopy) >> 1, part = (warp - kFirstCopy) & 1;
     const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
     const int cc = lane & 7;
-    if (b == 1 && nt > 1) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
-    for (int i = b; i < nt; i += 2) {
+    constexpr int kH = kUnit / 2;
+    for (int k = 0; k < b && k + 1 < nt; ++k) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+    uint32_t ph = 1;
+    for (int i = b; i < nt; i += kBufs, ph ^= 1u) {
       const Row row = rows.get<kUnit, ALIGN>(a, c.n);
-      const int j = c.t * kUnit + part * 16 + (lane & 15);
-      const bool there = j < row.rows;
+      const int j = c.t * kUnit + part * kH + lane;
+      const bool there = lane < kH && j < row.rows;
       const uint32_t pos = (uint32_t)(row.first + j), pg = P.page.div(pos);
       const int id = there ? a.table[(int64_t)row.req * a.width + pg] : 0;
       const bool good = there && id >= 0 && id < a.c.n_pages;
@@ -564,45 +556,27 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       const int64_t off = good ? (int64_t)id * a.c.k_page + (int64_t)(pos - pg * P.page.d) * a.c.k_row +
                                      (int64_t)(c.hg / P.sub) * a.c.k_head
                                : -1;
-      const uint32_t mask = __ballot_sync(0xffffffffu, good) & 0xffffu;
-      int64_t ro[4];  // positions 4 u + lane / 8 of this warp's sixteen
+      const uint32_t mask = __ballot_sync(0xffffffffu, good);
+      int64_t ro[kH / 4];  // positions 4 u + lane / 8 of this warp's 24
 #pragma unroll
-      for (int u = 0; u < 4; ++u) ro[u] = __shfl_sync(0xffffffffu, off, 4 * u + (lane >> 3));
-      const uint32_t dst = s_t + b * kBlocks * kBlock + (part * 16 + (lane >> 3)) * 128;
-      bool ok = true;
+      for (int u = 0; u < kH / 4; ++u) ro[u] = __shfl_sync(0xffffffffu, off, 4 * u + (lane >> 3));
+      const uint32_t dst = s_t + b * kBlocks * kBlock + (part * kH + (lane >> 3)) * 128;
+      if (i >= kBufs && !warp_wait(&empty[b], ph, abort_flag)) break;
+      if (lane == 0) masks[2 * b + part] = mask;
+#pragma unroll 1
+      for (int kb = 0; kb < nkb; ++kb) {
+        const bool f_in = kb * 64 + cc * 8 < hd;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {  // a quarter of the features as soon as the values before have read it
-        if (ok && i >= 2) ok = warp_wait(&empty[4 * b + w], par(i) ^ 1u, abort_flag);
-        if (ok && w == 3 && lane == 0) masks[4 * b + part] = mask;  // (the tile before is done with)
-#pragma unroll
-        for (int kb = 2 * w; kb < 2 * w + 2; ++kb) {
-          const bool f_in = kb * 64 + cc * 8 < hd;
-          if (ok && kb < nkb) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const bool in = ro[u] >= 0 && f_in;
-              const int r7 = (4 * u + (lane >> 3)) & 7;
-              attn::cp_async16(dst + kb * kBlock + u * 512 + ((cc ^ r7) << 4), in ? kbase + ro[u] + kb * 64 + cc * 8 : kbase, in);
-            }
-          }
+        for (int u = 0; u < kH / 4; ++u) {
+          const bool in = ro[u] >= 0 && f_in;
+          const int r7 = (4 * u + (lane >> 3)) & 7;
+          attn::cp_async16(dst + kb * kBlock + u * 512 + ((cc ^ r7) << 4), in ? kbase + ro[u] + kb * 64 + cc * 8 : kbase, in);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
       }
-      if (!ok) break;
-      asm volatile("cp.async.wait_group 3;" ::: "memory");
+      attn::cp_async_wait_all();
       attn::fence_proxy_async();
-      tc::mbar_arrive(&full[4 * b]);
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-      attn::fence_proxy_async();
-      tc::mbar_arrive(&full[4 * b + 1]);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      attn::fence_proxy_async();
-      tc::mbar_arrive(&full[4 * b + 2]);
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      attn::fence_proxy_async();
-      tc::mbar_arrive(&full[4 * b + 3]);
-      if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
-      if (i + 2 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+      tc::mbar_arrive(&full[b]);
+      for (int k = 1; k <= kBufs && i + k < nt; ++k) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
     }
     attn::cp_async_wait_all();
   }
@@ -694,8 +668,7 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
   // TMA where pages hold whole boxes of at least 8 rows (the swizzle's period), up to a tile; cp.async for other pages
   Pages pg;
   memset(&pg, 0, sizeof(pg));
-  pg.box_rows = a.c.page & -a.c.page;
-  if (pg.box_rows > kUnit) pg.box_rows = kUnit;
+  pg.box_rows = std::min(a.c.page & -a.c.page, kUnit & -kUnit);
   bool tma = pg.box_rows >= 8;
   if (tma) {
     const uint64_t dims[4] = {(uint64_t)a.c.head_dim, (uint64_t)a.c.kv_heads, (uint64_t)a.c.page, (uint64_t)a.c.n_pages};
@@ -706,7 +679,7 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
     tma = tma_map_pages_bf16(&pg.map, a.c.k, dims, strides, 64, (uint32_t)pg.box_rows);
   }
   static SmemAttr attr_tma, attr_copy;
-  const size_t smem = L::total + 1024;
+  const size_t smem = L::total;
   cudaError_t e = tma ? attr_tma.ensure((const void *)k_paged_attn_latent<true>, (int)smem)
                       : attr_copy.ensure((const void *)k_paged_attn_latent<false>, (int)smem);
   if (e != cudaSuccess) return e;
