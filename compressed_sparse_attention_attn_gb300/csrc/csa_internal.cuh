@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstddef>
 #include <mutex>
+#include <utility>
 
 #include "../../include/csa.h"
 
@@ -224,6 +225,29 @@ cudaError_t launch_compress(const CompressArgs &a, float *ws, size_t ws_bytes, i
 cudaError_t launch_fill_f32(float *p, int64_t n, float v, cudaStream_t s);
 
 // ---- a continuous batch over a paged cache -------------------------------------------------------
+// These kernels are launched as programmatic dependents and wait for the kernels before them (dependency_wait)
+// before they read or write anything: only the launch itself overlaps what came before.
+template <class... Args, class... Given>
+inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, unsigned cluster,
+                                    Given &&...given) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Given>(given)...);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The step's token maps and tables from the requests' lengths (k_page_step.cu; csa_page_step's arguments).
 struct PageStepArgs {
   const int32_t *new_len, *length;

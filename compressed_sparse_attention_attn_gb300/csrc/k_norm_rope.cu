@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, V == 2 ? (HALF ? 5 : 6) : 1) k_norm_
   const int hd = a.c.head_dim, h2 = a.rd >> 1;
   Item t;
   const int h = find_item(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
+  dependency_wait();
   int f[V];  // first feature of this lane's vectors (hd: none)
   uint4 x[V];
 #pragma unroll
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_any(const __grid_constan
   const int hd = a.c.head_dim, h2 = a.rd >> 1;
   Item t;
   const int h = find_item(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
+  dependency_wait();
   uint4 x[V];
   float r = 0.f, z[V][8];  // z: partners, normed but for r
 #pragma unroll
@@ -264,8 +266,7 @@ cudaError_t launch(Kernel k, int G, const NormRopeArgs &a, cudaStream_t s) {
   const int64_t items = (int64_t)a.N * per_token;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;  // (refused by the entry)
   const Grid g{(int)items, paged::FastDiv((uint32_t)per_token), paged::FastDiv((uint32_t)a.c.page)};
-  k<<<(unsigned)((items * G + kThreads - 1) / kThreads), kThreads, 0, s>>>(a, g);
-  return cudaGetLastError();
+  return launch_dependent(k, dim3((unsigned)((items * G + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, 1, a, g);
 }
 template <int G, int V>
 cudaError_t launch_vectors(const NormRopeArgs &a, cudaStream_t s) {

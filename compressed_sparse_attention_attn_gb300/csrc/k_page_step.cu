@@ -13,8 +13,6 @@
 // and takes an eighth of the tokens and pages.  The hardware's cluster barrier, after everything has been
 // read, lets length_out and state_out be length and state: one launch, and no counter that two calls could
 // share.
-#include <cstring>
-
 #include "csa_internal.cuh"
 #include "paged_common.cuh"
 
@@ -57,6 +55,7 @@ __global__ void __launch_bounds__(1024) k_page_step(const __grid_constant__ Page
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5, nw = nt >> 5;
   const int gt = blockIdx.x * nt + tid, gn = gridDim.x * nt;  // over the cluster
   if (tid == 0) s_err = 0;
+  dependency_wait();
   const int head = a.state[0], count = a.state[1];
   __syncthreads();
   // ---- the running sums: a thread takes `per` requests in a row
@@ -204,21 +203,10 @@ cudaError_t launch_page_step(const PageStepArgs &a, cudaStream_t s) {
   const size_t smem = 4 * sizeof(uint32_t) * (size_t)a.R;
   cudaError_t e = attr.ensure((const void *)k_page_step, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
   const bool large = a.N > 4096 || a.R > 4096;
-  cfg.gridDim = dim3(large ? kClusterCtas : 1);
-  cfg.blockDim = dim3(a.N <= 256 && a.R <= 256 ? 256 : 1024);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cfg.gridDim.x;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_page_step, a, paged::FastDiv((uint32_t)a.page));
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  const unsigned ctas = large ? kClusterCtas : 1;
+  return launch_dependent(k_page_step, dim3(ctas), dim3(a.N <= 256 && a.R <= 256 ? 256 : 1024), smem, s, ctas, a,
+                          paged::FastDiv((uint32_t)a.page));
 }
 
 }  // namespace csa

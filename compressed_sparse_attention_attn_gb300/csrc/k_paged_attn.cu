@@ -92,6 +92,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   __shared__ Rows rows;
   __shared__ Range rg;
+  dependency_wait();
   const int nunits = find_range<kUnit, kThreads, false>(P, s_scan, rows, rg);
   if (nunits == 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
@@ -421,8 +422,7 @@ cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cuda
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * NH * HD;
   if (sizeof(float) * 2 * grid * NH * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;
-  k_paged_attn<HD, NH><<<(unsigned)grid, S::kThreads, S::kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(k_paged_attn<HD, NH>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, 1, p);
 }
 template <int HD>
 cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {

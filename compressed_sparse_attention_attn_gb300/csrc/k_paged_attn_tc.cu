@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
 
   Rows &rows = *reinterpret_cast<Rows *>(smem + L::rows);
   Range &rg = *reinterpret_cast<Range *>(smem + L::range);
+  dependency_wait();
   const int nt = find_range<kUnit, kThreads<TMA>, ALIGN>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
   if (nt == 0) {
     if (tid == 0 && !P.by_segment) P.split[blockIdx.x] = make_int2(0, 0);
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         // this tile's values and the next tile's scores, whichever is ready (a new segment's q, and so its scores,
         // only behind the values)
         bool pv = false, qk = i + 1 == nt;
-        const uint64_t t0 = tc::global_ns();
+        uint64_t t0 = 0;  // (when it first had to wait: the timer is slow to read)
         uint32_t spins = 0;
         while (!pv || !qk) {
           // (both barriers asked at once: a read of shared memory takes 250 cycles beside the products' operands)
@@ -455,10 +456,13 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
             scores(nx.b, sb ^ 1);
             qk = true;
           }
-          if ((++spins & 63) == 0 && (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
+          if ((++spins & 63) == 0) {
+            if (t0 == 0) t0 = tc::global_ns();
+            if (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs) {
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
           }
         }
         if (!ok) break;
@@ -598,7 +602,7 @@ constexpr int kJoinChunk = 64;
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid_constant__ Params P) {
   __shared__ float s_f[kJoinThreads / 32][kMaxCtas];
   const PagedAttnArgs &a = P.a;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (a programmatic dependent of the kernel above)
+  dependency_wait();
   const int2 sp = P.split[blockIdx.x];
   const int n_hg = P.by_segment ? (int)blockIdx.x : sp.x, n = n_hg / P.Hg, hg = n_hg - n * P.Hg, parts = sp.y;
   if (P.by_segment && row_of<kUnit, false>(a, n, false).units == 0) return;  // (a row that was left alone: nothing told)
@@ -696,25 +700,12 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
   p.by_segment = segments <= grid;
   p.ctas = (int)grid;
   if (sizeof(float) * 2 * grid * kHeads * (kHD + 2) + sizeof(int2) * grid > ws_bytes) return cudaErrorInvalidValue;
-  if (tma)
-    k_paged_attn_latent<true><<<(unsigned)grid, kThreads<true>, smem, s>>>(p, pg);
-  else
-    k_paged_attn_latent<false><<<(unsigned)grid, kThreads<false>, smem, s>>>(p, pg);
-  if ((e = cudaGetLastError()) != cudaSuccess || segments == units) return e;  // (one tile a segment: nothing is shared)
+  e = tma ? launch_dependent(k_paged_attn_latent<true>, dim3((unsigned)grid), dim3(kThreads<true>), smem, s, 1, p, pg)
+          : launch_dependent(k_paged_attn_latent<false>, dim3((unsigned)grid), dim3(kThreads<false>), smem, s, 1, p, pg);
+  if (e != cudaSuccess || segments == units) return e;  // (one tile a segment: nothing is shared)
   // about 600 blocks of the join, and no more than there is work
   const int64_t x = std::min(segments, grid), y = std::min<int64_t>(std::max<int64_t>(1, 4 * num_sms / x), kHeads);
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)x, (unsigned)y);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_paged_join_latent, p);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return launch_dependent(k_paged_join_latent, dim3((unsigned)x, (unsigned)y), dim3(kJoinThreads), 0, s, 1, p);
 }
 
 }  // namespace paged
