@@ -7,7 +7,7 @@
 // rate, far below what warp-level products give, and their accumulators stay in registers -- no trip
 // through tensor memory between the scores and the values.
 //
-// A unit is 16 positions for each of a CTA's warps (four; six at 256 features).  Every warp streams its own tiles (16 key rows,
+// A unit is 16 positions for each of a CTA's warps (four; at 256 features three, or six with more than eight heads a kv head).  Every warp streams its own tiles (16 key rows,
 // 16 value rows) through a ring of its own in shared memory, with no barrier between the warps before the
 // end of a segment; the ring runs on across segments.  Rows come by 16-byte cp.async from the page of each
 // position (looked up two tiles ahead), rows past the end and features past head_dim as zeros; chunks are
@@ -28,16 +28,19 @@ constexpr int kTile = 16;  // positions of a warp's tile
 
 // Warps and ring stages are set so that the rings fill an SM's shared memory and 64 to 128 KB are in flight: 4 x 3 x 4 KB
 // x 4 (or 3) CTAs at 64 features, 4 x 2 x 8 KB x 3 (x 3 x 8 KB x 2 where 16 heads' accumulators need the
-// registers) at 128, 6 x 2 x 16 KB x 1 at 256 (4 warps of 3 stages took 94 against 81 us over 48 rows of 16 x 256).
+// registers) at 128, 3 x 2 x 16 KB x 2 at 256 (one CTA of 6: 83 against 74 us over 48 windows of 16 heads, whose segments end
+// every few units), 6 x 2 x 16 KB x 1 with 16 heads (two CTAs of 3 spill: 90 against 47 us over 16 rows of 32 x 256).
 template <int HD, int NH>
 struct Shape {
-  static constexpr int kWarps = HD == 256 ? 6 : 4;
+  static constexpr int kWarps = HD == 256 ? (NH == 8 ? 3 : 6) : 4;
   static constexpr int kStages = HD == 256 || (HD == 128 && NH == 8) ? 2 : 3;
-  static constexpr int kCtas = HD == 64 ? (NH == 8 ? 4 : 3) : (HD == 128 ? (NH == 8 ? 3 : 2) : 1);  // resident an SM
+  static constexpr int kCtas = HD == 64 ? (NH == 8 ? 4 : 3) : (HD == 128 ? (NH == 8 ? 3 : 2) : NH == 8 ? 2 : 1);  // resident an SM
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kUnit = kWarps * kTile;            // positions of a unit
   static constexpr int kStageBytes = 2 * kTile * HD * 2;  // key rows, value rows
-  static constexpr int kSmem = kWarps * kStages * kStageBytes;
+  // q as fragments in registers, but in shared memory where its 64 registers and 128 of accumulators are too many
+  static constexpr bool kQShared = HD == 256 && NH == 16;
+  static constexpr int kQAt = kWarps * kStages * kStageBytes, kSmem = kQAt + (kQShared ? NH * HD * 2 : 0);
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -145,36 +148,22 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       const int64_t ko = good ? (int64_t)f.page * a.c.k_page + (int64_t)r * a.c.k_row : -1;
       const int64_t vo = good ? (int64_t)f.page * v_page + (int64_t)r * v_row : -1;
       const bf16 *kh = kbase + (int64_t)f.kvh * a.c.k_head, *vh = vbase + (int64_t)f.kvh * v_head;
-      constexpr int CH = HD / 8;             // 16-byte chunks of a row
-      constexpr int RI = 32 / CH > 0 ? 32 / CH : 1;  // rows a warp copies at a time
-      const uint32_t st = ring + stage * S::kStageBytes;
-      const int ch = lane % CH, r0 = lane / CH;
-      const bool f_in = ch * 8 < hd;
-      if (ok == kAll && __all_sync(0xffffffffu, __shfl_sync(0xffffffffu, r, 0) + (lane & (kTile - 1)) == r)) {
-        // the tile lies in one page: rows one k_row apart
-        const bf16 *ks = kh + __shfl_sync(0xffffffffu, ko, 0) + r0 * a.c.k_row + ch * 8;
-        const bf16 *vs = vh + __shfl_sync(0xffffffffu, vo, 0) + r0 * v_row + ch * 8;
-        if (!f_in) ks = kbase, vs = vbase;
-        const int64_t k_step = f_in ? RI * a.c.k_row : 0, v_step = f_in ? RI * v_row : 0;
+      // Eight lanes a row, four rows at a time, 128 bytes of a row at a time (its further parts one constant apart).  Rows
+      // that are not there as zeros: their weights are 0, but 0 x NaN is not.
+      const int ch = lane & 7, r0 = lane >> 3;
+      const uint32_t st = ring + stage * S::kStageBytes + r0 * (HD * 2);
 #pragma unroll
-        for (int i = 0; i < kTile / RI; ++i) {
-          const int row = r0 + RI * i;
-          const uint32_t dst = st + row * (HD * 2) + ((ch ^ (row & 7)) << 4);
-          attn::cp_async16(dst, ks, f_in);
-          attn::cp_async16(dst + kTile * HD * 2, vs, f_in);
-          ks += k_step;
-          vs += v_step;
-        }
-      } else {
-        // (rows that are not there as zeros: their weights are 0, but 0 x NaN is not)
-#pragma unroll 4
-        for (int i = 0; i < kTile / RI; ++i) {
-          const int row = r0 + RI * i;
-          const int64_t k_off = __shfl_sync(0xffffffffu, ko, row), v_off = __shfl_sync(0xffffffffu, vo, row);
-          const bool in = k_off >= 0 && f_in;
-          const uint32_t dst = st + row * (HD * 2) + ((ch ^ (row & 7)) << 4);
-          attn::cp_async16(dst, in ? kh + k_off + ch * 8 : kbase, in);
-          attn::cp_async16(dst + kTile * HD * 2, in ? vh + v_off + ch * 8 : vbase, in);
+      for (int i = 0; i < kTile / 4; ++i) {
+        const int row = r0 + 4 * i;
+        const int64_t k_off = __shfl_sync(0xffffffffu, ko, row), v_off = __shfl_sync(0xffffffffu, vo, row);
+        const bool in = k_off >= 0;
+        const bf16 *ks = in ? kh + k_off + ch * 8 : kbase, *vs = in ? vh + v_off + ch * 8 : vbase;
+        const uint32_t dst = st + i * (4 * HD * 2) + ((ch ^ (row & 7)) << 4);
+#pragma unroll
+        for (int c = 0; c < HD / 64; ++c) {
+          const bool f_in = in && ch * 8 + c * 64 < hd;
+          attn::cp_async16(dst + c * 128, f_in ? ks + c * 64 : kbase, f_in);
+          attn::cp_async16(dst + c * 128 + kTile * HD * 2, f_in ? vs + c * 64 : vbase, f_in);
         }
       }
     }
@@ -186,7 +175,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   // rows of the first product, features of the second, and the heads the columns of both: half the products,
   // exponentials and registers where a kv head has no more than eight query heads.
   constexpr int QR = NH == 16 ? 4 : 2, AT = NH == 16 ? HD / 8 : HD / 16;
-  uint32_t qf[HD / 16][QR];
+  uint32_t qf[S::kQShared ? 1 : HD / 16][QR];
   float acc[AT][4], m[2], l[2];  // m, l: of heads qr, qr + 8 (NH 16) or qc, qc + 1 (NH 8); l of this thread's positions
   int h0 = 0, nh = 0;
   int seg = 0;  // the CTA's first unit of the current segment
@@ -196,13 +185,22 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
     h0 = kvh * P.g + sg * kHeads;
     nh = min(kHeads, P.g - sg * kHeads);
     const bf16 *q = a.q + (int64_t)cc.n * a.q_t + (int64_t)h0 * hd;
-#pragma unroll
-    for (int kk = 0; kk < HD / 16; ++kk)
-#pragma unroll
-      for (int e = 0; e < QR; ++e) {
-        const int h = NH == 16 ? qr + 8 * (e & 1) : qr, d = 16 * kk + qc + 8 * (NH == 16 ? e >> 1 : e);
-        qf[kk][e] = h < nh && d < hd ? *reinterpret_cast<const uint32_t *>(q + h * hd + d) : 0u;
+    if constexpr (S::kQShared) {  // (between two barriers: the one before this, and this one)
+      for (int i = tid; i < NH * (HD / 8); i += kThreads) {
+        const int h = i / (HD / 8), ch = i % (HD / 8);
+        const uint4 x = h < nh && ch * 8 < hd ? *reinterpret_cast<const uint4 *>(q + h * hd + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(smem + S::kQAt + h * (HD * 2) + ((ch ^ (h & 7)) << 4)) = x;
       }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < QR; ++e) {
+          const int h = NH == 16 ? qr + 8 * (e & 1) : qr, d = 16 * kk + qc + 8 * (NH == 16 ? e >> 1 : e);
+          qf[kk][e] = h < nh && d < hd ? *reinterpret_cast<const uint32_t *>(q + h * hd + d) : 0u;
+        }
+    }
 #pragma unroll
     for (int t = 0; t < AT; ++t)
 #pragma unroll
@@ -235,7 +233,12 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       for (int kk = 0; kk < HD / 16; ++kk) {
         uint32_t b[4];
         ldsm4(b, sk + krow * (HD * 2) + (((2 * kk + kch) ^ (krow & 7)) << 4));
-        if constexpr (NH == 16) {
+        if constexpr (S::kQShared) {
+          uint32_t qa[4];
+          ldsm4(qa, tc::smem_u32(smem) + S::kQAt + (lane & 15) * (HD * 2) + (((2 * kk + (lane >> 4)) ^ (lane & 7)) << 4));
+          mma16816(c[0], qa, b[0], b[1]);
+          mma16816(c[1], qa, b[2], b[3]);
+        } else if constexpr (NH == 16) {
           mma16816(c[0], qf[kk], b[0], b[1]);
           mma16816(c[1], qf[kk], b[2], b[3]);
         } else {
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       }
     }
     if (u >= 0 && (cc.t == cc.units - 1 || u + 1 == nunits)) {
-      // ---- the segment's end in this CTA: the four warps' accumulators joined
+      // ---- the segment's end in this CTA: the warps' accumulators joined
       float *mine = reinterpret_cast<float *>(ring_p + stage * S::kStageBytes);
       __syncwarp();
 #pragma unroll
