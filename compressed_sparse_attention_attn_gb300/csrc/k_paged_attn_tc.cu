@@ -594,13 +594,16 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
 }
 
 // Join the shares of the segments that several CTAs worked on: block x a segment (or the CTA that a split segment
-// began in), its heads and 64-feature chunks dealt over the warps of the blocks y.  A share is 128 KB, which the
-// last CTA to finish alone would take tens of microseconds to read; here the whole device reads them.  Shares are
-// added in their order.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinChunk = 64;
+// began in), its heads and 64-feature chunks dealt over the blocks y.  A share is 128 KB, which the last CTA to finish
+// alone would take tens of microseconds to read; here the whole device reads them, 16 lanes a chunk of a share, every
+// load of a group in flight at once.  One group adds up to eight shares of an item, two or four groups the shares of a segment that
+// more CTAs had (up to sixteen: the same within 1 us from 2 to 152 shares).  Shares are added in an order that their number alone
+// sets.  32 segments of 5 to 6 shares (24 MB): 7 us with the launch; the shares' way through L2 bounds it.
+constexpr int kJoinThreads = 256, kJoinChunk = 64, kJoinLanes = kJoinChunk / 4, kJoinGroups = kJoinThreads / kJoinLanes;
+constexpr int kJoinShares = 8, kJoinSplit = 4;
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid_constant__ Params P) {
-  __shared__ float s_f[kJoinThreads / 32][kMaxCtas];
+  __shared__ float4 s_v[kJoinGroups][kJoinLanes];
+  __shared__ float2 s_ml[kJoinGroups];
   const PagedAttnArgs &a = P.a;
   dependency_wait();
   const int2 sp = P.split[blockIdx.x];
@@ -609,58 +612,76 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid
   const int c0 = P.by_segment ? sp.x : (int)blockIdx.x;
   // (after a wait that ran out the notes may be those of another call: nothing outside the workspace is read)
   if (parts <= 1 || c0 < 0 || parts > P.ctas - c0 || n < 0 || n >= a.N) return;
-  auto slot = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
   const int kvh = hg / P.sub, sg = hg - kvh * P.sub, h0 = kvh * P.g + sg * kHeads, nh = min(kHeads, P.g - sg * kHeads);
-  const int hd = a.c.head_dim, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hd = a.c.head_dim, lane = threadIdx.x % kJoinLanes, grp = threadIdx.x / kJoinLanes;
   const int chunks = (hd + kJoinChunk - 1) / kJoinChunk;
-  float *f = s_f[warp];
-  for (int it = blockIdx.y * (kJoinThreads / 32) + warp; it < nh * chunks; it += gridDim.y * (kJoinThreads / 32)) {
-    const int h = it / chunks, d = (it - h * chunks) * kJoinChunk + (lane & 15) * 4;
+  int G = 1;  // groups an item
+  while (G < kJoinSplit && G * kJoinShares < parts) G *= 2;
+  const int sub = grp & (G - 1), per = kJoinGroups / G;
+  for (int it0 = blockIdx.y * per; it0 < nh * chunks; it0 += gridDim.y * per) {
+    const int it = it0 + grp / G, h = it / chunks, d = (it - h * chunks) * kJoinChunk + lane * 4;
+    const bool in = h < nh && d < hd;
     float M = -INFINITY, Lp = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-      const float m = __ldcg(P.share_ml + ((int64_t)slot(p) * kHeads + h) * 2);
-      f[p] = m;
-      M = fmaxf(M, m);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int p = lane; p < parts; p += 32) {
-      const float e = f[p] == -INFINITY ? 0.f : exp2f(f[p] - M);
-      f[p] = e;
-      Lp = fmaf(__ldcg(P.share_ml + ((int64_t)slot(p) * kHeads + h) * 2 + 1), e, Lp);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) Lp += __shfl_xor_sync(0xffffffffu, Lp, o);
-    __syncwarp();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = lane >> 4; p0 < parts; p0 += 8) {  // the half-warps take every other share, four in flight
-      float4 x[4];
+    for (int p0 = sub; p0 < parts && h < nh; p0 += G * kJoinShares) {
+      float4 x[kJoinShares];
+      float2 ml[kJoinShares];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (p0 + 2 * u < parts && d < hd)
-          x[u] = __ldcg(reinterpret_cast<const float4 *>(P.share_o + ((int64_t)slot(p0 + 2 * u) * kHeads + h) * kHD + d));
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (p0 + 2 * u < parts && d < hd) {
-          const float e = f[p0 + 2 * u];
-          v.x = fmaf(x[u].x, e, v.x);
-          v.y = fmaf(x[u].y, e, v.y);
-          v.z = fmaf(x[u].z, e, v.z);
-          v.w = fmaf(x[u].w, e, v.w);
+      for (int u = 0; u < kJoinShares; ++u) {
+        const int p = p0 + u * G;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < parts) {
+          const int64_t r = (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * kHeads + h;
+          ml[u] = __ldcg(reinterpret_cast<const float2 *>(P.share_ml + r * 2));
+          if (in) x[u] = __ldcg(reinterpret_cast<const float4 *>(P.share_o + r * kHD + d));
         }
+      }
+      float mx = M;
+#pragma unroll
+      for (int u = 0; u < kJoinShares; ++u) mx = fmaxf(mx, ml[u].x);
+      const float f0 = M == -INFINITY ? 0.f : exp2f(M - mx);
+      M = mx;
+      Lp *= f0;
+      v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
+#pragma unroll
+      for (int u = 0; u < kJoinShares; ++u) {
+        const float e = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - M);
+        Lp = fmaf(ml[u].y, e, Lp);
+        v.x = fmaf(x[u].x, e, v.x);
+        v.y = fmaf(x[u].y, e, v.y);
+        v.z = fmaf(x[u].z, e, v.z);
+        v.w = fmaf(x[u].w, e, v.w);
+      }
     }
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
-    v.z += __shfl_xor_sync(0xffffffffu, v.z, 16);
-    v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
-    if (lane < 16 && d < hd) {
+    if (G > 1) {  // (uniform over the block)
+      s_v[grp][lane] = v;
+      if (lane == 0) s_ml[grp] = make_float2(M, Lp);
+      __syncthreads();
+      if (sub == 0) {
+        for (int k = 1; k < G; ++k) M = fmaxf(M, s_ml[grp + k].x);
+        Lp = 0.f;
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < G; ++k) {
+          const float2 ml = s_ml[grp + k];
+          const float4 x = s_v[grp + k][lane];
+          const float e = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+          Lp = fmaf(ml.y, e, Lp);
+          v.x = fmaf(x.x, e, v.x);
+          v.y = fmaf(x.y, e, v.y);
+          v.z = fmaf(x.z, e, v.z);
+          v.w = fmaf(x.w, e, v.w);
+        }
+      }
+      __syncthreads();
+    }
+    if (sub == 0 && in) {
       const float fo = out_factor(M, Lp, a.sink, h0 + h);
       const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * fo, v.y * fo), hi = __floats2bfloat162_rn(v.z * fo, v.w * fo);
       *reinterpret_cast<uint2 *>(a.o + (int64_t)n * a.o_t + (int64_t)(h0 + h) * hd + d) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
       if (a.lse && d == 0) a.lse[(int64_t)n * a.H + h0 + h] = Lp == 0.f ? -INFINITY : (M + log2f(Lp)) * 0.6931471805599453f;
     }
-    __syncwarp();
   }
 }
 
@@ -703,8 +724,9 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
   e = tma ? launch_dependent(k_paged_attn_latent<true>, dim3((unsigned)grid), dim3(kThreads<true>), smem, s, 1, p, pg)
           : launch_dependent(k_paged_attn_latent<false>, dim3((unsigned)grid), dim3(kThreads<false>), smem, s, 1, p, pg);
   if (e != cudaSuccess || segments == units) return e;  // (one tile a segment: nothing is shared)
-  // about 600 blocks of the join, and no more than there is work
-  const int64_t x = std::min(segments, grid), y = std::min<int64_t>(std::max<int64_t>(1, 4 * num_sms / x), kHeads);
+  // blocks of the join: one group an item, and four blocks an SM where segments are few and so split over many CTAs
+  const int64_t x = std::min(segments, grid), items = (int64_t)std::min(p.g, kHeads) * ((a.c.head_dim + kJoinChunk - 1) / kJoinChunk);
+  const int64_t y = std::min(items, std::max((items + kJoinGroups - 1) / kJoinGroups, 4 * num_sms / x));
   return launch_dependent(k_paged_join_latent, dim3((unsigned)x, (unsigned)y), dim3(kJoinThreads), 0, s, 1, p);
 }
 
