@@ -97,7 +97,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   __shared__ Range rg;
   dependency_wait();
   const int nunits = find_range<kUnit, kThreads, false>(P, s_scan, rows, rg);
-  if (nunits == 0) return;
+  if (nunits <= 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
   Cursor cl = first_unit(rg, rows), cc = cl;  // of the lookups, of the products

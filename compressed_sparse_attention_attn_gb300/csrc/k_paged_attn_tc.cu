@@ -99,13 +99,6 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
 
   Rows &rows = *reinterpret_cast<Rows *>(smem + L::rows);
   Range &rg = *reinterpret_cast<Range *>(smem + L::range);
-  dependency_wait();
-  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
-  if (nt == 0) {
-    if (tid == 0 && !P.by_segment) P.split[blockIdx.x] = make_int2(0, 0);
-    return;
-  }
-  Cursor c = first_unit(rg, rows);
   if (tid == 0) {
     for (int i = 0; i < kBufs; ++i) {
       tc::mbar_init(&full[i], TMA ? 4 : 64);  // the four warps, or the lanes of the buffer's two
@@ -125,6 +118,17 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
   }
   if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
   tc::tc_fence_before();
+  dependency_wait();
+  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
+  if (nt <= 0) {  // (< 0: more units than can be counted, so that no segment is told of)
+    if (tid == 0 && (nt < 0 || !P.by_segment)) P.split[blockIdx.x] = make_int2(0, 0);
+    if (warp == 8) {
+      tc::tc_fence_after();
+      tc::tmem_dealloc(*tmem_slot, 512);
+    }
+    return;
+  }
+  Cursor c = first_unit(rg, rows);
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kS;  // S: 2 x 64 columns, O^T: 4 x 64

@@ -156,7 +156,7 @@ __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Row
   int64_t incl = scan(mine, sum);
   if (sum * P.Hg > 0x7fffffff) {
     if (report && tid == 0) atomicOr(a.status, kStatusBadIndex);
-    return 0;
+    return -1;
   }
   // no more CTAs than there are units, so that none between two has nothing
   const uint32_t total = (uint32_t)sum * P.Hg, ctas = min(gridDim.x, total);
