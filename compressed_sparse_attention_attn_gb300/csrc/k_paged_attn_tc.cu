@@ -3,23 +3,25 @@
 //
 // Up to 64 query heads share a row of 512 features that is key and value: 4 x 64 x 512 flops for 1 KB, 860
 // TFLOP/s at the card's copy rate, which warp-level products do not reach.  A CTA an SM works through its
-// range of 64-position tiles (paged_common.cuh), the accumulators in tensor memory:
-//   S[h][r] = sum_d q[h][d] K[r][d]       M = 128 lanes (64 heads; the other lanes read what lies behind q and are
-//                                         never looked at), N = 64 positions, K = 512
-//   p = exp2(S scale - m), bf16           a thread a head: the running maximum m and the sum never leave it; m is
-//                                         raised only by more than 2^8 (the sums so far are then rescaled)
-//   O^T[d][h] += sum_r K[r][d] p[h][r]    M = 4 x 128 features, N = 64 heads, K = 64 positions (the same tile read
+// range of 48-position tiles (paged_common.cuh), the accumulators in tensor memory:
+//   S[h][r] = sum_d q[h][d] K[r][d]       M = 64 heads (the first 16 lanes of each quarter), N = 48 positions, K = 512
+//   p = exp2(S scale - m), bf16           a quad of lanes a head: the running maximum m and the sum stay in their registers;
+//                                         m is raised only by more than 2^8 (the sums so far are then rescaled)
+//   O^T[d][h] += sum_r K[r][d] p[h][r]    M = 4 x 128 features, N = 64 heads, K = 48 positions (the same tile read
 //                                         as an MN-major operand)
-// p rounded to bf16 is off by at most 2^-8 of itself, which moves O by at most 2^-8 sum_r w_r |K_rd|; scores,
-// maxima, sums and O are f32.
+// p rounded to bf16 is off by at most 2^-8 of itself, which moves O by at most 2^-8 sum_r w_r |K_rd| (a second
+// term for what the rounding leaves would double the products of the values); scores, maxima, sums and O are f32.
 //
-// Shared memory holds q (64 KB) and two tiles (64 KB each), so that one is in flight while the other is used:
-// 64 KB an SM in flight covers the copy rate's latency twice.  Four warps serve each tile buffer (cp.async
-// from the page of each position, 16 bytes a lane, rows past the end as zeros), and signals it a quarter of the
-// features at a time; one thread issues whichever product is ready first, the next tile's scores or
-// this tile's values, so a buffer is handed back as soon as its weights are there.  Two warps do the softmax, and
-// load the next segment's q behind the last scores that read it; four warps rescale O and write it out.  All
-// waits are time-bounded.
+// Shared memory holds q (64 KB) and three tiles (48 KB each): one whose values are used, one whose scores are, one in flight
+// (two of 64 positions took 217 against 182 us over 64 rows of 12 to 16 thousand).  Tiles come by TMA, boxes of up to 16 rows inside
+// a page, where pages hold whole boxes of 8 rows at least, else by cp.async from the page of each position.  One thread issues
+// whichever product is ready first, the next tile's scores or this tile's values, so a buffer is handed back
+// as soon as its weights are there.  Four warps do the softmax, and load the next segment's q behind the last
+// scores that read it; four rescale O and write it out.  All waits are time-bounded.
+//
+// 64 x 1 over 12 to 16 thousand rows: 176 us, 5.3 TB/s (79 % of a copy); of the 2500 to 2800 cycles of a tile the products take
+// 1300, and the rest is what their hand-overs take: scores to softmax to values.  32 x 1 over about 900 rows (4 to 5 tiles a CTA): 23 us, of
+// which the shares' 128 KB a CTA take 2 us each to write and 7 us to join.
 #include <algorithm>
 #include <cstring>
 
@@ -60,7 +62,7 @@ struct L {
   static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [18]
   static constexpr size_t range = scan + 18 * 8;                             // Range
   static constexpr size_t rows = range + ((sizeof(Range) + 7) & ~7);         // Rows
-  static constexpr size_t bars = rows + ((sizeof(Rows) + 7) & ~7);                            // u64 [16]
+  static constexpr size_t bars = rows + ((sizeof(Rows) + 7) & ~7);           // u64 [16]
   static constexpr size_t misc = bars + 16 * 8;                              // masks [3][2], flags [2][4], slot, abort
   static constexpr size_t total = misc + 96;
 };

@@ -3,16 +3,17 @@
 //
 // A segment is the work of one (row, head group): its positions in units of U rows, at least one (an empty row
 // writes zeros).  The segments' units stand one behind the other (row, head group, unit); of their total T
-// each of G CTAs takes T / G in a row (the first T mod G one more), so every CTA has the same number of rows to read whatever the
-// lengths are (the first T mod G CTAs one unit more), and at most the first and the last segment of its range are shared with others.  The host knows
-// no lengths: every CTA sums the units itself.
+// each of G CTAs takes T / G in a row (the first T mod G CTAs one more), so every CTA has as much to read as any other
+// whatever the lengths are, and at most the first and the last segment of its range are shared with others.  The
+// host knows no lengths: every CTA sums the units itself.
 //
 // A CTA's share of a segment is (M, L, O): its running maximum (base 2), sum of weights and weighted sum of
 // values relative to M, in f32, in one of its two slots (0: a segment that began in an earlier CTA, 1: one
-// that begins here).  Twelve consecutive shares of a segment are a group.  The CTA that completes a group
-// joins it (in the order of the shares, whoever is last); with more than one group the joined shares go to
-// the group's first slot, and the CTA that completes the last group joins those.  So a long row over 300
-// CTAs is joined in two steps, of 12 and of 26 shares, and nothing waits.  The counters return to zero.
+// that begins here).  Up to 256 features, twelve consecutive shares of a segment are a group.  The CTA that completes a
+// group joins it (in the order of the shares, whoever is last); with more than one group the joined shares go
+// to the group's first slot, and the CTA that completes the last group joins those.  So a long row over 300
+// CTAs is joined in two steps, of 12 and of 26 shares, and nothing waits.  The counters return to zero.  Shares of latent
+// rows, 128 KB each, are joined by a second kernel (k_paged_attn_tc.cu).
 #pragma once
 
 #include "csa_internal.cuh"

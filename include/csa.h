@@ -426,8 +426,10 @@ CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64
  * head_dim <= 256 with separate or shared values, or up to 512 with cache->v NULL.  A req >= R (its row is
  * left as it was), a pos past width pages (the rows past them are left out) and a page id outside
  * [0, n_pages) (its rows are left out) are caller errors, recorded in the context's status word.
- * Rows of different length are dealt evenly over the device and joined within the one launch, in a fixed
- * order (the same inputs give the same bits); the shares lie in the context's workspace. */
+ * Rows of different length are dealt evenly over the device and joined in a fixed order (the same inputs give
+ * the same bits), for head_dim <= 256 within the one launch, above by a second one; the shares lie in the
+ * context's workspace.  Rows that come to more than 2^31 units (of 16 to 96 positions of a head group) are a caller
+ * error too: the call then writes nothing. */
 CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
                            const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos,
                            const float *sink, float scale, int window, csa_bf16 *o, int64_t o_t, float *lse,
