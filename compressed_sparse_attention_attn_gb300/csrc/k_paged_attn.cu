@@ -25,6 +25,7 @@ namespace csa {
 namespace paged {
 
 constexpr int kTile = 16;  // positions of a warp's tile
+constexpr int kEnd = 1;    // units that the end of a segment counts for (2 to 4 thousand cycles, as one unit takes)
 
 // Warps and ring stages are set so that the rings fill an SM's shared memory and 64 to 128 KB are in flight: 4 x 3 x 4 KB
 // x 4 (or 3) CTAs at 64 features, 4 x 2 x 8 KB x 3 (x 3 x 8 KB x 2 where 16 heads' accumulators need the
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   using S = Shape<HD, NH>;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kUnit = S::kUnit, kHeads = NH;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[kWarps + 1];
+  __shared__ int64_t s_scan[2 * kWarps];
   __shared__ float s_ml[2][kWarps][kHeads];
   __shared__ float s_f[kWarps][kHeads];
   __shared__ float s_out[kHeads];
@@ -96,11 +97,11 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   __shared__ Rows rows;
   __shared__ Range rg;
   dependency_wait();
-  const int nunits = find_range<kUnit, kThreads, false>(P, s_scan, rows, rg);
+  const int nunits = find_range<kUnit, kThreads, false, kEnd>(P, s_scan, rows, rg);
   if (nunits <= 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
-  Cursor cl = first_unit(rg, rows), cc = cl;  // of the lookups, of the products
+  Cursor cl = first_unit<kUnit, false, kEnd>(a, P.Hg, rg, rows), cc = cl;  // of the lookups, of the products
   const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
   const bf16 *vbase = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) : kbase;
   const int64_t v_page = a.c.v ? a.c.v_page : a.c.k_page, v_row = a.c.v ? a.c.v_row : a.c.k_row,
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       }
       --todo;
       const int hg0 = cl.hg, n0 = cl.n;
-      advance<kUnit, false>(a, P.Hg, rows, cl);
+      advance<kUnit, false, kEnd>(a, P.Hg, rows, cl);
       if (warp == 0 && todo > 0 && (cl.hg != hg0 || cl.n != n0)) {  // the next segment's q on its way to L1
         const int kv2 = cl.hg / P.sub, sg = cl.hg - kv2 * P.sub, nq = min(NH, P.g - sg * NH);
         const bf16 *q = a.q + (int64_t)cl.n * a.q_t + (int64_t)(kv2 * P.g + sg * NH) * hd;
@@ -393,9 +394,9 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
         }
       }
       __syncthreads();  // the stage may be refilled
-      if (!whole) publish<kHeads, HD, kThreads>(P, rg.begin + sb, rg.begin + se, rg, cc.n, h0, nh, &s_flag);
+      if (!whole) publish<kHeads, HD, kThreads>(P, cc.base, cc.base + cc.units, rg, cc.n, h0, nh, &s_flag);
       if (u + 1 < nunits) {
-        advance<kUnit, false>(a, P.Hg, rows, cc);
+        advance<kUnit, false, kEnd>(a, P.Hg, rows, cc);
         seg = u + 1;
         begin_segment();
       }

@@ -40,6 +40,7 @@ namespace latent {
 constexpr int kHD = 512;
 constexpr int kHeads = 64;              // query heads of a head group
 constexpr int kUnit = 48;               // positions of a tile
+constexpr int kEnd = 1;                 // tiles that the end of a segment counts for
 constexpr int kJ = kUnit / 8;
 constexpr int kBufs = 3;                // tile buffers
 constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile
@@ -59,8 +60,8 @@ struct L {
   static constexpr size_t p = t + (size_t)kBufs * kBlocks * kBlock;          // [2][64][128 B]
   static constexpr size_t alpha = p + (size_t)2 * kHeads * 128;              // float [2][64]
   static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
-  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [18]
-  static constexpr size_t range = scan + 18 * 8;                             // Range
+  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [32]
+  static constexpr size_t range = scan + 32 * 8;                             // Range
   static constexpr size_t rows = range + ((sizeof(Range) + 7) & ~7);         // Rows
   static constexpr size_t bars = rows + ((sizeof(Rows) + 7) & ~7);           // u64 [16]
   static constexpr size_t misc = bars + 16 * 8;                              // masks [3][2], flags [2][4], slot, abort
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
   if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
   tc::tc_fence_before();
   dependency_wait();
-  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
+  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN, kEnd>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
   if (nt <= 0) {  // (< 0: more units than can be counted, so that no segment is told of)
     if (tid == 0 && (nt < 0 || !P.by_segment)) P.split[blockIdx.x] = make_int2(0, 0);
     if (warp == 8) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     }
     return;
   }
-  Cursor c = first_unit(rg, rows);
+  Cursor c = first_unit<kUnit, ALIGN, kEnd>(a, P.Hg, rg, rows);
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot, tO = tmem + 2 * kS;  // S: 2 x 64 columns, O^T: 4 x 64
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       Cursor nx = c;
       if (last && i + 1 < nt) {  // q's last reader is done: the next segment's q on its way
         nx.t = nx.units - 1;
-        advance<kUnit, ALIGN>(a, P.Hg, rows, nx);
+        advance<kUnit, ALIGN, kEnd>(a, P.Hg, rows, nx);
         load_q(nx);
       }
       float s[4 * kJ];  // s[4 j + 2 x + e]: position 8 j + qc + e of head x
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       }
       tc::tc_fence_before();
       if (seg == sb && jt == 0) {  // (the segment begins here)
-        const int parts = whole ? 0 : cta_of(se + rg.begin - 1, rg) - (int)blockIdx.x + 1;
+        const int parts = whole ? 0 : cta_of(c.base + c.units - 1, rg) - (int)blockIdx.x + 1;
         if (P.by_segment) {
           P.split[(int64_t)c.n * P.Hg + c.hg] = make_int2(blockIdx.x, parts);
         } else if (!whole) {
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       ++nseg;
       seg = i + 1;
       c.t = c.units - 1;
-      if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+      if (i + 1 < nt) advance<kUnit, ALIGN, kEnd>(a, P.Hg, rows, c);
     }
     if (!P.by_segment && jt == 0 && !told) P.split[blockIdx.x] = make_int2(0, 0);
   } else if (warp == 8) {
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         first = last;
         if (last) {
           c.t = c.units - 1;
-          if (i + 1 < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+          if (i + 1 < nt) advance<kUnit, ALIGN, kEnd>(a, P.Hg, rows, c);
         } else {
           ++c.t;
         }
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         constexpr int kH = kUnit / 2;
         x.m0 = __ballot_sync(0xffffffffu, lane < kH && lane >= lo && lane < hi && ((x.boxes >> (lane >> r_log)) & 1u));
         x.m1 = __ballot_sync(0xffffffffu, lane < kH && lane + kH >= lo && lane + kH < hi && ((x.boxes >> ((lane + kH) >> r_log)) & 1u));
-        if (++looked < nt) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+        if (++looked < nt) advance<kUnit, ALIGN, kEnd>(a, P.Hg, rows, c);
       }
       return x;
     };
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
     const int cc = lane & 7;
     constexpr int kH = kUnit / 2;
-    for (int k = 0; k < b && k + 1 < nt; ++k) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+    for (int k = 0; k < b && k + 1 < nt; ++k) advance<kUnit, ALIGN, kEnd>(a, P.Hg, rows, c);
     uint32_t ph = 1;
     for (int i = b; i < nt; i += kBufs, ph ^= 1u) {
       const Row row = rows.get<kUnit, ALIGN>(a, c.n);
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       attn::cp_async_wait_all();
       attn::fence_proxy_async();
       tc::mbar_arrive(&full[b]);
-      for (int k = 1; k <= kBufs && i + k < nt; ++k) advance<kUnit, ALIGN>(a, P.Hg, rows, c);
+      for (int k = 1; k <= kBufs && i + k < nt; ++k) advance<kUnit, ALIGN, kEnd>(a, P.Hg, rows, c);
     }
     attn::cp_async_wait_all();
   }
