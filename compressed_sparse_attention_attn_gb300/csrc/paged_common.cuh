@@ -139,9 +139,11 @@ __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Row
   struct Two {
     int64_t units, segs;
   };
+  Row last{0, 0, 0, 0, 0};  // the row a thread has read last
   auto of_row = [&](int n, bool rep) -> Two {
-    const int u = n < a.N ? row_of<U, ALIGN>(a, n, rep).units : 0;
-    return {u, u > 0 ? 1 : 0};
+    if (n >= a.N) return {0, 0};
+    last = row_of<U, ALIGN>(a, n, rep);
+    return {last.units, last.units > 0 ? 1 : 0};
   };
   auto scan = [&](Two v, Two &sum) -> Two {  // inclusive over the CTA; sum: of all
 #pragma unroll
@@ -205,11 +207,12 @@ __device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Row
     if (end <= places(base)) break;
   }
   __syncthreads();
-  if (tid < kRowsKept) {
-    const int n = out.row + tid;
-    const Row none{0, 0, 0, 0, 0};
-    if (tid == 0) rows.n0 = n;
-    rows.row[tid] = n < a.N ? row_of<U, ALIGN>(a, n, false) : none;
+  if (tid == 0) rows.n0 = out.row;
+  if (a.N <= NT) {  // (a thread has its row still; entries past the last row are never read)
+    const unsigned i = (unsigned)(tid - out.row);
+    if (i < (unsigned)kRowsKept) rows.row[i] = last;
+  } else if (tid < kRowsKept && out.row + tid < a.N) {
+    rows.row[tid] = row_of<U, ALIGN>(a, out.row + tid, false);
   }
   __syncthreads();
   return (int)(out.u1 - out.u0);
