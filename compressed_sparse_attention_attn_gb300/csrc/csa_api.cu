@@ -590,15 +590,30 @@ static int check_paged(const csa_paged *c, const char *who) {
   return CSA_OK;
 }
 
+// Rows of `inner` elements at all index combinations of up to three (count, stride) lie apart (each stride passes over all
+// that the smaller ones span), as rows that are written have to.
+static bool rows_apart(int64_t inner, std::initializer_list<std::pair<int64_t, int64_t>> dims) {
+  std::pair<int64_t, int64_t> d[3];
+  int n = 0;
+  for (const auto &x : dims)
+    if (x.first > 1) d[n++] = {x.second, x.first};
+  std::sort(d, d + n);
+  for (int i = 0; i < n; ++i) {
+    if (d[i].first < inner) return false;
+    inner += d[i].first * (d[i].second - 1);
+  }
+  return true;
+}
+
 int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, const csa_bf16 *k, int64_t k_t,
                      int64_t k_h, const csa_bf16 *v, int64_t v_t, int64_t v_h, int N, int H, const csa_paged *cache,
                      const int32_t *pos, const int32_t *slot, const float *q_norm, const float *k_norm, float eps,
                      const float *tab, int tab_rows, int rd, int at, int half, csa_bf16 *q_out, int64_t o_t,
                      int64_t o_h, csa_stream stream) {
   const char *who = "csa_qk_norm_rope";
-  if (!ctx || !k || !pos || (q && !q_out)) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
+  if (!ctx || (N > 0 && (!k || !pos || (q && !q_out)))) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
   if (int rc = check_paged(cache, who)) return rc;
-  if (cache->v && !v) return fail(CSA_ERR_ARG, "%s: the cache holds values, v is NULL", who);
+  if (N > 0 && cache->v && !v) return fail(CSA_ERR_ARG, "%s: the cache holds values, v is NULL", who);
   const int hd = cache->head_dim;
   if (N < 0 || (q && H <= 0) || hd > 1024) return fail(CSA_ERR_ARG, "%s: N %d, H %d, head_dim %d (<= 1024)", who, N, H, hd);
   if ((int64_t)N * ((q ? H : 0) + (int64_t)cache->kv_heads * (cache->v ? 2 : 1)) > 0x7fffffff)
@@ -612,6 +627,10 @@ int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, 
   const int64_t st[] = {q ? q_t : 0, q ? q_h : 0, k_t, k_h, cache->v ? v_t : 0, cache->v ? v_h : 0, q ? o_t : 0, q ? o_h : 0};
   for (int64_t x : st)
     if (x < 0 || x % 8) return fail(CSA_ERR_ARG, "%s: strides must be non-negative multiples of 8 elements", who);
+  if (!rows_apart(hd, {{cache->n_pages, cache->k_page}, {cache->page, cache->k_row}, {cache->kv_heads, cache->k_head}}) ||
+      (cache->v && !rows_apart(hd, {{cache->n_pages, cache->v_page}, {cache->page, cache->v_row}, {cache->kv_heads, cache->v_head}})))
+    return fail(CSA_ERR_ARG, "%s: rows of the cache overlap", who);
+  if (q && !rows_apart(hd, {{N, o_t}, {H, o_h}})) return fail(CSA_ERR_ARG, "%s: rows of q_out overlap", who);
   if (!slot && N > (int64_t)cache->n_pages * cache->page)
     return fail(CSA_ERR_SHAPE, "%s: %d tokens and no slots, %d rows", who, N, cache->n_pages * cache->page);
   if (int rc = check_device(ctx, who)) return rc;
@@ -627,7 +646,7 @@ int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, c
                    const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos, const float *sink,
                    float scale, int window, csa_bf16 *o, int64_t o_t, float *lse, csa_stream stream) {
   const char *who = "csa_paged_attn";
-  if (!ctx || !q || !table || !pos || !o) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
+  if (!ctx || !table || (N > 0 && (!q || !pos || !o))) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
   if (int rc = check_paged(cache, who)) return rc;
   const int hd = cache->head_dim;
   if (N < 0 || H <= 0 || H % cache->kv_heads || H > 65535 || R <= 0 || width <= 0 || window < 0 ||

@@ -406,7 +406,8 @@ CSA_API int csa_page_step(const int32_t *new_len, int R, int page, const int32_t
  * multiples of 8, 16-byte aligned bases); q_out likewise, it may be q itself.  pos, slot int32 [N].
  * A token with pos < 0 is padding: nothing of it is written.  slot -1: only its query is produced.
  * cache->v NULL: v is not read (may be NULL).  q NULL: keys and values only.  slot NULL: token n goes to row
- * n.  No two tokens may have the same slot, and k, v may not overlap the cache.
+ * n.  No two tokens may have the same slot, k, v may not overlap the cache, and rows that are written (of the
+ * cache, of q_out) not one another.  N 0: nothing to do, the tokens' pointers may be NULL.
  * A pos >= tab_rows or a slot outside [-1, n_pages * page) is a caller error: the token is skipped and
  * recorded in the context's status word (csa_status).  head_dim <= 1024, at even. */
 CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64_t q_h, const csa_bf16 *k, int64_t k_t,
@@ -421,7 +422,8 @@ CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64
  * sum_j e^{S_j}) (sink NULL: without that term), lse = ln sum_j e^{S_j} (without the sink); scores, maxima and
  * sums in f32, O rounded once to bf16.  pos -1: no rows, O = 0 and lse = -inf.  A row with pos < -1 or
  * req < 0 is padding: nothing of it is written.
- * q, o bf16 [N][H][head_dim] with a stride per token (elements, multiples of 8; heads follow one another);
+ * q, o bf16 [N][H][head_dim] with a stride per token (elements, multiples of 8; heads follow one another); o
+ * may be q itself (same stride).  N 0: nothing to do, the rows' pointers may be NULL.
  * table int32 [R][width] of page ids; lse f32 [N][H] or NULL; sink f32 [H] or NULL.
  * head_dim <= 256 with separate or shared values, or up to 512 with cache->v NULL.  A req >= R (its row is
  * left as it was), a pos past width pages (the rows past them are left out) and a page id outside

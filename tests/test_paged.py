@@ -555,6 +555,101 @@ def test_paged_attn_streams_and_contexts(csa, ctx, H, kv, hd, latent):
     other.close()
 
 
+@pytest.mark.parametrize("H,kv,hd,page,order,window,pad", [
+    (16, 2, 512, 24, "nhd", 0, 0), (32, 2, 512, 8, "hnd", 50, 0), (8, 4, 384, 48, "hnd", 100, 8), (64, 1, 512, 128, "nhd", 300, 0),
+    (64, 1, 512, 4, "nhd", 0, 0), (9, 3, 288, 12, "nhd", 33, 8), (200, 1, 512, 40, "hnd", 0, 24), (65, 1, 448, 96, "nhd", 1, 64)])
+def test_paged_attn_latent_pages(csa, ctx, H, kv, hd, page, order, window, pad):
+    """Latent rows in pages of many sizes, several kv heads, windows that begin inside a tile, rows that lie apart."""
+    lens = [1, 0, 47, 48, 49, 95, 96, 97, 300, 1000]
+    b = Batch(lens, H, kv, hd, page, True, order, seed=hd + page)
+    if pad:  # a cache with room between its rows
+        wide = torch.full(b.k.shape[:3] + (hd + pad,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        k = wide[..., 8:8 + hd] if pad > 8 else wide[..., :hd]
+        k.copy_(b.k)
+    else:
+        k = b.k
+    pos = [x - 1 for x in lens]
+    q = b.queries(len(lens))
+    sink = torch.randn(H, generator=b.g, device="cuda")
+    o, lse = ctx.paged_attn(q, csa.PagedCache(k), b.table, i32(pos), b.scale, sink=sink, window=window, with_lse=True)
+    check_rows(b, q, o, lse, pos, None, sink, window)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd,latent", [(8, 2, 128, False), (4, 4, 256, False), (32, 2, 256, False), (6, 3, 64, False),
+                                            (64, 1, 512, True), (66, 1, 264, True)])
+@pytest.mark.parametrize("seed", range(4))
+def test_paged_attn_uneven_rows(csa, ctx, H, kv, hd, latent, seed):
+    """Few long rows among many short, empty and padding ones, in any order."""
+    rng = np.random.default_rng(100 * hd + seed)
+    lens = [int(rng.choice([0, 1, 3, 16, 33, 97, 200])) for _ in range(int(rng.integers(3, 60)))]
+    for _ in range(int(rng.integers(1, 4))):
+        lens.insert(int(rng.integers(0, len(lens) + 1)), int(rng.integers(500, 9000)))
+    b = Batch(lens, H, kv, hd, int(rng.choice([5, 16, 64])), latent, seed=seed)
+    N = len(lens)
+    pos = [x - 1 if rng.random() > 0.2 else -2 for x in lens]
+    q = b.queries(N)
+    out = torch.full((N, H, hd), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, H), 3.0, device="cuda")
+    ctx.paged_attn(q, csa.PagedCache(b.k, b.v), b.table, i32(pos), b.scale, out=out, lse=lse)
+    live = [n for n in range(N) if pos[n] >= -1]
+    check_rows(b, q[live], out[live], lse[live], [pos[n] for n in live], live)
+    for n in set(range(N)) - set(live):
+        assert (out[n] == 3).all() and (lse[n] == 3).all()
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd,latent", [(8, 2, 128, False), (20, 1, 256, False), (64, 1, 512, True)])
+def test_paged_attn_replayed_and_in_place(csa, ctx, H, kv, hd, latent):
+    """Two captured graphs of one context replayed by turns while positions change, and the result over q itself."""
+    lens = [3000, 1, 0, 700, 64]
+    b = Batch(lens, H, kv, hd, 16, latent, seed=5)
+    q = b.queries(len(lens))
+    cache = csa.PagedCache(b.k, b.v)
+    p1, p2 = i32([x - 1 for x in lens]), i32([-1, 0, -2, 5, 63])
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    graphs = []
+    for p, o in zip((p1, p2), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ctx.paged_attn(q, cache, b.table, p, b.scale, out=o)
+        graphs.append(g)
+    for step in range(4):
+        if step == 2:
+            p1.copy_(i32([1500, 0, -1, 699, 2]))
+        want = []
+        for p, o in zip((p1, p2), outs):
+            o.zero_()
+            want.append(ctx.paged_attn(q, cache, b.table, p, b.scale, out=torch.zeros_like(q)))
+        for g in graphs:
+            g.replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    pos = [x - 1 for x in lens]
+    want, lse = ctx.paged_attn(q, cache, b.table, i32(pos), b.scale, with_lse=True)
+    check_rows(b, q, want, lse, pos)
+    mine = q.clone()
+    got = ctx.paged_attn(mine, cache, b.table, i32(pos), b.scale, out=mine)
+    assert got is mine and torch.equal(mine, want)
+    assert ctx.status() == 0
+
+
+def test_empty_batches(csa, ctx):
+    """No tokens: nothing happens, whatever an empty tensor's pointer is."""
+    b = Batch([40], 8, 2, 64, 16)
+    cache = csa.PagedCache(b.k, b.v)
+    none = i32([])
+    e = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = ctx.paged_attn(e, cache, b.table, none, 0.1, req=none, with_lse=True)
+    assert o.shape == (0, 8, 64) and lse.shape == (0, 8)
+    kv = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    k0 = b.k.clone()
+    assert ctx.qk_norm_rope(e, kv, kv, cache, none, none, tab=rope_tab(8, 64), rd=64).shape == (0, 8, 64)
+    assert torch.equal(k0.nan_to_num(7.0), b.k.nan_to_num(7.0))
+    length, state = i32([5]), i32([0, 2])
+    info = csa.page_step(i32([0]), length, b.table, i32([1, 2]), state, 16, none, none, none)
+    assert info.tolist() == [0, 0, 0, 0] and length.tolist() == [5] and ctx.status() == 0
+
+
 # ------------------------------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("latent", [False, True])

@@ -78,6 +78,18 @@ def test_paged_attn_refuses(L, change, code):
     assert b"csa_paged_attn" in L.attn_v41_last_error()
 
 
+@pytest.mark.parametrize("change", [
+    dict(o_t=0), dict(o_h=0), dict(o_h=56), dict(o_t=248), dict(o_t=64), dict(cache=dict(k_head=0)), dict(cache=dict(v_head=0)),
+    dict(cache=dict(k_row=64)), dict(cache=dict(k_page=1024)), dict(cache=dict(v_page=2040)),
+    dict(cache=dict(k_row=64, k_head=960, k_page=2048))])
+def test_qk_norm_rope_refuses_rows_that_overlap(L, change):
+    a = {**NORM, **change}
+    c = paged(**a["cache"])
+    a["cache"] = ctypes.byref(c)
+    assert L.csa_qk_norm_rope(*a.values()) == -1
+    assert b"overlap" in L.attn_v41_last_error()
+
+
 def test_the_binding_refuses_what_is_not_on_the_gpu():
     t = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
