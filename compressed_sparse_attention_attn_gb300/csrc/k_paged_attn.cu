@@ -15,6 +15,9 @@
 // weights enter the second product as two bf16 terms (their sum carries 16 bits), so the only rounding that
 // counts is the result's.  At the end of a segment each warp leaves its accumulators in the stage it has
 // just read (exactly as large: 16 rows of keys and values in bf16 are 16 heads of f32), and the CTA joins them.  How CTAs share the rows: paged_common.cuh.
+//
+// Bound by HBM: 4 rows of 50 to 65 thousand (64 heads over 8 of 128) 150 us, 94 % of a copy; 32 rows of 300 to 4000 (32 over 8 of
+// 128) 37 us, 77 %; 48 windows of up to 1000 (16 of 256) 53 us, 79 %: what is left is the start and the segments' ends.
 #include <algorithm>
 #include <cstring>
 
