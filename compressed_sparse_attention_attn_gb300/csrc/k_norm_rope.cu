@@ -4,12 +4,12 @@
 //   y = x r w,  r = 1 / sqrt(mean(x^2) + eps);  (y_a, y_b) -> (y_a c - y_b s, y_a s + y_b c) over the pairs
 // of the turned part, everything in f32, one rounding to bf16 at the store (a normed value rounded before its
 // turn would add a second error of the same size).  A group of 2 to 32
-// lanes holds a row, its angles and weights come from L1 (all rows of a token, and all tokens, share them).
+// lanes holds two rows, whose angles and weights come from L1 (all rows of a token, and all tokens, share them).
 //
-// Bound by HBM: a row is read and written once (4096 tokens of 64 x 512 and one 512-wide key row, 546 MB: 96 us, 5.7
-// TB/s; 8000 tokens of 32 + 8 + 8 heads of 128, 201 MB: 42 us, 4.8 TB/s).  The instructions come close to it at 64 to
-// 128 features, so the arithmetic is on pairs of f32 and a lane holds both vectors of a pair of halves: nothing is
-// read twice, and only the sum of squares crosses lanes.
+// Bound by HBM: a row is read and written once (4096 tokens of 64 x 512 and one 512-wide key row, 546 MB: 89 us, 6.2
+// TB/s; 8000 tokens of 32 + 8 + 8 heads of 128, 201 MB: 39 us, 5.2 TB/s, with halves 42 us).  The instructions and L1 come close to
+// it at 64 to 128 features, so the arithmetic is on pairs of f32 and a lane holds both vectors of a pair of halves:
+// nothing is read twice, and only the sum of squares crosses lanes.
 #include <algorithm>
 
 #include "csa_internal.cuh"
@@ -19,6 +19,10 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
+// CTAs an SM: of two rows of two vectors a group (4 against 3 with adjacent pairs, 4096 x 64 x 512: 89 against 100 us; 3 against 2
+// with halves, 8000 tokens of 48 x 128: 42 against 52; one more spills)
+template <int V, bool HALF>
+constexpr int kResident = V > 2 ? 1 : HALF ? 3 : 4;
 
 // ---- two f32 at a time ----
 struct f2 {
@@ -58,28 +62,32 @@ __device__ __forceinline__ uint32_t pack2(f2 a) {
 // What the two kernels share: the row a group of lanes works on, and whether it is written.
 struct Item {
   bool in, live, plain;  // plain: a value row, copied
-  int n, pos;
+  int n, pos, rows;      // rows: heads of the item
   const bf16 *x;
   bf16 *y;
   const float *w;
+  int64_t x_h, y_h;      // to the next of its heads
 };
-struct Grid {  // items are (token, head), a token's query, key and value heads in a row
-  int items;
+struct Grid {  // items are (token, `each` heads of one kind), a token's query, key and value heads in a row
+  int items, nq, nk;       // nq, nk: items of a token's queries, of its keys
   paged::FastDiv per_token, page;
 };
+template <int R>
 __device__ __forceinline__ int find_item(const NormRopeArgs &a, const Grid &g, int64_t i, Item &t) {
   t.in = i < g.items;
   const int item = t.in ? (int)i : 0;
   t.n = (int)g.per_token.div((uint32_t)item);
   const int h = item - t.n * (int)g.per_token.d;
-  const int kind = h < a.H ? 0 : (h < a.H + a.c.kv_heads ? 1 : 2);
-  const int hh = kind == 0 ? h : (kind == 1 ? h - a.H : h - a.H - a.c.kv_heads);
+  const int kind = h < g.nq ? 0 : (h < g.nq + g.nk ? 1 : 2);
+  const int hh = R * (kind == 0 ? h : (kind == 1 ? h - g.nq : h - g.nq - g.nk));
   t.plain = kind == 2;
-  t.x = kind == 0 ? a.q + t.n * a.q_t + hh * a.q_h
-                  : (kind == 1 ? a.k + t.n * a.k_t + hh * a.k_h : a.v + t.n * a.v_t + hh * a.v_h);
+  t.rows = min(R, (kind == 0 ? a.H : a.c.kv_heads) - hh);
+  t.x_h = kind == 0 ? a.q_h : (kind == 1 ? a.k_h : a.v_h);
+  t.x = (kind == 0 ? a.q + t.n * a.q_t : (kind == 1 ? a.k + t.n * a.k_t : a.v + t.n * a.v_t)) + hh * t.x_h;
   t.w = kind == 0 ? a.q_norm : (kind == 1 ? a.k_norm : nullptr);
   return h;
 }
+template <int R>
 __device__ __forceinline__ void find_place(const NormRopeArgs &a, const Grid &g, int h, int lane, Item &t) {
   t.pos = a.pos[t.n];
   const int slot = a.slot ? a.slot[t.n] : t.n;
@@ -88,14 +96,16 @@ __device__ __forceinline__ void find_place(const NormRopeArgs &a, const Grid &g,
     if (h == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
     t.live = false;
   }
-  if (h < a.H) {
-    t.y = a.q_out + t.n * a.o_t + h * a.o_h;
+  if (h < g.nq) {
+    t.y_h = a.o_h;
+    t.y = a.q_out + t.n * a.o_t + R * h * a.o_h;
   } else {
     if (slot < 0) t.live = false;
     const int pg = t.live ? (int)g.page.div((uint32_t)slot) : 0, row = t.live ? slot - pg * a.c.page : 0;
-    const int hk = h - a.H;
-    t.y = t.plain ? reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row + (hk - a.c.kv_heads) * a.c.v_head
-                  : reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row + hk * a.c.k_head;
+    const int hk = R * (h - g.nq - (t.plain ? g.nk : 0));
+    t.y_h = t.plain ? a.c.v_head : a.c.k_head;
+    t.y = (t.plain ? reinterpret_cast<bf16 *>(a.c.v) + pg * a.c.v_page + row * a.c.v_row
+                   : reinterpret_cast<bf16 *>(a.c.k) + pg * a.c.k_page + row * a.c.k_row) + hk * t.y_h;
   }
 }
 
@@ -110,19 +120,21 @@ __device__ __forceinline__ void load8(const float *w, f2 (&v)[4]) {
 
 // G lanes a row, V (even) vectors of 8 features a lane, head_dim <= 8 G V a multiple of 16; the turned part and its halves
 // start and end on vector borders.  Adjacent pairs lie inside a vector; with HALF vectors u and u + 1 (u even) of a lane are
-// partners, rd / 2 features apart, or lie both outside the turned part.  A row a group and no loop: what hides the
-// latency is many resident warps (five or six CTAs an SM), each with its row in flight; keeping a token's
-// weights and angles in registers over several rows needed 80 to 128 of them and took 113 against 96 us.
-template <int G, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads, V == 2 ? (HALF ? 5 : 6) : 1) k_norm_rope(const __grid_constant__ NormRopeArgs a,
-                                                                                    const __grid_constant__ Grid g) {
+// partners, rd / 2 features apart, or lie both outside the turned part.  R rows a group and no loop: what hides the
+// latency is many resident warps, each with its rows in flight.  Two heads of a token take each weight and angle
+// once (with one row they are twice the row's own bytes on their way from L1; 4096 x 64 x 512: 97 us, 8000 tokens of 48
+// x 128 42.6 against 38.8 with adjacent pairs, 46.1 against 42.1 with halves); more rows, looped over with weights
+// and angles in registers, needed 80 to 128 of them and took 113 us.
+template <int G, int V, bool HALF, int R>
+__global__ void __launch_bounds__(kThreads, kResident<V, HALF>) k_norm_rope(const __grid_constant__ NormRopeArgs a,
+                                                                                const __grid_constant__ Grid g) {
   const int lane = threadIdx.x & (G - 1);
   const int hd = a.c.head_dim, h2 = a.rd >> 1;
   Item t;
-  const int h = find_item(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
+  const int h = find_item<R>(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
   dependency_wait();
   int f[V];  // first feature of this lane's vectors (hd: none)
-  uint4 x[V];
+  uint4 x[R][V];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     if (HALF) {
@@ -136,37 +148,52 @@ __global__ void __launch_bounds__(kThreads, V == 2 ? (HALF ? 5 : 6) : 1) k_norm_
     } else {
       f[u] = 8 * (lane + G * u);
     }
-    x[u] = make_uint4(0, 0, 0, 0);
-    if (f[u] < hd) x[u] = *reinterpret_cast<const uint4 *>(t.x + f[u]);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      x[i][u] = make_uint4(0, 0, 0, 0);
+      if (f[u] < hd && i < t.rows) x[i][u] = *reinterpret_cast<const uint4 *>(t.x + i * t.x_h + f[u]);
+    }
   }
-  find_place(a, g, h, lane, t);
-  f2 v[V][4], q[2] = {{0.f, 0.f}, {0.f, 0.f}};
+  find_place<R>(a, g, h, lane, t);
+  f2 v[R][V][4];
+  float r[R];
 #pragma unroll
-  for (int u = 0; u < V; ++u) {
-    unpack(x[u], v[u]);
+  for (int i = 0; i < R; ++i) {
+    f2 q[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e & 1] = fma2(v[u][e], v[u][e], q[e & 1]);
+    for (int u = 0; u < V; ++u) {
+      unpack(x[i][u], v[i][u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e & 1] = fma2(v[i][u][e], v[i][u][e], q[e & 1]);
+    }
+    r[i] = (q[0].x + q[0].y) + (q[1].x + q[1].y);
   }
-  float r = (q[0].x + q[0].y) + (q[1].x + q[1].y);
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < R; ++i) r[i] += __shfl_xor_sync(0xffffffffu, r[i], o);
   if (!t.live) return;
   if (t.plain) {
 #pragma unroll
-    for (int u = 0; u < V; ++u)
-      if (f[u] < hd) *reinterpret_cast<uint4 *>(t.y + f[u]) = x[u];
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int u = 0; u < V; ++u)
+        if (f[u] < hd && i < t.rows) *reinterpret_cast<uint4 *>(t.y + i * t.y_h + f[u]) = x[i][u];
     return;
   }
   if (t.w) {
-    r = rsqrtf(r / (float)hd + a.eps);  // (within 2 units of the last place: 2^-22, far below the result's 2^-8)
-    const f2 rr = {r, r};
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      r[i] = rsqrtf(r[i] / (float)hd + a.eps);  // (within 2 units of the last place: 2^-22, far below the result's 2^-8)
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       if (f[u] >= hd) continue;
       f2 w[4];
       load8(t.w + f[u], w);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[u][e] = mul2(mul2(v[u][e], rr), w[e]);
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][u][e] = mul2(mul2(v[i][u][e], f2{r[i], r[i]}), w[e]);
     }
   }
   const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)t.pos * h2;
@@ -178,24 +205,35 @@ __global__ void __launch_bounds__(kThreads, V == 2 ? (HALF ? 5 : 6) : 1) k_norm_
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 cs = __ldg(ap + e);
-        const f2 c = {cs.x, cs.z}, s = {cs.y, cs.w}, m = {-cs.y, -cs.w}, lo = v[u][e], hi = v[u + 1][e];
-        v[u][e] = fma2(hi, m, mul2(lo, c));
-        v[u + 1][e] = fma2(lo, s, mul2(hi, c));
+        const f2 c = {cs.x, cs.z}, s = {cs.y, cs.w}, m = {-cs.y, -cs.w};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const f2 lo = v[i][u][e], hi = v[i][u + 1][e];
+          v[i][u][e] = fma2(hi, m, mul2(lo, c));
+          v[i][u + 1][e] = fma2(lo, s, mul2(hi, c));
+        }
       }
     } else {
       const float4 *ap = reinterpret_cast<const float4 *>(tp + ((f[u] - a.at) >> 1));
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
         const float4 cs = __ldg(ap + e / 2);
-        v[u][e] = fma2(f2{v[u][e].y, v[u][e].x}, f2{-cs.y, cs.y}, mul2(v[u][e], f2{cs.x, cs.x}));
-        v[u][e + 1] = fma2(f2{v[u][e + 1].y, v[u][e + 1].x}, f2{-cs.w, cs.w}, mul2(v[u][e + 1], f2{cs.z, cs.z}));
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const f2 y = v[i][u][e], z = v[i][u][e + 1];
+          v[i][u][e] = fma2(f2{y.y, y.x}, f2{-cs.y, cs.y}, mul2(y, f2{cs.x, cs.x}));
+          v[i][u][e + 1] = fma2(f2{z.y, z.x}, f2{-cs.w, cs.w}, mul2(z, f2{cs.z, cs.z}));
+        }
       }
     }
   }
 #pragma unroll
-  for (int u = 0; u < V; ++u)
-    if (f[u] < hd)
-      *reinterpret_cast<uint4 *>(t.y + f[u]) = make_uint4(pack2(v[u][0]), pack2(v[u][1]), pack2(v[u][2]), pack2(v[u][3]));
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+      if (f[u] < hd && i < t.rows)
+        *reinterpret_cast<uint4 *>(t.y + i * t.y_h + f[u]) =
+            make_uint4(pack2(v[i][u][0]), pack2(v[i][u][1]), pack2(v[i][u][2]), pack2(v[i][u][3]));
 }
 
 // Any even turned part and alignment of weights and angles: a feature at a time, partners read from the row again.
@@ -205,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_any(const __grid_constan
   const int lane = threadIdx.x & (G - 1);
   const int hd = a.c.head_dim, h2 = a.rd >> 1;
   Item t;
-  const int h = find_item(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
+  const int h = find_item<1>(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
   dependency_wait();
   uint4 x[V];
   float r = 0.f, z[V][8];  // z: partners, normed but for r
@@ -226,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_any(const __grid_constan
       z[u][e] = __bfloat162float(t.x[fp]) * (t.w ? __ldg(t.w + fp) : 1.f);
     }
   }
-  find_place(a, g, h, lane, t);
+  find_place<1>(a, g, h, lane, t);
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
   __syncwarp();  // (q_out may be q: every lane has read its partners)
@@ -261,16 +299,16 @@ __global__ void __launch_bounds__(kThreads) k_norm_rope_any(const __grid_constan
 
 using Kernel = void (*)(NormRopeArgs, Grid);
 
-cudaError_t launch(Kernel k, int G, const NormRopeArgs &a, cudaStream_t s) {
-  const int per_token = a.H + a.c.kv_heads * (a.v ? 2 : 1);
+cudaError_t launch(Kernel k, int G, int R, const NormRopeArgs &a, cudaStream_t s) {
+  const int nq = (a.H + R - 1) / R, nk = (a.c.kv_heads + R - 1) / R, per_token = nq + nk * (a.v ? 2 : 1);
   const int64_t items = (int64_t)a.N * per_token;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;  // (refused by the entry)
-  const Grid g{(int)items, paged::FastDiv((uint32_t)per_token), paged::FastDiv((uint32_t)a.c.page)};
+  const Grid g{(int)items, nq, nk, paged::FastDiv((uint32_t)per_token), paged::FastDiv((uint32_t)a.c.page)};
   return launch_dependent(k, dim3((unsigned)((items * G + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, 1, a, g);
 }
-template <int G, int V>
+template <int G, int V, int R>
 cudaError_t launch_vectors(const NormRopeArgs &a, cudaStream_t s) {
-  return launch(a.half ? (Kernel)k_norm_rope<G, V, true> : (Kernel)k_norm_rope<G, V, false>, G, a, s);
+  return launch(a.half ? (Kernel)k_norm_rope<G, V, true, R> : (Kernel)k_norm_rope<G, V, false, R>, G, R, a, s);
 }
 
 }  // namespace
@@ -281,17 +319,17 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s) {
   const bool vectors = hd % 16 == 0 && a.at % 8 == 0 && a.rd % (a.half ? 16 : 8) == 0 &&
                        (((uintptr_t)a.tab | (uintptr_t)a.q_norm | (uintptr_t)a.k_norm) & 15) == 0;
   if (!vectors) {
-    if (hd <= 64) return launch(k_norm_rope_any<8, 1>, 8, a, s);
-    if (hd <= 128) return launch(k_norm_rope_any<16, 1>, 16, a, s);
-    if (hd <= 256) return launch(k_norm_rope_any<32, 1>, 32, a, s);
-    return launch(hd <= 512 ? (Kernel)k_norm_rope_any<32, 2> : (Kernel)k_norm_rope_any<32, 4>, 32, a, s);
+    if (hd <= 64) return launch(k_norm_rope_any<8, 1>, 8, 1, a, s);
+    if (hd <= 128) return launch(k_norm_rope_any<16, 1>, 16, 1, a, s);
+    if (hd <= 256) return launch(k_norm_rope_any<32, 1>, 32, 1, a, s);
+    return launch(hd <= 512 ? (Kernel)k_norm_rope_any<32, 2> : (Kernel)k_norm_rope_any<32, 4>, 32, 1, a, s);
   }
-  if (hd <= 32) return launch_vectors<2, 2>(a, s);
-  if (hd <= 64) return launch_vectors<4, 2>(a, s);
-  if (hd <= 128) return launch_vectors<8, 2>(a, s);
-  if (hd <= 256) return launch_vectors<16, 2>(a, s);
-  if (hd <= 512) return launch_vectors<32, 2>(a, s);
-  return launch_vectors<32, 4>(a, s);
+  if (hd <= 32) return launch_vectors<2, 2, 2>(a, s);
+  if (hd <= 64) return launch_vectors<4, 2, 2>(a, s);
+  if (hd <= 128) return launch_vectors<8, 2, 2>(a, s);
+  if (hd <= 256) return launch_vectors<16, 2, 2>(a, s);
+  if (hd <= 512) return launch_vectors<32, 2, 2>(a, s);
+  return launch_vectors<32, 4, 1>(a, s);
 }
 
 }  // namespace csa
