@@ -90,7 +90,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   using S = Shape<HD, NH>;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kUnit = S::kUnit, kHeads = NH;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_scan[2 * kWarps];
+  __shared__ Two s_scan[kWarps];
   __shared__ float s_ml[2][kWarps][kHeads];
   __shared__ float s_f[kWarps][kHeads];
   __shared__ float s_out[kHeads];
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   __shared__ Rows rows;
   __shared__ Range rg;
   dependency_wait();
-  const int nunits = find_range<kUnit, kThreads, false, kEnd>(P, s_scan, rows, rg);
+  const int nunits = find_range<kUnit, kThreads, false, kEnd, false>(P, s_scan, rows, rg);
   if (nunits <= 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
@@ -397,7 +397,11 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
         }
       }
       __syncthreads();  // the stage may be refilled
-      if (!whole) publish<kHeads, HD, kThreads>(P, cc.base, cc.base + cc.units, rg, cc.n, h0, nh, &s_flag);
+      if (!whole) {
+        int c0;
+        const int parts = sharers(rg, cc, c0);
+        publish<kHeads, HD, kThreads>(P, c0, parts, cc.n, h0, nh, &s_flag);
+      }
       if (u + 1 < nunits) {
         advance<kUnit, false, kEnd>(a, P.Hg, rows, cc);
         seg = u + 1;

@@ -20,8 +20,8 @@
 // scores that read it; four rescale O and write it out.  All waits are time-bounded.
 //
 // 64 x 1 over 12 to 16 thousand rows: 176 us, 5.3 TB/s (79 % of a copy); of the 2500 to 2800 cycles of a tile the products take
-// 1300, and the rest is what their hand-overs take: scores to softmax to values.  32 x 1 over about 900 rows (4 to 5 tiles a CTA): 23 us, of
-// which the shares' 128 KB a CTA take 2 us each to write and 7 us to join.
+// 1300, and the rest is what their hand-overs take: scores to softmax to values.  32 x 1 over about 900 rows (5 tiles a CTA): 21 us, of
+// which the shares' 128 KB a CTA take 2 us to write and 6 us to join.
 #include <algorithm>
 #include <cstring>
 
@@ -40,7 +40,7 @@ namespace latent {
 constexpr int kHD = 512;
 constexpr int kHeads = 64;              // query heads of a head group
 constexpr int kUnit = 48;               // positions of a tile
-constexpr int kEnd = 1;                 // tiles that the end of a segment counts for
+constexpr int kEnd = 2;                 // tiles that the end of a segment counts for (its share takes 2 us to write)
 constexpr int kJ = kUnit / 8;
 constexpr int kBufs = 3;                // tile buffers
 constexpr int kBlock = kUnit * 128;     // bytes of a 64-feature block of a tile
@@ -60,8 +60,8 @@ struct L {
   static constexpr size_t p = t + (size_t)kBufs * kBlocks * kBlock;          // [2][64][128 B]
   static constexpr size_t alpha = p + (size_t)2 * kHeads * 128;              // float [2][64]
   static constexpr size_t f = alpha + 2 * kHeads * 4;                        // float [2][64]
-  static constexpr size_t scan = f + 2 * kHeads * 4;                         // int64 [32]
-  static constexpr size_t range = scan + 32 * 8;                             // Range
+  static constexpr size_t scan = f + 2 * kHeads * 4;                         // Two [16]
+  static constexpr size_t range = scan + 16 * 8;                             // Range
   static constexpr size_t rows = range + ((sizeof(Range) + 7) & ~7);         // Rows
   static constexpr size_t bars = rows + ((sizeof(Rows) + 7) & ~7);           // u64 [16]
   static constexpr size_t misc = bars + 16 * 8;                              // masks [3][2], flags [2][4], slot, abort
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
   if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
   tc::tc_fence_before();
   dependency_wait();
-  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN, kEnd>(P, reinterpret_cast<int64_t *>(smem + L::scan), rows, rg);  // this CTA's tiles
+  const int nt = find_range<kUnit, kThreads<TMA>, ALIGN, kEnd, true>(P, reinterpret_cast<Two *>(smem + L::scan), rows, rg);  // this CTA's tiles
   if (nt <= 0) {  // (< 0: more units than can be counted, so that no segment is told of)
     if (tid == 0 && (nt < 0 || !P.by_segment)) P.split[blockIdx.x] = make_int2(0, 0);
     if (warp == 8) {
@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       }
       tc::tc_fence_before();
       if (seg == sb && jt == 0) {  // (the segment begins here)
-        const int parts = whole ? 0 : cta_of(c.base + c.units - 1, rg) - (int)blockIdx.x + 1;
+        int c0;
+        const int parts = whole ? 0 : sharers(rg, c, c0);
         if (P.by_segment) {
           P.split[(int64_t)c.n * P.Hg + c.hg] = make_int2(blockIdx.x, parts);
         } else if (!whole) {

@@ -89,14 +89,15 @@ __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report
   return r;
 }
 
-// A CTA's range of places and the row its first place lies in.  Places are counted in 32 bits: a call whose rows come
-// to 2^31 or more (2^35 positions and heads at least) does nothing but report it.
+// A CTA's range: the row, head group and unit it begins with and its units.  Places are counted in 32 bits: a call whose rows
+// come to 2^31 or more (2^35 positions and heads at least) does nothing but report it.
 struct Range {
-  uint32_t begin;        // its first place
+  int row, hg, t;        // t may be behind the segment's units (then the next segment's first unit is meant)
+  uint32_t base;         // first place of that segment
   uint32_t each, more;   // places a CTA; the first `more` CTAs have one more
-  uint32_t before;       // places (of all its segments) before the row
-  int row;
   uint32_t u0, u1;       // units before its first place and before its end
+  int c0, parts;         // parts > 0: all its units are of one segment, dealt over CTAs c0 .. c0 + parts - 1
+  int n_units;
 };
 // The first rows of a CTA's range, kept in shared memory: the cursors read a new row there and not through two
 // dependent loads from global memory.
@@ -128,91 +129,145 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, int Hg, const Ro
   } while (c.units == 0);
 }
 
-// Called by all NT threads of the CTA.  scratch: int64 [NT / 16], rows, out: all in shared memory.  Returns how many
-// units the CTA has (-1: more than can be counted in all).
-template <int U, int NT, bool ALIGN, int W>
-__device__ __forceinline__ int find_range(const Params &P, int64_t *scratch, Rows &rows, Range &out) {
+// Sums of units and of segments, held at 2^31 - 1 once they reach it.
+struct Two {
+  uint32_t units, segs;
+};
+__device__ __forceinline__ Two plus(Two a, Two b) { return {min(a.units + b.units, 0x7fffffffu), min(a.segs + b.segs, 0x7fffffffu)}; }
+__device__ __forceinline__ Two warp_scan(Two v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Two o{__shfl_up_sync(0xffffffffu, v.units, d), __shfl_up_sync(0xffffffffu, v.segs, d)};
+    if (lane >= d) v = plus(v, o);
+  }
+  return v;
+}
+
+// Called by all NT threads of the CTA.  scratch: Two [NT / 32], rows, out: all in shared memory.  Returns how many
+// units the CTA has (-1: more than can be counted in all).  Up to 32 rows the first warp finds it alone, and the CTA meets
+// once.  WHOLE: few segments (and rows) get whole CTAs, as many as ceil(its units / q) says, if such a q close to
+// the even share exists: a CTA then has one segment's end and not two (32 latent rows of about 20 tiles: 20.9
+// against 22.6 us, 128 shares of 128 KB instead of 184; up to 256 features, where ends are cheap, one row of 8000 lost 1 us).
+template <int U, int NT, bool ALIGN, int W, bool WHOLE>
+__device__ __forceinline__ int find_range(const Params &P, Two *scratch, Rows &rows, Range &out) {
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  constexpr int NW = NT / 32;
+  const uint32_t Hg = (uint32_t)P.Hg, G = gridDim.x;
   const bool report = blockIdx.x == 0;
-  struct Two {
-    int64_t units, segs;
+  auto of_row = [&](int n, Row &r) -> Two {
+    r = Row{0, 0, 0, 0, 0};
+    if (n < a.N) r = row_of<U, ALIGN>(a, n, report);
+    return {(uint32_t)r.units, r.units > 0 ? 1u : 0u};
   };
-  Row last{0, 0, 0, 0, 0};  // the row a thread has read last
-  auto of_row = [&](int n, bool rep) -> Two {
-    if (n >= a.N) return {0, 0};
-    last = row_of<U, ALIGN>(a, n, rep);
-    return {last.units, last.units > 0 ? 1 : 0};
+  auto places = [&](Two v) -> int64_t { return ((int64_t)v.units + (int64_t)W * v.segs) * Hg; };
+  // no more CTAs than there are places, so that none between two has none
+  uint32_t begin = 0, end = 0;
+  auto shares = [&](Two sum, bool tell) -> int {  // this CTA's places; 0: it has some
+    const int64_t all = places(sum);
+    if (all > 0x7fffffff) {
+      if (report && tell) atomicOr(a.status, kStatusBadIndex);
+      return -1;
+    }
+    const uint32_t total = (uint32_t)all, ctas = min(G, total);
+    if (blockIdx.x >= ctas) return 1;
+    const uint32_t each = total / ctas, more = total - each * ctas;
+    begin = each * blockIdx.x + min(blockIdx.x, more);
+    end = begin + each + (blockIdx.x < more ? 1 : 0);
+    if (tell) {
+      out.each = each;
+      out.more = more;
+      out.parts = 0;
+    }
+    return 0;
   };
-  auto scan = [&](Two v, Two &sum) -> Two {  // inclusive over the CTA; sum: of all
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, v.units, d), p = __shfl_up_sync(0xffffffffu, v.segs, d);
-      if (lane >= d) v.units += o, v.segs += p;
+  auto look = [&](Two from, uint32_t u, int n) -> bool {  // at row n of u units a segment; whether the range begins there
+    const uint32_t lo = (uint32_t)places(from), hi = lo + (u ? (u + W) * Hg : 0u), before = from.units * Hg;
+    if (end > lo && end <= hi) {
+      const uint32_t in = end - lo, hg = in / (u + W), t = in - hg * (u + W);
+      out.u1 = before + hg * u + min(t, u);
+    }
+    if (begin < lo || begin >= hi) return false;
+    const uint32_t in = begin - lo, hg = in / (u + W), t = in - hg * (u + W);
+    out.row = n;
+    out.hg = (int)hg;
+    out.t = (int)t;
+    out.base = begin - t;
+    out.u0 = before + hg * u + min(t, u);
+    return true;
+  };
+
+  if (a.N <= 32) {
+    if (wid == 0) {
+      Row row;
+      const Two mine = of_row(lane, row), incl = warp_scan(mine, lane);
+      const Two sum{__shfl_sync(0xffffffffu, incl.units, 31), __shfl_sync(0xffffffffu, incl.segs, 31)};
+      const int none = shares(sum, lane == 0);
+      __syncwarp();  // (out.parts may be written again)
+      bool here = false, whole = WHOLE && none >= 0 && sum.segs > 0 && sum.segs * Hg <= G;
+      if (whole) {
+        const uint32_t u = mine.units, q = (sum.units * Hg + G - 1) / G;
+        const Two c{(u + q - 1) / q, (u + q) / (q + 1)}, to = warp_scan(c, lane);
+        const bool first = __shfl_sync(0xffffffffu, to.units, 31) * Hg <= G;
+        whole = first || __shfl_sync(0xffffffffu, to.segs, 31) * Hg <= G;
+        const uint32_t n = first ? c.units : c.segs, in = blockIdx.x - ((first ? to.units : to.segs) - n) * Hg;
+        if (whole && in < n * Hg) {  // (a CTA before the row's: wraps)
+          const uint32_t hg = in / n, part = in - hg * n, one = u / n, rest = u - one * n;
+          here = true;
+          out.row = lane;
+          out.hg = (int)hg;
+          out.t = (int)(part * one + min(part, rest));
+          out.base = out.u0 = 0;
+          out.u1 = one + (part < rest ? 1 : 0);
+          out.c0 = (int)(blockIdx.x - part);
+          out.parts = (int)n;
+        }
+      }
+      if (!whole && none == 0) here = look(Two{incl.units - mine.units, incl.segs - mine.segs}, mine.units, lane);
+      const uint32_t who = __ballot_sync(0xffffffffu, here);
+      const int first_row = __ffs(who) - 1;
+      if (lane >= first_row) rows.row[lane - max(first_row, 0)] = row;
+      if (lane == 0) {
+        rows.n0 = first_row;
+        out.n_units = none < 0 ? -1 : who ? (int)(out.u1 - out.u0) : 0;
+      }
     }
     __syncthreads();
-    if (lane == 31) scratch[2 * wid] = v.units, scratch[2 * wid + 1] = v.segs;
+    return out.n_units;
+  }
+
+  auto scan = [&](Two v, Two &sum) -> Two {  // inclusive over the CTA; sum: of all
+    v = warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) scratch[wid] = v;
     __syncthreads();
     sum = {0, 0};
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const int64_t o = scratch[2 * w], p = scratch[2 * w + 1];
-      if (w < wid) v.units += o, v.segs += p;
-      sum.units += o, sum.segs += p;
+    Two before{0, 0};
+#pragma unroll 1
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w == wid) before = sum;
+      sum = plus(sum, scratch[w]);
     }
-    return v;
+    return plus(v, before);
   };
-  auto places = [&](Two v) -> int64_t { return (v.units + W * v.segs) * P.Hg; };
-  Two mine{0, 0};
-  for (int n = tid; n < a.N; n += NT) {
-    const Two v = of_row(n, report);
-    mine.units += v.units, mine.segs += v.segs;
-  }
-  Two sum;
-  Two incl = scan(mine, sum);
-  if (places(sum) > 0x7fffffff) {
-    if (report && tid == 0) atomicOr(a.status, kStatusBadIndex);
-    return -1;
-  }
-  // no more CTAs than there are places, so that none between two has none
-  const uint32_t total = (uint32_t)places(sum), ctas = min(gridDim.x, total);
-  if (blockIdx.x >= ctas) return 0;
-  const uint32_t each = total / ctas, more = total - each * ctas;
-  const uint32_t begin = each * blockIdx.x + min(blockIdx.x, more), end = begin + each + (blockIdx.x < more ? 1 : 0);
-  if (tid == 0) {
-    out.begin = begin;
-    out.each = each;
-    out.more = more;
-  }
+  Two mine{0, 0}, sum;
+  Row row;
+  for (int n = tid; n < a.N; n += NT) mine = plus(mine, of_row(n, row));
+  scan(mine, sum);
+  const int none = shares(sum, tid == 0);
+  if (none) return none < 0 ? -1 : 0;
   Two base{0, 0};
-  for (int n0 = 0; n0 < a.N; n0 += NT) {  // one round for up to NT rows
-    if (a.N > NT) {
-      mine = of_row(n0 + tid, false);
-      incl = scan(mine, sum);
-    }
-    const Two to{base.units + incl.units, base.segs + incl.segs}, from{to.units - mine.units, to.segs - mine.segs};
-    const int64_t lo = places(from), hi = places(to);
-    auto units_before = [&](uint32_t place) -> uint32_t {  // of a place of this row
-      const uint32_t in = place - (uint32_t)lo, u = (uint32_t)mine.units, s = in / (u + W);
-      return (uint32_t)(from.units * P.Hg) + s * u + min(in - s * (u + W), u);
-    };
-    if (begin >= lo && begin < hi) {
-      out.row = n0 + tid;
-      out.before = (uint32_t)lo;
-      out.u0 = units_before(begin);
-    }
-    if (end > lo && end <= hi) out.u1 = units_before(end);
-    base.units += sum.units, base.segs += sum.segs;
+  for (int n0 = 0; n0 < a.N; n0 += NT) {
+    mine = of_row(n0 + tid, row);
+    const Two incl = plus(base, scan(mine, sum));
+    look(Two{incl.units - mine.units, incl.segs - mine.segs}, mine.units, n0 + tid);
+    base = plus(base, sum);
     if (end <= places(base)) break;
   }
   __syncthreads();
   if (tid == 0) rows.n0 = out.row;
-  if (a.N <= NT) {  // (a thread has its row still; entries past the last row are never read)
-    const unsigned i = (unsigned)(tid - out.row);
-    if (i < (unsigned)kRowsKept) rows.row[i] = last;
-  } else if (tid < kRowsKept && out.row + tid < a.N) {
-    rows.row[tid] = row_of<U, ALIGN>(a, out.row + tid, false);
+  if (tid < kRowsKept) {
+    of_row(out.row + tid, row);
+    rows.row[tid] = row;
   }
   __syncthreads();
   return (int)(out.u1 - out.u0);
@@ -223,10 +278,9 @@ __device__ __forceinline__ Cursor first_unit(const PagedAttnArgs &a, int Hg, con
   Cursor c;
   c.n = r.row;
   c.units = rows.row[0].units;
-  const uint32_t in = r.begin - r.before, s = (uint32_t)c.units + W;
-  c.hg = (int)(in / s);
-  c.base = r.before + (uint32_t)c.hg * s;
-  c.t = (int)(r.begin - c.base);
+  c.hg = r.hg;
+  c.base = r.base;
+  c.t = r.t;
   if (c.t >= c.units) {  // (behind a segment's units)
     c.t = c.units - 1;
     advance<U, ALIGN, W>(a, Hg, rows, c);
@@ -245,6 +299,12 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ int cta_of(uint32_t u, const Range &r) {
   const uint32_t first = r.more * (r.each + 1);  // places of the CTAs with one more
   return (int)(u < first ? u / (r.each + 1) : r.more + (u - first) / r.each);
+}
+
+// The CTAs that share the cursor's segment: c0 .. c0 + (returned) - 1.
+__device__ __forceinline__ int sharers(const Range &r, const Cursor &c, int &c0) {
+  c0 = r.parts ? r.c0 : cta_of(c.base, r);
+  return r.parts ? r.parts : cta_of(c.base + c.units - 1, r) - c0 + 1;
 }
 
 // One more arrival at a counter of `of` (by one thread, after a CTA barrier behind the writes it publishes);
@@ -341,13 +401,11 @@ __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool
   }
 }
 
-// Publish this CTA's share of the segment with units in places [sb, se) (already written to its slot by the CTA's threads) and join
-// what it completes.  flag: an int in shared memory.
+// Publish this CTA's share of the segment that CTAs c0 .. c0 + parts - 1 share (already written to its slot by the CTA's threads)
+// and join what it completes.  flag: an int in shared memory.
 template <int NH, int HD, int NT>
-__device__ __forceinline__ void publish(const Params &P, uint32_t sb, uint32_t se, const Range &r, int n, int h0, int nh,
-                                        int *flag) {
-  const int c0 = cta_of(sb, r), c1 = cta_of(se - 1, r);
-  const int parts = c1 - c0 + 1, mine = (int)blockIdx.x - c0, grp = mine / kJoin, ngrp = (parts + kJoin - 1) / kJoin;
+__device__ __forceinline__ void publish(const Params &P, int c0, int parts, int n, int h0, int nh, int *flag) {
+  const int mine = (int)blockIdx.x - c0, grp = mine / kJoin, ngrp = (parts + kJoin - 1) / kJoin;
   const int first = grp * kJoin, in_grp = min(kJoin, parts - first);
   auto slot_of = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
   __syncthreads();
