@@ -599,6 +599,29 @@ def test_paged_attn_uneven_rows(csa, ctx, H, kv, hd, latent, seed):
     assert ctx.status() == 0
 
 
+@pytest.mark.parametrize("H,kv,hd,latent", [(640, 1, 512, True), (130, 1, 512, True), (64, 1, 512, True), (256, 1, 128, False),
+                                            (96, 32, 64, False)])
+@pytest.mark.parametrize("N", [20, 32, 33])
+def test_paged_attn_few_live_rows(csa, ctx, H, kv, hd, latent, N):
+    """Mostly padding: few rows over many head groups, one row past the others' length by far."""
+    lens = [0] * N
+    lens[2], lens[N // 2], lens[N - 1] = 2500, 1, 300
+    b = Batch(lens, H, kv, hd, 16, latent, seed=N)
+    pos = [x - 1 if x else -5 for x in lens]
+    q = b.queries(N)
+    out = torch.full((N, H, hd), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, H), 3.0, device="cuda")
+    ctx.paged_attn(q, csa.PagedCache(b.k, b.v), b.table, i32(pos), b.scale, out=out, lse=lse)
+    live = [n for n in range(N) if lens[n]]
+    check_rows(b, q[live], out[live], lse[live], [pos[n] for n in live], live)
+    for n in set(range(N)) - set(live):
+        assert (out[n] == 3).all() and (lse[n] == 3).all()
+    # nothing but padding
+    out.fill_(3.0)
+    ctx.paged_attn(q, csa.PagedCache(b.k, b.v), b.table, i32([-2] * N), b.scale, out=out)
+    assert (out == 3).all() and ctx.status() == 0
+
+
 @pytest.mark.parametrize("H,kv,hd,latent", [(8, 2, 128, False), (20, 1, 256, False), (64, 1, 512, True)])
 def test_paged_attn_replayed_and_in_place(csa, ctx, H, kv, hd, latent):
     """Two captured graphs of one context replayed by turns while positions change, and the result over q itself."""
