@@ -236,64 +236,90 @@ __global__ void __launch_bounds__(kThreads, kResident<V, HALF>) k_norm_rope(cons
             make_uint4(pack2(v[i][u][0]), pack2(v[i][u][1]), pack2(v[i][u][2]), pack2(v[i][u][3]));
 }
 
-// Any even turned part and alignment of weights and angles: a feature at a time, partners read from the row again.
+// Any even turned part and alignment of weights and angles.  Adjacent pairs still lie inside a vector; halves meet through shared
+// memory, where a row's normed features wait for their partners (one row a group, 11475 tokens of 56 x 80 with 4 features
+// turned: 74 us; partners read from the row again, a feature at a time: 147).
 template <int G, int V>
 __global__ void __launch_bounds__(kThreads) k_norm_rope_any(const __grid_constant__ NormRopeArgs a,
                                                             const __grid_constant__ Grid g) {
+  __shared__ __align__(16) float s_row[kThreads / G][8 * G * V];
   const int lane = threadIdx.x & (G - 1);
   const int hd = a.c.head_dim, h2 = a.rd >> 1;
+  float *mine = s_row[threadIdx.x / G];
   Item t;
   const int h = find_item<1>(a, g, ((int64_t)blockIdx.x * kThreads + threadIdx.x) / G, t);
   dependency_wait();
   uint4 x[V];
-  float r = 0.f, z[V][8];  // z: partners, normed but for r
+  f2 v[V][4], q = {0.f, 0.f};
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int f0 = 8 * (lane + G * u);
-    x[u] = f0 < hd ? *reinterpret_cast<const uint4 *>(t.x + f0) : make_uint4(0, 0, 0, 0);
-    f2 v[4];
-    unpack(x[u], v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r = fmaf(v[e].x, v[e].x, fmaf(v[e].y, v[e].y, r));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int f = f0 + e, d = f - a.at;
-      z[u][e] = 0.f;
-      if (t.plain || f >= hd || d < 0 || d >= a.rd) continue;
-      const int fp = a.half ? (d < h2 ? f + h2 : f - h2) : (d & 1 ? f - 1 : f + 1);
-      z[u][e] = __bfloat162float(t.x[fp]) * (t.w ? __ldg(t.w + fp) : 1.f);
-    }
+    const int f = 8 * (lane + G * u);
+    x[u] = f < hd ? *reinterpret_cast<const uint4 *>(t.x + f) : make_uint4(0, 0, 0, 0);
   }
   find_place<1>(a, g, h, lane, t);
 #pragma unroll
+  for (int u = 0; u < V; ++u) {
+    unpack(x[u], v[u]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q = fma2(v[u][e], v[u][e], q);
+  }
+  float r = q.x + q.y;
+#pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-  __syncwarp();  // (q_out may be q: every lane has read its partners)
-  if (!t.live) return;
-  r = t.w ? rsqrtf(r / (float)hd + a.eps) : 1.f;
-  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)t.pos * h2;
+  if (t.w) {
+    r = rsqrtf(r / (float)hd + a.eps);
+    const bool whole = ((uintptr_t)t.w & 15) == 0;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int f = 8 * (lane + G * u);
+      if (f >= hd) continue;
+      f2 w[4];
+      if (whole) {
+        load8(t.w + f, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = {__ldg(t.w + f + 2 * e), __ldg(t.w + f + 2 * e + 1)};
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[u][e] = mul2(mul2(v[u][e], f2{r, r}), w[e]);
+    }
+  }
+  const bool turn = t.live && !t.plain;
+  const float2 *tp = reinterpret_cast<const float2 *>(a.tab) + (int64_t)(turn ? t.pos : 0) * h2;
+  if (a.half) {
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      float4 *to = reinterpret_cast<float4 *>(mine + 8 * (lane + G * u));
+      to[0] = make_float4(v[u][0].x, v[u][0].y, v[u][1].x, v[u][1].y);
+      to[1] = make_float4(v[u][2].x, v[u][2].y, v[u][3].x, v[u][3].y);
+    }
+    __syncwarp();
+  }
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int f0 = 8 * (lane + G * u);
-    if (f0 >= hd) continue;
+    const int f = 8 * (lane + G * u);
+    if (f >= hd || !t.live) continue;
     uint4 out = x[u];
-    if (!t.plain) {
-      f2 v[4];
-      unpack(x[u], v);
-      float o[8];
+    if (turn) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int f = f0 + e, d = f - a.at;
-        o[e] = (e & 1 ? v[e >> 1].y : v[e >> 1].x) * (t.w ? __ldg(t.w + f) : 1.f);
-        if (d >= 0 && d < a.rd) {
-          const bool first = a.half ? d < h2 : !(d & 1);
-          const float2 cs = __ldg(tp + (a.half ? (first ? d : d - h2) : d >> 1));
-          o[e] = first ? o[e] * cs.x - z[u][e] * cs.y : z[u][e] * cs.y + o[e] * cs.x;
+      for (int e = 0; e < 4; ++e) {
+        const int d = f + 2 * e - a.at;  // (even, as `at` and rd are; rd / 2 may be odd)
+        if (d < 0 || d >= a.rd) continue;
+        if (a.half) {
+          const bool lo = d < h2, lo1 = d + 1 < h2;
+          const float2 c0 = __ldg(tp + (lo ? d : d - h2)), c1 = __ldg(tp + (lo1 ? d + 1 : d + 1 - h2));
+          const float *p = mine + a.at + d;
+          const float p0 = lo ? p[h2] : p[-h2], p1 = lo1 ? p[1 + h2] : p[1 - h2];
+          v[u][e] = {fmaf(lo ? -p0 : p0, c0.y, v[u][e].x * c0.x), fmaf(lo1 ? -p1 : p1, c1.y, v[u][e].y * c1.x)};
+        } else {
+          const float2 cs = __ldg(tp + (d >> 1));
+          const f2 y = v[u][e];
+          v[u][e] = fma2(f2{y.y, y.x}, f2{-cs.y, cs.y}, mul2(y, f2{cs.x, cs.x}));
         }
-        o[e] *= r;
       }
-      out = make_uint4(pack2({o[0], o[1]}), pack2({o[2], o[3]}), pack2({o[4], o[5]}), pack2({o[6], o[7]}));
+      out = make_uint4(pack2(v[u][0]), pack2(v[u][1]), pack2(v[u][2]), pack2(v[u][3]));
     }
-    *reinterpret_cast<uint4 *>(t.y + f0) = out;
+    *reinterpret_cast<uint4 *>(t.y + f) = out;
   }
 }
 
@@ -319,9 +345,9 @@ cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t s) {
   const bool vectors = hd % 16 == 0 && a.at % 8 == 0 && a.rd % (a.half ? 16 : 8) == 0 &&
                        (((uintptr_t)a.tab | (uintptr_t)a.q_norm | (uintptr_t)a.k_norm) & 15) == 0;
   if (!vectors) {
-    if (hd <= 64) return launch(k_norm_rope_any<8, 1>, 8, 1, a, s);
-    if (hd <= 128) return launch(k_norm_rope_any<16, 1>, 16, 1, a, s);
-    if (hd <= 256) return launch(k_norm_rope_any<32, 1>, 32, 1, a, s);
+    if (hd <= 64) return launch(k_norm_rope_any<4, 2>, 4, 1, a, s);
+    if (hd <= 128) return launch(k_norm_rope_any<8, 2>, 8, 1, a, s);
+    if (hd <= 256) return launch(k_norm_rope_any<16, 2>, 16, 1, a, s);
     return launch(hd <= 512 ? (Kernel)k_norm_rope_any<32, 2> : (Kernel)k_norm_rope_any<32, 4>, 32, 1, a, s);
   }
   if (hd <= 32) return launch_vectors<2, 2, 2>(a, s);

@@ -9,7 +9,7 @@
 // step does not write) or one it takes now (a ring entry), so no thread reads what another one writes.
 //
 // Bound by latency: a 64-token step moves 2 KB and takes 3.2 us, 1500 requests 8.8 us (device times).
-// One CTA does small steps; larger ones (above 2048 tokens or requests) take one cluster of
+// One CTA does small steps; larger ones (above 2048 tokens or requests, or with long tables) take one cluster of
 // eight CTAs, each of which forms the sums for itself (R <= 14000 lengths from L2, kept in its shared memory)
 // and takes an eighth of the tokens and pages.  The hardware's cluster barrier, after everything has been
 // read, lets length_out and state_out be length and state: one launch, and no counter that two calls could
@@ -205,8 +205,9 @@ cudaError_t launch_page_step(const PageStepArgs &a, cudaStream_t s) {
   cudaError_t e = attr.ensure((const void *)k_page_step, (int)smem);
   if (e != cudaSuccess) return e;
   // One CTA against eight: 1000 requests 5.2 against 6.0 us, 2000 tokens 4.2 / 4.4, 4000 tokens 5.0 / 4.5, 4000 requests 12.2 /
-  // 9.1.  256 threads against 1024: 200 requests 3.4 / 3.9, 300 4.4 / 4.3, 1000 6.7 / 5.2.
-  const bool large = a.N > 2048 || a.R > 2048;
+  // 9.1, 1400 requests of which 113 end with up to 1700 pages each 28 / 9.5 (what a step releases is not known here, only how
+  // wide the tables are).  256 threads against 1024: 200 requests 3.4 / 3.9, 300 4.4 / 4.3, 1000 6.7 / 5.2.
+  const bool large = a.N > 2048 || a.R > 2048 || (a.R > 256 && a.width > 1024);
   const unsigned ctas = large ? kClusterCtas : 1;
   return launch_dependent(k_page_step, dim3(ctas), dim3(a.N <= 256 && a.R <= 256 ? 256 : 1024), smem, s, ctas, a,
                           paged::FastDiv((uint32_t)a.page));
