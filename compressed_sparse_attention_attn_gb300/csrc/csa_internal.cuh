@@ -301,7 +301,7 @@ struct PagedAttnArgs {
   int *status;
 };
 // ws: the shares of rows that several CTAs work on; counters: kPagedCounters ints, zero between launches.
-constexpr int kPagedCounters = 3 * 640;
+constexpr int kPagedCounters = 3 * 2 * 640;
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms,
                               cudaStream_t s);
 

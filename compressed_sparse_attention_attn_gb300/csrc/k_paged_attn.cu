@@ -448,7 +448,7 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms,
                               cudaStream_t s) {
-  static_assert(kPagedCounters == 3 * paged::kMaxCtas, "the context's counters");
+  static_assert(kPagedCounters == 3 * 2 * paged::kMaxCtas && paged::kJoin * paged::kJoin * paged::kJoin >= paged::kMaxCtas, "the context's counters");
   paged::Params p;
   p.a = a;
   p.page = paged::FastDiv((uint32_t)a.c.page);

@@ -12,9 +12,9 @@
 // values relative to M, in f32, in one of its two slots (0: a segment that began in an earlier CTA, 1: one
 // that begins here).  Up to 256 features, twelve consecutive shares of a segment are a group.  The CTA that completes a
 // group joins it (in the order of the shares, whoever is last); with more than one group the joined shares go
-// to the group's first slot, and the CTA that completes the last group joins those.  So a long row over 300
-// CTAs is joined in two steps, of 12 and of 26 shares, and nothing waits.  The counters return to zero.  Shares of latent
-// rows, 128 KB each, are joined by a second kernel (k_paged_attn_tc.cu).
+// to the group's first slot, and twelve groups are joined in the same way.  So a long row over 400 CTAs is joined
+// in three steps, and nothing waits (in two, of 12 and of 38 shares, one row of 46000 took 20.0 against 17.4 us).  The
+// counters return to zero.  Shares of latent rows, 128 KB each, are joined by a second kernel (k_paged_attn_tc.cu).
 #pragma once
 
 #include "csa_internal.cuh"
@@ -48,7 +48,7 @@ struct Params {
   float scale_log2;     // softmax scale * log2(e)
   float *share_o;       // [2 G][heads of a group][padded head_dim]
   float *share_ml;      // [2 G][heads of a group][2]
-  int *counters;        // [3][kMaxCtas]: groups past a segment's first, first groups, segments
+  int *counters;        // [3][2][kMaxCtas]: for each step of joining, groups past a segment's first, first groups
   int2 *split;          // latent rows: of the segments that several CTAs shared, the first CTA and how many
   int ctas;             // CTAs launched
   int by_segment;       // `split` is by segment (no more of them than CTAs), else by first CTA
@@ -402,26 +402,26 @@ __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool
 }
 
 // Publish this CTA's share of the segment that CTAs c0 .. c0 + parts - 1 share (already written to its slot by the CTA's threads)
-// and join what it completes.  flag: an int in shared memory.
+// and join what it completes: a dozen shares, a dozen of such groups, and so on.  flag: an int in shared memory.
 template <int NH, int HD, int NT>
 __device__ __forceinline__ void publish(const Params &P, int c0, int parts, int n, int h0, int nh, int *flag) {
-  const int mine = (int)blockIdx.x - c0, grp = mine / kJoin, ngrp = (parts + kJoin - 1) / kJoin;
-  const int first = grp * kJoin, in_grp = min(kJoin, parts - first);
   auto slot_of = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int *ctr = grp == 0 ? P.counters + kMaxCtas + c0 : P.counters + c0 + first;
-    *flag = arrive_last(ctr, in_grp) ? 1 : 0;
+  int mine = (int)blockIdx.x - c0, step = 1;  // of `parts` joined shares, `step` CTAs apart
+#pragma unroll 1
+  for (int *counters = P.counters + c0;; counters += 2 * kMaxCtas) {
+    const int first = mine / kJoin * kJoin, in_grp = min(kJoin, parts - first);
+    __syncthreads();
+    // (a segment's first group and another's later one may belong to one CTA: each has a counter of its own)
+    if (threadIdx.x == 0) *flag = arrive_last(counters + (first == 0 ? kMaxCtas : first * step), in_grp) ? 1 : 0;
+    __syncthreads();
+    if (!*flag) return;
+    const bool fin = parts <= kJoin;
+    join<NH, HD, NT>(P, in_grp, [&](int p) { return slot_of((first + p) * step); }, fin, slot_of(first * step), n, h0, nh);
+    if (fin) return;
+    mine = first / kJoin;
+    parts = (parts + kJoin - 1) / kJoin;
+    step *= kJoin;
   }
-  __syncthreads();
-  if (!*flag) return;
-  join<NH, HD, NT>(P, in_grp, [&](int p) { return slot_of(first + p); }, ngrp == 1, slot_of(first), n, h0, nh);
-  if (ngrp == 1) return;
-  __syncthreads();
-  if (threadIdx.x == 0) *flag = arrive_last(P.counters + 2 * kMaxCtas + c0, ngrp) ? 1 : 0;
-  __syncthreads();
-  if (!*flag) return;
-  join<NH, HD, NT>(P, ngrp, [&](int p) { return slot_of(p * kJoin); }, true, 0, n, h0, nh);
 }
 
 }  // namespace paged
