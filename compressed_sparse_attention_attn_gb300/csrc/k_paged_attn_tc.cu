@@ -19,9 +19,9 @@
 // as soon as its weights are there.  Four warps do the softmax, and load the next segment's q behind the last
 // scores that read it; four rescale O and write it out.  All waits are time-bounded.
 //
-// 64 x 1 over 12 to 16 thousand rows: 176 us, 5.3 TB/s (79 % of a copy); of the 2500 to 2800 cycles of a tile the products take
-// 1300, and the rest is what their hand-overs take: scores to softmax to values.  32 x 1 over about 900 rows (5 tiles a CTA): 21 us, of
-// which the shares' 128 KB a CTA take 2 us to write and 6 us to join.
+// 64 x 1 over 12 to 16 thousand rows: 175 us, 5.3 TB/s (79 % of a copy); of the 2500 to 2800 cycles of a tile the products take
+// 1300, and the rest is what their hand-overs take: scores to softmax to values.  32 x 1 over about 900 rows (5 tiles a CTA): 20 us, of
+// which the shares' 128 KB a CTA take 2 us to write and 5 us to join.
 #include <algorithm>
 #include <cstring>
 
@@ -604,12 +604,13 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
 // Join the shares of the segments that several CTAs worked on: block x a segment (or the CTA that a split segment
 // began in), its heads and 64-feature chunks dealt over the blocks y.  A share is 128 KB, which the last CTA to finish
 // alone would take tens of microseconds to read; here the whole device reads them, 16 lanes a chunk of a share, every
-// load of a group in flight at once.  One group adds up to eight shares of an item, two or four groups the shares of a segment that
+// load of a group in flight at once.  One group adds up to six shares of an item, two or four groups the shares of a segment that
 // more CTAs had (up to sixteen: the same within 1 us from 2 to 152 shares).  Shares are added in an order that their number alone
-// sets.  32 segments of 5 to 6 shares (24 MB): 7 us with the launch; the shares' way through L2 bounds it.
+// sets.  32 segments of 4 to 5 shares (17 MB): 5 us with the launch; the shares' way through L2 bounds it.  (Eight
+// shares, or four, 1 to 2 us more; a fifth block an SM spills.)
 constexpr int kJoinThreads = 256, kJoinChunk = 64, kJoinLanes = kJoinChunk / 4, kJoinGroups = kJoinThreads / kJoinLanes;
-constexpr int kJoinShares = 8, kJoinSplit = 4;
-__global__ void __launch_bounds__(kJoinThreads) k_paged_join_latent(const __grid_constant__ Params P) {
+constexpr int kJoinShares = 6, kJoinSplit = 4;
+__global__ void __launch_bounds__(kJoinThreads, 4) k_paged_join_latent(const __grid_constant__ Params P) {
   __shared__ float4 s_v[kJoinGroups][kJoinLanes];
   __shared__ float2 s_ml[kJoinGroups];
   const PagedAttnArgs &a = P.a;
