@@ -361,16 +361,28 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         float v[32];
         attn::tmem_ld_32cols(tO + (uint32_t)((cq >> 1) * kHeads + hh) + lane_off, v);
         if (whole) {
-          const float *f = f_sm + (nseg & 1) * kHeads + hh;
-          bf16 *o = a.o + (int64_t)c.n * a.o_t + (int64_t)(h0 + hh) * hd + (d & ~1);
-          const bool odd = lane & 1;
+          // (all factors first, and no branch a store: with both inside the loop a result took 14 thousand cycles)
+          float f[16];
+          bf16 *o = a.o + (int64_t)c.n * a.o_t + (int64_t)(h0 + hh) * hd + d;
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {  // two heads at a time: even lanes write the first, two features each
-            const float x = v[k] * f[k], y = v[k + 1] * f[k + 1];
-            const float z = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-            if (hh + k + (odd ? 1 : 0) < nh && d < hd)
-              *reinterpret_cast<__nv_bfloat162 *>(o + (int64_t)(k + (odd ? 1 : 0)) * hd) =
-                  odd ? __floats2bfloat162_rn(z, y) : __floats2bfloat162_rn(x, z);
+          for (int k = 0; k < 32; k += 16) {
+            attn::lds16(f, f_sm + (nseg & 1) * kHeads + hh + k);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[k + e] *= f[e];
+          }
+          if (hh + 32 <= nh && (cq >> 1) * 128 + quad * 32 + 32 <= hd) {
+            const bool odd = lane & 1;
+            o += odd ? hd - 1 : 0;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {  // two heads at a time: even lanes write the first, two features each
+              const float z = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
+              *reinterpret_cast<__nv_bfloat162 *>(o + k * hd) =
+                  odd ? __floats2bfloat162_rn(z, v[k + 1]) : __floats2bfloat162_rn(v[k], z);
+            }
+          } else if (d < hd) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (hh + k < nh) o[k * hd] = __float2bfloat16(v[k]);
           }
         } else if (d < hd) {
           float *o = P.share_o + ((int64_t)slot * kHeads + hh) * kHD + d;
