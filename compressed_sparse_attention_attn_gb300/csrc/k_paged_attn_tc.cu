@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     *abort_flag = 0;
     tc::fence_barrier_init();
   }
-  if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
-  tc::tc_fence_before();
   dependency_wait();
+  if (warp == 8) tc::tmem_alloc(tmem_slot, 512);  // (a block of the kernel before may still ask for tensor memory until then)
+  tc::tc_fence_before();
   const int nt = find_range<kUnit, kThreads<TMA>, ALIGN, kEnd, true>(P, reinterpret_cast<Two *>(smem + L::scan), rows, rg);  // this CTA's tiles
   if (nt <= 0) {  // (< 0: more units than can be counted, so that no segment is told of)
     if (tid == 0 && (nt < 0 || !P.by_segment)) P.split[blockIdx.x] = make_int2(0, 0);
