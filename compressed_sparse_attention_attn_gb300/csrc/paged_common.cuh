@@ -226,6 +226,7 @@ __device__ __forceinline__ int find_range(const Params &P, Two *scratch, Rows &r
       const uint32_t who = __ballot_sync(0xffffffffu, here);
       const int first_row = __ffs(who) - 1;
       if (lane >= first_row) rows.row[lane - max(first_row, 0)] = row;
+      __syncwarp();
       if (lane == 0) {
         rows.n0 = first_row;
         out.n_units = none < 0 ? -1 : who ? (int)(out.u1 - out.u0) : 0;
