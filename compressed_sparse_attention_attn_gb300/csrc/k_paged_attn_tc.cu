@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         float v[32];
         attn::tmem_ld_32cols(tO + (uint32_t)((cq >> 1) * kHeads + hh) + lane_off, v);
         if (whole) {
-          // (all factors first, and no branch a store: with both inside the loop a result took 14 thousand cycles)
+          // (all factors first, and no branch a store: with both inside the loop a result took 14 thousand cycles, not 5; two
+          // features a store, exchanged between lanes, are no faster)
           float f[16];
           bf16 *o = a.o + (int64_t)c.n * a.o_t + (int64_t)(h0 + hh) * hd + d;
 #pragma unroll
@@ -371,14 +372,8 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
             for (int e = 0; e < 16; ++e) v[k + e] *= f[e];
           }
           if (hh + 32 <= nh && (cq >> 1) * 128 + quad * 32 + 32 <= hd) {
-            const bool odd = lane & 1;
-            o += odd ? hd - 1 : 0;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {  // two heads at a time: even lanes write the first, two features each
-              const float z = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
-              *reinterpret_cast<__nv_bfloat162 *>(o + k * hd) =
-                  odd ? __floats2bfloat162_rn(z, v[k + 1]) : __floats2bfloat162_rn(v[k], z);
-            }
+            for (int k = 0; k < 32; ++k) o[k * hd] = __float2bfloat16(v[k]);
           } else if (d < hd) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
