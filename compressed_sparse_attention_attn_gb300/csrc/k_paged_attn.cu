@@ -118,11 +118,11 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   auto lookup = [&]() -> Found {
     Found f{0, -1, -1};
     if (todo > 0) {
-      const int j = cl.t * kUnit + warp * kTile + (lane & (kTile - 1));
+      const uint32_t j = (uint32_t)cl.t * kUnit + warp * kTile + (lane & (kTile - 1));
       f.kvh = cl.hg / P.sub;
       const Row row = rows.get<kUnit, false>(a, cl.n);
-      if (j < row.rows) {
-        f.pos = row.first + j;
+      if (j < (uint32_t)row.rows) {
+        f.pos = row.first + (int)j;
         f.page = a.table[(int64_t)row.req * a.width + P.page.div((uint32_t)f.pos)];
       }
       --todo;

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         const int lo = max(row.lead - c.t * kUnit, 0), hi = min(row.rows - c.t * kUnit, kUnit);  // positions lo .. hi - 1
         x.kvh = c.hg / P.sub;
         const bool wanted = lane < nbox && lane * R < hi && (lane + 1) * R > lo;
-        const uint32_t pos = (uint32_t)(row.first + c.t * kUnit + lane * R), pg = P.page.div(pos);
+        const uint32_t pos = (uint32_t)row.first + c.t * kUnit + lane * R, pg = P.page.div(pos);
         x.row = (int)(pos - pg * P.page.d);
         x.page = wanted ? a.table[(int64_t)row.req * a.width + pg] : 0;
         const bool good = wanted && x.page >= 0 && x.page < a.c.n_pages;
@@ -566,9 +566,9 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     uint32_t ph = 1;
     for (int i = b; i < nt; i += kBufs, ph ^= 1u) {
       const Row row = rows.get<kUnit, ALIGN>(a, c.n);
-      const int j = c.t * kUnit + part * kH + lane;
-      const bool there = lane < kH && j < row.rows;
-      const uint32_t pos = (uint32_t)(row.first + j), pg = P.page.div(pos);
+      const uint32_t j = (uint32_t)c.t * kUnit + part * kH + lane;
+      const bool there = lane < kH && j < (uint32_t)row.rows;
+      const uint32_t pos = row.first + j, pg = P.page.div(pos);
       const int id = there ? a.table[(int64_t)row.req * a.width + pg] : 0;
       const bool good = there && id >= 0 && id < a.c.n_pages;
       if (there && !good) atomicOr(a.status, kStatusBadIndex);

@@ -85,7 +85,7 @@ __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report
     r.first -= r.lead;
     r.rows += r.lead;
   }
-  r.units = max(1, (r.rows + U - 1) / U);
+  r.units = r.rows > 0 ? (r.rows - 1) / U + 1 : 1;  // (rows may be 2^31 - 1: positions of the last unit pass 31 bits)
   return r;
 }
 

@@ -424,7 +424,7 @@ CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64
  * req < 0 is padding: nothing of it is written.
  * q, o bf16 [N][H][head_dim] with a stride per token (elements, multiples of 8; heads follow one another); o
  * may be q itself (same stride).  N 0: nothing to do, the rows' pointers may be NULL.
- * table int32 [R][width] of page ids; lse f32 [N][H] or NULL; sink f32 [H] or NULL.
+ * table int32 [R][width] of page ids, width * page < 2^31; lse f32 [N][H] or NULL; sink f32 [H] or NULL.
  * head_dim <= 256 with separate or shared values, or up to 512 with cache->v NULL.  A req >= R (its row is
  * left as it was), a pos past width pages (the rows past them are left out) and a page id outside
  * [0, n_pages) (its rows are left out) are caller errors, recorded in the context's status word.

@@ -673,6 +673,27 @@ def test_empty_batches(csa, ctx):
     assert info.tolist() == [0, 0, 0, 0] and length.tolist() == [5] and ctx.status() == 0
 
 
+# ------------------------------------------------------------------------------------------ at the bounds
+
+@pytest.mark.parametrize("H,kv,hd,page", [(1, 1, 64, 16), (12, 1, 128, 17), (2, 1, 512, 16), (2, 1, 512, 17)])
+def test_paged_attn_rows_up_to_2_31(csa, ctx, H, kv, hd, page):
+    """One row over the most positions that a table may hold (the table names the same pages again and again): the
+    last unit ends past 2^31.  All scores are 0 and all values of a feature the same power of two, so that the
+    result is that value and every sum before the shares are joined is exact; up to 640 roundings of the joins'
+    sums move lse by at most 640 x 2^-24."""
+    width = (2 ** 31 - 1) // page
+    rows = width * page
+    n_pages = 1024
+    row = 2.0 ** (torch.arange(hd, device="cuda") % 5 - 2)
+    k = row.to(torch.bfloat16).expand(n_pages, page, kv, hd).contiguous()
+    table = (torch.arange(width, device="cuda", dtype=torch.int32) % n_pages)[None]
+    q = torch.zeros(1, H, hd, dtype=torch.bfloat16, device="cuda")
+    o, lse = ctx.paged_attn(q, csa.PagedCache(k), table, i32([rows - 1]), 1.0, with_lse=True)
+    assert torch.equal(o, row.to(torch.bfloat16).expand(1, H, hd))
+    assert ((lse.double() - math.log(rows)).abs() <= 640 * 2.0 ** -24 + 2.0 ** -21 * math.log(rows)).all()
+    assert ctx.status() == 0
+
+
 # ------------------------------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("latent", [False, True])
