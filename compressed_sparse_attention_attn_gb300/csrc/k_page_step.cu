@@ -21,7 +21,7 @@ namespace csa {
 namespace {
 
 constexpr int kClusterCtas = 8;
-constexpr uint32_t kCap = (1u << 30) - 1;  // the sums saturate here, above every count that is accepted
+constexpr uint32_t kCap = 1u << 30;  // the sums saturate here, above every count that is accepted (two of them fit 32 bits)
 
 __device__ __forceinline__ uint32_t sat(uint32_t a, uint32_t b) { return min(a + b, kCap); }
 

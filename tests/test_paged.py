@@ -694,6 +694,28 @@ def test_paged_attn_rows_up_to_2_31(csa, ctx, H, kv, hd, page):
     assert ctx.status() == 0
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+def test_page_step_as_many_tokens_as_can_be_counted(csa, in_place):
+    """Twice 2^30 - 2 new tokens on pages that the requests hold already, N at its bound: one request's fit, two's do not."""
+    N = 2 ** 30 - 1
+    page = N
+    maps = [torch.empty(N, dtype=torch.int32, device="cuda") for _ in range(3)]
+    for new, err in (([N - 1, N - 1], 1), ([N - 1, 1], 0)):
+        t, L, S, F = i32([[0], [0]]), i32([1, 1]), i32([0, 0]), i32([7])
+        cu = i32([9, 9, 9])
+        outs = {} if in_place else dict(length_out=i32([5, 5]), state_out=i32([5, 5]))
+        info = csa.page_step(i32(new), L, t, F, S, page, *maps, cu, **outs)
+        got_l, got_s = (L, S) if in_place else (outs["length_out"], outs["state_out"])
+        assert info.tolist() == ([0, 0, 0, 1] if err else [N, 0, 0, 0])
+        assert got_l.tolist() == ([1, 1] if err else [N, 2]) and got_s.tolist() == [0, 0]
+        assert cu.tolist() == ([0, 0, 0] if err else [0, N - 1, N])
+        assert t.tolist() == [[0], [0]] and F.tolist() == [7]
+        if err:
+            assert all(bool((m == -1).all()) for m in maps)
+        else:
+            assert [int(m[N - 1]) for m in maps] == [1, 1, 1] and [int(m[N - 2]) for m in maps] == [0, N - 1, N - 1]
+
+
 # ------------------------------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("latent", [False, True])
