@@ -110,6 +110,8 @@ class PagedCache:
             if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape != k.shape or t.stride(3) != 1:
                 raise ValueError("%s: expected a CUDA bfloat16 tensor [n_pages, page, kv_heads, hd] with contiguous "
                                  "features, got %s %s, strides %s on %s" % (what, tuple(t.shape), t.dtype, t.stride(), t.device))
+        if v is not None and v.device != k.device:
+            raise ValueError("v: expected on %s as k is, got one on %s" % (k.device, v.device))
         self.k, self.v = k, v
         self.n_pages, self.page, self.kv_heads, self.head_dim = k.shape
         st = lambda t: [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]  # noqa: E731

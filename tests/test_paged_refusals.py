@@ -98,3 +98,31 @@ def test_the_binding_refuses_what_is_not_on_the_gpu():
         csa._rows(torch.zeros(2, 4, 64, dtype=torch.bfloat16), 0, "q")
     with pytest.raises(ValueError, match="CUDA"):
         csa._vec(torch.zeros(4, dtype=torch.int32), 4, torch.int32, 0, "pos")
+
+
+class OnDevice:
+    """Stands for a CUDA tensor: what the binding asks of one, and no memory."""
+    is_cuda, dtype, shape = True, torch.bfloat16, torch.Size((4, 16, 2, 64))
+
+    def __init__(self, index):
+        self.index, self.device = index, torch.device("cuda", index)
+
+    def dim(self):
+        return 4
+
+    def stride(self, i=None):
+        s = (2048, 128, 64, 1)
+        return s if i is None else s[i]
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return A
+
+
+def test_the_binding_refuses_a_cache_over_two_devices():
+    assert csa.PagedCache(OnDevice(1), OnDevice(1)).device == 1
+    for k, v in ((0, 1), (1, 0)):
+        with pytest.raises(ValueError, match="v: expected on cuda:%d" % k):
+            csa.PagedCache(OnDevice(k), OnDevice(v))
