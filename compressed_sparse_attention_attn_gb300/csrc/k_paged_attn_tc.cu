@@ -9,8 +9,10 @@
 //                                         m is raised only by more than 2^8 (the sums so far are then rescaled)
 //   O^T[d][h] += sum_r K[r][d] p[h][r]    M = 4 x 128 features, N = 64 heads, K = 48 positions (the same tile read
 //                                         as an MN-major operand)
-// p rounded to bf16 is off by at most 2^-8 of itself, which moves O by at most 2^-8 sum_r w_r |K_rd| (a second
-// term for what the rounding leaves would double the products of the values); scores, maxima, sums and O are f32.
+// p is rounded to bf16, by at most 2^-8 of itself: a second term for what the rounding leaves would double the products of
+// the values, and its tiles do not fit beside q and three tiles of rows.  O's denominator adds up the rounded
+// p, so that its weights still add up to 1 (with the sink's): O moves by at most 2^-8 sum_r w_r |K_rd - O_d|, and a feature
+// that all rows share by nothing.  lse is of the p as they were.  Scores, maxima, sums and O are f32.
 //
 // Shared memory holds q (64 KB) and three tiles (48 KB each): one whose values are used, one whose scores are, one in flight
 // (two of 64 positions took 217 against 182 us over 64 rows of 12 to 16 thousand).  Tiles come by TMA, boxes of up to 16 rows inside
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
     attn::cp_async_wait_all();
     attn::fence_proxy_async();
     tc::mbar_arrive(q_full);
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: of this thread's positions
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};  // l, lr: of this thread's positions; lr as rounded
     int nseg = 0;
     bool first = true;
     int seg = 0;  // the segment's first tile here
@@ -233,6 +235,7 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
       if (lane == 0) flags[4 * b + warp] = any ? 1 : 0;
       __syncwarp();
       tc::mbar_arrive(&stat[b]);
+      uint32_t pk[2][kJ];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float ref = m[x] == -INFINITY ? 0.f : m[x];
@@ -243,15 +246,22 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         for (int j = 0; j < kJ; ++j) {
           const float p0 = ex2(fmaf(s[4 * j + 2 * x], sc, -ref)), p1 = ex2(fmaf(s[4 * j + 2 * x + 1], sc, -ref));
           sum += p0 + p1;
-          const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + ((j ^ (h & 7)) << 4)), "r"(*reinterpret_cast<const uint32_t *>(&pk))
-                       : "memory");
+          const __nv_bfloat162 pr = __floats2bfloat162_rn(p0, p1);
+          pk[x][j] = *reinterpret_cast<const uint32_t *>(&pr);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(prow + ((j ^ (h & 7)) << 4)), "r"(pk[x][j]) : "memory");
         }
         l[x] = l[x] * al[x] + sum;
       }
       attn::fence_proxy_async();
       tc::tc_fence_before();
       tc::mbar_arrive(&p_full[b]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {  // (behind what the products wait for)
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) sum += __uint_as_float(pk[x][j] << 16) + __uint_as_float(pk[x][j] & 0xffff0000u);
+        lr[x] = lr[x] * al[x] + sum;
+      }
       first = false;
       if (last) {
         const int kvh = c.hg / P.sub, sg = c.hg - kvh * P.sub;
@@ -262,21 +272,24 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
         for (int x = 0; x < 2; ++x) {
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
           l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+          lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], 1);
+          lr[x] += __shfl_xor_sync(0xffffffffu, lr[x], 2);
           const int h = hA + 8 * x;
           float fo = 1.f;
           if (qc == 0 && h < nh) {
             if (whole) {
-              fo = out_factor(m[x], l[x], a.sink, h0 + h);
+              fo = out_factor(m[x], lr[x], a.sink, h0 + h);
               if (a.lse)
                 a.lse[(int64_t)c.n * a.H + h0 + h] = l[x] == 0.f ? -INFINITY : (m[x] + log2f(l[x])) * 0.6931471805599453f;
             } else {
               const int slot = 2 * blockIdx.x + (seg == sb ? 1 : 0);
-              *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + h) * 2) = make_float2(m[x], l[x]);
+              *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + h) * 2) = make_float2(m[x], lr[x]);
+              P.share_l[(int64_t)slot * kHeads + h] = l[x];
             }
           }
           if (qc == 0) f_sm[(nseg & 1) * kHeads + h] = fo;
           m[x] = -INFINITY;
-          l[x] = 0.f;
+          l[x] = lr[x] = 0.f;
         }
         __syncwarp();
         tc::mbar_arrive(&fin[nseg & 1]);
@@ -619,7 +632,7 @@ constexpr int kJoinThreads = 256, kJoinChunk = 64, kJoinLanes = kJoinChunk / 4, 
 constexpr int kJoinShares = 6, kJoinSplit = 4;
 __global__ void __launch_bounds__(kJoinThreads, 4) k_paged_join_latent(const __grid_constant__ Params P) {
   __shared__ float4 s_v[kJoinGroups][kJoinLanes];
-  __shared__ float2 s_ml[kJoinGroups];
+  __shared__ float3 s_ml[kJoinGroups];
   const PagedAttnArgs &a = P.a;
   dependency_wait();
   const int2 sp = P.split[blockIdx.x];
@@ -637,11 +650,16 @@ __global__ void __launch_bounds__(kJoinThreads, 4) k_paged_join_latent(const __g
   for (int it0 = blockIdx.y * per; it0 < nh * chunks; it0 += gridDim.y * per) {
     const int it = it0 + grp / G, h = it / chunks, d = (it - h * chunks) * kJoinChunk + lane * 4;
     const bool in = h < nh && d < hd;
-    float M = -INFINITY, Lp = 0.f;
+    float M = -INFINITY, Lr = 0.f;  // (of the rounded weights)
+    float L = 0.f;                  // of the weights as they were: share u of a round in lane u
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = sub; p0 < parts && h < nh; p0 += G * kJoinShares) {
       float4 x[kJoinShares];
       float2 ml[kJoinShares];
+      const int pl = p0 + lane * G;
+      const float l = lane < kJoinShares && pl < parts
+                          ? __ldcg(P.share_l + (int64_t)(pl == 0 ? 2 * c0 + 1 : 2 * (c0 + pl)) * kHeads + h)
+                          : 0.f;
 #pragma unroll
       for (int u = 0; u < kJoinShares; ++u) {
         const int p = p0 + u * G;
@@ -658,31 +676,36 @@ __global__ void __launch_bounds__(kJoinThreads, 4) k_paged_join_latent(const __g
       for (int u = 0; u < kJoinShares; ++u) mx = fmaxf(mx, ml[u].x);
       const float f0 = M == -INFINITY ? 0.f : exp2f(M - mx);
       M = mx;
-      Lp *= f0;
+      Lr *= f0;
+      L *= f0;
       v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
 #pragma unroll
       for (int u = 0; u < kJoinShares; ++u) {
         const float e = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - M);
-        Lp = fmaf(ml[u].y, e, Lp);
+        Lr = fmaf(ml[u].y, e, Lr);
+        if (lane == u) L = fmaf(l, e, L);
         v.x = fmaf(x[u].x, e, v.x);
         v.y = fmaf(x[u].y, e, v.y);
         v.z = fmaf(x[u].z, e, v.z);
         v.w = fmaf(x[u].w, e, v.w);
       }
     }
+#pragma unroll
+    for (int o = kJoinLanes / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (G > 1) {  // (uniform over the block)
       s_v[grp][lane] = v;
-      if (lane == 0) s_ml[grp] = make_float2(M, Lp);
+      if (lane == 0) s_ml[grp] = make_float3(M, Lr, L);
       __syncthreads();
       if (sub == 0) {
         for (int k = 1; k < G; ++k) M = fmaxf(M, s_ml[grp + k].x);
-        Lp = 0.f;
+        Lr = L = 0.f;
         v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < G; ++k) {
-          const float2 ml = s_ml[grp + k];
+          const float3 ml = s_ml[grp + k];
           const float4 x = s_v[grp + k][lane];
           const float e = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-          Lp = fmaf(ml.y, e, Lp);
+          Lr = fmaf(ml.y, e, Lr);
+          L = fmaf(ml.z, e, L);
           v.x = fmaf(x.x, e, v.x);
           v.y = fmaf(x.y, e, v.y);
           v.z = fmaf(x.z, e, v.z);
@@ -692,11 +715,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4) k_paged_join_latent(const __g
       __syncthreads();
     }
     if (sub == 0 && in) {
-      const float fo = out_factor(M, Lp, a.sink, h0 + h);
+      const float fo = out_factor(M, Lr, a.sink, h0 + h);
       const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * fo, v.y * fo), hi = __floats2bfloat162_rn(v.z * fo, v.w * fo);
       *reinterpret_cast<uint2 *>(a.o + (int64_t)n * a.o_t + (int64_t)(h0 + h) * hd + d) =
           make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-      if (a.lse && d == 0) a.lse[(int64_t)n * a.H + h0 + h] = Lp == 0.f ? -INFINITY : (M + log2f(Lp)) * 0.6931471805599453f;
+      if (a.lse && d == 0) a.lse[(int64_t)n * a.H + h0 + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
   }
 }
@@ -734,9 +757,10 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * kHeads * kHD;
   p.split = reinterpret_cast<int2 *>(p.share_ml + 2 * grid * kHeads * 2);
+  p.share_l = reinterpret_cast<float *>(p.split + grid);
   p.by_segment = segments <= grid;
   p.ctas = (int)grid;
-  if (sizeof(float) * 2 * grid * kHeads * (kHD + 2) + sizeof(int2) * grid > ws_bytes) return cudaErrorInvalidValue;
+  if (sizeof(float) * 2 * grid * kHeads * (kHD + 3) + sizeof(int2) * grid > ws_bytes) return cudaErrorInvalidValue;
   e = tma ? launch_dependent(k_paged_attn_latent<true>, dim3((unsigned)grid), dim3(kThreads<true>), smem, s, 1, p, pg)
           : launch_dependent(k_paged_attn_latent<false>, dim3((unsigned)grid), dim3(kThreads<false>), smem, s, 1, p, pg);
   if (e != cudaSuccess || segments == units) return e;  // (one tile a segment: nothing is shared)

@@ -47,7 +47,8 @@ struct Params {
   int g, sub, Hg;       // query heads a kv head, head groups a kv head, segments a row
   float scale_log2;     // softmax scale * log2(e)
   float *share_o;       // [2 G][heads of a group][padded head_dim]
-  float *share_ml;      // [2 G][heads of a group][2]
+  float *share_ml;      // [2 G][heads of a group][2]: M, L (latent rows: L of the weights as the product takes them)
+  float *share_l;       // latent rows: [2 G][heads of a group], L of the weights as they were
   int *counters;        // [3][2][kMaxCtas]: for each step of joining, groups past a segment's first, first groups
   int2 *split;          // latent rows: of the segments that several CTAs shared, the first CTA and how many
   int ctas;             // CTAs launched

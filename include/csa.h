@@ -420,8 +420,11 @@ CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64
  * pos[n] (window 0: from 0) of request req[n] (req NULL: request n), its own just-written row among them.
  * Query head h uses kv head h / (H / kv_heads).  S_j = scale q_h . K_j, O = sum_j e^{S_j} V_j / (e^{sink_h} +
  * sum_j e^{S_j}) (sink NULL: without that term), lse = ln sum_j e^{S_j} (without the sink); scores, maxima and
- * sums in f32, O rounded once to bf16.  pos -1: no rows, O = 0 and lse = -inf.  A row with pos < -1 or
- * req < 0 is padding: nothing of it is written.
+ * sums in f32, O rounded once to bf16.  The weights e^{S_j} enter the product with the values as two bf16 terms
+ * (about 16 bits), for head_dim above 256 as one; there the sum below O is of the same rounded weights, so that they
+ * add up to 1, and lse is of the f32 ones.  An infinity or a NaN in an attended row leaves results that it enters
+ * infinite or NaN.  pos -1: no rows, O = 0 and lse = -inf.  A row with pos < -1 or req < 0 is padding: nothing of it
+ * is written.
  * q, o bf16 [N][H][head_dim] with a stride per token (elements, multiples of 8; heads follow one another); o
  * may be q itself (same stride).  N 0: nothing to do, the rows' pointers may be NULL.
  * table int32 [R][width] of page ids, width * page < 2^31; lse f32 [N][H] or NULL; sink f32 [H] or NULL.

@@ -673,6 +673,31 @@ def test_empty_batches(csa, ctx):
     assert info.tolist() == [0, 0, 0, 0] and length.tolist() == [5] and ctx.status() == 0
 
 
+@pytest.mark.parametrize("H,kv,hd,latent", [(8, 2, 128, False), (16, 1, 256, True), (64, 1, 512, True), (70, 1, 320, True)])
+def test_paged_attn_weights_add_up_to_one(csa, ctx, H, kv, hd, latent):
+    """A feature that is the same in all rows comes back as it is: what the weights are rounded to for their product
+    is what the denominator adds up.  Every 40th row scores higher than the others by so much that a weight of the
+    others, 2^-0.99442 = 1.003875 / 2, lies just below a border of bf16's (1 + 2^-8) / 2 and loses 2^-8.04 of itself:
+    with the weights as they were in the denominator, 1.9921875 would become 1.984375.  The f32 errors of a sum of 4000
+    products are at most 2^-12 of it, half a step is 2^-9.  lse is of the weights as they were."""
+    lens, page, scale, same = [40, 4000, 1, 160], 16, 0.68928, 255 / 128
+    R, per = len(lens), 4000 // 16
+    k = torch.full((R * per, page, kv, hd), same, dtype=torch.bfloat16, device="cuda")
+    k[..., 0] = 0
+    k.view(R, per * page, kv, hd)[:, 20::40, :, 0] = 1
+    v = None if latent else k.clone()
+    q = torch.zeros(R, H, hd, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    table = torch.arange(R * per, device="cuda", dtype=torch.int32).view(R, per)
+    o, lse = ctx.paged_attn(q, csa.PagedCache(k, v), table, i32([x - 1 for x in lens]), scale, with_lse=True)
+    assert (o[..., 1:].float() == same).all()
+    for r, n in enumerate(lens):
+        high = len(range(20, n, 40))
+        want = math.log(high * math.exp(scale) + n - high)
+        assert ((lse[r].double() - want).abs() <= 2.0 ** -20 * (1 + want) + n * 2.0 ** -24).all()
+    assert ctx.status() == 0
+
+
 # ------------------------------------------------------------------------------------------ at the bounds
 
 @pytest.mark.parametrize("H,kv,hd,page", [(1, 1, 64, 16), (12, 1, 128, 17), (2, 1, 512, 16), (2, 1, 512, 17)])
