@@ -13,8 +13,8 @@ point, and the CPU oracle timed on a bounded sample.
 Timing: W untimed steps, then K steps captured once as a CUDA graph and replayed, each bracketed
 by CUDA events on the launching stream; L2 is flushed (a 512 MiB memset) between timed steps and
 outside the event pair.  N > 1 (torchrun): every rank runs the full workload on its own GPU
-(replicas, weak scaling, no collective on the data path); value = all ranks' tokens / the slowest
-rank's time.
+(replicas, weak scaling, no collective on the data path, no TMA multicast); value = all ranks' tokens /
+the slowest rank's time.
 """
 import argparse
 import ctypes
@@ -674,6 +674,8 @@ def main():
         import torch
         import torch.distributed as dist_
         os.environ.setdefault("MASTER_ADDR", "127.0.0.1")
+        import compressed_sparse_attention_attn_gb300 as csa
+        csa.multicast(False)  # for GPUs that work alone
         torch.cuda.set_device(int(os.environ.get("LOCAL_RANK", 0)))
         dist_.init_process_group("nccl")
         dist = dist_

@@ -422,6 +422,12 @@ class Context:
         return out if lse is None else (out, lse)
 
 
+def multicast(allow=None):
+    """csa_multicast: let this process's launches use TMA multicast or not (None: leave it); returns what held
+    before.  A rank of a job over several GPUs turns it off first."""
+    return bool(lib().csa_multicast(-1 if allow is None else int(bool(allow))))
+
+
 def rmsnorm(x, w, eps, out=None, stream=None):
     N = x.shape[-1]
     out = torch.empty_like(x) if out is None else out

@@ -83,6 +83,7 @@ SIGNATURES = {
     "csa_linear_noalloc": (I, [P, I, I, I, P, I, I, P, I, I, P]),
     "csa_linear_noalloc_status": (I, [I]),
     "csa_debug_stall": (I, [ctypes.c_ulonglong]),
+    "csa_multicast": (I, [I]),
     "csa_linear_fp8w": (I, [P, P, I, I, I, P, P, I, I, P, I, I, P]),
     "csa_compress": (I, [P, ctypes.POINTER(LayerWeights), ctypes.POINTER(LayerState), P, I, I, I,
                          ctypes.POINTER(Shared), P, P]),

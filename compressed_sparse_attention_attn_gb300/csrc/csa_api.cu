@@ -174,6 +174,12 @@ static int check_cfg(const csa_cfg *c) {
   return CSA_OK;
 }
 
+int csa_multicast(int allow) {
+  const int before = csa::multicast_allowed() ? 1 : 0;
+  if (allow >= 0) csa::allow_multicast(allow != 0);
+  return before;
+}
+
 int csa_create(const csa_cfg *cfg, csa_ctx **out) {
   if (!out) return fail(CSA_ERR_ARG, "out is NULL");
   *out = nullptr;
@@ -825,7 +831,7 @@ int attn_v41_forward(csa_ctx *ctx, const csa_layer_weights *w, csa_layer_state *
     // and it is itself one of the kernel before (the layer's input is read after the wait)
     for (int i = 0; i < np; ++i) px[i].pdl = 1;
     // many tokens and one slice: the paired-CTA kernel writes the f32 slice itself
-    bool paired = S == 1 && NT >= 2048;
+    bool paired = S == 1 && NT >= 2048 && csa::multicast_allowed();
     for (int i = 0; i < np; ++i) paired = paired && csa::gemm_tc_supported(px[i]);
     if (paired)
       STEP(csa::launch_gemm_tc(px, np, ctx->ws, ctx->gemm_ws_bytes(), ctx->num_sms, ctx->status, s), "proj x");

@@ -116,6 +116,8 @@ cudaError_t launch_gemm_tc(const LinearProblem *probs, int nprob, float *ws, siz
 // The largest split count S <= max_S dividing the problems' k-slices with tiles * S <= max_ctas (>= 1).
 int gemm_tc_split_count(const LinearProblem *probs, int nprob, int max_ctas, int max_S);
 bool gemm_tc_supported(const LinearProblem &q);
+bool multicast_allowed();  // TMA multicast between the CTAs of a cluster (csa_multicast)
+void allow_multicast(bool on);
 
 // The window rows and the query latent from split-K partials of [wq_a | wkv | weights_proj] x:
 // per token, the sum of the S slices rounded to bf16 (linear_bf16), then qr = RMSNorm * q_norm,

@@ -22,13 +22,15 @@
 // together are consecutive ones whose operands share L2, then Stream-K over the last partial wave.
 // Launches of 2048 tokens or more on bf16 weights go one step further, to k_gemm_tc_pairs: clusters
 // of two CTAs on neighbouring weight tiles of one 256-token tile, each copying half of the token
-// tile and multicasting it into both (a third less L2 operand traffic a CTA).
+// tile and multicasting it into both (a third less L2 operand traffic a CTA).  TMA multicast is for a
+// process whose GPU works alone (csa_multicast): elsewhere those launches stay with the kernels above.
 // L2 policies follow the reuse: weights read by one token tile only stream past evict-first,
 // activations small next to L2 stay evict-last, everything else is normal.
 //
 // Warp roles (192 threads): warps 0-3 epilogue (TMEM lane quadrant = warp), warp 4 TMA producer,
 // warp 5 TMEM allocation + MMA issue.  Every mbarrier wait is time-bounded; a timeout raises the
 // device status word and the CTA drains its copies and MMAs, frees TMEM and exits.
+#include <atomic>
 #include <mutex>
 
 #include "csa_internal.cuh"
@@ -1428,6 +1430,21 @@ static void unify_policies(gemm::Params &P, int nprob) {
   }
 }
 
+// Whether launches may use TMA multicast: what csa_multicast said last, else whether this process sees one
+// GPU only (a rank of a job over several usually sees all of them).
+static std::atomic<int> g_multicast{-1};
+bool multicast_allowed() {
+  const int said = g_multicast.load(std::memory_order_relaxed);
+  if (said >= 0) return said != 0;
+  static const bool alone = [] {
+    int n = 0;
+    if (cudaGetDeviceCount(&n) != cudaSuccess) (void)cudaGetLastError();  // (no GPU: nothing is launched)
+    return n <= 1;
+  }();
+  return alone;
+}
+void allow_multicast(bool on) { g_multicast.store(on ? 1 : 0, std::memory_order_relaxed); }
+
 int gemm_tc_bn(int M, bool f8) {
   if (M > 256) return f8 ? 128 : 256;  // (fp8 stages hold two k-slices: 256-token tiles leave room for one)
   int bn = (M + 15) / 16 * 16;
@@ -1460,7 +1477,7 @@ cudaError_t launch_gemm_tc(const LinearProblem *probs, int nprob, float *ws, siz
                          : std::min(8, ((f8 ? 222 : 200) * 1024 - conv_bytes) / stage_bytes);
   if (P.stages < 2) return cudaErrorInvalidValue;
   // many token tiles (prefill): clusters of two CTAs on adjacent weight tiles sharing the token tile
-  const bool pairs = !f8 && P.BN == 256 && ATOMS == 1 && M >= 2048;
+  const bool pairs = !f8 && P.BN == 256 && ATOMS == 1 && M >= 2048 && multicast_allowed();
   for (int i = 0; i < nprob; ++i)  // an f32 result (a split-K slice layout) only from the paired kernel
     if (probs[i].part && !pairs) return cudaErrorInvalidValue;
   int units = 0, tiles = 0;

@@ -81,3 +81,31 @@ def test_reference_arm_prints_one_contract_line():
     cb = d["cpu_baseline"]
     assert cb["kind"] == "oracle" and cb["value"] == d["value"] and cb["cores"] >= 1 and cb["sample"]
     assert d["e2e"] == {"value": d["value"], "unit": d["unit"], "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0}
+
+
+def test_ranks_of_a_job_run_without_multicast(monkeypatch):
+    """Two ranks or more: TMA multicast is off before the process group, the inputs or any launch; one process alone
+    leaves it as it is."""
+    import bench
+    import compressed_sparse_attention_attn_gb300 as csa
+    from compressed_sparse_attention_attn_gb300 import _build
+    _build.build()
+    seen = []
+    monkeypatch.setattr(torch.cuda, "set_device", lambda d: seen.append(csa.multicast()))
+    monkeypatch.setattr(dist, "init_process_group", lambda backend: seen.append(csa.multicast()))
+    monkeypatch.setattr(dist, "barrier", lambda: None)
+    monkeypatch.setattr(dist, "destroy_process_group", lambda: None)
+    monkeypatch.setattr(bench, "run_csa", lambda args, rank, world, d: seen.append(csa.multicast()) or (None, None))
+    monkeypatch.setattr(sys, "argv", ["bench.py", "--gpus", "2"])
+    monkeypatch.setenv("RANK", "1")
+    before = csa.multicast(True)
+    try:
+        monkeypatch.setenv("WORLD_SIZE", "2")
+        bench.main()
+        assert seen == [False] * 3
+        assert csa.multicast(True) is False and csa.multicast() is True
+        monkeypatch.setenv("WORLD_SIZE", "1")
+        bench.main()
+        assert seen[3:] == [True]
+    finally:
+        csa.multicast(before)
