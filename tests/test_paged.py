@@ -698,6 +698,143 @@ def test_paged_attn_weights_add_up_to_one(csa, ctx, H, kv, hd, latent):
     assert ctx.status() == 0
 
 
+# ------------------------------------------------------------------------------------------ kernels by size, alignment and heads
+
+@pytest.mark.parametrize("R,width,N", [(300, 1100, 900), (257, 1025, 2048), (256, 1100, 300), (2049, 40, 2048), (2048, 40, 2049)])
+def test_page_step_long_tables(csa, R, width, N):
+    """Both sides of the rule for one CTA or eight: by the tables' width, the requests and the tokens."""
+    rng = np.random.default_rng(R + width)
+    lens = rng.integers(0, 30 * 16, R)
+    lens[rng.integers(0, R, 5)] = (width - 3) * 16 + 7 if width > 100 else 37 * 16
+    steps = []
+    for _ in range(2):
+        new = rng.integers(-1, 2, R)
+        new[np.cumsum(np.maximum(new, 0)) > N - 20] = 0
+        new[3] = 20
+        steps.append(new.tolist())
+    lens[3] = 5
+    n_pages = int(sum(-(-x // 16) for x in lens)) + 2 * (N + R)
+    check_step(csa, lens.tolist(), steps, 16, n_pages, width, N, n_pages - 5, seed=R)
+
+
+@pytest.mark.parametrize("case,bit", [("tokens", 1), ("negative length", 2), ("width", 2), ("pool", 4), ("state", 8), ("overfull", 8)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_page_step_errors_over_eight_ctas_change_nothing(csa, case, bit, in_place):
+    """An error in the middle of a large step: nothing of it is done by any CTA."""
+    R, N, page, width, n_pages = 3000, 5000, 4, 30, 60000
+    rng = np.random.default_rng(7)
+    lens = rng.integers(0, 100, R)
+    new = rng.integers(-1, 3, R)
+    lens[1700], new[1700] = 17, 1
+    held = int(sum(-(-x // page) for x in lens))
+    head, count = 39000, n_pages - held
+    if case == "tokens":
+        new[1700] = N
+        lens[1700] = 0
+        width = 1300
+    elif case == "negative length":
+        lens[1700] = -2
+    elif case == "width":
+        lens[1700] = width * page
+    elif case == "pool":
+        count = 10
+    elif case == "state":
+        head = n_pages
+    elif case == "overfull":
+        count = n_pages - 5
+    t = torch.randint(0, n_pages, (R, width), dtype=torch.int32, device="cuda")
+    F = torch.randperm(n_pages, device="cuda").to(torch.int32)
+    L, S = i32(lens), i32([head, count])
+    keep = [x.clone() for x in (t, F, L, S)]
+    maps = [torch.full((N,), 5, dtype=torch.int32, device="cuda") for _ in range(3)]
+    cu = torch.full((R + 1,), 9, dtype=torch.int32, device="cuda")
+    outs = {} if in_place else dict(length_out=torch.full_like(L, 3), state_out=torch.full_like(S, 3))
+    info = csa.page_step(i32(new), L, t, F, S, page, *maps, cu, **outs)
+    assert info.tolist() == [0, 0, 0, bit]
+    assert all(torch.equal(a, b) for a, b in zip((t, F, L, S), keep))
+    if not in_place:
+        assert torch.equal(outs["length_out"], L) and torch.equal(outs["state_out"], S)
+    assert (cu == 0).all() and all((m == -1).all() for m in maps)
+
+
+@pytest.mark.parametrize("hd,rd,at", [(64, 64, 0), (128, 64, 64), (80, 32, 48), (256, 256, 0), (512, 64, 448), (576, 64, 512)])
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("off", [(1, 0), (0, 2), (3, 2), (2, 2)])
+def test_norm_rope_tables_of_any_alignment(csa, ctx, hd, rd, at, half, off):
+    """Weights that start on any 4 bytes and angles on any 8 of their buffers."""
+    N, H, kv, page = 11, 3, 2, 8
+    g = gen(hd + off[0])
+    q, k, v = randn(g, N, H, hd), randn(g, N, kv, hd), randn(g, N, kv, hd)
+    wbuf = 1 + 0.2 * torch.randn(2 * hd + 8, generator=g, device="cuda")
+    qw, kw = wbuf[off[0]:off[0] + hd], wbuf[hd + 4 + off[0]:2 * hd + 4 + off[0]]
+    tbuf = torch.empty(90 * rd + 4, device="cuda")
+    tab = tbuf[off[1]:off[1] + 90 * rd].view(90, rd // 2, 2)
+    tab.copy_(rope_tab(90, rd))
+    pos = torch.randint(0, 90, (N,), generator=g, device="cuda").to(torch.int32)
+    slot = torch.randperm(16, generator=g, device="cuda")[:N].to(torch.int32)
+    kp, vp = (torch.zeros(2, page, kv, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out = ctx.qk_norm_rope(q, k, v, csa.PagedCache(kp, vp), pos, slot, tab=tab, rd=rd, rope_at=at, half=half, q_norm=qw,
+                           k_norm=kw, eps=1e-6)
+    s = slot.long()
+    close_rows(out, ref_rows(q, qw, 1e-6, tab, pos, rd, at, half), "q")
+    close_rows(kp[s // page, s % page], ref_rows(k, kw, 1e-6, tab, pos, rd, at, half), "k")
+    assert torch.equal(vp[s // page, s % page], v) and ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd,latent", [(48, 2, 64, False), (100, 1, 64, True), (33, 1, 64, False), (51, 3, 128, False),
+                                            (64, 1, 256, True), (17, 1, 256, False)])
+def test_paged_attn_many_heads_a_kv_head(csa, ctx, H, kv, hd, latent):
+    """Head groups past the first, the last of them partly filled."""
+    lens = [1, 0, 70, 333, 2000, 5]
+    b = Batch(lens, H, kv, hd, 16, latent, seed=H)
+    pos = [x - 1 for x in lens]
+    q = b.queries(len(lens))
+    sink = torch.randn(H, generator=b.g, device="cuda")
+    o, lse = ctx.paged_attn(q, csa.PagedCache(b.k, b.v), b.table, i32(pos), b.scale, sink=sink, with_lse=True)
+    check_rows(b, q, o, lse, pos, None, sink)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd,latent", [(8, 2, 128, False), (24, 2, 64, False), (4, 1, 256, True), (64, 1, 512, True)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_paged_attn_values_that_are_not_finite(csa, ctx, H, kv, hd, latent, bad):
+    """A NaN or an infinity in an attended row: results that it enters are not finite, every other request's are as without
+    it, and so are those of rows that end before it."""
+    lens = [300, 2500, 40, 2500]
+    b = Batch(lens, H, kv, hd, 16, latent, seed=2)
+    q = b.queries(6)
+    cache = csa.PagedCache(b.k, b.v)
+    req, pos = [0, 1, 2, 3, 1, 1], [299, 2499, 39, 2499, 1199, 2000]
+    args = (q, cache, b.table, i32(pos), b.scale)
+    want, want_lse = ctx.paged_attn(*args, req=i32(req), with_lse=True)
+    page, at = int(b.table[1, 1200 // 16]), 1200 % 16
+    if latent:
+        b.k[page, at, 0, 3] = bad
+    else:
+        b.v[page, at, 1, 3] = bad
+    o, lse = ctx.paged_attn(*args, req=i32(req), with_lse=True)
+    hit = [1, 5]
+    kept = [n for n in range(6) if n not in hit]
+    assert torch.equal(o[kept], want[kept]) and torch.equal(lse[kept], want_lse[kept])
+    if latent:  # (the row's score is an infinity or NaN too: it takes the whole head, or leaves it but for the feature)
+        assert not o[hit][..., 3].isfinite().any()
+        nan_head = lse[hit].isnan() | lse[hit].isposinf()
+        assert o[hit].isnan()[nan_head].all()
+    else:
+        g = H // kv
+        assert not o[hit][:, g:, 3].isfinite().any() and torch.equal(lse[hit], want_lse[hit])
+        rest = [d for d in range(hd) if d != 3]
+        assert torch.equal(o[hit][:, :, rest], want[hit][:, :, rest]) and torch.equal(o[hit][:, :g], want[hit][:, :g])
+    # a key: the whole head
+    if not latent:
+        b.v[page, at, 1, 3] = 0
+        b.k[page, at, 1, :] = float("nan")
+        o, lse = ctx.paged_attn(*args, req=i32(req), with_lse=True)
+        assert o[hit][:, g:].isnan().all() and lse[hit][:, g:].isnan().all() and torch.equal(o[hit][:, :g], want[hit][:, :g])
+        assert torch.equal(o[kept], want[kept])
+    assert ctx.status() == 0
+
+
 # ------------------------------------------------------------------------------------------ at the bounds
 
 @pytest.mark.parametrize("H,kv,hd,page", [(1, 1, 64, 16), (12, 1, 128, 17), (2, 1, 512, 16), (2, 1, 512, 17)])
