@@ -21,9 +21,10 @@
 // as soon as its weights are there.  Four warps do the softmax, and load the next segment's q behind the last
 // scores that read it; four rescale O and write it out.  All waits are time-bounded.
 //
-// 64 x 1 over 12 to 16 thousand rows: 175 us, 5.3 TB/s (79 % of a copy); of the 2500 to 2800 cycles of a tile the products take
-// 1300, and the rest is what their hand-overs take: scores to softmax to values.  32 x 1 over about 900 rows (5 tiles a CTA): 20 us, of
-// which the shares' 128 KB a CTA take 2 us to write and 5 us to join.
+// 64 x 1 over 12 to 16 thousand rows: 176 us, 5.3 TB/s (79 % of a copy); of the 2550 cycles that an SM is active for each of its
+// 124 tiles, the segments' ends among them, the products take 1300, and most of the rest is what their hand-overs take:
+// scores to softmax to values.  32 x 1 over about 900 rows (4 tiles a CTA): 20 us, of which the shares' 128 KB a CTA take 2 us to
+// write and 5 us to join.
 #include <algorithm>
 #include <cstring>
 
@@ -150,8 +151,8 @@ __global__ void __launch_bounds__(kThreads<TMA>, 1) k_paged_attn_latent(const __
 
   if (warp < 4) {
     // ------------------------------------------------------------------------------ softmax
-    // The scores' 64 rows lie in the first 16 lanes of each quarter of tensor memory; a thread holds 16 positions of two
-    // heads, hA and hB = hA + 8, a head's 64 positions the four lanes of a quad.
+    // The scores' 64 rows lie in the first 16 lanes of each quarter of tensor memory; a thread holds 12 positions of two
+    // heads, hA and hB = hA + 8, a head's 48 positions the four lanes of a quad.
     const int hA = 16 * warp + (lane >> 2), qc = 2 * (lane & 3);
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     auto load_q = [&](const Cursor &k) {

@@ -90,8 +90,8 @@ __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report
   return r;
 }
 
-// A CTA's range: the row, head group and unit it begins with and its units.  Places are counted in 32 bits: a call whose rows
-// come to 2^31 or more (2^35 positions and heads at least) does nothing but report it.
+// A CTA's range: the row, head group and unit it begins with and its units.  Places are counted in 31 bits: a call whose
+// segments come to 2^31 or more of them (an empty row has 1 + W too) does nothing but report it.
 struct Range {
   int row, hg, t;        // t may be behind the segment's units (then the next segment's first unit is meant)
   uint32_t base;         // first place of that segment

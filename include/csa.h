@@ -440,8 +440,9 @@ CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64
  * [0, n_pages) (its rows are left out) are caller errors, recorded in the context's status word.
  * Rows of different length are dealt evenly over the device and joined in a fixed order (the same inputs give
  * the same bits), for head_dim <= 256 within the one launch, above by a second one; the shares lie in the
- * context's workspace.  Rows that come to more than 2^31 units (of 16 to 96 positions of a head group) are a caller
- * error too: the call then writes nothing. */
+ * context's workspace.  A call's work is counted in 31 bits: a unit for every 64 positions (48 or 96 for head_dim
+ * above 128, 48 above 256) of a row and group of 8, 16 or (above 256) 64 query heads, one at least, and one more (above 256
+ * two) for the row and group.  Rows that come to 2^31 or more are a caller error too: the call then writes nothing. */
 CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
                            const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos,
                            const float *sink, float scale, int window, csa_bf16 *o, int64_t o_t, float *lse,
