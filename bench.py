@@ -670,12 +670,12 @@ def main():
     if args.impl == "reference":
         run_reference(args, rank, world)
         return
+    import compressed_sparse_attention_attn_gb300 as csa
+    csa.multicast(world == 1)  # for a GPU that works alone
     if world > 1:
         import torch
         import torch.distributed as dist_
         os.environ.setdefault("MASTER_ADDR", "127.0.0.1")
-        import compressed_sparse_attention_attn_gb300 as csa
-        csa.multicast(False)  # for GPUs that work alone
         torch.cuda.set_device(int(os.environ.get("LOCAL_RANK", 0)))
         dist_.init_process_group("nccl")
         dist = dist_

@@ -410,7 +410,8 @@ CSA_API int csa_page_step(const int32_t *new_len, int R, int page, const int32_t
  * (c, s) = tab[pos[n]][i], tab f32 [tab_rows][rd/2][2] (csa_rope_table_get's layout; tables scaled for long
  * contexts come in through it).  Value rows are copied.
  * q [N][H][head_dim], k and v [N][cache->kv_heads][head_dim] with element strides per token and head (x_t, x_h,
- * multiples of 8, 16-byte aligned bases); q_out likewise, it may be q itself.  pos, slot int32 [N].
+ * multiples of 8, 16-byte aligned bases); q_out likewise, it may be q itself (same strides), else its rows lie
+ * apart from those of q, k and v.  pos, slot int32 [N].
  * A token with pos < 0 is padding: nothing of it is written.  slot -1: only its query is produced.
  * cache->v NULL: v is not read (may be NULL).  q NULL: keys and values only.  slot NULL: token n goes to row
  * n.  No two tokens may have the same slot, k, v may not overlap the cache, and rows that are written (of the
@@ -433,7 +434,7 @@ CSA_API int csa_qk_norm_rope(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int64
  * infinite or NaN.  pos -1: no rows, O = 0 and lse = -inf.  A row with pos < -1 or req < 0 is padding: nothing of it
  * is written.
  * q, o bf16 [N][H][head_dim] with a stride per token (elements, multiples of 8; heads follow one another); o
- * may be q itself (same stride).  N 0: nothing to do, the rows' pointers may be NULL.
+ * may be q itself (same stride), else its rows lie apart from q's.  N 0: nothing to do, the rows' pointers may be NULL.
  * table int32 [R][width] of page ids, width * page < 2^31; lse f32 [N][H] or NULL; sink f32 [H] or NULL.
  * head_dim <= 256 with separate or shared values, or up to 512 with cache->v NULL.  A req >= R (its row is
  * left as it was), a pos past width pages (the rows past them are left out) and a page id outside
