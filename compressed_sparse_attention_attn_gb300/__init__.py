@@ -421,6 +421,60 @@ class Context:
             _vec(lse, N * H, torch.float32, dev, "lse"), st), "csa_paged_attn")
         return out if lse is None else (out, lse)
 
+    def _rows_call(self, q, cache, table, what, out, lse, with_lse, stream):
+        """What prompt_attn and prefix_attn marshal alike: (device, stream, out, lse, leading C arguments, trailing ones)."""
+        N, H, hd = q.shape
+        dev, st = _now(stream)
+        if hd != cache.head_dim:
+            raise ValueError("q: expected [N, H, %d], got %s" % (cache.head_dim, tuple(q.shape)))
+        if cache.device != dev:
+            raise ValueError("cache: on CUDA device %d, the current one is %d" % (cache.device, dev))
+        if table.dim() != 2:
+            raise ValueError("table: expected [%s, width], got %s" % (what, tuple(table.shape)))
+        R, width = table.shape
+        if out is None:
+            out = _empty((N, H, hd), torch.bfloat16, q.device, stream)
+        elif out.shape != q.shape:
+            raise ValueError("out: expected %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+        if lse is None and with_lse:
+            lse = _empty((N, H), torch.float32, q.device, stream)
+        qp, q_t, q_h = _rows(q, dev, "q")
+        op, o_t, o_h = _rows(out, dev, "out")
+        if H > 1 and (q_h != hd or o_h != hd):
+            raise ValueError("q, out: the heads of a token must follow one another")
+        return (dev, st, out, lse, (self.h, qp, q_t, N, H, cache.ref, _vec(table, R * width, torch.int32, dev, "table"), R, width),
+                (op, o_t, _vec(lse, N * H, torch.float32, dev, "lse"), st))
+
+    def prompt_attn(self, q, cache, table, cu, length, scale, sink=None, window=0, out=None, lse=None, with_lse=False,
+                    stream=None):
+        """csa_prompt_attn: causal attention of each request's new tokens over the PagedCache.  Rows cu[r] .. cu[r+1]-1 of
+        q [N, H, hd] (a token stride is allowed) are the newest of the length[r] rows that request r has behind table
+        int32 [R, width]; cu int32 [R+1] and length int32 [R] are page_step's cu and length_out.  Rows outside every request
+        are left as they are.  sink f32 [H].  Returns out, or (out, lse) as paged_attn does."""
+        dev, st, out, lse, head, tail = self._rows_call(q, cache, table, "requests", out, lse, with_lse, stream)
+        R, H, i32 = table.shape[0], q.shape[1], torch.int32
+        _check(lib().csa_prompt_attn(*head, _vec(cu, R + 1, i32, dev, "cu"), _vec(length, R, i32, dev, "length"),
+                                     _vec(sink, H, torch.float32, dev, "sink"), scale, window, *tail), "csa_prompt_attn")
+        return out if lse is None else (out, lse)
+
+    def prefix_attn(self, q, cache, table, pos, prefix, prefix_len, scale, cu=None, req=None, sink=None, window=0, out=None,
+                    lse=None, with_lse=False, stream=None):
+        """csa_prefix_attn: paged_attn for rows that share a prefix.  Row n of q [N, H, hd] attends the prefix_len[g] rows
+        behind prefix int32 [G, width] of its prefix g, then rows 0 .. pos[n] of request req[n] (None: request n) behind
+        table int32 [R, width]; with a window, the last `window` of them.  Prefix g is that of rows cu[g] .. cu[g+1]-1
+        (cu None: one prefix for all).  pos -1: the prefix alone; pos < -1 or req < 0: padding, left as it is.
+        Returns out, or (out, lse) as paged_attn does."""
+        dev, st, out, lse, head, tail = self._rows_call(q, cache, table, "requests", out, lse, with_lse, stream)
+        N, H, i32 = q.shape[0], q.shape[1], torch.int32
+        if prefix.dim() != 2:
+            raise ValueError("prefix: expected [prefixes, width], got %s" % (tuple(prefix.shape),))
+        G, width = prefix.shape
+        _check(lib().csa_prefix_attn(
+            *head, _vec(req, N, i32, dev, "req"), _vec(pos, N, i32, dev, "pos"), _vec(prefix, G * width, i32, dev, "prefix"), G,
+            width, _vec(prefix_len, G, i32, dev, "prefix_len"), _vec(cu, G + 1, i32, dev, "cu"),
+            _vec(sink, H, torch.float32, dev, "sink"), scale, window, *tail), "csa_prefix_attn")
+        return out if lse is None else (out, lse)
+
 
 def multicast(allow=None):
     """csa_multicast: let this process's launches use TMA multicast or not (None: leave it); returns what held

@@ -99,6 +99,8 @@ SIGNATURES = {
     "csa_qk_norm_rope": (I, [P, P, I64, I64, P, I64, I64, P, I64, I64, I, I, P, P, P, P, P, F, P, I, I, I, I, P, I64,
                              I64, P]),
     "csa_paged_attn": (I, [P, P, I64, I, I, P, P, I, I, P, P, P, F, I, P, I64, P, P]),
+    "csa_prompt_attn": (I, [P, P, I64, I, I, P, P, I, I, P, P, P, F, I, P, I64, P, P]),
+    "csa_prefix_attn": (I, [P, P, I64, I, I, P, P, I, I, P, P, P, I, I, P, P, P, F, I, P, I64, P, P]),
 }
 
 

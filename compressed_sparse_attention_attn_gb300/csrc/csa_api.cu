@@ -674,6 +674,60 @@ int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, c
   return CSA_OK;
 }
 
+// What csa_prompt_attn and csa_prefix_attn ask alike of their arguments (behind check_paged).
+static int check_rows(const char *who, const csa_paged *cache, const csa_bf16 *q, int64_t q_t, int N, int H, int S, int width,
+                      int window, const csa_bf16 *o, int64_t o_t) {
+  const int hd = cache->head_dim;
+  if (N < 0 || H <= 0 || H % cache->kv_heads || H > 65535 || S <= 0 || width <= 0 || window < 0 ||
+      (int64_t)width * cache->page >= ((int64_t)1 << 31))
+    return fail(CSA_ERR_ARG, "%s: N %d, H %d over %d kv heads, %d tables of width %d, window %d", who, N, H, cache->kv_heads, S,
+                width, window);
+  if (hd > 256) return fail(CSA_ERR_UNSUPPORTED, "%s: head_dim %d: up to 256", who, hd);
+  if ((int64_t)N * H >= ((int64_t)1 << 31)) return fail(CSA_ERR_SHAPE, "%s: %d tokens of %d heads: 2^31 rows or more", who, N, H);
+  if (((uintptr_t)q | (uintptr_t)o) & 15) return fail(CSA_ERR_ARG, "%s: q and o must be 16-byte aligned", who);
+  if (q_t < (int64_t)H * hd || q_t % 8 || o_t < (int64_t)H * hd || o_t % 8)
+    return fail(CSA_ERR_ARG, "%s: token strides must hold the heads and be multiples of 8", who);
+  return CSA_OK;
+}
+
+int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache, const int32_t *table,
+                    int R, int width, const int32_t *cu, const int32_t *length, const float *sink, float scale, int window,
+                    csa_bf16 *o, int64_t o_t, float *lse, csa_stream stream) {
+  const char *who = "csa_prompt_attn";
+  if (!ctx || !table || !cu || !length || (N > 0 && (!q || !o))) return fail(CSA_ERR_ARG, "%s: NULL argument", who);
+  if (int rc = check_paged(cache, who)) return rc;
+  if (int rc = check_rows(who, cache, q, q_t, N, H, R, width, window, o, o_t)) return rc;
+  if (int rc = check_device(ctx, who)) return rc;
+  if (N == 0) return CSA_OK;
+  csa::RowsAttnArgs a{(const bf16 *)q, q_t, N, H, *cache, cu, length, table, R, width, nullptr, nullptr, nullptr, 0, 0, sink, scale,
+                      window, (bf16 *)o, o_t, lse, ctx->status};
+  CSA_CUDA(csa::launch_rows_attn(a, ctx->comp_ws(), ctx->comp_ws_bytes(), ctx->paged_counters, ctx->num_sms,
+                                 (cudaStream_t)stream), who);
+  return CSA_OK;
+}
+
+int csa_prefix_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache, const int32_t *table,
+                    int R, int width, const int32_t *req, const int32_t *pos, const int32_t *prefix, int G, int prefix_width,
+                    const int32_t *prefix_len, const int32_t *cu, const float *sink, float scale, int window, csa_bf16 *o,
+                    int64_t o_t, float *lse, csa_stream stream) {
+  const char *who = "csa_prefix_attn";
+  if (!ctx || !table || !prefix || !prefix_len || (N > 0 && (!q || !pos || !o)))
+    return fail(CSA_ERR_ARG, "%s: NULL argument", who);
+  if (int rc = check_paged(cache, who)) return rc;
+  if (int rc = check_rows(who, cache, q, q_t, N, H, G, prefix_width, window, o, o_t)) return rc;
+  if (R <= 0 || width <= 0 || (int64_t)width * cache->page >= ((int64_t)1 << 31))
+    return fail(CSA_ERR_ARG, "%s: R %d, width %d", who, R, width);
+  if (!cu && G != 1) return fail(CSA_ERR_ARG, "%s: %d prefixes and no cu", who, G);
+  if (!req && N > R) return fail(CSA_ERR_SHAPE, "%s: %d rows over %d requests and no req", who, N, R);
+  if (int rc = check_device(ctx, who)) return rc;
+  if (N == 0) return CSA_OK;
+  csa::RowsAttnArgs a{(const bf16 *)q, q_t, N, H, *cache, cu, prefix_len, prefix, G, prefix_width, pos, req, table, R, width, sink,
+                      scale, window, (bf16 *)o, o_t, lse, ctx->status};
+  CSA_CUDA(csa::launch_rows_attn(a, ctx->comp_ws(), ctx->comp_ws_bytes(), ctx->paged_counters, ctx->num_sms,
+                                 (cudaStream_t)stream), who);
+  return CSA_OK;
+}
+
 // ---------------------------------------------------------------------------------------------
 // the layer
 // ---------------------------------------------------------------------------------------------

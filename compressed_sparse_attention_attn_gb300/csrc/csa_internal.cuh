@@ -307,6 +307,29 @@ constexpr int kPagedCounters = 3 * 2 * 640;
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms,
                               cudaStream_t s);
 
+// Attention of many rows over the paged cache (csa_prompt_attn's and csa_prefix_attn's arguments): segment s of S has rows
+// cu[s] .. cu[s+1]-1 of q (cu NULL: one segment of all rows) and len[s] rows of the cache behind table[s][width].  pos NULL: the
+// segment's last len rows are its own tokens (causal).  Else row n attends all of them and rows 0 .. pos[n] of request
+// req[n] behind own_table [R][own_width].
+struct RowsAttnArgs {
+  const bf16 *q;
+  int64_t q_t;
+  int N, H;
+  csa_paged c;
+  const int32_t *cu, *len, *table;
+  int S, width;
+  const int32_t *pos, *req, *own_table;
+  int R, own_width;
+  const float *sink;
+  float scale;
+  int window;
+  bf16 *o;
+  int64_t o_t;
+  float *lse;
+  int *status;
+};
+cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s);
+
 // Record the calling thread's last error (attn_v41_last_error) and return `code`.
 int set_error(int code, const char *fmt, ...);
 

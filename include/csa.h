@@ -360,7 +360,7 @@ CSA_API int csa_sparse_attn(csa_ctx *ctx, const csa_bf16 *q, int B, int T, int H
  * A continuous batch over a paged cache
  *
  * A server's requests have lengths of their own and share one pool of pages.  The pages print no paged
- * cache; these three calls are additions beside csa_kv_finish (rotation and cache write),
+ * cache; these calls are additions beside csa_kv_finish (rotation and cache write),
  * csa_rmsnorm / csa_rope and csa_sparse_attn.  One step of such a batch is
  *   csa_page_step      the step's tokens from the requests' lengths: request, position and slot of each
  *   csa_qk_norm_rope   their query and key heads normed and turned, key and value rows into their slots
@@ -448,6 +448,38 @@ CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, 
                            const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos,
                            const float *sink, float scale, int window, csa_bf16 *o, int64_t o_t, float *lse,
                            csa_stream stream);
+
+/* Causal attention of each request's new tokens over a paged cache: a whole prompt, a further chunk of one, a single token, in one
+ * call.  Request r's tokens are rows t = cu[r] .. cu[r+1]-1 of q (its n = cu[r+1] - cu[r] newest), and length[r] its rows in the
+ * cache with them: row t stands at position p = length[r] - cu[r+1] + t and attends rows max(0, p+1-window) .. p of its request
+ * (window 0: from 0).  cu and length are what csa_page_step leaves in cu and length_out.  Heads, scores, sink, lse, infinities, the
+ * cache and the layout of q, o (which may be q itself), table, lse and sink are those of csa_paged_attn; head_dim <= 256.
+ * Rows of q outside every request's are padding: nothing of them is written.  A request without tokens has no rows (its length is
+ * not read).  N 0: nothing to do, q and o may be NULL.
+ * An infinity or NaN in the cache reaches the rows that attend it and no others.
+ * Caller errors, recorded in the context's status word: a request with cu[r] < 0, cu[r] > cu[r+1], cu[r+1] > N or length[r] < n (its
+ * rows are left as they were), a length past width pages (the rows past them are left out), a page id outside [0, n_pages) (its rows
+ * are left out).  Rows that two requests both claim are written by either.  N * H < 2^31.
+ * The same inputs give the same bits. */
+CSA_API int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
+                            const int32_t *table, int R, int width, const int32_t *cu, const int32_t *length,
+                            const float *sink, float scale, int window, csa_bf16 *o, int64_t o_t, float *lse,
+                            csa_stream stream);
+
+/* csa_paged_attn for rows that share a prefix, whose rows are read once for all of them: row n attends the prefix_len[g] rows
+ * behind prefix[g], and behind them its own rows 0 .. pos[n] of request req[n] (req NULL: request n) behind table; positions
+ * count on through both, so with a window it attends the last `window` of them.  Prefix g of G is that of rows cu[g] ..
+ * cu[g+1]-1 (int32 [G+1]; cu NULL: one prefix, of all rows).  prefix int32 [G][prefix_width] page ids, prefix_len int32 [G].
+ * pos -1: no rows of its own.  A row that attends nothing: O = 0 and lse = -inf.  pos < -1, req < 0, or a row outside cu: padding,
+ * nothing of it is written.  A request's own table holds none of the prefix's pages, so csa_page_step serves it as any other; angles
+ * for csa_qk_norm_rope are its table from row prefix_len on.
+ * The rest is as in csa_paged_attn, with head_dim <= 256; infinities and errors as in csa_prompt_attn, with prefix_len for length
+ * (a negative one counts as 0) and its errors of req, pos and page ids.  N * H < 2^31. */
+CSA_API int csa_prefix_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
+                            const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos,
+                            const int32_t *prefix, int G, int prefix_width, const int32_t *prefix_len, const int32_t *cu,
+                            const float *sink, float scale, int window, csa_bf16 *o, int64_t o_t, float *lse,
+                            csa_stream stream);
 
 /* Allocation-free projection.  The pages have no counterpart: this is an addition for callers that
  * cannot allocate device memory -- a host runtime that owns a fixed device-memory budget and forbids
