@@ -690,6 +690,16 @@ static int check_rows(const char *who, const csa_paged *cache, const csa_bf16 *q
   return CSA_OK;
 }
 
+static int run_rows(csa_ctx *ctx, const csa::RowsAttnArgs &a, const char *who, csa_stream stream) {
+  const size_t need = csa::rows_attn_bytes(a, ctx->num_sms);
+  if (need > ctx->comp_ws_bytes())
+    return fail(CSA_ERR_SHAPE, "%s: %d rows of %d heads of %d over %d tables need %zu bytes of the %zu of workspace", who, a.N, a.H,
+                a.c.head_dim, a.S, need, ctx->comp_ws_bytes());
+  CSA_CUDA(csa::launch_rows_attn(a, ctx->comp_ws(), ctx->comp_ws_bytes(), ctx->paged_counters, ctx->num_sms, (cudaStream_t)stream),
+           who);
+  return CSA_OK;
+}
+
 int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache, const int32_t *table,
                     int R, int width, const int32_t *cu, const int32_t *length, const float *sink, float scale, int window,
                     csa_bf16 *o, int64_t o_t, float *lse, csa_stream stream) {
@@ -701,9 +711,7 @@ int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, 
   if (N == 0) return CSA_OK;
   csa::RowsAttnArgs a{(const bf16 *)q, q_t, N, H, *cache, cu, length, table, R, width, nullptr, nullptr, nullptr, 0, 0, sink, scale,
                       window, (bf16 *)o, o_t, lse, ctx->status};
-  CSA_CUDA(csa::launch_rows_attn(a, ctx->comp_ws(), ctx->comp_ws_bytes(), ctx->paged_counters, ctx->num_sms,
-                                 (cudaStream_t)stream), who);
-  return CSA_OK;
+  return run_rows(ctx, a, who, stream);
 }
 
 int csa_prefix_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache, const int32_t *table,
@@ -723,9 +731,7 @@ int csa_prefix_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, 
   if (N == 0) return CSA_OK;
   csa::RowsAttnArgs a{(const bf16 *)q, q_t, N, H, *cache, cu, prefix_len, prefix, G, prefix_width, pos, req, table, R, width, sink,
                       scale, window, (bf16 *)o, o_t, lse, ctx->status};
-  CSA_CUDA(csa::launch_rows_attn(a, ctx->comp_ws(), ctx->comp_ws_bytes(), ctx->paged_counters, ctx->num_sms,
-                                 (cudaStream_t)stream), who);
-  return CSA_OK;
+  return run_rows(ctx, a, who, stream);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -301,6 +301,10 @@ struct PagedAttnArgs {
   int64_t o_t;
   float *lse;
   int *status;
+  // head_dim up to 256: instead of o and lse (and without the sink), the share of each row that is no padding: the weighted sum
+  // f32 [N][H][head_dim], and maximum (base 2) and sum of weights [N][H]
+  float *part_o = nullptr;
+  float2 *part_ml = nullptr;
 };
 // ws: the shares of rows that several CTAs work on; counters: kPagedCounters ints, zero between launches.
 constexpr int kPagedCounters = 3 * 2 * 640;
@@ -328,6 +332,8 @@ struct RowsAttnArgs {
   float *lse;
   int *status;
 };
+constexpr size_t kPagedShareBytes = (size_t)24 << 20;  // more than launch_paged_attn's shares take up to 256 features
+size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms);  // of workspace
 cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s);
 
 // Record the calling thread's last error (attn_v41_last_error) and return `code`.

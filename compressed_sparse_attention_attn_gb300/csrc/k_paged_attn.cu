@@ -85,7 +85,7 @@ __device__ __forceinline__ int swizzle(int h) {
   return (NH == 8 ? (h >> 1) & 3 : h & 3) << 3;
 }
 
-template <int HD, int NH>
+template <int HD, int NH, bool PART>
 __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCtas)) k_paged_attn(const __grid_constant__ Params P) {
   using S = Shape<HD, NH>;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kUnit = S::kUnit, kHeads = NH;
@@ -366,7 +366,9 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
           s_f[w][tid] = f;
           L = fmaf(s_ml[1][w][tid], f, L);
         }
-        if (whole) {
+        if (PART && whole) {
+          a.part_ml[(int64_t)cc.n * a.H + h0 + tid] = make_float2(M, L);
+        } else if (whole) {
           s_out[tid] = out_factor(M, L, a.sink, h0 + tid);
           if (a.lse) a.lse[(int64_t)cc.n * a.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         } else {
@@ -388,7 +390,9 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
           v.z = fmaf(x.z, f, v.z);
           v.w = fmaf(x.w, f, v.w);
         }
-        if (whole) {
+        if (PART && whole) {
+          *reinterpret_cast<float4 *>(a.part_o + ((int64_t)cc.n * a.H + h0 + h) * hd + d) = v;
+        } else if (whole) {
           const float f = s_out[h];
           *reinterpret_cast<uint2 *>(a.o + (int64_t)cc.n * a.o_t + (int64_t)(h0 + h) * hd + d) =
               make_uint2(bits(__floats2bfloat162_rn(v.x * f, v.y * f)), bits(__floats2bfloat162_rn(v.z * f, v.w * f)));
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       if (!whole) {
         int c0;
         const int parts = sharers(rg, cc, c0);
-        publish<kHeads, HD, kThreads>(P, c0, parts, cc.n, h0, nh, &s_flag);
+        publish<kHeads, HD, kThreads, PART>(P, c0, parts, cc.n, h0, nh, &s_flag);
       }
       if (u + 1 < nunits) {
         advance<kUnit, false, kEnd>(a, P.Hg, rows, cc);
@@ -417,11 +421,11 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int HD, int NH>
+template <int HD, int NH, bool PART>
 cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   using S = Shape<HD, NH>;
   static SmemAttr attr;
-  cudaError_t e = attr.ensure((const void *)k_paged_attn<HD, NH>, S::kSmem);
+  cudaError_t e = attr.ensure((const void *)k_paged_attn<HD, NH, PART>, S::kSmem);
   if (e != cudaSuccess) return e;
   const PagedAttnArgs &a = p.a;
   p.sub = (p.g + NH - 1) / NH;
@@ -433,12 +437,14 @@ cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cuda
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * NH * HD;
   if (sizeof(float) * 2 * grid * NH * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;
-  return launch_dependent(k_paged_attn<HD, NH>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, 1, p);
+  return launch_dependent(k_paged_attn<HD, NH, PART>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, 1, p);
 }
 template <int HD>
 cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   p.g = p.a.H / p.a.c.kv_heads;
-  return p.g <= 8 ? launch_heads<HD, 8>(p, ws, ws_bytes, num_sms, s) : launch_heads<HD, 16>(p, ws, ws_bytes, num_sms, s);
+  if (p.a.part_o)
+    return p.g <= 8 ? launch_heads<HD, 8, true>(p, ws, ws_bytes, num_sms, s) : launch_heads<HD, 16, true>(p, ws, ws_bytes, num_sms, s);
+  return p.g <= 8 ? launch_heads<HD, 8, false>(p, ws, ws_bytes, num_sms, s) : launch_heads<HD, 16, false>(p, ws, ws_bytes, num_sms, s);
 }
 
 // (head_dim above 256: k_paged_attn_tc.cu)

@@ -1,125 +1,1037 @@
-// k_rows_attn.cu -- attention of many rows over a paged cache: the new tokens of prompts, and decode rows that share a prefix.
+// k_rows_attn.cu -- attention of many rows over a paged cache (head_dim up to 256): the new tokens of prompts, and decode rows that
+// share a prefix, on the 5th-generation tensor cores.
 //
-// A warp takes one row (token n, query head h) and goes through its positions 32 at a time: a lane the score of one position, then
-// a lane eight features of the weighted values.  Softmax statistics are f32 (base 2), one pass with the running maximum and sum.
+// The g query heads of a kv head and the tokens of a segment (a request's new tokens, the rows of a prefix) are rows of one
+// product: row i of a segment is token i / g, head i mod g, whatever g is, so a cache row is read once for all of them.
+// An item is a tile of up to QT x 128 such rows of one kv head with the tiles of KVT positions that any of them attends:
+//   S[i][j] = sum_d q[i][d] K[j][d]       M = 128 rows, N = KVT positions, K = head_dim
+//   p = exp2(S scale - m), bf16           a lane a row: the running maximum m and the sums stay in its registers; m is
+//                                         raised only by more than 2^8 (the sums so far are then rescaled)
+//   O[i][d] += sum_j p[i][j] V[j][d]      N = head_dim, K = KVT: p from tensor memory, where it lies over S
+// p is rounded to bf16, by at most 2^-8 of itself (a second term would double that product); O's denominator adds up the
+// rounded p, so that its weights still add up to 1 (with the sink's), lse the p as they were.  Scores, maxima, sums and O are f32.
+//
+// Up to 192 features two tiles of 128 rows share the keys and values, and one's softmax runs while the other's products do; at 256, where
+// O takes half of tensor memory, one tile has two score buffers instead.
+//
+// A plan kernel lists the items with the number of their position tiles (k_rows_plan); the tiles of all items and kv heads stand one
+// behind the other, and each CTA takes an equal part of them in a row, so every CTA has as much to do as any other whatever
+// the lengths and masks are.  An item that several CTAs worked on is joined from their shares (M, L, O), in the order of the
+// CTAs, by k_rows_join.  The rows of a request that is no one's prefix come from k_paged_attn as one more share.
+#include <algorithm>
+#include <cstring>
+
+#include "attn_common.cuh"
 #include "paged_common.cuh"
 
 namespace csa {
 namespace rows {
 
+constexpr int kSub = 128;     // rows of a product
+constexpr int kEnd = 1;       // tiles that the end of an item counts for
+constexpr int kMinPlaces = 4; // tiles a CTA has at least
+constexpr int kNote = 8;      // tiles (and items) whose notes are kept: more than the copies can be ahead
+constexpr float kRaise = 8.f;
+
+// Rows row0 .. row0 + rows - 1 of the segment whose first token is tok0; positions begin .. end - 1 behind table row seg are all that
+// any of them attends.  Token t of a prompt stands at t + shift; of a prefix shift is its length.
+struct Item {
+  int tok0, row0, rows, seg, begin, end, shift, spare;
+};
+struct Plan {
+  unsigned long long places;  // of one kv head
+  int items, spare;
+};
+
 struct Params {
   RowsAttnArgs a;
-  paged::FastDiv page;
+  paged::FastDiv page, g;
   float scale_log2;
+  Plan *plan;
+  Item *item;                  // [cap]
+  unsigned long long *start;   // [cap + 1]: first place of an item
+  int cap;
+  float *share_o;              // [2 ctas][QT * 128][HDP]
+  float4 *share_ml;            // [2 ctas][QT * 128]: M, L of the rounded weights, L
+  int4 *split;                 // [ctas]: the item that began in this CTA and goes on behind it: item, kv head, CTAs
+  const float *own_o;          // prefix: [N][H][head_dim], the share of each row's own pages
+  const float2 *own_ml;        // [N][H]: M, L
 };
 
-// The positions first .. last of a table's row that token n (of the segment with rows t0 .. t1 - 1) attends.
-struct Span {
-  const int32_t *pages;
-  int64_t first, last;
+// Sizes by padded head_dim.
+template <int HDP>
+struct Shape {
+  static constexpr int QT = HDP == 256 ? 1 : 2;             // tiles of 128 rows an item
+  static constexpr int KVT = HDP <= 128 ? 128 : 64;         // positions of a tile
+  static constexpr int NP = HDP / 64;                       // 64-feature panels
+  static constexpr int kQBytes = kSub * HDP * 2, kStage = KVT * HDP * 2;
+  static constexpr int NST = HDP == 64 ? 8 : 5;             // stages: a tile's keys or values
+  static constexpr int kSoft = 4 * QT, kLoad = 3;           // warps
+  static constexpr int kThreads = (kSoft + 1 + kLoad) * 32;
+  // Registers a thread, softmax and the others: a row's 128 scores do not fit in the 168 that 384 threads get each.  They add up
+  // to what the block is launched with: 256 x 208 + 128 x 88 = 384 x 168.
+  static constexpr bool kSplit = HDP <= 128;
+  static constexpr int kRegsSoft = 208, kRegsRest = 88;
+  static constexpr int kQ = 0, kRing = QT * kQBytes, kBars = kRing + NST * kStage;
+  static constexpr int kSmem = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 32;  // (all that the kernel has: the swizzled tiles come first)
+  static constexpr int kColO = 2 * KVT;                     // columns of tensor memory: two score buffers, then QT x HDP of O
 };
 
-__global__ void __launch_bounds__(128) k_rows_attn(const __grid_constant__ Params P) {
+// ------------------------------------------------------------------------------------------------ plan
+
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *warp_sum, unsigned long long &sum) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sum[wid] = v;
+  __syncthreads();
+  unsigned long long w = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += o;
+  }
+  sum = __shfl_sync(0xffffffffu, w, 31);
+  const unsigned long long before = __shfl_sync(0xffffffffu, w, wid > 0 ? wid - 1 : 0);
+  return v + (wid > 0 ? before : 0);
+}
+
+template <int TR, int KVT>
+__global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constant__ Params P) {
   const RowsAttnArgs &a = P.a;
-  const int lane = threadIdx.x & 31, hd = a.c.head_dim;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  dependency_wait();
-  if (i >= (int64_t)a.N * a.H) return;
-  const int n = (int)(i / a.H), h = (int)(i - (int64_t)n * a.H), kvh = h / (a.H / a.c.kv_heads);
-  int seg = -1, t0 = 0, t1 = a.N;
-  if (a.cu) {
-    for (int s = 0; s < a.S; ++s) {
-      const int lo = a.cu[s], hi = a.cu[s + 1];
-      if (lo < 0 || hi < lo || hi > a.N) {
-        if (i == 0 && lane == 0) atomicOr(a.status, kStatusBadIndex);
-        continue;
-      }
-      if (seg < 0 && n >= lo && n < hi) seg = s, t0 = lo, t1 = hi;
-    }
-  } else {
-    seg = 0;
-  }
-  if (seg < 0) return;
-  Span sp[2];
-  int spans = 1;
+  __shared__ unsigned long long s_sum[32];
+  __shared__ int4 s_seg[kPlanThreads];  // first token, tokens, length, tiles up to and with this segment's
+  const int tid = threadIdx.x;
   const int64_t cap = min((int64_t)a.width * a.c.page, (int64_t)0x7fffffff);
-  int64_t len = a.len[seg];
-  if (a.pos) {  // a prefix, and the row's own pages
-    const int req = a.req ? a.req[n] : n, pos = a.pos[n];
-    if (req < 0 || pos < -1) return;
-    const int64_t own = min((int64_t)a.own_width * a.c.page, (int64_t)0x7fffffff);
-    if (req >= a.R) {
-      if (lane == 0) atomicOr(a.status, kStatusBadIndex);
-      return;
+  dependency_wait();
+  unsigned long long places = 0;
+  int items = 0;
+  bool full = false;
+  for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int t0 = 0, n = 0, len = 0;
+    if (s < a.S) {
+      int t1 = a.N;
+      if (a.cu) t0 = a.cu[s], t1 = a.cu[s + 1];
+      bool bad = t0 < 0 || t1 < t0 || t1 > a.N;
+      n = bad ? 0 : t1 - t0;
+      if (n > 0) {
+        len = a.len[s];
+        if (a.pos == nullptr && len < n) {
+          bad = true;
+          n = 0;
+        }
+        if (len < 0 || len > cap) bad = true;
+        if (a.pos) len = max(len, 0);
+      }
+      if (bad) atomicOr(a.status, kStatusBadIndex);
     }
-    if (lane == 0 && (pos >= own || len < 0 || len > cap)) atomicOr(a.status, kStatusBadIndex);
-    len = max((int64_t)0, len);
-    const int64_t first = a.window > 0 ? max((int64_t)0, len + pos + 1 - a.window) : 0;
-    sp[0] = {a.table + (int64_t)seg * a.width, first, min(len, cap) - 1};
-    sp[1] = {a.own_table + (int64_t)req * a.own_width, max((int64_t)0, first - len), min((int64_t)pos, own - 1)};
-    spans = 2;
-  } else {
-    if (len < t1 - t0) {
-      if (lane == 0) atomicOr(a.status, kStatusBadIndex);
-      return;
-    }
-    const int64_t at = len - t1 + n;
-    if (lane == 0 && len > cap) atomicOr(a.status, kStatusBadIndex);
-    sp[0] = {a.table + (int64_t)seg * a.width, a.window > 0 ? max((int64_t)0, at + 1 - a.window) : 0, min(at, cap - 1)};
-  }
-  const bf16 *q = a.q + (int64_t)n * a.q_t + (int64_t)h * hd;
-  const bf16 *kb = reinterpret_cast<const bf16 *>(a.c.k) + kvh * a.c.k_head;
-  const bf16 *vb = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) + kvh * a.c.v_head : kb;
-  const int64_t v_page = a.c.v ? a.c.v_page : a.c.k_page, v_row = a.c.v ? a.c.v_row : a.c.k_row;
-  float m = -INFINITY, l = 0.f, acc[8] = {};
-  for (int s = 0; s < spans; ++s)
-    for (int64_t j0 = sp[s].first; j0 <= sp[s].last; j0 += 32) {
-      const int64_t j = j0 + lane;
-      int64_t vo = -1;
-      float x = -INFINITY;
-      if (j <= sp[s].last) {
-        const int pg = (int)P.page.div((uint32_t)j), r = (int)j - pg * a.c.page, id = sp[s].pages[pg];
-        if (id >= 0 && id < a.c.n_pages) {
-          const bf16 *k = kb + (int64_t)id * a.c.k_page + (int64_t)r * a.c.k_row;
-          vo = (int64_t)id * v_page + (int64_t)r * v_row;
-          x = 0.f;
-          for (int d = 0; d < hd; ++d) x = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), x);
-          x *= P.scale_log2;
+    unsigned long long sum;
+    const unsigned long long tiles = n > 0 ? ((unsigned long long)n * P.g.d + TR - 1) / TR : 0;
+    const unsigned long long to = block_scan(tiles, s_sum, sum);
+    s_seg[tid] = make_int4(t0, n, len, (int)min(to, 0x7fffffffull));
+    __syncthreads();
+    const int room = P.cap - items, all = (int)min(sum, (unsigned long long)room);
+    full = full || sum > (unsigned long long)room;
+    for (int i0 = 0; i0 < all; i0 += kPlanThreads) {
+      const int i = i0 + tid;
+      unsigned long long mine = 0;
+      Item it{};
+      if (i < all) {
+        int lo = 0, hi = kPlanThreads - 1;  // the first segment with more than i tiles up to its end
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (s_seg[mid].w > i) hi = mid;
+          else lo = mid + 1;
+        }
+        const int4 sg = s_seg[lo];
+        const int first = lo ? s_seg[lo - 1].w : 0;
+        it.tok0 = sg.x;
+        it.row0 = (i - first) * TR;
+        it.rows = (int)min((long long)TR, (long long)sg.y * P.g.d - it.row0);
+        it.seg = s0 + lo;
+        if (a.pos) {  // (a row's own part begins at len or behind it: the window reaches back to len - window at most)
+          it.shift = sg.z;
+          it.begin = a.window > 0 ? max(0, sg.z - a.window) : 0;
+          it.end = (int)min((int64_t)sg.z, cap);
         } else {
-          atomicOr(a.status, kStatusBadIndex);
+          it.shift = sg.z - sg.x - sg.y;
+          const int ta = sg.x + (int)P.g.div(it.row0), tb = sg.x + (int)P.g.div(it.row0 + it.rows - 1);
+          it.begin = a.window > 0 ? max(0, ta + it.shift - a.window + 1) : 0;
+          it.end = (int)min((int64_t)tb + it.shift + 1, cap);
+        }
+        mine = it.end > it.begin ? (it.end - 1) / KVT - it.begin / KVT + 1 : 1;
+        mine += kEnd;
+      }
+      const unsigned long long incl = block_scan(mine, s_sum, sum);
+      if (i < all) {
+        reinterpret_cast<int4 *>(P.item + items + i)[0] = make_int4(it.tok0, it.row0, it.rows, it.seg);
+        reinterpret_cast<int4 *>(P.item + items + i)[1] = make_int4(it.begin, it.end, it.shift, 0);
+        P.start[items + i] = places + incl - mine;
+      }
+      places += sum;
+    }
+    items += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    P.start[items] = places;
+    P.plan->places = places;
+    P.plan->items = items;
+    if (full) atomicOr(a.status, kStatusBadIndex);  // (more items than rows can make: requests that overlap)
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ a CTA's part
+
+// The places first .. last - 1 of CTA c of n.
+__device__ __forceinline__ unsigned long long part_begin(unsigned long long total, int n, int c) { return total / n * c + total % n * c / n; }
+// The CTAs that the places are dealt to.
+__device__ __forceinline__ int parts_of(unsigned long long total, int ctas) {
+  return (int)min((unsigned long long)ctas, max(1ull, total / kMinPlaces));
+}
+
+struct Walk {
+  const Params *P;
+  unsigned long long places, p0, p1, base = 0;
+  int items, i, kvh, seq = -1;  // seq: items so far
+  Item d;
+  int kt0, tiles;               // the item's tiles of positions
+  int u0, u1;                   // of these, the CTA's
+  template <int KVT>
+  __device__ __forceinline__ bool load() {
+    for (;; step()) {
+      if (kvh >= P->a.c.kv_heads) return false;
+      base = places * kvh + __ldg(P->start + i);
+      if (base >= p1) return false;
+      const int4 x = __ldg(reinterpret_cast<const int4 *>(P->item + i)), y = __ldg(reinterpret_cast<const int4 *>(P->item + i) + 1);
+      d = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, 0};
+      kt0 = d.begin / KVT;
+      tiles = d.end > d.begin ? (d.end - 1) / KVT - kt0 + 1 : 1;
+      u0 = base < p0 ? (int)min(p0 - base, 0x7fffffffull) : 0;
+      u1 = (int)min((unsigned long long)tiles, p1 - base);
+      if (u0 < u1) {
+        ++seq;
+        return true;
+      }
+    }
+  }
+  __device__ __forceinline__ void step() {
+    if (++i == items) i = 0, ++kvh;
+  }
+  template <int KVT>
+  __device__ __forceinline__ bool next() {
+    step();
+    return load<KVT>();
+  }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == tiles; }
+};
+
+// The position tiles x .. y - 1, of the CTA's, that 128-row tile t of an item attends.
+template <int KVT>
+__device__ __forceinline__ void sub_range(const Params &P, const Walk &w, int t, int &x, int &y) {
+  const Item &d = w.d;
+  const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1, r0 = kSub * t;
+  x = y = j0;
+  if (r0 >= d.rows) return;
+  int lo = d.begin, end = d.end;
+  if (!P.a.pos) {
+    const int ta = d.tok0 + (int)P.g.div(d.row0 + r0), tb = d.tok0 + (int)P.g.div(d.row0 + min(r0 + kSub, d.rows) - 1);
+    if (P.a.window > 0) lo = max(0, ta + d.shift - P.a.window + 1);
+    end = (int)min((int64_t)end, (int64_t)tb + d.shift + 1);
+  }
+  if (end <= lo) return;
+  x = max(j0, lo / KVT);
+  y = max(x, min(j1, (end - 1) / KVT + 1));
+}
+
+// ------------------------------------------------------------------------------------------------ building blocks
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  const bool ok = tc::mbar_wait(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+// D += A B: A (128 x 16 bf16) from tensor memory, B from shared memory.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Keeps the uses of loaded registers behind the wait above it.
+__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ bool not_finite(uint32_t v) {  // either half
+  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+}
+
+// What goes below O and on it: factors of a row's share (m, lr) and of its own pages' (own), and lse.
+struct Finish {
+  float f, f_own, lse;
+};
+__device__ __forceinline__ Finish finish(float m, float lr, float l, float2 own, const float *sink, int h) {
+  const float M = fmaxf(m, own.x);
+  const float e = m == -INFINITY ? 0.f : exp2f(m - M), eo = own.x == -INFINITY ? 0.f : exp2f(own.x - M);
+  const float L = lr * e + own.y * eo, Lt = l * e + own.y * eo;
+  const float f = paged::out_factor(M, L, sink, h);
+  return {f * e, f * eo, Lt == 0.f ? -INFINITY : (M + log2f(Lt)) * 0.6931471805599453f};
+}
+// Whether a row of the prefix form is there, and not padding.
+__device__ __forceinline__ bool row_live(const RowsAttnArgs &a, int n) {
+  if (!a.pos) return true;
+  const int req = a.req ? a.req[n] : n;
+  return a.pos[n] >= -1 && req >= 0 && req < a.R;
+}
+
+// ------------------------------------------------------------------------------------------------ attention
+
+template <int HDP>
+__global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __grid_constant__ Params P) {
+  using S = Shape<HDP>;
+  constexpr int QT = S::QT, KVT = S::KVT, NP = S::NP, NST = S::NST, kSoft = S::kSoft, kW = KVT / 32;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const RowsAttnArgs &a = P.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim, g = P.g.d;
+  const int hd16 = (hd + 15) & ~15;
+  const uint32_t s_q = tc::smem_u32(smem + S::kQ), s_ring = tc::smem_u32(smem + S::kRing);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
+  // full, empty: a stage has landed, has been used; s_full, p_full: scores, weights; pv_done: values added up; q_full
+  uint64_t *full = bars, *empty = bars + NST, *s_full = bars + 2 * NST, *p_full = s_full + 2, *pv_done = s_full + 4,
+           *q_full = s_full + 6, *drain = s_full + 8;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(bars + 32);  // [kNote][4]: positions of a tile that are there
+  int *odd_item = reinterpret_cast<int *>(masks + 4 * kNote);  // [kNote]: items with a value that is not finite where not all attend
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(odd_item + kNote);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int *first_item = reinterpret_cast<int *>(tmem_slot + 2);
+  static_assert(2 * NST + 9 <= 32 && NST / 2 + 2 < kNote, "barriers, notes");
+
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(&full[i], 32);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&s_full[b], 2);   // the products' completion, and the issuing thread (which has seen the stage's notes)
+      tc::mbar_init(&p_full[b], 128);
+      tc::mbar_init(&pv_done[b], 2);
+      tc::mbar_init(&q_full[b], 128);
+    }
+    tc::mbar_init(drain, 1);
+    for (int i = 0; i < kNote; ++i) odd_item[i] = -1;
+    *abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  dependency_wait();
+  Walk w{&P};
+  w.places = P.plan->places;
+  w.items = P.plan->items;
+  const unsigned long long total = w.places * a.c.kv_heads;
+  const int parts = parts_of(total, gridDim.x), cta = blockIdx.x;
+  if (total == 0 || cta >= parts) {
+    if (tid == 0) P.split[cta] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  w.p0 = part_begin(total, parts, cta);
+  w.p1 = part_begin(total, parts, cta + 1);
+  {
+    const unsigned long long in = w.p0 % w.places;
+    for (int i = tid; i < w.items; i += S::kThreads)
+      if (P.start[i] <= in && in < P.start[i + 1]) *first_item = i;
+  }
+  if (warp == kSoft) tc::tmem_alloc(tmem_slot, 512);  // (behind the wait: a block of the kernel before may still ask for tensor memory)
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  w.i = *first_item;
+  w.kvh = (int)(w.p0 / w.places);
+  bool more = w.load<KVT>();
+
+  if (warp < kSoft) {
+    // ------------------------------------------------------------------------------ softmax and results: a lane a row
+    if constexpr (S::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoft));
+    const int t = warp >> 2, quad = warp & 3, r = quad * 32 + lane;  // of tile t of the item
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16, tO = tmem + S::kColO + t * HDP + lane_off;
+    auto load_q = [&](const Item &d, int kvh) {
+      const int cc = lane & 7;
+#pragma unroll 2
+      for (int i = 0; i < 8; ++i) {
+        const int row = quad * 32 + 4 * i + (lane >> 3), R = d.row0 + t * kSub + row;
+        const bool in = t * kSub + row < d.rows;
+        const int tok = (int)P.g.div(R), h = R - tok * g;
+        const bf16 *q = in ? a.q + (int64_t)(d.tok0 + tok) * a.q_t + (int64_t)(kvh * g + h) * hd + cc * 8 : a.q;
+#pragma unroll
+        for (int kb = 0; kb < NP; ++kb) {
+          const bool f_in = in && kb * 64 + cc * 8 < hd;
+          attn::cp_async16(s_q + t * S::kQBytes + kb * (kSub * 128) + row * 128 + ((cc ^ (row & 7)) << 4), f_in ? q + kb * 64 : a.q, f_in);
         }
       }
-      float mx = x;
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mx = fmaxf(m, mx);
-      const float ref = mx == -INFINITY ? 0.f : mx, f = paged::ex2(m - ref), p = vo < 0 ? 0.f : paged::ex2(x - ref);
-      m = mx;
-      l = l * f + p;
-      for (int e = 0; e < 8; ++e) acc[e] *= f;
-      for (int u = 0; u < 32; ++u) {
-        const int64_t off = __shfl_sync(0xffffffffu, vo, u);
-        const float w = __shfl_sync(0xffffffffu, p, u);
-        if (off < 0) continue;
-        for (int e = 0; e < 8; ++e)
-          if (e * 32 + lane < hd) acc[e] = fmaf(w, __bfloat162float(vb[off + e * 32 + lane]), acc[e]);
+    };
+    auto has_rows = [&](const Walk &x) {  // whether tile t has anything to do in this CTA's part of the item
+      int from, to;
+      sub_range<KVT>(P, x, t, from, to);
+      return to > from;
+    };
+    if (more && has_rows(w)) {
+      load_q(w.d, w.kvh);
+      attn::cp_async_wait_all();
+      attn::fence_proxy_async();
+      tc::mbar_arrive(&q_full[t]);
+    }
+    int n_s = 0, n_pv = 0, tile0 = 0;  // scores taken, products of values asked for, first tile of the item
+    // The last product of values asked for is done, and all before it.  (With two score buffers their products take turns at two
+    // barriers: the one before the last may not be done either when the last is waited for.)
+    auto values_done = [&]() {
+      const int n = n_pv - 1;
+      return QT == 2 ? warp_wait(&pv_done[t], n & 1, abort_flag) : warp_wait(&pv_done[n & 1], (n >> 1) & 1, abort_flag);
+    };
+    const bool odd_scale = !(P.scale_log2 > 0.f);
+    bool ok = true;
+    int4 split = make_int4(0, 0, 0, 0);
+    while (more) {
+      const Item d = w.d;
+      int x, y;
+      sub_range<KVT>(P, w, t, x, y);
+      const int R = t * kSub + r;
+      const bool mine = R < d.rows;
+      int tok = 0, h = 0, lo = 0, hi = 0x7fffffff;  // (a row that is not there attends all: no mask for its sake)
+      if (mine) {
+        const int q = (int)P.g.div(d.row0 + R);
+        tok = d.tok0 + q;
+        h = w.kvh * g + (d.row0 + R - q * g);
+        if (!a.pos) {
+          hi = tok + d.shift;
+          if (a.window > 0) lo = max(0, hi - a.window + 1);
+        } else if (a.window > 0) {
+          const int64_t first = (int64_t)d.shift + a.pos[tok] + 1 - a.window;
+          lo = (int)max((int64_t)0, min(first, (int64_t)0x7fffffff));
+        }
+      }
+      const bool work = t * kSub + quad * 32 < d.rows;  // (of the warp)
+      float m = -INFINITY, l = 0.f, lr = 0.f;
+      const int j0 = w.kt0 + w.u0, item_tiles = w.u1 - w.u0;
+      Walk nx = w;
+      bool more_next = false;
+      if (y == x) {
+        more_next = nx.next<KVT>();
+        if (more_next && has_rows(nx)) {
+          load_q(nx.d, nx.kvh);
+          attn::cp_async_wait_all();
+          attn::fence_proxy_async();
+          tc::mbar_arrive(&q_full[t]);
+        }
+      }
+      for (int j = x; j < y; ++j) {
+        const int b = QT == 2 ? t : n_s & 1;
+        if (!(ok = warp_wait(&s_full[b], QT == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag))) break;
+        tc::tc_fence_after();
+        const bool last = j + 1 == y;
+        bool q_next = false;
+        if (last) {  // q's last reader is done: the next item's q on its way
+          more_next = nx.next<KVT>();
+          q_next = more_next && has_rows(nx);
+          if (q_next) load_q(nx.d, nx.kvh);
+        }
+        if (work) {
+          const uint32_t tS = tmem + b * KVT + lane_off;
+          float s[KVT];
+          {
+            uint32_t v[kW][32];
+#pragma unroll
+            for (int k = 0; k < kW; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+              tie32(v[k]);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[32 * k + e] = __uint_as_float(v[k][e]);
+            }
+          }
+          float sc = P.scale_log2;
+          if (odd_scale) {  // (a negative one would make the largest score the smallest; 0 times a mask's -inf is not -inf)
+#pragma unroll
+            for (int k = 0; k < KVT; ++k) s[k] *= sc;
+            sc = 1.f;
+          }
+          {
+            const uint32_t *mk = masks + 4 * ((tile0 + j - j0) & (kNote - 1));
+            const int at = j * KVT, from = lo - at, to = hi - at;  // positions of the tile that the row attends
+            uint32_t there[kW], all = 0xffffffffu;
+#pragma unroll
+            for (int k = 0; k < kW; ++k) all &= there[k] = mk[k];
+            if (!__all_sync(0xffffffffu, all == 0xffffffffu && from <= 0 && to >= KVT - 1)) {
+#pragma unroll
+              for (int k = 0; k < kW; ++k) {
+                const int f = min(max(from - 32 * k, 0), 32), e = min(max(to - 32 * k, -1), 31) + 1;
+                uint32_t mask = e == 32 ? 0xffffffffu : (1u << e) - 1u;
+                mask &= f == 32 ? 0u : 0xffffffffu << f;
+                mask &= there[k];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[32 * k + c] = (mask >> c) & 1u ? s[32 * k + c] : -INFINITY;
+              }
+            }
+          }
+          float mx = fmaxf(s[0], s[1]);
+#pragma unroll
+          for (int k = 2; k < KVT; k += 2) mx = fmaxf(mx, fmaxf(s[k], s[k + 1]));
+          if (j == x) {
+            m = mx;
+          } else {
+            const bool raise = (mx - m) * sc > kRaise || (m == -INFINITY && mx > m);
+            const float al = raise ? (m == -INFINITY ? 0.f : paged::ex2((m - mx) * sc)) : 1.f;
+            if (__any_sync(0xffffffffu, raise)) {
+              if (!(ok = values_done())) break;
+              tc::tc_fence_after();
+              if (raise) m = mx;
+              l *= al;
+              lr *= al;
+#pragma unroll 1
+              for (int c = 0; c < hd16; c += 16) {
+                uint32_t v[16];
+                tc::tmem_ld16_wait(tO + c, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                attn::tmem_st16(tO + c, v);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m * sc;
+          uint32_t pk[KVT / 2];
+#pragma unroll
+          for (int k = 0; k < KVT / 32; ++k) {
+            uint32_t v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = paged::ex2(fmaf(s[32 * k + 2 * e], sc, -ref)), p1 = paged::ex2(fmaf(s[32 * k + 2 * e + 1], sc, -ref));
+              l += p0 + p1;
+              v[e] = pk[16 * k + e] = pack2(p0, p1);
+            }
+            attn::tmem_st16(tS + 16 * k, v);
+          }
+          attn::tmem_st_wait();
+          tc::tc_fence_before();
+          tc::mbar_arrive(&p_full[b]);
+          // (behind what the product waits for)
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < KVT / 2; ++k) sum += low(pk[k]) + high(pk[k]);
+          lr += sum;
+        } else {
+          tc::tc_fence_before();
+          tc::mbar_arrive(&p_full[b]);
+        }
+        ++n_s;
+        ++n_pv;
+        if (q_next) {
+          attn::cp_async_wait_all();
+          attn::fence_proxy_async();
+          tc::mbar_arrive(&q_full[t]);
+        }
+      }
+      if (!ok) break;
+      // ---- the end of the item in this CTA
+      if (y > x) {
+        if (!(ok = values_done())) break;
+        tc::tc_fence_after();
+      }
+      if (work) {
+        const bool whole = w.whole(), live = mine && row_live(a, tok);
+        if (odd_scale || m == -INFINITY) {
+        } else {
+          m *= P.scale_log2;
+        }
+        const bool odd = y > x && odd_item[w.seq & (kNote - 1)] == w.seq;
+        float f = 1.f, f_own = 0.f;
+        float *share = nullptr;
+        bf16 *o = nullptr;
+        const float *own = nullptr;
+        if (whole) {
+          float2 oml = make_float2(-INFINITY, 0.f);
+          if (live && P.own_o) {
+            oml = P.own_ml[(int64_t)tok * a.H + h];
+            own = P.own_o + ((int64_t)tok * a.H + h) * hd;
+          }
+          const Finish fin = finish(m, lr, l, oml, a.sink, h);
+          f = fin.f;
+          f_own = fin.f_own;
+          if (live && a.lse) a.lse[(int64_t)tok * a.H + h] = fin.lse;
+          o = a.o + (int64_t)tok * a.o_t + (int64_t)h * hd;
+        } else {
+          const int64_t at = (int64_t)(2 * cta + (w.u0 == 0 ? 1 : 0)) * (QT * kSub) + R;
+          share = P.share_o + at * HDP;
+          if (mine) P.share_ml[at] = make_float4(m, lr, l, 0.f);
+        }
+#pragma unroll 1
+        for (int c = 0; c < hd; c += 16) {
+          uint32_t u[16];
+          __syncwarp();
+          if (y > x) {
+            tc::tmem_ld16_wait(tO + c, u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) u[k] = 0u;
+          }
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]);
+          if (odd && mine) {
+            // values that are not finite were left out of tiles that not every row attends: to the rows that do
+            const bf16 *vb = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) + w.kvh * a.c.v_head
+                                   : reinterpret_cast<const bf16 *>(a.c.k) + w.kvh * a.c.k_head;
+            const int64_t st_page = a.c.v ? a.c.v_page : a.c.k_page, st_row = a.c.v ? a.c.v_row : a.c.k_row;
+            const int64_t p_end = min(min((int64_t)hi + 1, (int64_t)d.end), (int64_t)y * KVT);
+            // (without a window those are the tiles behind the first token's position)
+            const int64_t part = a.window > 0 ? 0 : ((int64_t)d.tok0 + P.g.div(d.row0) + d.shift + 1) / KVT * KVT;
+            for (int64_t p = max(max((int64_t)lo, (int64_t)d.begin), max(part, (int64_t)x * KVT)); p < p_end; ++p) {
+              const int pg = (int)P.page.div((uint32_t)p), id = a.table[(int64_t)d.seg * a.width + pg];
+              if (id < 0 || id >= a.c.n_pages) continue;
+              const uint4 *src = reinterpret_cast<const uint4 *>(vb + id * st_page + (int64_t)((int)p - pg * a.c.page) * st_row + c);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (c + 8 * e >= hd) break;
+                const uint4 z = src[e];
+                const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((zz[k] & 0x7f80u) == 0x7f80u) v[8 * e + 2 * k] += low(zz[k]);
+                  if ((zz[k] & 0x7f800000u) == 0x7f800000u) v[8 * e + 2 * k + 1] += high(zz[k]);
+                }
+              }
+            }
+          }
+          if (share) {
+            if (mine)
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4 *>(share + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          } else if (live) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] *= f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (c + 8 * e >= hd) break;
+              if (own) {
+                const float4 y0 = *reinterpret_cast<const float4 *>(own + c + 8 * e), y1 = *reinterpret_cast<const float4 *>(own + c + 8 * e + 4);
+                const float yy[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[8 * e + k] = fmaf(yy[k], f_own, v[8 * e + k]);
+              }
+              *reinterpret_cast<uint4 *>(o + c + 8 * e) =
+                  make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]), pack2(v[8 * e + 4], v[8 * e + 5]),
+                             pack2(v[8 * e + 6], v[8 * e + 7]));
+            }
+          }
+        }
+        tc::tc_fence_before();
+      }
+      if (tid == 0 && w.u0 == 0 && w.u1 < w.tiles) {  // (the CTA's last item: it goes on in the next ones)
+        const unsigned long long last_place = w.base + w.tiles - 1;
+        int c = cta;
+        while (c + 1 < parts && part_begin(total, parts, c + 1) <= last_place) ++c;
+        split = make_int4(w.i, w.kvh, c - cta + 1, 0);
+      }
+      tile0 += item_tiles;
+      w = nx;
+      more = more_next;
+    }
+    attn::cp_async_wait_all();
+    if (tid == 0) P.split[cta] = split;
+  } else {
+    if constexpr (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsRest));
+    if (warp == kSoft) {
+    // ------------------------------------------------------------------------------ products, issued by one elected lane
+    if (tc::elect_one()) {
+      const uint32_t id_s = tc::idesc_bf16_f32(kSub, KVT), id_v = tc::idesc_bf16_f32(kSub, hd16, false, /*b_mn_major=*/true);
+      const uint32_t dq = (uint32_t)tc::sdesc_sw128(s_q, 16, 1024), dk = (uint32_t)tc::sdesc_sw128(s_ring, 16, 1024),
+                     dv = (uint32_t)tc::sdesc_sw128(s_ring, KVT * 128, 1024);
+      const uint64_t hi = tc::sdesc_sw128(0, 16, 1024) & 0xffffffff00000000ull;
+      const int ks = hd16 / 16;
+      int s = 0;  // stages so far
+      auto stage_ready = [&](int i) { return tc::mbar_wait(&full[i % NST], (uint32_t)((i / NST) & 1), abort_flag); };
+      uint32_t n_q[2] = {}, n_s = 0, n_p[2] = {};
+      auto scores = [&](int t, int b, int stage) {
+        const uint32_t A = dq + t * (S::kQBytes >> 4), B = dk + (stage % NST) * (S::kStage >> 4);
+#pragma unroll 1
+        for (int k = 0; k < ks; ++k)
+          tc::mma_bf16(tmem + b * KVT, hi | (A + (k >> 2) * (kSub * 128 >> 4) + (k & 3) * 2),
+                       hi | (B + (k >> 2) * (KVT * 128 >> 4) + (k & 3) * 2), id_s, k ? 1u : 0u);
+        tc::mma_commit(&s_full[b]);
+        tc::mbar_arrive(&s_full[b]);
+      };
+      auto values = [&](int t, int b, int stage, bool first) {
+        tc::tc_fence_after();
+        const uint32_t B = dv + (stage % NST) * (S::kStage >> 4);
+#pragma unroll
+        for (int k = 0; k < KVT / 16; ++k)
+          mma_ts(tmem + S::kColO + t * HDP, tmem + b * KVT + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
+        tc::mma_commit(&pv_done[b]);
+        tc::mbar_arrive(&pv_done[b]);
+      };
+      bool ok = true;
+      while (more && ok) {
+        const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1;
+        int x[QT], y[QT];
+#pragma unroll
+        for (int t = 0; t < QT; ++t) sub_range<KVT>(P, w, t, x[t], y[t]);
+        if (!(ok = stage_ready(s))) break;
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          if (x[t] == j0 && y[t] > j0) {
+            if (!(ok = ok && tc::mbar_wait(&q_full[t], n_q[t]++ & 1, abort_flag))) break;
+            scores(t, QT == 2 ? t : n_s & 1, s);
+            ++n_s;
+          }
+        if (!ok) break;
+        tc::mma_commit(&empty[s % NST]);
+        for (int j = j0; j < j1; ++j, s += 2) {
+          const int sv = s + 1, sk = s + 2;
+          const bool next = j + 1 < j1;
+          bool v_in = false, k_in = false;
+          if (QT == 1 && next) {  // (the other score buffer: the next tile's scores before this one's values)
+            if (!(ok = stage_ready(sk))) break;
+            k_in = true;
+            if (x[0] <= j + 1 && j + 1 < y[0]) {
+              if (x[0] == j + 1 && !(ok = tc::mbar_wait(&q_full[0], n_q[0]++ & 1, abort_flag))) break;
+              scores(0, n_s & 1, sk);
+              ++n_s;
+            }
+            tc::mma_commit(&empty[sk % NST]);
+          }
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            if (x[t] <= j && j < y[t]) {
+              const int b = QT == 2 ? t : n_p[0] & 1;
+              if (!(ok = tc::mbar_wait(&p_full[b], QT == 2 ? n_p[t] & 1 : (n_p[0] >> 1) & 1, abort_flag))) break;
+              ++n_p[t];
+              if (!v_in && !(ok = stage_ready(sv))) break;
+              v_in = true;
+              values(t, b, sv, j == x[t]);
+            }
+            if (QT == 2 && next && x[t] <= j + 1 && j + 1 < y[t]) {
+              if (!k_in && !(ok = stage_ready(sk))) break;
+              k_in = true;
+              if (x[t] == j + 1 && !(ok = tc::mbar_wait(&q_full[t], n_q[t]++ & 1, abort_flag))) break;
+              scores(t, t, sk);
+            }
+          }
+          if (!ok) break;
+          if (!v_in && !(ok = stage_ready(sv))) break;
+          tc::mma_commit(&empty[sv % NST]);
+          if (QT == 2 && next) {
+            if (!k_in && !(ok = stage_ready(sk))) break;
+            tc::mma_commit(&empty[sk % NST]);
+          }
+        }
+        more = w.next<KVT>();
+      }
+      // nothing may still read shared memory, write tensor memory or arrive when the CTA ends
+      tc::mma_commit(drain);
+      const uint64_t t1 = tc::global_ns();
+      while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
       }
     }
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float f = paged::out_factor(m, l, a.sink, h);
-  bf16 *out = a.o + (int64_t)n * a.o_t + (int64_t)h * hd;
-  for (int e = 0; e < 8; ++e)
-    if (e * 32 + lane < hd) out[e * 32 + lane] = __float2bfloat16(acc[e] * f);
-  if (a.lse && lane == 0) a.lse[(int64_t)n * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------------------ copies: every third stage a warp
+    // The pages of a warp's next stage are looked up while its copies are in flight.
+    const int lw = warp - kSoft - 1, cc = lane & 7;
+    struct Look {
+      int page[kW];
+      uint32_t at;     // first position
+      int kvh, seg, begin, end, seq, tile;
+      bool values, part;  // part: positions that not every row attends
+    };
+    int s = lw, x = lw, tile0 = 0;  // stage, stage of the item, first tile of the item
+    auto look = [&](Look &f) -> bool {
+      while (more && x >= 2 * (w.u1 - w.u0)) {
+        x -= 2 * (w.u1 - w.u0);
+        tile0 += w.u1 - w.u0;
+        more = w.next<KVT>();
+      }
+      if (!more) return false;
+      const Item &d = w.d;
+      f.at = (uint32_t)(w.kt0 + w.u0 + (x >> 1)) * KVT;
+      f.values = x & 1;
+      f.kvh = w.kvh;
+      f.begin = d.begin;
+      f.end = d.end;
+      f.seq = w.seq;
+      f.seg = d.seg;
+      f.tile = tile0 + (x >> 1);
+      if (a.pos) {
+        f.part = a.window > 0;
+      } else {
+        const int ta = d.tok0 + (int)P.g.div(d.row0), tb = d.tok0 + (int)P.g.div(d.row0 + d.rows - 1);
+        f.part = (int64_t)f.at + KVT - 1 > (int64_t)ta + d.shift || (a.window > 0 && (int64_t)f.at < (int64_t)tb + d.shift - a.window + 1);
+      }
+#pragma unroll
+      for (int k = 0; k < kW; ++k) {
+        const uint32_t p = f.at + 32 * k + lane;
+        const bool in = p >= (uint32_t)d.begin && p < (uint32_t)d.end;
+        f.page[k] = in ? a.table[(int64_t)d.seg * a.width + P.page.div(p)] : 0;
+      }
+      return true;
+    };
+    Look f;
+    bool have = look(f);
+    while (have) {
+      const bool vals = f.values && a.c.v;
+      const bf16 *src = reinterpret_cast<const bf16 *>(vals ? a.c.v : a.c.k) + f.kvh * (vals ? a.c.v_head : a.c.k_head) + cc * 8;
+      const int64_t st_page = vals ? a.c.v_page : a.c.k_page, st_row = vals ? a.c.v_row : a.c.k_row;
+      const int buf = s % NST;
+      int64_t off[kW];
+      uint32_t there[kW];
+#pragma unroll
+      for (int k = 0; k < kW; ++k) {
+        const uint32_t p = f.at + 32 * k + lane;
+        const bool in = p >= (uint32_t)f.begin && p < (uint32_t)f.end, good = in && f.page[k] >= 0 && f.page[k] < a.c.n_pages;
+        if (in && !good) atomicOr(a.status, kStatusBadIndex);
+        off[k] = good ? f.page[k] * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
+        there[k] = __ballot_sync(0xffffffffu, good);
+      }
+      if (s >= NST && !warp_wait(&empty[buf], (uint32_t)((s / NST - 1) & 1), abort_flag)) break;
+      if (!f.values && lane == 0)
+#pragma unroll
+        for (int k = 0; k < kW; ++k) masks[4 * (f.tile & (kNote - 1)) + k] = there[k];
+      const uint32_t dst = s_ring + buf * S::kStage + (lane >> 3) * 128;
+#pragma unroll
+      for (int k = 0; k < kW; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes 128 bytes of a row
+          const int row = 32 * k + 4 * i, r7 = (row + (lane >> 3)) & 7;
+          const int64_t o = __shfl_sync(0xffffffffu, off[k], 4 * i + (lane >> 3));
+#pragma unroll
+          for (int kb = 0; kb < NP; ++kb) {
+            const bool in = o >= 0 && kb * 64 + cc * 8 < hd;
+            attn::cp_async16(dst + kb * (KVT * 128) + row * 128 + ((cc ^ r7) << 4), in ? src + o + kb * 64 : src, in);
+          }
+        }
+      const bool check = f.values && f.part;
+      const int seq = f.seq, cur = s;
+      s += S::kLoad;
+      x += S::kLoad;
+      have = look(f);
+      attn::cp_async_wait_all();
+      if (check) {
+        // A weight of 0 does not undo a NaN: values that are not finite are left out of the product here, and the rows that
+        // attend them get them at the end.  (A lane looks at what it has copied itself.)
+        bool odd = false;
+#pragma unroll 1
+        for (int i = 0; i < KVT / 4; ++i) {
+          const int r7 = (4 * i + (lane >> 3)) & 7;
+#pragma unroll
+          for (int kb = 0; kb < NP; ++kb) {
+            const uint32_t at = dst + kb * (KVT * 128) + i * 512 + ((cc ^ r7) << 4);
+            uint32_t z[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(at) : "memory");
+            if (not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3])) {
+              odd = true;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+                if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]) : "memory");
+            }
+          }
+        }
+        if (odd) odd_item[seq & (kNote - 1)] = seq;
+      }
+      attn::fence_proxy_async();
+      tc::mbar_arrive(&full[cur % NST]);
+    }
+    attn::cp_async_wait_all();
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kSoft) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_flag) atomicOr(a.status, kStatusTimeout);
+}
+
+// ------------------------------------------------------------------------------------------------ joining
+
+constexpr int kJoinThreads = 256, kJoinAhead = 4;
+
+template <int HDP>
+__global__ void __launch_bounds__(kJoinThreads) k_rows_join(const __grid_constant__ Params P, int ctas) {
+  constexpr int kRows = Shape<HDP>::QT * kSub, kLanes = HDP / 4;
+  const RowsAttnArgs &a = P.a;
+  dependency_wait();
+  const int c0 = blockIdx.x;
+  const int4 sp = P.split[c0];
+  const int parts = sp.z, hd = a.c.head_dim, g = P.g.d;
+  // (after a wait that ran out the notes may be those of another call: nothing outside the workspace is read)
+  if (parts <= 1 || parts > ctas - c0 || sp.x < 0 || sp.x >= P.plan->items || sp.y < 0 || sp.y >= a.c.kv_heads) return;
+  const int4 x = reinterpret_cast<const int4 *>(P.item + sp.x)[0];
+  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < x.z * kLanes; i += gridDim.y * kJoinThreads) {
+    const int r = i / kLanes, dd = (i - r * kLanes) * 4;
+    if (dd >= hd) continue;
+    const int q = (int)P.g.div(x.y + r), tok = x.x + q, h = sp.y * g + (x.y + r - q * g);
+    if (tok >= a.N || !row_live(a, tok)) continue;
+    float M = -INFINITY, Lr = 0.f, L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < parts; p0 += kJoinAhead) {
+      float4 o[kJoinAhead], ml[kJoinAhead];
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        ml[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p0 + u < parts) {
+          const int64_t at = (int64_t)(p0 + u == 0 ? 2 * c0 + 1 : 2 * (c0 + p0 + u)) * kRows + r;
+          ml[u] = __ldcg(P.share_ml + at);
+          o[u] = __ldcg(reinterpret_cast<const float4 *>(P.share_o + at * HDP + dd));
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) top = fmaxf(top, ml[u].x);
+      const float ref = top == -INFINITY ? 0.f : top, f0 = exp2f(M - ref);
+      M = top;
+      L *= f0;
+      Lr *= f0;
+      v.x *= f0;
+      v.y *= f0;
+      v.z *= f0;
+      v.w *= f0;
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const float f = exp2f(ml[u].x - ref);
+        Lr = fmaf(ml[u].y, f, Lr);
+        L = fmaf(ml[u].z, f, L);
+        v.x = fmaf(o[u].x, f, v.x);
+        v.y = fmaf(o[u].y, f, v.y);
+        v.z = fmaf(o[u].z, f, v.z);
+        v.w = fmaf(o[u].w, f, v.w);
+      }
+    }
+    float2 oml = make_float2(-INFINITY, 0.f);
+    float4 own = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (P.own_o) {
+      oml = P.own_ml[(int64_t)tok * a.H + h];
+      own = *reinterpret_cast<const float4 *>(P.own_o + ((int64_t)tok * a.H + h) * hd + dd);
+    }
+    const Finish fin = finish(M, Lr, L, oml, a.sink, h);
+    *reinterpret_cast<uint2 *>(a.o + (int64_t)tok * a.o_t + (int64_t)h * hd + dd) =
+        make_uint2(pack2(fmaf(own.x, fin.f_own, v.x * fin.f), fmaf(own.y, fin.f_own, v.y * fin.f)),
+                   pack2(fmaf(own.z, fin.f_own, v.z * fin.f), fmaf(own.w, fin.f_own, v.w * fin.f)));
+    if (a.lse && dd == 0) a.lse[(int64_t)tok * a.H + h] = fin.lse;
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ launch
+
+// Hands out parts of the workspace.
+struct Room {
+  uint8_t *at, *end;
+  template <class T>
+  T *take(size_t n) {
+    uint8_t *p = at;
+    at += (n * sizeof(T) + 255) / 256 * 256;
+    return reinterpret_cast<T *>(p);
+  }
+};
+
+template <int HDP>
+cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
+  using S = Shape<HDP>;
+  const RowsAttnArgs &a = p.a;
+  constexpr int TR = S::QT * kSub;
+  static SmemAttr attr;
+  cudaError_t e = attr.ensure((const void *)k_rows_attn<HDP>, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int g = a.H / a.c.kv_heads;
+  const int64_t cap = ((int64_t)a.N * g + TR - 1) / TR + a.S;
+  // no more CTAs than there can be tiles
+  const int64_t rows = (int64_t)a.width * a.c.page;
+  const int64_t tiles = (a.window > 0 ? std::min<int64_t>(rows, (int64_t)a.window + TR) : rows) / S::KVT + 2;
+  const bool one = rows <= S::KVT;  // (every item has one tile: nothing is shared)
+  const int64_t most = (double)cap * a.c.kv_heads * tiles > 1e9 ? num_sms : cap * a.c.kv_heads * (one ? 1 : tiles);
+  const int grid = (int)std::min<int64_t>(num_sms, most);
+  p.cap = (int)cap;
+  p.plan = room.take<Plan>(1);
+  p.item = room.take<Item>(cap);
+  p.start = room.take<unsigned long long>(cap + 1);
+  p.split = room.take<int4>(grid);
+  p.share_ml = room.take<float4>((size_t)2 * grid * TR);
+  p.share_o = room.take<float>((size_t)2 * grid * TR * HDP);
+  if (room.at > room.end || cap > (1 << 24)) return cudaErrorInvalidValue;
+  e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
+  if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p);
+  if (e != cudaSuccess || one) return e;
+  return launch_dependent(k_rows_join<HDP>, dim3(grid, 8), dim3(kJoinThreads), 0, s, 1, p, grid);
 }
 
 }  // namespace rows
 
+// Bytes of workspace that launch_rows_attn needs (an upper bound).
+size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms) {
+  const size_t hd = (size_t)(a.c.head_dim + 63) / 64 * 64, items = (size_t)a.N * (a.H / a.c.kv_heads) / 128 + 1 + a.S;
+  const size_t shares = (size_t)2 * num_sms * (hd == 256 ? 128 : 256) * (hd * 4 + 16);
+  const size_t own = a.pos ? (size_t)a.N * a.H * (a.c.head_dim * 4 + 8) + kPagedShareBytes : 0;
+  return items * 40 + shares + own + num_sms * 16 + 8192;
+}
+
 cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s) {
   rows::Params p;
+  memset((void *)&p, 0, sizeof(p));
   p.a = a;
   p.page = paged::FastDiv((uint32_t)a.c.page);
+  p.g = paged::FastDiv((uint32_t)(a.H / a.c.kv_heads));
   p.scale_log2 = (float)(a.scale * 1.4426950408889634);
-  return launch_dependent(rows::k_rows_attn, dim3((unsigned)(((int64_t)a.N * a.H + 3) / 4)), dim3(128), 0, s, 1, p);
+  rows::Room room{reinterpret_cast<uint8_t *>(ws), reinterpret_cast<uint8_t *>(ws) + ws_bytes};
+  if (a.pos) {  // the rows' own pages
+    PagedAttnArgs o{};
+    o.q = a.q;
+    o.q_t = a.q_t;
+    o.N = a.N;
+    o.H = a.H;
+    o.c = a.c;
+    o.table = a.own_table;
+    o.R = a.R;
+    o.width = a.own_width;
+    o.req = a.req;
+    o.pos = a.pos;
+    o.scale = a.scale;
+    o.window = a.window;
+    o.status = a.status;
+    float *own = room.take<float>((size_t)a.N * a.H * a.c.head_dim);
+    float2 *ml = room.take<float2>((size_t)a.N * a.H);
+    float *shares = room.take<float>(kPagedShareBytes / 4);
+    if (room.at > room.end) return cudaErrorInvalidValue;
+    o.part_o = own;
+    o.part_ml = ml;
+    const cudaError_t e = launch_paged_attn(o, shares, kPagedShareBytes, counters, num_sms, s);
+    if (e != cudaSuccess) return e;
+    p.own_o = own;
+    p.own_ml = ml;
+  }
+  const int hd = a.c.head_dim;
+  if (hd <= 64) return rows::launch<64>(p, room, num_sms, s);
+  if (hd <= 128) return rows::launch<128>(p, room, num_sms, s);
+  if (hd <= 192) return rows::launch<192>(p, room, num_sms, s);
+  return rows::launch<256>(p, room, num_sms, s);
 }
 
 }  // namespace csa

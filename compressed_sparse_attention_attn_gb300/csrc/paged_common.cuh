@@ -331,9 +331,9 @@ __device__ __forceinline__ float out_factor(float M, float L, const float *sink,
 
 // Join `parts` shares, shares i of slots slot(i), of NH heads x HD features by the NT threads of the CTA.  fin: write O
 // and lse of heads h0 .. h0+nh-1 of row n; else the joined share to slot `to` (one of the slots: a thread writes
-// only what it alone has read, the maxima and sums behind a barrier).  A thread reads the maxima and sums of its
+// only what it alone has read, the maxima and sums behind a barrier).  PART: a row's share is its result.  A thread reads the maxima and sums of its
 // head itself, with the values: one round trip a dozen shares, and no barrier.
-template <int NH, int HD, int NT, class Slot>
+template <int NH, int HD, int NT, bool PART, class Slot>
 __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool fin, int to, int n, int h0, int nh) {
   const PagedAttnArgs &a = P.a;
   const int hd = a.c.head_dim;
@@ -383,7 +383,11 @@ __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool
     }
     keep_m[rd] = M;
     keep_l[rd] = L;
-    if (fin) {
+    if (PART && fin) {
+      const int64_t at = (int64_t)n * a.H + h0 + h;
+      *reinterpret_cast<float4 *>(a.part_o + at * hd + d) = v;
+      if (d == 0) a.part_ml[at] = make_float2(M, L);
+    } else if (fin) {
       const float f = out_factor(M, L, a.sink, h0 + h);
       const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
       *reinterpret_cast<uint2 *>(a.o + (int64_t)n * a.o_t + (int64_t)(h0 + h) * hd + d) =
@@ -405,7 +409,7 @@ __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool
 
 // Publish this CTA's share of the segment that CTAs c0 .. c0 + parts - 1 share (already written to its slot by the CTA's threads)
 // and join what it completes: a dozen shares, a dozen of such groups, and so on.  flag: an int in shared memory.
-template <int NH, int HD, int NT>
+template <int NH, int HD, int NT, bool PART>
 __device__ __forceinline__ void publish(const Params &P, int c0, int parts, int n, int h0, int nh, int *flag) {
   auto slot_of = [c0](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
   int mine = (int)blockIdx.x - c0, step = 1;  // of `parts` joined shares, `step` CTAs apart
@@ -418,7 +422,7 @@ __device__ __forceinline__ void publish(const Params &P, int c0, int parts, int 
     __syncthreads();
     if (!*flag) return;
     const bool fin = parts <= kJoin;
-    join<NH, HD, NT>(P, in_grp, [&](int p) { return slot_of((first + p) * step); }, fin, slot_of(first * step), n, h0, nh);
+    join<NH, HD, NT, PART>(P, in_grp, [&](int p) { return slot_of((first + p) * step); }, fin, slot_of(first * step), n, h0, nh);
     if (fin) return;
     mine = first / kJoin;
     parts = (parts + kJoin - 1) / kJoin;
