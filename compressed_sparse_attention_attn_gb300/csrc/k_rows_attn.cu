@@ -25,6 +25,11 @@
 #include "paged_common.cuh"
 
 namespace csa {
+
+// 4-D bf16 tensor map with 128-byte swizzle, boxes {box_inner, 1, box_rows, 1} (defined with the GEMM's TMA helpers).
+bool tma_map_pages_bf16(CUtensorMap *m, const void *base, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t box_inner,
+                        uint32_t box_rows);
+
 namespace rows {
 
 constexpr int kSub = 128;     // rows of a product
@@ -73,7 +78,7 @@ struct Shape {
   static constexpr bool kSplit = HDP <= 128;
   static constexpr int kRegsSoft = 208, kRegsRest = 88;
   static constexpr int kQ = 0, kRing = QT * kQBytes, kBars = kRing + NST * kStage;
-  static constexpr int kSmem = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 32;  // (all that the kernel has: the swizzled tiles come first)
+  static constexpr int kSmem = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 48;  // (all that the kernel has: the swizzled tiles come first)
   static constexpr int kColO = 2 * KVT;                     // columns of tensor memory: two score buffers, then QT x HDP of O
 };
 
@@ -197,10 +202,15 @@ __device__ __forceinline__ int parts_of(unsigned long long total, int ctas) {
   return (int)min((unsigned long long)ctas, max(1ull, total / kMinPlaces));
 }
 
+struct Range {
+  unsigned long long places, p0, p1;  // of a kv head; the CTA's first and the end
+  int items, first;                   // of a kv head; the item that the CTA begins with
+};
 struct Walk {
   const Params *P;
-  unsigned long long places, p0, p1, base = 0;
-  int items, i, kvh, seq = -1;  // seq: items so far
+  const Range *rg;  // (in shared memory)
+  unsigned long long base = 0;
+  int i, kvh, seq = -1;  // seq: items so far
   Item d;
   int kt0, tiles;               // the item's tiles of positions
   int u0, u1;                   // of these, the CTA's
@@ -208,7 +218,8 @@ struct Walk {
   __device__ __forceinline__ bool load() {
     for (;; step()) {
       if (kvh >= P->a.c.kv_heads) return false;
-      base = places * kvh + __ldg(P->start + i);
+      const unsigned long long p0 = rg->p0, p1 = rg->p1;
+      base = rg->places * kvh + __ldg(P->start + i);
       if (base >= p1) return false;
       const int4 x = __ldg(reinterpret_cast<const int4 *>(P->item + i)), y = __ldg(reinterpret_cast<const int4 *>(P->item + i) + 1);
       d = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, 0};
@@ -223,7 +234,7 @@ struct Walk {
     }
   }
   __device__ __forceinline__ void step() {
-    if (++i == items) i = 0, ++kvh;
+    if (++i == rg->items) i = 0, ++kvh;
   }
   template <int KVT>
   __device__ __forceinline__ bool next() {
@@ -280,6 +291,17 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 }
 __device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+// sum + both halves (bf16), each added in f32
+__device__ __forceinline__ void add_halves(uint32_t v, float &x, float &y) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "r"(v));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ bool not_finite(uint32_t v) {  // either half
   return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
 }
@@ -304,8 +326,14 @@ __device__ __forceinline__ bool row_live(const RowsAttnArgs &a, int n) {
 
 // ------------------------------------------------------------------------------------------------ attention
 
+// Maps of the pages [page][row][kv head][feature], boxes of box_rows rows x 64 features inside a page (0: none).
+struct Maps {
+  CUtensorMap k, v;
+  int box_rows;
+};
+
 template <int HDP>
-__global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __grid_constant__ Params P, const __grid_constant__ Maps G) {
   using S = Shape<HDP>;
   constexpr int QT = S::QT, KVT = S::KVT, NP = S::NP, NST = S::NST, kSoft = S::kSoft, kW = KVT / 32;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -316,13 +344,13 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
   // full, empty: a stage has landed, has been used; s_full, p_full: scores, weights; pv_done: values added up; q_full
   uint64_t *full = bars, *empty = bars + NST, *s_full = bars + 2 * NST, *p_full = s_full + 2, *pv_done = s_full + 4,
-           *q_full = s_full + 6, *drain = s_full + 8;
+           *q_full = s_full + 6, *p_half = s_full + 8, *drain = s_full + 10;
   uint32_t *masks = reinterpret_cast<uint32_t *>(bars + 32);  // [kNote][4]: positions of a tile that are there
   int *odd_item = reinterpret_cast<int *>(masks + 4 * kNote);  // [kNote]: items with a value that is not finite where not all attend
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(odd_item + kNote);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  int *first_item = reinterpret_cast<int *>(tmem_slot + 2);
-  static_assert(2 * NST + 9 <= 32 && NST / 2 + 2 < kNote, "barriers, notes");
+  Range &rg = *reinterpret_cast<Range *>(tmem_slot + 2);
+  static_assert(2 * NST + 11 <= 32 && NST / 2 + 2 < kNote, "barriers, notes");
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -331,7 +359,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&s_full[b], 2);   // the products' completion, and the issuing thread (which has seen the stage's notes)
-      tc::mbar_init(&p_full[b], 128);
+      tc::mbar_init(&p_half[b], 4);   // a warp of the four each
+      tc::mbar_init(&p_full[b], 4);
       tc::mbar_init(&pv_done[b], 2);
       tc::mbar_init(&q_full[b], 128);
     }
@@ -341,29 +370,30 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     tc::fence_barrier_init();
   }
   dependency_wait();
-  Walk w{&P};
-  w.places = P.plan->places;
-  w.items = P.plan->items;
-  const unsigned long long total = w.places * a.c.kv_heads;
+  const unsigned long long places = P.plan->places, total = places * a.c.kv_heads;
+  const int items = P.plan->items;
   const int parts = parts_of(total, gridDim.x), cta = blockIdx.x;
   if (total == 0 || cta >= parts) {
     if (tid == 0) P.split[cta] = make_int4(0, 0, 0, 0);
     return;
   }
-  w.p0 = part_begin(total, parts, cta);
-  w.p1 = part_begin(total, parts, cta + 1);
-  {
-    const unsigned long long in = w.p0 % w.places;
-    for (int i = tid; i < w.items; i += S::kThreads)
-      if (P.start[i] <= in && in < P.start[i + 1]) *first_item = i;
+  const unsigned long long p0 = part_begin(total, parts, cta), in_head = p0 % places;
+  for (int i = tid; i < items; i += S::kThreads)
+    if (P.start[i] <= in_head && in_head < P.start[i + 1]) rg.first = i;
+  if (tid == 0) {
+    rg.places = places;
+    rg.p0 = p0;
+    rg.p1 = part_begin(total, parts, cta + 1);
+    rg.items = items;
   }
   if (warp == kSoft) tc::tmem_alloc(tmem_slot, 512);  // (behind the wait: a block of the kernel before may still ask for tensor memory)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  w.i = *first_item;
-  w.kvh = (int)(w.p0 / w.places);
+  Walk w{&P, &rg};
+  w.i = rg.first;
+  w.kvh = (int)(p0 / places);
   bool more = w.load<KVT>();
 
   if (warp < kSoft) {
@@ -429,31 +459,26 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       const bool work = t * kSub + quad * 32 < d.rows;  // (of the warp)
       float m = -INFINITY, l = 0.f, lr = 0.f;
       const int j0 = w.kt0 + w.u0, item_tiles = w.u1 - w.u0;
-      Walk nx = w;
-      bool more_next = false;
-      if (y == x) {
-        more_next = nx.next<KVT>();
-        if (more_next && has_rows(nx)) {
-          load_q(nx.d, nx.kvh);
-          attn::cp_async_wait_all();
-          attn::fence_proxy_async();
-          tc::mbar_arrive(&q_full[t]);
-        }
+      auto next_q = [&]() -> bool {  // the next item's q on its way (its last reader is done); w stays, not to hold two items in registers
+        Walk nx = w;
+        if (!nx.next<KVT>() || !has_rows(nx)) return false;
+        load_q(nx.d, nx.kvh);
+        return true;
+      };
+      if (y == x && next_q()) {
+        attn::cp_async_wait_all();
+        attn::fence_proxy_async();
+        tc::mbar_arrive(&q_full[t]);
       }
       for (int j = x; j < y; ++j) {
         const int b = QT == 2 ? t : n_s & 1;
         if (!(ok = warp_wait(&s_full[b], QT == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag))) break;
         tc::tc_fence_after();
-        const bool last = j + 1 == y;
-        bool q_next = false;
-        if (last) {  // q's last reader is done: the next item's q on its way
-          more_next = nx.next<KVT>();
-          q_next = more_next && has_rows(nx);
-          if (q_next) load_q(nx.d, nx.kvh);
-        }
+        const bool q_next = j + 1 == y && next_q();
         if (work) {
           const uint32_t tS = tmem + b * KVT + lane_off;
-          float s[KVT];
+          float2 s[KVT / 2];
+          float q4[4];  // maxima in four chains, so that one's latency passes in the others
           {
             uint32_t v[kW][32];
 #pragma unroll
@@ -463,13 +488,13 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
             for (int k = 0; k < kW; ++k) {
               tie32(v[k]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[32 * k + e] = __uint_as_float(v[k][e]);
+              for (int e = 0; e < 16; ++e) s[16 * k + e] = make_float2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1]));
             }
           }
           float sc = P.scale_log2;
-          if (odd_scale) {  // (a negative one would make the largest score the smallest; 0 times a mask's -inf is not -inf)
+          if (__builtin_expect(odd_scale, 0)) {  // (a negative one would make the largest score the smallest; 0 times a mask's -inf is not -inf)
 #pragma unroll
-            for (int k = 0; k < KVT; ++k) s[k] *= sc;
+            for (int k = 0; k < KVT / 2; ++k) s[k].x *= sc, s[k].y *= sc;
             sc = 1.f;
           }
           {
@@ -478,7 +503,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
             uint32_t there[kW], all = 0xffffffffu;
 #pragma unroll
             for (int k = 0; k < kW; ++k) all &= there[k] = mk[k];
-            if (!__all_sync(0xffffffffu, all == 0xffffffffu && from <= 0 && to >= KVT - 1)) {
+            if (__builtin_expect(!__all_sync(0xffffffffu, all == 0xffffffffu && from <= 0 && to >= KVT - 1), 0)) {
 #pragma unroll
               for (int k = 0; k < kW; ++k) {
                 const int f = min(max(from - 32 * k, 0), 32), e = min(max(to - 32 * k, -1), 31) + 1;
@@ -486,19 +511,27 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
                 mask &= f == 32 ? 0u : 0xffffffffu << f;
                 mask &= there[k];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) s[32 * k + c] = (mask >> c) & 1u ? s[32 * k + c] : -INFINITY;
+                for (int c = 0; c < 16; ++c) {
+                  s[16 * k + c].x = (mask >> (2 * c)) & 1u ? s[16 * k + c].x : -INFINITY;
+                  s[16 * k + c].y = (mask >> (2 * c + 1)) & 1u ? s[16 * k + c].y : -INFINITY;
+                }
               }
             }
           }
-          float mx = fmaxf(s[0], s[1]);
+          float mx;
+          {
 #pragma unroll
-          for (int k = 2; k < KVT; k += 2) mx = fmaxf(mx, fmaxf(s[k], s[k + 1]));
+            for (int k = 0; k < 4; ++k) q4[k] = fmaxf(s[k].x, s[k].y);
+#pragma unroll
+            for (int k = 4; k < KVT / 2; ++k) q4[k & 3] = max3(q4[k & 3], s[k].x, s[k].y);
+            mx = fmaxf(max3(q4[0], q4[1], q4[2]), q4[3]);
+          }
           if (j == x) {
             m = mx;
           } else {
             const bool raise = (mx - m) * sc > kRaise || (m == -INFINITY && mx > m);
             const float al = raise ? (m == -INFINITY ? 0.f : paged::ex2((m - mx) * sc)) : 1.f;
-            if (__any_sync(0xffffffffu, raise)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
               if (!(ok = values_done())) break;
               tc::tc_fence_after();
               if (raise) m = mx;
@@ -515,29 +548,39 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
             }
           }
           const float ref = m == -INFINITY ? 0.f : m * sc;
+          const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
           uint32_t pk[KVT / 2];
+          float2 l4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int k = 0; k < KVT / 32; ++k) {
             uint32_t v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = paged::ex2(fmaf(s[32 * k + 2 * e], sc, -ref)), p1 = paged::ex2(fmaf(s[32 * k + 2 * e + 1], sc, -ref));
-              l += p0 + p1;
-              v[e] = pk[16 * k + e] = pack2(p0, p1);
+              const float2 z = __ffma2_rn(s[16 * k + e], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
+              l4[e & 1] = __fadd2_rn(l4[e & 1], p);
+              v[e] = pk[16 * k + e] = pack2(p.x, p.y);
             }
             attn::tmem_st16(tS + 16 * k, v);
+            if (k == KVT / 64 - 1 || k == KVT / 32 - 1) {  // (the product of the first half begins beside the second half's exponentials)
+              attn::tmem_st_wait();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(k == KVT / 64 - 1 ? &p_half[b] : &p_full[b]);
+            }
           }
-          attn::tmem_st_wait();
-          tc::tc_fence_before();
-          tc::mbar_arrive(&p_full[b]);
           // (behind what the product waits for)
-          float sum = 0.f;
+          l += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
+          l4[0] = l4[1] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < KVT / 2; ++k) sum += low(pk[k]) + high(pk[k]);
-          lr += sum;
+          for (int k = 0; k < KVT / 2; ++k) add_halves(pk[k], l4[k & 1].x, l4[k & 1].y);
+          lr += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
         } else {
           tc::tc_fence_before();
-          tc::mbar_arrive(&p_full[b]);
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(&p_half[b]);
+            tc::mbar_arrive(&p_full[b]);
+          }
         }
         ++n_s;
         ++n_pv;
@@ -649,8 +692,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         split = make_int4(w.i, w.kvh, c - cta + 1, 0);
       }
       tile0 += item_tiles;
-      w = nx;
-      more = more_next;
+      more = w.next<KVT>();
     }
     attn::cp_async_wait_all();
     if (tid == 0) P.split[cta] = split;
@@ -669,21 +711,25 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       uint32_t n_q[2] = {}, n_s = 0, n_p[2] = {};
       auto scores = [&](int t, int b, int stage) {
         const uint32_t A = dq + t * (S::kQBytes >> 4), B = dk + (stage % NST) * (S::kStage >> 4);
-#pragma unroll 1
-        for (int k = 0; k < ks; ++k)
-          tc::mma_bf16(tmem + b * KVT, hi | (A + (k >> 2) * (kSub * 128 >> 4) + (k & 3) * 2),
+#pragma unroll
+        for (int k = 0; k < HDP / 16; ++k)
+          if (k < 4 * (NP - 1) + 1 || k < ks) tc::mma_bf16(tmem + b * KVT, hi | (A + (k >> 2) * (kSub * 128 >> 4) + (k & 3) * 2),
                        hi | (B + (k >> 2) * (KVT * 128 >> 4) + (k & 3) * 2), id_s, k ? 1u : 0u);
         tc::mma_commit(&s_full[b]);
         tc::mbar_arrive(&s_full[b]);
       };
-      auto values = [&](int t, int b, int stage, bool first) {
+      auto values = [&](int t, int b, int stage, bool first, uint32_t parity) -> bool {  // (the weights' first half is there)
         tc::tc_fence_after();
-        const uint32_t B = dv + (stage % NST) * (S::kStage >> 4);
+        const uint32_t B = dv + (stage % NST) * (S::kStage >> 4), dO = tmem + S::kColO + t * HDP, A = tmem + b * KVT;
 #pragma unroll
-        for (int k = 0; k < KVT / 16; ++k)
-          mma_ts(tmem + S::kColO + t * HDP, tmem + b * KVT + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
+        for (int k = 0; k < KVT / 32; ++k) mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
+        if (!tc::mbar_wait(&p_full[b], parity, abort_flag)) return false;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = KVT / 32; k < KVT / 16; ++k) mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, 1u);
         tc::mma_commit(&pv_done[b]);
         tc::mbar_arrive(&pv_done[b]);
+        return true;
       };
       bool ok = true;
       while (more && ok) {
@@ -719,11 +765,12 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           for (int t = 0; t < QT; ++t) {
             if (x[t] <= j && j < y[t]) {
               const int b = QT == 2 ? t : n_p[0] & 1;
-              if (!(ok = tc::mbar_wait(&p_full[b], QT == 2 ? n_p[t] & 1 : (n_p[0] >> 1) & 1, abort_flag))) break;
+              const uint32_t parity = QT == 2 ? n_p[t] & 1 : (n_p[0] >> 1) & 1;
+              if (!(ok = tc::mbar_wait(&p_half[b], parity, abort_flag))) break;
               ++n_p[t];
               if (!v_in && !(ok = stage_ready(sv))) break;
               v_in = true;
-              values(t, b, sv, j == x[t]);
+              if (!(ok = values(t, b, sv, j == x[t], parity))) break;
             }
             if (QT == 2 && next && x[t] <= j + 1 && j + 1 < y[t]) {
               if (!k_in && !(ok = stage_ready(sk))) break;
@@ -760,7 +807,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       bool values, part;  // part: positions that not every row attends
     };
     int s = lw, x = lw, tile0 = 0;  // stage, stage of the item, first tile of the item
-    auto look = [&](Look &f) -> bool {
+    auto look = [&](Look &f) __attribute__((always_inline)) -> bool {
       while (more && x >= 2 * (w.u1 - w.u0)) {
         x -= 2 * (w.u1 - w.u0);
         tile0 += w.u1 - w.u0;
@@ -792,38 +839,73 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     };
     Look f;
     bool have = look(f);
+    if (G.box_rows && lane == 0) {
+      tc::prefetch_tmap(&G.k);
+      tc::prefetch_tmap(&G.v);
+    }
     while (have) {
       const bool vals = f.values && a.c.v;
       const bf16 *src = reinterpret_cast<const bf16 *>(vals ? a.c.v : a.c.k) + f.kvh * (vals ? a.c.v_head : a.c.k_head) + cc * 8;
       const int64_t st_page = vals ? a.c.v_page : a.c.k_page, st_row = vals ? a.c.v_row : a.c.k_row;
       const int buf = s % NST;
-      int64_t off[kW];
-      uint32_t there[kW];
+      uint32_t there[kW], all = 0xffffffffu;  // positions that are there
 #pragma unroll
       for (int k = 0; k < kW; ++k) {
         const uint32_t p = f.at + 32 * k + lane;
         const bool in = p >= (uint32_t)f.begin && p < (uint32_t)f.end, good = in && f.page[k] >= 0 && f.page[k] < a.c.n_pages;
         if (in && !good) atomicOr(a.status, kStatusBadIndex);
-        off[k] = good ? f.page[k] * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
-        there[k] = __ballot_sync(0xffffffffu, good);
+        all &= there[k] = __ballot_sync(0xffffffffu, good);
       }
       if (s >= NST && !warp_wait(&empty[buf], (uint32_t)((s / NST - 1) & 1), abort_flag)) break;
       if (!f.values && lane == 0)
 #pragma unroll
         for (int k = 0; k < kW; ++k) masks[4 * (f.tile & (kNote - 1)) + k] = there[k];
-      const uint32_t dst = s_ring + buf * S::kStage + (lane >> 3) * 128;
+      if (G.box_rows && all == 0xffffffffu && !(f.values && f.part)) {
+        // A whole tile, which every row attends: by TMA, a lane a box.
+        const int R = G.box_rows, first = lane * R;
+        int page = 0;
 #pragma unroll
-      for (int k = 0; k < kW; ++k)
+        for (int k = 0; k < kW; ++k) {
+          const int x0 = __shfl_sync(0xffffffffu, f.page[k], first & 31);
+          if ((first >> 5) == k) page = x0;
+        }
+        if (lane == 0) tc::mbar_expect_tx(&full[buf], S::kStage);
+        __syncwarp();
+        if (first < KVT) {
+          const uint32_t p = f.at + first;
+          const int row = (int)(p - P.page.div(p) * P.page.d);
+#pragma unroll
+          for (int kb = 0; kb < NP; ++kb)
+            tc::tma_load_4d(s_ring + buf * S::kStage + kb * (KVT * 128) + first * 128, vals ? &G.v : &G.k, &full[buf], kb * 64, f.kvh, row,
+                            page);
+        }
+        if (lane != 0) tc::mbar_arrive(&full[buf]);
+        s += S::kLoad;
+        x += S::kLoad;
+        have = look(f);
+        continue;
+      }
+      const uint32_t dst = s_ring + buf * S::kStage + (lane >> 3) * 128;
+#pragma unroll 1
+      for (int k = 0; k < kW; ++k) {  // (rolled: four times the code would be fetched anew for every stage)
+        int page = f.page[0];
+        uint32_t good = there[0];
+#pragma unroll
+        for (int e = 1; e < kW; ++e)
+          if (k == e) page = f.page[e], good = there[e];
+        const uint32_t p = f.at + 32 * k + lane;
+        const int64_t off = (good >> lane) & 1u ? page * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes 128 bytes of a row
-          const int row = 32 * k + 4 * i, r7 = (row + (lane >> 3)) & 7;
-          const int64_t o = __shfl_sync(0xffffffffu, off[k], 4 * i + (lane >> 3));
+          const int r7 = (4 * i + (lane >> 3)) & 7;
+          const int64_t o = __shfl_sync(0xffffffffu, off, 4 * i + (lane >> 3));
 #pragma unroll
           for (int kb = 0; kb < NP; ++kb) {
             const bool in = o >= 0 && kb * 64 + cc * 8 < hd;
-            attn::cp_async16(dst + kb * (KVT * 128) + row * 128 + ((cc ^ r7) << 4), in ? src + o + kb * 64 : src, in);
+            attn::cp_async16(dst + kb * (KVT * 128) + k * 4096 + i * 512 + ((cc ^ r7) << 4), in ? src + o + kb * 64 : src, in);
           }
         }
+      }
       const bool check = f.values && f.part;
       const int seq = f.seq, cur = s;
       s += S::kLoad;
@@ -859,6 +941,13 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       tc::mbar_arrive(&full[cur % NST]);
     }
     attn::cp_async_wait_all();
+    // Nothing is in flight when the CTA ends.  The products wait for every stage; after a wait that ran out, they do not.
+    if (*abort_flag)
+      for (int i = s - S::kLoad; i >= 0 && i > s - S::kLoad - NST; i -= S::kLoad) {
+        const uint64_t t1 = tc::global_ns();
+        while (!tc::mbar_try_wait(&full[i % NST], (uint32_t)((i / NST) & 1)) && tc::global_ns() - t1 < 10000000) {
+        }
+      }
     }
   }
   tc::tc_fence_before();
@@ -977,8 +1066,24 @@ cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
   p.share_ml = room.take<float4>((size_t)2 * grid * TR);
   p.share_o = room.take<float>((size_t)2 * grid * TR * HDP);
   if (room.at > room.end || cap > (1 << 24)) return cudaErrorInvalidValue;
+  // TMA where pages hold whole boxes of 8 rows (the swizzle's period) or more, up to a tile
+  Maps maps;
+  memset((void *)&maps, 0, sizeof(maps));
+  const int box = std::min(a.c.page & -a.c.page, S::KVT);
+  if (box >= 8) {
+    auto map = [&](CUtensorMap *m, const void *base, int64_t page, int64_t row, int64_t head) {
+      const uint64_t dims[4] = {(uint64_t)a.c.head_dim, (uint64_t)a.c.kv_heads, (uint64_t)a.c.page, (uint64_t)a.c.n_pages};
+      const uint64_t one_row = 2 * (uint64_t)a.c.head_dim;  // (strides of dimensions of size 1 may be anything)
+      const uint64_t strides[3] = {a.c.kv_heads > 1 ? 2 * (uint64_t)head : one_row, a.c.page > 1 ? 2 * (uint64_t)row : one_row,
+                                   a.c.n_pages > 1 ? 2 * (uint64_t)page : one_row};
+      return tma_map_pages_bf16(m, base, dims, strides, 64, (uint32_t)box);
+    };
+    if (map(&maps.k, a.c.k, a.c.k_page, a.c.k_row, a.c.k_head) &&
+        (!a.c.v || map(&maps.v, a.c.v, a.c.v_page, a.c.v_row, a.c.v_head)))
+      maps.box_rows = box;
+  }
   e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
-  if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p);
+  if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
   if (e != cudaSuccess || one) return e;
   return launch_dependent(k_rows_join<HDP>, dim3(grid, 8), dim3(kJoinThreads), 0, s, 1, p, grid);
 }
