@@ -40,8 +40,9 @@ constexpr float kRaise = 8.f;
 
 // Rows row0 .. row0 + rows - 1 of the segment whose first token is tok0; positions begin .. end - 1 behind table row seg are all that
 // any of them attends.  Token t of a prompt stands at t + shift; of a prefix shift is its length.
+// end0, begin1: of its first 128 rows, of the others.  at0 .. at1: positions that every row attends (with a window in a prefix: none).
 struct Item {
-  int tok0, row0, rows, seg, begin, end, shift, spare;
+  int tok0, row0, rows, seg, begin, end, shift, end0, begin1, at0, at1, spare;
 };
 struct Plan {
   unsigned long long places;  // of one kv head
@@ -52,6 +53,7 @@ struct Params {
   RowsAttnArgs a;
   paged::FastDiv page, g;
   float scale_log2;
+  int wide;                    // o's rows are whole 32 bytes on such borders
   Plan *plan;
   Item *item;                  // [cap]
   unsigned long long *start;   // [cap + 1]: first place of an item
@@ -71,14 +73,15 @@ struct Shape {
   static constexpr int NP = HDP / 64;                       // 64-feature panels
   static constexpr int kQBytes = kSub * HDP * 2, kStage = KVT * HDP * 2;
   static constexpr int NST = HDP == 64 ? 8 : 5;             // stages: a tile's keys or values
-  static constexpr int kSoft = 4 * QT, kLoad = 3;           // warps
-  static constexpr int kThreads = (kSoft + 1 + kLoad) * 32;
+  static constexpr int kSoft = 4 * QT, kMma = QT, kLoad = 4 - QT;  // warps
+  static constexpr int kThreads = (kSoft + kMma + kLoad) * 32;
   // Registers a thread, softmax and the others: a row's 128 scores do not fit in the 168 that 384 threads get each.  They add up
   // to what the block is launched with: 256 x 208 + 128 x 88 = 384 x 168.
   static constexpr bool kSplit = HDP <= 128;
   static constexpr int kRegsSoft = 208, kRegsRest = 88;
   static constexpr int kQ = 0, kRing = QT * kQBytes, kBars = kRing + NST * kStage;
-  static constexpr int kSmem = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 48;  // (all that the kernel has: the swizzled tiles come first)
+  static constexpr int kSlots = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 80;
+  static constexpr int kSmem = kSlots + (kSoft + kMma) * 2 * 64;  // (all that the kernel has: the swizzled tiles come first)
   static constexpr int kColO = 2 * KVT;                     // columns of tensor memory: two score buffers, then QT x HDP of O
 };
 
@@ -163,13 +166,20 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
         it.seg = s0 + lo;
         if (a.pos) {  // (a row's own part begins at len or behind it: the window reaches back to len - window at most)
           it.shift = sg.z;
-          it.begin = a.window > 0 ? max(0, sg.z - a.window) : 0;
-          it.end = (int)min((int64_t)sg.z, cap);
+          it.begin = it.begin1 = a.window > 0 ? max(0, sg.z - a.window) : 0;
+          it.end = it.end0 = (int)min((int64_t)sg.z, cap);
+          it.at0 = 0;
+          it.at1 = a.window > 0 ? 0 : it.end;
         } else {
           it.shift = sg.z - sg.x - sg.y;
-          const int ta = sg.x + (int)P.g.div(it.row0), tb = sg.x + (int)P.g.div(it.row0 + it.rows - 1);
-          it.begin = a.window > 0 ? max(0, ta + it.shift - a.window + 1) : 0;
-          it.end = (int)min((int64_t)tb + it.shift + 1, cap);
+          auto pos = [&](int r) { return (int64_t)sg.x + P.g.div(it.row0 + min(r, it.rows - 1)) + it.shift; };  // of a row
+          auto first = [&](int64_t p) { return (int)(a.window > 0 ? max((int64_t)0, p - a.window + 1) : 0); };
+          it.begin = first(pos(0));
+          it.begin1 = first(pos(kSub));
+          it.end0 = (int)min(pos(kSub - 1) + 1, cap);
+          it.end = (int)min(pos(it.rows - 1) + 1, cap);
+          it.at0 = first(pos(it.rows - 1));
+          it.at1 = (int)min(pos(0) + 1, cap);
         }
         mine = it.end > it.begin ? (it.end - 1) / KVT - it.begin / KVT + 1 : 1;
         mine += kEnd;
@@ -177,7 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
       const unsigned long long incl = block_scan(mine, s_sum, sum);
       if (i < all) {
         reinterpret_cast<int4 *>(P.item + items + i)[0] = make_int4(it.tok0, it.row0, it.rows, it.seg);
-        reinterpret_cast<int4 *>(P.item + items + i)[1] = make_int4(it.begin, it.end, it.shift, 0);
+        reinterpret_cast<int4 *>(P.item + items + i)[1] = make_int4(it.begin, it.end, it.shift, it.end0);
+        reinterpret_cast<int4 *>(P.item + items + i)[2] = make_int4(it.begin1, it.at0, it.at1, 0);
         P.start[items + i] = places + incl - mine;
       }
       places += sum;
@@ -204,66 +215,102 @@ __device__ __forceinline__ int parts_of(unsigned long long total, int ctas) {
 
 struct Range {
   unsigned long long places, p0, p1;  // of a kv head; the CTA's first and the end
-  int items, first;                   // of a kv head; the item that the CTA begins with
+  int items, first, kvh;              // of a kv head; the item and the head that the CTA begins with
 };
+// An item as the plan has it, and its first place.
+struct Slot {
+  int4 a, b, c;
+  unsigned long long start, spare;
+};
+// A role's way through its CTA's items.  SLOT: the next item's description is on its way to shared memory (two slots a warp, by cp.async)
+// while one is worked on: from global memory it would take two trips in a row at the end of every item.
+template <int KVT, bool SLOT>
 struct Walk {
   const Params *P;
   const Range *rg;  // (in shared memory)
+  Slot *slot;
   unsigned long long base = 0;
   int i, kvh, seq = -1;  // seq: items so far
   Item d;
   int kt0, tiles;               // the item's tiles of positions
   int u0, u1;                   // of these, the CTA's
-  template <int KVT>
+
+  __device__ __forceinline__ void fetch(int to, int item, bool by) const {
+    if (!by) return;
+    const uint32_t dst = tc::smem_u32(slot + to);
+    const int4 *src = reinterpret_cast<const int4 *>(P->item + item);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%0 + 16], [%1 + 16], 16;\n\t"
+                 "cp.async.cg.shared.global [%0 + 32], [%1 + 32], 16;" ::"r"(dst), "l"(src)
+                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0 + 48], [%1], 8;" ::"r"(dst), "l"(P->start + item) : "memory");
+  }
+  // The item's place and parts from its description; false: it is behind the CTA's part.
+  __device__ __forceinline__ bool set(int4 x, int4 y, int4 z, unsigned long long start) {
+    const unsigned long long p0 = rg->p0, p1 = rg->p1;
+    base = rg->places * kvh + start;
+    if (base >= p1) return false;
+    d = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, 0};
+    kt0 = d.begin / KVT;
+    tiles = d.end > d.begin ? (d.end - 1) / KVT - kt0 + 1 : 1;
+    u0 = base < p0 ? (int)min(p0 - base, 0x7fffffffull) : 0;
+    u1 = (int)min((unsigned long long)tiles, p1 - base);
+    return true;
+  }
   __device__ __forceinline__ bool load() {
-    for (;; step()) {
-      if (kvh >= P->a.c.kv_heads) return false;
-      const unsigned long long p0 = rg->p0, p1 = rg->p1;
-      base = rg->places * kvh + __ldg(P->start + i);
-      if (base >= p1) return false;
-      const int4 x = __ldg(reinterpret_cast<const int4 *>(P->item + i)), y = __ldg(reinterpret_cast<const int4 *>(P->item + i) + 1);
-      d = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, 0};
-      kt0 = d.begin / KVT;
-      tiles = d.end > d.begin ? (d.end - 1) / KVT - kt0 + 1 : 1;
-      u0 = base < p0 ? (int)min(p0 - base, 0x7fffffffull) : 0;
-      u1 = (int)min((unsigned long long)tiles, p1 - base);
-      if (u0 < u1) {
-        ++seq;
-        return true;
-      }
-    }
+    if (kvh >= P->a.c.kv_heads) return false;
+    const int4 *at = reinterpret_cast<const int4 *>(P->item + i);
+    return set(__ldg(at), __ldg(at + 1), __ldg(at + 2), __ldg(P->start + i));
   }
   __device__ __forceinline__ void step() {
     if (++i == rg->items) i = 0, ++kvh;
   }
-  template <int KVT>
-  __device__ __forceinline__ bool next() {
+  __device__ __forceinline__ void ahead(bool by) {  // the item after this one on its way
+    if (SLOT) fetch((seq + 1) & 1, i + 1 == rg->items ? 0 : i + 1, by);
+  }
+  // The first item (all lanes that use the slots together; `by`: the one that copies).
+  __device__ __forceinline__ bool first(bool by) {
+    bool more = load();
+    if (more && u0 >= u1) {  // (the part begins in the place of an item's end)
+      step();
+      more = load();
+    }
+    seq = 0;
+    if (more) ahead(by);
+    return more;
+  }
+  __device__ __forceinline__ bool peek() {  // on to the next item (copies waited for by whoever made them)
     step();
-    return load<KVT>();
+    if (!SLOT) return load();
+    if (kvh >= P->a.c.kv_heads) return false;
+    const Slot &n = slot[(seq + 1) & 1];
+    return set(n.a, n.b, n.c, n.start);
+  }
+  __device__ __forceinline__ bool next(bool by) {
+    const bool more = peek();
+    ++seq;
+    if (more) ahead(by);
+    return more;
   }
   __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == tiles; }
 };
 
 // The position tiles x .. y - 1, of the CTA's, that 128-row tile t of an item attends.
-template <int KVT>
-__device__ __forceinline__ void sub_range(const Params &P, const Walk &w, int t, int &x, int &y) {
-  const Item &d = w.d;
-  const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1, r0 = kSub * t;
-  x = y = j0;
-  if (r0 >= d.rows) return;
-  int lo = d.begin, end = d.end;
-  if (!P.a.pos) {
-    const int ta = d.tok0 + (int)P.g.div(d.row0 + r0), tb = d.tok0 + (int)P.g.div(d.row0 + min(r0 + kSub, d.rows) - 1);
-    if (P.a.window > 0) lo = max(0, ta + d.shift - P.a.window + 1);
-    end = (int)min((int64_t)end, (int64_t)tb + d.shift + 1);
-  }
-  if (end <= lo) return;
+template <int KVT, bool SLOT>
+__device__ __forceinline__ void sub_range(const Walk<KVT, SLOT> &w, int t, int &x, int &y) {
+  const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1, lo = t ? w.d.begin1 : w.d.begin, end = t ? w.d.end : w.d.end0;
   x = max(j0, lo / KVT);
-  y = max(x, min(j1, (end - 1) / KVT + 1));
+  y = min(j1, (end - 1) / KVT + 1);  // (all of them not negative)
+  if (kSub * t >= w.d.rows || end <= lo || y < x) x = y = j0;
 }
 
 // ------------------------------------------------------------------------------------------------ building blocks
 
+// (The kernel's code is larger than the instruction cache next to the schedulers, and a line that is not there costs as much as 15
+// instructions: what is rarely run is out of line, loops are rolled where that costs little.)
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort) { return tc::mbar_wait(bar, parity, abort); }
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return tc::mbar_try_wait(bar, parity) || wait_on(bar, parity, abort);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
   const bool ok = tc::mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
@@ -284,6 +331,12 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
                  "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// 32 bytes by one lane: a row's whole sector (16 at a time, a row a lane, each store would touch 32 sectors twice).
+__device__ __forceinline__ void store32(void *p, const uint32_t *u) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
+               "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
@@ -311,17 +364,150 @@ struct Finish {
   float f, f_own, lse;
 };
 __device__ __forceinline__ Finish finish(float m, float lr, float l, float2 own, const float *sink, int h) {
-  const float M = fmaxf(m, own.x);
-  const float e = m == -INFINITY ? 0.f : exp2f(m - M), eo = own.x == -INFINITY ? 0.f : exp2f(own.x - M);
-  const float L = lr * e + own.y * eo, Lt = l * e + own.y * eo;
-  const float f = paged::out_factor(M, L, sink, h);
-  return {f * e, f * eo, Lt == 0.f ? -INFINITY : (M + log2f(Lt)) * 0.6931471805599453f};
+  const float M = fmaxf(m, own.x), ref = M == -INFINITY ? 0.f : M;
+  const float e = paged::ex2(m - ref), eo = paged::ex2(own.x - ref);  // (2^-inf = 0)
+  const float f = paged::out_factor(M, fmaf(own.y, eo, lr * e), sink, h), sum = fmaf(own.y, eo, l * e);
+  return {f * e, f * eo, sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f};
 }
 // Whether a row of the prefix form is there, and not padding.
 __device__ __forceinline__ bool row_live(const RowsAttnArgs &a, int n) {
   if (!a.pos) return true;
   const int req = a.req ? a.req[n] : n;
   return a.pos[n] >= -1 && req >= 0 && req < a.R;
+}
+
+// A row's weights of a tile from its scores, which the lane finds in its columns from tS on and where the weights go.  MASK: the row
+// attends positions from .. to where `there` has them, or the scale is not positive (in a copy of its own, so that the other's
+// code has no gaps).
+template <int HDP, bool MASK, class Done>
+__device__ __forceinline__ bool weights(float sc, int from, int to, uint4 there, float &m, float &l, float &lr, bool first, uint32_t tS,
+                                        uint32_t tO, int hd16, uint64_t *p_half, uint64_t *p_full, int lane, Done &&values_done) {
+  constexpr int KVT = Shape<HDP>::KVT, kW = KVT / 32;
+  const bool plain = !MASK || sc > 0.f;
+  const float2 sc2 = plain ? make_float2(sc, sc) : make_float2(1.f, 1.f);
+  float2 s[KVT / 2], l4[2];
+  uint32_t pk[KVT / 2];
+  float ref;
+  // The first quarter's exponentials by the maximum so far, the tile's maximum beside them (it costs nothing there); once more from the
+  // scores on in the rare case that it is larger by more than 2^8.
+#pragma unroll 1
+  for (;;) {
+    {
+      uint32_t v[kW][32];
+#pragma unroll
+      for (int k = 0; k < kW; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < kW; ++k) {
+        tie32(v[k]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[16 * k + e] = make_float2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1]));
+      }
+    }
+    if constexpr (MASK) {
+      if (!plain) {  // (a negative scale would make the largest score the smallest; 0 times a mask's -inf is not -inf)
+#pragma unroll
+        for (int k = 0; k < KVT / 2; ++k) s[k].x *= sc, s[k].y *= sc;
+      }
+      const uint32_t mk[4] = {there.x, there.y, there.z, there.w};
+#pragma unroll
+      for (int k = 0; k < kW; ++k) {
+        const int f = min(max(from - 32 * k, 0), 32), e = min(max(to - 32 * k, -1), 31) + 1;
+        uint32_t mask = e == 32 ? 0xffffffffu : (1u << e) - 1u;
+        mask &= f == 32 ? 0u : 0xffffffffu << f;
+        mask &= mk[k];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          s[16 * k + c].x = (mask >> (2 * c)) & 1u ? s[16 * k + c].x : -INFINITY;
+          s[16 * k + c].y = (mask >> (2 * c + 1)) & 1u ? s[16 * k + c].y : -INFINITY;
+        }
+      }
+    }
+    ref = m == -INFINITY ? 0.f : m * sc2.x;
+    const float2 ref2 = make_float2(-ref, -ref);
+    l4[0] = l4[1] = make_float2(0.f, 0.f);
+    float q4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four chains, so that one's latency passes in the others)
+#pragma unroll
+    for (int k = 0; k < KVT / 8; ++k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q4[e] = max3(q4[e], s[e * (KVT / 8) + k].x, s[e * (KVT / 8) + k].y);
+      const float2 z = __ffma2_rn(s[k], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
+      l4[k & 1] = __fadd2_rn(l4[k & 1], p);
+      pk[k] = pack2(p.x, p.y);
+    }
+    const float mx = fmaxf(max3(q4[0], q4[1], q4[2]), q4[3]);
+    const bool raise = (mx - m) * sc2.x > kRaise || (m == -INFINITY && mx > m);
+    if (__builtin_expect(!__any_sync(0xffffffffu, raise), 1)) break;
+    const float al = raise ? (m == -INFINITY ? 0.f : paged::ex2((m - mx) * sc2.x)) : 1.f;
+    if (raise) m = mx;
+    l *= al;
+    lr *= al;
+    if (!first) {
+      if (!values_done()) return false;
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < hd16; c += 16) {
+        uint32_t v[16];
+        tc::tmem_ld16_wait(tO + c, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+        attn::tmem_st16(tO + c, v);
+      }
+    }
+  }
+  const float2 ref2 = make_float2(-ref, -ref);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {  // (the product of the first half begins beside the second half's exponentials)
+#pragma unroll
+    for (int k = half * (KVT / 64); k < (half + 1) * (KVT / 64); ++k) {
+      uint32_t v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (half || 16 * k + e >= KVT / 8) {
+          const float2 z = __ffma2_rn(s[16 * k + e], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
+          l4[e & 1] = __fadd2_rn(l4[e & 1], p);
+          pk[16 * k + e] = pack2(p.x, p.y);
+        }
+        v[e] = pk[16 * k + e];
+      }
+      attn::tmem_st16(tS + 16 * k, v);
+    }
+    attn::tmem_st_wait();
+    tc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(half ? p_full : p_half);
+  }
+  // (behind what the product waits for)
+  l += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
+  l4[0] = l4[1] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < KVT / 2; ++k) add_halves(pk[k], l4[k & 1].x, l4[k & 1].y);
+  lr += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
+  return true;
+}
+
+// Values that are not finite were left out of tiles that not every row attends: to a row that attends positions from .. to - 1, in its
+// share or its result (whatever else is in the sum, it is not finite).
+__device__ __noinline__ void odd_values(const RowsAttnArgs &a, const paged::FastDiv &page, int seg, int kvh, int from, int to, float *share,
+                                        bf16 *o) {
+  const bf16 *vb = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) + kvh * a.c.v_head : reinterpret_cast<const bf16 *>(a.c.k) + kvh * a.c.k_head;
+  const int64_t st_page = a.c.v ? a.c.v_page : a.c.k_page, st_row = a.c.v ? a.c.v_row : a.c.k_row;
+  for (int p = from; p < to; ++p) {
+    const int pg = (int)page.div((uint32_t)p), id = a.table[(int64_t)seg * a.width + pg];
+    if (id < 0 || id >= a.c.n_pages) continue;
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(vb + id * st_page + (int64_t)(p - pg * a.c.page) * st_row);
+    for (int c = 0; c < a.c.head_dim / 2; ++c) {
+      const uint32_t z = src[c];
+      if (!not_finite(z)) continue;
+      const float x[2] = {low(z), high(z)};
+      for (int k = 0; k < 2; ++k) {
+        if (isfinite(x[k])) continue;
+        if (share) share[2 * c + k] += x[k];
+        else if (isfinite(__bfloat162float(o[2 * c + k]))) o[2 * c + k] = __float2bfloat16(x[k]);
+        else o[2 * c + k] = __float2bfloat16(__bfloat162float(o[2 * c + k]) + x[k]);
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------------------ attention
@@ -346,16 +532,17 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
   uint64_t *full = bars, *empty = bars + NST, *s_full = bars + 2 * NST, *p_full = s_full + 2, *pv_done = s_full + 4,
            *q_full = s_full + 6, *p_half = s_full + 8, *drain = s_full + 10;
   uint32_t *masks = reinterpret_cast<uint32_t *>(bars + 32);  // [kNote][4]: positions of a tile that are there
-  int *odd_item = reinterpret_cast<int *>(masks + 4 * kNote);  // [kNote]: items with a value that is not finite where not all attend
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(odd_item + kNote);
+  volatile int *odd_item = reinterpret_cast<volatile int *>(masks + 4 * kNote);  // [kNote]: items with a value that is not finite where not all attend
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(masks + 5 * kNote);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  Range &rg = *reinterpret_cast<Range *>(tmem_slot + 2);
+  int *issue_lock = reinterpret_cast<int *>(tmem_slot + 2);
+  Range &rg = *reinterpret_cast<Range *>(tmem_slot + 4);
   static_assert(2 * NST + 11 <= 32 && NST / 2 + 2 < kNote, "barriers, notes");
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       tc::mbar_init(&full[i], 32);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], QT);   // both tiles of rows
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&s_full[b], 2);   // the products' completion, and the issuing thread (which has seen the stage's notes)
@@ -364,9 +551,10 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       tc::mbar_init(&pv_done[b], 2);
       tc::mbar_init(&q_full[b], 128);
     }
-    tc::mbar_init(drain, 1);
+    tc::mbar_init(drain, S::kMma);
     for (int i = 0; i < kNote; ++i) odd_item[i] = -1;
     *abort_flag = 0;
+    *issue_lock = 0;
     tc::fence_barrier_init();
   }
   dependency_wait();
@@ -385,16 +573,20 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     rg.p0 = p0;
     rg.p1 = part_begin(total, parts, cta + 1);
     rg.items = items;
+    rg.kvh = (int)(p0 / places);
   }
   if (warp == kSoft) tc::tmem_alloc(tmem_slot, 512);  // (behind the wait: a block of the kernel before may still ask for tensor memory)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk w{&P, &rg};
-  w.i = rg.first;
-  w.kvh = (int)(p0 / places);
-  bool more = w.load<KVT>();
+  auto begin = [&](auto &w) {
+    w.P = &P;
+    w.rg = &rg;
+    w.slot = reinterpret_cast<Slot *>(smem + S::kSlots) + 2 * warp;  // (of the warps that have slots)
+    w.i = rg.first;
+    w.kvh = rg.kvh;
+  };
 
   if (warp < kSoft) {
     // ------------------------------------------------------------------------------ softmax and results: a lane a row
@@ -416,10 +608,17 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         }
       }
     };
-    auto has_rows = [&](const Walk &x) {  // whether tile t has anything to do in this CTA's part of the item
+    Walk<KVT, true> w;
+    begin(w);
+    bool more = w.first(lane == 0);
+    auto has_rows = [&](const Walk<KVT, true> &x) {  // whether tile t has anything to do in this CTA's part of the item
       int from, to;
-      sub_range<KVT>(P, x, t, from, to);
+      sub_range(x, t, from, to);
       return to > from;
+    };
+    auto slot_there = [&]() {  // what lane 0 has copied, for the warp
+      attn::cp_async_wait_all();
+      __syncwarp();
     };
     if (more && has_rows(w)) {
       load_q(w.d, w.kvh);
@@ -438,142 +637,59 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     bool ok = true;
     int4 split = make_int4(0, 0, 0, 0);
     while (more) {
-      const Item d = w.d;
-      int x, y;
-      sub_range<KVT>(P, w, t, x, y);
-      const int R = t * kSub + r;
-      const bool mine = R < d.rows;
-      int tok = 0, h = 0, lo = 0, hi = 0x7fffffff;  // (a row that is not there attends all: no mask for its sake)
-      if (mine) {
-        const int q = (int)P.g.div(d.row0 + R);
-        tok = d.tok0 + q;
-        h = w.kvh * g + (d.row0 + R - q * g);
+      int x, y, lo = 0, hi = 0x7fffffff;  // (a row that is not there attends all: no mask for its sake)
+      sub_range(w, t, x, y);
+      const bool work = t * kSub + quad * 32 < w.d.rows;  // (of the warp)
+      if (t * kSub + r < w.d.rows) {
+        const int tok = w.d.tok0 + (int)P.g.div(w.d.row0 + t * kSub + r);
         if (!a.pos) {
-          hi = tok + d.shift;
+          hi = tok + w.d.shift;
           if (a.window > 0) lo = max(0, hi - a.window + 1);
         } else if (a.window > 0) {
-          const int64_t first = (int64_t)d.shift + a.pos[tok] + 1 - a.window;
+          const int64_t first = (int64_t)w.d.shift + a.pos[tok] + 1 - a.window;
           lo = (int)max((int64_t)0, min(first, (int64_t)0x7fffffff));
         }
       }
-      const bool work = t * kSub + quad * 32 < d.rows;  // (of the warp)
       float m = -INFINITY, l = 0.f, lr = 0.f;
-      const int j0 = w.kt0 + w.u0, item_tiles = w.u1 - w.u0;
-      auto next_q = [&]() -> bool {  // the next item's q on its way (its last reader is done); w stays, not to hold two items in registers
-        Walk nx = w;
-        if (!nx.next<KVT>() || !has_rows(nx)) return false;
-        load_q(nx.d, nx.kvh);
-        return true;
-      };
-      if (y == x && next_q()) {
-        attn::cp_async_wait_all();
-        attn::fence_proxy_async();
-        tc::mbar_arrive(&q_full[t]);
-      }
+      const int note0 = tile0 - (w.kt0 + w.u0);
+      tile0 += w.u1 - w.u0;
       for (int j = x; j < y; ++j) {
-        const int b = QT == 2 ? t : n_s & 1;
+        const int b = QT == 2 ? t : n_s & 1, at = j * KVT;
+        const bool in_part = odd_scale || !__all_sync(0xffffffffu, lo <= at && hi - at >= KVT - 1);  // some row attends not all of the tile
+        if (at < w.d.at0 || at + KVT > w.d.at1) {
+          // A weight of 0 does not undo a NaN: in a tile that not every row of the item attends, values that are not finite are
+          // taken out before the product (by both tiles of rows, whichever comes first), and the rows that attend them get them
+          // at the end.
+          const int stage = 2 * (note0 + j) + 1;
+          if (!(ok = warp_wait(&full[stage % NST], (uint32_t)((stage / NST) & 1), abort_flag))) break;
+#pragma unroll 4
+          for (int i = 0; i < S::kStage / 16 / kSub; ++i) {
+            const uint32_t v_at = s_ring + (stage % NST) * S::kStage + (i * kSub + r) * 16;
+            uint32_t z[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(v_at) : "memory");
+            if (__builtin_expect(not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3]), 0)) {
+              odd_item[w.seq & (kNote - 1)] = w.seq;  // (before they are gone: the other tile of rows may find them gone)
+              __threadfence_block();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+                if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v_at), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]) : "memory");
+            }
+          }
+          attn::fence_proxy_async();
+        }
         if (!(ok = warp_wait(&s_full[b], QT == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag))) break;
         tc::tc_fence_after();
-        const bool q_next = j + 1 == y && next_q();
         if (work) {
           const uint32_t tS = tmem + b * KVT + lane_off;
-          float2 s[KVT / 2];
-          float q4[4];  // maxima in four chains, so that one's latency passes in the others
-          {
-            uint32_t v[kW][32];
-#pragma unroll
-            for (int k = 0; k < kW; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < kW; ++k) {
-              tie32(v[k]);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) s[16 * k + e] = make_float2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1]));
-            }
-          }
-          float sc = P.scale_log2;
-          if (__builtin_expect(odd_scale, 0)) {  // (a negative one would make the largest score the smallest; 0 times a mask's -inf is not -inf)
-#pragma unroll
-            for (int k = 0; k < KVT / 2; ++k) s[k].x *= sc, s[k].y *= sc;
-            sc = 1.f;
-          }
-          {
-            const uint32_t *mk = masks + 4 * ((tile0 + j - j0) & (kNote - 1));
-            const int at = j * KVT, from = lo - at, to = hi - at;  // positions of the tile that the row attends
-            uint32_t there[kW], all = 0xffffffffu;
-#pragma unroll
-            for (int k = 0; k < kW; ++k) all &= there[k] = mk[k];
-            if (__builtin_expect(!__all_sync(0xffffffffu, all == 0xffffffffu && from <= 0 && to >= KVT - 1), 0)) {
-#pragma unroll
-              for (int k = 0; k < kW; ++k) {
-                const int f = min(max(from - 32 * k, 0), 32), e = min(max(to - 32 * k, -1), 31) + 1;
-                uint32_t mask = e == 32 ? 0xffffffffu : (1u << e) - 1u;
-                mask &= f == 32 ? 0u : 0xffffffffu << f;
-                mask &= there[k];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  s[16 * k + c].x = (mask >> (2 * c)) & 1u ? s[16 * k + c].x : -INFINITY;
-                  s[16 * k + c].y = (mask >> (2 * c + 1)) & 1u ? s[16 * k + c].y : -INFINITY;
-                }
-              }
-            }
-          }
-          float mx;
-          {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) q4[k] = fmaxf(s[k].x, s[k].y);
-#pragma unroll
-            for (int k = 4; k < KVT / 2; ++k) q4[k & 3] = max3(q4[k & 3], s[k].x, s[k].y);
-            mx = fmaxf(max3(q4[0], q4[1], q4[2]), q4[3]);
-          }
-          if (j == x) {
-            m = mx;
-          } else {
-            const bool raise = (mx - m) * sc > kRaise || (m == -INFINITY && mx > m);
-            const float al = raise ? (m == -INFINITY ? 0.f : paged::ex2((m - mx) * sc)) : 1.f;
-            if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-              if (!(ok = values_done())) break;
-              tc::tc_fence_after();
-              if (raise) m = mx;
-              l *= al;
-              lr *= al;
-#pragma unroll 1
-              for (int c = 0; c < hd16; c += 16) {
-                uint32_t v[16];
-                tc::tmem_ld16_wait(tO + c, v);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
-                attn::tmem_st16(tO + c, v);
-              }
-            }
-          }
-          const float ref = m == -INFINITY ? 0.f : m * sc;
-          const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
-          uint32_t pk[KVT / 2];
-          float2 l4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int k = 0; k < KVT / 32; ++k) {
-            uint32_t v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 z = __ffma2_rn(s[16 * k + e], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
-              l4[e & 1] = __fadd2_rn(l4[e & 1], p);
-              v[e] = pk[16 * k + e] = pack2(p.x, p.y);
-            }
-            attn::tmem_st16(tS + 16 * k, v);
-            if (k == KVT / 64 - 1 || k == KVT / 32 - 1) {  // (the product of the first half begins beside the second half's exponentials)
-              attn::tmem_st_wait();
-              tc::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(k == KVT / 64 - 1 ? &p_half[b] : &p_full[b]);
-            }
-          }
-          // (behind what the product waits for)
-          l += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
-          l4[0] = l4[1] = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < KVT / 2; ++k) add_halves(pk[k], l4[k & 1].x, l4[k & 1].y);
-          lr += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
+          const uint4 there = *reinterpret_cast<const uint4 *>(masks + 4 * ((note0 + j) & (kNote - 1)));  // positions that are there
+          if (in_part || (kW == 4 ? (there.x & there.y & there.z & there.w) : (there.x & there.y)) != 0xffffffffu)
+            ok = weights<HDP, true>(P.scale_log2, lo - at, hi - at, there, m, l, lr, j == x, tS, tO, hd16, &p_half[b], &p_full[b], lane, values_done);
+          else
+            ok = weights<HDP, false>(P.scale_log2, 0, 0, there, m, l, lr, j == x, tS, tO, hd16, &p_half[b], &p_full[b], lane, values_done);
+          if (!ok) break;
         } else {
           tc::tc_fence_before();
           __syncwarp();
@@ -584,24 +700,33 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         }
         ++n_s;
         ++n_pv;
-        if (q_next) {
-          attn::cp_async_wait_all();
-          attn::fence_proxy_async();
-          tc::mbar_arrive(&q_full[t]);
-        }
       }
       if (!ok) break;
-      // ---- the end of the item in this CTA
+      // ---- the end of the item in this CTA; the next one's q comes beside the last values (its last reader is done; w stays, not to
+      // hold two items in registers)
+      bool q_next = false;
+      {
+        slot_there();
+        Walk<KVT, true> nx = w;
+        if (nx.peek() && has_rows(nx)) {
+          load_q(nx.d, nx.kvh);
+          q_next = true;
+        }
+      }
       if (y > x) {
         if (!(ok = values_done())) break;
         tc::tc_fence_after();
       }
+      if (q_next) {
+        attn::cp_async_wait_all();
+        attn::fence_proxy_async();
+        tc::mbar_arrive(&q_full[t]);
+      }
       if (work) {
-        const bool whole = w.whole(), live = mine && row_live(a, tok);
-        if (odd_scale || m == -INFINITY) {
-        } else {
-          m *= P.scale_log2;
-        }
+        const Item &d = w.d;
+        const int R = t * kSub + r, q = (int)P.g.div(d.row0 + R), tok = d.tok0 + q, h = w.kvh * g + (d.row0 + R - q * g);
+        const bool whole = w.whole(), mine = R < d.rows, live = mine && row_live(a, tok);
+        if (!odd_scale && m != -INFINITY) m *= P.scale_log2;
         const bool odd = y > x && odd_item[w.seq & (kNote - 1)] == w.seq;
         float f = 1.f, f_own = 0.f;
         float *share = nullptr;
@@ -624,66 +749,54 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           if (mine) P.share_ml[at] = make_float4(m, lr, l, 0.f);
         }
 #pragma unroll 1
-        for (int c = 0; c < hd; c += 16) {
-          uint32_t u[16];
+        for (int c = 0; c < hd; c += 32) {
+          float v[32];
           __syncwarp();
           if (y > x) {
-            tc::tmem_ld16_wait(tO + c, u);
+            attn::tmem_ld_32cols(tO + c, v);
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = 0u;
-          }
-          float v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]);
-          if (odd && mine) {
-            // values that are not finite were left out of tiles that not every row attends: to the rows that do
-            const bf16 *vb = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) + w.kvh * a.c.v_head
-                                   : reinterpret_cast<const bf16 *>(a.c.k) + w.kvh * a.c.k_head;
-            const int64_t st_page = a.c.v ? a.c.v_page : a.c.k_page, st_row = a.c.v ? a.c.v_row : a.c.k_row;
-            const int64_t p_end = min(min((int64_t)hi + 1, (int64_t)d.end), (int64_t)y * KVT);
-            // (without a window those are the tiles behind the first token's position)
-            const int64_t part = a.window > 0 ? 0 : ((int64_t)d.tok0 + P.g.div(d.row0) + d.shift + 1) / KVT * KVT;
-            for (int64_t p = max(max((int64_t)lo, (int64_t)d.begin), max(part, (int64_t)x * KVT)); p < p_end; ++p) {
-              const int pg = (int)P.page.div((uint32_t)p), id = a.table[(int64_t)d.seg * a.width + pg];
-              if (id < 0 || id >= a.c.n_pages) continue;
-              const uint4 *src = reinterpret_cast<const uint4 *>(vb + id * st_page + (int64_t)((int)p - pg * a.c.page) * st_row + c);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (c + 8 * e >= hd) break;
-                const uint4 z = src[e];
-                const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((zz[k] & 0x7f80u) == 0x7f80u) v[8 * e + 2 * k] += low(zz[k]);
-                  if ((zz[k] & 0x7f800000u) == 0x7f800000u) v[8 * e + 2 * k + 1] += high(zz[k]);
-                }
-              }
-            }
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
           }
           if (share) {
-            if (mine)
+            if (mine) {
 #pragma unroll
-              for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4 *>(share + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-          } else if (live) {
+              for (int e = 0; e < 4; ++e) {
+                uint32_t u[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] *= f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (c + 8 * e >= hd) break;
-              if (own) {
-                const float4 y0 = *reinterpret_cast<const float4 *>(own + c + 8 * e), y1 = *reinterpret_cast<const float4 *>(own + c + 8 * e + 4);
-                const float yy[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[8 * e + k] = fmaf(yy[k], f_own, v[8 * e + k]);
+                for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(v[8 * e + k]);
+                store32(share + c + 8 * e, u);
               }
-              *reinterpret_cast<uint4 *>(o + c + 8 * e) =
-                  make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]), pack2(v[8 * e + 4], v[8 * e + 5]),
-                             pack2(v[8 * e + 6], v[8 * e + 7]));
+            }
+          } else if (live) {
+            uint32_t u[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float yy[8] = {};
+              if (own && c + 8 * e < hd) {
+                const float4 y0 = *reinterpret_cast<const float4 *>(own + c + 8 * e), y1 = *reinterpret_cast<const float4 *>(own + c + 8 * e + 4);
+                yy[0] = y0.x, yy[1] = y0.y, yy[2] = y0.z, yy[3] = y0.w, yy[4] = y1.x, yy[5] = y1.y, yy[6] = y1.z, yy[7] = y1.w;
+              }
+#pragma unroll
+              for (int k = 0; k < 8; k += 2)
+                u[4 * e + k / 2] = pack2(fmaf(yy[k], f_own, v[8 * e + k] * f), fmaf(yy[k + 1], f_own, v[8 * e + k + 1] * f));
+            }
+            if (P.wide) {  // (rows of whole 32 bytes, on their borders)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (c + 16 * e < hd) store32(o + c + 16 * e, u + 8 * e);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (c + 8 * e < hd) *reinterpret_cast<uint4 *>(o + c + 8 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
             }
           }
         }
         tc::tc_fence_before();
+        if (__builtin_expect(odd && mine && (share || live), 0)) {
+          const int from = max(max(lo, d.begin), a.window > 0 ? 0 : d.at1 / KVT * KVT);  // (tiles that all attend have theirs already)
+          odd_values(a, P.page, d.seg, w.kvh, max(from, x * KVT), (int)min(min((int64_t)hi + 1, (int64_t)d.end), (int64_t)y * KVT), share, o);
+        }
       }
       if (tid == 0 && w.u0 == 0 && w.u1 < w.tiles) {  // (the CTA's last item: it goes on in the next ones)
         const unsigned long long last_place = w.base + w.tiles - 1;
@@ -691,14 +804,14 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         while (c + 1 < parts && part_begin(total, parts, c + 1) <= last_place) ++c;
         split = make_int4(w.i, w.kvh, c - cta + 1, 0);
       }
-      tile0 += item_tiles;
-      more = w.next<KVT>();
+      slot_there();
+      more = w.next(lane == 0);
     }
     attn::cp_async_wait_all();
     if (tid == 0) P.split[cta] = split;
   } else {
     if constexpr (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsRest));
-    if (warp == kSoft) {
+    if (warp < kSoft + S::kMma) {
     // ------------------------------------------------------------------------------ products, issued by one elected lane
     if (tc::elect_one()) {
       const uint32_t id_s = tc::idesc_bf16_f32(kSub, KVT), id_v = tc::idesc_bf16_f32(kSub, hd16, false, /*b_mn_major=*/true);
@@ -707,87 +820,99 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       const uint64_t hi = tc::sdesc_sw128(0, 16, 1024) & 0xffffffff00000000ull;
       const int ks = hd16 / 16;
       int s = 0;  // stages so far
-      auto stage_ready = [&](int i) { return tc::mbar_wait(&full[i % NST], (uint32_t)((i / NST) & 1), abort_flag); };
-      uint32_t n_q[2] = {}, n_s = 0, n_p[2] = {};
-      auto scores = [&](int t, int b, int stage) {
-        const uint32_t A = dq + t * (S::kQBytes >> 4), B = dk + (stage % NST) * (S::kStage >> 4);
+      auto stage_ready = [&](int i) { return wait(&full[i % NST], (uint32_t)((i / NST) & 1), abort_flag); };
+      // A warp has one tile of rows of each item, and lets the stages that the tile attends nothing of pass by.
+      const int t = warp - kSoft;
+      Walk<KVT, true> w;
+      begin(w);
+      bool more = w.first(true);
+      uint32_t n_q = 0, n_s = 0, n_p = 0;
+      const uint32_t dO = tmem + S::kColO + t * HDP;
+      auto buffer = [&](uint32_t n) { return QT == 2 ? (uint32_t)t : n & 1; };
+      auto phase = [&](uint32_t n) { return QT == 2 ? n & 1 : (n >> 1) & 1; };
+      auto scores = [&](int stage) {
+        const uint32_t A = dq + t * (S::kQBytes >> 4), B = dk + (stage % NST) * (S::kStage >> 4), b = buffer(n_s++);
+        const uint32_t d = tmem + b * KVT;
+        uint32_t al = A, bl = B;
+        int k = 0;
+#pragma unroll 1
+        for (; k + 4 <= ks; k += 4, al += kSub * 128 >> 4, bl += KVT * 128 >> 4)
 #pragma unroll
-        for (int k = 0; k < HDP / 16; ++k)
-          if (k < 4 * (NP - 1) + 1 || k < ks) tc::mma_bf16(tmem + b * KVT, hi | (A + (k >> 2) * (kSub * 128 >> 4) + (k & 3) * 2),
-                       hi | (B + (k >> 2) * (KVT * 128 >> 4) + (k & 3) * 2), id_s, k ? 1u : 0u);
+          for (int e = 0; e < 4; ++e) tc::mma_bf16(d, hi | (al + 2 * e), hi | (bl + 2 * e), id_s, e ? 1u : (k ? 1u : 0u));
+#pragma unroll 1
+        for (; k < ks; ++k, al += 2, bl += 2) tc::mma_bf16(d, hi | al, hi | bl, id_s, k ? 1u : 0u);
         tc::mma_commit(&s_full[b]);
         tc::mbar_arrive(&s_full[b]);
       };
-      auto values = [&](int t, int b, int stage, bool first, uint32_t parity) -> bool {  // (the weights' first half is there)
+      auto values = [&](int stage, int half, bool first) {  // (the half's weights are there)
         tc::tc_fence_after();
-        const uint32_t B = dv + (stage % NST) * (S::kStage >> 4), dO = tmem + S::kColO + t * HDP, A = tmem + b * KVT;
-#pragma unroll
-        for (int k = 0; k < KVT / 32; ++k) mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
-        if (!tc::mbar_wait(&p_full[b], parity, abort_flag)) return false;
-        tc::tc_fence_after();
-#pragma unroll
-        for (int k = KVT / 32; k < KVT / 16; ++k) mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, 1u);
-        tc::mma_commit(&pv_done[b]);
-        tc::mbar_arrive(&pv_done[b]);
+        const uint32_t A = tmem + buffer(n_p) * KVT, B = dv + (stage % NST) * (S::kStage >> 4);
+#pragma unroll 2
+        for (int k = 0; k < KVT / 32; ++k) {
+          const int kk = half * (KVT / 32) + k;
+          mma_ts(dO, A + 8 * kk, hi | (B + kk * 128), id_v, first && kk == 0 ? 0u : 1u);
+        }
+      };
+      // The two warps' products come in groups, each as a whole behind the other's: one tile's scores are then there while the other's
+      // are computed (product by product in turn, both would be late, and both softmaxes run at once).
+      auto lock = [&]() -> bool {
+        uint32_t spins = 0;
+        uint64_t t0 = 0;
+        while (QT == 2 && atomicCAS(issue_lock, 0, 1) != 0)
+          if ((++spins & 255) == 0) {
+            if (t0 == 0) t0 = tc::global_ns();
+            if (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs) return false;
+          }
         return true;
       };
+      auto unlock = [&]() {
+        if (QT == 2) atomicExch(issue_lock, 0);
+      };
       bool ok = true;
-      while (more && ok) {
+      while (more) {
         const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1;
-        int x[QT], y[QT];
-#pragma unroll
-        for (int t = 0; t < QT; ++t) sub_range<KVT>(P, w, t, x[t], y[t]);
-        if (!(ok = stage_ready(s))) break;
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-          if (x[t] == j0 && y[t] > j0) {
-            if (!(ok = ok && tc::mbar_wait(&q_full[t], n_q[t]++ & 1, abort_flag))) break;
-            scores(t, QT == 2 ? t : n_s & 1, s);
-            ++n_s;
-          }
+        int x, y;
+        sub_range(w, t, x, y);
+        auto keys_there = [&](int j, int stage) { return stage_ready(stage) && (j != x || x == y || wait(&q_full[t], n_q++ & 1, abort_flag)); };
+        auto keys = [&](int j, int stage) {  // tile j's scores
+          if (x <= j && j < y) scores(stage);
+          tc::mma_commit(&empty[stage % NST]);
+        };
+        ok = keys_there(j0, s) && lock();
         if (!ok) break;
-        tc::mma_commit(&empty[s % NST]);
+        keys(j0, s);
+        unlock();
         for (int j = j0; j < j1; ++j, s += 2) {
-          const int sv = s + 1, sk = s + 2;
-          const bool next = j + 1 < j1;
-          bool v_in = false, k_in = false;
-          if (QT == 1 && next) {  // (the other score buffer: the next tile's scores before this one's values)
-            if (!(ok = stage_ready(sk))) break;
-            k_in = true;
-            if (x[0] <= j + 1 && j + 1 < y[0]) {
-              if (x[0] == j + 1 && !(ok = tc::mbar_wait(&q_full[0], n_q[0]++ & 1, abort_flag))) break;
-              scores(0, n_s & 1, sk);
-              ++n_s;
-            }
-            tc::mma_commit(&empty[sk % NST]);
+          const bool live = x <= j && j < y, next = j + 1 < j1;
+          if (QT == 1 && next) {  // (the other score buffer: before this tile's values)
+            if (!(ok = keys_there(j + 1, s + 2))) break;
+            keys(j + 1, s + 2);
           }
-#pragma unroll
-          for (int t = 0; t < QT; ++t) {
-            if (x[t] <= j && j < y[t]) {
-              const int b = QT == 2 ? t : n_p[0] & 1;
-              const uint32_t parity = QT == 2 ? n_p[t] & 1 : (n_p[0] >> 1) & 1;
-              if (!(ok = tc::mbar_wait(&p_half[b], parity, abort_flag))) break;
-              ++n_p[t];
-              if (!v_in && !(ok = stage_ready(sv))) break;
-              v_in = true;
-              if (!(ok = values(t, b, sv, j == x[t], parity))) break;
-            }
-            if (QT == 2 && next && x[t] <= j + 1 && j + 1 < y[t]) {
-              if (!k_in && !(ok = stage_ready(sk))) break;
-              k_in = true;
-              if (x[t] == j + 1 && !(ok = tc::mbar_wait(&q_full[t], n_q[t]++ & 1, abort_flag))) break;
-              scores(t, t, sk);
-            }
+          if (!(ok = stage_ready(s + 1))) break;
+          if (live) {
+            const uint32_t b = buffer(n_p), ph = phase(n_p);
+            if (!(ok = wait(&p_half[b], ph, abort_flag))) break;
+            values(s + 1, 0, j == x);
+            if (!(ok = wait(&p_full[b], ph, abort_flag))) break;
           }
-          if (!ok) break;
-          if (!v_in && !(ok = stage_ready(sv))) break;
-          tc::mma_commit(&empty[sv % NST]);
           if (QT == 2 && next) {
-            if (!k_in && !(ok = stage_ready(sk))) break;
-            tc::mma_commit(&empty[sk % NST]);
+            if (!(ok = keys_there(j + 1, s + 2))) break;
           }
+          ok = lock();
+          if (!ok) break;
+          if (live) {
+            values(s + 1, 1, false);
+            const uint32_t b = buffer(n_p++);
+            tc::mma_commit(&pv_done[b]);
+            tc::mbar_arrive(&pv_done[b]);
+          }
+          tc::mma_commit(&empty[(s + 1) % NST]);
+          if (QT == 2 && next) keys(j + 1, s + 2);
+          unlock();
         }
-        more = w.next<KVT>();
+        if (!ok) break;
+        attn::cp_async_wait_all();
+        more = w.next(true);
       }
       // nothing may still read shared memory, write tensor memory or arrive when the CTA ends
       tc::mma_commit(drain);
@@ -797,21 +922,24 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------------------------ copies: every third stage a warp
+    // ------------------------------------------------------------------------------ copies: a warp every second or third stage
     // The pages of a warp's next stage are looked up while its copies are in flight.
-    const int lw = warp - kSoft - 1, cc = lane & 7;
+    const int lw = warp - kSoft - S::kMma, cc = lane & 7;
+    Walk<KVT, false> w;
+    begin(w);
+    bool more = w.first(false);
     struct Look {
       int page[kW];
       uint32_t at;     // first position
-      int kvh, seg, begin, end, seq, tile;
-      bool values, part;  // part: positions that not every row attends
+      int kvh, seg, begin, end, tile;
+      bool values;
     };
     int s = lw, x = lw, tile0 = 0;  // stage, stage of the item, first tile of the item
     auto look = [&](Look &f) __attribute__((always_inline)) -> bool {
       while (more && x >= 2 * (w.u1 - w.u0)) {
         x -= 2 * (w.u1 - w.u0);
         tile0 += w.u1 - w.u0;
-        more = w.next<KVT>();
+        more = w.next(false);
       }
       if (!more) return false;
       const Item &d = w.d;
@@ -820,15 +948,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       f.kvh = w.kvh;
       f.begin = d.begin;
       f.end = d.end;
-      f.seq = w.seq;
       f.seg = d.seg;
       f.tile = tile0 + (x >> 1);
-      if (a.pos) {
-        f.part = a.window > 0;
-      } else {
-        const int ta = d.tok0 + (int)P.g.div(d.row0), tb = d.tok0 + (int)P.g.div(d.row0 + d.rows - 1);
-        f.part = (int64_t)f.at + KVT - 1 > (int64_t)ta + d.shift || (a.window > 0 && (int64_t)f.at < (int64_t)tb + d.shift - a.window + 1);
-      }
 #pragma unroll
       for (int k = 0; k < kW; ++k) {
         const uint32_t p = f.at + 32 * k + lane;
@@ -837,13 +958,16 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       }
       return true;
     };
-    Look f;
-    bool have = look(f);
+    Look f{};
     if (G.box_rows && lane == 0) {
       tc::prefetch_tmap(&G.k);
       tc::prefetch_tmap(&G.v);
     }
-    while (have) {
+    for (bool begun = false, have = true; have; begun = true) {  // (from the second round on with a stage to fill)
+      const uint32_t dst = s_ring + (s % NST) * S::kStage + (lane >> 3) * 128;
+      const int cur = s;
+      bool copied = false;  // by cp.async
+      if (begun) {
       const bool vals = f.values && a.c.v;
       const bf16 *src = reinterpret_cast<const bf16 *>(vals ? a.c.v : a.c.k) + f.kvh * (vals ? a.c.v_head : a.c.k_head) + cc * 8;
       const int64_t st_page = vals ? a.c.v_page : a.c.k_page, st_row = vals ? a.c.v_row : a.c.k_row;
@@ -860,8 +984,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       if (!f.values && lane == 0)
 #pragma unroll
         for (int k = 0; k < kW; ++k) masks[4 * (f.tile & (kNote - 1)) + k] = there[k];
-      if (G.box_rows && all == 0xffffffffu && !(f.values && f.part)) {
-        // A whole tile, which every row attends: by TMA, a lane a box.
+      if (G.box_rows && all == 0xffffffffu) {
+        // A whole tile: by TMA, a lane a box.
         const int R = G.box_rows, first = lane * R;
         int page = 0;
 #pragma unroll
@@ -880,12 +1004,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
                             page);
         }
         if (lane != 0) tc::mbar_arrive(&full[buf]);
-        s += S::kLoad;
-        x += S::kLoad;
-        have = look(f);
-        continue;
-      }
-      const uint32_t dst = s_ring + buf * S::kStage + (lane >> 3) * 128;
+      } else {
+      copied = true;
 #pragma unroll 1
       for (int k = 0; k < kW; ++k) {  // (rolled: four times the code would be fetched anew for every stage)
         int page = f.page[0];
@@ -895,7 +1015,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           if (k == e) page = f.page[e], good = there[e];
         const uint32_t p = f.at + 32 * k + lane;
         const int64_t off = (good >> lane) & 1u ? page * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes 128 bytes of a row
           const int r7 = (4 * i + (lane >> 3)) & 7;
           const int64_t o = __shfl_sync(0xffffffffu, off, 4 * i + (lane >> 3));
@@ -906,37 +1026,13 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           }
         }
       }
-      const bool check = f.values && f.part;
-      const int seq = f.seq, cur = s;
+      }
       s += S::kLoad;
       x += S::kLoad;
-      have = look(f);
-      attn::cp_async_wait_all();
-      if (check) {
-        // A weight of 0 does not undo a NaN: values that are not finite are left out of the product here, and the rows that
-        // attend them get them at the end.  (A lane looks at what it has copied itself.)
-        bool odd = false;
-#pragma unroll 1
-        for (int i = 0; i < KVT / 4; ++i) {
-          const int r7 = (4 * i + (lane >> 3)) & 7;
-#pragma unroll
-          for (int kb = 0; kb < NP; ++kb) {
-            const uint32_t at = dst + kb * (KVT * 128) + i * 512 + ((cc ^ r7) << 4);
-            uint32_t z[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(at) : "memory");
-            if (not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3])) {
-              odd = true;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
-                if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
-              }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]) : "memory");
-            }
-          }
-        }
-        if (odd) odd_item[seq & (kNote - 1)] = seq;
       }
+      have = look(f);
+      if (!copied) continue;
+      attn::cp_async_wait_all();
       attn::fence_proxy_async();
       tc::mbar_arrive(&full[cur % NST]);
     }
@@ -1105,6 +1201,7 @@ cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, 
   p.page = paged::FastDiv((uint32_t)a.c.page);
   p.g = paged::FastDiv((uint32_t)(a.H / a.c.kv_heads));
   p.scale_log2 = (float)(a.scale * 1.4426950408889634);
+  p.wide = ((uintptr_t)a.o | (uintptr_t)(a.o_t * 2) | (uintptr_t)(a.c.head_dim * 2)) % 32 == 0;
   rows::Room room{reinterpret_cast<uint8_t *>(ws), reinterpret_cast<uint8_t *>(ws) + ws_bytes};
   if (a.pos) {  // the rows' own pages
     PagedAttnArgs o{};
