@@ -656,10 +656,12 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       for (int j = x; j < y; ++j) {
         const int b = QT == 2 ? t : n_s & 1, at = j * KVT;
         const bool in_part = odd_scale || !__all_sync(0xffffffffu, lo <= at && hi - at >= KVT - 1);  // some row attends not all of the tile
+        if (!(ok = warp_wait(&s_full[b], QT == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag))) break;
+        tc::tc_fence_after();
         if (at < w.d.at0 || at + KVT > w.d.at1) {
           // A weight of 0 does not undo a NaN: in a tile that not every row of the item attends, values that are not finite are
           // taken out before the product (by both tiles of rows, whichever comes first), and the rows that attend them get them
-          // at the end.
+          // at the end.  (Behind the scores: only then is the stage's barrier in the phase that is asked for, or the next.)
           const int stage = 2 * (note0 + j) + 1;
           if (!(ok = warp_wait(&full[stage % NST], (uint32_t)((stage / NST) & 1), abort_flag))) break;
 #pragma unroll 4
@@ -680,8 +682,6 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           }
           attn::fence_proxy_async();
         }
-        if (!(ok = warp_wait(&s_full[b], QT == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag))) break;
-        tc::tc_fence_after();
         if (work) {
           const uint32_t tS = tmem + b * KVT + lane_off;
           const uint4 there = *reinterpret_cast<const uint4 *>(masks + 4 * ((note0 + j) & (kNote - 1)));  // positions that are there

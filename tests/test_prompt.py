@@ -158,6 +158,32 @@ def test_prompt_uneven(csa, ctx, H, kv, hd, window, seed):
     assert ctx.status() == 0
 
 
+@pytest.mark.parametrize("H,kv,hd", [(8, 2, 128), (20, 4, 80), (16, 2, 256), (4, 4, 64), (6, 2, 192)])
+def test_prompt_cold(csa, ctx, H, kv, hd):
+    """Every call on another batch than the one before, with nothing of it in L2: what a stage still holds of an earlier one, or
+    shares of an earlier call, may not be taken for what is on its way."""
+    batches = []
+    for seed in range(4):
+        rng = np.random.default_rng(1000 * hd + seed)
+        lens = [int(rng.choice([1, 3, 16, 33, 97, 200])) for _ in range(int(rng.integers(8, 30)))]
+        for _ in range(3):
+            lens.insert(int(rng.integers(0, len(lens) + 1)), int(rng.integers(500, 3000)))
+        new = [int(rng.integers(1, min(x, 700) + 1)) for x in lens]
+        b = Batch(lens, H, kv, hd, int(rng.choice([5, 16, 64])), seed=seed)
+        q = b.queries(sum(new))
+        batches.append((b, new, q, (q, csa.PagedCache(b.k, b.v), b.table, i32(cus(new)), i32(lens), b.scale)))
+    flush = torch.empty(96 << 20, device="cuda")
+    for turn in range(3):
+        for b, new, q, args in batches:
+            flush.fill_(float("nan"))
+            o, lse = ctx.prompt_attn(*args, with_lse=True)
+            if turn == 0:
+                check_prompt(b, new, q, o, lse)
+                b.want = o, lse
+            assert torch.equal(o, b.want[0]) and torch.equal(lse, b.want[1])
+    assert ctx.status() == 0
+
+
 @pytest.mark.parametrize("H,kv,hd", [(8, 2, 128), (4, 1, 256)])
 def test_prompt_strided_rows_and_in_place(csa, ctx, H, kv, hd):
     """Rows of a wider buffer, whose other columns stay, and the result over q itself."""
