@@ -44,9 +44,11 @@ constexpr float kRaise = 8.f;
 struct Item {
   int tok0, row0, rows, seg, begin, end, shift, end0, begin1, at0, at1, spare;
 };
-struct Plan {
-  unsigned long long places;  // of one kv head
-  int items, spare;
+// A CTA's part of the places (a kv head's items one behind the other, head after head): first .. end - 1, of which the first is in item
+// `item` of head kvh; `items` of a head, `places` of a head.  No places: first == end.
+struct Part {
+  unsigned long long first, end, places;
+  int item, kvh, items, spare;
 };
 
 struct Params {
@@ -54,7 +56,8 @@ struct Params {
   paged::FastDiv page, g;
   float scale_log2;
   int wide;                    // o's rows are whole 32 bytes on such borders
-  Plan *plan;
+  Part *part;                  // [ctas + 1] (of the last one: first)
+  int ctas;
   Item *item;                  // [cap]
   unsigned long long *start;   // [cap + 1]: first place of an item
   int cap;
@@ -198,25 +201,32 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
   }
   if (tid == 0) {
     P.start[items] = places;
-    P.plan->places = places;
-    P.plan->items = items;
     if (full) atomicOr(a.status, kStatusBadIndex);  // (more items than rows can make: requests that overlap)
+  }
+  __syncthreads();
+  const unsigned long long total = places * a.c.kv_heads;
+  const int parts = (int)min((unsigned long long)P.ctas, max(1ull, total / kMinPlaces));
+  for (int c = tid; c <= P.ctas; c += kPlanThreads) {
+    const int n = min(c, parts);
+    Part q{total / parts * n + total % parts * n / parts, 0, places, 0, 0, items, 0};
+    q.end = c < parts ? total / parts * (n + 1) + total % parts * (n + 1) / parts : q.first;
+    if (q.first < q.end) {
+      q.kvh = (int)(q.first / places);
+      const unsigned long long in = q.first - places * q.kvh;
+      int lo = 0, hi = items - 1;  // the last item that begins at `in` or before
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (P.start[mid] <= in) lo = mid;
+        else hi = mid - 1;
+      }
+      q.item = lo;
+    }
+    P.part[c] = q;
   }
 }
 
 // ------------------------------------------------------------------------------------------------ a CTA's part
 
-// The places first .. last - 1 of CTA c of n.
-__device__ __forceinline__ unsigned long long part_begin(unsigned long long total, int n, int c) { return total / n * c + total % n * c / n; }
-// The CTAs that the places are dealt to.
-__device__ __forceinline__ int parts_of(unsigned long long total, int ctas) {
-  return (int)min((unsigned long long)ctas, max(1ull, total / kMinPlaces));
-}
-
-struct Range {
-  unsigned long long places, p0, p1;  // of a kv head; the CTA's first and the end
-  int items, first, kvh;              // of a kv head; the item and the head that the CTA begins with
-};
 // An item as the plan has it, and its first place.
 struct Slot {
   int4 a, b, c;
@@ -227,7 +237,7 @@ struct Slot {
 template <int KVT, bool SLOT>
 struct Walk {
   const Params *P;
-  const Range *rg;  // (in shared memory)
+  const Part *rg;  // (in shared memory)
   Slot *slot;
   unsigned long long base = 0;
   int i, kvh, seq = -1;  // seq: items so far
@@ -246,7 +256,7 @@ struct Walk {
   }
   // The item's place and parts from its description; false: it is behind the CTA's part.
   __device__ __forceinline__ bool set(int4 x, int4 y, int4 z, unsigned long long start) {
-    const unsigned long long p0 = rg->p0, p1 = rg->p1;
+    const unsigned long long p0 = rg->first, p1 = rg->end;
     base = rg->places * kvh + start;
     if (base >= p1) return false;
     d = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, 0};
@@ -376,106 +386,90 @@ __device__ __forceinline__ bool row_live(const RowsAttnArgs &a, int n) {
   return a.pos[n] >= -1 && req >= 0 && req < a.R;
 }
 
-// A row's weights of a tile from its scores, which the lane finds in its columns from tS on and where the weights go.  MASK: the row
-// attends positions from .. to where `there` has them, or the scale is not positive (in a copy of its own, so that the other's
-// code has no gaps).
-template <int HDP, bool MASK, class Done>
-__device__ __forceinline__ bool weights(float sc, int from, int to, uint4 there, float &m, float &l, float &lr, bool first, uint32_t tS,
-                                        uint32_t tO, int hd16, uint64_t *p_half, uint64_t *p_full, int lane, Done &&values_done) {
-  constexpr int KVT = Shape<HDP>::KVT, kW = KVT / 32;
-  const bool plain = !MASK || sc > 0.f;
-  const float2 sc2 = plain ? make_float2(sc, sc) : make_float2(1.f, 1.f);
-  float2 s[KVT / 2], l4[2];
-  uint32_t pk[KVT / 2];
-  float ref;
-  // The first quarter's exponentials by the maximum so far, the tile's maximum beside them (it costs nothing there); once more from the
-  // scores on in the rare case that it is larger by more than 2^8.
+// A row's scores of a tile, which the lane finds in its KVT columns from tS on, times `by` and -inf where the row attends nothing: it
+// attends positions from .. to of the tile as far as `there` has them.  (Rolled, and apart from the weights: few tiles need it.)
+template <int KVT>
+__device__ __forceinline__ void mask_scores(uint32_t tS, float by, int from, int to, const uint32_t *there) {
 #pragma unroll 1
-  for (;;) {
-    {
-      uint32_t v[kW][32];
+  for (int k = 0; k < KVT / 32; ++k, tS += 32, from -= 32, to -= 32) {
+    float v[32];
+    attn::tmem_ld_32cols(tS, v);
+    const int f = min(max(from, 0), 32), e = min(max(to, -1), 31) + 1;
+    const uint32_t mask = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & (f == 32 ? 0u : 0xffffffffu << f) & there[k];
+    uint32_t u[16];
 #pragma unroll
-      for (int k = 0; k < kW; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
-      tc::tmem_ld_wait();
-#pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        tie32(v[k]);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[16 * k + e] = make_float2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1]));
-      }
+    for (int c = 0; c < 32; ++c) {
+      u[c & 15] = __float_as_uint((mask >> c) & 1u ? v[c] * by : -INFINITY);
+      if ((c & 15) == 15) attn::tmem_st16(tS + (c & 16), u);
     }
-    if constexpr (MASK) {
-      if (!plain) {  // (a negative scale would make the largest score the smallest; 0 times a mask's -inf is not -inf)
+  }
+  attn::tmem_st_wait();
+}
+
+// The row's weights where its scores were: exponentials by the maximum, which is raised by more than 2^8 only, in two halves, so that
+// the first one's product begins beside the second's exponentials.  An exponential takes a warp 4 cycles at least, two with what goes
+// with them 12: 64 such pairs are most of a tile's time.
+template <int HDP, class Done>
+__device__ __forceinline__ bool weights(float sc, float &m, float &l, float &lr, bool first, uint32_t tS, uint32_t tO, int hd16,
+                                        uint64_t *p_half, uint64_t *p_full, int lane, Done &&values_done) {
+  constexpr int KVT = Shape<HDP>::KVT, kW = KVT / 32;
+  float2 s[KVT / 2], l4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  {
+    uint32_t v[kW][32];
 #pragma unroll
-        for (int k = 0; k < KVT / 2; ++k) s[k].x *= sc, s[k].y *= sc;
-      }
-      const uint32_t mk[4] = {there.x, there.y, there.z, there.w};
+    for (int k = 0; k < kW; ++k) tc::tmem_ld32(tS + 32 * k, v[k]);
+    tc::tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        const int f = min(max(from - 32 * k, 0), 32), e = min(max(to - 32 * k, -1), 31) + 1;
-        uint32_t mask = e == 32 ? 0xffffffffu : (1u << e) - 1u;
-        mask &= f == 32 ? 0u : 0xffffffffu << f;
-        mask &= mk[k];
+    for (int k = 0; k < kW; ++k) {
+      tie32(v[k]);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          s[16 * k + c].x = (mask >> (2 * c)) & 1u ? s[16 * k + c].x : -INFINITY;
-          s[16 * k + c].y = (mask >> (2 * c + 1)) & 1u ? s[16 * k + c].y : -INFINITY;
-        }
-      }
+      for (int e = 0; e < 16; ++e) s[16 * k + e] = make_float2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1]));
     }
-    ref = m == -INFINITY ? 0.f : m * sc2.x;
-    const float2 ref2 = make_float2(-ref, -ref);
-    l4[0] = l4[1] = make_float2(0.f, 0.f);
-    float q4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four chains, so that one's latency passes in the others)
+  }
+  float q4[4];  // (four chains, so that one's latency passes in the others)
 #pragma unroll
-    for (int k = 0; k < KVT / 8; ++k) {
+  for (int k = 0; k < 4; ++k) q4[k] = fmaxf(s[k].x, s[k].y);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q4[e] = max3(q4[e], s[e * (KVT / 8) + k].x, s[e * (KVT / 8) + k].y);
-      const float2 z = __ffma2_rn(s[k], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
-      l4[k & 1] = __fadd2_rn(l4[k & 1], p);
-      pk[k] = pack2(p.x, p.y);
-    }
-    const float mx = fmaxf(max3(q4[0], q4[1], q4[2]), q4[3]);
-    const bool raise = (mx - m) * sc2.x > kRaise || (m == -INFINITY && mx > m);
-    if (__builtin_expect(!__any_sync(0xffffffffu, raise), 1)) break;
-    const float al = raise ? (m == -INFINITY ? 0.f : paged::ex2((m - mx) * sc2.x)) : 1.f;
+  for (int k = 4; k < KVT / 2; ++k) q4[k & 3] = max3(q4[k & 3], s[k].x, s[k].y);
+  const float mx = fmaxf(max3(q4[0], q4[1], q4[2]), q4[3]);
+  const bool raise = first ? mx > m : (mx - m) * sc > kRaise || (m == -INFINITY && mx > m);
+  if (first) {
+    m = mx;
+  } else if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
+    const float al = raise ? (m == -INFINITY ? 0.f : paged::ex2((m - mx) * sc)) : 1.f;
     if (raise) m = mx;
     l *= al;
     lr *= al;
-    if (!first) {
-      if (!values_done()) return false;
-      tc::tc_fence_after();
+    if (!values_done()) return false;
+    tc::tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < hd16; c += 16) {
-        uint32_t v[16];
-        tc::tmem_ld16_wait(tO + c, v);
+    for (int c = 0; c < hd16; c += 16) {
+      uint32_t v[16];
+      tc::tmem_ld16_wait(tO + c, v);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
-        attn::tmem_st16(tO + c, v);
-      }
+      for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+      attn::tmem_st16(tO + c, v);
     }
   }
-  const float2 ref2 = make_float2(-ref, -ref);
+  const float ref = m == -INFINITY ? 0.f : m * sc;
+  const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+  uint32_t pk[KVT / 2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {  // (the product of the first half begins beside the second half's exponentials)
+  for (int k = 0; k < KVT / 32; ++k) {
+    uint32_t v[16];
 #pragma unroll
-    for (int k = half * (KVT / 64); k < (half + 1) * (KVT / 64); ++k) {
-      uint32_t v[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if (half || 16 * k + e >= KVT / 8) {
-          const float2 z = __ffma2_rn(s[16 * k + e], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
-          l4[e & 1] = __fadd2_rn(l4[e & 1], p);
-          pk[16 * k + e] = pack2(p.x, p.y);
-        }
-        v[e] = pk[16 * k + e];
-      }
-      attn::tmem_st16(tS + 16 * k, v);
+    for (int e = 0; e < 16; ++e) {
+      const float2 z = __ffma2_rn(s[16 * k + e], sc2, ref2), p = make_float2(paged::ex2(z.x), paged::ex2(z.y));
+      l4[e & 1] = __fadd2_rn(l4[e & 1], p);
+      v[e] = pk[16 * k + e] = pack2(p.x, p.y);
     }
-    attn::tmem_st_wait();
-    tc::tc_fence_before();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(half ? p_full : p_half);
+    attn::tmem_st16(tS + 16 * k, v);
+    if (k == KVT / 64 - 1 || k == KVT / 32 - 1) {
+      attn::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(k == KVT / 64 - 1 ? p_half : p_full);
+    }
   }
   // (behind what the product waits for)
   l += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
@@ -536,7 +530,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(masks + 5 * kNote);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *issue_lock = reinterpret_cast<int *>(tmem_slot + 2);
-  Range &rg = *reinterpret_cast<Range *>(tmem_slot + 4);
+  Part &rg = *reinterpret_cast<Part *>(tmem_slot + 4);
   static_assert(2 * NST + 11 <= 32 && NST / 2 + 2 < kNote, "barriers, notes");
 
   if (tid == 0) {
@@ -558,23 +552,12 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     tc::fence_barrier_init();
   }
   dependency_wait();
-  const unsigned long long places = P.plan->places, total = places * a.c.kv_heads;
-  const int items = P.plan->items;
-  const int parts = parts_of(total, gridDim.x), cta = blockIdx.x;
-  if (total == 0 || cta >= parts) {
+  const int cta = blockIdx.x;
+  if (P.part[cta].first == P.part[cta].end) {
     if (tid == 0) P.split[cta] = make_int4(0, 0, 0, 0);
     return;
   }
-  const unsigned long long p0 = part_begin(total, parts, cta), in_head = p0 % places;
-  for (int i = tid; i < items; i += S::kThreads)
-    if (P.start[i] <= in_head && in_head < P.start[i + 1]) rg.first = i;
-  if (tid == 0) {
-    rg.places = places;
-    rg.p0 = p0;
-    rg.p1 = part_begin(total, parts, cta + 1);
-    rg.items = items;
-    rg.kvh = (int)(p0 / places);
-  }
+  if (tid == 0) rg = P.part[cta];
   if (warp == kSoft) tc::tmem_alloc(tmem_slot, 512);  // (behind the wait: a block of the kernel before may still ask for tensor memory)
   tc::tc_fence_before();
   __syncthreads();
@@ -584,7 +567,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     w.P = &P;
     w.rg = &rg;
     w.slot = reinterpret_cast<Slot *>(smem + S::kSlots) + 2 * warp;  // (of the warps that have slots)
-    w.i = rg.first;
+    w.i = rg.item;
     w.kvh = rg.kvh;
   };
 
@@ -633,7 +616,9 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       const int n = n_pv - 1;
       return QT == 2 ? warp_wait(&pv_done[t], n & 1, abort_flag) : warp_wait(&pv_done[n & 1], (n >> 1) & 1, abort_flag);
     };
+    // (a negative scale would make the largest score the smallest, and 0 times a mask's -inf is not -inf: scores are then scaled first)
     const bool odd_scale = !(P.scale_log2 > 0.f);
+    const float sc = odd_scale ? 1.f : P.scale_log2;
     bool ok = true;
     int4 split = make_int4(0, 0, 0, 0);
     while (more) {
@@ -684,11 +669,11 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         }
         if (work) {
           const uint32_t tS = tmem + b * KVT + lane_off;
-          const uint4 there = *reinterpret_cast<const uint4 *>(masks + 4 * ((note0 + j) & (kNote - 1)));  // positions that are there
-          if (in_part || (kW == 4 ? (there.x & there.y & there.z & there.w) : (there.x & there.y)) != 0xffffffffu)
-            ok = weights<HDP, true>(P.scale_log2, lo - at, hi - at, there, m, l, lr, j == x, tS, tO, hd16, &p_half[b], &p_full[b], lane, values_done);
-          else
-            ok = weights<HDP, false>(P.scale_log2, 0, 0, there, m, l, lr, j == x, tS, tO, hd16, &p_half[b], &p_full[b], lane, values_done);
+          const uint32_t *there = masks + 4 * ((note0 + j) & (kNote - 1));  // positions that are there
+          const uint4 mk = *reinterpret_cast<const uint4 *>(there);
+          if (__builtin_expect(in_part || (kW == 4 ? (mk.x & mk.y & mk.z & mk.w) : (mk.x & mk.y)) != 0xffffffffu, 0))
+            mask_scores<KVT>(tS, odd_scale ? P.scale_log2 : 1.f, lo - at, hi - at, there);
+          ok = weights<HDP>(sc, m, l, lr, j == x, tS, tO, hd16, &p_half[b], &p_full[b], lane, values_done);
           if (!ok) break;
         } else {
           tc::tc_fence_before();
@@ -726,7 +711,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         const Item &d = w.d;
         const int R = t * kSub + r, q = (int)P.g.div(d.row0 + R), tok = d.tok0 + q, h = w.kvh * g + (d.row0 + R - q * g);
         const bool whole = w.whole(), mine = R < d.rows, live = mine && row_live(a, tok);
-        if (!odd_scale && m != -INFINITY) m *= P.scale_log2;
+        if (m != -INFINITY) m *= sc;
         const bool odd = y > x && odd_item[w.seq & (kNote - 1)] == w.seq;
         float f = 1.f, f_own = 0.f;
         float *share = nullptr;
@@ -749,46 +734,42 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           if (mine) P.share_ml[at] = make_float4(m, lr, l, 0.f);
         }
 #pragma unroll 1
-        for (int c = 0; c < hd; c += 32) {
-          float v[32];
+        for (int c = 0; c < hd; c += 16) {
+          uint32_t u[16];
           __syncwarp();
           if (y > x) {
-            attn::tmem_ld_32cols(tO + c, v);
+            tc::tmem_ld16_wait(tO + c, u);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            for (int k = 0; k < 16; ++k) u[k] = 0u;
           }
           if (share) {
             if (mine) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t u[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(v[8 * e + k]);
-                store32(share + c + 8 * e, u);
-              }
+              store32(share + c, u);
+              store32(share + c + 8, u + 8);
             }
           } else if (live) {
-            uint32_t u[16];
+            float v[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float yy[8] = {};
-              if (own && c + 8 * e < hd) {
-                const float4 y0 = *reinterpret_cast<const float4 *>(own + c + 8 * e), y1 = *reinterpret_cast<const float4 *>(own + c + 8 * e + 4);
-                yy[0] = y0.x, yy[1] = y0.y, yy[2] = y0.z, yy[3] = y0.w, yy[4] = y1.x, yy[5] = y1.y, yy[6] = y1.z, yy[7] = y1.w;
-              }
-#pragma unroll
-              for (int k = 0; k < 8; k += 2)
-                u[4 * e + k / 2] = pack2(fmaf(yy[k], f_own, v[8 * e + k] * f), fmaf(yy[k + 1], f_own, v[8 * e + k + 1] * f));
-            }
-            if (P.wide) {  // (rows of whole 32 bytes, on their borders)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (c + 16 * e < hd) store32(o + c + 16 * e, u + 8 * e);
-            } else {
+            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]) * f;
+            if (own) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (c + 8 * e < hd) *reinterpret_cast<uint4 *>(o + c + 8 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+                if (c + 4 * e < hd) {
+                  const float4 z = *reinterpret_cast<const float4 *>(own + c + 4 * e);
+                  v[4 * e] = fmaf(z.x, f_own, v[4 * e]);
+                  v[4 * e + 1] = fmaf(z.y, f_own, v[4 * e + 1]);
+                  v[4 * e + 2] = fmaf(z.z, f_own, v[4 * e + 2]);
+                  v[4 * e + 3] = fmaf(z.w, f_own, v[4 * e + 3]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = pack2(v[2 * k], v[2 * k + 1]);
+            if (P.wide) {  // (rows of whole 32 bytes, on their borders)
+              store32(o + c, u);
+            } else {
+              *reinterpret_cast<uint4 *>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
+              if (c + 8 < hd) *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
             }
           }
         }
@@ -801,7 +782,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       if (tid == 0 && w.u0 == 0 && w.u1 < w.tiles) {  // (the CTA's last item: it goes on in the next ones)
         const unsigned long long last_place = w.base + w.tiles - 1;
         int c = cta;
-        while (c + 1 < parts && part_begin(total, parts, c + 1) <= last_place) ++c;
+        while (c + 1 < P.ctas && P.part[c + 1].first < P.part[c + 1].end && P.part[c + 1].first <= last_place) ++c;
         split = make_int4(w.i, w.kvh, c - cta + 1, 0);
       }
       slot_there();
@@ -1057,7 +1038,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
 
 // ------------------------------------------------------------------------------------------------ joining
 
-constexpr int kJoinThreads = 256, kJoinAhead = 4;
+constexpr int kJoinThreads = 256, kJoinAhead = 6;
 
 template <int HDP>
 __global__ void __launch_bounds__(kJoinThreads) k_rows_join(const __grid_constant__ Params P, int ctas) {
@@ -1068,7 +1049,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_rows_join(const __grid_constan
   const int4 sp = P.split[c0];
   const int parts = sp.z, hd = a.c.head_dim, g = P.g.d;
   // (after a wait that ran out the notes may be those of another call: nothing outside the workspace is read)
-  if (parts <= 1 || parts > ctas - c0 || sp.x < 0 || sp.x >= P.plan->items || sp.y < 0 || sp.y >= a.c.kv_heads) return;
+  if (parts <= 1 || parts > ctas - c0 || sp.x < 0 || sp.x >= P.part[0].items || sp.y < 0 || sp.y >= a.c.kv_heads) return;
   const int4 x = reinterpret_cast<const int4 *>(P.item + sp.x)[0];
   for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < x.z * kLanes; i += gridDim.y * kJoinThreads) {
     const int r = i / kLanes, dd = (i - r * kLanes) * 4;
@@ -1155,7 +1136,8 @@ cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
   const int64_t most = (double)cap * a.c.kv_heads * tiles > 1e9 ? num_sms : cap * a.c.kv_heads * (one ? 1 : tiles);
   const int grid = (int)std::min<int64_t>(num_sms, most);
   p.cap = (int)cap;
-  p.plan = room.take<Plan>(1);
+  p.part = room.take<Part>(grid + 1);
+  p.ctas = grid;
   p.item = room.take<Item>(cap);
   p.start = room.take<unsigned long long>(cap + 1);
   p.split = room.take<int4>(grid);
@@ -1181,7 +1163,9 @@ cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
   e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
   if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
   if (e != cudaSuccess || one) return e;
-  return launch_dependent(k_rows_join<HDP>, dim3(grid, 8), dim3(kJoinThreads), 0, s, 1, p, grid);
+  // blocks of the join: a thread a quarter of 16 features; more of them an item where items are few, and so split over many CTAs
+  const int64_t all = (int64_t)TR * HDP / 4 / kJoinThreads, y = std::min(all, std::max<int64_t>(4, 8 * num_sms / std::min<int64_t>(cap * a.c.kv_heads, grid)));
+  return launch_dependent(k_rows_join<HDP>, dim3(grid, (unsigned)y), dim3(kJoinThreads), 0, s, 1, p, grid);
 }
 
 }  // namespace rows
@@ -1191,7 +1175,7 @@ size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms) {
   const size_t hd = (size_t)(a.c.head_dim + 63) / 64 * 64, items = (size_t)a.N * (a.H / a.c.kv_heads) / 128 + 1 + a.S;
   const size_t shares = (size_t)2 * num_sms * (hd == 256 ? 128 : 256) * (hd * 4 + 16);
   const size_t own = a.pos ? (size_t)a.N * a.H * (a.c.head_dim * 4 + 8) + kPagedShareBytes : 0;
-  return items * 40 + shares + own + num_sms * 16 + 8192;
+  return items * 56 + shares + own + (num_sms + 1) * 64 + 8192;
 }
 
 cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s) {
