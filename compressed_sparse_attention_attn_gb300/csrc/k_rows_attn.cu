@@ -34,7 +34,7 @@ namespace rows {
 
 constexpr int kSub = 128;     // rows of a product
 constexpr int kEnd = 1;       // tiles that the end of an item counts for
-constexpr int kMinPlaces = 4; // tiles a CTA has at least
+constexpr int kMinPlaces = 2; // places a CTA has at least
 constexpr int kNote = 8;      // tiles (and items) whose notes are kept: more than the copies can be ahead
 constexpr float kRaise = 8.f;
 
@@ -47,8 +47,9 @@ struct Item {
 // A CTA's part of the places (a kv head's items one behind the other, head after head): first .. end - 1, of which the first is in item
 // `item` of head kvh; `items` of a head, `places` of a head.  No places: first == end.
 struct Part {
-  unsigned long long first, end, places;
+  unsigned long long first, end, places, start;  // start: first place of the item
   int item, kvh, items, spare;
+  Item d;
 };
 
 struct Params {
@@ -83,14 +84,14 @@ struct Shape {
   static constexpr bool kSplit = HDP <= 128;
   static constexpr int kRegsSoft = 208, kRegsRest = 88;
   static constexpr int kQ = 0, kRing = QT * kQBytes, kBars = kRing + NST * kStage;
-  static constexpr int kSlots = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 80;
+  static constexpr int kSlots = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 128;
   static constexpr int kSmem = kSlots + (kSoft + kMma) * 2 * 64;  // (all that the kernel has: the swizzled tiles come first)
   static constexpr int kColO = 2 * KVT;                     // columns of tensor memory: two score buffers, then QT x HDP of O
 };
 
 // ------------------------------------------------------------------------------------------------ plan
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;  // (1024: 1 us more for every step's barriers)
 
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *warp_sum, unsigned long long &sum) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -208,7 +209,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
   const int parts = (int)min((unsigned long long)P.ctas, max(1ull, total / kMinPlaces));
   for (int c = tid; c <= P.ctas; c += kPlanThreads) {
     const int n = min(c, parts);
-    Part q{total / parts * n + total % parts * n / parts, 0, places, 0, 0, items, 0};
+    Part q{};
+    q.first = total / parts * n + total % parts * n / parts;
+    q.places = places;
+    q.items = items;
     q.end = c < parts ? total / parts * (n + 1) + total % parts * (n + 1) / parts : q.first;
     if (q.first < q.end) {
       q.kvh = (int)(q.first / places);
@@ -220,6 +224,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
         else hi = mid - 1;
       }
       q.item = lo;
+      q.start = P.start[lo];
+      q.d = P.item[lo];
     }
     P.part[c] = q;
   }
@@ -279,7 +285,8 @@ struct Walk {
   }
   // The first item (all lanes that use the slots together; `by`: the one that copies).
   __device__ __forceinline__ bool first(bool by) {
-    bool more = load();
+    const int4 *at = reinterpret_cast<const int4 *>(&rg->d);
+    bool more = set(at[0], at[1], at[2], rg->start);
     if (more && u0 >= u1) {  // (the part begins in the place of an item's end)
       step();
       more = load();
@@ -305,6 +312,13 @@ struct Walk {
 };
 
 // The position tiles x .. y - 1, of the CTA's, that 128-row tile t of an item attends.
+// The rows of position tile j that are filled, and multiplied with: up to the item's last position, in steps of a product.
+template <int KVT>
+__device__ __forceinline__ int tile_rows(int end, int j) {
+  const int left = max(end - j * KVT, 1);
+  return left >= KVT ? KVT : (left + 15) & ~15;
+}
+
 template <int KVT, bool SLOT>
 __device__ __forceinline__ void sub_range(const Walk<KVT, SLOT> &w, int t, int &x, int &y) {
   const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1, lo = t ? w.d.begin1 : w.d.begin, end = t ? w.d.end : w.d.end0;
@@ -557,7 +571,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     if (tid == 0) P.split[cta] = make_int4(0, 0, 0, 0);
     return;
   }
-  if (tid == 0) rg = P.part[cta];
+  if (tid < (int)sizeof(Part) / 16) reinterpret_cast<int4 *>(&rg)[tid] = reinterpret_cast<const int4 *>(P.part + cta)[tid];
   if (warp == kSoft) tc::tmem_alloc(tmem_slot, 512);  // (behind the wait: a block of the kernel before may still ask for tensor memory)
   tc::tc_fence_before();
   __syncthreads();
@@ -647,10 +661,11 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           // A weight of 0 does not undo a NaN: in a tile that not every row of the item attends, values that are not finite are
           // taken out before the product (by both tiles of rows, whichever comes first), and the rows that attend them get them
           // at the end.  (Behind the scores: only then is the stage's barrier in the phase that is asked for, or the next.)
-          const int stage = 2 * (note0 + j) + 1;
+          const int stage = 2 * (note0 + j) + 1, rows = tile_rows<KVT>(w.d.end, j);
           if (!(ok = warp_wait(&full[stage % NST], (uint32_t)((stage / NST) & 1), abort_flag))) break;
 #pragma unroll 4
           for (int i = 0; i < S::kStage / 16 / kSub; ++i) {
+            if ((i * kSub + r) / 8 % KVT >= rows) continue;
             const uint32_t v_at = s_ring + (stage % NST) * S::kStage + (i * kSub + r) * 16;
             uint32_t z[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(v_at) : "memory");
@@ -825,14 +840,12 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         tc::mma_commit(&s_full[b]);
         tc::mbar_arrive(&s_full[b]);
       };
-      auto values = [&](int stage, int half, bool first) {  // (the half's weights are there)
+      auto values = [&](int stage, int half, int rows, bool first) {  // (the half's weights are there)
         tc::tc_fence_after();
         const uint32_t A = tmem + buffer(n_p) * KVT, B = dv + (stage % NST) * (S::kStage >> 4);
+        const int k1 = min((half + 1) * (KVT / 32), rows / 16);
 #pragma unroll 2
-        for (int k = 0; k < KVT / 32; ++k) {
-          const int kk = half * (KVT / 32) + k;
-          mma_ts(dO, A + 8 * kk, hi | (B + kk * 128), id_v, first && kk == 0 ? 0u : 1u);
-        }
+        for (int k = half * (KVT / 32); k < k1; ++k) mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
       };
       // The two warps' products come in groups, each as a whole behind the other's: one tile's scores are then there while the other's
       // are computed (product by product in turn, both would be late, and both softmaxes run at once).
@@ -865,6 +878,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         unlock();
         for (int j = j0; j < j1; ++j, s += 2) {
           const bool live = x <= j && j < y, next = j + 1 < j1;
+          const int rows = tile_rows<KVT>(w.d.end, j);
           if (QT == 1 && next) {  // (the other score buffer: before this tile's values)
             if (!(ok = keys_there(j + 1, s + 2))) break;
             keys(j + 1, s + 2);
@@ -873,7 +887,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           if (live) {
             const uint32_t b = buffer(n_p), ph = phase(n_p);
             if (!(ok = wait(&p_half[b], ph, abort_flag))) break;
-            values(s + 1, 0, j == x);
+            values(s + 1, 0, rows, j == x);
             if (!(ok = wait(&p_full[b], ph, abort_flag))) break;
           }
           if (QT == 2 && next) {
@@ -882,7 +896,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           ok = lock();
           if (!ok) break;
           if (live) {
-            values(s + 1, 1, false);
+            values(s + 1, 1, rows, false);
             const uint32_t b = buffer(n_p++);
             tc::mma_commit(&pv_done[b]);
             tc::mbar_arrive(&pv_done[b]);
@@ -987,8 +1001,9 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         if (lane != 0) tc::mbar_arrive(&full[buf]);
       } else {
       copied = true;
+      const int rows = tile_rows<KVT>(f.end, (int)(f.at / KVT));
 #pragma unroll 1
-      for (int k = 0; k < kW; ++k) {  // (rolled: four times the code would be fetched anew for every stage)
+      for (int k = 0; 32 * k < rows; ++k) {  // (rolled: four times the code would be fetched anew for every stage)
         int page = f.page[0];
         uint32_t good = there[0];
 #pragma unroll
@@ -998,6 +1013,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         const int64_t off = (good >> lane) & 1u ? page * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
 #pragma unroll 2
         for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes 128 bytes of a row
+          if (32 * k + 4 * i >= rows) break;
           const int r7 = (4 * i + (lane >> 3)) & 7;
           const int64_t o = __shfl_sync(0xffffffffu, off, 4 * i + (lane >> 3));
 #pragma unroll
@@ -1175,7 +1191,7 @@ size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms) {
   const size_t hd = (size_t)(a.c.head_dim + 63) / 64 * 64, items = (size_t)a.N * (a.H / a.c.kv_heads) / 128 + 1 + a.S;
   const size_t shares = (size_t)2 * num_sms * (hd == 256 ? 128 : 256) * (hd * 4 + 16);
   const size_t own = a.pos ? (size_t)a.N * a.H * (a.c.head_dim * 4 + 8) + kPagedShareBytes : 0;
-  return items * 56 + shares + own + (num_sms + 1) * 64 + 8192;
+  return items * 56 + shares + own + (num_sms + 1) * 112 + 8192;
 }
 
 cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s) {
