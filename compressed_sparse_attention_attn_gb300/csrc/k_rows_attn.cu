@@ -390,8 +390,16 @@ struct Finish {
 __device__ __forceinline__ Finish finish(float m, float lr, float l, float2 own, const float *sink, int h) {
   const float M = fmaxf(m, own.x), ref = M == -INFINITY ? 0.f : M;
   const float e = paged::ex2(m - ref), eo = paged::ex2(own.x - ref);  // (2^-inf = 0)
-  const float f = paged::out_factor(M, fmaf(own.y, eo, lr * e), sink, h), sum = fmaf(own.y, eo, l * e);
-  return {f * e, f * eo, sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f};
+  const float below = fmaf(own.y, eo, lr * e), sum = fmaf(own.y, eo, l * e);
+  float top = ref, with = 0.f;  // with the sink's term
+  if (sink) {
+    const float s2 = sink[h] * 1.4426950408889634f;
+    top = M == -INFINITY && s2 == -INFINITY ? 0.f : fmaxf(M, s2);
+    with = s2 == INFINITY ? INFINITY : paged::ex2(s2 - top);
+  }
+  const float em = M == -INFINITY ? 0.f : paged::ex2(M - top), all = fmaf(below, em, with);
+  const float f = all == 0.f ? 0.f : __fdividef(em, all);
+  return {f * e, f * eo, sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.6931471805599453f};
 }
 // Whether a row of the prefix form is there, and not padding.
 __device__ __forceinline__ bool row_live(const RowsAttnArgs &a, int n) {
@@ -406,10 +414,11 @@ template <int KVT>
 __device__ __forceinline__ void mask_scores(uint32_t tS, float by, int from, int to, const uint32_t *there) {
 #pragma unroll 1
   for (int k = 0; k < KVT / 32; ++k, tS += 32, from -= 32, to -= 32) {
-    float v[32];
-    attn::tmem_ld_32cols(tS, v);
     const int f = min(max(from, 0), 32), e = min(max(to, -1), 31) + 1;
     const uint32_t mask = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & (f == 32 ? 0u : 0xffffffffu << f) & there[k];
+    if (by == 1.f && __all_sync(0xffffffffu, mask == 0xffffffffu)) continue;
+    float v[32];
+    attn::tmem_ld_32cols(tS, v);
     uint32_t u[16];
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
@@ -492,6 +501,25 @@ __device__ __forceinline__ bool weights(float sc, float &m, float &l, float &lr,
   for (int k = 0; k < KVT / 2; ++k) add_halves(pk[k], l4[k & 1].x, l4[k & 1].y);
   lr += (l4[0].x + l4[0].y) + (l4[1].x + l4[1].y);
   return true;
+}
+
+// A lane's share of a tile of values, 16 bytes of every 2 KB: those that are not finite, in the tile's first `rows` rows (behind them lies
+// what was there before), become 0.
+template <int KVT>
+__device__ __noinline__ void clear_odd(uint32_t at, int n, int r, int rows, volatile int *odd_item, int seq) {
+  for (int i = 0; i < n; ++i, at += kSub * 16) {
+    if ((i * kSub + r) / 8 % KVT >= rows) continue;
+    uint32_t z[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(at) : "memory");
+    if (!(not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3]))) continue;
+    *odd_item = seq;  // (before they are gone: the other tile of rows may find them gone)
+    __threadfence_block();
+    for (int k = 0; k < 4; ++k) {
+      if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
+      if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]) : "memory");
+  }
 }
 
 // Values that are not finite were left out of tiles that not every row attends: to a row that attends positions from .. to - 1, in its
@@ -663,23 +691,16 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           // at the end.  (Behind the scores: only then is the stage's barrier in the phase that is asked for, or the next.)
           const int stage = 2 * (note0 + j) + 1, rows = tile_rows<KVT>(w.d.end, j);
           if (!(ok = warp_wait(&full[stage % NST], (uint32_t)((stage / NST) & 1), abort_flag))) break;
+          const uint32_t v_at = s_ring + (stage % NST) * S::kStage + r * 16;
+          uint32_t odd = 0;
 #pragma unroll 4
           for (int i = 0; i < S::kStage / 16 / kSub; ++i) {
-            if ((i * kSub + r) / 8 % KVT >= rows) continue;
-            const uint32_t v_at = s_ring + (stage % NST) * S::kStage + (i * kSub + r) * 16;
             uint32_t z[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(v_at) : "memory");
-            if (__builtin_expect(not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3]), 0)) {
-              odd_item[w.seq & (kNote - 1)] = w.seq;  // (before they are gone: the other tile of rows may find them gone)
-              __threadfence_block();
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(v_at + i * (kSub * 16)) : "memory");
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
-                if ((z[k] & 0x7f800000u) == 0x7f800000u) z[k] &= 0xffffu;
-              }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v_at), "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3]) : "memory");
-            }
+            for (int k = 0; k < 4; ++k) odd |= (z[k] & 0x7f807f80u) + 0x00800080u;  // (a carry where an exponent is all ones)
           }
+          if (__builtin_expect((odd & 0x80008000u) != 0, 0)) clear_odd<KVT>(v_at, S::kStage / 16 / kSub, r, rows, odd_item + (w.seq & (kNote - 1)), w.seq);
           attn::fence_proxy_async();
         }
         if (work) {
@@ -843,9 +864,17 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       auto values = [&](int stage, int half, int rows, bool first) {  // (the half's weights are there)
         tc::tc_fence_after();
         const uint32_t A = tmem + buffer(n_p) * KVT, B = dv + (stage % NST) * (S::kStage >> 4);
-        const int k1 = min((half + 1) * (KVT / 32), rows / 16);
+        if (rows == KVT) {  // (known counts: 2 % of a long prompt's time)
 #pragma unroll 2
-        for (int k = half * (KVT / 32); k < k1; ++k) mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
+          for (int k = 0; k < KVT / 32; ++k) {
+            const int kk = half * (KVT / 32) + k;
+            mma_ts(dO, A + 8 * kk, hi | (B + kk * 128), id_v, first && kk == 0 ? 0u : 1u);
+          }
+        } else {
+#pragma unroll 1
+          for (int k = half * (KVT / 32); k < min((half + 1) * (KVT / 32), rows / 16); ++k)
+            mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
+        }
       };
       // The two warps' products come in groups, each as a whole behind the other's: one tile's scores are then there while the other's
       // are computed (product by product in turn, both would be late, and both softmaxes run at once).
