@@ -311,7 +311,6 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == tiles; }
 };
 
-// The position tiles x .. y - 1, of the CTA's, that 128-row tile t of an item attends.
 // The rows of position tile j that are filled, and multiplied with: up to the item's last position, in steps of a product.
 template <int KVT>
 __device__ __forceinline__ int tile_rows(int end, int j) {
@@ -319,12 +318,22 @@ __device__ __forceinline__ int tile_rows(int end, int j) {
   return left >= KVT ? KVT : (left + 15) & ~15;
 }
 
+// The first row of the item that the warps of tile of rows t have, -1: none.  An item of no more than 128 rows is tile 0's or tile 1's by turns,
+// so that the end of one and the beginning of the next pass beside each other (a mixed step of 64 decodes 127 against XXX us).
 template <int KVT, bool SLOT>
-__device__ __forceinline__ void sub_range(const Walk<KVT, SLOT> &w, int t, int &x, int &y) {
-  const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1, lo = t ? w.d.begin1 : w.d.begin, end = t ? w.d.end : w.d.end0;
+__device__ __forceinline__ int sub_rows(const Walk<KVT, SLOT> &w, int t, bool two) {
+  if (!two) return 0;
+  if (w.d.rows > kSub) return kSub * t;
+  return (w.seq & 1) == t ? 0 : -1;
+}
+// The position tiles x .. y - 1, of the CTA's, that the warps of tile of rows t have to do with.
+template <int KVT, bool SLOT>
+__device__ __forceinline__ void sub_range(const Walk<KVT, SLOT> &w, int t, bool two, int &x, int &y) {
+  const int sub = sub_rows(w, t, two);
+  const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1, lo = sub > 0 ? w.d.begin1 : w.d.begin, end = sub > 0 ? w.d.end : w.d.end0;
   x = max(j0, lo / KVT);
   y = min(j1, (end - 1) / KVT + 1);  // (all of them not negative)
-  if (kSub * t >= w.d.rows || end <= lo || y < x) x = y = j0;
+  if (sub < 0 || end <= lo || y < x) x = y = j0;
 }
 
 // ------------------------------------------------------------------------------------------------ building blocks
@@ -618,12 +627,12 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     if constexpr (S::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoft));
     const int t = warp >> 2, quad = warp & 3, r = quad * 32 + lane;  // of tile t of the item
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16, tO = tmem + S::kColO + t * HDP + lane_off;
-    auto load_q = [&](const Item &d, int kvh) {
+    auto load_q = [&](const Item &d, int kvh, int sub) {
       const int cc = lane & 7;
 #pragma unroll 2
       for (int i = 0; i < 8; ++i) {
-        const int row = quad * 32 + 4 * i + (lane >> 3), R = d.row0 + t * kSub + row;
-        const bool in = t * kSub + row < d.rows;
+        const int row = quad * 32 + 4 * i + (lane >> 3), R = d.row0 + sub + row;
+        const bool in = sub + row < d.rows;
         const int tok = (int)P.g.div(R), h = R - tok * g;
         const bf16 *q = in ? a.q + (int64_t)(d.tok0 + tok) * a.q_t + (int64_t)(kvh * g + h) * hd + cc * 8 : a.q;
 #pragma unroll
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     bool more = w.first(lane == 0);
     auto has_rows = [&](const Walk<KVT, true> &x) {  // whether tile t has anything to do in this CTA's part of the item
       int from, to;
-      sub_range(x, t, from, to);
+      sub_range(x, t, QT == 2, from, to);
       return to > from;
     };
     auto slot_there = [&]() {  // what lane 0 has copied, for the warp
@@ -646,7 +655,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       __syncwarp();
     };
     if (more && has_rows(w)) {
-      load_q(w.d, w.kvh);
+      load_q(w.d, w.kvh, sub_rows(w, t, QT == 2));
       attn::cp_async_wait_all();
       attn::fence_proxy_async();
       tc::mbar_arrive(&q_full[t]);
@@ -665,10 +674,11 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     int4 split = make_int4(0, 0, 0, 0);
     while (more) {
       int x, y, lo = 0, hi = 0x7fffffff;  // (a row that is not there attends all: no mask for its sake)
-      sub_range(w, t, x, y);
-      const bool work = t * kSub + quad * 32 < w.d.rows;  // (of the warp)
-      if (t * kSub + r < w.d.rows) {
-        const int tok = w.d.tok0 + (int)P.g.div(w.d.row0 + t * kSub + r);
+      sub_range(w, t, QT == 2, x, y);
+      const int sub = sub_rows(w, t, QT == 2);
+      const bool work = sub >= 0 && sub + quad * 32 < w.d.rows;  // (of the warp)
+      if (work && sub + r < w.d.rows) {
+        const int tok = w.d.tok0 + (int)P.g.div(w.d.row0 + sub + r);
         if (!a.pos) {
           hi = tok + w.d.shift;
           if (a.window > 0) lo = max(0, hi - a.window + 1);
@@ -729,8 +739,10 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       {
         slot_there();
         Walk<KVT, true> nx = w;
-        if (nx.peek() && has_rows(nx)) {
-          load_q(nx.d, nx.kvh);
+        const bool there = nx.peek();
+        ++nx.seq;
+        if (there && has_rows(nx)) {
+          load_q(nx.d, nx.kvh, sub_rows(nx, t, QT == 2));
           q_next = true;
         }
       }
@@ -745,7 +757,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       }
       if (work) {
         const Item &d = w.d;
-        const int R = t * kSub + r, q = (int)P.g.div(d.row0 + R), tok = d.tok0 + q, h = w.kvh * g + (d.row0 + R - q * g);
+        const int R = sub + r, q = (int)P.g.div(d.row0 + R), tok = d.tok0 + q, h = w.kvh * g + (d.row0 + R - q * g);
         const bool whole = w.whole(), mine = R < d.rows, live = mine && row_live(a, tok);
         if (m != -INFINITY) m *= sc;
         const bool odd = y > x && odd_item[w.seq & (kNote - 1)] == w.seq;
@@ -895,7 +907,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       while (more) {
         const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1;
         int x, y;
-        sub_range(w, t, x, y);
+        sub_range(w, t, QT == 2, x, y);
         auto keys_there = [&](int j, int stage) { return stage_ready(stage) && (j != x || x == y || wait(&q_full[t], n_q++ & 1, abort_flag)); };
         auto keys = [&](int j, int stage) {  // tile j's scores
           if (x <= j && j < y) scores(stage);
