@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         const bool in_part = odd_scale || !__all_sync(0xffffffffu, lo <= at && hi - at >= KVT - 1);  // some row attends not all of the tile
         if (!(ok = warp_wait(&s_full[b], QT == 2 ? n_s & 1 : (n_s >> 1) & 1, abort_flag))) break;
         tc::tc_fence_after();
-        if (at < w.d.at0 || at + KVT > w.d.at1) {
+        if (at < w.d.at0 || w.d.at1 - at < KVT) {  // (at + KVT may pass 31 bits)
           // A weight of 0 does not undo a NaN: in a tile that not every row of the item attends, values that are not finite are
           // taken out before the product (by both tiles of rows, whichever comes first), and the rows that attend them get them
           // at the end.  (Behind the scores: only then is the stage's barrier in the phase that is asked for, or the next.)

@@ -639,6 +639,38 @@ def test_prefix_replayed(csa, ctx):
     assert torch.equal(got[[0, 2, 3]], want[1][[0, 2, 3]]) and ctx.status() == 0
 
 
+def test_workspace(csa, ctx):
+    """More rows of a prefix batch than the context's workspace holds shares for: refused, and nothing is written."""
+    H, hd, N = 64, 128, 4096
+    b = Batch([40], H, 8, hd, 16)
+    q = torch.full((N, H, hd), 3.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(csa.CsaError, match="workspace") as e:
+        ctx.prefix_attn(q, csa.PagedCache(b.k, b.v), b.table, i32([39] * N), b.table, i32([40]), 0.1, req=i32([0] * N), out=q)
+    assert e.value.code == -2
+    torch.cuda.synchronize()
+    assert (q == 3).all() and ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+def test_prompt_last_positions(csa, ctx, hd):
+    """Tokens whose tile of positions ends past 2^31: a NaN behind a token's position does not reach it there either."""
+    H, kv, page, n = 2, 1, 2 ** 16, 200
+    width = (2 ** 31 - 1) // page
+    rows, window = width * page, 90
+    k = torch.ones(2, page, kv, hd, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones_like(k)
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    v[1, page - 100, 0, 5] = float("nan")
+    q = torch.zeros(n, H, hd, dtype=torch.bfloat16, device="cuda")
+    o = ctx.prompt_attn(q, csa.PagedCache(k, v), table, i32([0, n]), i32([rows]), 1.0, window=window)
+    pos = torch.arange(n, device="cuda") - n + page
+    hit = (pos >= page - 100) & (pos < page - 100 + window)
+    assert o[hit][..., 5].isnan().all() and (o[~hit] == 1).all()
+    o[..., 5] = 1
+    assert (o == 1).all() and ctx.status() == 0
+
+
 def test_no_tokens(csa, ctx):
     b = Batch([40], 8, 2, 64, 16)
     cache, none = csa.PagedCache(b.k, b.v), i32([])
