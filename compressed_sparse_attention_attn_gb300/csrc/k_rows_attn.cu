@@ -531,6 +531,32 @@ __device__ __noinline__ void clear_odd(uint32_t at, int n, int r, int rows, vola
   }
 }
 
+// A row's result with the share of its own pages (own, none: NULL): O from the columns from tO on (there: if it was computed), times f.
+// o NULL: nothing is written.  (Out of line: prompts run the code around it.)
+__device__ __noinline__ void out_with_own(uint32_t tO, bool there, float f, const float *own, float f_own, int hd, bf16 *o) {
+#pragma unroll 1
+  for (int c = 0; c < hd; c += 8) {
+    uint32_t u[8] = {};
+    __syncwarp();
+    if (there)
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                   : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                   : "r"(tO + c)
+                   : "memory");
+    if (!o) continue;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(u[k]) * f;
+    if (own) {
+      const float4 z0 = *reinterpret_cast<const float4 *>(own + c), z1 = *reinterpret_cast<const float4 *>(own + c + 4);
+      const float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = fmaf(z[k], f_own, v[k]);
+    }
+    *reinterpret_cast<uint4 *>(o + c) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+  }
+}
+
 // Values that are not finite were left out of tiles that not every row attends: to a row that attends positions from .. to - 1, in its
 // share or its result (whatever else is in the sum, it is not finite).
 __device__ __noinline__ void odd_values(const RowsAttnArgs &a, const paged::FastDiv &page, int seg, int kvh, int from, int to, float *share,
@@ -781,6 +807,9 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           share = P.share_o + at * HDP;
           if (mine) P.share_ml[at] = make_float4(m, lr, l, 0.f);
         }
+        if (whole && P.own_o) {
+          out_with_own(tO, y > x, f, own, f_own, hd, live ? o : nullptr);
+        } else {
 #pragma unroll 1
         for (int c = 0; c < hd; c += 16) {
           uint32_t u[16];
@@ -800,17 +829,6 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
             float v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]) * f;
-            if (own) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (c + 4 * e < hd) {
-                  const float4 z = *reinterpret_cast<const float4 *>(own + c + 4 * e);
-                  v[4 * e] = fmaf(z.x, f_own, v[4 * e]);
-                  v[4 * e + 1] = fmaf(z.y, f_own, v[4 * e + 1]);
-                  v[4 * e + 2] = fmaf(z.z, f_own, v[4 * e + 2]);
-                  v[4 * e + 3] = fmaf(z.w, f_own, v[4 * e + 3]);
-                }
-            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) u[k] = pack2(v[2 * k], v[2 * k + 1]);
             if (P.wide) {  // (rows of whole 32 bytes, on their borders)
@@ -820,6 +838,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
               if (c + 8 < hd) *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
             }
           }
+        }
         }
         tc::tc_fence_before();
         if (__builtin_expect(odd && mine && (share || live), 0)) {
