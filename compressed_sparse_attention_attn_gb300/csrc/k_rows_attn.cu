@@ -15,9 +15,21 @@
 // O takes half of tensor memory, one tile has two score buffers instead.
 //
 // A plan kernel lists the items with the number of their position tiles (k_rows_plan); the tiles of all items and kv heads stand one
-// behind the other, and each CTA takes an equal part of them in a row, so every CTA has as much to do as any other whatever
-// the lengths and masks are.  An item that several CTAs worked on is joined from their shares (M, L, O), in the order of the
-// CTAs, by k_rows_join.  The rows of a request that is no one's prefix come from k_paged_attn as one more share.
+// behind the other, with places for each item's end, and each CTA takes an equal part of them in a row, so every CTA has as much to do
+// as any other whatever the lengths and masks are.  An item that several CTAs worked on is joined from their shares (M, L, O), in the
+// order of the CTAs, by k_rows_join.  The rows of a prefix batch's own pages come from k_paged_attn as one more share.
+//
+// A CTA an SM: four warps a tile of rows for the softmax and the results, a warp that issues its products, and the copies (whole
+// tiles by TMA, boxes of up to 128 rows inside a page where pages hold whole boxes of 8 rows at least; ragged tiles and other pages by
+// cp.async, rows that are not there as zeros).  Shared memory holds q (64 KB at 128 features) and a ring of five tiles of keys or values.
+// All waits are time-bounded.
+//
+// Bound by the way of a tile through its stages: scores to softmax (1600 cycles, of which 64 pairs of exponentials take 770 at least),
+// softmax to values and the next scores (768 cycles of products, behind the other tile's).  The products alone take 2700 cycles for two
+// tiles of rows and a tile of positions (2048 by the measured peak: two products read q and the keys from shared memory at
+// 128 bytes a cycle, all of its rate), with the softmax 3400.  16384 tokens of 64 heads over 8 of 128: 3.32 ms, 1325 TFLOP/s, 69 % of
+// the measured bf16 rate (77 % of the sustained one); 12 ragged prompts of 100 to 4000 tokens (32 over 8 of 128) 311 us, 45 %:
+// the ends of their items.  256 rows behind 32768 shared ones (64 over 8 of 128) 355 us, of which their own pages take 115.
 #include <algorithm>
 #include <cstring>
 
@@ -33,7 +45,9 @@ bool tma_map_pages_bf16(CUtensorMap *m, const void *base, const uint64_t (&dims)
 namespace rows {
 
 constexpr int kSub = 128;     // rows of a product
-constexpr int kEnd = 1;       // tiles that the end of an item counts for
+// Tiles that the end of an item counts for: its last tiles' masks and values looked over, the wait for the last product, results, the next
+// q, 10 thousand cycles in all where a tile takes 3.4.  (4096 tokens of 64 heads over 8 of 128: 322, 282, 276 and 280 us for 1 to 4.)
+constexpr int kEnd = 3;
 constexpr int kMinPlaces = 2; // places a CTA has at least
 constexpr int kNote = 8;      // tiles (and items) whose notes are kept: more than the copies can be ahead
 constexpr float kRaise = 8.f;
@@ -318,8 +332,8 @@ __device__ __forceinline__ int tile_rows(int end, int j) {
   return left >= KVT ? KVT : (left + 15) & ~15;
 }
 
-// The first row of the item that the warps of tile of rows t have, -1: none.  An item of no more than 128 rows is tile 0's or tile 1's by turns,
-// so that the end of one and the beginning of the next pass beside each other (a mixed step of 64 decodes 127 against XXX us).
+// The first row of the item that the warps of tile of rows t have, -1: none.  An item of no more than 128 rows is tile 0's or tile 1's
+// by turns, so that the end of one and the beginning of the next pass beside each other (a mixed step of 64 decodes 125 against 127 us).
 template <int KVT, bool SLOT>
 __device__ __forceinline__ int sub_rows(const Walk<KVT, SLOT> &w, int t, bool two) {
   if (!two) return 0;
@@ -370,6 +384,9 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *u) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
                "r"(u[5]), "r"(u[6]), "r"(u[7])
                : "memory");
+}
+__device__ __forceinline__ void lds4(uint32_t (&z)[4], uint32_t at) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(at) : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
@@ -464,7 +481,7 @@ __device__ __forceinline__ bool weights(float sc, float &m, float &l, float &lr,
 #pragma unroll
   for (int k = 4; k < KVT / 2; ++k) q4[k & 3] = max3(q4[k & 3], s[k].x, s[k].y);
   const float mx = fmaxf(max3(q4[0], q4[1], q4[2]), q4[3]);
-  const bool raise = first ? mx > m : (mx - m) * sc > kRaise || (m == -INFINITY && mx > m);
+  const bool raise = (mx - m) * sc > kRaise || (m == -INFINITY && mx > m);
   if (first) {
     m = mx;
   } else if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
@@ -519,7 +536,7 @@ __device__ __noinline__ void clear_odd(uint32_t at, int n, int r, int rows, vola
   for (int i = 0; i < n; ++i, at += kSub * 16) {
     if ((i * kSub + r) / 8 % KVT >= rows) continue;
     uint32_t z[4];
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(at) : "memory");
+    lds4(z, at);
     if (!(not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3]))) continue;
     *odd_item = seq;  // (before they are gone: the other tile of rows may find them gone)
     __threadfence_block();
@@ -561,7 +578,7 @@ __device__ __noinline__ void out_with_own(uint32_t tO, bool there, float f, cons
 // share or its result (whatever else is in the sum, it is not finite).
 __device__ __noinline__ void odd_values(const RowsAttnArgs &a, const paged::FastDiv &page, int seg, int kvh, int from, int to, float *share,
                                         bf16 *o) {
-  const bf16 *vb = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) + kvh * a.c.v_head : reinterpret_cast<const bf16 *>(a.c.k) + kvh * a.c.k_head;
+  const bf16 *vb = reinterpret_cast<const bf16 *>(a.c.v ? a.c.v : a.c.k) + kvh * (a.c.v ? a.c.v_head : a.c.k_head);
   const int64_t st_page = a.c.v ? a.c.v_page : a.c.k_page, st_row = a.c.v ? a.c.v_row : a.c.k_row;
   for (int p = from; p < to; ++p) {
     const int pg = (int)page.div((uint32_t)p), id = a.table[(int64_t)seg * a.width + pg];
@@ -603,7 +620,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
   uint64_t *full = bars, *empty = bars + NST, *s_full = bars + 2 * NST, *p_full = s_full + 2, *pv_done = s_full + 4,
            *q_full = s_full + 6, *p_half = s_full + 8, *drain = s_full + 10;
   uint32_t *masks = reinterpret_cast<uint32_t *>(bars + 32);  // [kNote][4]: positions of a tile that are there
-  volatile int *odd_item = reinterpret_cast<volatile int *>(masks + 4 * kNote);  // [kNote]: items with a value that is not finite where not all attend
+  // [kNote]: items with a value that is not finite in a tile that not every row attends
+  volatile int *odd_item = reinterpret_cast<volatile int *>(masks + 4 * kNote);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(masks + 5 * kNote);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *issue_lock = reinterpret_cast<int *>(tmem_slot + 2);
@@ -732,11 +750,12 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
 #pragma unroll 4
           for (int i = 0; i < S::kStage / 16 / kSub; ++i) {
             uint32_t z[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3]) : "r"(v_at + i * (kSub * 16)) : "memory");
+            lds4(z, v_at + i * (kSub * 16));
 #pragma unroll
             for (int k = 0; k < 4; ++k) odd |= (z[k] & 0x7f807f80u) + 0x00800080u;  // (a carry where an exponent is all ones)
           }
-          if (__builtin_expect((odd & 0x80008000u) != 0, 0)) clear_odd<KVT>(v_at, S::kStage / 16 / kSub, r, rows, odd_item + (w.seq & (kNote - 1)), w.seq);
+          if (__builtin_expect((odd & 0x80008000u) != 0, 0))
+            clear_odd<KVT>(v_at, S::kStage / 16 / kSub, r, rows, odd_item + (w.seq & (kNote - 1)), w.seq);
           attn::fence_proxy_async();
         }
         if (work) {
@@ -843,7 +862,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         tc::tc_fence_before();
         if (__builtin_expect(odd && mine && (share || live), 0)) {
           const int from = max(max(lo, d.begin), a.window > 0 ? 0 : d.at1 / KVT * KVT);  // (tiles that all attend have theirs already)
-          odd_values(a, P.page, d.seg, w.kvh, max(from, x * KVT), (int)min(min((int64_t)hi + 1, (int64_t)d.end), (int64_t)y * KVT), share, o);
+          const int to = (int)min(min((int64_t)hi + 1, (int64_t)d.end), (int64_t)y * KVT);
+          odd_values(a, P.page, d.seg, w.kvh, max(from, x * KVT), to, share, o);
         }
       }
       if (tid == 0 && w.u0 == 0 && w.u1 < w.tiles) {  // (the CTA's last item: it goes on in the next ones)
@@ -860,247 +880,249 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
   } else {
     if constexpr (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsRest));
     if (warp < kSoft + S::kMma) {
-    // ------------------------------------------------------------------------------ products, issued by one elected lane
-    if (tc::elect_one()) {
-      const uint32_t id_s = tc::idesc_bf16_f32(kSub, KVT), id_v = tc::idesc_bf16_f32(kSub, hd16, false, /*b_mn_major=*/true);
-      const uint32_t dq = (uint32_t)tc::sdesc_sw128(s_q, 16, 1024), dk = (uint32_t)tc::sdesc_sw128(s_ring, 16, 1024),
-                     dv = (uint32_t)tc::sdesc_sw128(s_ring, KVT * 128, 1024);
-      const uint64_t hi = tc::sdesc_sw128(0, 16, 1024) & 0xffffffff00000000ull;
-      const int ks = hd16 / 16;
-      int s = 0;  // stages so far
-      auto stage_ready = [&](int i) { return wait(&full[i % NST], (uint32_t)((i / NST) & 1), abort_flag); };
-      // A warp has one tile of rows of each item, and lets the stages that the tile attends nothing of pass by.
-      const int t = warp - kSoft;
-      Walk<KVT, true> w;
-      begin(w);
-      bool more = w.first(true);
-      uint32_t n_q = 0, n_s = 0, n_p = 0;
-      const uint32_t dO = tmem + S::kColO + t * HDP;
-      auto buffer = [&](uint32_t n) { return QT == 2 ? (uint32_t)t : n & 1; };
-      auto phase = [&](uint32_t n) { return QT == 2 ? n & 1 : (n >> 1) & 1; };
-      auto scores = [&](int stage) {
-        const uint32_t A = dq + t * (S::kQBytes >> 4), B = dk + (stage % NST) * (S::kStage >> 4), b = buffer(n_s++);
-        const uint32_t d = tmem + b * KVT;
-        uint32_t al = A, bl = B;
-        int k = 0;
+      // ------------------------------------------------------------------------------ products, issued by one elected lane
+      if (tc::elect_one()) {
+        const uint32_t id_s = tc::idesc_bf16_f32(kSub, KVT), id_v = tc::idesc_bf16_f32(kSub, hd16, false, /*b_mn_major=*/true);
+        const uint32_t dq = (uint32_t)tc::sdesc_sw128(s_q, 16, 1024), dk = (uint32_t)tc::sdesc_sw128(s_ring, 16, 1024),
+                       dv = (uint32_t)tc::sdesc_sw128(s_ring, KVT * 128, 1024);
+        const uint64_t hi = tc::sdesc_sw128(0, 16, 1024) & 0xffffffff00000000ull;
+        const int ks = hd16 / 16;
+        int s = 0;  // stages so far
+        auto stage_ready = [&](int i) { return wait(&full[i % NST], (uint32_t)((i / NST) & 1), abort_flag); };
+        // A warp has one tile of rows of each item, and lets the stages that the tile attends nothing of pass by.
+        const int t = warp - kSoft;
+        Walk<KVT, true> w;
+        begin(w);
+        bool more = w.first(true);
+        uint32_t n_q = 0, n_s = 0, n_p = 0;
+        const uint32_t dO = tmem + S::kColO + t * HDP;
+        auto buffer = [&](uint32_t n) { return QT == 2 ? (uint32_t)t : n & 1; };
+        auto phase = [&](uint32_t n) { return QT == 2 ? n & 1 : (n >> 1) & 1; };
+        auto scores = [&](int stage) {
+          const uint32_t A = dq + t * (S::kQBytes >> 4), B = dk + (stage % NST) * (S::kStage >> 4), b = buffer(n_s++);
+          const uint32_t d = tmem + b * KVT;
+          uint32_t al = A, bl = B;
+          int k = 0;
 #pragma unroll 1
-        for (; k + 4 <= ks; k += 4, al += kSub * 128 >> 4, bl += KVT * 128 >> 4)
+          for (; k + 4 <= ks; k += 4, al += kSub * 128 >> 4, bl += KVT * 128 >> 4)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) tc::mma_bf16(d, hi | (al + 2 * e), hi | (bl + 2 * e), id_s, e ? 1u : (k ? 1u : 0u));
+            for (int e = 0; e < 4; ++e) tc::mma_bf16(d, hi | (al + 2 * e), hi | (bl + 2 * e), id_s, e ? 1u : (k ? 1u : 0u));
 #pragma unroll 1
-        for (; k < ks; ++k, al += 2, bl += 2) tc::mma_bf16(d, hi | al, hi | bl, id_s, k ? 1u : 0u);
-        tc::mma_commit(&s_full[b]);
-        tc::mbar_arrive(&s_full[b]);
-      };
-      auto values = [&](int stage, int half, int rows, bool first) {  // (the half's weights are there)
-        tc::tc_fence_after();
-        const uint32_t A = tmem + buffer(n_p) * KVT, B = dv + (stage % NST) * (S::kStage >> 4);
-        if (rows == KVT) {  // (known counts: 2 % of a long prompt's time)
-#pragma unroll 2
-          for (int k = 0; k < KVT / 32; ++k) {
-            const int kk = half * (KVT / 32) + k;
-            mma_ts(dO, A + 8 * kk, hi | (B + kk * 128), id_v, first && kk == 0 ? 0u : 1u);
-          }
-        } else {
-#pragma unroll 1
-          for (int k = half * (KVT / 32); k < min((half + 1) * (KVT / 32), rows / 16); ++k)
-            mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
-        }
-      };
-      // The two warps' products come in groups, each as a whole behind the other's: one tile's scores are then there while the other's
-      // are computed (product by product in turn, both would be late, and both softmaxes run at once).
-      auto lock = [&]() -> bool {
-        uint32_t spins = 0;
-        uint64_t t0 = 0;
-        while (QT == 2 && atomicCAS(issue_lock, 0, 1) != 0)
-          if ((++spins & 255) == 0) {
-            if (t0 == 0) t0 = tc::global_ns();
-            if (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs) return false;
-          }
-        return true;
-      };
-      auto unlock = [&]() {
-        if (QT == 2) atomicExch(issue_lock, 0);
-      };
-      bool ok = true;
-      while (more) {
-        const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1;
-        int x, y;
-        sub_range(w, t, QT == 2, x, y);
-        auto keys_there = [&](int j, int stage) { return stage_ready(stage) && (j != x || x == y || wait(&q_full[t], n_q++ & 1, abort_flag)); };
-        auto keys = [&](int j, int stage) {  // tile j's scores
-          if (x <= j && j < y) scores(stage);
-          tc::mma_commit(&empty[stage % NST]);
+          for (; k < ks; ++k, al += 2, bl += 2) tc::mma_bf16(d, hi | al, hi | bl, id_s, k ? 1u : 0u);
+          tc::mma_commit(&s_full[b]);
+          tc::mbar_arrive(&s_full[b]);
         };
-        ok = keys_there(j0, s) && lock();
-        if (!ok) break;
-        keys(j0, s);
-        unlock();
-        for (int j = j0; j < j1; ++j, s += 2) {
-          const bool live = x <= j && j < y, next = j + 1 < j1;
-          const int rows = tile_rows<KVT>(w.d.end, j);
-          if (QT == 1 && next) {  // (the other score buffer: before this tile's values)
-            if (!(ok = keys_there(j + 1, s + 2))) break;
-            keys(j + 1, s + 2);
+        auto values = [&](int stage, int half, int rows, bool first) {  // (the half's weights are there)
+          tc::tc_fence_after();
+          const uint32_t A = tmem + buffer(n_p) * KVT, B = dv + (stage % NST) * (S::kStage >> 4);
+          if (rows == KVT) {  // (known counts: 2 % of a long prompt's time)
+#pragma unroll 2
+            for (int k = 0; k < KVT / 32; ++k) {
+              const int kk = half * (KVT / 32) + k;
+              mma_ts(dO, A + 8 * kk, hi | (B + kk * 128), id_v, first && kk == 0 ? 0u : 1u);
+            }
+          } else {
+#pragma unroll 1
+            for (int k = half * (KVT / 32); k < min((half + 1) * (KVT / 32), rows / 16); ++k)
+              mma_ts(dO, A + 8 * k, hi | (B + k * 128), id_v, first && k == 0 ? 0u : 1u);
           }
-          if (!(ok = stage_ready(s + 1))) break;
-          if (live) {
-            const uint32_t b = buffer(n_p), ph = phase(n_p);
-            if (!(ok = wait(&p_half[b], ph, abort_flag))) break;
-            values(s + 1, 0, rows, j == x);
-            if (!(ok = wait(&p_full[b], ph, abort_flag))) break;
-          }
-          if (QT == 2 && next) {
-            if (!(ok = keys_there(j + 1, s + 2))) break;
-          }
-          ok = lock();
+        };
+        // The two warps' products come in groups, each as a whole behind the other's: one tile's scores are then there while the other's
+        // are computed (product by product in turn, both would be late, and both softmaxes run at once).
+        auto lock = [&]() -> bool {
+          uint32_t spins = 0;
+          uint64_t t0 = 0;
+          while (QT == 2 && atomicCAS(issue_lock, 0, 1) != 0)
+            if ((++spins & 255) == 0) {
+              if (t0 == 0) t0 = tc::global_ns();
+              if (*abort_flag || tc::global_ns() - t0 > tc::kWaitLimitNs) return false;
+            }
+          return true;
+        };
+        auto unlock = [&]() {
+          if (QT == 2) atomicExch(issue_lock, 0);
+        };
+        bool ok = true;
+        while (more) {
+          const int j0 = w.kt0 + w.u0, j1 = w.kt0 + w.u1;
+          int x, y;
+          sub_range(w, t, QT == 2, x, y);
+          auto keys_there = [&](int j, int stage) {
+          return stage_ready(stage) && (j != x || x == y || wait(&q_full[t], n_q++ & 1, abort_flag));
+        };
+          auto keys = [&](int j, int stage) {  // tile j's scores
+            if (x <= j && j < y) scores(stage);
+            tc::mma_commit(&empty[stage % NST]);
+          };
+          ok = keys_there(j0, s) && lock();
           if (!ok) break;
-          if (live) {
-            values(s + 1, 1, rows, false);
-            const uint32_t b = buffer(n_p++);
-            tc::mma_commit(&pv_done[b]);
-            tc::mbar_arrive(&pv_done[b]);
-          }
-          tc::mma_commit(&empty[(s + 1) % NST]);
-          if (QT == 2 && next) keys(j + 1, s + 2);
+          keys(j0, s);
           unlock();
+          for (int j = j0; j < j1; ++j, s += 2) {
+            const bool live = x <= j && j < y, next = j + 1 < j1;
+            const int rows = tile_rows<KVT>(w.d.end, j);
+            if (QT == 1 && next) {  // (the other score buffer: before this tile's values)
+              if (!(ok = keys_there(j + 1, s + 2))) break;
+              keys(j + 1, s + 2);
+            }
+            if (!(ok = stage_ready(s + 1))) break;
+            if (live) {
+              const uint32_t b = buffer(n_p), ph = phase(n_p);
+              if (!(ok = wait(&p_half[b], ph, abort_flag))) break;
+              values(s + 1, 0, rows, j == x);
+              if (!(ok = wait(&p_full[b], ph, abort_flag))) break;
+            }
+            if (QT == 2 && next) {
+              if (!(ok = keys_there(j + 1, s + 2))) break;
+            }
+            ok = lock();
+            if (!ok) break;
+            if (live) {
+              values(s + 1, 1, rows, false);
+              const uint32_t b = buffer(n_p++);
+              tc::mma_commit(&pv_done[b]);
+              tc::mbar_arrive(&pv_done[b]);
+            }
+            tc::mma_commit(&empty[(s + 1) % NST]);
+            if (QT == 2 && next) keys(j + 1, s + 2);
+            unlock();
+          }
+          if (!ok) break;
+          attn::cp_async_wait_all();
+          more = w.next(true);
         }
-        if (!ok) break;
-        attn::cp_async_wait_all();
-        more = w.next(true);
+        // nothing may still read shared memory, write tensor memory or arrive when the CTA ends
+        tc::mma_commit(drain);
+        const uint64_t t1 = tc::global_ns();
+        while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
+        }
       }
-      // nothing may still read shared memory, write tensor memory or arrive when the CTA ends
-      tc::mma_commit(drain);
-      const uint64_t t1 = tc::global_ns();
-      while (!tc::mbar_try_wait(drain, 0) && tc::global_ns() - t1 < tc::kWaitLimitNs) {
-      }
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------------------------ copies: a warp every second or third stage
-    // The pages of a warp's next stage are looked up while its copies are in flight.
-    const int lw = warp - kSoft - S::kMma, cc = lane & 7;
-    Walk<KVT, false> w;
-    begin(w);
-    bool more = w.first(false);
-    struct Look {
-      int page[kW];
-      uint32_t at;     // first position
-      int kvh, seg, begin, end, tile;
-      bool values;
-    };
-    int s = lw, x = lw, tile0 = 0;  // stage, stage of the item, first tile of the item
-    auto look = [&](Look &f) __attribute__((always_inline)) -> bool {
-      while (more && x >= 2 * (w.u1 - w.u0)) {
-        x -= 2 * (w.u1 - w.u0);
-        tile0 += w.u1 - w.u0;
-        more = w.next(false);
-      }
-      if (!more) return false;
-      const Item &d = w.d;
-      f.at = (uint32_t)(w.kt0 + w.u0 + (x >> 1)) * KVT;
-      f.values = x & 1;
-      f.kvh = w.kvh;
-      f.begin = d.begin;
-      f.end = d.end;
-      f.seg = d.seg;
-      f.tile = tile0 + (x >> 1);
-#pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        const uint32_t p = f.at + 32 * k + lane;
-        const bool in = p >= (uint32_t)d.begin && p < (uint32_t)d.end;
-        f.page[k] = in ? a.table[(int64_t)d.seg * a.width + P.page.div(p)] : 0;
-      }
-      return true;
-    };
-    Look f{};
-    if (G.box_rows && lane == 0) {
-      tc::prefetch_tmap(&G.k);
-      tc::prefetch_tmap(&G.v);
-    }
-    for (bool begun = false, have = true; have; begun = true) {  // (from the second round on with a stage to fill)
-      const uint32_t dst = s_ring + (s % NST) * S::kStage + (lane >> 3) * 128;
-      const int cur = s;
-      bool copied = false;  // by cp.async
-      if (begun) {
-      const bool vals = f.values && a.c.v;
-      const bf16 *src = reinterpret_cast<const bf16 *>(vals ? a.c.v : a.c.k) + f.kvh * (vals ? a.c.v_head : a.c.k_head) + cc * 8;
-      const int64_t st_page = vals ? a.c.v_page : a.c.k_page, st_row = vals ? a.c.v_row : a.c.k_row;
-      const int buf = s % NST;
-      uint32_t there[kW], all = 0xffffffffu;  // positions that are there
-#pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        const uint32_t p = f.at + 32 * k + lane;
-        const bool in = p >= (uint32_t)f.begin && p < (uint32_t)f.end, good = in && f.page[k] >= 0 && f.page[k] < a.c.n_pages;
-        if (in && !good) atomicOr(a.status, kStatusBadIndex);
-        all &= there[k] = __ballot_sync(0xffffffffu, good);
-      }
-      if (s >= NST && !warp_wait(&empty[buf], (uint32_t)((s / NST - 1) & 1), abort_flag)) break;
-      if (!f.values && lane == 0)
-#pragma unroll
-        for (int k = 0; k < kW; ++k) masks[4 * (f.tile & (kNote - 1)) + k] = there[k];
-      if (G.box_rows && all == 0xffffffffu) {
-        // A whole tile: by TMA, a lane a box.
-        const int R = G.box_rows, first = lane * R;
-        int page = 0;
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------------------ copies: a warp every second or third stage
+      // The pages of a warp's next stage are looked up while its copies are in flight.
+      const int lw = warp - kSoft - S::kMma, cc = lane & 7;
+      Walk<KVT, false> w;
+      begin(w);
+      bool more = w.first(false);
+      struct Look {
+        int page[kW];
+        uint32_t at;     // first position
+        int kvh, seg, begin, end, tile;
+        bool values;
+      };
+      int s = lw, x = lw, tile0 = 0;  // stage, stage of the item, first tile of the item
+      auto look = [&](Look &f) __attribute__((always_inline)) -> bool {
+        while (more && x >= 2 * (w.u1 - w.u0)) {
+          x -= 2 * (w.u1 - w.u0);
+          tile0 += w.u1 - w.u0;
+          more = w.next(false);
+        }
+        if (!more) return false;
+        const Item &d = w.d;
+        f.at = (uint32_t)(w.kt0 + w.u0 + (x >> 1)) * KVT;
+        f.values = x & 1;
+        f.kvh = w.kvh;
+        f.begin = d.begin;
+        f.end = d.end;
+        f.seg = d.seg;
+        f.tile = tile0 + (x >> 1);
 #pragma unroll
         for (int k = 0; k < kW; ++k) {
-          const int x0 = __shfl_sync(0xffffffffu, f.page[k], first & 31);
-          if ((first >> 5) == k) page = x0;
+          const uint32_t p = f.at + 32 * k + lane;
+          const bool in = p >= (uint32_t)d.begin && p < (uint32_t)d.end;
+          f.page[k] = in ? a.table[(int64_t)d.seg * a.width + P.page.div(p)] : 0;
         }
-        if (lane == 0) tc::mbar_expect_tx(&full[buf], S::kStage);
-        __syncwarp();
-        if (first < KVT) {
-          const uint32_t p = f.at + first;
-          const int row = (int)(p - P.page.div(p) * P.page.d);
+        return true;
+      };
+      Look f{};
+      if (G.box_rows && lane == 0) {
+        tc::prefetch_tmap(&G.k);
+        if (a.c.v) tc::prefetch_tmap(&G.v);
+      }
+      for (bool begun = false, have = true; have; begun = true) {  // (from the second round on with a stage to fill)
+        const uint32_t dst = s_ring + (s % NST) * S::kStage + (lane >> 3) * 128;
+        const int cur = s;
+        bool copied = false;  // by cp.async
+        if (begun) {
+          const bool vals = f.values && a.c.v;
+          const bf16 *src = reinterpret_cast<const bf16 *>(vals ? a.c.v : a.c.k) + f.kvh * (vals ? a.c.v_head : a.c.k_head) + cc * 8;
+          const int64_t st_page = vals ? a.c.v_page : a.c.k_page, st_row = vals ? a.c.v_row : a.c.k_row;
+          const int buf = s % NST;
+          uint32_t there[kW], all = 0xffffffffu;  // positions that are there
 #pragma unroll
-          for (int kb = 0; kb < NP; ++kb)
-            tc::tma_load_4d(s_ring + buf * S::kStage + kb * (KVT * 128) + first * 128, vals ? &G.v : &G.k, &full[buf], kb * 64, f.kvh, row,
-                            page);
-        }
-        if (lane != 0) tc::mbar_arrive(&full[buf]);
-      } else {
-      copied = true;
-      const int rows = tile_rows<KVT>(f.end, (int)(f.at / KVT));
+          for (int k = 0; k < kW; ++k) {
+            const uint32_t p = f.at + 32 * k + lane;
+            const bool in = p >= (uint32_t)f.begin && p < (uint32_t)f.end, good = in && f.page[k] >= 0 && f.page[k] < a.c.n_pages;
+            if (in && !good) atomicOr(a.status, kStatusBadIndex);
+            all &= there[k] = __ballot_sync(0xffffffffu, good);
+          }
+          if (s >= NST && !warp_wait(&empty[buf], (uint32_t)((s / NST - 1) & 1), abort_flag)) break;
+          if (!f.values && lane == 0)
+#pragma unroll
+            for (int k = 0; k < kW; ++k) masks[4 * (f.tile & (kNote - 1)) + k] = there[k];
+          if (G.box_rows && all == 0xffffffffu) {
+            // A whole tile: by TMA, a lane a box.
+            const int R = G.box_rows, first = lane * R;
+            int page = 0;
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+              const int x0 = __shfl_sync(0xffffffffu, f.page[k], first & 31);
+              if ((first >> 5) == k) page = x0;
+            }
+            if (lane == 0) tc::mbar_expect_tx(&full[buf], S::kStage);
+            __syncwarp();
+            if (first < KVT) {
+              const uint32_t p = f.at + first;
+              const int row = (int)(p - P.page.div(p) * P.page.d);
+#pragma unroll
+              for (int kb = 0; kb < NP; ++kb)
+                tc::tma_load_4d(s_ring + buf * S::kStage + kb * (KVT * 128) + first * 128, vals ? &G.v : &G.k, &full[buf], kb * 64, f.kvh, row,
+                                page);
+            }
+            if (lane != 0) tc::mbar_arrive(&full[buf]);
+          } else {
+            copied = true;
+            const int rows = tile_rows<KVT>(f.end, (int)(f.at / KVT));
 #pragma unroll 1
-      for (int k = 0; 32 * k < rows; ++k) {  // (rolled: four times the code would be fetched anew for every stage)
-        int page = f.page[0];
-        uint32_t good = there[0];
+            for (int k = 0; 32 * k < rows; ++k) {  // (rolled: four times the code would be fetched anew for every stage)
+              int page = f.page[0];
+              uint32_t good = there[0];
 #pragma unroll
-        for (int e = 1; e < kW; ++e)
-          if (k == e) page = f.page[e], good = there[e];
-        const uint32_t p = f.at + 32 * k + lane;
-        const int64_t off = (good >> lane) & 1u ? page * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
+              for (int e = 1; e < kW; ++e)
+                if (k == e) page = f.page[e], good = there[e];
+              const uint32_t p = f.at + 32 * k + lane;
+              const int64_t off = (good >> lane) & 1u ? page * st_page + (int64_t)(p - P.page.div(p) * P.page.d) * st_row : -1;
 #pragma unroll 2
-        for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes 128 bytes of a row
-          if (32 * k + 4 * i >= rows) break;
-          const int r7 = (4 * i + (lane >> 3)) & 7;
-          const int64_t o = __shfl_sync(0xffffffffu, off, 4 * i + (lane >> 3));
+              for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes 128 bytes of a row
+                if (32 * k + 4 * i >= rows) break;
+                const int r7 = (4 * i + (lane >> 3)) & 7;
+                const int64_t o = __shfl_sync(0xffffffffu, off, 4 * i + (lane >> 3));
 #pragma unroll
-          for (int kb = 0; kb < NP; ++kb) {
-            const bool in = o >= 0 && kb * 64 + cc * 8 < hd;
-            attn::cp_async16(dst + kb * (KVT * 128) + k * 4096 + i * 512 + ((cc ^ r7) << 4), in ? src + o + kb * 64 : src, in);
+                for (int kb = 0; kb < NP; ++kb) {
+                  const bool in = o >= 0 && kb * 64 + cc * 8 < hd;
+                  attn::cp_async16(dst + kb * (KVT * 128) + k * 4096 + i * 512 + ((cc ^ r7) << 4), in ? src + o + kb * 64 : src, in);
+                }
+              }
+            }
+          }
+          s += S::kLoad;
+          x += S::kLoad;
+        }
+        have = look(f);
+        if (!copied) continue;
+        attn::cp_async_wait_all();
+        attn::fence_proxy_async();
+        tc::mbar_arrive(&full[cur % NST]);
+      }
+      attn::cp_async_wait_all();
+      // Nothing is in flight when the CTA ends.  The products wait for every stage; after a wait that ran out, they do not.
+      if (*abort_flag)
+        for (int i = s - S::kLoad; i >= 0 && i > s - S::kLoad - NST; i -= S::kLoad) {
+          const uint64_t t1 = tc::global_ns();
+          while (!tc::mbar_try_wait(&full[i % NST], (uint32_t)((i / NST) & 1)) && tc::global_ns() - t1 < 10000000) {
           }
         }
-      }
-      }
-      s += S::kLoad;
-      x += S::kLoad;
-      }
-      have = look(f);
-      if (!copied) continue;
-      attn::cp_async_wait_all();
-      attn::fence_proxy_async();
-      tc::mbar_arrive(&full[cur % NST]);
-    }
-    attn::cp_async_wait_all();
-    // Nothing is in flight when the CTA ends.  The products wait for every stage; after a wait that ran out, they do not.
-    if (*abort_flag)
-      for (int i = s - S::kLoad; i >= 0 && i > s - S::kLoad - NST; i -= S::kLoad) {
-        const uint64_t t1 = tc::global_ns();
-        while (!tc::mbar_try_wait(&full[i % NST], (uint32_t)((i / NST) & 1)) && tc::global_ns() - t1 < 10000000) {
-        }
-      }
     }
   }
   tc::tc_fence_before();
@@ -1240,7 +1262,8 @@ cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
   if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
   if (e != cudaSuccess || one) return e;
   // blocks of the join: a thread a quarter of 16 features; more of them an item where items are few, and so split over many CTAs
-  const int64_t all = (int64_t)TR * HDP / 4 / kJoinThreads, y = std::min(all, std::max<int64_t>(4, 8 * num_sms / std::min<int64_t>(cap * a.c.kv_heads, grid)));
+  const int64_t all = (int64_t)TR * HDP / 4 / kJoinThreads, few = std::min<int64_t>(cap * a.c.kv_heads, grid);
+  const int64_t y = std::min(all, std::max<int64_t>(4, 8 * num_sms / few));
   return launch_dependent(k_rows_join<HDP>, dim3(grid, (unsigned)y), dim3(kJoinThreads), 0, s, 1, p, grid);
 }
 
