@@ -99,9 +99,12 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   __shared__ Rows rows;
   __shared__ Range rg;
-  dependency_wait();
+  if constexpr (!PART) dependency_wait();  // (a part's kernel starts when that has happened, and waits for the plan at its end)
   const int nunits = find_range<kUnit, kThreads, false, kEnd, false>(P, s_scan, rows, rg);
-  if (nunits <= 0) return;
+  if (nunits <= 0) {
+    if constexpr (PART) dependency_wait();
+    return;
+  }
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
   Cursor cl = first_unit<kUnit, false, kEnd>(a, P.Hg, rg, rows), cc = cl;  // of the lookups, of the products
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (PART) dependency_wait();
 }
 
 template <int HD, int NH, bool PART>
@@ -433,7 +437,8 @@ cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cuda
   // no more CTAs than there can be units
   const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
   const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + S::kUnit - 1) / S::kUnit);
-  const int64_t grid = std::min<int64_t>(std::min(units, (int64_t)num_sms * S::kCtas), kMaxCtas);
+  // (a part's grid leaves room for the plan's one CTA, which runs when it starts)
+  const int64_t grid = std::min<int64_t>(std::min(units, (int64_t)num_sms * S::kCtas - PART), kMaxCtas);
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * NH * HD;
   if (sizeof(float) * 2 * grid * NH * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;

@@ -29,7 +29,7 @@
 // tiles of rows and a tile of positions (2048 by the measured peak: two products read q and the keys from shared memory at
 // 128 bytes a cycle, all of its rate), with the softmax 3400.  16384 tokens of 64 heads over 8 of 128: 3.32 ms, 1325 TFLOP/s, 69 % of
 // the measured bf16 rate (77 % of the sustained one); 12 ragged prompts of 100 to 4000 tokens (32 over 8 of 128) 311 us, 45 %:
-// the ends of their items.  256 rows behind 32768 shared ones (64 over 8 of 128) 355 us, of which their own pages take 115.
+// the ends of their items.  256 rows behind 32768 shared ones (64 over 8 of 128) 353 us, of which their own pages take 115.
 #include <algorithm>
 #include <cstring>
 
@@ -136,6 +136,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
   const int tid = threadIdx.x;
   const int64_t cap = min((int64_t)a.width * a.c.page, (int64_t)0x7fffffff);
   dependency_wait();
+  // What comes next may start: the rows' own pages, which need nothing of this kernel (k_paged_attn waits for it when it is done), or
+  // k_rows_attn's start, up to its own wait.  (64 rows of 40 to 700 own positions behind 8192: 57.7 -> 53.5 us, 2 x 500 22.9 -> 20.9.)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned long long places = 0;
   int items = 0;
   bool full = false;
@@ -1217,8 +1220,15 @@ struct Room {
   }
 };
 
+// The launch of the rows' own pages.
+struct Own {
+  PagedAttnArgs a;
+  float *shares;
+  int *counters;
+};
+
 template <int HDP>
-cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
+cudaError_t launch(Params p, Room room, const Own *own, int num_sms, cudaStream_t s) {
   using S = Shape<HDP>;
   const RowsAttnArgs &a = p.a;
   constexpr int TR = S::QT * kSub;
@@ -1259,6 +1269,7 @@ cudaError_t launch(Params p, Room room, int num_sms, cudaStream_t s) {
       maps.box_rows = box;
   }
   e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
+  if (e == cudaSuccess && own) e = launch_paged_attn(own->a, own->shares, kPagedShareBytes, own->counters, num_sms, s);
   if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
   if (e != cudaSuccess || one) return e;
   // blocks of the join: a thread a quarter of 16 features; more of them an item where items are few, and so split over many CTAs
@@ -1286,8 +1297,9 @@ cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, 
   p.scale_log2 = (float)(a.scale * 1.4426950408889634);
   p.wide = ((uintptr_t)a.o | (uintptr_t)(a.o_t * 2) | (uintptr_t)(a.c.head_dim * 2)) % 32 == 0;
   rows::Room room{reinterpret_cast<uint8_t *>(ws), reinterpret_cast<uint8_t *>(ws) + ws_bytes};
+  rows::Own own{};
   if (a.pos) {  // the rows' own pages
-    PagedAttnArgs o{};
+    PagedAttnArgs &o = own.a;
     o.q = a.q;
     o.q_t = a.q_t;
     o.N = a.N;
@@ -1301,22 +1313,17 @@ cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, 
     o.scale = a.scale;
     o.window = a.window;
     o.status = a.status;
-    float *own = room.take<float>((size_t)a.N * a.H * a.c.head_dim);
-    float2 *ml = room.take<float2>((size_t)a.N * a.H);
-    float *shares = room.take<float>(kPagedShareBytes / 4);
-    if (room.at > room.end) return cudaErrorInvalidValue;
-    o.part_o = own;
-    o.part_ml = ml;
-    const cudaError_t e = launch_paged_attn(o, shares, kPagedShareBytes, counters, num_sms, s);
-    if (e != cudaSuccess) return e;
-    p.own_o = own;
-    p.own_ml = ml;
+    p.own_o = o.part_o = room.take<float>((size_t)a.N * a.H * a.c.head_dim);
+    p.own_ml = o.part_ml = room.take<float2>((size_t)a.N * a.H);
+    own.shares = room.take<float>(kPagedShareBytes / 4);
+    own.counters = counters;
   }
+  const rows::Own *own_pages = a.pos ? &own : nullptr;
   const int hd = a.c.head_dim;
-  if (hd <= 64) return rows::launch<64>(p, room, num_sms, s);
-  if (hd <= 128) return rows::launch<128>(p, room, num_sms, s);
-  if (hd <= 192) return rows::launch<192>(p, room, num_sms, s);
-  return rows::launch<256>(p, room, num_sms, s);
+  if (hd <= 64) return rows::launch<64>(p, room, own_pages, num_sms, s);
+  if (hd <= 128) return rows::launch<128>(p, room, own_pages, num_sms, s);
+  if (hd <= 192) return rows::launch<192>(p, room, own_pages, num_sms, s);
+  return rows::launch<256>(p, room, own_pages, num_sms, s);
 }
 
 }  // namespace csa
