@@ -85,7 +85,7 @@ __device__ __forceinline__ int swizzle(int h) {
   return (NH == 8 ? (h >> 1) & 3 : h & 3) << 3;
 }
 
-template <int HD, int NH, bool PART>
+template <int HD, int NH, int MODE>
 __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCtas)) k_paged_attn(const __grid_constant__ Params P) {
   using S = Shape<HD, NH>;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kUnit = S::kUnit, kHeads = NH;
@@ -99,10 +99,11 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   __shared__ Rows rows;
   __shared__ Range rg;
-  if constexpr (!PART) dependency_wait();  // (a part's kernel starts when that has happened, and waits for the plan at its end)
+  constexpr bool PART = MODE == kPart, kBeside = MODE != kRow;
+  if constexpr (!kBeside) dependency_wait();  // (beside k_rows_plan, which has waited, only for the plan, at the end)
   const int nunits = find_range<kUnit, kThreads, false, kEnd, false>(P, s_scan, rows, rg);
   if (nunits <= 0) {
-    if constexpr (PART) dependency_wait();
+    if constexpr (kBeside) dependency_wait();
     return;
   }
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       advance<kUnit, false, kEnd>(a, P.Hg, rows, cl);
       if (warp == 0 && todo > 0 && (cl.hg != hg0 || cl.n != n0)) {  // the next segment's q on its way to L1
         const int kv2 = cl.hg / P.sub, sg = cl.hg - kv2 * P.sub, nq = min(NH, P.g - sg * NH);
-        const bf16 *q = a.q + (int64_t)cl.n * a.q_t + (int64_t)(kv2 * P.g + sg * NH) * hd;
+        const bf16 *q = a.q + (int64_t)token_of<MODE>(a, cl.n) * a.q_t + (int64_t)(kv2 * P.g + sg * NH) * hd;
         for (int i = lane * 64; i < nq * hd; i += 32 * 64) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
       }
     }
@@ -184,14 +185,15 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   constexpr int QR = NH == 16 ? 4 : 2, AT = NH == 16 ? HD / 8 : HD / 16;
   uint32_t qf[S::kQShared ? 1 : HD / 16][QR];
   float acc[AT][4], m[2], l[2];  // m, l: of heads qr, qr + 8 (NH 16) or qc, qc + 1 (NH 8); l of this thread's positions
-  int h0 = 0, nh = 0;
+  int h0 = 0, nh = 0, tok = 0;
   int seg = 0;  // the CTA's first unit of the current segment
   const int qr = lane >> 2, qc = 2 * (lane & 3);
   auto begin_segment = [&]() {
     const int kvh = cc.hg / P.sub, sg = cc.hg - kvh * P.sub;
     h0 = kvh * P.g + sg * kHeads;
     nh = min(kHeads, P.g - sg * kHeads);
-    const bf16 *q = a.q + (int64_t)cc.n * a.q_t + (int64_t)h0 * hd;
+    tok = token_of<MODE>(a, cc.n);
+    const bf16 *q = a.q + (int64_t)tok * a.q_t + (int64_t)h0 * hd;
     if constexpr (S::kQShared) {  // (between two barriers: the one before this, and this one)
       for (int i = tid; i < NH * (HD / 8); i += kThreads) {
         const int h = i / (HD / 8), ch = i % (HD / 8);
@@ -370,10 +372,10 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
           L = fmaf(s_ml[1][w][tid], f, L);
         }
         if (PART && whole) {
-          a.part_ml[(int64_t)cc.n * a.H + h0 + tid] = make_float2(M, L);
+          a.part_ml[(int64_t)tok * a.H + h0 + tid] = make_float2(M, L);
         } else if (whole) {
           s_out[tid] = out_factor(M, L, a.sink, h0 + tid);
-          if (a.lse) a.lse[(int64_t)cc.n * a.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          if (a.lse) a.lse[(int64_t)tok * a.H + h0 + tid] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         } else {
           *reinterpret_cast<float2 *>(P.share_ml + ((int64_t)slot * kHeads + tid) * 2) = make_float2(M, L);
         }
@@ -394,10 +396,10 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
           v.w = fmaf(x.w, f, v.w);
         }
         if (PART && whole) {
-          *reinterpret_cast<float4 *>(a.part_o + ((int64_t)cc.n * a.H + h0 + h) * hd + d) = v;
+          *reinterpret_cast<float4 *>(a.part_o + ((int64_t)tok * a.H + h0 + h) * hd + d) = v;
         } else if (whole) {
           const float f = s_out[h];
-          *reinterpret_cast<uint2 *>(a.o + (int64_t)cc.n * a.o_t + (int64_t)(h0 + h) * hd + d) =
+          *reinterpret_cast<uint2 *>(a.o + (int64_t)tok * a.o_t + (int64_t)(h0 + h) * hd + d) =
               make_uint2(bits(__floats2bfloat162_rn(v.x * f, v.y * f)), bits(__floats2bfloat162_rn(v.z * f, v.w * f)));
         } else {
           *reinterpret_cast<float4 *>(P.share_o + ((int64_t)slot * kHeads + h) * HD + d) = v;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
       if (!whole) {
         int c0;
         const int parts = sharers(rg, cc, c0);
-        publish<kHeads, HD, kThreads, PART>(P, c0, parts, cc.n, h0, nh, &s_flag);
+        publish<kHeads, HD, kThreads, PART>(P, c0, parts, tok, h0, nh, &s_flag);
       }
       if (u + 1 < nunits) {
         advance<kUnit, false, kEnd>(a, P.Hg, rows, cc);
@@ -422,14 +424,14 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (PART) dependency_wait();
+  if constexpr (kBeside) dependency_wait();
 }
 
-template <int HD, int NH, bool PART>
+template <int HD, int NH, int MODE>
 cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   using S = Shape<HD, NH>;
   static SmemAttr attr;
-  cudaError_t e = attr.ensure((const void *)k_paged_attn<HD, NH, PART>, S::kSmem);
+  cudaError_t e = attr.ensure((const void *)k_paged_attn<HD, NH, MODE>, S::kSmem);
   if (e != cudaSuccess) return e;
   const PagedAttnArgs &a = p.a;
   p.sub = (p.g + NH - 1) / NH;
@@ -437,19 +439,25 @@ cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cuda
   // no more CTAs than there can be units
   const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
   const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + S::kUnit - 1) / S::kUnit);
-  // (a part's grid leaves room for the plan's one CTA, which runs when it starts)
-  const int64_t grid = std::min<int64_t>(std::min(units, (int64_t)num_sms * S::kCtas - PART), kMaxCtas);
+  // (room for the plan's one CTA, where that runs when this starts)
+  const int64_t grid = std::min<int64_t>(std::min(units, (int64_t)num_sms * S::kCtas - (MODE != kRow)), kMaxCtas);
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * NH * HD;
   if (sizeof(float) * 2 * grid * NH * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;
-  return launch_dependent(k_paged_attn<HD, NH, PART>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, 1, p);
+  return launch_dependent(k_paged_attn<HD, NH, MODE>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, 1, p);
+}
+template <int HD, int MODE>
+cudaError_t launch_mode(const Params &p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+  if (p.g <= 8) return launch_heads<HD, 8, MODE>(p, ws, ws_bytes, num_sms, s);
+  if constexpr (MODE != kSegment) return launch_heads<HD, 16, MODE>(p, ws, ws_bytes, num_sms, s);
+  return cudaErrorInvalidValue;
 }
 template <int HD>
 cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   p.g = p.a.H / p.a.c.kv_heads;
-  if (p.a.part_o)
-    return p.g <= 8 ? launch_heads<HD, 8, true>(p, ws, ws_bytes, num_sms, s) : launch_heads<HD, 16, true>(p, ws, ws_bytes, num_sms, s);
-  return p.g <= 8 ? launch_heads<HD, 8, false>(p, ws, ws_bytes, num_sms, s) : launch_heads<HD, 16, false>(p, ws, ws_bytes, num_sms, s);
+  return p.a.cu       ? launch_mode<HD, kSegment>(p, ws, ws_bytes, num_sms, s)
+         : p.a.part_o ? launch_mode<HD, kPart>(p, ws, ws_bytes, num_sms, s)
+                      : launch_mode<HD, kRow>(p, ws, ws_bytes, num_sms, s);
 }
 
 // (head_dim above 256: k_paged_attn_tc.cu)

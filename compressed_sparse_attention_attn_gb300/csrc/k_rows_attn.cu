@@ -17,7 +17,8 @@
 // A plan kernel lists the items with the number of their position tiles (k_rows_plan); the tiles of all items and kv heads stand one
 // behind the other, with places for each item's end, and each CTA takes an equal part of them in a row, so every CTA has as much to do
 // as any other whatever the lengths and masks are.  An item that several CTAs worked on is joined from their shares (M, L, O), in the
-// order of the CTAs, by k_rows_join.  The rows of a prefix batch's own pages come from k_paged_attn as one more share.
+// order of the CTAs, by k_rows_join.  The rows of a prefix batch's own pages come from k_paged_attn as one more share, and it takes a
+// prompt batch's requests of one token (single_tokens below); it runs beside the plan.
 //
 // A CTA an SM: four warps a tile of rows for the softmax and the results, a warp that issues its products, and the copies (whole
 // tiles by TMA, boxes of up to 128 rows inside a page where pages hold whole boxes of 8 rows at least; ragged tiles and other pages by
@@ -29,7 +30,7 @@
 // tiles of rows and a tile of positions (2048 by the measured peak: two products read q and the keys from shared memory at
 // 128 bytes a cycle, all of its rate), with the softmax 3400.  16384 tokens of 64 heads over 8 of 128: 3.32 ms, 1325 TFLOP/s, 69 % of
 // the measured bf16 rate (77 % of the sustained one); 12 ragged prompts of 100 to 4000 tokens (32 over 8 of 128) 311 us, 45 %:
-// the ends of their items.  256 rows behind 32768 shared ones (64 over 8 of 128) 353 us, of which their own pages take 115.
+// the ends of their items.  64 decodes of 1 to 5000 beside two prompts (40 over 8 of 80) 101 us.  256 rows behind 32768 shared ones (64 over 8 of 128) 353 us, of which their own pages take 115.
 #include <algorithm>
 #include <cstring>
 
@@ -79,6 +80,7 @@ struct Params {
   float *share_o;              // [2 ctas][QT * 128][HDP]
   float4 *share_ml;            // [2 ctas][QT * 128]: M, L of the rounded weights, L
   int4 *split;                 // [ctas]: the item that began in this CTA and goes on behind it: item, kv head, CTAs
+  bool single;                 // prompts: segments of one token are k_paged_attn's
   const float *own_o;          // prefix: [N][H][head_dim], the share of each row's own pages
   const float2 *own_ml;        // [N][H]: M, L
 };
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
   const int tid = threadIdx.x;
   const int64_t cap = min((int64_t)a.width * a.c.page, (int64_t)0x7fffffff);
   dependency_wait();
-  // What comes next may start: the rows' own pages, which need nothing of this kernel (k_paged_attn waits for it when it is done), or
+  // What comes next may start: k_paged_attn over the rows' own pages or the segments of one token, which needs nothing of this kernel (and waits for it at its end), or
   // k_rows_attn's start, up to its own wait.  (64 rows of 40 to 700 own positions behind 8192: 57.7 -> 53.5 us, 2 x 500 22.9 -> 20.9.)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned long long places = 0;
@@ -160,6 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
         if (a.pos) len = max(len, 0);
       }
       if (bad) atomicOr(a.status, kStatusBadIndex);
+      if (n == 1 && P.single) n = 0;
     }
     unsigned long long sum;
     const unsigned long long tiles = n > 0 ? ((unsigned long long)n * P.g.d + TR - 1) / TR : 0;
@@ -336,7 +339,8 @@ __device__ __forceinline__ int tile_rows(int end, int j) {
 }
 
 // The first row of the item that the warps of tile of rows t have, -1: none.  An item of no more than 128 rows is tile 0's or tile 1's
-// by turns, so that the end of one and the beginning of the next pass beside each other (a mixed step of 64 decodes 125 against 127 us).
+// by turns, so that the end of one and the beginning of the next pass beside each other (64 decodes and two
+// prompts, with the decodes as items here: 125 against 127 us).
 template <int KVT, bool SLOT>
 __device__ __forceinline__ int sub_rows(const Walk<KVT, SLOT> &w, int t, bool two) {
   if (!two) return 0;
@@ -1220,15 +1224,15 @@ struct Room {
   }
 };
 
-// The launch of the rows' own pages.
-struct Own {
+// What runs beside the plan: the rows' own pages, or the segments of one token.
+struct Beside {
   PagedAttnArgs a;
   float *shares;
   int *counters;
 };
 
 template <int HDP>
-cudaError_t launch(Params p, Room room, const Own *own, int num_sms, cudaStream_t s) {
+cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaStream_t s) {
   using S = Shape<HDP>;
   const RowsAttnArgs &a = p.a;
   constexpr int TR = S::QT * kSub;
@@ -1269,7 +1273,7 @@ cudaError_t launch(Params p, Room room, const Own *own, int num_sms, cudaStream_
       maps.box_rows = box;
   }
   e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
-  if (e == cudaSuccess && own) e = launch_paged_attn(own->a, own->shares, kPagedShareBytes, own->counters, num_sms, s);
+  if (e == cudaSuccess && beside) e = launch_paged_attn(beside->a, beside->shares, kPagedShareBytes, beside->counters, num_sms, s);
   if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
   if (e != cudaSuccess || one) return e;
   // blocks of the join: a thread a quarter of 16 features; more of them an item where items are few, and so split over many CTAs
@@ -1280,12 +1284,18 @@ cudaError_t launch(Params p, Room room, const Own *own, int num_sms, cudaStream_
 
 }  // namespace rows
 
+// Whether a prompt batch's segments of one token go to k_paged_attn.  Up to 8 query heads a kv head it takes half the time over them
+// (a step of nothing else, with the launches that then find nothing to do: 64 of up to 5000 positions, 32 heads over 8 of 128, 43
+// against 74 us; 64 of 100 to 3000, 32 over 8 of 64, 37, 73; 4 x 8000, 32 over 8 of 128, 40, 43).  With 16 it does not (32 of 2000 to
+// 8000, 32 over 2 of 128: 48 against 46 us; 16 of 3000 to 9000, 32 over 2 of 256: 64, 51).  A batch of one prompt has none.
+static bool single_tokens(const RowsAttnArgs &a) { return !a.pos && a.H / a.c.kv_heads <= 8 && (a.S > 1 || a.N == 1); }
+
 // Bytes of workspace that launch_rows_attn needs (an upper bound).
 size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms) {
   const size_t hd = (size_t)(a.c.head_dim + 63) / 64 * 64, items = (size_t)a.N * (a.H / a.c.kv_heads) / 128 + 1 + a.S;
   const size_t shares = (size_t)2 * num_sms * (hd == 256 ? 128 : 256) * (hd * 4 + 16);
-  const size_t own = a.pos ? (size_t)a.N * a.H * (a.c.head_dim * 4 + 8) + kPagedShareBytes : 0;
-  return items * 56 + shares + own + (num_sms + 1) * 112 + 8192;
+  const size_t own = a.pos ? (size_t)a.N * a.H * (a.c.head_dim * 4 + 8) : 0;
+  return items * 56 + shares + own + (a.pos || single_tokens(a) ? kPagedShareBytes : 0) + (num_sms + 1) * 112 + 8192;
 }
 
 cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s) {
@@ -1297,33 +1307,47 @@ cudaError_t launch_rows_attn(const RowsAttnArgs &a, float *ws, size_t ws_bytes, 
   p.scale_log2 = (float)(a.scale * 1.4426950408889634);
   p.wide = ((uintptr_t)a.o | (uintptr_t)(a.o_t * 2) | (uintptr_t)(a.c.head_dim * 2)) % 32 == 0;
   rows::Room room{reinterpret_cast<uint8_t *>(ws), reinterpret_cast<uint8_t *>(ws) + ws_bytes};
-  rows::Own own{};
-  if (a.pos) {  // the rows' own pages
-    PagedAttnArgs &o = own.a;
+  rows::Beside beside{};
+  PagedAttnArgs &o = beside.a;
+  p.single = single_tokens(a);
+  if (a.pos || p.single) {
     o.q = a.q;
     o.q_t = a.q_t;
-    o.N = a.N;
     o.H = a.H;
     o.c = a.c;
-    o.table = a.own_table;
-    o.R = a.R;
-    o.width = a.own_width;
-    o.req = a.req;
-    o.pos = a.pos;
     o.scale = a.scale;
     o.window = a.window;
     o.status = a.status;
-    p.own_o = o.part_o = room.take<float>((size_t)a.N * a.H * a.c.head_dim);
-    p.own_ml = o.part_ml = room.take<float2>((size_t)a.N * a.H);
-    own.shares = room.take<float>(kPagedShareBytes / 4);
-    own.counters = counters;
+    beside.counters = counters;
+    if (a.pos) {
+      o.N = a.N;
+      o.table = a.own_table;
+      o.R = a.R;
+      o.width = a.own_width;
+      o.req = a.req;
+      o.pos = a.pos;
+      p.own_o = o.part_o = room.take<float>((size_t)a.N * a.H * a.c.head_dim);
+      p.own_ml = o.part_ml = room.take<float2>((size_t)a.N * a.H);
+    } else {
+      o.N = o.R = a.S;
+      o.table = a.table;
+      o.width = a.width;
+      o.cu = a.cu;
+      o.len = a.len;
+      o.tokens = a.N;
+      o.sink = a.sink;
+      o.o = a.o;
+      o.o_t = a.o_t;
+      o.lse = a.lse;
+    }
+    beside.shares = room.take<float>(kPagedShareBytes / 4);
   }
-  const rows::Own *own_pages = a.pos ? &own : nullptr;
+  const rows::Beside *b = a.pos || p.single ? &beside : nullptr;
   const int hd = a.c.head_dim;
-  if (hd <= 64) return rows::launch<64>(p, room, own_pages, num_sms, s);
-  if (hd <= 128) return rows::launch<128>(p, room, own_pages, num_sms, s);
-  if (hd <= 192) return rows::launch<192>(p, room, own_pages, num_sms, s);
-  return rows::launch<256>(p, room, own_pages, num_sms, s);
+  if (hd <= 64) return rows::launch<64>(p, room, b, num_sms, s);
+  if (hd <= 128) return rows::launch<128>(p, room, b, num_sms, s);
+  if (hd <= 192) return rows::launch<192>(p, room, b, num_sms, s);
+  return rows::launch<256>(p, room, b, num_sms, s);
 }
 
 }  // namespace csa

@@ -64,7 +64,13 @@ template <int U, bool ALIGN>
 __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report) {
   Row r;
   r.req = a.req ? a.req[n] : n;
-  const int pos = a.pos[n];
+  int pos;
+  if (a.cu) {
+    const int t = a.cu[n], len = a.len[n];
+    pos = t >= 0 && t < a.tokens && a.cu[n + 1] == t + 1 && len > 0 ? len - 1 : -2;
+  } else {
+    pos = a.pos[n];
+  }
   r.first = r.lead = r.rows = r.units = 0;
   if (r.req < 0 || pos < -1) return r;
   if (r.req >= a.R) {
@@ -100,6 +106,12 @@ struct Range {
   int c0, parts;         // parts > 0: all its units are of one segment, dealt over CTAs c0 .. c0 + parts - 1
   int n_units;
 };
+// What a row is: row n of q and o, the same with its share as the result, or a segment's one token.
+enum Mode { kRow, kPart, kSegment };
+template <int MODE>
+__device__ __forceinline__ int token_of(const PagedAttnArgs &a, int n) {
+  return MODE == kSegment ? a.cu[n] : n;
+}
 // The first rows of a CTA's range, kept in shared memory: the cursors read a new row there and not through two
 // dependent loads from global memory.
 constexpr int kRowsKept = 32;

@@ -365,6 +365,8 @@ CSA_API int csa_sparse_attn(csa_ctx *ctx, const csa_bf16 *q, int B, int T, int H
  *   csa_page_step      the step's tokens from the requests' lengths: request, position and slot of each
  *   csa_qk_norm_rope   their query and key heads normed and turned, key and value rows into their slots
  *   csa_paged_attn     each token's attention over its request's rows 0 .. position
+ *                      (or csa_prompt_attn where requests have several new tokens, whose rows are then read once for all of them,
+ *                      or csa_prefix_attn where rows share a prefix)
  * and nothing of it is decided on the host: the three can be captured into one CUDA graph whose
  * replays serve successive steps (csa_page_step in place on length and state).
  * -------------------------------------------------------------------------------------------*/
@@ -454,8 +456,11 @@ CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, 
  * cache with them: row t stands at position p = length[r] - cu[r+1] + t and attends rows max(0, p+1-window) .. p of its request
  * (window 0: from 0).  cu and length are what csa_page_step leaves in cu and length_out.  Heads, scores, sink, lse, infinities, the
  * cache and the layout of q, o (which may be q itself), table, lse and sink are those of csa_paged_attn; head_dim <= 256.
- * Rows of q outside every request's are padding: nothing of them is written.  A request without tokens has no rows (its length is
- * not read).  N 0: nothing to do, q and o may be NULL.
+ * Rows of q outside every request's are padding: nothing of them is written.  A request without tokens has no rows (its length
+ * does not count).  N 0: nothing to do, q and o may be NULL.
+ * The weights enter the product with the values as one bf16 term, and the sum below O is of those, so that they add up to 1 (lse is of the
+ * f32 ones); but those of requests of one token as two, up to 8 query heads a kv head and where R > 1 or N = 1: csa_paged_attn's kernel
+ * serves these, and its bound on a call's work holds for them.
  * An infinity or NaN in the cache reaches the rows that attend it and no others.
  * Caller errors, recorded in the context's status word: a request with cu[r] < 0, cu[r] > cu[r+1], cu[r+1] > N or length[r] < n (its
  * rows are left as they were), a length past width pages (the rows past them are left out), a page id outside [0, n_pages) (its rows
@@ -473,6 +478,8 @@ CSA_API int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N,
  * pos -1: no rows of its own.  A row that attends nothing: O = 0 and lse = -inf.  pos < -1, req < 0, or a row outside cu: padding,
  * nothing of it is written.  A request's own table holds none of the prefix's pages, so csa_page_step serves it as any other; angles
  * for csa_qk_norm_rope are its table from row prefix_len on.
+ * The weights of the prefix's rows enter the product as one bf16 term, those of a row's own as two.  Rows whose own pages come to
+ * csa_paged_attn's bound on a call's work are a caller error too: what the call then writes does not count.
  * The rest is as in csa_paged_attn, with head_dim <= 256; infinities and errors as in csa_prompt_attn, with prefix_len for length
  * (a negative one counts as 0) and its errors of req, pos and page ids.  N * H < 2^31. */
 CSA_API int csa_prefix_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,

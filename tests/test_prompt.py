@@ -278,6 +278,67 @@ def test_prompt_values_that_are_not_finite(csa, ctx, hd, bad):
     assert ctx.status() == 0
 
 
+@pytest.mark.parametrize("H,kv,hd,page", [(8, 1, 128, 16), (16, 2, 64, 17), (9, 1, 128, 16), (24, 8, 256, 8), (18, 2, 192, 64),
+                                          (5, 1, 80, 1), (17, 1, 256, 16)])
+@pytest.mark.parametrize("window,sink", [(0, False), (150, True)])
+def test_prompt_single_tokens(csa, ctx, H, kv, hd, page, window, sink):
+    """Decoding requests alone, one behind padding, among chunks and prompts, on both sides of 8 heads a key head; the rows
+    that a window hides hold nothing that counts."""
+    for lens, new, pad in (([700], [1], 0), ([700], [1], 5), ([1], [1], 3), ([1, 2, 33, 0, 5000, 64, 65], [1] * 3 + [0] + [1] * 3, 2),
+                           ([900, 3, 1, 400, 2000, 17], [1, 3, 1, 200, 1, 0], 0), ([129] * 90, [1, 2, 1] * 30, 7)):
+        b = Batch(lens, H, kv, hd, page, seed=len(lens) * hd + pad)
+        sw = torch.randn(H, generator=b.g, device="cuda") if sink else None
+        q, o, lse = prompt(csa, ctx, b, new, pad=pad, sink=sw, window=window)
+        check_prompt(b, new, q, o, lse, sw, window)
+        if not window:
+            continue
+        pages = {}  # (the rows before every window, not finite)
+        for r, n in enumerate(lens):
+            for j in range(max(0, n - new[r] - window + 1)):
+                pages.setdefault(int(b.table[r, j // page]), []).append(j % page)
+        for at, rows in pages.items():
+            b.k[at, rows], b.v[at, rows] = float("nan"), float("inf")
+        o2, lse2 = ctx.prompt_attn(q, csa.PagedCache(b.k, b.v), b.table, i32(cus(new)), i32(lens), b.scale, sink=sw, window=window,
+                                   with_lse=True)
+        n = sum(new)
+        assert torch.equal(o2[:n], o[:n]) and torch.equal(lse2[:n], lse[:n])
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv", [(8, 2), (9, 1)])
+def test_prompt_single_token_errors(csa, ctx, H, kv):
+    """A decoding request's length, page or place that cannot be: recorded, its row left or what is there attended, and no other's."""
+    lens, new = [300, 64, 50, 90], [1, 1, 20, 1]
+    b = Batch(lens, H, kv, 128, 16, seed=77)
+    q, cache = b.queries(sum(new) + 2), csa.PagedCache(b.k, b.v)
+
+    def run(table=b.table, cu=cus(new), lens=lens):
+        out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 3.0, device="cuda")
+        ctx.prompt_attn(q, cache, table, i32(cu), i32(lens), b.scale, out=out, lse=lse)
+        return out, lse
+
+    for le, row, rest in (([300, 0, 50, 90], 1, [0, 2, 3]), ([-5, 64, 50, 90], 0, [1, 2, 3])):
+        o, lse = run(lens=le)
+        assert ctx.status() == -1 and ctx.status() == 0
+        assert (o[row] == 3).all() and (lse[row] == 3).all()
+        check_prompt(b, new, q, o, lse, only=rest)
+    o, lse = run(cu=[0, 1, 2, 22, q.shape[0] + 1])
+    assert ctx.status() == -1 and ctx.status() == 0
+    assert (o[22:] == 3).all() and (lse[22:] == 3).all()
+    check_prompt(b, new, q, o, lse, only=[0, 1, 2])
+    o, lse = run(table=b.table[:, :10].contiguous())  # 300 positions in 160: those
+    assert ctx.status() == -1 and ctx.status() == 0
+    zero = torch.zeros(1, dtype=torch.long, device="cuda")
+    close(o[:1], lse[:1], ref(q[:1], b.rows_k[0][:160], b.rows_v[0][:160], kv, b.scale, None, zero, zero + 159), "past the table")
+    check_prompt(b, new, q, o, lse, only=[1, 2, 3])
+    t = b.table.clone()
+    t[3, 0] = -1  # no page: its rows are left out
+    o, lse = run(table=t)
+    assert ctx.status() == -1 and ctx.status() == 0
+    close(o[22:23], lse[22:23], ref(q[22:23], b.rows_k[3][16:90], b.rows_v[3][16:90], kv, b.scale, None, zero, zero + 73), "no page")
+    check_prompt(b, new, q, o, lse, only=[0, 1, 2])
+
+
 @pytest.mark.parametrize("hd", [64, 128, 256])
 def test_prompt_caller_errors(csa, ctx, hd):
     """Each is recorded, and nothing else of the call suffers."""
