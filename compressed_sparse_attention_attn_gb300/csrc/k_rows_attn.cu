@@ -1287,8 +1287,12 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
 // Whether a prompt batch's segments of one token go to k_paged_attn.  Up to 8 query heads a kv head it takes half the time over them
 // (a step of nothing else, with the launches that then find nothing to do: 64 of up to 5000 positions, 32 heads over 8 of 128, 43
 // against 74 us; 64 of 100 to 3000, 32 over 8 of 64, 37, 73; 4 x 8000, 32 over 8 of 128, 40, 43).  With 16 it does not (32 of 2000 to
-// 8000, 32 over 2 of 128: 48 against 46 us; 16 of 3000 to 9000, 32 over 2 of 256: 64, 51).  A batch of one prompt has none.
-static bool single_tokens(const RowsAttnArgs &a) { return !a.pos && a.H / a.c.kv_heads <= 8 && (a.S > 1 || a.N == 1); }
+// 8000, 32 over 2 of 128: 48 against 46 us; 16 of 3000 to 9000, 32 over 2 of 256: 64, 51).  A batch of one prompt has none, and in one of
+// 512 tokens a request or more they would be too few for the launch (6 windows of up to 6001 tokens, 16 of 256: 207 against 212 us without
+// and with it; 12 prompts of 100 to 4000: 311, 313).
+static bool single_tokens(const RowsAttnArgs &a) {
+  return !a.pos && a.H / a.c.kv_heads <= 8 && (a.S > 1 ? a.N < (int64_t)512 * a.S : a.N == 1);
+}
 
 // Bytes of workspace that launch_rows_attn needs (an upper bound).
 size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms) {
