@@ -450,7 +450,8 @@ class Context:
         """csa_prompt_attn: causal attention of each request's new tokens over the PagedCache.  Rows cu[r] .. cu[r+1]-1 of
         q [N, H, hd] (a token stride is allowed) are the newest of the length[r] rows that request r has behind table
         int32 [R, width]; cu int32 [R+1] and length int32 [R] are page_step's cu and length_out.  Decoding requests may be
-        among them; a step of nothing else is faster with paged_attn.  Rows outside every request are left as they are.  sink f32 [H].  Returns out, or (out, lse) as paged_attn does."""
+        among them; a step of nothing else is faster with paged_attn.  Rows outside every request are left as they are.
+        sink f32 [H].  Returns out, or (out, lse) as paged_attn does."""
         dev, st, out, lse, head, tail = self._rows_call(q, cache, table, "requests", out, lse, with_lse, stream)
         R, H, i32 = table.shape[0], q.shape[1], torch.int32
         _check(lib().csa_prompt_attn(*head, _vec(cu, R + 1, i32, dev, "cu"), _vec(length, R, i32, dev, "length"),
