@@ -295,7 +295,7 @@ struct Walk {
   __device__ __forceinline__ bool load() {
     if (kvh >= P->a.c.kv_heads) return false;
     const int4 *at = reinterpret_cast<const int4 *>(P->item + i);
-    return set(__ldg(at), __ldg(at + 1), __ldg(at + 2), __ldg(P->start + i));
+    return set(__ldcg(at), __ldcg(at + 1), __ldcg(at + 2), __ldcg(P->start + i));  // (this kernel may begin before the plan has written them)
   }
   __device__ __forceinline__ void step() {
     if (++i == rg->items) i = 0, ++kvh;
@@ -1262,6 +1262,7 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
   const int box = std::min(a.c.page & -a.c.page, S::KVT);
   if (box >= 8) {
     auto map = [&](CUtensorMap *m, const void *base, int64_t page, int64_t row, int64_t head) {
+      if ((a.c.kv_heads > 1 && head == 0) || (a.c.page > 1 && row == 0) || (a.c.n_pages > 1 && page == 0)) return false;  // (one for all)
       const uint64_t dims[4] = {(uint64_t)a.c.head_dim, (uint64_t)a.c.kv_heads, (uint64_t)a.c.page, (uint64_t)a.c.n_pages};
       const uint64_t one_row = 2 * (uint64_t)a.c.head_dim;  // (strides of dimensions of size 1 may be anything)
       const uint64_t strides[3] = {a.c.kv_heads > 1 ? 2 * (uint64_t)head : one_row, a.c.page > 1 ? 2 * (uint64_t)row : one_row,

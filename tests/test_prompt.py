@@ -206,6 +206,41 @@ def test_prompt_strided_rows_and_in_place(csa, ctx, H, kv, hd):
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256])
+def test_rows_that_heads_and_pages_share(csa, ctx, hd):
+    """A cache with strides of 0: one key head for all, one page, one row of a page."""
+    H, kv, page = 8, 4, 16
+    b = Batch([70, 300, 33], H, kv, hd, page, seed=hd)
+    new, cu = [70, 200, 1], i32([0, 70, 270, 271])
+    q = b.queries(271)
+    pos, prefix_len = i32([69, -1, 32]), i32([290])
+    k, v = b.k.nan_to_num(0.5), b.v.nan_to_num(0.5)
+    for shared in ([t[:, :, 1:2].expand_as(t) for t in (k, v)], [t[3:4].expand_as(t) for t in (k, v)], [t[:, 2:3].expand_as(t) for t in (k, v)]):
+        whole, flat = csa.PagedCache(*(t.contiguous() for t in shared)), csa.PagedCache(*shared)
+        for f in (lambda c: ctx.prompt_attn(q, c, b.table, cu, i32(b.lens), b.scale, with_lse=True),
+                  lambda c: ctx.prefix_attn(q[:3].contiguous(), c, b.table, pos, b.table[1:2].contiguous(), prefix_len, b.scale,
+                                            with_lse=True)):
+            (o, lse), (o2, lse2) = f(whole), f(flat)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd", [(8, 2, 128), (16, 2, 64), (6, 1, 256), (18, 2, 128)])
+def test_prompt_single_tokens_in_place(csa, ctx, H, kv, hd):
+    """Decodes and prompts whose results take the place of their queries."""
+    lens, new = [6000, 40, 1, 333, 9000, 64], [1, 40, 1, 100, 1, 0]
+    b = Batch(lens, H, kv, hd, 16, seed=3 * hd)
+    q = b.queries(sum(new) + 2)
+    o, lse = ctx.prompt_attn(q, csa.PagedCache(b.k, b.v), b.table, i32(cus(new)), i32(lens), b.scale, with_lse=True)
+    for _ in range(5):
+        p = q.clone()
+        o2, lse2 = ctx.prompt_attn(p, csa.PagedCache(b.k, b.v), b.table, i32(cus(new)), i32(lens), b.scale, out=p, with_lse=True)
+        n = sum(new)
+        assert o2 is p and torch.equal(p[:n], o[:n]) and torch.equal(lse2[:n], lse[:n]) and torch.equal(p[n:], q[n:])
+    check_prompt(b, new, q, o, lse)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
 def test_prompt_extreme_scores(csa, ctx, hd):
     """Scores of +-thousands, a scale of either sign and of 0, sinks far above and below and infinite."""
     H, kv, lens, new = 8, 2, [200, 64, 1], [200, 10, 1]
