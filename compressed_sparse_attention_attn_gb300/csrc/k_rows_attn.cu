@@ -48,7 +48,11 @@ namespace rows {
 constexpr int kSub = 128;     // rows of a product
 // Tiles that the end of an item counts for: its last tiles' masks and values looked over, the wait for the last product, results, the next
 // q, 10 thousand cycles in all where a tile takes 3.4.  (4096 tokens of 64 heads over 8 of 128: 322, 282, 276 and 280 us for 1 to 4.)
-constexpr int kEnd = 3;
+// At 256 features a tile is half as long, and one tile of rows has nothing beside its end (32 over 8 of 256, 4096 tokens: 298, 282, 265 and
+// 263 us for 3 to 6, 6 chunks behind 5000 to 30000, 16 over 2: 581, 586, 599, 606) -- but where its rows come by cp.async, tiles are longer
+// (windows in pages of 17: 209 and 218 us for 3 and 5).
+template <int HDP>
+constexpr int end_tiles(bool tma) { return HDP == 256 && tma ? 5 : 3; }
 constexpr int kMinPlaces = 2; // places a CTA has at least
 constexpr int kNote = 8;      // tiles (and items) whose notes are kept: more than the copies can be ahead
 constexpr float kRaise = 8.f;
@@ -71,6 +75,7 @@ struct Params {
   RowsAttnArgs a;
   paged::FastDiv page, g;
   float scale_log2;
+  int end_tiles;
   int wide;                    // o's rows are whole 32 bytes on such borders
   Part *part;                  // [ctas + 1] (of the last one: first)
   int ctas;
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
           it.at1 = (int)min(pos(0) + 1, cap);
         }
         mine = it.end > it.begin ? (it.end - 1) / KVT - it.begin / KVT + 1 : 1;
-        mine += kEnd;
+        mine += P.end_tiles;
       }
       const unsigned long long incl = block_scan(mine, s_sum, sum);
       if (i < all) {
@@ -1273,6 +1278,7 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
         (!a.c.v || map(&maps.v, a.c.v, a.c.v_page, a.c.v_row, a.c.v_head)))
       maps.box_rows = box;
   }
+  p.end_tiles = end_tiles<HDP>(maps.box_rows > 0);
   e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
   if (e == cudaSuccess && beside) e = launch_paged_attn(beside->a, beside->shares, kPagedShareBytes, beside->counters, num_sms, s);
   if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
