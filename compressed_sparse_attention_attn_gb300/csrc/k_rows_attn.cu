@@ -30,7 +30,8 @@
 // tiles of rows and a tile of positions (2048 by the measured peak: two products read q and the keys from shared memory at
 // 128 bytes a cycle, all of its rate), with the softmax 3400.  16384 tokens of 64 heads over 8 of 128: 3.34 ms, 1318 TFLOP/s, 68 % of
 // the measured bf16 rate (77 % of the sustained one); 12 ragged prompts of 100 to 4000 tokens (32 over 8 of 128) 311 us, 45 %:
-// the ends of their items.  64 decodes of 1 to 5000 beside two prompts (40 over 8 of 80) 100 us.  256 rows behind 32768 shared ones (64 over 8 of 128) 353 us, of which their own pages take 115.
+// the ends of their items.  64 decodes of 1 to 5000 beside two prompts (40 over 8 of 80) 100 us.  256 rows behind 32768 shared ones (64
+// over 8 of 128) 353 us, of which their own pages take 115.
 #include <algorithm>
 #include <cstring>
 
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constan
   const int tid = threadIdx.x;
   const int64_t cap = min((int64_t)a.width * a.c.page, (int64_t)0x7fffffff);
   dependency_wait();
-  // What comes next may start: k_paged_attn over the rows' own pages or the segments of one token, which needs nothing of this kernel (and waits for it at its end), or
-  // k_rows_attn's start, up to its own wait.  (64 rows of 40 to 700 own positions behind 8192: 57.7 -> 53.5 us, 2 x 500 22.9 -> 20.9.)
+  // What comes next may start: k_paged_attn over the rows' own pages or the segments of one token, which needs nothing of this
+  // kernel (and waits for it at its end), or k_rows_attn's start, up to its own wait.  (64 rows of 40 to 700 own positions behind 8192: 57.7 -> 53.5 us, 2 x 500 22.9 -> 20.9.)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   unsigned long long places = 0;
   int items = 0;
