@@ -55,7 +55,7 @@ constexpr int kSub = 128;     // rows of a product
 template <int HDP>
 constexpr int end_tiles(bool tma) { return HDP == 256 && tma ? 5 : 3; }
 constexpr int kMinPlaces = 2; // places a CTA has at least
-constexpr int kNote = 8;      // tiles (and items) whose notes are kept: more than the copies can be ahead
+constexpr int kNote = 8;      // tiles whose notes are kept: more than the copies can be ahead
 constexpr float kRaise = 8.f;
 
 // Rows row0 .. row0 + rows - 1 of the segment whose first token is tok0; positions begin .. end - 1 behind table row seg are all that
@@ -106,7 +106,7 @@ struct Shape {
   static constexpr bool kSplit = HDP <= 128;
   static constexpr int kRegsSoft = 208, kRegsRest = 88;
   static constexpr int kQ = 0, kRing = QT * kQBytes, kBars = kRing + NST * kStage;
-  static constexpr int kSlots = kBars + 32 * 8 + kNote * 16 + kNote * 4 + 128;
+  static constexpr int kSlots = kBars + 32 * 8 + kNote * 16 + 160;
   static constexpr int kSmem = kSlots + (kSoft + kMma) * 2 * 64;  // (all that the kernel has: the swizzled tiles come first)
   static constexpr int kColO = 2 * KVT;                     // columns of tensor memory: two score buffers, then QT x HDP of O
 };
@@ -542,16 +542,29 @@ __device__ __forceinline__ bool weights(float sc, float &m, float &l, float &lr,
   return true;
 }
 
+// The first and the last tile (item in the CTA, tile of its positions) that values which are not finite were taken out of.
+struct OddTiles {
+  unsigned long long first, last;
+  __device__ __forceinline__ void note(int seq, int j) {
+    const unsigned long long at = (unsigned long long)(uint32_t)seq << 32 | (uint32_t)j;
+    atomicMin(&first, at);
+    atomicMax(&last, at);
+  }
+  __device__ __forceinline__ bool any() const {
+    const volatile OddTiles &v = *this;
+    return v.first <= v.last;
+  }
+};
 // A lane's share of a tile of values, 16 bytes of every 2 KB: those that are not finite, in the tile's first `rows` rows (behind them lies
-// what was there before), become 0.
+// what was there before), become 0, and the tile (the CTA's item seq, tile j of its positions) is noted.
 template <int KVT>
-__device__ __noinline__ void clear_odd(uint32_t at, int n, int r, int rows, volatile int *odd_item, int seq) {
+__device__ __noinline__ void clear_odd(uint32_t at, int n, int r, int rows, OddTiles *odd, int seq, int j) {
   for (int i = 0; i < n; ++i, at += kSub * 16) {
     if ((i * kSub + r) / 8 % KVT >= rows) continue;
     uint32_t z[4];
     lds4(z, at);
     if (!(not_finite(z[0]) || not_finite(z[1]) || not_finite(z[2]) || not_finite(z[3]))) continue;
-    *odd_item = seq;  // (before they are gone: the other tile of rows may find them gone)
+    odd->note(seq, j);  // (before they are gone: the other tile of rows may find them gone)
     __threadfence_block();
     for (int k = 0; k < 4; ++k) {
       if ((z[k] & 0x7f80u) == 0x7f80u) z[k] &= 0xffff0000u;
@@ -587,25 +600,96 @@ __device__ __noinline__ void out_with_own(uint32_t tO, bool there, float f, cons
   }
 }
 
-// Values that are not finite were left out of tiles that not every row attends: to a row that attends positions from .. to - 1, in its
-// share or its result (whatever else is in the sum, it is not finite).
-__device__ __noinline__ void odd_values(const RowsAttnArgs &a, const paged::FastDiv &page, int seg, int kvh, int from, int to, float *share,
-                                        bf16 *o) {
-  const bf16 *vb = reinterpret_cast<const bf16 *>(a.c.v ? a.c.v : a.c.k) + kvh * (a.c.v ? a.c.v_head : a.c.k_head);
-  const int64_t st_page = a.c.v ? a.c.v_page : a.c.k_page, st_row = a.c.v ? a.c.v_row : a.c.k_row;
-  for (int p = from; p < to; ++p) {
-    const int pg = (int)page.div((uint32_t)p), id = a.table[(int64_t)seg * a.width + pg];
-    if (id < 0 || id >= a.c.n_pages) continue;
-    const uint32_t *src = reinterpret_cast<const uint32_t *>(vb + id * st_page + (int64_t)(p - pg * a.c.page) * st_row);
-    for (int c = 0; c < a.c.head_dim / 2; ++c) {
-      const uint32_t z = src[c];
-      if (!not_finite(z)) continue;
-      const float x[2] = {low(z), high(z)};
-      for (int k = 0; k < 2; ++k) {
-        if (isfinite(x[k])) continue;
-        if (share) share[2 * c + k] += x[k];
-        else if (isfinite(__bfloat162float(o[2 * c + k]))) o[2 * c + k] = __float2bfloat16(x[k]);
-        else o[2 * c + k] = __float2bfloat16(__bfloat162float(o[2 * c + k]) + x[k]);
+// Positions lo .. hi that token tok attends, as far as the segment has them.  (hi of a prefix: all.)
+__device__ __forceinline__ void span(const RowsAttnArgs &a, int tok, int shift, int &lo, int &hi) {
+  if (!a.pos) {
+    hi = tok + shift;
+    if (a.window > 0) lo = max(0, hi - a.window + 1);
+  } else if (a.window > 0) {
+    const int64_t first = (int64_t)shift + a.pos[tok] + 1 - a.window;
+    lo = (int)max((int64_t)0, min(first, (int64_t)0x7fffffff));
+  }
+}
+
+// Values that are not finite were left out of the products of tiles that not every row attends: here each is added to the rows that
+// attend it, in their shares or results (whatever else is in the sum, it is not finite).  The softmax warps come here once, behind all of
+// the CTA's items, when nothing waits for them any more, however many such tiles there are: each goes through them from the first to the last
+// with such values, for the rows that it had, a lane a row as before, 32 positions at a time.  (Loops rolled: the tile loop above is as fast as
+// its code is short and well placed; 8 loads a round here cost it 1 %.)
+template <int HDP>
+__device__ __forceinline__ void odd_values(const Params &P, const Part *rg, const OddTiles *odd) {  // (inline: a call cost a spill)
+  using S = Shape<HDP>;
+  constexpr int QT = S::QT, KVT = S::KVT;
+  const RowsAttnArgs &a = P.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, row0 = (warp & 3) * 32, hd = a.c.head_dim, g = P.g.d;
+  const unsigned long long first = odd->first, last = odd->last;
+  const bool vals = a.c.v != nullptr;
+  Walk<KVT, false> w;
+  w.P = &P;
+  w.rg = rg;
+  w.i = rg->item;
+  w.kvh = rg->kvh;
+  for (bool more = w.first(false); more && w.seq <= (int)(last >> 32); more = w.next(false)) {
+    const Item &d = w.d;
+    const int sub = sub_rows(w, t, QT == 2);
+    if (w.seq < (int)(first >> 32) || sub < 0 || sub + row0 >= d.rows) continue;
+    int x, y, lo = 0, hi = 0x7fffffff;
+    sub_range(w, t, QT == 2, x, y);
+    if (w.seq == (int)(first >> 32)) x = max(x, (int)(uint32_t)first);
+    if (w.seq == (int)(last >> 32)) y = min(y, (int)(uint32_t)last + 1);
+    const int R = sub + row0 + lane;
+    float *share = nullptr;
+    bf16 *o = nullptr;
+    if (R < d.rows) {
+      const int q = (int)P.g.div(d.row0 + R), tok = d.tok0 + q, h = w.kvh * g + (d.row0 + R - q * g);
+      span(a, tok, d.shift, lo, hi);
+      if (!w.whole()) share = P.share_o + ((int64_t)(2 * blockIdx.x + (w.u0 == 0 ? 1 : 0)) * (QT * kSub) + R) * HDP;
+      else if (row_live(a, tok)) o = a.o + (int64_t)tok * a.o_t + (int64_t)h * hd;
+    }
+    const bf16 *vb = reinterpret_cast<const bf16 *>(vals ? a.c.v : a.c.k) + w.kvh * (vals ? a.c.v_head : a.c.k_head);
+#pragma unroll 1
+    for (int j = x; j < y; ++j) {
+      if (j * KVT >= d.at0 && d.at1 - j * KVT >= KVT) {  // (tiles that all attend have theirs already)
+        j = d.at1 / KVT - 1;
+        continue;
+      }
+#pragma unroll 1
+      for (int k = 0; k < KVT; k += 32) {
+        const uint32_t p = (uint32_t)j * KVT + k + lane, pg = P.page.div(p);
+        const int id = p >= (uint32_t)d.begin && p < (uint32_t)d.end ? a.table[(int64_t)d.seg * a.width + pg] : -1;
+        const bool there = id >= 0 && id < a.c.n_pages;
+        const bf16 *src =
+            there ? vb + id * (vals ? a.c.v_page : a.c.k_page) + (int64_t)(p - pg * P.page.d) * (vals ? a.c.v_row : a.c.k_row) : vb;
+        uint32_t any = 0;
+#pragma unroll 2
+        for (int c = 0; c < hd; c += 8) {
+          const uint4 z = *reinterpret_cast<const uint4 *>(src + c);
+          any |= not_finite(z.x) || not_finite(z.y) || not_finite(z.z) || not_finite(z.w);
+        }
+        if (!__any_sync(0xffffffffu, there && any)) continue;
+#pragma unroll 1
+        for (int c = 0; c < hd; c += 8) {
+          const uint4 z = *reinterpret_cast<const uint4 *>(src + c);
+          const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+          const bool bad = there && (not_finite(z.x) || not_finite(z.y) || not_finite(z.z) || not_finite(z.w));
+          float add[8] = {};
+          for (uint32_t who = __ballot_sync(0xffffffffu, bad); who; who &= who - 1) {
+            const int by = __ffs(who) - 1, pos = j * KVT + k + by;
+            const bool here = pos >= lo && pos <= hi;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t v = __shfl_sync(0xffffffffu, u[e], by);
+              if (here && !isfinite(low(v))) add[2 * e] += low(v);
+              if (here && !isfinite(high(v))) add[2 * e + 1] += high(v);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (add[e] == 0.f) continue;
+            if (share) share[c + e] += add[e];
+            else if (o) o[c + e] = __float2bfloat16(__bfloat162float(o[c + e]) + add[e]);
+          }
+        }
       }
     }
   }
@@ -633,12 +717,11 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
   uint64_t *full = bars, *empty = bars + NST, *s_full = bars + 2 * NST, *p_full = s_full + 2, *pv_done = s_full + 4,
            *q_full = s_full + 6, *p_half = s_full + 8, *drain = s_full + 10;
   uint32_t *masks = reinterpret_cast<uint32_t *>(bars + 32);  // [kNote][4]: positions of a tile that are there
-  // [kNote]: items with a value that is not finite in a tile that not every row attends
-  volatile int *odd_item = reinterpret_cast<volatile int *>(masks + 4 * kNote);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(masks + 5 * kNote);
+  uint32_t *tmem_slot = masks + 4 * kNote;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *issue_lock = reinterpret_cast<int *>(tmem_slot + 2);
   Part &rg = *reinterpret_cast<Part *>(tmem_slot + 4);
+  OddTiles &odd = *reinterpret_cast<OddTiles *>(&rg + 1);
   static_assert(2 * NST + 11 <= 32 && NST / 2 + 2 < kNote, "barriers, notes");
 
   if (tid == 0) {
@@ -654,7 +737,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       tc::mbar_init(&q_full[b], 128);
     }
     tc::mbar_init(drain, S::kMma);
-    for (int i = 0; i < kNote; ++i) odd_item[i] = -1;
+    odd = OddTiles{~0ull, 0};
     *abort_flag = 0;
     *issue_lock = 0;
     tc::fence_barrier_init();
@@ -735,14 +818,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       const int sub = sub_rows(w, t, QT == 2);
       const bool work = sub >= 0 && sub + quad * 32 < w.d.rows;  // (of the warp)
       if (work && sub + r < w.d.rows) {
-        const int tok = w.d.tok0 + (int)P.g.div(w.d.row0 + sub + r);
-        if (!a.pos) {
-          hi = tok + w.d.shift;
-          if (a.window > 0) lo = max(0, hi - a.window + 1);
-        } else if (a.window > 0) {
-          const int64_t first = (int64_t)w.d.shift + a.pos[tok] + 1 - a.window;
-          lo = (int)max((int64_t)0, min(first, (int64_t)0x7fffffff));
-        }
+        span(a, w.d.tok0 + (int)P.g.div(w.d.row0 + sub + r), w.d.shift, lo, hi);
       }
       float m = -INFINITY, l = 0.f, lr = 0.f;
       const int note0 = tile0 - (w.kt0 + w.u0);
@@ -755,20 +831,20 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         if (at < w.d.at0 || w.d.at1 - at < KVT) {  // (at + KVT may pass 31 bits)
           // A weight of 0 does not undo a NaN: in a tile that not every row of the item attends, values that are not finite are
           // taken out before the product (by both tiles of rows, whichever comes first), and the rows that attend them get them
-          // at the end.  (Behind the scores: only then is the stage's barrier in the phase that is asked for, or the next.)
+          // at the CTA's end.  (Behind the scores: only then is the stage's barrier in the phase that is asked for, or the next.)
           const int stage = 2 * (note0 + j) + 1, rows = tile_rows<KVT>(w.d.end, j);
           if (!(ok = warp_wait(&full[stage % NST], (uint32_t)((stage / NST) & 1), abort_flag))) break;
           const uint32_t v_at = s_ring + (stage % NST) * S::kStage + r * 16;
-          uint32_t odd = 0;
+          uint32_t bits = 0;
 #pragma unroll 4
           for (int i = 0; i < S::kStage / 16 / kSub; ++i) {
             uint32_t z[4];
             lds4(z, v_at + i * (kSub * 16));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) odd |= (z[k] & 0x7f807f80u) + 0x00800080u;  // (a carry where an exponent is all ones)
+            for (int k = 0; k < 4; ++k) bits |= (z[k] & 0x7f807f80u) + 0x00800080u;  // (a carry where an exponent is all ones)
           }
-          if (__builtin_expect((odd & 0x80008000u) != 0, 0))
-            clear_odd<KVT>(v_at, S::kStage / 16 / kSub, r, rows, odd_item + (w.seq & (kNote - 1)), w.seq);
+          if (__builtin_expect((bits & 0x80008000u) != 0, 0))
+            clear_odd<KVT>(v_at, S::kStage / 16 / kSub, r, rows, &odd, w.seq, j);
           attn::fence_proxy_async();
         }
         if (work) {
@@ -818,7 +894,6 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         const int R = sub + r, q = (int)P.g.div(d.row0 + R), tok = d.tok0 + q, h = w.kvh * g + (d.row0 + R - q * g);
         const bool whole = w.whole(), mine = R < d.rows, live = mine && row_live(a, tok);
         if (m != -INFINITY) m *= sc;
-        const bool odd = y > x && odd_item[w.seq & (kNote - 1)] == w.seq;
         float f = 1.f, f_own = 0.f;
         float *share = nullptr;
         bf16 *o = nullptr;
@@ -873,11 +948,6 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
         }
         }
         tc::tc_fence_before();
-        if (__builtin_expect(odd && mine && (share || live), 0)) {
-          const int from = max(max(lo, d.begin), a.window > 0 ? 0 : d.at1 / KVT * KVT);  // (tiles that all attend have theirs already)
-          const int to = (int)min(min((int64_t)hi + 1, (int64_t)d.end), (int64_t)y * KVT);
-          odd_values(a, P.page, d.seg, w.kvh, max(from, x * KVT), to, share, o);
-        }
       }
       if (tid == 0 && w.u0 == 0 && w.u1 < w.tiles) {  // (the CTA's last item: it goes on in the next ones)
         const unsigned long long last_place = w.base + w.tiles - 1;
@@ -1145,6 +1215,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
     tc::tmem_dealloc(tmem, 512);
   }
   if (tid == 0 && *abort_flag) atomicOr(a.status, kStatusTimeout);
+  // (a share or result is its lane's own; *abort_flag: results are lost anyway)
+  if (warp < kSoft && !*abort_flag && __any_sync(0xffffffffu, odd.any())) odd_values<HDP>(P, &rg, &odd);
 }
 
 // ------------------------------------------------------------------------------------------------ joining

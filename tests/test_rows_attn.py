@@ -1,0 +1,93 @@
+"""csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows.
+
+What a call leaves is compared bit for bit with what it leaves without the value: the sums of the other rows and features do not
+change with it.
+"""
+import pytest
+import torch
+
+from test_paged import csa, ctx, gen, i32, make_ctx, randn  # noqa: F401
+from test_prompt import Prefixes
+
+pytestmark = pytest.mark.gpu
+
+
+class Far:
+    """1.2 million positions over eight pages by turns, of which two more pages hold a place each."""
+
+    page, width, N, H, window = 4096, 300, 320, 128, 2 ** 20
+
+    def __init__(self, hd, places):
+        g = gen(hd)
+        self.hd, self.rows = hd, self.page * self.width
+        self.k, self.v = (randn(g, 8 + len(places), self.page, 1, hd) for _ in range(2))
+        self.table = (torch.arange(self.width, device="cuda", dtype=torch.int32) % 8)[None].contiguous()
+        for i, p in enumerate(places):
+            self.table[0, p // self.page] = 8 + i
+        self.q = randn(g, self.N, self.H, hd)
+
+    def check(self, run, i, place, bad, hit):
+        """The value at `place`, in the i-th page of its own, reaches the rows of `hit` in its feature, and nothing else."""
+        want, want_lse = run()
+        assert want.isfinite().all()
+        at = (8 + i, place % self.page, 0, 3)
+        keep = self.v[at].clone()
+        self.v[at] = bad
+        o, lse = run()
+        self.v[at] = keep
+        assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse, want_lse)
+        assert not o[hit][..., 3].isfinite().any()
+        rest = [d for d in range(self.hd) if d != 3]
+        assert torch.equal(o[..., rest], want[..., rest])
+
+
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefix_bad_value_in_a_long_window(csa, ctx, hd, bad):
+    """More items than CTAs, windows of a million positions that begin at five different ones: a value at their edge, and one that
+    every row attends."""
+    first = Far.page * Far.width - Far.window  # of a row without rows of its own
+    places = [first + 2, 700000]
+    F = Far(hd, places)
+    own = torch.arange(F.N, device="cuda", dtype=torch.int32) % 5 - 1
+    args = (F.q, csa.PagedCache(F.k, F.v), F.table.expand(F.N, -1)[:, :1].contiguous(), own, F.table, i32([F.rows]), hd ** -0.5)
+    for i, place in enumerate(places):
+        hit = first + own + 1 <= place
+        F.check(lambda: ctx.prefix_attn(*args, window=F.window, with_lse=True), i, place, bad, hit)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_prompt_bad_value_in_a_long_window(csa, ctx, hd, bad):
+    """More items than CTAs, windows of a million positions: a value where the first ones begin, one in the middle of all, one
+    among the tokens' own rows."""
+    rows, w, N = Far.page * Far.width, Far.window, Far.N
+    places = [rows - N + 101 - w, 700000, rows - 200]
+    F = Far(hd, places)
+    pos = torch.arange(N, device="cuda") + rows - N
+    args = (F.q, csa.PagedCache(F.k, F.v), F.table, i32([0, N]), i32([rows]), hd ** -0.5)
+    for i, place in enumerate(places):
+        hit = (pos >= place) & (pos - w < place)
+        F.check(lambda: ctx.prompt_attn(*args, window=w, with_lse=True), i, place, bad, hit)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 80, 192, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefix_bad_values_in_every_tile(csa, ctx, hd, bad):
+    """A feature without one finite value, in windows that begin in the prefix: the other features keep their bits."""
+    own = [300, 40, 0, 90, 5, 7, 0, 1]
+    P = Prefixes(own, [5000], 8, 2, hd, 16, seed=4)
+    q = P.b.queries(8)
+
+    def run():
+        return ctx.prefix_attn(q, csa.PagedCache(P.k, P.v), P.table, i32([x - 1 for x in own]), P.prefix, i32([5000]), P.scale,
+                               window=4000, with_lse=True)
+
+    want, want_lse = run()
+    P.v.view(torch.int16)[..., 1] = torch.tensor([bad], dtype=torch.bfloat16).view(torch.int16).item()
+    o, lse = run()
+    assert not o[..., 1].isfinite().any() and torch.equal(lse, want_lse)
+    assert torch.equal(o[..., 2:], want[..., 2:]) and torch.equal(o[..., 0], want[..., 0])
+    assert ctx.status() == 0
