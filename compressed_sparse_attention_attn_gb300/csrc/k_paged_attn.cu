@@ -101,14 +101,14 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   __shared__ Range rg;
   constexpr bool PART = MODE == kPart, kBeside = MODE != kRow;
   if constexpr (!kBeside) dependency_wait();  // (beside k_rows_plan, which has waited, only for the plan, at the end)
-  const int nunits = find_range<kUnit, kThreads, false, kEnd, false>(P, s_scan, rows, rg);
+  const int nunits = find_range<kUnit, kThreads, false, kEnd, false, MODE>(P, s_scan, rows, rg);
   if (nunits <= 0) {
     if constexpr (kBeside) dependency_wait();
     return;
   }
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
-  Cursor cl = first_unit<kUnit, false, kEnd>(a, P.Hg, rg, rows), cc = cl;  // of the lookups, of the products
+  Cursor cl = first_unit<kUnit, false, kEnd, MODE>(a, P.Hg, rg, rows), cc = cl;  // of the lookups, of the products
   const bf16 *kbase = reinterpret_cast<const bf16 *>(a.c.k);
   const bf16 *vbase = a.c.v ? reinterpret_cast<const bf16 *>(a.c.v) : kbase;
   const int64_t v_page = a.c.v ? a.c.v_page : a.c.k_page, v_row = a.c.v ? a.c.v_row : a.c.k_row,
@@ -124,14 +124,14 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
     if (todo > 0) {
       const uint32_t j = (uint32_t)cl.t * kUnit + warp * kTile + (lane & (kTile - 1));
       f.kvh = cl.hg / P.sub;
-      const Row row = rows.get<kUnit, false>(a, cl.n);
+      const Row row = rows.get<kUnit, false, MODE>(a, cl.n);
       if (j < (uint32_t)row.rows) {
         f.pos = row.first + (int)j;
         f.page = a.table[(int64_t)row.req * a.width + P.page.div((uint32_t)f.pos)];
       }
       --todo;
       const int hg0 = cl.hg, n0 = cl.n;
-      advance<kUnit, false, kEnd>(a, P.Hg, rows, cl);
+      advance<kUnit, false, kEnd, MODE>(a, P.Hg, rows, cl);
       if (warp == 0 && todo > 0 && (cl.hg != hg0 || cl.n != n0)) {  // the next segment's q on its way to L1
         const int kv2 = cl.hg / P.sub, sg = cl.hg - kv2 * P.sub, nq = min(NH, P.g - sg * NH);
         const bf16 *q = a.q + (int64_t)token_of<MODE>(a, cl.n) * a.q_t + (int64_t)(kv2 * P.g + sg * NH) * hd;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
         publish<kHeads, HD, kThreads, PART>(P, c0, parts, tok, h0, nh, &s_flag);
       }
       if (u + 1 < nunits) {
-        advance<kUnit, false, kEnd>(a, P.Hg, rows, cc);
+        advance<kUnit, false, kEnd, MODE>(a, P.Hg, rows, cc);
         seg = u + 1;
         begin_segment();
       }

@@ -55,17 +55,25 @@ struct Params {
   int by_segment;       // `split` is by segment (no more of them than CTAs), else by first CTA
 };
 
+// What a row is: row n of q and o, the same with its share as the result, or a segment's one token.
+enum Mode { kRow, kPart, kSegment };
+template <int MODE>
+__device__ __forceinline__ int token_of(const PagedAttnArgs &a, int n) {
+  return MODE == kSegment ? a.cu[n] : n;
+}
+
 // The positions first + lead .. first + rows - 1 of row n; units of U rows from `first` on (0: a row that is left alone).
 // ALIGN: `first` is a multiple of U (with a window it may lie before the first position that counts), else lead is 0.
+// MODE: what a row is (a kSegment's request is n).
 struct Row {
   int req, first, lead, rows, units;
 };
-template <int U, bool ALIGN>
+template <int U, bool ALIGN, int MODE = kRow>
 __device__ __forceinline__ Row row_of(const PagedAttnArgs &a, int n, bool report) {
   Row r;
-  r.req = a.req ? a.req[n] : n;
+  r.req = MODE != kSegment && a.req ? a.req[n] : n;
   int pos;
-  if (a.cu) {
+  if constexpr (MODE == kSegment) {
     const int t = a.cu[n], len = a.len[n];
     pos = t >= 0 && t < a.tokens && a.cu[n + 1] == t + 1 && len > 0 ? len - 1 : -2;
   } else {
@@ -106,21 +114,15 @@ struct Range {
   int c0, parts;         // parts > 0: all its units are of one segment, dealt over CTAs c0 .. c0 + parts - 1
   int n_units;
 };
-// What a row is: row n of q and o, the same with its share as the result, or a segment's one token.
-enum Mode { kRow, kPart, kSegment };
-template <int MODE>
-__device__ __forceinline__ int token_of(const PagedAttnArgs &a, int n) {
-  return MODE == kSegment ? a.cu[n] : n;
-}
 // The first rows of a CTA's range, kept in shared memory: the cursors read a new row there and not through two
 // dependent loads from global memory.
 constexpr int kRowsKept = 32;
 struct Rows {
   int n0;
   Row row[kRowsKept];
-  template <int U, bool ALIGN>
+  template <int U, bool ALIGN, int MODE = kRow>
   __device__ __forceinline__ Row get(const PagedAttnArgs &a, int n) const {
-    return (unsigned)(n - n0) < (unsigned)kRowsKept ? row[n - n0] : row_of<U, ALIGN>(a, n, false);
+    return (unsigned)(n - n0) < (unsigned)kRowsKept ? row[n - n0] : row_of<U, ALIGN, MODE>(a, n, false);
   }
 };
 
@@ -129,7 +131,7 @@ struct Cursor {
   int n, hg, t, units;
   uint32_t base;
 };
-template <int U, bool ALIGN, int W>
+template <int U, bool ALIGN, int W, int MODE = kRow>
 __device__ __forceinline__ void advance(const PagedAttnArgs &a, int Hg, const Rows &rows, Cursor &c) {
   if (++c.t < c.units) return;
   c.t = 0;
@@ -138,7 +140,7 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, int Hg, const Ro
   c.hg = 0;
   do {
     if (++c.n >= a.N) return;  // (past the last unit: not used any more)
-    c.units = rows.get<U, ALIGN>(a, c.n).units;
+    c.units = rows.get<U, ALIGN, MODE>(a, c.n).units;
   } while (c.units == 0);
 }
 
@@ -161,7 +163,7 @@ __device__ __forceinline__ Two warp_scan(Two v, int lane) {
 // once.  WHOLE: few segments (and rows) get whole CTAs, as many as ceil(its units / q) says, if such a q close to
 // the even share exists: a CTA then has one segment's end and not two (32 latent rows of about 20 tiles: 20.9
 // against 22.6 us, 128 shares of 128 KB instead of 184; up to 256 features, where ends are cheap, one row of 8000 lost 1 us).
-template <int U, int NT, bool ALIGN, int W, bool WHOLE>
+template <int U, int NT, bool ALIGN, int W, bool WHOLE, int MODE = kRow>
 __device__ __forceinline__ int find_range(const Params &P, Two *scratch, Rows &rows, Range &out) {
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -169,7 +171,7 @@ __device__ __forceinline__ int find_range(const Params &P, Two *scratch, Rows &r
   const bool report = blockIdx.x == 0;
   auto of_row = [&](int n, Row &r) -> Two {
     r = Row{0, 0, 0, 0, 0};
-    if (n < a.N) r = row_of<U, ALIGN>(a, n, report);
+    if (n < a.N) r = row_of<U, ALIGN, MODE>(a, n, report);
     return {(uint32_t)r.units, r.units > 0 ? 1u : 0u};
   };
   auto places = [&](Two v) -> int64_t { return ((int64_t)v.units + (int64_t)W * v.segs) * Hg; };
@@ -287,7 +289,7 @@ __device__ __forceinline__ int find_range(const Params &P, Two *scratch, Rows &r
   return (int)(out.u1 - out.u0);
 }
 // The cursor at the first unit of a range that has one.
-template <int U, bool ALIGN, int W>
+template <int U, bool ALIGN, int W, int MODE = kRow>
 __device__ __forceinline__ Cursor first_unit(const PagedAttnArgs &a, int Hg, const Range &r, const Rows &rows) {
   Cursor c;
   c.n = r.row;
@@ -297,7 +299,7 @@ __device__ __forceinline__ Cursor first_unit(const PagedAttnArgs &a, int Hg, con
   c.t = r.t;
   if (c.t >= c.units) {  // (behind a segment's units)
     c.t = c.units - 1;
-    advance<U, ALIGN, W>(a, Hg, rows, c);
+    advance<U, ALIGN, W, MODE>(a, Hg, rows, c);
   }
   return c;
 }
