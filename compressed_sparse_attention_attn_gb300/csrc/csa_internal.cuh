@@ -230,7 +230,7 @@ cudaError_t launch_fill_f32(float *p, int64_t n, float v, cudaStream_t s);
 // These kernels are launched as programmatic dependents and wait for the kernels before them (dependency_wait)
 // before they read or write anything: only the launch itself overlaps what came before.  They let no dependent start early
 // (griddepcontrol.launch_dependents): the index kernels read before their own wait what was written two launches earlier, which
-// has to be complete then.  (It would save 0.5 us of a step's three launches.)  k_rows_plan does, for kernels that wait for it in turn.
+// has to be complete then.  (It would save 0.5 us of a step's three launches.)  A plan does (rows_plan.cuh), for k_rows_attn, which waits for it in turn.
 template <class... Args, class... Given>
 inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, unsigned cluster,
                                     Given &&...given) {
@@ -312,8 +312,12 @@ struct PagedAttnArgs {
 };
 // ws: the shares of rows that several CTAs work on; counters: kPagedCounters ints, zero between launches.
 constexpr int kPagedCounters = 3 * 2 * 640;
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms,
-                              cudaStream_t s);
+// plan: with part_o or cu, what one more CTA makes for k_rows_attn (rows_plan.cuh).
+namespace rows {
+struct Plan;
+}
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s,
+                              const rows::Plan *plan = nullptr);
 
 // Attention of many rows over the paged cache (csa_prompt_attn's and csa_prefix_attn's arguments): segment s of S has rows
 // cu[s] .. cu[s+1]-1 of q (cu NULL: one segment of all rows) and len[s] rows of the cache behind table[s][width].  pos NULL: the

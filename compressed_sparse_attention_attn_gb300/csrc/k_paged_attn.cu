@@ -22,7 +22,7 @@
 #include <cstring>
 
 #include "attn_common.cuh"
-#include "paged_common.cuh"
+#include "rows_plan.cuh"
 
 namespace csa {
 namespace paged {
@@ -85,8 +85,22 @@ __device__ __forceinline__ int swizzle(int h) {
   return (NH == 8 ? (h >> 1) & 3 : h & 3) << 3;
 }
 
+// What runs in the grid's last CTA, beside the rows: the plan of the kernel that comes next, where one does.
+template <int MODE>
+struct Beside {
+  rows::Plan plan;
+};
+template <>
+struct Beside<kRow> {};
+
+template <int NT>
+__device__ __noinline__ void plan_beside(const rows::Plan &P, int4 *s_seg, unsigned long long *s_sum) {  // (apart: few registers here)
+  rows::make_plan<NT>(P, s_seg, s_sum);
+}
+
 template <int HD, int NH, int MODE>
-__global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCtas)) k_paged_attn(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCtas))
+    k_paged_attn(const __grid_constant__ Params P, const __grid_constant__ Beside<MODE> beside) {
   using S = Shape<HD, NH>;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kUnit = S::kUnit, kHeads = NH;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -99,13 +113,21 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.head_dim;
   __shared__ Rows rows;
   __shared__ Range rg;
-  constexpr bool PART = MODE == kPart, kBeside = MODE != kRow;
-  if constexpr (!kBeside) dependency_wait();  // (beside k_rows_plan, which has waited, only for the plan, at the end)
-  const int nunits = find_range<kUnit, kThreads, false, kEnd, false, MODE>(P, s_scan, rows, rg);
-  if (nunits <= 0) {
-    if constexpr (kBeside) dependency_wait();
-    return;
+  constexpr bool PART = MODE == kPart;
+  dependency_wait();
+  uint32_t ctas = gridDim.x;
+  if constexpr (MODE != kRow) {
+    if (blockIdx.x == --ctas) {
+      static_assert(rows::kAtOnce<kThreads> * 16 + 256 <= S::kSmem, "the plan's segments");
+      // (k_rows_attn may start when the others are done, up to its own wait)
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      plan_beside<kThreads>(beside.plan, reinterpret_cast<int4 *>(smem),
+                            reinterpret_cast<unsigned long long *>(smem + rows::kAtOnce<kThreads> * 16));
+      return;
+    }
   }
+  const int nunits = find_range<kUnit, kThreads, false, kEnd, false, MODE>(P, ctas, s_scan, rows, rg);
+  if (nunits <= 0) return;
   const uint32_t ring = tc::smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   uint8_t *ring_p = smem + warp * (S::kStages * S::kStageBytes);
   Cursor cl = first_unit<kUnit, false, kEnd, MODE>(a, P.Hg, rg, rows), cc = cl;  // of the lookups, of the products
@@ -424,11 +446,10 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (kBeside) dependency_wait();
 }
 
 template <int HD, int NH, int MODE>
-cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+cudaError_t launch_heads(Params p, const Beside<MODE> &beside, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   using S = Shape<HD, NH>;
   static SmemAttr attr;
   cudaError_t e = attr.ensure((const void *)k_paged_attn<HD, NH, MODE>, S::kSmem);
@@ -439,25 +460,25 @@ cudaError_t launch_heads(Params p, float *ws, size_t ws_bytes, int num_sms, cuda
   // no more CTAs than there can be units
   const int64_t rows = a.window > 0 ? std::min<int64_t>(a.window, (int64_t)a.width * a.c.page) : (int64_t)a.width * a.c.page;
   const int64_t units = (int64_t)a.N * p.Hg * std::max<int64_t>(1, (rows + S::kUnit - 1) / S::kUnit);
-  // (room for the plan's one CTA, where that runs when this starts)
+  // (and the plan's one CTA)
   const int64_t grid = std::min<int64_t>(std::min(units, (int64_t)num_sms * S::kCtas - (MODE != kRow)), kMaxCtas);
   p.share_o = ws;
   p.share_ml = ws + 2 * grid * NH * HD;
   if (sizeof(float) * 2 * grid * NH * (HD + 2) > ws_bytes) return cudaErrorInvalidValue;
-  return launch_dependent(k_paged_attn<HD, NH, MODE>, dim3((unsigned)grid), dim3(S::kThreads), S::kSmem, s, 1, p);
+  return launch_dependent(k_paged_attn<HD, NH, MODE>, dim3((unsigned)grid + (MODE != kRow)), dim3(S::kThreads), S::kSmem, s, 1, p, beside);
 }
 template <int HD, int MODE>
-cudaError_t launch_mode(const Params &p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
-  if (p.g <= 8) return launch_heads<HD, 8, MODE>(p, ws, ws_bytes, num_sms, s);
-  if constexpr (MODE != kSegment) return launch_heads<HD, 16, MODE>(p, ws, ws_bytes, num_sms, s);
+cudaError_t launch_mode(const Params &p, const Beside<MODE> &beside, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+  if (p.g <= 8) return launch_heads<HD, 8, MODE>(p, beside, ws, ws_bytes, num_sms, s);
+  if constexpr (MODE != kSegment) return launch_heads<HD, 16, MODE>(p, beside, ws, ws_bytes, num_sms, s);
   return cudaErrorInvalidValue;
 }
 template <int HD>
-cudaError_t launch(Params p, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
+cudaError_t launch(Params p, const rows::Plan *plan, float *ws, size_t ws_bytes, int num_sms, cudaStream_t s) {
   p.g = p.a.H / p.a.c.kv_heads;
-  return p.a.cu       ? launch_mode<HD, kSegment>(p, ws, ws_bytes, num_sms, s)
-         : p.a.part_o ? launch_mode<HD, kPart>(p, ws, ws_bytes, num_sms, s)
-                      : launch_mode<HD, kRow>(p, ws, ws_bytes, num_sms, s);
+  return p.a.cu       ? launch_mode<HD, kSegment>(p, Beside<kSegment>{*plan}, ws, ws_bytes, num_sms, s)
+         : p.a.part_o ? launch_mode<HD, kPart>(p, Beside<kPart>{*plan}, ws, ws_bytes, num_sms, s)
+                      : launch_mode<HD, kRow>(p, Beside<kRow>{}, ws, ws_bytes, num_sms, s);
 }
 
 // (head_dim above 256: k_paged_attn_tc.cu)
@@ -465,8 +486,8 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
 
 }  // namespace paged
 
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms,
-                              cudaStream_t s) {
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s,
+                              const rows::Plan *plan) {
   static_assert(kPagedCounters == 3 * 2 * paged::kMaxCtas && paged::kJoin * paged::kJoin * paged::kJoin >= paged::kMaxCtas, "the context's counters");
   paged::Params p;
   p.a = a;
@@ -474,9 +495,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes
   p.scale_log2 = (float)(a.scale * 1.4426950408889634);
   p.counters = counters;
   const int hd = a.c.head_dim;
-  if (hd <= 64) return paged::launch<64>(p, ws, ws_bytes, num_sms, s);
-  if (hd <= 128) return paged::launch<128>(p, ws, ws_bytes, num_sms, s);
-  if (hd <= 256) return paged::launch<256>(p, ws, ws_bytes, num_sms, s);
+  if (hd <= 64) return paged::launch<64>(p, plan, ws, ws_bytes, num_sms, s);
+  if (hd <= 128) return paged::launch<128>(p, plan, ws, ws_bytes, num_sms, s);
+  if (hd <= 256) return paged::launch<256>(p, plan, ws, ws_bytes, num_sms, s);
   return paged::launch_latent(p, ws, ws_bytes, num_sms, s);
 }
 

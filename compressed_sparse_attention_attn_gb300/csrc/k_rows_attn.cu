@@ -14,11 +14,11 @@
 // Up to 192 features two tiles of 128 rows share the keys and values, and one's softmax runs while the other's products do; at 256, where
 // O takes half of tensor memory, one tile has two score buffers instead.
 //
-// A plan kernel lists the items with the number of their position tiles (k_rows_plan); the tiles of all items and kv heads stand one
+// A plan lists the items with the number of their position tiles (rows_plan.cuh); the tiles of all items and kv heads stand one
 // behind the other, with places for each item's end, and each CTA takes an equal part of them in a row, so every CTA has as much to do
 // as any other whatever the lengths and masks are.  An item that several CTAs worked on is joined from their shares (M, L, O), in the
 // order of the CTAs, by k_rows_join.  The rows of a prefix batch's own pages come from k_paged_attn as one more share, and it takes a
-// prompt batch's requests of one token (single_tokens below); it runs beside the plan.
+// prompt batch's requests of one token (single_tokens below); its last CTA then makes the plan, beside the others' work.
 //
 // A CTA an SM: four warps a tile of rows for the softmax and the results, a warp that issues its products, and the copies (whole
 // tiles by TMA, boxes of up to 128 rows inside a page where pages hold whole boxes of 8 rows at least; ragged tiles and other pages by
@@ -36,7 +36,7 @@
 #include <cstring>
 
 #include "attn_common.cuh"
-#include "paged_common.cuh"
+#include "rows_plan.cuh"
 
 namespace csa {
 
@@ -46,7 +46,6 @@ bool tma_map_pages_bf16(CUtensorMap *m, const void *base, const uint64_t (&dims)
 
 namespace rows {
 
-constexpr int kSub = 128;     // rows of a product
 // Tiles that the end of an item counts for: its last tiles' masks and values looked over, the wait for the last product, results, the next
 // q, 10 thousand cycles in all where a tile takes 3.4.  (4096 tokens of 64 heads over 8 of 128: 322, 282, 276 and 280 us for 1 to 4.)
 // At 256 features a tile is half as long, and one tile of rows has nothing beside its end (32 over 8 of 256, 4096 tokens: 298, 282, 265 and
@@ -54,39 +53,15 @@ constexpr int kSub = 128;     // rows of a product
 // (windows in pages of 17: 209 and 218 us for 3 and 5).
 template <int HDP>
 constexpr int end_tiles(bool tma) { return HDP == 256 && tma ? 5 : 3; }
-constexpr int kMinPlaces = 2; // places a CTA has at least
 constexpr int kNote = 8;      // tiles whose notes are kept: more than the copies can be ahead
 constexpr float kRaise = 8.f;
 
-// Rows row0 .. row0 + rows - 1 of the segment whose first token is tok0; positions begin .. end - 1 behind table row seg are all that
-// any of them attends.  Token t of a prompt stands at t + shift; of a prefix shift is its length.
-// end0, begin1: of its first 128 rows, of the others.  at0 .. at1: positions that every row attends (with a window in a prefix: none).
-struct Item {
-  int tok0, row0, rows, seg, begin, end, shift, end0, begin1, at0, at1, spare;
-};
-// A CTA's part of the places (a kv head's items one behind the other, head after head): first .. end - 1, of which the first is in item
-// `item` of head kvh; `items` of a head, `places` of a head.  No places: first == end.
-struct Part {
-  unsigned long long first, end, places, start;  // start: first place of the item
-  int item, kvh, items, spare;
-  Item d;
-};
-
-struct Params {
-  RowsAttnArgs a;
-  paged::FastDiv page, g;
+struct Params : Plan {
   float scale_log2;
-  int end_tiles;
   int wide;                    // o's rows are whole 32 bytes on such borders
-  Part *part;                  // [ctas + 1] (of the last one: first)
-  int ctas;
-  Item *item;                  // [cap]
-  unsigned long long *start;   // [cap + 1]: first place of an item
-  int cap;
   float *share_o;              // [2 ctas][QT * 128][HDP]
   float4 *share_ml;            // [2 ctas][QT * 128]: M, L of the rounded weights, L
   int4 *split;                 // [ctas]: the item that began in this CTA and goes on behind it: item, kv head, CTAs
-  bool single;                 // prompts: segments of one token are k_paged_attn's
   const float *own_o;          // prefix: [N][H][head_dim], the share of each row's own pages
   const float2 *own_ml;        // [N][H]: M, L
 };
@@ -115,146 +90,13 @@ struct Shape {
 
 constexpr int kPlanThreads = 512;  // (1024: 1 us more for every step's barriers)
 
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *warp_sum, unsigned long long &sum) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sum[wid] = v;
-  __syncthreads();
-  unsigned long long w = lane < kPlanThreads / 32 ? warp_sum[lane] : 0;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long o = __shfl_up_sync(0xffffffffu, w, d);
-    if (lane >= d) w += o;
-  }
-  sum = __shfl_sync(0xffffffffu, w, 31);
-  const unsigned long long before = __shfl_sync(0xffffffffu, w, wid > 0 ? wid - 1 : 0);
-  return v + (wid > 0 ? before : 0);
-}
-
-template <int TR, int KVT>
-__global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constant__ Params P) {
-  const RowsAttnArgs &a = P.a;
+// (Where k_paged_attn does not make it.)
+__global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constant__ Plan P) {
   __shared__ unsigned long long s_sum[32];
-  __shared__ int4 s_seg[kPlanThreads];  // first token, tokens, length, tiles up to and with this segment's
-  const int tid = threadIdx.x;
-  const int64_t cap = min((int64_t)a.width * a.c.page, (int64_t)0x7fffffff);
+  __shared__ int4 s_seg[kAtOnce<kPlanThreads>];
   dependency_wait();
-  // What comes next may start: k_paged_attn over the rows' own pages or the segments of one token, which needs nothing of this
-  // kernel (and waits for it at its end), or k_rows_attn's start, up to its own wait.  (64 rows of 40 to 700 own positions behind 8192: 57.7 -> 53.5 us, 2 x 500 22.9 -> 20.9.)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  unsigned long long places = 0;
-  int items = 0;
-  bool full = false;
-  for (int s0 = 0; s0 < a.S; s0 += kPlanThreads) {
-    const int s = s0 + tid;
-    int t0 = 0, n = 0, len = 0;
-    if (s < a.S) {
-      int t1 = a.N;
-      if (a.cu) t0 = a.cu[s], t1 = a.cu[s + 1];
-      bool bad = t0 < 0 || t1 < t0 || t1 > a.N;
-      n = bad ? 0 : t1 - t0;
-      if (n > 0) {
-        len = a.len[s];
-        if (a.pos == nullptr && len < n) {
-          bad = true;
-          n = 0;
-        }
-        if (len < 0 || len > cap) bad = true;
-        if (a.pos) len = max(len, 0);
-      }
-      if (bad) atomicOr(a.status, kStatusBadIndex);
-      if (n == 1 && P.single) n = 0;
-    }
-    unsigned long long sum;
-    const unsigned long long tiles = n > 0 ? ((unsigned long long)n * P.g.d + TR - 1) / TR : 0;
-    const unsigned long long to = block_scan(tiles, s_sum, sum);
-    s_seg[tid] = make_int4(t0, n, len, (int)min(to, 0x7fffffffull));
-    __syncthreads();
-    const int room = P.cap - items, all = (int)min(sum, (unsigned long long)room);
-    full = full || sum > (unsigned long long)room;
-    for (int i0 = 0; i0 < all; i0 += kPlanThreads) {
-      const int i = i0 + tid;
-      unsigned long long mine = 0;
-      Item it{};
-      if (i < all) {
-        int lo = 0, hi = kPlanThreads - 1;  // the first segment with more than i tiles up to its end
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (s_seg[mid].w > i) hi = mid;
-          else lo = mid + 1;
-        }
-        const int4 sg = s_seg[lo];
-        const int first = lo ? s_seg[lo - 1].w : 0;
-        it.tok0 = sg.x;
-        it.row0 = (i - first) * TR;
-        it.rows = (int)min((long long)TR, (long long)sg.y * P.g.d - it.row0);
-        it.seg = s0 + lo;
-        if (a.pos) {  // (a row's own part begins at len or behind it: the window reaches back to len - window at most)
-          it.shift = sg.z;
-          it.begin = it.begin1 = a.window > 0 ? max(0, sg.z - a.window) : 0;
-          it.end = it.end0 = (int)min((int64_t)sg.z, cap);
-          it.at0 = 0;
-          it.at1 = a.window > 0 ? 0 : it.end;
-        } else {
-          it.shift = sg.z - sg.x - sg.y;
-          auto pos = [&](int r) { return (int64_t)sg.x + P.g.div(it.row0 + min(r, it.rows - 1)) + it.shift; };  // of a row
-          auto first = [&](int64_t p) { return (int)(a.window > 0 ? max((int64_t)0, p - a.window + 1) : 0); };
-          it.begin = first(pos(0));
-          it.begin1 = first(pos(kSub));
-          it.end0 = (int)min(pos(kSub - 1) + 1, cap);
-          it.end = (int)min(pos(it.rows - 1) + 1, cap);
-          it.at0 = first(pos(it.rows - 1));
-          it.at1 = (int)min(pos(0) + 1, cap);
-        }
-        mine = it.end > it.begin ? (it.end - 1) / KVT - it.begin / KVT + 1 : 1;
-        mine += P.end_tiles;
-      }
-      const unsigned long long incl = block_scan(mine, s_sum, sum);
-      if (i < all) {
-        reinterpret_cast<int4 *>(P.item + items + i)[0] = make_int4(it.tok0, it.row0, it.rows, it.seg);
-        reinterpret_cast<int4 *>(P.item + items + i)[1] = make_int4(it.begin, it.end, it.shift, it.end0);
-        reinterpret_cast<int4 *>(P.item + items + i)[2] = make_int4(it.begin1, it.at0, it.at1, 0);
-        P.start[items + i] = places + incl - mine;
-      }
-      places += sum;
-    }
-    items += all;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    P.start[items] = places;
-    if (full) atomicOr(a.status, kStatusBadIndex);  // (more items than rows can make: requests that overlap)
-  }
-  __syncthreads();
-  const unsigned long long total = places * a.c.kv_heads;
-  const int parts = (int)min((unsigned long long)P.ctas, max(1ull, total / kMinPlaces));
-  for (int c = tid; c <= P.ctas; c += kPlanThreads) {
-    const int n = min(c, parts);
-    Part q{};
-    q.first = total / parts * n + total % parts * n / parts;
-    q.places = places;
-    q.items = items;
-    q.end = c < parts ? total / parts * (n + 1) + total % parts * (n + 1) / parts : q.first;
-    if (q.first < q.end) {
-      q.kvh = (int)(q.first / places);
-      const unsigned long long in = q.first - places * q.kvh;
-      int lo = 0, hi = items - 1;  // the last item that begins at `in` or before
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (P.start[mid] <= in) lo = mid;
-        else hi = mid - 1;
-      }
-      q.item = lo;
-      q.start = P.start[lo];
-      q.d = P.item[lo];
-    }
-    P.part[c] = q;
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (k_rows_attn may start, up to its own wait)
+  make_plan<kPlanThreads>(P, s_seg, s_sum);
 }
 
 // ------------------------------------------------------------------------------------------------ a CTA's part
@@ -1302,7 +1144,8 @@ struct Room {
   }
 };
 
-// What runs beside the plan: the rows' own pages, or the segments of one token.
+// What runs beside the plan: the rows' own pages, or the segments of one token.  (In one grid: 64 rows of 40 to 700 own positions behind
+// 8192 53.5 us, two launches in a row 57.7; 2 x 500 20.7, 22.9.)
 struct Beside {
   PagedAttnArgs a;
   float *shares;
@@ -1352,8 +1195,11 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
       maps.box_rows = box;
   }
   p.end_tiles = end_tiles<HDP>(maps.box_rows > 0);
-  e = launch_dependent(k_rows_plan<TR, S::KVT>, dim3(1), dim3(kPlanThreads), 0, s, 1, p);
-  if (e == cudaSuccess && beside) e = launch_paged_attn(beside->a, beside->shares, kPagedShareBytes, beside->counters, num_sms, s);
+  p.rows_log2 = TR == 256 ? 8 : 7;
+  p.tile_log2 = S::KVT == 128 ? 7 : 6;
+  const Plan &plan = p;
+  e = beside ? launch_paged_attn(beside->a, beside->shares, kPagedShareBytes, beside->counters, num_sms, s, &plan)
+             : launch_dependent(k_rows_plan, dim3(1), dim3(kPlanThreads), 0, s, 1, plan);
   if (e == cudaSuccess) e = launch_dependent(k_rows_attn<HDP>, dim3(grid), dim3(S::kThreads), S::kSmem, s, 1, p, maps);
   if (e != cudaSuccess || one) return e;
   // blocks of the join: a thread a quarter of 16 features; more of them an item where items are few, and so split over many CTAs

@@ -158,16 +158,16 @@ __device__ __forceinline__ Two warp_scan(Two v, int lane) {
   return v;
 }
 
-// Called by all NT threads of the CTA.  scratch: Two [NT / 32], rows, out: all in shared memory.  Returns how many
+// Called by all NT threads of the CTA, one of the first G of the grid.  scratch: Two [NT / 32], rows, out: all in shared memory.  Returns how many
 // units the CTA has (-1: more than can be counted in all).  Up to 32 rows the first warp finds it alone, and the CTA meets
 // once.  WHOLE: few segments (and rows) get whole CTAs, as many as ceil(its units / q) says, if such a q close to
 // the even share exists: a CTA then has one segment's end and not two (32 latent rows of about 20 tiles: 20.9
 // against 22.6 us, 128 shares of 128 KB instead of 184; up to 256 features, where ends are cheap, one row of 8000 lost 1 us).
 template <int U, int NT, bool ALIGN, int W, bool WHOLE, int MODE = kRow>
-__device__ __forceinline__ int find_range(const Params &P, Two *scratch, Rows &rows, Range &out) {
+__device__ __forceinline__ int find_range(const Params &P, uint32_t G, Two *scratch, Rows &rows, Range &out) {
   const PagedAttnArgs &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const uint32_t Hg = (uint32_t)P.Hg, G = gridDim.x;
+  const uint32_t Hg = (uint32_t)P.Hg;
   const bool report = blockIdx.x == 0;
   auto of_row = [&](int n, Row &r) -> Two {
     r = Row{0, 0, 0, 0, 0};

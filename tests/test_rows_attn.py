@@ -1,4 +1,5 @@
-"""csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows.
+"""csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows, calls right behind the
+kernels that write their inputs.
 
 What a call leaves is compared bit for bit with what it leaves without the value: the sums of the other rows and features do not
 change with it.
@@ -6,8 +7,8 @@ change with it.
 import pytest
 import torch
 
-from test_paged import csa, ctx, gen, i32, make_ctx, randn  # noqa: F401
-from test_prompt import Prefixes
+from test_paged import Batch, csa, ctx, gen, i32, randn  # noqa: F401
+from test_prompt import Prefixes, cus
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,51 @@ def test_prefix_bad_values_in_every_tile(csa, ctx, hd, bad):
     assert not o[..., 1].isfinite().any() and torch.equal(lse, want_lse)
     assert torch.equal(o[..., 2:], want[..., 2:]) and torch.equal(o[..., 0], want[..., 0])
     assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd", [(8, 2, 128), (4, 4, 64), (16, 2, 256), (18, 2, 128)])
+def test_inputs_written_by_the_kernel_before(csa, ctx, H, kv, hd):
+    """Calls in one graph, the inputs of each (queries, lengths, places, tables, a row of the cache) written by the kernels right before
+    it: every call finds its own, not those of the call before."""
+    lens, new = [3000, 900, 25, 2500, 64], [[1, 40, 1, 0, 1], [1, 1, 25, 300, 1], [0, 1, 1, 1, 64]]
+    b = Batch(lens, H, kv, hd, 16, seed=hd)
+    cache, N, R = csa.PagedCache(b.k, b.v), 400, len(lens)
+    g = gen(hd + 1)
+    steps = []
+    for i, n in enumerate(new):
+        order = torch.randperm(R, generator=torch.Generator().manual_seed(i)).tolist()
+        length = [lens[r] - 3 * i for r in order]
+        n = [min(a, x) for a, x in zip(n, length)]
+        steps.append(dict(q=randn(g, N, H, hd), row=randn(g, kv, hd), table=b.table[order].contiguous(), cu=i32(cus(n)),
+                          length=i32(length), pos=i32([x - 1 for x in length]), plen=i32([lens[i % R]])))
+    now = {k: torch.empty_like(v) for k, v in steps[0].items()}
+    last = cache.v[int(b.table[0, 0]), 0]
+
+    def calls(s, o, p):
+        for k, v in s.items():
+            now[k].copy_(v)
+        last.copy_(now["row"])
+        ctx.prompt_attn(now["q"], cache, now["table"], now["cu"], now["length"], b.scale, out=o)
+        now["q"].copy_(s["q"].flip(0))
+        last.copy_(s["row"] * 2)
+        ctx.prefix_attn(now["q"][:R], cache, now["table"], now["pos"], now["table"][:1], now["plen"], b.scale, out=p)
+
+    def outs():
+        return [(torch.zeros(N, H, hd, dtype=torch.bfloat16, device="cuda"), torch.zeros(R, H, hd, dtype=torch.bfloat16, device="cuda"))
+                for _ in steps]
+
+    want, got = outs(), outs()
+    for s, (o, p) in zip(steps, want):
+        torch.cuda.synchronize()
+        calls(s, o, p)
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for s, (o, p) in zip(steps, got):
+            calls(s, o, p)
+    for _ in range(20):
+        for o, p in got:
+            o.zero_(), p.zero_()
+        graph.replay()
+        assert all(torch.equal(x, y) for a, e in zip(got, want) for x, y in zip(a, e))
+    assert ctx.status() == -1 and ctx.status() == 0  # (prefixes that are longer than the pages behind them: recorded, left out)
