@@ -305,8 +305,8 @@ struct PagedAttnArgs {
   // f32 [N][H][head_dim], and maximum (base 2) and sum of weights [N][H]
   float *part_o = nullptr;
   float2 *part_ml = nullptr;
-  // head_dim up to 256, up to 8 query heads a kv head: row n is the one new token of segment n, token cu[n] at position len[n] - 1; segments of more, of none, or behind
-  // `tokens` are padding (req and pos are not read)
+  // head_dim up to 256, up to 8 query heads a kv head: row n is the one new token of segment n, token cu[n] at position len[n] - 1;
+  // segments of more, of none, or behind `tokens` are padding (req and pos are not read)
   const int32_t *cu = nullptr, *len = nullptr;
   int tokens = 0;
 };

@@ -93,11 +93,6 @@ struct Beside {
 template <>
 struct Beside<kRow> {};
 
-template <int NT>
-__device__ __noinline__ void plan_beside(const rows::Plan &P, int4 *s_seg, unsigned long long *s_sum) {  // (apart: few registers here)
-  rows::make_plan<NT>(P, s_seg, s_sum);
-}
-
 template <int HD, int NH, int MODE>
 __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCtas))
     k_paged_attn(const __grid_constant__ Params P, const __grid_constant__ Beside<MODE> beside) {
@@ -118,11 +113,10 @@ __global__ void __launch_bounds__((Shape<HD, NH>::kThreads), (Shape<HD, NH>::kCt
   uint32_t ctas = gridDim.x;
   if constexpr (MODE != kRow) {
     if (blockIdx.x == --ctas) {
-      static_assert(rows::kAtOnce<kThreads> * 16 + 256 <= S::kSmem, "the plan's segments");
+      static_assert(sizeof(rows::PlanRoom<kThreads>) <= S::kSmem, "the plan's notes");
       // (k_rows_attn may start when the others are done, up to its own wait)
       asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-      plan_beside<kThreads>(beside.plan, reinterpret_cast<int4 *>(smem),
-                            reinterpret_cast<unsigned long long *>(smem + rows::kAtOnce<kThreads> * 16));
+      rows::make_plan<kThreads>(beside.plan, *reinterpret_cast<rows::PlanRoom<kThreads> *>(smem));
       return;
     }
   }

@@ -92,11 +92,10 @@ constexpr int kPlanThreads = 512;  // (1024: 1 us more for every step's barriers
 
 // (Where k_paged_attn does not make it.)
 __global__ void __launch_bounds__(kPlanThreads) k_rows_plan(const __grid_constant__ Plan P) {
-  __shared__ unsigned long long s_sum[32];
-  __shared__ int4 s_seg[kAtOnce<kPlanThreads>];
+  __shared__ PlanRoom<kPlanThreads> room;
   dependency_wait();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (k_rows_attn may start, up to its own wait)
-  make_plan<kPlanThreads>(P, s_seg, s_sum);
+  make_plan<kPlanThreads>(P, room);
 }
 
 // ------------------------------------------------------------------------------------------------ a CTA's part
@@ -1162,11 +1161,12 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
   if (e != cudaSuccess) return e;
   const int g = a.H / a.c.kv_heads;
   const int64_t cap = ((int64_t)a.N * g + TR - 1) / TR + a.S;
-  // no more CTAs than there can be tiles
+  // no more CTAs than can get places (so that their number, and with it the split, does not go by rows that are padding)
   const int64_t rows = (int64_t)a.width * a.c.page;
   const int64_t tiles = (a.window > 0 ? std::min<int64_t>(rows, (int64_t)a.window + TR) : rows) / S::KVT + 2;
   const bool one = rows <= S::KVT;  // (every item has one tile: nothing is shared)
-  const int64_t most = (double)cap * a.c.kv_heads * tiles > 1e9 ? num_sms : cap * a.c.kv_heads * (one ? 1 : tiles);
+  const int64_t each = one ? 1 : std::max(tiles, (tiles + end_tiles<HDP>(true) + 1) / kMinPlaces);
+  const int64_t most = (double)cap * a.c.kv_heads * each > 1e9 ? num_sms : cap * a.c.kv_heads * each;
   const int grid = (int)std::min<int64_t>(num_sms, most);
   p.cap = (int)cap;
   p.part = room.take<Part>(grid + 1);
@@ -1210,15 +1210,14 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
 
 }  // namespace rows
 
-// Whether a prompt batch's segments of one token go to k_paged_attn.  Up to 8 query heads a kv head it takes half the time over them
-// (a step of nothing else, with the launches that then find nothing to do: 64 of up to 5000 positions, 32 heads over 8 of 128, 43
-// against 74 us; 64 of 100 to 3000, 32 over 8 of 64, 37, 73; 4 x 8000, 32 over 8 of 128, 40, 43).  With 16 it does not (32 of 2000 to
-// 8000, 32 over 2 of 128: 48 against 46 us; 16 of 3000 to 9000, 32 over 2 of 256: 64, 51).  A batch of one prompt has none, and in one of
-// 512 tokens a request or more they would be too few for the launch (6 windows of up to 6001 tokens, 16 of 256: 207 against 212 us without
-// and with it; 12 prompts of 100 to 4000: 311, 313).
-static bool single_tokens(const RowsAttnArgs &a) {
-  return !a.pos && a.H / a.c.kv_heads <= 8 && (a.S > 1 ? a.N < (int64_t)512 * a.S : a.N == 1);
-}
+// Whether a prompt batch's segments of one token go to k_paged_attn: up to 8 query heads a kv head, always, so that neither the other
+// requests nor padding rows change how a token is computed.  There it takes half the time over them (64 of up to 5000 positions, 32 heads
+// over 8 of 128: 41 against 73 us; 32 of up to 64000 beside a chunk of 2000 309, 330; 15 of 16 to 64 thousand beside one of 8200 1185,
+// 1262; 15 of 1 to 32 thousand beside 8200, 32 over 8 of 64, 820, 858; four of 64000 beside 8200 1033, 1062), and where there are none it costs
+// no more than the plan alone (4096 tokens 277, 276 us; 12 prompts of 100 to 4000 312 both).  It is slower where few single tokens are
+// short (one beside 4 windows of up to 6001, 16 of 256: 214, 209; 4 of up to 64000 beside 2000: 224, 217).  With 16 heads a kv head it is
+// not faster (32 of 2000 to 8000, 32 over 2 of 128: 48 against 46 us; 16 of 3000 to 9000, 32 over 2 of 256: 64, 51).
+static bool single_tokens(const RowsAttnArgs &a) { return !a.pos && a.H / a.c.kv_heads <= 8; }
 
 // Bytes of workspace that launch_rows_attn needs (an upper bound).
 size_t rows_attn_bytes(const RowsAttnArgs &a, int num_sms) {

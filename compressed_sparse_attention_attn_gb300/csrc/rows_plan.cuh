@@ -37,10 +37,6 @@ struct Plan {
   bool single;                 // prompts: segments of one token are k_paged_attn's
 };
 
-// Segments (and items) that a CTA of NT threads looks at in one go.
-template <int NT>
-constexpr int kAtOnce = (512 + NT - 1) / NT * NT;
-
 // Inclusive over the CTA's threads; sum: of all.
 template <int NT>
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *warp_sum, unsigned long long &sum) {
@@ -64,70 +60,65 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
   return v + (wid > 0 ? before : 0);
 }
 
-// By all NT threads of a CTA, behind the wait for what came before.  s_seg [kAtOnce<NT>], s_sum [32]: in shared memory.
+// Shared memory of the CTA that makes the plan.
+constexpr int kStartsKept = 2048;
 template <int NT>
-__device__ __forceinline__ void make_plan(const Plan &P, int4 *s_seg, unsigned long long *s_sum) {
-  constexpr int kMine = kAtOnce<NT> / NT;  // of a thread, one behind the other
+struct PlanRoom {
+  int4 seg[NT];  // first token, tokens, length, items up to and with this segment's
+  unsigned long long sum[32];
+  unsigned long long start[kStartsKept];  // first places of the first items
+};
+
+// By all NT threads of a CTA, behind the wait for what came before.  (What is run once costs its fetches: a thread with four segments,
+// items and parts at a time, unrolled, took 18.5 us where this takes 6.)
+template <int NT>
+__device__ __forceinline__ void make_plan(const Plan P, PlanRoom<NT> &room) {
   const RowsAttnArgs &a = P.a;
   const int tid = threadIdx.x, RL = P.rows_log2, KL = P.tile_log2;
   const int64_t cap = min((int64_t)a.width * a.c.page, (int64_t)0x7fffffff);
-  auto tiles = [&](int n) { return ((unsigned long long)n * P.g.d + (1 << RL) - 1) >> RL; };  // items of n tokens
   unsigned long long places = 0;
   int items = 0;
   bool full = false;
-  for (int s0 = 0; s0 < a.S; s0 += kAtOnce<NT>) {
-    int4 seg[kMine];  // first token, tokens, length, tiles up to and with this segment's
-    unsigned long long mine = 0, sum;
-#pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      const int s = s0 + tid * kMine + e;
-      int t0 = 0, n = 0, len = 0;
-      if (s < a.S) {
-        int t1 = a.N;
-        if (a.cu) t0 = a.cu[s], t1 = a.cu[s + 1];
-        bool bad = t0 < 0 || t1 < t0 || t1 > a.N;
-        n = bad ? 0 : t1 - t0;
-        if (n > 0) {
-          len = a.len[s];
-          if (a.pos == nullptr && len < n) {
-            bad = true;
-            n = 0;
-          }
-          if (len < 0 || len > cap) bad = true;
-          if (a.pos) len = max(len, 0);
+#pragma unroll 1
+  for (int s0 = 0; s0 < a.S; s0 += NT) {
+    const int s = s0 + tid, segs = min(NT, a.S - s0);
+    int t0 = 0, n = 0, len = 0;
+    if (s < a.S) {
+      int t1 = a.N;
+      if (a.cu) t0 = a.cu[s], t1 = a.cu[s + 1];
+      len = a.len[s];
+      bool bad = t0 < 0 || t1 < t0 || t1 > a.N;
+      n = bad ? 0 : t1 - t0;
+      if (n > 0) {
+        if (len < 0 || len > cap) bad = true;
+        if (a.pos == nullptr && len < n) {
+          bad = true;
+          n = 0;
         }
-        if (bad) atomicOr(a.status, kStatusBadIndex);
-        if (n == 1 && P.single) n = 0;
+        if (a.pos) len = max(len, 0);
       }
-      seg[e] = make_int4(t0, n, len, 0);
-      mine += tiles(n);
+      if (bad) atomicOr(a.status, kStatusBadIndex);
+      if (n == 1 && P.single) n = 0;
     }
-    unsigned long long to = block_scan<NT>(mine, s_sum, sum) - mine;
-#pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      to += tiles(seg[e].y);
-      seg[e].w = (int)min(to, 0x7fffffffull);
-      s_seg[tid * kMine + e] = seg[e];
-    }
+    unsigned long long sum;
+    const unsigned long long tiles = ((unsigned long long)n * P.g.d + (1 << RL) - 1) >> RL, to = block_scan<NT>(tiles, room.sum, sum);
+    room.seg[tid] = make_int4(t0, n, len, (int)min(to, 0x7fffffffull));
     __syncthreads();
-    const int room = P.cap - items, all = (int)min(sum, (unsigned long long)room);
-    full = full || sum > (unsigned long long)room;
-    for (int i0 = 0; i0 < all; i0 += kAtOnce<NT>) {
-      unsigned long long of[kMine];
-      mine = 0;
-#pragma unroll
-      for (int e = 0; e < kMine; ++e) {
-        const int i = i0 + tid * kMine + e;
-        of[e] = 0;
-        if (i >= all) continue;
-        int lo = 0, hi = kAtOnce<NT> - 1;  // the first segment with more than i tiles up to its end
+    const int left = P.cap - items, all = (int)min(sum, (unsigned long long)left);
+    full = full || sum > (unsigned long long)left;
+#pragma unroll 1
+    for (int i0 = 0; i0 < all; i0 += NT) {
+      const int i = i0 + tid;
+      unsigned long long mine = 0;
+      if (i < all) {
+        int lo = 0, hi = segs - 1;  // the first segment with more than i items up to its end
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
-          if (s_seg[mid].w > i) hi = mid;
+          if (room.seg[mid].w > i) hi = mid;
           else lo = mid + 1;
         }
-        const int4 sg = s_seg[lo];
-        const int first = lo ? s_seg[lo - 1].w : 0;
+        const int4 sg = room.seg[lo];
+        const int first = lo ? room.seg[lo - 1].w : 0;
         Item it{};
         it.tok0 = sg.x;
         it.row0 = (i - first) << RL;
@@ -150,18 +141,15 @@ __device__ __forceinline__ void make_plan(const Plan &P, int4 *s_seg, unsigned l
           it.at0 = first(pos(it.rows - 1));
           it.at1 = (int)min(pos(0) + 1, cap);
         }
-        of[e] = (it.end > it.begin ? ((it.end - 1) >> KL) - (it.begin >> KL) + 1 : 1) + P.end_tiles;
+        mine = (it.end > it.begin ? ((it.end - 1) >> KL) - (it.begin >> KL) + 1 : 1) + P.end_tiles;
         reinterpret_cast<int4 *>(P.item + items + i)[0] = make_int4(it.tok0, it.row0, it.rows, it.seg);
         reinterpret_cast<int4 *>(P.item + items + i)[1] = make_int4(it.begin, it.end, it.shift, it.end0);
         reinterpret_cast<int4 *>(P.item + items + i)[2] = make_int4(it.begin1, it.at0, it.at1, 0);
-        mine += of[e];
       }
-      unsigned long long at = places + block_scan<NT>(mine, s_sum, sum) - mine;
-#pragma unroll
-      for (int e = 0; e < kMine; ++e) {
-        const int i = i0 + tid * kMine + e;
-        if (i < all) P.start[items + i] = at;
-        at += of[e];
+      const unsigned long long at = places + block_scan<NT>(mine, room.sum, sum) - mine;
+      if (i < all) {
+        P.start[items + i] = at;
+        if (items + i < kStartsKept) room.start[items + i] = at;
       }
       places += sum;
     }
@@ -175,24 +163,27 @@ __device__ __forceinline__ void make_plan(const Plan &P, int4 *s_seg, unsigned l
   __syncthreads();
   const unsigned long long total = places * a.c.kv_heads;
   const int parts = (int)min((unsigned long long)P.ctas, max(1ull, total / kMinPlaces));
+  const unsigned long long each = total / parts, more = total % parts;
+  const unsigned long long *starts = items <= kStartsKept ? room.start : P.start;
+#pragma unroll 1
   for (int c = tid; c <= P.ctas; c += NT) {
     const int n = min(c, parts);
     Part q{};
-    q.first = total / parts * n + total % parts * n / parts;
+    q.first = each * n + more * n / parts;
     q.places = places;
     q.items = items;
-    q.end = c < parts ? total / parts * (n + 1) + total % parts * (n + 1) / parts : q.first;
+    q.end = c < parts ? each * (n + 1) + more * (n + 1) / parts : q.first;
     if (q.first < q.end) {
       q.kvh = (int)(q.first / places);
       const unsigned long long in = q.first - places * q.kvh;
       int lo = 0, hi = items - 1;  // the last item that begins at `in` or before
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (P.start[mid] <= in) lo = mid;
+        if (starts[mid] <= in) lo = mid;
         else hi = mid - 1;
       }
       q.item = lo;
-      q.start = P.start[lo];
+      q.start = starts[lo];
       q.d = P.item[lo];
     }
     P.part[c] = q;

@@ -459,8 +459,8 @@ CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, 
  * Rows of q outside every request's are padding: nothing of them is written.  A request without tokens has no rows (its length
  * does not count).  N 0: nothing to do, q and o may be NULL.
  * The weights enter the product with the values as one bf16 term, and the sum below O is of those, so that they add up to 1 (lse is of the
- * f32 ones); but those of requests of one token as two, up to 8 query heads a kv head and where N < 512 R (R = 1: N = 1):
- * csa_paged_attn's kernel serves these, and its bound on a call's work holds for them.
+ * f32 ones); but those of requests of one token as two, up to 8 query heads a kv head: csa_paged_attn's kernel serves these,
+ * and its bound on a call's work holds for them.  Padding rows change no bit of the others.
  * An infinity or NaN in the cache reaches the rows that attend it and no others.
  * Caller errors, recorded in the context's status word: a request with cu[r] < 0, cu[r] > cu[r+1], cu[r+1] > N or length[r] < n (its
  * rows are left as they were), a length past width pages (the rows past them are left out), a page id outside [0, n_pages) (its rows

@@ -1,5 +1,5 @@
 """csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows, calls right behind the
-kernels that write their inputs.
+kernels that write their inputs, single tokens among many others and behind padding.
 
 What a call leaves is compared bit for bit with what it leaves without the value: the sums of the other rows and features do not
 change with it.
@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from test_paged import Batch, csa, ctx, gen, i32, randn  # noqa: F401
-from test_prompt import Prefixes, cus
+from test_prompt import Prefixes, check_prompt, cus, prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +140,32 @@ def test_inputs_written_by_the_kernel_before(csa, ctx, H, kv, hd):
         graph.replay()
         assert all(torch.equal(x, y) for a, e in zip(got, want) for x, y in zip(a, e))
     assert ctx.status() == -1 and ctx.status() == 0  # (prefixes that are longer than the pages behind them: recorded, left out)
+
+
+@pytest.mark.parametrize("H,kv,hd", [(8, 2, 128), (4, 4, 64), (16, 2, 256), (9, 1, 128), (6, 2, 192)])
+@pytest.mark.parametrize("lens,new", [([900], [1]), ([1], [1]), ([40], [17]), ([300, 64, 5000, 7], [1, 1, 1, 1]), ([700, 0, 2000, 130], [1, 0, 300, 1]),
+                                      ([150, 90], [150, 20]), ([6000], [33])])
+def test_padding_changes_no_bit(csa, ctx, H, kv, hd, lens, new):
+    """The same batch with no padding rows, with a few, and with thousands, as a graph captured at its largest step has them."""
+    b = Batch(lens, H, kv, hd, 16, seed=hd)
+    n, cu, length, cache = sum(new), i32(cus(new)), i32(lens), csa.PagedCache(b.k, b.v)
+    q = b.queries(n + 6000)
+    o, lse = ctx.prompt_attn(q[:n], cache, b.table, cu, length, b.scale, with_lse=True)
+    check_prompt(b, new, q, o, lse)
+    for pad in (1, 511, 6000):
+        out, lse2 = torch.full_like(q[:n + pad], 3.0), torch.full((n + pad, H), 3.0, device="cuda")
+        ctx.prompt_attn(q[:n + pad], cache, b.table, cu, length, b.scale, out=out, lse=lse2)
+        assert torch.equal(out[:n], o) and torch.equal(lse2[:n], lse) and (out[n:] == 3).all() and (lse2[n:] == 3).all()
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd,page", [(8, 2, 128, 16), (16, 2, 64, 17), (4, 4, 256, 16), (18, 2, 128, 16)])
+@pytest.mark.parametrize("window", [0, 600])
+def test_single_tokens_beside_long_chunks(csa, ctx, H, kv, hd, page, window):
+    """Decodes, short and long, in a batch of more than 512 tokens a request: on either side of 8 heads a key head."""
+    lens, new = [5000, 3400, 1, 33, 9000], [1, 2900, 1, 1, 1]
+    b = Batch(lens, H, kv, hd, page, seed=hd)
+    sink = torch.randn(H, generator=b.g, device="cuda")
+    q, o, lse = prompt(csa, ctx, b, new, pad=2, sink=sink, window=window)
+    check_prompt(b, new, q, o, lse, sink, window)
+    assert ctx.status() == 0
