@@ -263,7 +263,9 @@ __device__ __forceinline__ bool not_finite(uint32_t v) {  // either half
   return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
 }
 
-// What goes below O and on it: factors of a row's share (m, lr) and of its own pages' (own), and lse.
+// What goes below O and on it: factors of a row's share (m, lr) and of its own pages' (own), and lse.  (Powers as those of the weights, 2^-22
+// off; the logarithm and the division in full, as k_paged_attn's: where one score outweighs the others lse is little more than the error of
+// the short logarithm.  Full powers too cost a long prompt 1.3 %.)
 struct Finish {
   float f, f_own, lse;
 };
@@ -278,8 +280,8 @@ __device__ __forceinline__ Finish finish(float m, float lr, float l, float2 own,
     with = s2 == INFINITY ? INFINITY : paged::ex2(s2 - top);
   }
   const float em = M == -INFINITY ? 0.f : paged::ex2(M - top), all = fmaf(below, em, with);
-  const float f = all == 0.f ? 0.f : __fdividef(em, all);
-  return {f * e, f * eo, sum == 0.f ? -INFINITY : (M + __log2f(sum)) * 0.6931471805599453f};
+  const float f = all == 0.f ? 0.f : em / all;
+  return {f * e, f * eo, sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f};
 }
 // Whether a row of the prefix form is there, and not padding.
 __device__ __forceinline__ bool row_live(const RowsAttnArgs &a, int n) {

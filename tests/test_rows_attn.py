@@ -1,5 +1,5 @@
 """csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows, calls right behind the
-kernels that write their inputs, single tokens among many others and behind padding.
+kernels that write their inputs, single tokens among many others and behind padding, lse where it is small.
 
 What a call leaves is compared bit for bit with what it leaves without the value: the sums of the other rows and features do not
 change with it.
@@ -169,3 +169,27 @@ def test_single_tokens_beside_long_chunks(csa, ctx, H, kv, hd, page, window):
     q, o, lse = prompt(csa, ctx, b, new, pad=2, sink=sink, window=window)
     check_prompt(b, new, q, o, lse, sink, window)
     assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_lse_of_one_score_and_a_little(csa, ctx, hd):
+    """Two scores, 0 and -x: lse = log(1 + e^-x).  With w = e^-x the sum 1 + w is off by half a step of 1 (2^-24), by w 2^-22 (the power)
+    and by w x 2^-22 (the score in base 2, two roundings), and lse again by a step of the logarithm's and two roundings, 2^-22 of it."""
+    n, page = 120, 16
+    gap = 1 + torch.arange(n, device="cuda").float() / 16  # (exact in bf16 up to 8 bits of it: what the rows hold is read back)
+    k = torch.zeros(n + 1, page, 1, hd, dtype=torch.bfloat16, device="cuda")
+    k[:n, 1, 0, 0] = -gap.to(torch.bfloat16)
+    x = -k[:n, 1, 0, 0].double()
+    q = torch.zeros(2 * n, 1, hd, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    w = torch.exp(-x)
+    want = torch.log1p(w)
+    tol = 2.0 ** -24 + w * (1 + x) * 2.0 ** -22 + want * 2.0 ** -22
+    table = torch.arange(n, device="cuda", dtype=torch.int32)[:, None]
+    cache = csa.PagedCache(k, torch.ones_like(k))
+    _, lse = ctx.prompt_attn(q, cache, table, i32(list(range(0, 2 * n + 1, 2))), i32([2] * n), 1.0, with_lse=True)
+    assert (lse[0::2, 0] == 0).all() and ((lse[1::2, 0].double() - want).abs() <= tol).all()
+    _, lse = ctx.prefix_attn(q[:n], cache, table, i32([-1] * n), table, i32([2] * n), 1.0, cu=i32(list(range(n + 1))), with_lse=True)
+    assert ((lse[:, 0].double() - want).abs() <= tol).all()
+    o, lse = ctx.prefix_attn(q[:n], cache, table, i32([1] * n), i32([[n]]), i32([1]), 1.0, with_lse=True)  # 0, and 0 and -x of its own
+    assert (o == 1).all() and ((lse[:, 0].double() - torch.log1p(1 + w)).abs() <= tol + 2.0 ** -22).all() and ctx.status() == 0
