@@ -464,6 +464,7 @@ class Context:
         behind prefix int32 [G, width] of its prefix g, then rows 0 .. pos[n] of request req[n] (None: request n) behind
         table int32 [R, width]; with a window, the last `window` of them.  Prefix g is that of rows cu[g] .. cu[g+1]-1
         (cu None: one prefix for all).  pos -1: the prefix alone; pos < -1 or req < 0: padding, left as it is.
+        N * H up to 330, 130, 61 and 66 thousand at 64, 128, 192 and 256 features fit the workspace; more raises CsaError.
         Returns out, or (out, lse) as paged_attn does."""
         dev, st, out, lse, head, tail = self._rows_call(q, cache, table, "requests", out, lse, with_lse, stream)
         N, H, i32 = q.shape[0], q.shape[1], torch.int32

@@ -1,5 +1,6 @@
 """csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows, calls right behind the
-kernels that write their inputs, single tokens among many others and behind padding, lse where it is small.
+kernels that write their inputs, single tokens among many others and behind padding, lse where it is small,
+the largest prefix batches.
 
 What a call leaves is compared bit for bit with what it leaves without the value: the sums of the other rows and features do not
 change with it.
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 from test_paged import Batch, csa, ctx, gen, i32, randn  # noqa: F401
-from test_prompt import Prefixes, check_prompt, cus, prompt
+from test_prompt import Prefixes, check_prompt, close, cus, prompt, ref
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +194,30 @@ def test_lse_of_one_score_and_a_little(csa, ctx, hd):
     assert ((lse[:, 0].double() - want).abs() <= tol).all()
     o, lse = ctx.prefix_attn(q[:n], cache, table, i32([1] * n), i32([[n]]), i32([1]), 1.0, with_lse=True)  # 0, and 0 and -x of its own
     assert (o == 1).all() and ((lse[:, 0].double() - torch.log1p(1 + w)).abs() <= tol + 2.0 ** -22).all() and ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd,thousand", [(64, 330), (128, 130), (192, 61), (256, 66)])
+def test_prefix_rows_that_fit_the_workspace(csa, ctx, hd, thousand):
+    """The most rows by the header's sum, and 64 rows more, which are refused before anything is written."""
+    H, kv = 64, 8
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    room = (128 << 20) - (256 << 10) - (24 << 20) - sms * 2 * (256 if hd < 256 else 128) * (4 * hd + 16)
+    N = (room - (64 << 10)) // (H * (4 * hd + 8))  # (and the plan, below 64 KiB)
+    assert sms != 152 or abs(N * H / 1000 - thousand) < 2
+    b = Batch([40, 70], H, kv, hd, 16, seed=hd)
+    q = b.queries(N + 64)
+    args = (csa.PagedCache(b.k, b.v), b.table)
+    more = (b.table[1:2].contiguous(), i32([70]), b.scale)
+    pos, req = torch.arange(N + 64, dtype=torch.int32, device="cuda") % 41 - 1, torch.zeros(N + 64, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 3.0)
+    with pytest.raises(csa.CsaError, match="workspace") as e:
+        ctx.prefix_attn(q, *args, pos, *more, req=req, out=out)
+    torch.cuda.synchronize()
+    assert e.value.code == -2 and (out == 3).all()
+    o, lse = ctx.prefix_attn(q[:N], *args, pos[:N], *more, req=req[:N], with_lse=True)
+    for n in (0, 1, 40, N // 2, N - 41, N - 1):
+        p = int(pos[n])
+        K, V = (torch.cat([rows[1], rows[0][:p + 1]]) for rows in (b.rows_k, b.rows_v))
+        last = torch.tensor([70 + p], device="cuda")
+        close(o[n:n + 1], lse[n:n + 1], ref(q[n:n + 1], K, V, kv, b.scale, None, last * 0, last), "row %d" % n)
+    assert ctx.status() == 0
