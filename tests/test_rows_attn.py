@@ -1,6 +1,6 @@
 """csa_prompt_attn and csa_prefix_attn on the GPU: values that are not finite behind long windows, calls right behind the
 kernels that write their inputs, single tokens among many others and behind padding, lse where it is small,
-the largest prefix batches.
+the largest prefix batches, prefixes against the same rows in one table, bad values among own rows.
 
 What a call leaves is compared bit for bit with what it leaves without the value: the sums of the other rows and features do not
 change with it.
@@ -220,4 +220,57 @@ def test_prefix_rows_that_fit_the_workspace(csa, ctx, hd, thousand):
         K, V = (torch.cat([rows[1], rows[0][:p + 1]]) for rows in (b.rows_k, b.rows_v))
         last = torch.tensor([70 + p], device="cuda")
         close(o[n:n + 1], lse[n:n + 1], ref(q[n:n + 1], K, V, kv, b.scale, None, last * 0, last), "row %d" % n)
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("H,kv,hd,page,window", [(8, 2, 128, 16, 0), (4, 4, 64, 8, 200), (9, 1, 128, 16, 330), (16, 2, 256, 32, 0), (6, 2, 192, 16, 90)])
+def test_prefix_and_own_rows_in_one_table(csa, ctx, H, kv, hd, page, window):
+    """Prefix and own pages one behind the other in a table are rows of paged_attn: the same results, whichever way they are split.  Both are
+    within the tolerance of prefix_attn's one bf16 term of the 64-bit form, so they are within twice that of each other."""
+    own, plen = [1, 0, 2, 15, 16, 17, 100, 300], 20 * page
+    P = Prefixes(own, [plen], H, kv, hd, page, seed=hd + page)
+    n, pos = len(own), [x - 1 for x in own]
+    q, sink = P.b.queries(n), torch.randn(H, generator=P.b.g, device="cuda")
+    cache = csa.PagedCache(P.k, P.v)
+    o, lse = ctx.prefix_attn(q, cache, P.table, i32(pos), P.prefix, i32([plen]), P.scale, sink=sink, window=window, with_lse=True)
+    joined = torch.cat([P.prefix[:, :20].expand(n, -1), P.table], 1).contiguous()
+    o2, lse2 = ctx.paged_attn(q, cache, joined, i32([plen + x for x in pos]), P.scale, sink=sink, window=window, with_lse=True)
+    for i in range(n):
+        K, V = (torch.cat([rows[n], rows[i][:pos[i] + 1]]) for rows in (P.b.rows_k, P.b.rows_v))
+        last = torch.tensor([plen + pos[i]], device="cuda")
+        first = (last + 1 - window).clamp(min=0) if window else last * 0
+        want, e, tol, tol_l = ref(q[i:i + 1], K, V, kv, P.scale, sink, first, last)
+        close(o[i:i + 1], lse[i:i + 1], (want, e, tol, tol_l), "prefix_attn, row %d" % i)
+        close(o2[i:i + 1], lse2[i:i + 1], (want, e, tol, tol_l), "paged_attn, row %d" % i)
+        assert ((o[i:i + 1].double() - o2[i:i + 1].double()).abs() <= 2 * tol).all()
+        assert ((lse[i:i + 1].double() - lse2[i:i + 1].double()).abs() <= 2 * tol_l).all()
+    assert ctx.status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("window", [0, 60, 400])
+def test_prefix_bad_value_among_own_rows(csa, ctx, hd, bad, window):
+    """It reaches its request's rows that attend it, in its feature of its kv head's heads; all else keeps its bits."""
+    H, kv, own, page = 8, 2, [300, 40, 0, 90, 5, 7], 16
+    g = H // kv
+    P = Prefixes(own, [500, 300], H, kv, hd, page, seed=2)
+    req = [0, 1, 2, 3, 3, 3, 4, 5]
+    pos = [299, 39, -1, 89, 35, 36, 4, 6]
+    q = P.b.queries(len(req))
+
+    def run():
+        return ctx.prefix_attn(q, csa.PagedCache(P.k, P.v), P.table, i32(pos), P.prefix, i32([500, 300]), P.scale, cu=i32([0, 5, 8]),
+                               req=i32(req), window=window, with_lse=True)
+
+    want, want_lse = run()
+    assert want.isfinite().all()
+    at = 36
+    P.v[int(P.table[3, at // page]), at % page][1, 3] = bad
+    hit = torch.tensor([r == 3 and p >= at and (not window or p < at + window) for r, p in zip(req, pos)], device="cuda")
+    assert hit.tolist() == [False] * 3 + [True, False, True] + [False] * 2
+    o, lse = run()
+    assert torch.equal(lse, want_lse) and torch.equal(o[~hit], want[~hit]) and torch.equal(o[:, :g], want[:, :g])
+    rest = [d for d in range(hd) if d != 3]
+    assert torch.equal(o[..., rest], want[..., rest]) and not o[hit][:, g:, 3].isfinite().any()
     assert ctx.status() == 0
