@@ -230,7 +230,8 @@ cudaError_t launch_fill_f32(float *p, int64_t n, float v, cudaStream_t s);
 // These kernels are launched as programmatic dependents and wait for the kernels before them (dependency_wait)
 // before they read or write anything: only the launch itself overlaps what came before.  They let no dependent start early
 // (griddepcontrol.launch_dependents): the index kernels read before their own wait what was written two launches earlier, which
-// has to be complete then.  (It would save 0.5 us of a step's three launches.)  A plan does (rows_plan.cuh), for k_rows_attn, which waits for it in turn.
+// has to be complete then.  (It would save 0.5 us of a step's three launches.)  A plan does (rows_plan.cuh), for k_rows_attn, which
+// waits for it in turn.
 template <class... Args, class... Given>
 inline cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, unsigned cluster,
                                     Given &&...given) {

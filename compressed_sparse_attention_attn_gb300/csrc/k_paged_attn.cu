@@ -7,14 +7,15 @@
 // rate, far below what warp-level products give, and their accumulators stay in registers -- no trip
 // through tensor memory between the scores and the values.
 //
-// A unit is 16 positions for each of a CTA's warps (four; at 256 features three, or six with more than eight heads a kv head).  Every warp streams its own tiles (16 key rows,
-// 16 value rows) through a ring of its own in shared memory, with no barrier between the warps before the
+// A unit is 16 positions for each of a CTA's warps (four; at 256 features three, or six with more than eight heads a kv head).
+// Every warp streams its own tiles (16 key rows, 16 value rows) through a ring of its own in shared memory, with no barrier between the warps before the
 // end of a segment; the ring runs on across segments.  Rows come by 16-byte cp.async from the page of each
 // position (looked up two tiles ahead), rows past the end and features past head_dim as zeros; chunks are
 // XOR-swizzled by the row so that ldmatrix reads without conflicts.  Softmax statistics are f32 (base 2); the
 // weights enter the second product as two bf16 terms (their sum carries 16 bits), so the only rounding that
 // counts is the result's.  At the end of a segment each warp leaves its accumulators in the stage it has
-// just read (exactly as large: 16 rows of keys and values in bf16 are 16 heads of f32), and the CTA joins them.  How CTAs share the rows: paged_common.cuh.
+// just read (exactly as large: 16 rows of keys and values in bf16 are 16 heads of f32), and the CTA joins them.  How CTAs share the
+// rows: paged_common.cuh.
 //
 // Bound by HBM: 4 rows of 50 to 65 thousand (64 heads over 8 of 128) 150 us, 94 % of a copy; 32 rows of 300 to 4000 (32 over 8 of
 // 128) 37 us, 77 %; 48 windows of up to 1000 (16 of 256) 53 us, 79 %: what is left is the start and the segments' ends.
@@ -482,7 +483,8 @@ cudaError_t launch_latent(Params p, float *ws, size_t ws_bytes, int num_sms, cud
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, float *ws, size_t ws_bytes, int *counters, int num_sms, cudaStream_t s,
                               const rows::Plan *plan) {
-  static_assert(kPagedCounters == 3 * 2 * paged::kMaxCtas && paged::kJoin * paged::kJoin * paged::kJoin >= paged::kMaxCtas, "the context's counters");
+  static_assert(kPagedCounters == 3 * 2 * paged::kMaxCtas && paged::kJoin * paged::kJoin * paged::kJoin >= paged::kMaxCtas,
+                "the context's counters");
   paged::Params p;
   p.a = a;
   p.page = paged::FastDiv((uint32_t)a.c.page);

@@ -142,7 +142,8 @@ struct Walk {
   __device__ __forceinline__ bool load() {
     if (kvh >= P->a.c.kv_heads) return false;
     const int4 *at = reinterpret_cast<const int4 *>(P->item + i);
-    return set(__ldcg(at), __ldcg(at + 1), __ldcg(at + 2), __ldcg(P->start + i));  // (this kernel may begin before the plan has written them)
+    // (past L1: this kernel may begin before the plan has written them)
+    return set(__ldcg(at), __ldcg(at + 1), __ldcg(at + 2), __ldcg(P->start + i));
   }
   __device__ __forceinline__ void step() {
     if (++i == rg->items) i = 0, ++kvh;
@@ -263,9 +264,9 @@ __device__ __forceinline__ bool not_finite(uint32_t v) {  // either half
   return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
 }
 
-// What goes below O and on it: factors of a row's share (m, lr) and of its own pages' (own), and lse.  (Powers as those of the weights, 2^-22
-// off; the logarithm and the division in full, as k_paged_attn's: where one score outweighs the others lse is little more than the error of
-// the short logarithm.  Full powers too cost a long prompt 1.3 %.)
+// What goes below O and on it: factors of a row's share (m, lr) and of its own pages' (own), and lse.  (Powers as those of the
+// weights, 2^-22 off; the logarithm and the division in full, as k_paged_attn's: where one score outweighs the others lse is little
+// more than the error of the short logarithm.  Full powers too cost a long prompt 1.3 %.)
 struct Finish {
   float f, f_own, lse;
 };
@@ -455,10 +456,10 @@ __device__ __forceinline__ void span(const RowsAttnArgs &a, int tok, int shift, 
 }
 
 // Values that are not finite were left out of the products of tiles that not every row attends: here each is added to the rows that
-// attend it, in their shares or results (whatever else is in the sum, it is not finite).  The softmax warps come here once, behind all of
-// the CTA's items, when nothing waits for them any more, however many such tiles there are: each goes through them from the first to the last
-// with such values, for the rows that it had, a lane a row as before, 32 positions at a time.  (Loops rolled: the tile loop above is as fast as
-// its code is short and well placed; 8 loads a round here cost it 1 %.)
+// attend it, in their shares or results (whatever else is in the sum, it is not finite).  The softmax warps come here once, behind all
+// of the CTA's items, when nothing waits for them any more, however many such tiles there are: each goes through them from the first to
+// the last with such values, for the rows that it had, a lane a row as before, 32 positions at a time.  (Loops rolled: the tile loop is
+// as fast as its code is short and well placed; 8 loads a round here cost it 1 %.)
 template <int HDP>
 __device__ __forceinline__ void odd_values(const Params &P, const Part *rg, const OddTiles *odd) {  // (inline: a call cost a spill)
   using S = Shape<HDP>;
@@ -761,34 +762,34 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           out_with_own(tO, y > x, f, own, f_own, hd, live ? o : nullptr);
         } else {
 #pragma unroll 1
-        for (int c = 0; c < hd; c += 16) {
-          uint32_t u[16];
-          __syncwarp();
-          if (y > x) {
-            tc::tmem_ld16_wait(tO + c, u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = 0u;
-          }
-          if (share) {
-            if (mine) {
-              store32(share + c, u);
-              store32(share + c + 8, u + 8);
-            }
-          } else if (live) {
-            float v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]) * f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = pack2(v[2 * k], v[2 * k + 1]);
-            if (P.wide) {  // (rows of whole 32 bytes, on their borders)
-              store32(o + c, u);
+          for (int c = 0; c < hd; c += 16) {
+            uint32_t u[16];
+            __syncwarp();
+            if (y > x) {
+              tc::tmem_ld16_wait(tO + c, u);
             } else {
-              *reinterpret_cast<uint4 *>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
-              if (c + 8 < hd) *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = 0u;
+            }
+            if (share) {
+              if (mine) {
+                store32(share + c, u);
+                store32(share + c + 8, u + 8);
+              }
+            } else if (live) {
+              float v[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(u[k]) * f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) u[k] = pack2(v[2 * k], v[2 * k + 1]);
+              if (P.wide) {  // (rows of whole 32 bytes, on their borders)
+                store32(o + c, u);
+              } else {
+                *reinterpret_cast<uint4 *>(o + c) = make_uint4(u[0], u[1], u[2], u[3]);
+                if (c + 8 < hd) *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+              }
             }
           }
-        }
         }
         tc::tc_fence_before();
       }
@@ -874,8 +875,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
           int x, y;
           sub_range(w, t, QT == 2, x, y);
           auto keys_there = [&](int j, int stage) {
-          return stage_ready(stage) && (j != x || x == y || wait(&q_full[t], n_q++ & 1, abort_flag));
-        };
+            return stage_ready(stage) && (j != x || x == y || wait(&q_full[t], n_q++ & 1, abort_flag));
+          };
           auto keys = [&](int j, int stage) {  // tile j's scores
             if (x <= j && j < y) scores(stage);
             tc::mma_commit(&empty[stage % NST]);
@@ -1003,8 +1004,8 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
               const int row = (int)(p - P.page.div(p) * P.page.d);
 #pragma unroll
               for (int kb = 0; kb < NP; ++kb)
-                tc::tma_load_4d(s_ring + buf * S::kStage + kb * (KVT * 128) + first * 128, vals ? &G.v : &G.k, &full[buf], kb * 64, f.kvh, row,
-                                page);
+                tc::tma_load_4d(s_ring + buf * S::kStage + kb * (KVT * 128) + first * 128, vals ? &G.v : &G.k, &full[buf], kb * 64,
+                                f.kvh, row, page);
             }
             if (lane != 0) tc::mbar_arrive(&full[buf]);
           } else {
@@ -1215,8 +1216,8 @@ cudaError_t launch(Params p, Room room, const Beside *beside, int num_sms, cudaS
 // Whether a prompt batch's segments of one token go to k_paged_attn: up to 8 query heads a kv head, always, so that neither the other
 // requests nor padding rows change how a token is computed.  There it takes half the time over them (64 of up to 5000 positions, 32 heads
 // over 8 of 128: 41 against 73 us; 32 of up to 64000 beside a chunk of 2000 309, 330; 15 of 16 to 64 thousand beside one of 8200 1185,
-// 1262; 15 of 1 to 32 thousand beside 8200, 32 over 8 of 64, 820, 858; four of 64000 beside 8200 1033, 1062), and where there are none it costs
-// no more than the plan alone (4096 tokens 277, 276 us; 12 prompts of 100 to 4000 312 both).  It is slower where few single tokens are
+// 1262; 15 of 1 to 32 thousand beside 8200, 32 over 8 of 64, 820, 858; four of 64000 beside 8200 1033, 1062), and where there are none it
+// costs no more than the plan alone (4096 tokens 277, 276 us; 12 prompts of 100 to 4000 312 both).  It is slower where few single tokens are
 // short (one beside 4 windows of up to 6001, 16 of 256: 214, 209; 4 of up to 64000 beside 2000: 224, 217).  With 16 heads a kv head it is
 // not faster (32 of 2000 to 8000, 32 over 2 of 128: 48 against 46 us; 16 of 3000 to 9000, 32 over 2 of 256: 64, 51).
 static bool single_tokens(const RowsAttnArgs &a) { return !a.pos && a.H / a.c.kv_heads <= 8; }

@@ -158,8 +158,8 @@ __device__ __forceinline__ Two warp_scan(Two v, int lane) {
   return v;
 }
 
-// Called by all NT threads of the CTA, one of the first G of the grid.  scratch: Two [NT / 32], rows, out: all in shared memory.  Returns how many
-// units the CTA has (-1: more than can be counted in all).  Up to 32 rows the first warp finds it alone, and the CTA meets
+// Called by all NT threads of the CTA, one of the first G of the grid.  scratch: Two [NT / 32], rows, out: all in shared memory.
+// Returns how many units the CTA has (-1: more than can be counted in all).  Up to 32 rows the first warp finds it alone, and the CTA meets
 // once.  WHOLE: few segments (and rows) get whole CTAs, as many as ceil(its units / q) says, if such a q close to
 // the even share exists: a CTA then has one segment's end and not two (32 latent rows of about 20 tiles: 20.9
 // against 22.6 us, 128 shares of 128 KB instead of 184; up to 256 features, where ends are cheap, one row of 8000 lost 1 us).
@@ -345,8 +345,8 @@ __device__ __forceinline__ float out_factor(float M, float L, const float *sink,
 
 // Join `parts` shares, shares i of slots slot(i), of NH heads x HD features by the NT threads of the CTA.  fin: write O
 // and lse of heads h0 .. h0+nh-1 of row n; else the joined share to slot `to` (one of the slots: a thread writes
-// only what it alone has read, the maxima and sums behind a barrier).  PART: a row's share is its result.  A thread reads the maxima and sums of its
-// head itself, with the values: one round trip a dozen shares, and no barrier.
+// only what it alone has read, the maxima and sums behind a barrier).  PART: a row's share is its result.  A thread reads the
+// maxima and sums of its head itself, with the values: one round trip a dozen shares, and no barrier.
 template <int NH, int HD, int NT, bool PART, class Slot>
 __device__ __forceinline__ void join(const Params &P, int parts, Slot slot, bool fin, int to, int n, int h0, int nh) {
   const PagedAttnArgs &a = P.a;

@@ -464,8 +464,9 @@ CSA_API int csa_paged_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, 
  * An infinity or NaN in the cache reaches the rows that attend it and no others.
  * Caller errors, recorded in the context's status word: a request with cu[r] < 0, cu[r] > cu[r+1], cu[r+1] > N or length[r] < n (its
  * rows are left as they were), a length past width pages (the rows past them are left out), a page id outside [0, n_pages) (its rows
- * are left out).  Rows that two requests both claim are written by either.  N * H < 2^31; the call's notes (56 bytes a request and 128 rows
- * of a kv head) have to fit the context's workspace: N * H / kv_heads up to 5 * 10^7 with R up to 4 * 10^5 do; more than fits is CSA_ERR_SHAPE.
+ * are left out).  Rows that two requests both claim are written by either.  N * H < 2^31; the call's notes (56 bytes a request
+ * and 128 rows of a kv head) have to fit the context's workspace: N * H / kv_heads up to 5 * 10^7 with R up to 4 * 10^5 do; more
+ * than fits is CSA_ERR_SHAPE.
  * The same inputs give the same bits. */
 CSA_API int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
                             const int32_t *table, int R, int width, const int32_t *cu, const int32_t *length,
@@ -483,9 +484,9 @@ CSA_API int csa_prompt_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N,
  * csa_paged_attn's bound on a call's work are a caller error too: what the call then writes does not count.
  * The rest is as in csa_paged_attn, with head_dim <= 256; infinities and errors as in csa_prompt_attn, with prefix_len for length
  * (a negative one counts as 0) and its errors of req, pos and page ids.
- * The rows' own shares have to fit the context's workspace, 128 MiB less 256 KiB: N H (4 head_dim + 8) bytes, beside 24 MiB and, with
- * head_dim rounded up to d = 64, 128, 192 or 256, 2 x 256 (4 d + 16) bytes an SM (at 256 half of that).  On 152 SMs N * H may be 330, 130, 61
- * and 66 thousand at these; more is CSA_ERR_SHAPE before anything is launched, and such rows go in several calls. */
+ * The rows' own shares have to fit the context's workspace, 128 MiB less 256 KiB: N H (4 head_dim + 8) bytes, beside 24 MiB and,
+ * with head_dim rounded up to d = 64, 128, 192 or 256, 2 x 256 (4 d + 16) bytes an SM (at 256 half of that).  On 152 SMs N * H may
+ * be 330, 130, 61 and 66 thousand at these; more is CSA_ERR_SHAPE before anything is launched, and such rows go in several calls. */
 CSA_API int csa_prefix_attn(csa_ctx *ctx, const csa_bf16 *q, int64_t q_t, int N, int H, const csa_paged *cache,
                             const int32_t *table, int R, int width, const int32_t *req, const int32_t *pos,
                             const int32_t *prefix, int G, int prefix_width, const int32_t *prefix_len, const int32_t *cu,

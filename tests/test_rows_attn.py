@@ -144,8 +144,8 @@ def test_inputs_written_by_the_kernel_before(csa, ctx, H, kv, hd):
 
 
 @pytest.mark.parametrize("H,kv,hd", [(8, 2, 128), (4, 4, 64), (16, 2, 256), (9, 1, 128), (6, 2, 192)])
-@pytest.mark.parametrize("lens,new", [([900], [1]), ([1], [1]), ([40], [17]), ([300, 64, 5000, 7], [1, 1, 1, 1]), ([700, 0, 2000, 130], [1, 0, 300, 1]),
-                                      ([150, 90], [150, 20]), ([6000], [33])])
+@pytest.mark.parametrize("lens,new", [([900], [1]), ([1], [1]), ([40], [17]), ([300, 64, 5000, 7], [1, 1, 1, 1]),
+                                      ([700, 0, 2000, 130], [1, 0, 300, 1]), ([150, 90], [150, 20]), ([6000], [33])])
 def test_padding_changes_no_bit(csa, ctx, H, kv, hd, lens, new):
     """The same batch with no padding rows, with a few, and with thousands, as a graph captured at its largest step has them."""
     b = Batch(lens, H, kv, hd, 16, seed=hd)
@@ -223,10 +223,11 @@ def test_prefix_rows_that_fit_the_workspace(csa, ctx, hd, thousand):
     assert ctx.status() == 0
 
 
-@pytest.mark.parametrize("H,kv,hd,page,window", [(8, 2, 128, 16, 0), (4, 4, 64, 8, 200), (9, 1, 128, 16, 330), (16, 2, 256, 32, 0), (6, 2, 192, 16, 90)])
+@pytest.mark.parametrize("H,kv,hd,page,window", [(8, 2, 128, 16, 0), (4, 4, 64, 8, 200), (9, 1, 128, 16, 330), (16, 2, 256, 32, 0),
+                                                 (6, 2, 192, 16, 90)])
 def test_prefix_and_own_rows_in_one_table(csa, ctx, H, kv, hd, page, window):
-    """Prefix and own pages one behind the other in a table are rows of paged_attn: the same results, whichever way they are split.  Both are
-    within the tolerance of prefix_attn's one bf16 term of the 64-bit form, so they are within twice that of each other."""
+    """Prefix and own pages one behind the other in a table are rows of paged_attn: the same results, whichever way they are split.
+    Both are within the tolerance of prefix_attn's one bf16 term of the 64-bit form, so they are within twice that of each other."""
     own, plen = [1, 0, 2, 15, 16, 17, 100, 300], 20 * page
     P = Prefixes(own, [plen], H, kv, hd, page, seed=hd + page)
     n, pos = len(own), [x - 1 for x in own]
