@@ -386,17 +386,18 @@ __device__ __forceinline__ bool weights(float sc, float &m, float &l, float &lr,
   return true;
 }
 
-// The first and the last tile (item in the CTA, tile of its positions) that values which are not finite were taken out of.
+// Between which of the CTA's items, and between which tiles of positions, values that are not finite were taken out.
 struct OddTiles {
-  unsigned long long first, last;
+  int seq0, seq1, j0, j1;
   __device__ __forceinline__ void note(int seq, int j) {
-    const unsigned long long at = (unsigned long long)(uint32_t)seq << 32 | (uint32_t)j;
-    atomicMin(&first, at);
-    atomicMax(&last, at);
+    atomicMin(&seq0, seq);
+    atomicMax(&seq1, seq);
+    atomicMin(&j0, j);
+    atomicMax(&j1, j);
   }
   __device__ __forceinline__ bool any() const {
     const volatile OddTiles &v = *this;
-    return v.first <= v.last;
+    return v.seq0 <= v.seq1;
   }
 };
 // A lane's share of a tile of values, 16 bytes of every 2 KB: those that are not finite, in the tile's first `rows` rows (behind them lies
@@ -457,30 +458,31 @@ __device__ __forceinline__ void span(const RowsAttnArgs &a, int tok, int shift, 
 
 // Values that are not finite were left out of the products of tiles that not every row attends: here each is added to the rows that
 // attend it, in their shares or results (whatever else is in the sum, it is not finite).  The softmax warps come here once, behind all
-// of the CTA's items, when nothing waits for them any more, however many such tiles there are: each goes through them from the first to
-// the last with such values, for the rows that it had, a lane a row as before, 32 positions at a time.  (Loops rolled: the tile loop is
-// as fast as its code is short and well placed; 8 loads a round here cost it 1 %.)
+// of the CTA's items, when nothing waits for them any more, however many such tiles there are: each goes through those between the first
+// and the last with such values, for the rows that it had, a lane a row as before, 32 positions at a time.  (Loops rolled: the tile loop is
+// as fast as its code is short and well placed; 4 or 8 loads a round here cost it 1 %.)  40 thousand rows of a prefix's window of a
+// million positions, 128 features: 20 ms with one such value or none, 74 with two half a window apart, 264 with one in every tile.
 template <int HDP>
 __device__ __forceinline__ void odd_values(const Params &P, const Part *rg, const OddTiles *odd) {  // (inline: a call cost a spill)
   using S = Shape<HDP>;
   constexpr int QT = S::QT, KVT = S::KVT;
   const RowsAttnArgs &a = P.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = warp >> 2, row0 = (warp & 3) * 32, hd = a.c.head_dim, g = P.g.d;
-  const unsigned long long first = odd->first, last = odd->last;
+  const OddTiles in = *odd;
   const bool vals = a.c.v != nullptr;
   Walk<KVT, false> w;
   w.P = &P;
   w.rg = rg;
   w.i = rg->item;
   w.kvh = rg->kvh;
-  for (bool more = w.first(false); more && w.seq <= (int)(last >> 32); more = w.next(false)) {
+  for (bool more = w.first(false); more && w.seq <= in.seq1; more = w.next(false)) {
     const Item &d = w.d;
     const int sub = sub_rows(w, t, QT == 2);
-    if (w.seq < (int)(first >> 32) || sub < 0 || sub + row0 >= d.rows) continue;
+    if (w.seq < in.seq0 || sub < 0 || sub + row0 >= d.rows) continue;
     int x, y, lo = 0, hi = 0x7fffffff;
     sub_range(w, t, QT == 2, x, y);
-    if (w.seq == (int)(first >> 32)) x = max(x, (int)(uint32_t)first);
-    if (w.seq == (int)(last >> 32)) y = min(y, (int)(uint32_t)last + 1);
+    x = max(x, in.j0);
+    y = min(y, in.j1 + 1);
     const int R = sub + row0 + lane;
     float *share = nullptr;
     bf16 *o = nullptr;
@@ -505,7 +507,7 @@ __device__ __forceinline__ void odd_values(const Params &P, const Part *rg, cons
         const bf16 *src =
             there ? vb + id * (vals ? a.c.v_page : a.c.k_page) + (int64_t)(p - pg * P.page.d) * (vals ? a.c.v_row : a.c.k_row) : vb;
         uint32_t any = 0;
-#pragma unroll 2
+#pragma unroll 1
         for (int c = 0; c < hd; c += 8) {
           const uint4 z = *reinterpret_cast<const uint4 *>(src + c);
           any |= not_finite(z.x) || not_finite(z.y) || not_finite(z.z) || not_finite(z.w);
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(Shape<HDP>::kThreads, 1) k_rows_attn(const __g
       tc::mbar_init(&q_full[b], 128);
     }
     tc::mbar_init(drain, S::kMma);
-    odd = OddTiles{~0ull, 0};
+    odd = OddTiles{0x7fffffff, -1, 0x7fffffff, -1};
     *abort_flag = 0;
     *issue_lock = 0;
     tc::fence_barrier_init();
