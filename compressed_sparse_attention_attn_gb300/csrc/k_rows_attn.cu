@@ -28,10 +28,10 @@
 // Bound by the way of a tile through its stages: scores to softmax (1600 cycles, of which 64 pairs of exponentials take 770 at least),
 // softmax to values and the next scores (768 cycles of products, behind the other tile's).  The products alone take 2700 cycles for two
 // tiles of rows and a tile of positions (2048 by the measured peak: two products read q and the keys from shared memory at
-// 128 bytes a cycle, all of its rate), with the softmax 3400.  16384 tokens of 64 heads over 8 of 128: 3.34 ms, 1318 TFLOP/s, 68 % of
-// the measured bf16 rate (77 % of the sustained one); 12 ragged prompts of 100 to 4000 tokens (32 over 8 of 128) 311 us, 45 %:
+// 128 bytes a cycle, all of its rate), with the softmax 3400.  16384 tokens of 64 heads over 8 of 128: 3.34 ms, 1316 TFLOP/s, 68 % of
+// the measured bf16 rate (76 % of the sustained one); 12 ragged prompts of 100 to 4000 tokens (32 over 8 of 128) 311 us, 45 %:
 // the ends of their items.  64 decodes of 1 to 5000 beside two prompts (40 over 8 of 80) 100 us.  256 rows behind 32768 shared ones (64
-// over 8 of 128) 353 us, of which their own pages take 115.
+// over 8 of 128) 350 us, of which their own pages take 115.
 #include <algorithm>
 #include <cstring>
 
